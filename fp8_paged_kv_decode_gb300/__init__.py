@@ -12,6 +12,10 @@ Entry points (same names as the C ABI):
   kv_page_tag_check                the separate per-page generation-tag check
   kv_append_fp8_tag_check          the step's FP8 append and the tag check in one launch
   kv_append_bf16_tag_check         the same for a BF16 cache
+  kv_append_fp4                    the same into a 4-bit cache (also kv_append_fp4_tag_check)
+  kv_gather                        cached tokens read back as bf16
+  qk_norm_rope                     RMS norm of the q and k heads and the position rotation in one pass
+  kv_step_tables                   page table, slots and positions of a step from request lengths
   kv_page_realloc                  bump tags (and optionally zero pages) of reallocated pages
   paged_decode_attn                decode attention over the paged cache
   paged_decode_attn_workspace_size bytes of scratch paged_decode_attn needs
@@ -23,8 +27,10 @@ import os
 import threading
 
 __all__ = [
-    "FkvError", "KV_FP8_E4M3", "KV_BF16", "library_path", "load_library", "kv_append_fp8", "kv_append_bf16",
+    "FkvError", "KV_FP8_E4M3", "KV_BF16", "KV_FP4", "FP4_ROW_BYTES", "library_path", "load_library", "kv_append_fp8", "kv_append_bf16",
     "kv_calibrate_scales", "kv_page_tag_check", "kv_append_fp8_tag_check", "kv_append_bf16_tag_check", "kv_page_realloc",
+    "kv_append_fp4", "kv_append_fp4_tag_check", "kv_gather", "qk_norm_rope", "kv_step_tables",
+    "kv_step_tables_workspace_size", "alloc_step_tables_workspace",
     "paged_decode_attn",
     "paged_decode_attn_workspace_size",
     "alloc_workspace",
@@ -34,10 +40,15 @@ __all__ = [
 
 KV_FP8_E4M3 = 0
 KV_BF16 = 1
+KV_FP4 = 2
+FP4_ROW_BYTES = 72
 DEVERR_APPEND_SLOT = 0x1
 DEVERR_ATTN_PAGE = 0x2
 DEVERR_TIMEOUT = 0x4
 DEVERR_REALLOC_PAGE = 0x8
+DEVERR_GATHER_SLOT = 0x10
+DEVERR_TABLES = 0x20
+DEVERR_ROPE_AXIS = 0x40
 HEAD_DIM = 128
 
 EXPORTED_SYMBOLS = (
@@ -45,6 +56,8 @@ EXPORTED_SYMBOLS = (
     "kv_append_fp8_tag_check", "kv_append_bf16_tag_check", "kv_page_realloc",
     "paged_decode_attn_workspace_size", "paged_decode_attn", "paged_decode_attn_noalloc", "fkv_device_error",
     "fkv_kernels_per_call", "fkv_selftest_wait",
+    "kv_append_fp4", "kv_append_fp4_tag_check", "kv_gather", "qk_norm_rope", "kv_step_tables",
+    "kv_step_tables_workspace_size",
 )
 ERR_SCRATCH_LIMIT = 4
 NOALLOC_SCRATCH_BYTES = 16 << 20
@@ -91,6 +104,20 @@ def load_library():
                                                 P, P]
         lib.kv_append_bf16_tag_check.restype = ctypes.c_int
         lib.kv_append_bf16_tag_check.argtypes = [P, P, P, i32, P, P, i32, i32, i32, i32, P, P, P, P, i32, i64, P, P]
+        lib.kv_append_fp4.restype = ctypes.c_int
+        lib.kv_append_fp4.argtypes = lib.kv_append_fp8.argtypes
+        lib.kv_append_fp4_tag_check.restype = ctypes.c_int
+        lib.kv_append_fp4_tag_check.argtypes = lib.kv_append_fp8_tag_check.argtypes
+        lib.kv_gather.restype = ctypes.c_int
+        lib.kv_gather.argtypes = [P, P, i32, P, P, P, i32, P, P, i32, i32, i32, i32, P]
+        lib.qk_norm_rope.restype = ctypes.c_int
+        lib.qk_norm_rope.argtypes = [P, i64, i32, P, i64, i32, P, i64, P, i64, i32, P, P, f32, P, i32, P, P, i32, i32,
+                                     f32, i32, P]
+        lib.kv_step_tables_workspace_size.restype = ctypes.c_size_t
+        lib.kv_step_tables_workspace_size.argtypes = [i32]
+        lib.kv_step_tables.restype = ctypes.c_int
+        lib.kv_step_tables.argtypes = [P, P, i32, P, P, i32, P, i32, P, P, i32, i32, P, P, P, P, P, P, i32, P, P, P,
+                                       i32, P, P, ctypes.c_size_t, P]
         lib.kv_calibrate_scales.restype = ctypes.c_int
         lib.kv_calibrate_scales.argtypes = [P, P, i64, i32, i32, P, P, P]
         lib.kv_page_realloc.restype = ctypes.c_int
@@ -148,6 +175,20 @@ def _raise(status: int, name: str):
 def _is_byte_cache(t):
     import torch
     return t.dtype in (torch.uint8, getattr(torch, "float8_e4m3fn", torch.uint8))
+
+
+def _is_fp4_cache(t):
+    import torch
+    return t.dtype == torch.uint8 and t.dim() == 4 and t.shape[-1] == FP4_ROW_BYTES
+
+
+def _here(*ts):
+    """Contiguous tensors of the current device (the one the call launches on)."""
+    import torch
+    _dev(*ts)
+    cur = torch.cuda.current_device()
+    for t in ts:
+        _need(t is None or t.device.index == cur, "tensors must be on the current device")
 
 
 # ---------------------------------------------------------------------------
@@ -267,6 +308,162 @@ def kv_calibrate_scales(k, v, k_scale, v_scale, stream=None):
                                               _stream(stream)), "kv_calibrate_scales")
 
 
+def _check_fp4_append(k_new, v_new, slot_mapping, k_scale, v_scale, k_cache, v_cache):
+    import torch
+    _need(k_new.dtype == torch.bfloat16 and v_new.dtype == torch.bfloat16, "k_new/v_new must be bf16")
+    _need(slot_mapping.dtype == torch.int64, "slot_mapping must be int64")
+    _need(_is_fp4_cache(k_cache) and _is_fp4_cache(v_cache), "FP4 caches must be uint8 [P][Hkv][S][72]")
+    P, Hkv, S, _ = k_cache.shape
+    _need(v_cache.shape == k_cache.shape, "k_cache/v_cache shapes differ")
+    _need(k_scale.dtype == torch.float32 and v_scale.dtype == torch.float32 and k_scale.numel() == Hkv
+          and v_scale.numel() == Hkv, "scales must be float32 [Hkv]")
+    N = slot_mapping.numel()
+    _need(tuple(k_new.shape) == (N, Hkv, HEAD_DIM) and tuple(v_new.shape) == (N, Hkv, HEAD_DIM), "k_new/v_new shape")
+    return P, Hkv, S, N
+
+
+def kv_append_fp4(k_new, v_new, slot_mapping, k_scale, v_scale, k_cache, v_cache, stream=None):
+    """Quantize bf16 ``k_new/v_new`` [N][Hkv][128] to e2m1 codes with an e4m3
+    scale per 16 dims into ``k_cache/v_cache`` [P][Hkv][S][72] (uint8) at
+    ``slot_mapping`` [N] (int64, <0 = skip).  The per-head fp32 scales are the
+    ones an FP8 cache would use (``kv_calibrate_scales``)."""
+    _here(k_new, v_new, slot_mapping, k_scale, v_scale, k_cache, v_cache)
+    P, Hkv, S, N = _check_fp4_append(k_new, v_new, slot_mapping, k_scale, v_scale, k_cache, v_cache)
+    _raise(load_library().kv_append_fp4(_ptr(k_new), _ptr(v_new), _ptr(slot_mapping), N, _ptr(k_scale),
+                                        _ptr(v_scale), _ptr(k_cache), _ptr(v_cache), P, Hkv, S, HEAD_DIM,
+                                        _stream(stream)), "kv_append_fp4")
+
+
+def kv_append_fp4_tag_check(k_new, v_new, slot_mapping, k_scale, v_scale, k_cache, v_cache,
+                            page_tags, page_indptr, page_indices, expected_tags, abort_mask, stream=None):
+    """``kv_append_fp4`` then ``kv_page_tag_check`` (same arguments, same
+    results) in one launch; ``page_tags`` has one entry per page of the pool."""
+    import torch
+    _here(k_new, v_new, slot_mapping, k_scale, v_scale, k_cache, v_cache, page_tags, page_indptr, page_indices,
+          expected_tags, abort_mask)
+    P, Hkv, S, N = _check_fp4_append(k_new, v_new, slot_mapping, k_scale, v_scale, k_cache, v_cache)
+    _need(page_tags.dtype in (torch.uint32, torch.int32) and expected_tags.dtype == page_tags.dtype,
+          "tags must be 32-bit, both of one dtype")
+    _need(page_tags.numel() == P, "page_tags must have one entry per page of the pool")
+    _need(page_indptr.dtype == torch.int32 and page_indices.dtype == torch.int32, "CSR must be int32")
+    _need(abort_mask.dtype == torch.uint8, "abort_mask must be uint8")
+    B = page_indptr.numel() - 1
+    _need(abort_mask.numel() == B and expected_tags.numel() == page_indices.numel(), "size mismatch")
+    _raise(load_library().kv_append_fp4_tag_check(
+        _ptr(k_new), _ptr(v_new), _ptr(slot_mapping), N, _ptr(k_scale), _ptr(v_scale), _ptr(k_cache),
+        _ptr(v_cache), P, Hkv, S, HEAD_DIM, _ptr(page_tags), _ptr(page_indptr), _ptr(page_indices),
+        _ptr(expected_tags), B, page_indices.numel(), _ptr(abort_mask), _stream(stream)), "kv_append_fp4_tag_check")
+
+
+def kv_gather(k_cache, v_cache, slots, k_out, v_out, k_scale=None, v_scale=None, stream=None):
+    """Cached tokens at ``slots`` [N] (int64; <0 gives zeros) as bf16
+    ``k_out/v_out`` [N][Hkv][128].  Caches: FP8 uint8 / float8_e4m3fn or bf16
+    [P][Hkv][S][128], or FP4 uint8 [P][Hkv][S][72]; scales fp32 [Hkv] unless bf16."""
+    import torch
+    _here(k_cache, v_cache, slots, k_out, v_out, k_scale, v_scale)
+    kv = KV_FP4 if _is_fp4_cache(k_cache) else KV_FP8_E4M3 if _is_byte_cache(k_cache) else KV_BF16
+    _need(kv != KV_BF16 or k_cache.dtype == torch.bfloat16, "cache must be uint8 / float8_e4m3fn or bf16")
+    P, Hkv, S, row = k_cache.shape
+    _need(v_cache.shape == k_cache.shape and v_cache.dtype == k_cache.dtype, "k_cache and v_cache differ")
+    _need(slots.dtype == torch.int64, "slots must be int64")
+    N, D = slots.numel(), row if kv != KV_FP4 else HEAD_DIM
+    for o in (k_out, v_out):
+        _need(o.dtype == torch.bfloat16 and tuple(o.shape) == (N, Hkv, D), "k_out/v_out must be bf16 [N][Hkv][128]")
+    if kv != KV_BF16:
+        for s in (k_scale, v_scale):
+            _need(s is not None and s.dtype == torch.float32 and s.numel() == Hkv, "scales must be float32 [Hkv]")
+    _raise(load_library().kv_gather(_ptr(k_cache), _ptr(v_cache), kv, _ptr(k_scale), _ptr(v_scale), _ptr(slots), N,
+                                    _ptr(k_out), _ptr(v_out), P, Hkv, S, D, _stream(stream)), "kv_gather")
+
+
+def qk_norm_rope(q, k, positions, inv_freq, q_out, k_out, q_weight=None, k_weight=None, eps=1e-6, axis_map=None,
+                 interleaved=False, rot_scale=1.0, stream=None):
+    """RMS norm of every head of ``q`` [N][Hq][128] and ``k`` [N][Hkv][128]
+    (bf16; heads contiguous, any token stride that is a multiple of 8) with
+    bf16 weights [128] (None: no norm), then the rotation by ``positions``
+    (int32 [N], or [axes][N] with ``axis_map`` uint8 [R/2]) at fp32
+    ``inv_freq`` [R/2], R <= 128 a multiple of 16; pairs are (j, j + R/2), or
+    (2j, 2j + 1) when ``interleaved``.  ``q_out``/``k_out`` may be q/k.
+    ``k`` and ``k_out`` may be None."""
+    import torch
+    _here(positions, inv_freq, q_weight, k_weight, axis_map)
+    _need((k is None) == (k_out is None), "k and k_out go together")
+    N, Hq, D = q.shape
+    Hkv = 0 if k is None else k.shape[1]
+    for x, h in ((q, Hq), (q_out, Hq), (k, Hkv), (k_out, Hkv)):
+        if x is None:
+            continue
+        _need(x.is_cuda and x.device.index == torch.cuda.current_device(), "tensors must be on the current device")
+        _need(x.dtype == torch.bfloat16 and tuple(x.shape) == (N, h, D), "q/k and outputs must be bf16 [N][H][128]")
+        _need(N == 0 or (x.stride(2) == 1 and (h == 1 or x.stride(1) == D)), "head rows must be contiguous")
+    for w in (q_weight, k_weight):
+        _need(w is None or (w.dtype == torch.bfloat16 and w.numel() == D), "weights must be bf16 [128]")
+    _need(positions.dtype == torch.int32 and positions.dim() in (1, 2) and positions.shape[-1] == N,
+          "positions must be int32 [N] or [axes][N]")
+    _need(inv_freq.dtype == torch.float32 and inv_freq.dim() == 1, "inv_freq must be float32 [R/2]")
+    _need(axis_map is None or (axis_map.dtype == torch.uint8 and axis_map.numel() == inv_freq.numel()),
+          "axis_map must be uint8 [R/2]")
+    axes = 1 if positions.dim() == 1 else positions.shape[0]
+
+    def stride(x, h):
+        return h * D if x is None or N <= 1 else x.stride(0)
+    _raise(load_library().qk_norm_rope(
+        _ptr(q), stride(q, Hq), Hq, _ptr(k), stride(k, Hkv), Hkv, _ptr(q_out), stride(q_out, Hq), _ptr(k_out),
+        stride(k_out, Hkv), N, _ptr(q_weight), _ptr(k_weight), float(eps), _ptr(positions), axes, _ptr(inv_freq),
+        _ptr(axis_map), 2 * inv_freq.numel(), 1 if interleaved else 0, float(rot_scale), D, _stream(stream)),
+        "qk_norm_rope")
+    return q_out, k_out
+
+
+def kv_step_tables_workspace_size(batch):
+    n = load_library().kv_step_tables_workspace_size(batch)
+    _need(n > 0, "batch must not be negative")
+    return int(n)
+
+
+def alloc_step_tables_workspace(batch, device="cuda"):
+    import torch
+    return torch.empty(kv_step_tables_workspace_size(batch), dtype=torch.uint8, device=device)
+
+
+def kv_step_tables(cached_lens, new_lens, block_table, block_tags, free_pages, free_count, page_tags, page_size,
+                   step_lens, cached_lens_out, refused, page_indptr, page_indices, expected_tags, token_indptr,
+                   slot_mapping, positions, free_left, workspace, stream=None):
+    """The tables of a step from the requests' lengths, pages taken from a free
+    list where a request grows into them (``block_table``/``block_tags``
+    [B][max_blocks] updated in place).  int32 throughout, but slot_mapping int64,
+    refused uint8 and tags 32-bit; the capacities are the arrays' lengths.  For
+    the next step pass ``cached_lens_out`` as ``cached_lens`` and ``free_left``
+    as ``free_count`` (each may also be the same array in one call)."""
+    import torch
+    _here(cached_lens, new_lens, block_table, block_tags, free_pages, free_count, page_tags, step_lens,
+          cached_lens_out, refused, page_indptr, page_indices, expected_tags, token_indptr, slot_mapping, positions,
+          free_left, workspace)
+    for x in (cached_lens, new_lens, block_table, free_pages, free_count, step_lens, cached_lens_out, page_indptr,
+              page_indices, token_indptr, positions, free_left):
+        _need(x.dtype == torch.int32, "lengths, tables, free list, indptr, indices and positions must be int32")
+    for x in (block_tags, page_tags, expected_tags):
+        _need(x.dtype in (torch.int32, torch.uint32) and x.dtype == page_tags.dtype, "tags must be 32-bit, of one dtype")
+    _need(slot_mapping.dtype == torch.int64, "slot_mapping must be int64")
+    _need(refused.dtype == torch.uint8, "refused must be uint8")
+    B = cached_lens.numel()
+    _need(block_table.dim() == 2 and block_table.shape[0] == B and block_tags.shape == block_table.shape,
+          "block_table and block_tags must be [B][max_blocks]")
+    _need(new_lens.numel() == B and step_lens.numel() == B and cached_lens_out.numel() == B and refused.numel() == B,
+          "one length per request")
+    _need(page_indptr.numel() == B + 1 and token_indptr.numel() == B + 1, "indptr arrays must be [B + 1]")
+    _need(expected_tags.numel() == page_indices.numel(), "expected_tags is parallel to page_indices")
+    _need(positions.numel() == slot_mapping.numel(), "positions is parallel to slot_mapping")
+    _need(free_count.numel() == 1 and free_left.numel() == 1, "free_count and free_left hold one value")
+    _raise(load_library().kv_step_tables(
+        _ptr(cached_lens), _ptr(new_lens), B, _ptr(block_table), _ptr(block_tags), block_table.shape[1],
+        _ptr(free_pages), free_pages.numel(), _ptr(free_count), _ptr(page_tags), page_tags.numel(), int(page_size),
+        _ptr(step_lens), _ptr(cached_lens_out), _ptr(refused), _ptr(page_indptr), _ptr(page_indices),
+        _ptr(expected_tags), page_indices.numel(), _ptr(token_indptr), _ptr(slot_mapping), _ptr(positions),
+        slot_mapping.numel(), _ptr(free_left), _ptr(workspace), workspace.numel() * workspace.element_size(),
+        _stream(stream)), "kv_step_tables")
+
+
 def kv_page_realloc(page_tags, pages, new_tags, k_cache=None, v_cache=None, stream=None):
     """Bump the live tag of each listed page (new owners record ``new_tags``)
     and, if the pools are given, zero those pages."""
@@ -277,13 +474,31 @@ def kv_page_realloc(page_tags, pages, new_tags, k_cache=None, v_cache=None, stre
     if k_cache is not None:
         _need(v_cache is not None and tuple(k_cache.shape) == tuple(v_cache.shape), "both pools, same shape")
         P, Hkv, S, D = k_cache.shape
-        kv = KV_FP8_E4M3 if _is_byte_cache(k_cache) else KV_BF16
+        if _is_fp4_cache(k_cache):
+            D, kv = HEAD_DIM, KV_FP4
+        else:
+            kv = KV_FP8_E4M3 if _is_byte_cache(k_cache) else KV_BF16
     else:
         Hkv = S = 0
         D, kv = HEAD_DIM, KV_FP8_E4M3
     _raise(load_library().kv_page_realloc(_ptr(page_tags), page_tags.numel(), _ptr(pages), pages.numel(),
                                           _ptr(new_tags), _ptr(k_cache), _ptr(v_cache), kv, Hkv, S, D,
                                           _stream(stream)), "kv_page_realloc")
+
+
+def _attn_cache(k_cache, v_cache, k_scale, v_scale):
+    """The caches' format and head dim."""
+    import torch
+    if _is_fp4_cache(k_cache):
+        _here(k_cache, v_cache, k_scale, v_scale)
+        _need(v_cache.shape == k_cache.shape and v_cache.dtype == k_cache.dtype, "k_cache and v_cache differ")
+        for s in (k_scale, v_scale):
+            _need(s is not None and s.dtype == torch.float32 and s.numel() == k_cache.shape[1],
+                  "scales must be float32 [Hkv]")
+        return KV_FP4, HEAD_DIM
+    fp8 = _is_byte_cache(k_cache)
+    _need(fp8 or k_cache.dtype == torch.bfloat16, "cache must be uint8 (e4m3) or bf16")
+    return (KV_FP8_E4M3 if fp8 else KV_BF16), k_cache.shape[-1]
 
 
 def paged_decode_attn_workspace_size(batch, num_q_heads, num_kv_heads, head_dim=HEAD_DIM, kv_dtype=KV_FP8_E4M3):
@@ -303,21 +518,21 @@ def paged_decode_attn(q, k_cache, v_cache, page_indptr, page_indices, seq_lens, 
     """out[r][i] = softmax(sm_scale q k^T) v over request r's paged tokens.
 
     q, out: bf16 [B][Hq][128]; caches [P][Hkv][S][128] uint8 (FP8 e4m3, with
-    k_scale/v_scale fp32 [Hkv]) or bf16; CSR page table int32; seq_lens int32
+    k_scale/v_scale fp32 [Hkv]) or bf16, or [P][Hkv][S][72] uint8 (FP4, with
+    the same scales; workspace for KV_FP4); CSR page table int32; seq_lens int32
     [B]; abort_mask uint8 [B] or None (no tracker)."""
     import torch
     _dev(q, k_cache, v_cache, page_indptr, page_indices, seq_lens, out, workspace, k_scale, v_scale, abort_mask)
-    fp8 = _is_byte_cache(k_cache)
-    _need(fp8 or k_cache.dtype == torch.bfloat16, "cache must be uint8 (e4m3) or bf16")
+    kv, D2 = _attn_cache(k_cache, v_cache, k_scale, v_scale)
     _need(q.dtype == torch.bfloat16 and out.dtype == torch.bfloat16, "q/out must be bf16")
     _need(seq_lens.dtype == torch.int32, "seq_lens must be int32")
     _need(abort_mask is None or abort_mask.dtype == torch.uint8, "abort_mask must be uint8")
     B, Hq, D = q.shape
-    P, Hkv, S, D2 = k_cache.shape
+    P, Hkv, S, _ = k_cache.shape
     _need(tuple(out.shape) == (B, Hq, D) and D2 == D and page_indptr.numel() == B + 1, "shape mismatch")
     _raise(load_library().paged_decode_attn(
-        _ptr(q), B, Hq, _ptr(k_cache), _ptr(v_cache), KV_FP8_E4M3 if fp8 else KV_BF16,
-        _ptr(k_scale) if fp8 else None, _ptr(v_scale) if fp8 else None, P, Hkv, S, D,
+        _ptr(q), B, Hq, _ptr(k_cache), _ptr(v_cache), kv,
+        _ptr(k_scale) if kv != KV_BF16 else None, _ptr(v_scale) if kv != KV_BF16 else None, P, Hkv, S, D,
         _ptr(page_indptr), _ptr(page_indices), page_indices.numel(), _ptr(seq_lens), _ptr(abort_mask),
         float(sm_scale),
         _ptr(out), _ptr(workspace), workspace.numel() * workspace.element_size(), _stream(stream)),
@@ -334,17 +549,16 @@ def paged_decode_attn_noalloc(q, k_cache, v_cache, page_indptr, page_indices, se
     scratch raise FkvError (status ERR_SCRATCH_LIMIT)."""
     import torch
     _dev(q, k_cache, v_cache, page_indptr, page_indices, seq_lens, out, k_scale, v_scale, abort_mask)
-    fp8 = _is_byte_cache(k_cache)
-    _need(fp8 or k_cache.dtype == torch.bfloat16, "cache must be uint8 (e4m3) or bf16")
+    kv, D2 = _attn_cache(k_cache, v_cache, k_scale, v_scale)
     _need(q.dtype == torch.bfloat16 and out.dtype == torch.bfloat16, "q/out must be bf16")
     _need(seq_lens.dtype == torch.int32, "seq_lens must be int32")
     _need(abort_mask is None or abort_mask.dtype == torch.uint8, "abort_mask must be uint8")
     B, Hq, D = q.shape
-    P, Hkv, S, D2 = k_cache.shape
+    P, Hkv, S, _ = k_cache.shape
     _need(tuple(out.shape) == (B, Hq, D) and D2 == D and page_indptr.numel() == B + 1, "shape mismatch")
     _raise(load_library().paged_decode_attn_noalloc(
-        _ptr(q), B, Hq, _ptr(k_cache), _ptr(v_cache), KV_FP8_E4M3 if fp8 else KV_BF16,
-        _ptr(k_scale) if fp8 else None, _ptr(v_scale) if fp8 else None, P, Hkv, S, D,
+        _ptr(q), B, Hq, _ptr(k_cache), _ptr(v_cache), kv,
+        _ptr(k_scale) if kv != KV_BF16 else None, _ptr(v_scale) if kv != KV_BF16 else None, P, Hkv, S, D,
         _ptr(page_indptr), _ptr(page_indices), page_indices.numel(), _ptr(seq_lens), _ptr(abort_mask),
         float(sm_scale), _ptr(out), _stream(stream)), "paged_decode_attn_noalloc")
     return out

@@ -46,7 +46,7 @@
 #include <cmath>
 #include <mutex>
 
-#include "fkv_common.cuh"
+#include "fp4_row.cuh"
 
 // Tokens per pipeline stage and ring depth of each KV dtype.
 #ifndef FKV_FP8_TILE
@@ -54,6 +54,12 @@
 #endif
 #ifndef FKV_FP8_STAGES
 #define FKV_FP8_STAGES 3
+#endif
+#ifndef FKV_FP4_TILE
+#define FKV_FP4_TILE 64
+#endif
+#ifndef FKV_FP4_STAGES
+#define FKV_FP4_STAGES 3
 #endif
 #ifndef FKV_BF16_TILE
 #define FKV_BF16_TILE 64
@@ -118,38 +124,51 @@ static_assert(kLocalPlanMax <= 1024, "one 32-request chunk per lane");
 // producer warp that issues copies and a consumer warp that computes.
 __host__ __device__ constexpr int attn_threads(bool ws) { return ws ? 64 : 32; }      // batches up to this size: each warp finds its own range
 
-template <bool kFp8>
+// kKv: the cache's format, an fkv_kv_dtype.
+template <int kKv>
 struct Cfg;
 template <>
-struct Cfg<true> {
+struct Cfg<FKV_KV_FP8_E4M3> {
     static constexpr int kTile = FKV_FP8_TILE;
     static constexpr int kStages = FKV_FP8_STAGES;
-    static constexpr int kHalves = 1;           // 128-byte-wide column blocks per token row
+    static constexpr int kHalves = 1;           // column blocks per token row
+    static constexpr int kRow = 128;            // bytes of a token row in one column block
 };
 template <>
-struct Cfg<false> {
+struct Cfg<FKV_KV_BF16> {
     static constexpr int kTile = FKV_BF16_TILE;
     static constexpr int kStages = FKV_BF16_STAGES;
     static constexpr int kHalves = 2;
+    static constexpr int kRow = 128;
+};
+template <>
+struct Cfg<FKV_KV_FP4> {
+    static constexpr int kTile = FKV_FP4_TILE;
+    static constexpr int kStages = FKV_FP4_STAGES;
+    static constexpr int kHalves = 1;
+    static constexpr int kRow = FKV_FP4_ROW_BYTES;
 };
 
-template <bool kFp8>
+template <int kKv>
 struct Layout {
-    static constexpr int kTile = Cfg<kFp8>::kTile;
-    static constexpr int kStages = Cfg<kFp8>::kStages;
-    static constexpr int kHalves = Cfg<kFp8>::kHalves;
-    static constexpr int kHalfBytes = kTile * 128;              // one column block of a K (or V) tile
+    static constexpr int kTile = Cfg<kKv>::kTile;
+    static constexpr int kStages = Cfg<kKv>::kStages;
+    static constexpr int kHalves = Cfg<kKv>::kHalves;
+    static constexpr int kRow = Cfg<kKv>::kRow;
+    static constexpr int kHalfBytes = kTile * kRow;             // one column block of a K (or V) tile
     static constexpr int kTileBytes = kHalves * kHalfBytes;     // a K (or V) tile
     static constexpr int kStageBytes = 2 * kTileBytes;          // K then V
     // stage buffers, then per stage a full and an empty mbarrier, the merge
     // mbarrier, and per stage a bad-page flag
     static constexpr int kSmem = 1024 + kStages * kStageBytes + 20 * kStages + 8;
     static_assert(kTile == 32 || kTile == 64, "tile of 32 or 64 tokens");
-    static_assert(kHalfBytes % 1024 == 0, "stage buffers stay 1024-byte aligned for the 128B swizzle");
+    static_assert(kKv == FKV_KV_FP4 || kHalfBytes % 1024 == 0, "stage buffers stay 1024-byte aligned for the 128B swizzle");
 };
 
 struct AttnParams {
     const __nv_bfloat16 *q;
+    const uint8_t *k_cache;    // the pools, for the 4-bit cache's untiled copies
+    const uint8_t *v_cache;
     const float *k_scale;
     const float *v_scale;
     const int32_t *indptr;
@@ -628,15 +647,24 @@ __device__ bool merge_parts_smem(const AttnParams &p, uint32_t sbuf, int cap, ui
     return true;
 }
 
+// Which of a lane's 16 output dims (in ascending order) the accumulator o[a]
+// holds in its rows g (half 0) and g + 8 (half 1).
+template <int kKv>
+__device__ constexpr int out_dim(int a, int half) {
+    return kKv == FKV_KV_FP4 ? 4 * (a >> 1) + 2 * half + (a & 1) : 2 * a + half;
+}
+
 // kAligned: the instance for batches of up to 64 requests, which gives units
 // whole warps (place_aligned) when the live requests' tiles pass its test and
 // uses the even split otherwise.  Larger batches use the instance without
 // the option (their warps do not hold the requests' rows).
-template <bool kFp8, bool kWS, bool kAligned>
+template <int kKv, bool kWS, bool kAligned>
 __global__ void __launch_bounds__(attn_threads(kWS), 1)
 paged_decode_attn_kernel(const AttnParams p, const __grid_constant__ CUtensorMap tmK,
                          const __grid_constant__ CUtensorMap tmV) {
-    using Lay = Layout<kFp8>;
+    using Lay = Layout<kKv>;
+    constexpr bool kFp8 = kKv == FKV_KV_FP8_E4M3, kFp4 = kKv == FKV_KV_FP4;
+    constexpr bool kScaled = kFp8 || kFp4;               // codes with per-head scales, computed in f16
     constexpr int kTile = Lay::kTile;
     constexpr int NST = Lay::kStages;
     constexpr int MT = kTile / 16;                       // 16-token MMA tiles per stage
@@ -668,8 +696,10 @@ paged_decode_attn_kernel(const AttnParams p, const __grid_constant__ CUtensorMap
         }
         mbar_init(merge_bar, 1);
         fence_mbar_init();
-        prefetch_tensormap(&tmK);
-        prefetch_tensormap(&tmV);
+        if (!kFp4) {
+            prefetch_tensormap(&tmK);
+            prefetch_tensormap(&tmV);
+        }
     }
     __syncthreads();
 
@@ -811,9 +841,28 @@ paged_decode_attn_kernel(const AttnParams p, const __grid_constant__ CUtensorMap
                 id = 0;
             }
             ids[k] = id;
-            bytes += 2u * rows * 128u * Lay::kHalves;
+            bytes += 2u * rows * Lay::kRow * Lay::kHalves;
         }
-        if (lane == 0) {
+        if (kFp4) {
+            // The rows of one (page, head) are contiguous, codes and scales
+            // together: one untiled copy of K and one of V per page, each issued
+            // by a lane of its own (0-3: K of pages 0-3, 4-7: V).  Sizes and
+            // addresses are multiples of 16: page rows come in multiples of 16.
+            const uint32_t bar = full_bars + 8 * stage;
+            if (lane == 0) {
+                st_shared_u32(bad_flags + 4 * stage, bad ? 1u : 0u);   // published by the arrive below
+                mbar_arrive_expect_tx(bar, bytes);
+            }
+            __syncwarp();
+            const int k = lane & 3;
+            const int id = k == 0 ? ids[0] : k == 1 ? ids[1] : k == 2 ? ids[2] : ids[3];
+            if (lane < 8 && id >= 0) {
+                const int64_t row = (static_cast<int64_t>(id) * (Hkv >> p.hshift) + (L.h >> p.hshift)) * S + rowoff;
+                const uint32_t dst = sbase + stage * Lay::kStageBytes + k * rows * Lay::kRow;
+                bulk_load_hint(lane < 4 ? dst : dst + Lay::kTileBytes,
+                               (lane < 4 ? p.k_cache : p.v_cache) + row * Lay::kRow, rows * Lay::kRow, bar, policy);
+            }
+        } else if (lane == 0) {
             const uint32_t bar = full_bars + 8 * stage;
             st_shared_u32(bad_flags + 4 * stage, bad ? 1u : 0u);   // published by the arrive below
             mbar_arrive_expect_tx(bar, bytes);
@@ -924,7 +973,7 @@ paged_decode_attn_kernel(const AttnParams p, const __grid_constant__ CUtensorMap
             cseq = __ldg(p.seq_lens + C.r);
             seg_start = C.tt;
             unit_bad = false;
-            cvsc = kFp8 ? __ldg(p.v_scale + (C.h >> p.hshift)) : 1.f;
+            cvsc = kScaled ? __ldg(p.v_scale + (C.h >> p.hshift)) : 1.f;
             // a unit that started in an earlier warp or ends in a later one is
             // split: find its parts now, off the merge's critical path
             // (the aligned schedule placed the warp's one unit already)
@@ -951,7 +1000,7 @@ paged_decode_attn_kernel(const AttnParams p, const __grid_constant__ CUtensorMap
             }
             const uint32_t qw[16] = {qv[0].x, qv[0].y, qv[0].z, qv[0].w, qv[1].x, qv[1].y, qv[1].z, qv[1].w,
                                      qv[2].x, qv[2].y, qv[2].z, qv[2].w, qv[3].x, qv[3].y, qv[3].z, qv[3].w};
-            if (kFp8) {
+            if (kScaled) {
                 // bf16 -> f16 with a power-of-two row scale so the row's largest
                 // magnitude lands in [2^14, 2^15): exact for every element within
                 // 2^-24 of it.  The scale is undone in the logit factor.
@@ -1011,10 +1060,14 @@ paged_decode_attn_kernel(const AttnParams p, const __grid_constant__ CUtensorMap
             // rows past the request's last token hold stale bytes: zero V there
             // (K rows are masked out of the softmax instead)
             const int nch = (kTile - nvalid) * 8;
+            if (kFp4) {                                    // zero scales make zero values of any codes
+                for (int c = nvalid + lane; c < kTile; c += 32) st_shared_v2_zero(vbase + c * Lay::kRow + kD / 2);
+            } else {
 #pragma unroll
-            for (int half = 0; half < Lay::kHalves; ++half)
-                for (int c = lane; c < nch; c += 32)
-                    st_shared_v4_zero(vbase + half * Lay::kHalfBytes + nvalid * 128 + c * 16);
+                for (int half = 0; half < Lay::kHalves; ++half)
+                    for (int c = lane; c < nch; c += 32)
+                        st_shared_v4_zero(vbase + half * Lay::kHalfBytes + nvalid * 128 + c * 16);
+            }
             fence_proxy_async_smem();
             __syncwarp();
         }
@@ -1039,6 +1092,26 @@ paged_decode_attn_kernel(const AttnParams p, const __grid_constant__ CUtensorMap
                 for (int ks = 0; ks < 8; ++ks) {
                     mma_f16(acc[ks % NACC], e4m3x2_to_f16x2(lo16(wa[ks])), e4m3x2_to_f16x2(lo16(wb[ks])),
                             e4m3x2_to_f16x2(hi16(wa[ks])), e4m3x2_to_f16x2(hi16(wb[ks])), qb[ks][0], qb[ks][1]);
+                }
+            } else if (kFp4) {
+                // This lane's 32 dims of rows ra, rb are the scale blocks t and
+                // 4 + t (8 bytes each).  code * scale is exact in f16: 2 and 4
+                // significant bits, magnitude 2^-10 .. 2688.
+                uint32_t ka[4], kb[4], sa[2], sb[2];
+                ld_fp4_row(kbase + ra * Lay::kRow, t, ka, sa);
+                ld_fp4_row(kbase + rb * Lay::kRow, t, kb, sb);
+#pragma unroll
+                for (int w2 = 0; w2 < 4; ++w2) {                     // word of 8 dims: k-steps 2 w2, 2 w2 + 1
+                    uint32_t fa[4], fb[4];
+                    e2m1x8_to_f16(ka[w2], fa);
+                    e2m1x8_to_f16(kb[w2], fb);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        fa[j] = mul_f16x2(fa[j], sa[w2 >> 1]);
+                        fb[j] = mul_f16x2(fb[j], sb[w2 >> 1]);
+                    }
+                    mma_f16(acc[0], fa[0], fb[0], fa[1], fb[1], qb[2 * w2][0], qb[2 * w2][1]);
+                    mma_f16(acc[NACC - 1], fa[2], fb[2], fa[3], fb[3], qb[2 * w2 + 1][0], qb[2 * w2 + 1][1]);
                 }
             } else {
                 // dims 16t..16t+15 (half 0, chunks 2t, 2t+1) and 64+16t.. (half 1)
@@ -1116,7 +1189,7 @@ paged_decode_attn_kernel(const AttnParams p, const __grid_constant__ CUtensorMap
         uint32_t pb[MT][2], pl[MT][2];
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt) {
-            if (kFp8) {
+            if (kScaled) {
                 pb[mt][0] = movmatrix_trans(pack_f16x2(pr[mt][0], pr[mt][1]));
                 pb[mt][1] = movmatrix_trans(pack_f16x2(pr[mt][2], pr[mt][3]));
                 pl[mt][0] = pl[mt][1] = 0u;
@@ -1155,6 +1228,28 @@ paged_decode_attn_kernel(const AttnParams p, const __grid_constant__ CUtensorMap
                             e4m3x2_to_f16x2(lo16(cd0)), e4m3x2_to_f16x2(hi16(cd0)), pb[mt][0], pb[mt][1]);
                     mma_f16(o[2 * qq + 1], e4m3x2_to_f16x2(lo16(ab1)), e4m3x2_to_f16x2(hi16(ab1)),
                             e4m3x2_to_f16x2(lo16(cd1)), e4m3x2_to_f16x2(hi16(cd1)), pb[mt][0], pb[mt][1]);
+                }
+            } else if (kFp4) {
+                // A byte holds dims 2j, 2j + 1 of one token, so a converted pair
+                // cannot feed the MMA's K axis (tokens) directly.  Instead the K
+                // axis takes (token, parity) slots: M is the 64 dim pairs, an
+                // MMA step covers 8 tokens, and P goes in twice, beside zeros,
+                // once against the even dims and once against the odd ones.
+                // That doubles the PV MMAs and saves regrouping nibbles, which
+                // costs 7 ALU operations per 8 values against this one's none.
+#pragma unroll
+                for (int hf = 0; hf < 2; ++hf) {                     // tokens 8 hf .. 8 hf + 7 of the 16
+                    const uint32_t v0 = vbase + (r0 + 8 * hf) * Lay::kRow, v1 = v0 + Lay::kRow;
+                    uint32_t x0[8], x1[8];
+                    ld_fp4_block(v0, g, x0);                         // dims 16g .. 16g+15 of tokens r0, r1
+                    ld_fp4_block(v1, g, x1);
+                    const uint32_t pp = pb[mt][hf];
+                    const uint32_t e0 = pp & 0xFFFFu, e1 = pp >> 16, o0 = pp << 16, o1 = pp & 0xFFFF0000u;
+#pragma unroll
+                    for (int a = 0; a < 4; ++a) {
+                        mma_f16(o[2 * a], x0[2 * a], x0[2 * a + 1], x1[2 * a], x1[2 * a + 1], e0, e1);
+                        mma_f16(o[2 * a + 1], x0[2 * a], x0[2 * a + 1], x1[2 * a], x1[2 * a + 1], o0, o1);
+                    }
                 }
             } else {
                 // dims 8g..8g+7 (half 0, chunk g) and 64+8g.. (half 1, chunk g)
@@ -1222,7 +1317,7 @@ paged_decode_attn_kernel(const AttnParams p, const __grid_constant__ CUtensorMap
             // row's bytes equal those of the merge through the stage ring.
             // The caller has acquired every other part.
             auto merge_regs = [&](int64_t u) {
-                const int d0 = kFp8 ? 16 * g : 8 * g, d1 = kFp8 ? 16 * g + 8 : 64 + 8 * g;
+                const int d0 = kScaled ? 16 * g : 8 * g, d1 = kScaled ? 16 * g + 8 : 64 + 8 * g;
                 int64_t x0 = 0, x1 = 0;                       // the other parts, in index order
                 int no = 0;
                 for (int64_t x = cgm.wf; x < cgm.wf + cgm.span; ++x) {
@@ -1268,8 +1363,8 @@ paged_decode_attn_kernel(const AttnParams p, const __grid_constant__ CUtensorMap
                     Lj[j] = __fmaf_rn(0.f, 0.f, sl);
 #pragma unroll
                     for (int a = 0; a < 8; ++a) {
-                        v[j][2 * a] = __fmaf_rn(w0, o[a][j], 0.f);
-                        v[j][2 * a + 1] = __fmaf_rn(w0, o[a][2 + j], 0.f);
+                        v[j][out_dim<kKv>(a, 0)] = __fmaf_rn(w0, o[a][j], 0.f);
+                        v[j][out_dim<kKv>(a, 1)] = __fmaf_rn(w0, o[a][2 + j], 0.f);
                     }
                 }
                 for (int k = 0; k < no; ++k) {
@@ -1338,11 +1433,11 @@ paged_decode_attn_kernel(const AttnParams p, const __grid_constant__ CUtensorMap
                 float v[16];
 #pragma unroll
                 for (int a = 0; a < 8; ++a) {
-                    v[2 * a] = o[a][j];
-                    v[2 * a + 1] = o[a][2 + j];
+                    v[out_dim<kKv>(a, 0)] = o[a][j];
+                    v[out_dim<kKv>(a, 1)] = o[a][2 + j];
                 }
-                const int d0 = kFp8 ? 16 * g : 8 * g;          // first run of dims
-                const int d1 = kFp8 ? 16 * g + 8 : 64 + 8 * g; // second run (8 dims each)
+                const int d0 = kScaled ? 16 * g : 8 * g;          // first run of dims
+                const int d1 = kScaled ? 16 * g + 8 : 64 + 8 * g; // second run (8 dims each)
                 if (whole) {
                     const float f = cvsc / lt[j];
                     __nv_bfloat16 *orow = p.out + (static_cast<int64_t>(C.r) * p.Hq + C.h * G + hd) * kD;
@@ -1423,14 +1518,14 @@ namespace {
 
 constexpr int kMaxDev = 64;
 std::mutex g_mu;
-// Resident CTAs per SM, [dev][kv_fp8][ws], with the id of the context in
+// Resident CTAs per SM, [dev][kv_dtype][ws], with the id of the context in
 // which the kernels' shared-memory limit was raised: a new context (after
 // cudaDeviceReset) loads the kernels again, so the attribute is set again.
 struct CtasPerSm {
     unsigned long long ctx_id;
     int n;
 };
-CtasPerSm g_ctas_per_sm[kMaxDev][2][2];
+CtasPerSm g_ctas_per_sm[kMaxDev][3][2];
 
 PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
     static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
@@ -1446,22 +1541,22 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
     return fn;
 }
 
-template <bool kFp8, bool kWS>
+template <int kKv, bool kWS>
 int ctas_per_sm() {
     int dev = -1;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDev) return 0;
     std::lock_guard<std::mutex> lk(g_mu);
-    CtasPerSm &c = g_ctas_per_sm[dev][kFp8 ? 1 : 0][kWS ? 1 : 0];
+    CtasPerSm &c = g_ctas_per_sm[dev][kKv][kWS ? 1 : 0];
     const unsigned long long ctx = current_context_id();
     if (!c.n || ctx == 0 || ctx != c.ctx_id) {
-        const int smem = Layout<kFp8>::kSmem;
-        if (cudaFuncSetAttribute(paged_decode_attn_kernel<kFp8, kWS, false>,
+        const int smem = Layout<kKv>::kSmem;
+        if (cudaFuncSetAttribute(paged_decode_attn_kernel<kKv, kWS, false>,
                                  cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess ||
-            cudaFuncSetAttribute(paged_decode_attn_kernel<kFp8, kWS, true>,
+            cudaFuncSetAttribute(paged_decode_attn_kernel<kKv, kWS, true>,
                                  cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
             return 0;
         int nb = 0;
-        if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&nb, paged_decode_attn_kernel<kFp8, kWS, false>,
+        if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&nb, paged_decode_attn_kernel<kKv, kWS, false>,
                                                           attn_threads(kWS), smem) != cudaSuccess ||
             nb <= 0)
             return 0;
@@ -1472,31 +1567,45 @@ int ctas_per_sm() {
 }
 
 // Computing warps of one launch (one per CTA).
-int grid_warps(bool fp8, bool ws) {
-    const int sms = device_sm_count();
-    const int per = fp8 ? (ws ? ctas_per_sm<true, true>() : ctas_per_sm<true, false>())
-                        : (ws ? ctas_per_sm<false, true>() : ctas_per_sm<false, false>());
-    return sms * per;
+template <int kKv>
+int grid_warps_of(bool ws) {
+    return device_sm_count() * (ws ? ctas_per_sm<kKv, true>() : ctas_per_sm<kKv, false>());
 }
+int grid_warps(int kv, bool ws) {
+    return kv == FKV_KV_FP8_E4M3 ? grid_warps_of<FKV_KV_FP8_E4M3>(ws)
+           : kv == FKV_KV_BF16   ? grid_warps_of<FKV_KV_BF16>(ws)
+                                 : grid_warps_of<FKV_KV_FP4>(ws);
+}
+
+int tile_tokens(int kv) {
+    return kv == FKV_KV_FP8_E4M3 ? Layout<FKV_KV_FP8_E4M3>::kTile
+           : kv == FKV_KV_BF16   ? Layout<FKV_KV_BF16>::kTile
+                                 : Layout<FKV_KV_FP4>::kTile;
+}
+
+bool known_kv(int kv) { return kv == FKV_KV_FP8_E4M3 || kv == FKV_KV_BF16 || kv == FKV_KV_FP4; }
 
 // The two-warp CTA when a tile spans several pages (page sizes below
 // FKV_WS_PAGE_LIMIT, by default the tile).
 #ifndef FKV_WS_PAGE_LIMIT
 #define FKV_WS_PAGE_LIMIT 64
 #endif
-bool use_ws(int page_size, bool fp8) {
-    const int tile = fp8 ? Layout<true>::kTile : Layout<false>::kTile;
+bool use_ws(int page_size, int kv) {
+    const int tile = tile_tokens(kv);
     return page_size < (FKV_WS_PAGE_LIMIT < tile ? FKV_WS_PAGE_LIMIT : tile);
 }
 
-template <bool kFp8, bool kWS>
-cudaError_t launch_attn(bool aligned, dim3 grid, cudaStream_t st, const AttnParams &p, const CUtensorMap &tmK,
+template <int kKv>
+cudaError_t launch_attn(bool two_warp, bool aligned, dim3 grid, cudaStream_t st, const AttnParams &p, const CUtensorMap &tmK,
                         const CUtensorMap &tmV) {
-    const dim3 block(attn_threads(kWS));
-    return aligned ? launch_pdl(paged_decode_attn_kernel<kFp8, kWS, true>, grid, block, Layout<kFp8>::kSmem, st, p,
-                                tmK, tmV)
-                   : launch_pdl(paged_decode_attn_kernel<kFp8, kWS, false>, grid, block, Layout<kFp8>::kSmem, st, p,
-                                tmK, tmV);
+    auto go = [&](auto kern, bool ws) {
+        return launch_pdl(kern, grid, dim3(attn_threads(ws)), Layout<kKv>::kSmem, st, p, tmK, tmV);
+    };
+    if (two_warp)
+        return aligned ? go(paged_decode_attn_kernel<kKv, true, true>, true)
+                       : go(paged_decode_attn_kernel<kKv, true, false>, true);
+    return aligned ? go(paged_decode_attn_kernel<kKv, false, true>, false)
+                   : go(paged_decode_attn_kernel<kKv, false, false>, false);
 }
 
 size_t align256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
@@ -1552,12 +1661,11 @@ using namespace fkv;
 extern "C" size_t paged_decode_attn_workspace_size(int32_t batch, int32_t num_q_heads, int32_t num_kv_heads,
                                                    int32_t head_dim, int32_t kv_dtype) {
     if (batch < 0 || num_q_heads <= 0 || num_kv_heads <= 0 || num_q_heads % num_kv_heads) return 0;
-    if (head_dim != kD || (kv_dtype != FKV_KV_FP8_E4M3 && kv_dtype != FKV_KV_BF16)) return 0;
+    if (head_dim != kD || !known_kv(kv_dtype)) return 0;
     const int R = group_split(num_q_heads / num_kv_heads);
     if (R == 0) return 0;
     // sized for either CTA shape (the page size is not known here)
-    const bool fp8 = kv_dtype == FKV_KV_FP8_E4M3;
-    const int n1 = grid_warps(fp8, false), n2 = grid_warps(fp8, true);
+    const int n1 = grid_warps(kv_dtype, false), n2 = grid_warps(kv_dtype, true);
     const int NW = n1 > n2 ? n1 : n2;
     if (n1 <= 0 || n2 <= 0) return 0;
     return ws_layout(batch, num_kv_heads * R, num_q_heads / num_kv_heads / R, NW).total;
@@ -1572,7 +1680,7 @@ extern "C" fkv_status paged_decode_attn(const void *q, int32_t batch, int32_t nu
                                         size_t workspace_bytes, void *stream) {
     if (batch < 0 || num_q_heads <= 0 || num_kv_heads <= 0 || num_pages <= 0 || nnz < 0) return FKV_ERR_INVALID_ARG;
     if (num_q_heads % num_kv_heads) return FKV_ERR_INVALID_ARG;
-    if (kv_dtype != FKV_KV_FP8_E4M3 && kv_dtype != FKV_KV_BF16) return FKV_ERR_INVALID_ARG;
+    if (!known_kv(kv_dtype)) return FKV_ERR_INVALID_ARG;
     if (head_dim != kD) return FKV_ERR_UNSUPPORTED;
     if (page_size != 16 && page_size != 32 && page_size != 64 && page_size != 128) return FKV_ERR_UNSUPPORTED;
     // units are (request, virtual KV head) pairs of G query heads each
@@ -1584,26 +1692,29 @@ extern "C" fkv_status paged_decode_attn(const void *q, int32_t batch, int32_t nu
     const bool fp8 = kv_dtype == FKV_KV_FP8_E4M3;
     if (!q || !k_cache || !v_cache || !page_indptr || !seq_lens || !out || !workspace) return FKV_ERR_INVALID_ARG;
     if (nnz > 0 && !page_indices) return FKV_ERR_INVALID_ARG;
-    if (fp8 && (!k_scale || !v_scale)) return FKV_ERR_INVALID_ARG;
+    if (kv_dtype != FKV_KV_BF16 && (!k_scale || !v_scale)) return FKV_ERR_INVALID_ARG;
     if (!aligned16(q) || !aligned16(k_cache) || !aligned16(v_cache) || !aligned16(out) ||
         (reinterpret_cast<uintptr_t>(workspace) & 255u))
         return FKV_ERR_INVALID_ARG;
-    const bool two_warp = use_ws(page_size, fp8);
-    const int NW = grid_warps(fp8, two_warp);
+    const bool two_warp = use_ws(page_size, kv_dtype);
+    const int NW = grid_warps(kv_dtype, two_warp);
     uint32_t *err = device_error_word();
     if (NW <= 0 || !err) return FKV_ERR_CUDA;
     const WsLayout wl = ws_layout(batch, Hv, G, NW);
     if (workspace_bytes < wl.total) return FKV_ERR_INVALID_ARG;
-    const int tile = fp8 ? Layout<true>::kTile : Layout<false>::kTile;
+    const int tile = tile_tokens(kv_dtype);
 
-    CUtensorMap tmK, tmV;
-    if (!make_kv_map(&tmK, k_cache, fp8, num_pages, num_kv_heads, page_size, tile) ||
-        !make_kv_map(&tmV, v_cache, fp8, num_pages, num_kv_heads, page_size, tile))
+    CUtensorMap tmK = {}, tmV = {};                    // unused by the 4-bit cache's untiled copies
+    if (kv_dtype != FKV_KV_FP4 &&
+        (!make_kv_map(&tmK, k_cache, fp8, num_pages, num_kv_heads, page_size, tile) ||
+         !make_kv_map(&tmV, v_cache, fp8, num_pages, num_kv_heads, page_size, tile)))
         return FKV_ERR_CUDA;
 
     uint8_t *ws = static_cast<uint8_t *>(workspace);
     AttnParams p;
     p.q = static_cast<const __nv_bfloat16 *>(q);
+    p.k_cache = static_cast<const uint8_t *>(k_cache);
+    p.v_cache = static_cast<const uint8_t *>(v_cache);
     p.k_scale = k_scale;
     p.v_scale = v_scale;
     p.indptr = page_indptr;
@@ -1642,14 +1753,12 @@ extern "C" fkv_status paged_decode_attn(const void *q, int32_t batch, int32_t nu
     // aborted or empty requests.
     const bool aligned = FKV_ALIGNED_SCHEDULE && batch <= 64;
     const dim3 grid(NW);
-    if (fp8 && two_warp)
-        e = launch_attn<true, true>(aligned, grid, st, p, tmK, tmV);
-    else if (fp8)
-        e = launch_attn<true, false>(aligned, grid, st, p, tmK, tmV);
-    else if (two_warp)
-        e = launch_attn<false, true>(aligned, grid, st, p, tmK, tmV);
+    if (fp8)
+        e = launch_attn<FKV_KV_FP8_E4M3>(two_warp, aligned, grid, st, p, tmK, tmV);
+    else if (kv_dtype == FKV_KV_BF16)
+        e = launch_attn<FKV_KV_BF16>(two_warp, aligned, grid, st, p, tmK, tmV);
     else
-        e = launch_attn<false, false>(aligned, grid, st, p, tmK, tmV);
+        e = launch_attn<FKV_KV_FP4>(two_warp, aligned, grid, st, p, tmK, tmV);
     if (e != cudaSuccess) return FKV_ERR_CUDA;
     return FKV_OK;
 }

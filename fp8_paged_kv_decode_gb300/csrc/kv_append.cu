@@ -13,6 +13,7 @@
 // work is tiny (one token per request); for a bulk prefill write it is plain
 // bandwidth, provided the arithmetic per element stays small -- hence the
 // division below.
+#include "fp4_row.cuh"
 #include "tag_check_row.cuh"
 
 namespace fkv {
@@ -53,8 +54,8 @@ constexpr int kTokensPerBlock = kBlock / kThreadsPerToken;   // 16
 // the scalar instruction does: 1.4 % faster on a bulk write than the scalar
 // sequence.  word holds two bf16 elements (low half = lower element); they
 // are widened to fp32 with their sign bits cleared.  nb = (-b, -b), yy = (y, y);
-// the result is the two e4m3 codes of |word|, the lower element in the low byte.
-__device__ __forceinline__ uint16_t div2_abs_to_e4m3x2(uint32_t word, uint64_t nb, uint64_t yy) {
+// the result is the two quotients of |word| (x: the lower element).
+__device__ __forceinline__ float2 div2_abs(uint32_t word, uint64_t nb, uint64_t yy) {
     const uint32_t wm = word & 0x7FFF7FFFu;
     uint64_t m, q0, r, q;
     asm("mov.b64 %0, {%1, %2};" : "=l"(m) : "r"(wm << 16), "r"(wm & 0xFFFF0000u));
@@ -63,7 +64,12 @@ __device__ __forceinline__ uint16_t div2_abs_to_e4m3x2(uint32_t word, uint64_t n
     asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(q) : "l"(r), "l"(yy), "l"(q0));
     uint32_t lo, hi;
     asm("mov.b64 {%0, %1}, %2;" : "=r"(lo), "=r"(hi) : "l"(q));
-    return f32x2_to_e4m3x2(__uint_as_float(hi), __uint_as_float(lo));
+    return make_float2(__uint_as_float(lo), __uint_as_float(hi));
+}
+
+__device__ __forceinline__ uint16_t div2_abs_to_e4m3x2(uint32_t word, uint64_t nb, uint64_t yy) {
+    const float2 q = div2_abs(word, nb, yy);
+    return f32x2_to_e4m3x2(q.y, q.x);
 }
 
 // Lane-wise maximum of two pairs of unsigned 16-bit values.
@@ -84,10 +90,10 @@ __device__ __forceinline__ int64_t token_of(int64_t n_tokens, unsigned bx) {
     return n < n_tokens ? n : -1;
 }
 
-// Element offset of the (slot, KV head by) row in the pool, or -1: nothing
+// Index of the (slot, KV head by) row in the pool, or -1: nothing
 // to write (a padding slot, or one outside the pool, which is recorded).
-__device__ __forceinline__ int64_t slot_offset(int64_t slot, int32_t num_pages, int32_t num_kv_heads,
-                                               int32_t page_size, int32_t page_shift, uint32_t *err, unsigned by) {
+__device__ __forceinline__ int64_t slot_row(int64_t slot, int32_t num_pages, int32_t num_kv_heads,
+                                            int32_t page_size, int32_t page_shift, uint32_t *err, unsigned by) {
     if (slot < 0) return -1;                                      // padding token
     const int64_t page = page_shift >= 0 ? (slot >> page_shift) : slot / page_size;
     const int64_t off = slot - page * page_size;
@@ -95,7 +101,14 @@ __device__ __forceinline__ int64_t slot_offset(int64_t slot, int32_t num_pages, 
         if ((threadIdx.x % kThreadsPerToken) == 0) atomicOr(err, FKV_DEVERR_APPEND_SLOT);
         return -1;
     }
-    return ((page * num_kv_heads + by) * page_size + off) * kHeadDim;
+    return (page * num_kv_heads + by) * page_size + off;
+}
+
+// The same as the row's first element, for rows of kHeadDim elements.
+__device__ __forceinline__ int64_t slot_offset(int64_t slot, int32_t num_pages, int32_t num_kv_heads,
+                                               int32_t page_size, int32_t page_shift, uint32_t *err, unsigned by) {
+    const int64_t row = slot_row(slot, num_pages, num_kv_heads, page_size, page_shift, err, by);
+    return row < 0 ? -1 : row * kHeadDim;
 }
 
 // The e4m3 codes of one thread's 16 bf16 elements (two uint4 of the row, in
@@ -272,6 +285,118 @@ kv_append_bf16_tag_check_kernel(const uint4 *__restrict__ k_new, const uint4 *__
                      page_shift, err, a % append_blocks_x, a / append_blocks_x);
 }
 
+// ---------------------------------------------------------------------------
+// The 4-bit cache.  The same threads and loads as the FP8 append: a thread's
+// 16 elements are one scale block, so the block's maximum, scale and codes need
+// no other thread.  Per (token, KV head): 512 bytes in, 144 out.
+// ---------------------------------------------------------------------------
+// The 16 codes (8 bytes) and the scale byte of one block of bf16 elements, for
+// the KV head's scale g.  The quotients are IEEE divisions, by div2_abs where
+// its range holds (see there), with the sign put back on the quotient.
+__device__ __forceinline__ uint2 encode_fp4_16(const uint4 r0, const uint4 r1, float g, uint32_t &scale) {
+    const uint32_t w[8] = {r0.x, r0.y, r0.z, r0.w, r1.x, r1.y, r1.z, r1.w};
+    uint32_t big = 0;                                          // largest |x| bit patterns, per half
+#pragma unroll
+    for (int j = 0; j < 8; ++j) big = max_u16x2(big, w[j] & 0x7FFF7FFFu);
+    big = max(big >> 16, big & 0xFFFFu);                       // a NaN's pattern is above every other
+    const float amax = __uint_as_float(big << 16);
+    scale = f32x2_to_e4m3x2(0.f, __fdiv_rn(amax, __fmul_rn(6.f, g))) & 0xFFu;
+    const uint32_t s16 = e4m3x2_to_f16x2(static_cast<uint16_t>(scale));
+    const float d = __fmul_rn(__half2float(__ushort_as_half(static_cast<unsigned short>(s16 & 0xFFFFu))), g);
+    if (!(d > 0.f)) return make_uint2(0u, 0u);                 // scale 0 or NaN
+    uint32_t code[8];                                          // two codes each
+    if (recip_scale_ok(d) && big <= 0x5F80u) {                 // |x| <= 2^64
+        const float y = __frcp_rn(d);
+        uint64_t nb, yy;
+        asm("mov.b64 %0, {%1, %1};" : "=l"(nb) : "r"(__float_as_uint(-d)));
+        asm("mov.b64 %0, {%1, %1};" : "=l"(yy) : "r"(__float_as_uint(y)));
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const float2 q = div2_abs(w[j], nb, yy);
+            code[j] = f32x2_to_e2m1x2(__uint_as_float(__float_as_uint(q.y) | (w[j] & 0x80000000u)),
+                                      __uint_as_float(__float_as_uint(q.x) | ((w[j] << 16) & 0x80000000u)));
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            code[j] = f32x2_to_e2m1x2(__fdiv_rn(__uint_as_float(w[j] & 0xFFFF0000u), d),
+                                      __fdiv_rn(__uint_as_float(w[j] << 16), d));
+    }
+    return make_uint2(code[0] | (code[1] << 8) | (code[2] << 16) | (code[3] << 24),
+                      code[4] | (code[5] << 8) | (code[6] << 16) | (code[7] << 24));
+}
+
+// One thread's share of the 4-bit append in block (bx, by).
+__device__ __forceinline__ void append_fp4_part(const uint4 *__restrict__ k_new, const uint4 *__restrict__ v_new,
+                                                const int64_t *__restrict__ slots, int64_t n_tokens,
+                                                const float *__restrict__ k_scale, const float *__restrict__ v_scale,
+                                                uint8_t *__restrict__ k_cache, uint8_t *__restrict__ v_cache,
+                                                int32_t num_pages, int32_t num_kv_heads, int32_t page_size,
+                                                int32_t page_shift, uint32_t *err, unsigned bx, unsigned by) {
+    const int64_t n = token_of(n_tokens, bx);
+    if (n < 0) return;
+    const int h = by;
+    const int sub = threadIdx.x % kThreadsPerToken;
+    const bool is_v = sub >= kThreadsPerRow;
+    const int chunk = sub % kThreadsPerRow;
+    const uint4 *src = (is_v ? v_new : k_new) + (n * num_kv_heads + h) * (kHeadDim / 8) + chunk * 2;
+    const uint4 r0 = __ldcs(src), r1 = __ldcs(src + 1);        // in flight with the scale's and the slot's loads
+    const float g = __ldg((is_v ? v_scale : k_scale) + h);
+    const int64_t slot = __ldg(slots + n);
+    const int64_t row = slot_row(slot, num_pages, num_kv_heads, page_size, page_shift, err, by);
+    if (row < 0) return;
+    uint32_t s;
+    const uint2 codes = encode_fp4_16(r0, r1, g, s);
+    uint8_t *dst = (is_v ? v_cache : k_cache) + row * kFp4Row;
+    __stcs(reinterpret_cast<uint2 *>(dst) + chunk, codes);
+    // the row's 8 scale bytes: four lanes' bytes make a word (the 8 threads of a
+    // row take the same branches, so their mask is whole)
+    const unsigned mask = 0xFFu << (threadIdx.x & 24u);
+    uint32_t word = s << (8 * (chunk & 3));
+    word |= __shfl_xor_sync(mask, word, 1);
+    word |= __shfl_xor_sync(mask, word, 2);
+    if ((chunk & 3) == 0) __stcs(reinterpret_cast<uint32_t *>(dst + kFp4Codes + chunk), word);
+}
+
+__global__ void __launch_bounds__(kBlock, FKV_APPEND_MIN_BLOCKS)
+kv_append_fp4_kernel(const uint4 *__restrict__ k_new, const uint4 *__restrict__ v_new,
+                     const int64_t *__restrict__ slots, int64_t n_tokens,
+                     const float *__restrict__ k_scale, const float *__restrict__ v_scale,
+                     uint8_t *__restrict__ k_cache, uint8_t *__restrict__ v_cache,
+                     int32_t num_pages, int32_t num_kv_heads, int32_t page_size, int32_t page_shift,
+                     uint32_t *err) {
+    grid_dep_wait();        // earlier readers of the pool (attention) have finished
+    grid_dep_launch();
+    append_fp4_part(k_new, v_new, slots, n_tokens, k_scale, v_scale, k_cache, v_cache, num_pages, num_kv_heads,
+                    page_size, page_shift, err, blockIdx.x, blockIdx.y);
+}
+
+// The 4-bit cache's step prologue in one launch, laid out like
+// kv_append_fp8_tag_check_kernel: check blocks first, then the append's.
+__global__ void __launch_bounds__(kBlock, FKV_APPEND_MIN_BLOCKS)
+kv_append_fp4_tag_check_kernel(const uint4 *__restrict__ k_new, const uint4 *__restrict__ v_new,
+                               const int64_t *__restrict__ slots, int64_t n_tokens,
+                               const float *__restrict__ k_scale, const float *__restrict__ v_scale,
+                               uint8_t *__restrict__ k_cache, uint8_t *__restrict__ v_cache,
+                               int32_t num_pages, int32_t num_kv_heads, int32_t page_size, int32_t page_shift,
+                               uint32_t *err, unsigned append_blocks_x,
+                               const uint32_t *__restrict__ page_tags, const int32_t *__restrict__ page_indptr,
+                               const int32_t *__restrict__ page_indices, const uint32_t *__restrict__ expected_tags,
+                               int32_t batch, int64_t nnz, uint8_t *__restrict__ abort_mask) {
+    grid_dep_wait();        // earlier kernels' tags, tables and pool readers are done
+    grid_dep_launch();
+    const unsigned b = blockIdx.x;
+    if (b < static_cast<unsigned>(batch)) {
+        const int bad = tag_check_row<kBlock>(page_tags, num_pages, page_indptr, page_indices, expected_tags, nnz,
+                                              static_cast<int>(b));
+        if (threadIdx.x == 0) abort_mask[b] = bad ? 1 : 0;
+        return;
+    }
+    const unsigned a = b - static_cast<unsigned>(batch);
+    append_fp4_part(k_new, v_new, slots, n_tokens, k_scale, v_scale, k_cache, v_cache, num_pages, num_kv_heads,
+                    page_size, page_shift, err, a % append_blocks_x, a / append_blocks_x);
+}
+
 static fkv_status check_append_args(const void *k_new, const void *v_new, const int64_t *slot_mapping,
                                     int32_t n_tokens, const void *k_cache, const void *v_cache,
                                     int32_t num_pages, int32_t num_kv_heads, int32_t page_size,
@@ -409,5 +534,50 @@ extern "C" fkv_status kv_append_bf16_tag_check(const void *k_new, const void *v_
                                      static_cast<uint4 *>(v_cache), num_pages, num_kv_heads, page_size,
                                      page_shift_of(page_size), err, static_cast<unsigned>(gx > 0 ? gx : 1),
                                      page_tags, page_indptr, page_indices, expected_tags, batch, nnz, abort_mask);
+    return e == cudaSuccess ? FKV_OK : FKV_ERR_CUDA;
+}
+
+extern "C" fkv_status kv_append_fp4(const void *k_new, const void *v_new, const int64_t *slot_mapping,
+                                    int32_t n_tokens, const float *k_scale, const float *v_scale,
+                                    uint8_t *k_cache, uint8_t *v_cache, int32_t num_pages,
+                                    int32_t num_kv_heads, int32_t page_size, int32_t head_dim,
+                                    void *stream) {
+    fkv_status st = check_append_args(k_new, v_new, slot_mapping, n_tokens, k_cache, v_cache, num_pages,
+                                      num_kv_heads, page_size, head_dim);
+    if (st != FKV_OK || n_tokens == 0) return st;
+    if (!k_scale || !v_scale) return FKV_ERR_INVALID_ARG;
+    uint32_t *err = device_error_word();
+    if (!err) return FKV_ERR_CUDA;
+    const cudaError_t e = launch_pdl(kv_append_fp4_kernel, append_grid(n_tokens, num_kv_heads), dim3(kBlock), 0,
+                                     static_cast<cudaStream_t>(stream), static_cast<const uint4 *>(k_new),
+                                     static_cast<const uint4 *>(v_new), slot_mapping, static_cast<int64_t>(n_tokens),
+                                     k_scale, v_scale, k_cache, v_cache, num_pages, num_kv_heads, page_size,
+                                     page_shift_of(page_size), err);
+    return e == cudaSuccess ? FKV_OK : FKV_ERR_CUDA;
+}
+
+extern "C" fkv_status kv_append_fp4_tag_check(const void *k_new, const void *v_new, const int64_t *slot_mapping,
+                                              int32_t n_tokens, const float *k_scale, const float *v_scale,
+                                              uint8_t *k_cache, uint8_t *v_cache, int32_t num_pages,
+                                              int32_t num_kv_heads, int32_t page_size, int32_t head_dim,
+                                              const uint32_t *page_tags, const int32_t *page_indptr,
+                                              const int32_t *page_indices, const uint32_t *expected_tags,
+                                              int32_t batch, int64_t nnz, uint8_t *abort_mask, void *stream) {
+    int64_t gx = 0, blocks = 0;
+    const fkv_status st = check_combined_args(k_new, v_new, slot_mapping, n_tokens, k_cache, v_cache, num_pages,
+                                              num_kv_heads, page_size, head_dim, page_tags, page_indptr,
+                                              page_indices, expected_tags, batch, nnz, abort_mask, gx, blocks);
+    if (st != FKV_OK) return st;
+    if (n_tokens > 0 && (!k_scale || !v_scale)) return FKV_ERR_INVALID_ARG;
+    if (blocks == 0) return FKV_OK;
+    uint32_t *err = device_error_word();
+    if (!err) return FKV_ERR_CUDA;
+    const cudaError_t e = launch_pdl(kv_append_fp4_tag_check_kernel, dim3(static_cast<unsigned>(blocks)),
+                                     dim3(kBlock), 0, static_cast<cudaStream_t>(stream),
+                                     static_cast<const uint4 *>(k_new), static_cast<const uint4 *>(v_new),
+                                     slot_mapping, static_cast<int64_t>(n_tokens), k_scale, v_scale, k_cache,
+                                     v_cache, num_pages, num_kv_heads, page_size, page_shift_of(page_size), err,
+                                     static_cast<unsigned>(gx > 0 ? gx : 1), page_tags, page_indptr, page_indices,
+                                     expected_tags, batch, nnz, abort_mask);
     return e == cudaSuccess ? FKV_OK : FKV_ERR_CUDA;
 }

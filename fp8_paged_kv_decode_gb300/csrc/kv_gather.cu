@@ -1,0 +1,123 @@
+// kv_gather.cu -- cached tokens read back as bf16 rows.
+//
+// A prompt's next chunk, or a request that reuses a cached prefix, attends over
+// cached tokens outside the decode kernel and needs them dense.  For each listed
+// slot and KV head: value * scale in fp32, one rounding to bf16 (BF16 rows are
+// copied).  e4m3 codes and e2m1 code * block scale are exact in f16, so the
+// product with the head's scale is the only fp32 rounding before bf16's.
+//
+// Layout as in the append: grid of (16-token groups, KV heads), 16 threads per
+// (token, head), 8 on its K row and 8 on its V row, 16 elements each, so a
+// 4-bit thread reads one scale block.  Bound by memory: per (token, KV head)
+// 512 bytes out and 144 (FP4), 256 (FP8) or 512 (BF16) in.
+#include "fp4_row.cuh"
+
+namespace fkv {
+
+constexpr int kGatherBlock = 256;
+constexpr int kGatherTokens = kGatherBlock / 16;
+
+// Two f16 values times the head's scale, rounded to bf16.
+__device__ __forceinline__ uint32_t scaled_bf16x2(uint32_t f16x2, float g) {
+    const __half2 h = *reinterpret_cast<const __half2 *>(&f16x2);
+    const float2 f = __half22float2(h);
+    return pack_bf16x2(__fmul_rn(f.x, g), __fmul_rn(f.y, g));
+}
+
+template <int kKv>
+__global__ void __launch_bounds__(kGatherBlock)
+kv_gather_kernel(const uint8_t *__restrict__ k_cache, const uint8_t *__restrict__ v_cache,
+                 const float *__restrict__ k_scale, const float *__restrict__ v_scale,
+                 const int64_t *__restrict__ slots, int32_t n_tokens, uint4 *__restrict__ k_out,
+                 uint4 *__restrict__ v_out, int32_t num_pages, int32_t num_kv_heads, int32_t page_size,
+                 int32_t page_shift, uint32_t *err) {
+    grid_dep_wait();
+    grid_dep_launch();
+    const int64_t n = static_cast<int64_t>(blockIdx.x) * kGatherTokens + threadIdx.x / 16;
+    if (n >= n_tokens) return;
+    const int h = blockIdx.y;
+    const bool is_v = (threadIdx.x & 8) != 0;
+    const int chunk = threadIdx.x & 7;
+    const int64_t slot = __ldg(slots + n);
+    uint4 *dst = (is_v ? v_out : k_out) + (n * num_kv_heads + h) * 16 + chunk * 2;
+    uint4 r0 = make_uint4(0u, 0u, 0u, 0u), r1 = r0;
+    if (slot >= 0) {
+        const int64_t page = page_shift >= 0 ? (slot >> page_shift) : slot / page_size;
+        const int64_t off = slot - page * page_size;
+        if (page >= num_pages) {
+            if ((threadIdx.x & 15) == 0) atomicOr(err, FKV_DEVERR_GATHER_SLOT);
+        } else {
+            const uint8_t *cache = is_v ? v_cache : k_cache;
+            const int64_t row = (page * num_kv_heads + h) * page_size + off;
+            if (kKv == FKV_KV_BF16) {
+                const uint4 *src = reinterpret_cast<const uint4 *>(cache) + row * 16 + chunk * 2;
+                r0 = __ldg(src);
+                r1 = __ldg(src + 1);
+            } else {
+                const float g = __ldg((is_v ? v_scale : k_scale) + h);
+                uint32_t f[8];                             // 16 values in f16, in order
+                if (kKv == FKV_KV_FP8_E4M3) {
+                    const uint4 c = __ldg(reinterpret_cast<const uint4 *>(cache + row * 128) + chunk);
+                    const uint32_t w[4] = {c.x, c.y, c.z, c.w};
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        f[2 * j] = e4m3x2_to_f16x2(static_cast<uint16_t>(w[j] & 0xFFFFu));
+                        f[2 * j + 1] = e4m3x2_to_f16x2(static_cast<uint16_t>(w[j] >> 16));
+                    }
+                } else {
+                    const uint8_t *src = cache + row * kFp4Row;
+                    const uint2 c = __ldg(reinterpret_cast<const uint2 *>(src) + chunk);
+                    const uint32_t s = e4m3_to_f16_pair(__ldg(src + kFp4Codes + chunk));
+                    uint32_t lo[4], hi[4];
+                    e2m1x8_to_f16(c.x, lo);
+                    e2m1x8_to_f16(c.y, hi);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        f[j] = mul_f16x2(lo[j], s);
+                        f[4 + j] = mul_f16x2(hi[j], s);
+                    }
+                }
+                r0 = make_uint4(scaled_bf16x2(f[0], g), scaled_bf16x2(f[1], g), scaled_bf16x2(f[2], g),
+                                scaled_bf16x2(f[3], g));
+                r1 = make_uint4(scaled_bf16x2(f[4], g), scaled_bf16x2(f[5], g), scaled_bf16x2(f[6], g),
+                                scaled_bf16x2(f[7], g));
+            }
+        }
+    }
+    dst[0] = r0;
+    dst[1] = r1;
+}
+
+}  // namespace fkv
+
+using namespace fkv;
+
+extern "C" fkv_status kv_gather(const void *k_cache, const void *v_cache, int32_t kv_dtype, const float *k_scale,
+                                const float *v_scale, const int64_t *slots, int32_t n_tokens, void *k_out,
+                                void *v_out, int32_t num_pages, int32_t num_kv_heads, int32_t page_size,
+                                int32_t head_dim, void *stream) {
+    if (n_tokens < 0 || num_pages <= 0 || num_kv_heads <= 0 || page_size <= 0) return FKV_ERR_INVALID_ARG;
+    if (kv_dtype != FKV_KV_FP8_E4M3 && kv_dtype != FKV_KV_BF16 && kv_dtype != FKV_KV_FP4) return FKV_ERR_INVALID_ARG;
+    if (head_dim != 128 || num_kv_heads > 65535) return FKV_ERR_UNSUPPORTED;
+    if (n_tokens == 0) return FKV_OK;
+    if (!k_cache || !v_cache || !slots || !k_out || !v_out) return FKV_ERR_INVALID_ARG;
+    if (kv_dtype != FKV_KV_BF16 && (!k_scale || !v_scale)) return FKV_ERR_INVALID_ARG;
+    if (!aligned16(k_cache) || !aligned16(v_cache) || !aligned16(k_out) || !aligned16(v_out))
+        return FKV_ERR_INVALID_ARG;
+    uint32_t *err = device_error_word();
+    if (!err) return FKV_ERR_CUDA;
+    int32_t shift = -1;
+    if ((page_size & (page_size - 1)) == 0) shift = __builtin_ctz(static_cast<unsigned>(page_size));
+    const dim3 grid(static_cast<unsigned>((static_cast<int64_t>(n_tokens) + kGatherTokens - 1) / kGatherTokens),
+                    static_cast<unsigned>(num_kv_heads));
+    auto go = [&](auto kern) {
+        return launch_pdl(kern, grid, dim3(kGatherBlock), 0, static_cast<cudaStream_t>(stream),
+                          static_cast<const uint8_t *>(k_cache), static_cast<const uint8_t *>(v_cache), k_scale,
+                          v_scale, slots, n_tokens, static_cast<uint4 *>(k_out), static_cast<uint4 *>(v_out),
+                          num_pages, num_kv_heads, page_size, shift, err);
+    };
+    const cudaError_t e = kv_dtype == FKV_KV_FP8_E4M3 ? go(kv_gather_kernel<FKV_KV_FP8_E4M3>)
+                          : kv_dtype == FKV_KV_BF16   ? go(kv_gather_kernel<FKV_KV_BF16>)
+                                                      : go(kv_gather_kernel<FKV_KV_FP4>);
+    return e == cudaSuccess ? FKV_OK : FKV_ERR_CUDA;
+}

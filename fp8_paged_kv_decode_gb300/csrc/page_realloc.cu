@@ -60,11 +60,15 @@ extern "C" fkv_status kv_page_realloc(uint32_t *page_tags, int32_t num_pages, co
     int64_t page_bytes = 0;
     unsigned chunks = 1;
     if (k_cache) {
-        if (kv_dtype != FKV_KV_FP8_E4M3 && kv_dtype != FKV_KV_BF16) return FKV_ERR_INVALID_ARG;
+        if (kv_dtype != FKV_KV_FP8_E4M3 && kv_dtype != FKV_KV_BF16 && kv_dtype != FKV_KV_FP4)
+            return FKV_ERR_INVALID_ARG;
         if (num_kv_heads <= 0 || page_size <= 0) return FKV_ERR_INVALID_ARG;
         if (head_dim != 128) return FKV_ERR_UNSUPPORTED;
         if (!aligned16(k_cache) || !aligned16(v_cache)) return FKV_ERR_INVALID_ARG;
-        page_bytes = static_cast<int64_t>(num_kv_heads) * page_size * head_dim * (kv_dtype == FKV_KV_BF16 ? 2 : 1);
+        const int row_bytes = kv_dtype == FKV_KV_BF16 ? 2 * head_dim
+                              : kv_dtype == FKV_KV_FP4 ? FKV_FP4_ROW_BYTES : head_dim;
+        page_bytes = static_cast<int64_t>(num_kv_heads) * page_size * row_bytes;
+        if (page_bytes % 16) return FKV_ERR_UNSUPPORTED;              // the scrub stores 16 bytes at a time
         const int64_t c = (page_bytes + kScrubChunk - 1) / kScrubChunk;
         if (c > 65535) return FKV_ERR_UNSUPPORTED;
         chunks = static_cast<unsigned>(c);

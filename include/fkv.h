@@ -33,6 +33,13 @@
  *       [num_pages][num_kv_heads][page_size][head_dim]
  *     one (page, head) tile is page_size * head_dim contiguous elements;
  *     elements are e4m3 codes (1 byte) or bf16 (2 bytes).
+ *     The 4-bit pool (FKV_KV_FP4) is uint8
+ *       [num_pages][num_kv_heads][page_size][FKV_FP4_ROW_BYTES]
+ *     with one row of 72 bytes per (token, KV head): byte j < 64 holds the e2m1
+ *     codes of dims 2j (low nibble) and 2j + 1 (high nibble), byte 64 + b the
+ *     e4m3 scale s_b of dims 16b .. 16b + 15.  With g the KV head's fp32 scale
+ *     (the same scale an FP8 cache of that head would use), dim d of the row
+ *     stands for e2m1(code_d) * s_(d / 16) * g: 0.5625 of the FP8 cache's bytes.
  *   Page table (CSR): page_indptr int32[batch + 1], page_indices int32[nnz];
  *     token t of request r lives in page page_indices[page_indptr[r] + t /
  *     page_size] at offset t % page_size.
@@ -66,14 +73,20 @@ typedef enum {
 
 typedef enum {
     FKV_KV_FP8_E4M3 = 0,
-    FKV_KV_BF16 = 1
+    FKV_KV_BF16 = 1,
+    FKV_KV_FP4 = 2      /* e2m1 codes with an e4m3 scale per 16 dims: rows of FKV_FP4_ROW_BYTES */
 } fkv_kv_dtype;
+
+#define FKV_FP4_ROW_BYTES 72   /* a token row of the 4-bit cache: 64 bytes of codes, 8 scales */
 
 /* Bits of the sticky device error word. */
 #define FKV_DEVERR_APPEND_SLOT   0x1u  /* kv_append_*: slot beyond the pool, token skipped */
 #define FKV_DEVERR_ATTN_PAGE     0x2u  /* paged_decode_attn: page id outside [0, num_pages), row zeroed */
 #define FKV_DEVERR_TIMEOUT       0x4u  /* a bounded wait on a copy gave up; the call's output is not valid */
 #define FKV_DEVERR_REALLOC_PAGE  0x8u  /* kv_page_realloc: a listed id is outside [0, num_pages), skipped */
+#define FKV_DEVERR_GATHER_SLOT   0x10u /* kv_gather: slot beyond the pool, its rows written as zeros */
+#define FKV_DEVERR_TABLES        0x20u /* kv_step_tables: a request was refused, or a free page id is outside [0, num_pages) */
+#define FKV_DEVERR_ROPE_AXIS     0x40u /* qk_norm_rope: an axis_map entry is not below n_axes, its pair was not turned */
 
 FKV_API const char *fkv_status_string(fkv_status s);
 
@@ -112,6 +125,143 @@ FKV_API fkv_status kv_append_bf16(const void *k_new, const void *v_new,
                           void *k_cache, void *v_cache,
                           int32_t num_pages, int32_t num_kv_heads,
                           int32_t page_size, int32_t head_dim, void *stream);
+
+/*
+ * kv_append_fp4 -- the 4-bit cache's counterpart of kv_append_fp8: the same
+ * arguments and placement, pools of FKV_FP4_ROW_BYTES rows (layout above).
+ * For each block of 16 dims of a row, with g = scale[h]:
+ *     s    = e4m3_rne_satfinite( fl32( max|x| / fl32(6 g) ) )
+ *     D    = fl32( s * g )
+ *     code = e2m1_rne_satfinite( fl32( x / D ) ),  sign kept on zeros;
+ *            0 for the whole block when D is 0 or NaN
+ * (IEEE divisions, ties to the even code).  Scales of kv_calibrate_scales fit:
+ * a block's s is then at most 74.7, so values up to six times the calibrated
+ * maximum are still held without saturation.  An infinity saturates (its
+ * block takes s = 448); a NaN makes its block's scale, and so its 16 values,
+ * NaN.
+ */
+FKV_API fkv_status kv_append_fp4(const void *k_new, const void *v_new,
+                         const int64_t *slot_mapping, int32_t n_tokens,
+                         const float *k_scale, const float *v_scale,
+                         uint8_t *k_cache, uint8_t *v_cache,
+                         int32_t num_pages, int32_t num_kv_heads,
+                         int32_t page_size, int32_t head_dim, void *stream);
+
+/*
+ * kv_gather -- read cached tokens back as bf16 (a prompt's next chunk, or a
+ * request that reuses a cached prefix, attends over them outside the decode
+ * kernel).  For every n with slot = slots[n] >= 0, KV head h and element d:
+ *     out[n][h][d] = bf16_rne( fl32( value * scale[h] ) )
+ * with value the e4m3 code's value (FKV_KV_FP8_E4M3) or e2m1 code * block scale
+ * (FKV_KV_FP4, exact before the product with scale[h]); FKV_KV_BF16 rows are
+ * copied.  The rows of slot < 0 (padding) are zeros, as are those of a slot
+ * whose page is >= num_pages, which sets FKV_DEVERR_GATHER_SLOT.
+ *
+ *   k_cache, v_cache  pools (layout above) of dtype kv_dtype
+ *   k_scale, v_scale  fp32 [num_kv_heads]; ignored (may be NULL) for BF16
+ *   slots          int64 [n_tokens], repeats allowed
+ *   k_out, v_out   bf16 [n_tokens][num_kv_heads][head_dim], 16-byte aligned
+ * n_tokens == 0 is a no-op.
+ */
+FKV_API fkv_status kv_gather(const void *k_cache, const void *v_cache, int32_t kv_dtype,
+                             const float *k_scale, const float *v_scale,
+                             const int64_t *slots, int32_t n_tokens, void *k_out, void *v_out,
+                             int32_t num_pages, int32_t num_kv_heads,
+                             int32_t page_size, int32_t head_dim, void *stream);
+
+/*
+ * qk_norm_rope -- RMS norm of every query and key head and the rotation by the
+ * token's position, in one pass, before the keys go into the cache.  For every
+ * token n and head row x of 128 elements (fp32 arithmetic, one rounding to
+ * bf16 at the end):
+ *     y = x * rsqrt(mean(x^2) + eps) * weight     (y = x when weight is NULL)
+ *     pair j < rotary_dim / 2:  theta = positions[axis_map[j]][n] * inv_freq[j]
+ *         (a, b) -> (a cos - b sin, b cos + a sin), cos and sin times rot_scale
+ *     with (a, b) = (y[j], y[j + rotary_dim / 2]), or (y[2j], y[2j + 1]) when
+ *     interleaved != 0; elements from rotary_dim on are y unchanged.
+ * The angle keeps its low bits at far positions: the product is formed in two
+ * fp32 words and reduced to a fraction of a turn before sin and cos (|theta|
+ * below 2^31; below 2^20 it is off by about 2^-23 of a turn).
+ *
+ *   q, k           bf16, token n's heads at q + n * q_token_stride (elements):
+ *                  num_q_heads (num_kv_heads) rows of 128, contiguous; token
+ *                  strides are multiples of 8, so q and k may lie in one
+ *                  projection's output.  k may be NULL with num_kv_heads 0.
+ *   q_out, k_out   bf16, the same with their own token strides; they may be q
+ *                  and k themselves (in place) but must not overlap otherwise
+ *   q_weight, k_weight  bf16 [128], or NULL for no norm of those heads
+ *   positions      int32 [n_axes][n_tokens]
+ *   inv_freq       fp32 [rotary_dim / 2], finite
+ *   axis_map       uint8 [rotary_dim / 2], each below n_axes (an entry that is
+ *                  not leaves its pair unturned and sets FKV_DEVERR_ROPE_AXIS);
+ *                  NULL: axis 0 for every pair.  n_axes is 1 .. 8
+ *   rotary_dim     a multiple of 16, 16 .. 128
+ * n_tokens == 0 is a no-op.
+ */
+FKV_API fkv_status qk_norm_rope(const void *q, int64_t q_token_stride, int32_t num_q_heads,
+                                const void *k, int64_t k_token_stride, int32_t num_kv_heads,
+                                void *q_out, int64_t q_out_token_stride,
+                                void *k_out, int64_t k_out_token_stride, int32_t n_tokens,
+                                const void *q_weight, const void *k_weight, float eps,
+                                const int32_t *positions, int32_t n_axes, const float *inv_freq,
+                                const uint8_t *axis_map, int32_t rotary_dim, int32_t interleaved,
+                                float rot_scale, int32_t head_dim, void *stream);
+
+/*
+ * kv_step_tables -- the tables of one step made on the device from the
+ * requests' lengths: page table, slots and positions of the new tokens, with
+ * pages taken from a free list where a request grows into them.  Request r
+ * holds c = cached_lens[r] tokens and gets n = new_lens[r] more (0: idle, 1:
+ * decode, more: a prompt chunk).  With S = page_size, have = ceil(c / S),
+ * pages = ceil((c + n) / S):
+ *   - its CSR row has `pages` entries: block_table[r][0 .. have), then pages -
+ *     have new pages, taken from the top of the free list (free_pages[*free_count
+ *     - 1] first) in request order and stored in block_table[r] with their live
+ *     tags in block_tags[r]; expected_tags is parallel to page_indices;
+ *   - its new tokens are entries token_indptr[r] .. token_indptr[r] + n - 1 of
+ *     slot_mapping (page * S + offset) and positions (c, c + 1, ...);
+ *   - step_lens[r] = c + n is what paged_decode_attn attends over, and
+ *     cached_lens_out[r] = c + n the length kept for the next step.
+ * Refused requests (refused[r] = 1, and FKV_DEVERR_TABLES is set): c or n
+ * negative or c + n over 2^31 - 1; pages > max_blocks; tokens past n_tokens or
+ * entries past nnz; or not enough free pages, counted in request order.  Their
+ * step_lens is 0, cached_lens_out[r] = c, their slots are -1 (appends skip
+ * them), no page is taken.  A request refused for the first two reasons has an
+ * empty CSR row; otherwise missing pages are -1 with tag 0, which
+ * kv_page_tag_check and paged_decode_attn reject.  Prefix sums that pass
+ * n_tokens or nnz are cut to it.  A taken page id outside [0, num_pages), or
+ * an existing one under a new token, makes its entries -1 and their slots -1
+ * and sets FKV_DEVERR_TABLES.
+ *
+ *   cached_lens, new_lens  int32 [batch]
+ *   block_table    int32 [batch][max_blocks], block_tags uint32, the same shape;
+ *                  only the cells of newly taken pages are written
+ *   free_pages     int32 [num_free]; free_count int32 [1] (at most num_free is used)
+ *   page_tags      uint32 [num_pages] live tags (read only: kv_page_realloc bumps
+ *                  a page's tag when it is given back)
+ *   step_lens, cached_lens_out  int32 [batch]; cached_lens_out may be cached_lens
+ *   refused        uint8 [batch]
+ *   page_indptr    int32 [batch + 1]; page_indices int32 [nnz] and expected_tags
+ *                  uint32 [nnz], entries past the last row left as they were
+ *   token_indptr   int32 [batch + 1]; slot_mapping int64 [n_tokens] and positions
+ *                  int32 [n_tokens], entries past the last token are -1 and 0
+ *   free_left      int32 [1], pages still free; may be free_count
+ *   workspace      kv_step_tables_workspace_size(batch) bytes, 256-byte aligned,
+ *                  not shared by calls that overlap on the GPU
+ * The result depends only on the inputs (no atomics), and a call repeated on
+ * the same inputs writes the same bytes.  batch == 0 still fills slot_mapping
+ * and positions, writes the two indptr's single 0 and free_left.
+ */
+FKV_API size_t kv_step_tables_workspace_size(int32_t batch);
+FKV_API fkv_status kv_step_tables(const int32_t *cached_lens, const int32_t *new_lens, int32_t batch,
+                                  int32_t *block_table, uint32_t *block_tags, int32_t max_blocks,
+                                  const int32_t *free_pages, int32_t num_free, const int32_t *free_count,
+                                  const uint32_t *page_tags, int32_t num_pages, int32_t page_size,
+                                  int32_t *step_lens, int32_t *cached_lens_out, uint8_t *refused,
+                                  int32_t *page_indptr, int32_t *page_indices, uint32_t *expected_tags,
+                                  int32_t nnz, int32_t *token_indptr, int64_t *slot_mapping,
+                                  int32_t *positions, int32_t n_tokens, int32_t *free_left,
+                                  void *workspace, size_t workspace_bytes, void *stream);
 
 /*
  * kv_calibrate_scales -- the per-KV-head scales for writing a whole prompt
@@ -199,6 +349,21 @@ FKV_API fkv_status kv_append_bf16_tag_check(const void *k_new, const void *v_new
                                     int32_t batch, int64_t nnz, uint8_t *abort_mask, void *stream);
 
 /*
+ * kv_append_fp4_tag_check -- the same one-launch prologue for a 4-bit cache:
+ * kv_append_fp4 followed by kv_page_tag_check, with the arguments, results,
+ * argument checks and rules of kv_append_fp8_tag_check.
+ */
+FKV_API fkv_status kv_append_fp4_tag_check(const void *k_new, const void *v_new,
+                                   const int64_t *slot_mapping, int32_t n_tokens,
+                                   const float *k_scale, const float *v_scale,
+                                   uint8_t *k_cache, uint8_t *v_cache,
+                                   int32_t num_pages, int32_t num_kv_heads,
+                                   int32_t page_size, int32_t head_dim,
+                                   const uint32_t *page_tags, const int32_t *page_indptr,
+                                   const int32_t *page_indices, const uint32_t *expected_tags,
+                                   int32_t batch, int64_t nnz, uint8_t *abort_mask, void *stream);
+
+/*
  * kv_page_realloc -- hand pages to new owners on the device ("Kimi and GLM
  * Reasoning Slimming: Hands-On Test", section "Giving Every Physical Cache
  * Page a 'Generation Number'": a page's tag changes each time it is
@@ -241,11 +406,12 @@ FKV_API size_t paged_decode_attn_workspace_size(int32_t batch, int32_t num_q_hea
  * query head i (kv head h = i / G):
  *     out[r][i] = sum_t softmax_t( sm_scale * q[r][i] . k_t ) v_t
  * over the request's seq_lens[r] tokens, with k_t = code * k_scale[h] and
- * v_t = code * v_scale[h] for FP8 (the bf16 values for BF16).
+ * v_t = code * v_scale[h] for FP8 (the bf16 values for BF16; for FP4 code *
+ * block scale * k_scale[h] or v_scale[h]).
  *
  *   q              bf16 [batch][num_q_heads][head_dim]
  *   k_cache, v_cache  pools (layout above) of dtype kv_dtype (fkv_kv_dtype)
- *   k_scale, v_scale  fp32 [num_kv_heads] for FP8; ignored (may be NULL) for BF16
+ *   k_scale, v_scale  fp32 [num_kv_heads] for FP8 and FP4; ignored (may be NULL) for BF16
  *   page_indptr, page_indices  the CSR page table; nnz = length of page_indices
  *   seq_lens       int32 [batch]  tokens to attend per request
  *   abort_mask     uint8 [batch] from kv_page_tag_check, or NULL (no tracker)
