@@ -151,7 +151,9 @@ def _ptr(t):
 def _stream(stream):
     import torch
     if stream is None:
-        stream = torch.cuda.current_stream()
+        # the raw handle of the current stream: torch.cuda.current_stream() builds a
+        # Stream object for it, 5 us a call on the host of a GB300
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
@@ -177,18 +179,21 @@ def _is_byte_cache(t):
     return t.dtype in (torch.uint8, getattr(torch, "float8_e4m3fn", torch.uint8))
 
 
+# The checks of the calls below cost host time on every step, as much as their
+# kernels run at decode sizes; so they read each property once, and compare
+# without a call per condition.
 def _is_fp4_cache(t):
     import torch
-    return t.dtype == torch.uint8 and t.dim() == 4 and t.shape[-1] == FP4_ROW_BYTES
+    return t.dtype is torch.uint8 and t.shape[-1] == FP4_ROW_BYTES and t.dim() == 4
 
 
 def _here(*ts):
     """Contiguous tensors of the current device (the one the call launches on)."""
     import torch
-    _dev(*ts)
-    cur = torch.cuda.current_device()
+    cur = torch._C._cuda_getDevice() if torch.cuda.is_initialized() else None
     for t in ts:
-        _need(t is None or t.device.index == cur, "tensors must be on the current device")
+        if t is not None and (t.get_device() != cur or not t.is_contiguous()):
+            raise FkvError("tensors must be contiguous CUDA tensors of the current device")
 
 
 # ---------------------------------------------------------------------------
@@ -310,15 +315,21 @@ def kv_calibrate_scales(k, v, k_scale, v_scale, stream=None):
 
 def _check_fp4_append(k_new, v_new, slot_mapping, k_scale, v_scale, k_cache, v_cache):
     import torch
-    _need(k_new.dtype == torch.bfloat16 and v_new.dtype == torch.bfloat16, "k_new/v_new must be bf16")
-    _need(slot_mapping.dtype == torch.int64, "slot_mapping must be int64")
-    _need(_is_fp4_cache(k_cache) and _is_fp4_cache(v_cache), "FP4 caches must be uint8 [P][Hkv][S][72]")
-    P, Hkv, S, _ = k_cache.shape
-    _need(v_cache.shape == k_cache.shape, "k_cache/v_cache shapes differ")
-    _need(k_scale.dtype == torch.float32 and v_scale.dtype == torch.float32 and k_scale.numel() == Hkv
-          and v_scale.numel() == Hkv, "scales must be float32 [Hkv]")
+    if not (k_new.dtype is torch.bfloat16 and v_new.dtype is torch.bfloat16):
+        raise FkvError("k_new/v_new must be bf16")
+    if slot_mapping.dtype is not torch.int64:
+        raise FkvError("slot_mapping must be int64")
+    shape = k_cache.shape
+    if not (_is_fp4_cache(k_cache) and v_cache.dtype is torch.uint8 and v_cache.shape == shape):
+        raise FkvError("FP4 caches must both be uint8 [P][Hkv][S][72]")
+    P, Hkv, S, _ = shape
+    if not (k_scale.dtype is torch.float32 and v_scale.dtype is torch.float32 and k_scale.numel() == Hkv
+            and v_scale.numel() == Hkv):
+        raise FkvError("scales must be float32 [Hkv]")
     N = slot_mapping.numel()
-    _need(tuple(k_new.shape) == (N, Hkv, HEAD_DIM) and tuple(v_new.shape) == (N, Hkv, HEAD_DIM), "k_new/v_new shape")
+    want = (N, Hkv, HEAD_DIM)
+    if not (k_new.shape == want and v_new.shape == want):
+        raise FkvError("k_new/v_new must be [N][Hkv][128]")
     return P, Hkv, S, N
 
 
@@ -329,9 +340,9 @@ def kv_append_fp4(k_new, v_new, slot_mapping, k_scale, v_scale, k_cache, v_cache
     ones an FP8 cache would use (``kv_calibrate_scales``)."""
     _here(k_new, v_new, slot_mapping, k_scale, v_scale, k_cache, v_cache)
     P, Hkv, S, N = _check_fp4_append(k_new, v_new, slot_mapping, k_scale, v_scale, k_cache, v_cache)
-    _raise(load_library().kv_append_fp4(_ptr(k_new), _ptr(v_new), _ptr(slot_mapping), N, _ptr(k_scale),
-                                        _ptr(v_scale), _ptr(k_cache), _ptr(v_cache), P, Hkv, S, HEAD_DIM,
-                                        _stream(stream)), "kv_append_fp4")
+    _raise(load_library().kv_append_fp4(
+        k_new.data_ptr(), v_new.data_ptr(), slot_mapping.data_ptr(), N, k_scale.data_ptr(), v_scale.data_ptr(),
+        k_cache.data_ptr(), v_cache.data_ptr(), P, Hkv, S, HEAD_DIM, _stream(stream)), "kv_append_fp4")
 
 
 def kv_append_fp4_tag_check(k_new, v_new, slot_mapping, k_scale, v_scale, k_cache, v_cache,
@@ -342,17 +353,20 @@ def kv_append_fp4_tag_check(k_new, v_new, slot_mapping, k_scale, v_scale, k_cach
     _here(k_new, v_new, slot_mapping, k_scale, v_scale, k_cache, v_cache, page_tags, page_indptr, page_indices,
           expected_tags, abort_mask)
     P, Hkv, S, N = _check_fp4_append(k_new, v_new, slot_mapping, k_scale, v_scale, k_cache, v_cache)
-    _need(page_tags.dtype in (torch.uint32, torch.int32) and expected_tags.dtype == page_tags.dtype,
-          "tags must be 32-bit, both of one dtype")
-    _need(page_tags.numel() == P, "page_tags must have one entry per page of the pool")
-    _need(page_indptr.dtype == torch.int32 and page_indices.dtype == torch.int32, "CSR must be int32")
-    _need(abort_mask.dtype == torch.uint8, "abort_mask must be uint8")
-    B = page_indptr.numel() - 1
-    _need(abort_mask.numel() == B and expected_tags.numel() == page_indices.numel(), "size mismatch")
+    if not (page_tags.dtype in (torch.uint32, torch.int32) and expected_tags.dtype is page_tags.dtype):
+        raise FkvError("tags must be 32-bit, both of one dtype")
+    if page_tags.numel() != P:
+        raise FkvError("page_tags must have one entry per page of the pool")
+    if not (page_indptr.dtype is torch.int32 and page_indices.dtype is torch.int32):
+        raise FkvError("CSR must be int32")
+    B, nnz = page_indptr.numel() - 1, page_indices.numel()
+    if not (abort_mask.dtype is torch.uint8 and abort_mask.numel() == B and expected_tags.numel() == nnz):
+        raise FkvError("abort_mask must be uint8 [B], expected_tags parallel to page_indices")
     _raise(load_library().kv_append_fp4_tag_check(
-        _ptr(k_new), _ptr(v_new), _ptr(slot_mapping), N, _ptr(k_scale), _ptr(v_scale), _ptr(k_cache),
-        _ptr(v_cache), P, Hkv, S, HEAD_DIM, _ptr(page_tags), _ptr(page_indptr), _ptr(page_indices),
-        _ptr(expected_tags), B, page_indices.numel(), _ptr(abort_mask), _stream(stream)), "kv_append_fp4_tag_check")
+        k_new.data_ptr(), v_new.data_ptr(), slot_mapping.data_ptr(), N, k_scale.data_ptr(), v_scale.data_ptr(),
+        k_cache.data_ptr(), v_cache.data_ptr(), P, Hkv, S, HEAD_DIM, page_tags.data_ptr(), page_indptr.data_ptr(),
+        page_indices.data_ptr(), expected_tags.data_ptr(), B, nnz, abort_mask.data_ptr(), _stream(stream)),
+        "kv_append_fp4_tag_check")
 
 
 def kv_gather(k_cache, v_cache, slots, k_out, v_out, k_scale=None, v_scale=None, stream=None):
@@ -361,19 +375,38 @@ def kv_gather(k_cache, v_cache, slots, k_out, v_out, k_scale=None, v_scale=None,
     [P][Hkv][S][128], or FP4 uint8 [P][Hkv][S][72]; scales fp32 [Hkv] unless bf16."""
     import torch
     _here(k_cache, v_cache, slots, k_out, v_out, k_scale, v_scale)
-    kv = KV_FP4 if _is_fp4_cache(k_cache) else KV_FP8_E4M3 if _is_byte_cache(k_cache) else KV_BF16
-    _need(kv != KV_BF16 or k_cache.dtype == torch.bfloat16, "cache must be uint8 / float8_e4m3fn or bf16")
-    P, Hkv, S, row = k_cache.shape
-    _need(v_cache.shape == k_cache.shape and v_cache.dtype == k_cache.dtype, "k_cache and v_cache differ")
-    _need(slots.dtype == torch.int64, "slots must be int64")
-    N, D = slots.numel(), row if kv != KV_FP4 else HEAD_DIM
-    for o in (k_out, v_out):
-        _need(o.dtype == torch.bfloat16 and tuple(o.shape) == (N, Hkv, D), "k_out/v_out must be bf16 [N][Hkv][128]")
-    if kv != KV_BF16:
-        for s in (k_scale, v_scale):
-            _need(s is not None and s.dtype == torch.float32 and s.numel() == Hkv, "scales must be float32 [Hkv]")
-    _raise(load_library().kv_gather(_ptr(k_cache), _ptr(v_cache), kv, _ptr(k_scale), _ptr(v_scale), _ptr(slots), N,
-                                    _ptr(k_out), _ptr(v_out), P, Hkv, S, D, _stream(stream)), "kv_gather")
+    kv, D = _attn_cache(k_cache, v_cache, k_scale, v_scale)
+    shape = k_cache.shape
+    P, Hkv, S, _ = shape
+    if not (v_cache.shape == shape and v_cache.dtype is k_cache.dtype):
+        raise FkvError("k_cache and v_cache differ")
+    if kv != KV_BF16 and not (k_scale is not None and v_scale is not None and k_scale.dtype is torch.float32
+                              and v_scale.dtype is torch.float32 and k_scale.numel() == Hkv
+                              and v_scale.numel() == Hkv):
+        raise FkvError("scales must be float32 [Hkv]")
+    if slots.dtype is not torch.int64:
+        raise FkvError("slots must be int64")
+    N = slots.numel()
+    want = (N, Hkv, D)
+    if not (k_out.dtype is torch.bfloat16 and v_out.dtype is torch.bfloat16 and k_out.shape == want
+            and v_out.shape == want):
+        raise FkvError("k_out/v_out must be bf16 [N][Hkv][128]")
+    _raise(load_library().kv_gather(
+        k_cache.data_ptr(), v_cache.data_ptr(), kv, _ptr(k_scale), _ptr(v_scale), slots.data_ptr(), N,
+        k_out.data_ptr(), v_out.data_ptr(), P, Hkv, S, D, _stream(stream)), "kv_gather")
+
+
+def _head_rows(x, want, cur):
+    """The token stride of bf16 [N][H][128] whose head rows lie together."""
+    import torch
+    if not (x.dtype is torch.bfloat16 and x.get_device() == cur and x.shape == want):
+        raise FkvError("q/k and outputs must be bf16 [N][H][128] on the current device")
+    if want[0] == 0:
+        return want[1] * want[2]
+    a, b, c = x.stride()
+    if c != 1 or (b != want[2] and want[1] != 1):
+        raise FkvError("head rows must be contiguous")
+    return a if want[0] > 1 else want[1] * want[2]
 
 
 def qk_norm_rope(q, k, positions, inv_freq, q_out, k_out, q_weight=None, k_weight=None, eps=1e-6, axis_map=None,
@@ -387,31 +420,35 @@ def qk_norm_rope(q, k, positions, inv_freq, q_out, k_out, q_weight=None, k_weigh
     ``k`` and ``k_out`` may be None."""
     import torch
     _here(positions, inv_freq, q_weight, k_weight, axis_map)
-    _need((k is None) == (k_out is None), "k and k_out go together")
+    cur = positions.get_device()
     N, Hq, D = q.shape
-    Hkv = 0 if k is None else k.shape[1]
-    for x, h in ((q, Hq), (q_out, Hq), (k, Hkv), (k_out, Hkv)):
-        if x is None:
-            continue
-        _need(x.is_cuda and x.device.index == torch.cuda.current_device(), "tensors must be on the current device")
-        _need(x.dtype == torch.bfloat16 and tuple(x.shape) == (N, h, D), "q/k and outputs must be bf16 [N][H][128]")
-        _need(N == 0 or (x.stride(2) == 1 and (h == 1 or x.stride(1) == D)), "head rows must be contiguous")
+    want = (N, Hq, D)
+    qs, qos = _head_rows(q, want, cur), _head_rows(q_out, want, cur)
+    if k is None:
+        if k_out is not None:
+            raise FkvError("k and k_out go together")
+        Hkv = ks = kos = 0
+    else:
+        if k_out is None or k.dim() != 3:
+            raise FkvError("k and k_out go together, both [N][Hkv][128]")
+        Hkv = k.shape[1]
+        want = (N, Hkv, D)
+        ks, kos = _head_rows(k, want, cur), _head_rows(k_out, want, cur)
     for w in (q_weight, k_weight):
-        _need(w is None or (w.dtype == torch.bfloat16 and w.numel() == D), "weights must be bf16 [128]")
-    _need(positions.dtype == torch.int32 and positions.dim() in (1, 2) and positions.shape[-1] == N,
-          "positions must be int32 [N] or [axes][N]")
-    _need(inv_freq.dtype == torch.float32 and inv_freq.dim() == 1, "inv_freq must be float32 [R/2]")
-    _need(axis_map is None or (axis_map.dtype == torch.uint8 and axis_map.numel() == inv_freq.numel()),
-          "axis_map must be uint8 [R/2]")
-    axes = 1 if positions.dim() == 1 else positions.shape[0]
-
-    def stride(x, h):
-        return h * D if x is None or N <= 1 else x.stride(0)
+        if w is not None and not (w.dtype is torch.bfloat16 and w.numel() == D):
+            raise FkvError("weights must be bf16 [128]")
+    pos_shape = positions.shape
+    if not (positions.dtype is torch.int32 and len(pos_shape) in (1, 2) and pos_shape[-1] == N):
+        raise FkvError("positions must be int32 [N] or [axes][N]")
+    half = inv_freq.numel()
+    if not (inv_freq.dtype is torch.float32 and inv_freq.dim() == 1):
+        raise FkvError("inv_freq must be float32 [R/2]")
+    if axis_map is not None and not (axis_map.dtype is torch.uint8 and axis_map.numel() == half):
+        raise FkvError("axis_map must be uint8 [R/2]")
     _raise(load_library().qk_norm_rope(
-        _ptr(q), stride(q, Hq), Hq, _ptr(k), stride(k, Hkv), Hkv, _ptr(q_out), stride(q_out, Hq), _ptr(k_out),
-        stride(k_out, Hkv), N, _ptr(q_weight), _ptr(k_weight), float(eps), _ptr(positions), axes, _ptr(inv_freq),
-        _ptr(axis_map), 2 * inv_freq.numel(), 1 if interleaved else 0, float(rot_scale), D, _stream(stream)),
-        "qk_norm_rope")
+        q.data_ptr(), qs, Hq, _ptr(k), ks, Hkv, q_out.data_ptr(), qos, _ptr(k_out), kos, N, _ptr(q_weight),
+        _ptr(k_weight), float(eps), positions.data_ptr(), 1 if len(pos_shape) == 1 else pos_shape[0], inv_freq.data_ptr(),
+        _ptr(axis_map), 2 * half, 1 if interleaved else 0, float(rot_scale), D, _stream(stream)), "qk_norm_rope")
     return q_out, k_out
 
 
@@ -441,26 +478,29 @@ def kv_step_tables(cached_lens, new_lens, block_table, block_tags, free_pages, f
           free_left, workspace)
     for x in (cached_lens, new_lens, block_table, free_pages, free_count, step_lens, cached_lens_out, page_indptr,
               page_indices, token_indptr, positions, free_left):
-        _need(x.dtype == torch.int32, "lengths, tables, free list, indptr, indices and positions must be int32")
-    for x in (block_tags, page_tags, expected_tags):
-        _need(x.dtype in (torch.int32, torch.uint32) and x.dtype == page_tags.dtype, "tags must be 32-bit, of one dtype")
-    _need(slot_mapping.dtype == torch.int64, "slot_mapping must be int64")
-    _need(refused.dtype == torch.uint8, "refused must be uint8")
-    B = cached_lens.numel()
-    _need(block_table.dim() == 2 and block_table.shape[0] == B and block_tags.shape == block_table.shape,
-          "block_table and block_tags must be [B][max_blocks]")
-    _need(new_lens.numel() == B and step_lens.numel() == B and cached_lens_out.numel() == B and refused.numel() == B,
-          "one length per request")
-    _need(page_indptr.numel() == B + 1 and token_indptr.numel() == B + 1, "indptr arrays must be [B + 1]")
-    _need(expected_tags.numel() == page_indices.numel(), "expected_tags is parallel to page_indices")
-    _need(positions.numel() == slot_mapping.numel(), "positions is parallel to slot_mapping")
-    _need(free_count.numel() == 1 and free_left.numel() == 1, "free_count and free_left hold one value")
+        if x.dtype is not torch.int32:
+            raise FkvError("lengths, tables, free list, indptr, indices and positions must be int32")
+    tag = page_tags.dtype
+    if not ((tag is torch.int32 or tag is torch.uint32) and block_tags.dtype is tag and expected_tags.dtype is tag):
+        raise FkvError("tags must be 32-bit, of one dtype")
+    if not (slot_mapping.dtype is torch.int64 and refused.dtype is torch.uint8):
+        raise FkvError("slot_mapping must be int64, refused uint8")
+    B, nnz, n_tokens, n_free = cached_lens.numel(), page_indices.numel(), slot_mapping.numel(), free_pages.numel()
+    shape = block_table.shape
+    if not (len(shape) == 2 and shape[0] == B and block_tags.shape == shape):
+        raise FkvError("block_table and block_tags must be [B][max_blocks]")
+    if not (new_lens.numel() == B and step_lens.numel() == B and cached_lens_out.numel() == B
+            and refused.numel() == B and page_indptr.numel() == B + 1 and token_indptr.numel() == B + 1):
+        raise FkvError("one length per request, indptr arrays of B + 1")
+    if not (expected_tags.numel() == nnz and positions.numel() == n_tokens and free_count.numel() == 1
+            and free_left.numel() == 1):
+        raise FkvError("expected_tags parallel to page_indices, positions to slot_mapping; free counts of one value")
     _raise(load_library().kv_step_tables(
-        _ptr(cached_lens), _ptr(new_lens), B, _ptr(block_table), _ptr(block_tags), block_table.shape[1],
-        _ptr(free_pages), free_pages.numel(), _ptr(free_count), _ptr(page_tags), page_tags.numel(), int(page_size),
-        _ptr(step_lens), _ptr(cached_lens_out), _ptr(refused), _ptr(page_indptr), _ptr(page_indices),
-        _ptr(expected_tags), page_indices.numel(), _ptr(token_indptr), _ptr(slot_mapping), _ptr(positions),
-        slot_mapping.numel(), _ptr(free_left), _ptr(workspace), workspace.numel() * workspace.element_size(),
+        cached_lens.data_ptr(), new_lens.data_ptr(), B, block_table.data_ptr(), block_tags.data_ptr(), shape[1],
+        free_pages.data_ptr(), n_free, free_count.data_ptr(), page_tags.data_ptr(), page_tags.numel(), int(page_size),
+        step_lens.data_ptr(), cached_lens_out.data_ptr(), refused.data_ptr(), page_indptr.data_ptr(),
+        page_indices.data_ptr(), expected_tags.data_ptr(), nnz, token_indptr.data_ptr(), slot_mapping.data_ptr(),
+        positions.data_ptr(), n_tokens, free_left.data_ptr(), workspace.data_ptr(), workspace.nbytes,
         _stream(stream)), "kv_step_tables")
 
 
@@ -490,15 +530,43 @@ def _attn_cache(k_cache, v_cache, k_scale, v_scale):
     """The caches' format and head dim."""
     import torch
     if _is_fp4_cache(k_cache):
-        _here(k_cache, v_cache, k_scale, v_scale)
-        _need(v_cache.shape == k_cache.shape and v_cache.dtype == k_cache.dtype, "k_cache and v_cache differ")
-        for s in (k_scale, v_scale):
-            _need(s is not None and s.dtype == torch.float32 and s.numel() == k_cache.shape[1],
-                  "scales must be float32 [Hkv]")
+        if not (v_cache.shape == k_cache.shape and v_cache.dtype is torch.uint8):
+            raise FkvError("k_cache and v_cache differ")
+        H = k_cache.shape[1]
+        if not (k_scale is not None and v_scale is not None and k_scale.dtype is torch.float32
+                and v_scale.dtype is torch.float32 and k_scale.numel() == H and v_scale.numel() == H):
+            raise FkvError("scales must be float32 [Hkv]")
         return KV_FP4, HEAD_DIM
     fp8 = _is_byte_cache(k_cache)
     _need(fp8 or k_cache.dtype == torch.bfloat16, "cache must be uint8 (e4m3) or bf16")
     return (KV_FP8_E4M3 if fp8 else KV_BF16), k_cache.shape[-1]
+
+
+def _check_attn(q, k_cache, v_cache, page_indptr, page_indices, seq_lens, out, workspace, k_scale, v_scale,
+                abort_mask):
+    import torch
+    for t in (q, k_cache, v_cache, page_indptr, page_indices, seq_lens, out, workspace, k_scale, v_scale, abort_mask):
+        if t is not None and not (t.is_cuda and t.is_contiguous()):
+            raise FkvError("tensors must be contiguous CUDA tensors")
+    kv, D2 = _attn_cache(k_cache, v_cache, k_scale, v_scale)
+    if not (q.dtype is torch.bfloat16 and out.dtype is torch.bfloat16):
+        raise FkvError("q/out must be bf16")
+    if seq_lens.dtype is not torch.int32:
+        raise FkvError("seq_lens must be int32")
+    if abort_mask is not None and abort_mask.dtype is not torch.uint8:
+        raise FkvError("abort_mask must be uint8")
+    shape = q.shape
+    B, Hq, D = shape
+    P, Hkv, S, _ = k_cache.shape
+    if not (out.shape == shape and D2 == D and page_indptr.numel() == B + 1):
+        raise FkvError("shape mismatch")
+    if kv == KV_FP4:
+        _here(q, k_cache, seq_lens)
+        if not (page_indptr.dtype is torch.int32 and page_indices.dtype is torch.int32 and seq_lens.numel() == B
+                and (abort_mask is None or abort_mask.numel() == B)):
+            raise FkvError("CSR must be int32, seq_lens and abort_mask [B]")
+    scales = (None, None) if kv == KV_BF16 else (_ptr(k_scale), _ptr(v_scale))
+    return kv, scales, B, Hq, P, Hkv, S, D
 
 
 def paged_decode_attn_workspace_size(batch, num_q_heads, num_kv_heads, head_dim=HEAD_DIM, kv_dtype=KV_FP8_E4M3):
@@ -521,21 +589,12 @@ def paged_decode_attn(q, k_cache, v_cache, page_indptr, page_indices, seq_lens, 
     k_scale/v_scale fp32 [Hkv]) or bf16, or [P][Hkv][S][72] uint8 (FP4, with
     the same scales; workspace for KV_FP4); CSR page table int32; seq_lens int32
     [B]; abort_mask uint8 [B] or None (no tracker)."""
-    import torch
-    _dev(q, k_cache, v_cache, page_indptr, page_indices, seq_lens, out, workspace, k_scale, v_scale, abort_mask)
-    kv, D2 = _attn_cache(k_cache, v_cache, k_scale, v_scale)
-    _need(q.dtype == torch.bfloat16 and out.dtype == torch.bfloat16, "q/out must be bf16")
-    _need(seq_lens.dtype == torch.int32, "seq_lens must be int32")
-    _need(abort_mask is None or abort_mask.dtype == torch.uint8, "abort_mask must be uint8")
-    B, Hq, D = q.shape
-    P, Hkv, S, _ = k_cache.shape
-    _need(tuple(out.shape) == (B, Hq, D) and D2 == D and page_indptr.numel() == B + 1, "shape mismatch")
+    kv, scales, B, Hq, P, Hkv, S, D = _check_attn(q, k_cache, v_cache, page_indptr, page_indices, seq_lens, out,
+                                                  workspace, k_scale, v_scale, abort_mask)
     _raise(load_library().paged_decode_attn(
-        _ptr(q), B, Hq, _ptr(k_cache), _ptr(v_cache), kv,
-        _ptr(k_scale) if kv != KV_BF16 else None, _ptr(v_scale) if kv != KV_BF16 else None, P, Hkv, S, D,
-        _ptr(page_indptr), _ptr(page_indices), page_indices.numel(), _ptr(seq_lens), _ptr(abort_mask),
-        float(sm_scale),
-        _ptr(out), _ptr(workspace), workspace.numel() * workspace.element_size(), _stream(stream)),
+        q.data_ptr(), B, Hq, k_cache.data_ptr(), v_cache.data_ptr(), kv, *scales, P, Hkv, S, D,
+        page_indptr.data_ptr(), page_indices.data_ptr(), page_indices.numel(), seq_lens.data_ptr(), _ptr(abort_mask),
+        float(sm_scale), out.data_ptr(), workspace.data_ptr(), workspace.nbytes, _stream(stream)),
         "paged_decode_attn")
     return out
 
@@ -547,20 +606,12 @@ def paged_decode_attn_noalloc(q, k_cache, v_cache, page_indptr, page_indices, se
     ``NOALLOC_SCRATCH_BYTES`` inside the library (shared by all calls on a
     device, so calls must not overlap on the GPU).  Shapes needing more
     scratch raise FkvError (status ERR_SCRATCH_LIMIT)."""
-    import torch
-    _dev(q, k_cache, v_cache, page_indptr, page_indices, seq_lens, out, k_scale, v_scale, abort_mask)
-    kv, D2 = _attn_cache(k_cache, v_cache, k_scale, v_scale)
-    _need(q.dtype == torch.bfloat16 and out.dtype == torch.bfloat16, "q/out must be bf16")
-    _need(seq_lens.dtype == torch.int32, "seq_lens must be int32")
-    _need(abort_mask is None or abort_mask.dtype == torch.uint8, "abort_mask must be uint8")
-    B, Hq, D = q.shape
-    P, Hkv, S, _ = k_cache.shape
-    _need(tuple(out.shape) == (B, Hq, D) and D2 == D and page_indptr.numel() == B + 1, "shape mismatch")
+    kv, scales, B, Hq, P, Hkv, S, D = _check_attn(q, k_cache, v_cache, page_indptr, page_indices, seq_lens, out, None,
+                                                  k_scale, v_scale, abort_mask)
     _raise(load_library().paged_decode_attn_noalloc(
-        _ptr(q), B, Hq, _ptr(k_cache), _ptr(v_cache), kv,
-        _ptr(k_scale) if kv != KV_BF16 else None, _ptr(v_scale) if kv != KV_BF16 else None, P, Hkv, S, D,
-        _ptr(page_indptr), _ptr(page_indices), page_indices.numel(), _ptr(seq_lens), _ptr(abort_mask),
-        float(sm_scale), _ptr(out), _stream(stream)), "paged_decode_attn_noalloc")
+        q.data_ptr(), B, Hq, k_cache.data_ptr(), v_cache.data_ptr(), kv, *scales, P, Hkv, S, D,
+        page_indptr.data_ptr(), page_indices.data_ptr(), page_indices.numel(), seq_lens.data_ptr(), _ptr(abort_mask),
+        float(sm_scale), out.data_ptr(), _stream(stream)), "paged_decode_attn_noalloc")
     return out
 
 
