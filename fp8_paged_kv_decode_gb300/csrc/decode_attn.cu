@@ -59,7 +59,14 @@
 #define FKV_FP4_TILE 64
 #endif
 #ifndef FKV_FP4_STAGES
-#define FKV_FP4_STAGES 3
+#define FKV_FP4_STAGES 2
+#endif
+// Computing warps of a 4-bit CTA and the CTAs an SM holds.
+#ifndef FKV_FP4_WARPS
+#define FKV_FP4_WARPS 4
+#endif
+#ifndef FKV_FP4_CTAS
+#define FKV_FP4_CTAS 2
 #endif
 #ifndef FKV_BF16_TILE
 #define FKV_BF16_TILE 64
@@ -120,10 +127,6 @@ constexpr int kMinAlignedTiles = FKV_ALIGNED_MIN_TILES;
 #endif
 constexpr int kLocalPlanMax = FKV_LOCAL_PLAN_MAX;
 static_assert(kLocalPlanMax <= 1024, "one 32-request chunk per lane");
-// Attention CTA: one warp that both issues copies and computes, or (kWS) a
-// producer warp that issues copies and a consumer warp that computes.
-__host__ __device__ constexpr int attn_threads(bool ws) { return ws ? 64 : 32; }      // batches up to this size: each warp finds its own range
-
 // kKv: the cache's format, an fkv_kv_dtype.
 template <int kKv>
 struct Cfg;
@@ -133,6 +136,8 @@ struct Cfg<FKV_KV_FP8_E4M3> {
     static constexpr int kStages = FKV_FP8_STAGES;
     static constexpr int kHalves = 1;           // column blocks per token row
     static constexpr int kRow = 128;            // bytes of a token row in one column block
+    static constexpr int kWarps = 1;            // computing warps per CTA
+    static constexpr int kMinCtas = 1;          // resident CTAs per SM the registers are held to
 };
 template <>
 struct Cfg<FKV_KV_BF16> {
@@ -140,6 +145,8 @@ struct Cfg<FKV_KV_BF16> {
     static constexpr int kStages = FKV_BF16_STAGES;
     static constexpr int kHalves = 2;
     static constexpr int kRow = 128;
+    static constexpr int kWarps = 1;
+    static constexpr int kMinCtas = 1;
 };
 template <>
 struct Cfg<FKV_KV_FP4> {
@@ -147,7 +154,17 @@ struct Cfg<FKV_KV_FP4> {
     static constexpr int kStages = FKV_FP4_STAGES;
     static constexpr int kHalves = 1;
     static constexpr int kRow = FKV_FP4_ROW_BYTES;
+    static constexpr int kWarps = FKV_FP4_WARPS;
+    static constexpr int kMinCtas = FKV_FP4_CTAS;
 };
+
+// Attention CTA: kWarps warps that each issue their copies and compute, on a
+// stage ring of their own, or (kWS, kWarps 1) a producer warp that issues copies
+// and a consumer warp that computes.
+template <int kKv>
+__host__ __device__ constexpr int attn_threads(bool ws) {
+    return ws ? 64 : 32 * Cfg<kKv>::kWarps;
+}
 
 template <int kKv>
 struct Layout {
@@ -158,9 +175,11 @@ struct Layout {
     static constexpr int kHalfBytes = kTile * kRow;             // one column block of a K (or V) tile
     static constexpr int kTileBytes = kHalves * kHalfBytes;     // a K (or V) tile
     static constexpr int kStageBytes = 2 * kTileBytes;          // K then V
-    // stage buffers, then per stage a full and an empty mbarrier, the merge
-    // mbarrier, and per stage a bad-page flag
-    static constexpr int kSmem = 1024 + kStages * kStageBytes + 20 * kStages + 8;
+    static constexpr int kAlign = kKv == FKV_KV_FP4 ? 128 : 1024;   // of the stage buffers (1024: 128B swizzle)
+    // per computing warp: stage buffers, then per stage a full and an empty
+    // mbarrier, the merge mbarrier, and per stage a bad-page flag
+    static constexpr int kWarpSmem = kStages * kStageBytes + (20 * kStages + 8 + 15) / 16 * 16;
+    static constexpr int kSmem = kAlign + Cfg<kKv>::kWarps * kWarpSmem;
     static_assert(kTile == 32 || kTile == 64, "tile of 32 or 64 tokens");
     static_assert(kKv == FKV_KV_FP4 || kHalfBytes % 1024 == 0, "stage buffers stay 1024-byte aligned for the 128B swizzle");
 };
@@ -647,19 +666,12 @@ __device__ bool merge_parts_smem(const AttnParams &p, uint32_t sbuf, int cap, ui
     return true;
 }
 
-// Which of a lane's 16 output dims (in ascending order) the accumulator o[a]
-// holds in its rows g (half 0) and g + 8 (half 1).
-template <int kKv>
-__device__ constexpr int out_dim(int a, int half) {
-    return kKv == FKV_KV_FP4 ? 4 * (a >> 1) + 2 * half + (a & 1) : 2 * a + half;
-}
-
 // kAligned: the instance for batches of up to 64 requests, which gives units
 // whole warps (place_aligned) when the live requests' tiles pass its test and
 // uses the even split otherwise.  Larger batches use the instance without
 // the option (their warps do not hold the requests' rows).
 template <int kKv, bool kWS, bool kAligned>
-__global__ void __launch_bounds__(attn_threads(kWS), 1)
+__global__ void __launch_bounds__(attn_threads<kKv>(kWS), Cfg<kKv>::kMinCtas)
 paged_decode_attn_kernel(const AttnParams p, const __grid_constant__ CUtensorMap tmK,
                          const __grid_constant__ CUtensorMap tmV) {
     using Lay = Layout<kKv>;
@@ -671,7 +683,9 @@ paged_decode_attn_kernel(const AttnParams p, const __grid_constant__ CUtensorMap
     constexpr int NACC = MT >= 4 ? 1 : 2;                // independent QK accumulator chains per M tile
 
     extern __shared__ uint8_t smem_raw[];
-    const uint32_t sbase = (smem_u32(smem_raw) + 1023u) & ~1023u;
+    constexpr int kWarps = Cfg<kKv>::kWarps;
+    const int warp = kWarps > 1 ? threadIdx.x / 32 : 0;
+    const uint32_t sbase = ((smem_u32(smem_raw) + (Lay::kAlign - 1u)) & ~(Lay::kAlign - 1u)) + warp * Lay::kWarpSmem;
     // Stage s completes on full[s] when its copies land.  With kWS the CTA has
     // two warps: warp 0 issues the K/V copies (the producer) and warp 1
     // computes (the consumer), which releases a stage on empty[s].  A tensor
@@ -686,10 +700,11 @@ paged_decode_attn_kernel(const AttnParams p, const __grid_constant__ CUtensorMap
     const int lane = threadIdx.x & 31;
     const bool producer = kWS && threadIdx.x < 32;
     const int g = lane >> 2, t = lane & 3;
-    const int w = blockIdx.x;
+    const int w = blockIdx.x * kWarps + warp;
     const int S = p.S, Hkv = p.Hkv, G = p.G;
+    const int S_log = 31 - __clz(S);                   // page sizes are powers of two
 
-    if (threadIdx.x == 0) {
+    if (kWarps > 1 ? lane == 0 : threadIdx.x == 0) {
         for (int s = 0; s < NST; ++s) {
             mbar_init(full_bars + 8 * s, 1);
             mbar_init(empty_bars + 8 * s, 1);
@@ -793,7 +808,7 @@ paged_decode_attn_kernel(const AttnParams p, const __grid_constant__ CUtensorMap
         pid_r = fr.r0;                                 // the first request's page-table row is known
         lseq = fr.sl0;
         lrow0 = fr.row0;
-        lneed = (lseq + S - 1) / S;
+        lneed = (lseq + S - 1) >> S_log;
         pbase = -1000;
     } else {
         cursor_init(L, p, lo, p.warp_req[w]);
@@ -804,7 +819,7 @@ paged_decode_attn_kernel(const AttnParams p, const __grid_constant__ CUtensorMap
         const int pos = b + lane;
         return pos < lneed ? __ldcg(p.indices + lrow0 + pos) : -1;
     };
-    auto page_id = [&](int pos) -> int {
+    auto page_window = [&](int pos) {                  // makes pidA hold page pos's aligned 32
         if (pos < pbase || pos >= pbase + 64) {
             pbase = pos & ~31;
             pidA = fetch_ids(pbase);
@@ -814,21 +829,67 @@ paged_decode_attn_kernel(const AttnParams p, const __grid_constant__ CUtensorMap
             pbase += 32;
             pidB = fetch_ids(pbase + 32);
         }
+    };
+    auto page_id = [&](int pos) -> int {
+        page_window(pos);
         return __shfl_sync(kFull, pidA, pos - pbase);
     };
-    auto issue = [&](int stage) {
+    // The 4-bit cache: the rows of one (page, head) are contiguous, codes and
+    // scales together, so a tile is one untiled copy of K and one of V per
+    // page.  Lane k issues page k's K copy, lane 4 + k its V copy.  Only rows up
+    // to the request's last token are copied, rounded up to an even count:
+    // sizes and addresses are then multiples of 16.
+    const int npg4 = S < kTile ? kTile >> S_log : 1, rows4 = S < kTile ? S : kTile;
+    const int lane_pg = lane & (npg4 - 1);
+    const uint32_t page_bytes = static_cast<uint32_t>(Hkv >> p.hshift) * S * Lay::kRow;
+    const uint8_t *lane_pool = lane < 4 ? p.k_cache : p.v_cache;
+    const uint32_t lane_dst = sbase + (lane < 4 ? 0 : Lay::kTileBytes) + lane_pg * rows4 * Lay::kRow;
+    auto issue_fp4 = [&](int stage) {
         if (L.r != pid_r) {
             pid_r = L.r;
             lseq = __ldcg(p.seq_lens + L.r);
             lrow0 = __ldcg(p.indptr + L.r);
-            lneed = (lseq + S - 1) / S;
+            lneed = (lseq + S - 1) >> S_log;
             pbase = -1000;
         }
         const int tok0 = L.tt * kTile;
-        const int npg = S < kTile ? kTile / S : 1;       // pages per tile (<= 4)
+        const int pos0 = tok0 >> S_log;                // a multiple of npg4
+        page_window(pos0);
+        int id = __shfl_sync(kFull, pidA, pos0 - pbase + lane_pg);
+        const int left = min(lseq - tok0, kTile);      // tokens of the tile
+        const int rows = (min(left - lane_pg * rows4, rows4) + 1) & ~1;
+        const bool outside = rows > 0 && (id < 0 || id >= p.P);
+        if (outside) id = 0;                           // never dereference an id outside the pool
+        const bool bad = __any_sync(kFull, outside);
+        const uint32_t bar = full_bars + 8 * stage;
+        if (lane == 0) {
+            st_shared_u32(bad_flags + 4 * stage, bad ? 1u : 0u);   // published by the arrive below
+            mbar_arrive_expect_tx(bar, ((left + 1) & ~1) * 2 * Lay::kRow);
+        }
+        __syncwarp();
+        if (rows > 0 && (lane & 3) < npg4 && lane < 8)
+            bulk_load_hint(lane_dst + stage * Lay::kStageBytes,
+                           lane_pool + static_cast<uint64_t>(static_cast<uint32_t>(id)) * page_bytes +
+                               ((L.h >> p.hshift) * S + (tok0 & (S - 1) & ~(rows4 - 1))) * Lay::kRow,
+                           rows * Lay::kRow, bar, policy);
+    };
+    auto issue = [&](int stage) {
+        if constexpr (kFp4) {
+            issue_fp4(stage);
+            return;
+        }
+        if (L.r != pid_r) {
+            pid_r = L.r;
+            lseq = __ldcg(p.seq_lens + L.r);
+            lrow0 = __ldcg(p.indptr + L.r);
+            lneed = (lseq + S - 1) >> S_log;
+            pbase = -1000;
+        }
+        const int tok0 = L.tt * kTile;
+        const int npg = S < kTile ? kTile >> S_log : 1;  // pages per tile (<= 4)
         const int rows = S < kTile ? S : kTile;
-        const int pos0 = tok0 / S;
-        const int rowoff = S < kTile ? 0 : tok0 % S;
+        const int pos0 = tok0 >> S_log;
+        const int rowoff = S < kTile ? 0 : tok0 & (S - 1);
         int ids[4] = {-1, -1, -1, -1};
         bool bad = false;
         uint32_t bytes = 0;
@@ -843,26 +904,7 @@ paged_decode_attn_kernel(const AttnParams p, const __grid_constant__ CUtensorMap
             ids[k] = id;
             bytes += 2u * rows * Lay::kRow * Lay::kHalves;
         }
-        if (kFp4) {
-            // The rows of one (page, head) are contiguous, codes and scales
-            // together: one untiled copy of K and one of V per page, each issued
-            // by a lane of its own (0-3: K of pages 0-3, 4-7: V).  Sizes and
-            // addresses are multiples of 16: page rows come in multiples of 16.
-            const uint32_t bar = full_bars + 8 * stage;
-            if (lane == 0) {
-                st_shared_u32(bad_flags + 4 * stage, bad ? 1u : 0u);   // published by the arrive below
-                mbar_arrive_expect_tx(bar, bytes);
-            }
-            __syncwarp();
-            const int k = lane & 3;
-            const int id = k == 0 ? ids[0] : k == 1 ? ids[1] : k == 2 ? ids[2] : ids[3];
-            if (lane < 8 && id >= 0) {
-                const int64_t row = (static_cast<int64_t>(id) * (Hkv >> p.hshift) + (L.h >> p.hshift)) * S + rowoff;
-                const uint32_t dst = sbase + stage * Lay::kStageBytes + k * rows * Lay::kRow;
-                bulk_load_hint(lane < 4 ? dst : dst + Lay::kTileBytes,
-                               (lane < 4 ? p.k_cache : p.v_cache) + row * Lay::kRow, rows * Lay::kRow, bar, policy);
-            }
-        } else if (lane == 0) {
+        if (lane == 0) {
             const uint32_t bar = full_bars + 8 * stage;
             st_shared_u32(bad_flags + 4 * stage, bad ? 1u : 0u);   // published by the arrive below
             mbar_arrive_expect_tx(bar, bytes);
@@ -1074,8 +1116,52 @@ paged_decode_attn_kernel(const AttnParams p, const __grid_constant__ CUtensorMap
 
         // ---- S^T = K Q^T : tokens on M (16-row tiles), heads on N ----
         float sacc[MT][4];
+        if (kFp4) {
+            // This lane's 32 dims of a row are the scale blocks t and 4 + t (8
+            // bytes each).  code * scale is exact in f16: 2 and 4 significant
+            // bits, magnitude 2^-10 .. 2688.  The M tiles go side by side, so
+            // that an accumulator's next MMA comes MT MMAs later, not at once.
+            uint32_t ksc[2 * MT];                          // per row: the scales of blocks t and 4 + t
 #pragma unroll
-        for (int mt = 0; mt < MT; ++mt) {
+            for (int j = 0; j < 2 * MT; ++j) ksc[j] = ld_fp4_scales(kbase + (8 * j + g) * Lay::kRow, t);
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt) sacc[mt][0] = sacc[mt][1] = sacc[mt][2] = sacc[mt][3] = 0.f;
+            // Steps of (block, word of 8 dims, M tile): 8 conversions, 8 products
+            // and 2 MMAs each, which run on three pipes; each step converts for
+            // the next one before its own MMAs, so that all three are fed.
+            uint2 kw[2 * MT];
+            uint32_t fa[2][4], fb[2][4];
+            auto convert = [&](int step) {
+                const int blk = step / (2 * MT), wd = step / MT & 1, mt = step % MT, b = step & 1;
+                e2m1x8_to_f16(wd ? kw[2 * mt].y : kw[2 * mt].x, fa[b]);
+                e2m1x8_to_f16(wd ? kw[2 * mt + 1].y : kw[2 * mt + 1].x, fb[b]);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    fa[b][j] = mul_f16_half(fa[b][j], ksc[2 * mt], blk);
+                    fb[b][j] = mul_f16_half(fb[b][j], ksc[2 * mt + 1], blk);
+                }
+            };
+            auto load_block = [&](int blk, int j) {
+                kw[j] = ld_shared_v2(kbase + (8 * j + g) * Lay::kRow + 32 * blk + 8 * t);
+            };
+#pragma unroll
+            for (int j = 0; j < 2 * MT; ++j) load_block(0, j);
+            convert(0);
+#pragma unroll
+            for (int step = 0; step < 4 * MT; ++step) {
+                const int blk = step / (2 * MT), wd = step / MT & 1, mt = step % MT, b = step & 1;
+                if (blk == 0 && wd == 1) {                 // this M tile's words of block t are used up
+                    load_block(1, 2 * mt);
+                    load_block(1, 2 * mt + 1);
+                }
+                if (step + 1 < 4 * MT) convert(step + 1);
+                const int ks = 4 * blk + 2 * wd;
+                mma_f16(sacc[mt], fa[b][0], fb[b][0], fa[b][1], fb[b][1], qb[ks][0], qb[ks][1]);
+                mma_f16(sacc[mt], fa[b][2], fb[b][2], fa[b][3], fb[b][3], qb[ks + 1][0], qb[ks + 1][1]);
+            }
+        }
+#pragma unroll
+        for (int mt = 0; mt < (kFp4 ? 0 : MT); ++mt) {
             float acc[NACC][4];
 #pragma unroll
             for (int a = 0; a < NACC; ++a) acc[a][0] = acc[a][1] = acc[a][2] = acc[a][3] = 0.f;
@@ -1092,26 +1178,6 @@ paged_decode_attn_kernel(const AttnParams p, const __grid_constant__ CUtensorMap
                 for (int ks = 0; ks < 8; ++ks) {
                     mma_f16(acc[ks % NACC], e4m3x2_to_f16x2(lo16(wa[ks])), e4m3x2_to_f16x2(lo16(wb[ks])),
                             e4m3x2_to_f16x2(hi16(wa[ks])), e4m3x2_to_f16x2(hi16(wb[ks])), qb[ks][0], qb[ks][1]);
-                }
-            } else if (kFp4) {
-                // This lane's 32 dims of rows ra, rb are the scale blocks t and
-                // 4 + t (8 bytes each).  code * scale is exact in f16: 2 and 4
-                // significant bits, magnitude 2^-10 .. 2688.
-                uint32_t ka[4], kb[4], sa[2], sb[2];
-                ld_fp4_row(kbase + ra * Lay::kRow, t, ka, sa);
-                ld_fp4_row(kbase + rb * Lay::kRow, t, kb, sb);
-#pragma unroll
-                for (int w2 = 0; w2 < 4; ++w2) {                     // word of 8 dims: k-steps 2 w2, 2 w2 + 1
-                    uint32_t fa[4], fb[4];
-                    e2m1x8_to_f16(ka[w2], fa);
-                    e2m1x8_to_f16(kb[w2], fb);
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        fa[j] = mul_f16x2(fa[j], sa[w2 >> 1]);
-                        fb[j] = mul_f16x2(fb[j], sb[w2 >> 1]);
-                    }
-                    mma_f16(acc[0], fa[0], fb[0], fa[1], fb[1], qb[2 * w2][0], qb[2 * w2][1]);
-                    mma_f16(acc[NACC - 1], fa[2], fb[2], fa[3], fb[3], qb[2 * w2 + 1][0], qb[2 * w2 + 1][1]);
                 }
             } else {
                 // dims 16t..16t+15 (half 0, chunks 2t, 2t+1) and 64+16t.. (half 1)
@@ -1134,6 +1200,7 @@ paged_decode_attn_kernel(const AttnParams p, const __grid_constant__ CUtensorMap
         }
 
         // ---- online softmax (log2 domain); columns are heads 2t, 2t+1 ----
+        if (!kFp4 || nvalid < kTile)
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt) {
             if (mt * 16 + g >= nvalid) sacc[mt][0] = sacc[mt][1] = -INFINITY;
@@ -1175,6 +1242,9 @@ paged_decode_attn_kernel(const AttnParams p, const __grid_constant__ CUtensorMap
             }
         l[0] = l[0] * alpha[0] + ls[0];
         l[1] = l[1] * alpha[1] + ls[1];
+        // (the 4-bit kernel, nearer its issue limit, skips the products by 1 once
+        // the maxima have settled)
+        if (!kFp4 || __any_sync(kFull, alpha[0] != 1.f || alpha[1] != 1.f))
 #pragma unroll
         for (int a = 0; a < 8; ++a) {
             o[a][0] *= alpha[0];
@@ -1208,8 +1278,25 @@ paged_decode_attn_kernel(const AttnParams p, const __grid_constant__ CUtensorMap
         }
 
         // ---- O^T += V^T P^T : dims on M (8 blocks of 16), tokens on K ----
+        if (kFp4) {
+            // dims 16g .. 16g+15 (scale block g) of four token rows per M tile
 #pragma unroll
-        for (int mt = 0; mt < MT; ++mt) {
+            for (int mt = 0; mt < MT; ++mt) {
+                const uint32_t v0 = vbase + (16 * mt + 2 * t) * Lay::kRow, v1 = v0 + 8 * Lay::kRow;
+                const Fp4Pair lo = ld_fp4_pair(v0, v0 + Lay::kRow, g), hi = ld_fp4_pair(v1, v1 + Lay::kRow, g);
+#pragma unroll
+                for (int wd = 0; wd < 2; ++wd) {
+                    uint32_t x[8], y[8];
+                    fp4_pairs(lo, wd, x);
+                    fp4_pairs(hi, wd, y);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        mma_f16(o[4 * wd + j], x[2 * j], x[2 * j + 1], y[2 * j], y[2 * j + 1], pb[mt][0], pb[mt][1]);
+                }
+            }
+        }
+#pragma unroll
+        for (int mt = 0; mt < (kFp4 ? 0 : MT); ++mt) {
             const int r0 = mt * 16 + 2 * t, r1 = r0 + 1, r2 = r0 + 8, r3 = r0 + 9;
             if (kFp8) {
                 // dims 16g .. 16g+15 of four token rows (16-byte chunk g, swizzled)
@@ -1228,28 +1315,6 @@ paged_decode_attn_kernel(const AttnParams p, const __grid_constant__ CUtensorMap
                             e4m3x2_to_f16x2(lo16(cd0)), e4m3x2_to_f16x2(hi16(cd0)), pb[mt][0], pb[mt][1]);
                     mma_f16(o[2 * qq + 1], e4m3x2_to_f16x2(lo16(ab1)), e4m3x2_to_f16x2(hi16(ab1)),
                             e4m3x2_to_f16x2(lo16(cd1)), e4m3x2_to_f16x2(hi16(cd1)), pb[mt][0], pb[mt][1]);
-                }
-            } else if (kFp4) {
-                // A byte holds dims 2j, 2j + 1 of one token, so a converted pair
-                // cannot feed the MMA's K axis (tokens) directly.  Instead the K
-                // axis takes (token, parity) slots: M is the 64 dim pairs, an
-                // MMA step covers 8 tokens, and P goes in twice, beside zeros,
-                // once against the even dims and once against the odd ones.
-                // That doubles the PV MMAs and saves regrouping nibbles, which
-                // costs 7 ALU operations per 8 values against this one's none.
-#pragma unroll
-                for (int hf = 0; hf < 2; ++hf) {                     // tokens 8 hf .. 8 hf + 7 of the 16
-                    const uint32_t v0 = vbase + (r0 + 8 * hf) * Lay::kRow, v1 = v0 + Lay::kRow;
-                    uint32_t x0[8], x1[8];
-                    ld_fp4_block(v0, g, x0);                         // dims 16g .. 16g+15 of tokens r0, r1
-                    ld_fp4_block(v1, g, x1);
-                    const uint32_t pp = pb[mt][hf];
-                    const uint32_t e0 = pp & 0xFFFFu, e1 = pp >> 16, o0 = pp << 16, o1 = pp & 0xFFFF0000u;
-#pragma unroll
-                    for (int a = 0; a < 4; ++a) {
-                        mma_f16(o[2 * a], x0[2 * a], x0[2 * a + 1], x1[2 * a], x1[2 * a + 1], e0, e1);
-                        mma_f16(o[2 * a + 1], x0[2 * a], x0[2 * a + 1], x1[2 * a], x1[2 * a + 1], o0, o1);
-                    }
                 }
             } else {
                 // dims 8g..8g+7 (half 0, chunk g) and 64+8g.. (half 1, chunk g)
@@ -1363,8 +1428,8 @@ paged_decode_attn_kernel(const AttnParams p, const __grid_constant__ CUtensorMap
                     Lj[j] = __fmaf_rn(0.f, 0.f, sl);
 #pragma unroll
                     for (int a = 0; a < 8; ++a) {
-                        v[j][out_dim<kKv>(a, 0)] = __fmaf_rn(w0, o[a][j], 0.f);
-                        v[j][out_dim<kKv>(a, 1)] = __fmaf_rn(w0, o[a][2 + j], 0.f);
+                        v[j][2 * a] = __fmaf_rn(w0, o[a][j], 0.f);
+                        v[j][2 * a + 1] = __fmaf_rn(w0, o[a][2 + j], 0.f);
                     }
                 }
                 for (int k = 0; k < no; ++k) {
@@ -1433,8 +1498,8 @@ paged_decode_attn_kernel(const AttnParams p, const __grid_constant__ CUtensorMap
                 float v[16];
 #pragma unroll
                 for (int a = 0; a < 8; ++a) {
-                    v[out_dim<kKv>(a, 0)] = o[a][j];
-                    v[out_dim<kKv>(a, 1)] = o[a][2 + j];
+                    v[2 * a] = o[a][j];
+                    v[2 * a + 1] = o[a][2 + j];
                 }
                 const int d0 = kScaled ? 16 * g : 8 * g;          // first run of dims
                 const int d1 = kScaled ? 16 * g + 8 : 64 + 8 * g; // second run (8 dims each)
@@ -1557,7 +1622,7 @@ int ctas_per_sm() {
             return 0;
         int nb = 0;
         if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&nb, paged_decode_attn_kernel<kKv, kWS, false>,
-                                                          attn_threads(kWS), smem) != cudaSuccess ||
+                                                          attn_threads<kKv>(kWS), smem) != cudaSuccess ||
             nb <= 0)
             return 0;
         c.n = nb < 16 ? nb : 16;
@@ -1569,7 +1634,10 @@ int ctas_per_sm() {
 // Computing warps of one launch (one per CTA).
 template <int kKv>
 int grid_warps_of(bool ws) {
-    return device_sm_count() * (ws ? ctas_per_sm<kKv, true>() : ctas_per_sm<kKv, false>());
+    if constexpr (kKv == FKV_KV_FP4)
+        return ws ? 0 : device_sm_count() * ctas_per_sm<kKv, false>() * Cfg<kKv>::kWarps;
+    else
+        return device_sm_count() * (ws ? ctas_per_sm<kKv, true>() : ctas_per_sm<kKv, false>());
 }
 int grid_warps(int kv, bool ws) {
     return kv == FKV_KV_FP8_E4M3 ? grid_warps_of<FKV_KV_FP8_E4M3>(ws)
@@ -1591,6 +1659,7 @@ bool known_kv(int kv) { return kv == FKV_KV_FP8_E4M3 || kv == FKV_KV_BF16 || kv 
 #define FKV_WS_PAGE_LIMIT 64
 #endif
 bool use_ws(int page_size, int kv) {
+    if (kv == FKV_KV_FP4) return false;      // its untiled copies go out one per lane
     const int tile = tile_tokens(kv);
     return page_size < (FKV_WS_PAGE_LIMIT < tile ? FKV_WS_PAGE_LIMIT : tile);
 }
@@ -1599,9 +1668,9 @@ template <int kKv>
 cudaError_t launch_attn(bool two_warp, bool aligned, dim3 grid, cudaStream_t st, const AttnParams &p, const CUtensorMap &tmK,
                         const CUtensorMap &tmV) {
     auto go = [&](auto kern, bool ws) {
-        return launch_pdl(kern, grid, dim3(attn_threads(ws)), Layout<kKv>::kSmem, st, p, tmK, tmV);
+        return launch_pdl(kern, grid, dim3(attn_threads<kKv>(ws)), Layout<kKv>::kSmem, st, p, tmK, tmV);
     };
-    if (two_warp)
+    if constexpr (kKv != FKV_KV_FP4) if (two_warp)
         return aligned ? go(paged_decode_attn_kernel<kKv, true, true>, true)
                        : go(paged_decode_attn_kernel<kKv, true, false>, true);
     return aligned ? go(paged_decode_attn_kernel<kKv, false, true>, false)
@@ -1667,7 +1736,7 @@ extern "C" size_t paged_decode_attn_workspace_size(int32_t batch, int32_t num_q_
     // sized for either CTA shape (the page size is not known here)
     const int n1 = grid_warps(kv_dtype, false), n2 = grid_warps(kv_dtype, true);
     const int NW = n1 > n2 ? n1 : n2;
-    if (n1 <= 0 || n2 <= 0) return 0;
+    if (n1 <= 0 || (n2 <= 0 && kv_dtype != FKV_KV_FP4)) return 0;
     return ws_layout(batch, num_kv_heads * R, num_q_heads / num_kv_heads / R, NW).total;
 }
 
@@ -1752,7 +1821,7 @@ extern "C" fkv_status paged_decode_attn(const void *q, int32_t batch, int32_t nu
     // decide from the live requests alone, so the schedule never depends on
     // aborted or empty requests.
     const bool aligned = FKV_ALIGNED_SCHEDULE && batch <= 64;
-    const dim3 grid(NW);
+    const dim3 grid(kv_dtype == FKV_KV_FP4 ? NW / Cfg<FKV_KV_FP4>::kWarps : NW);
     if (fp8)
         e = launch_attn<FKV_KV_FP8_E4M3>(two_warp, aligned, grid, st, p, tmK, tmV);
     else if (kv_dtype == FKV_KV_BF16)

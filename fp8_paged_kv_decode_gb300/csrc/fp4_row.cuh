@@ -49,32 +49,50 @@ __device__ __forceinline__ uint32_t e4m3_to_f16_pair(uint32_t byte) {
     return e4m3x2_to_f16x2(static_cast<uint16_t>(prmt(byte, 0u, 0x4400u)));
 }
 
-// A lane's share of a K row in shared memory: the codes of scale blocks t and
-// 4 + t (dims 16t .. 16t + 15 and 64 + 16t ..) and the blocks' scales as pairs.
-__device__ __forceinline__ void ld_fp4_row(uint32_t row, int t, uint32_t (&w)[4], uint32_t (&s)[2]) {
-    const uint2 a = ld_shared_v2(row + 8 * t), b = ld_shared_v2(row + 32 + 8 * t);
-    const uint2 sc = ld_shared_v2(row + kFp4Codes);
-    w[0] = a.x;
-    w[1] = a.y;
-    w[2] = b.x;
-    w[3] = b.y;
-    const uint32_t two = prmt(sc.x, sc.y, 0x4400u + 0x1111u * t);          // bytes t, t, 4 + t, 4 + t
-    s[0] = e4m3x2_to_f16x2(static_cast<uint16_t>(two & 0xFFFFu));
-    s[1] = e4m3x2_to_f16x2(static_cast<uint16_t>(two >> 16));
+// f times the low (0) or high (1) half of a pair of scales.
+__device__ __forceinline__ uint32_t mul_f16_half(uint32_t f, uint32_t pair, int half) {
+    const __half2 s = *reinterpret_cast<const __half2 *>(&pair);
+    const __half2 d = __hmul2(*reinterpret_cast<const __half2 *>(&f), half ? __high2half2(s) : __low2half2(s));
+    return *reinterpret_cast<const uint32_t *>(&d);
 }
 
-// A lane's share of a V row: the 16 values of scale block g as f16 pairs
-// (code * scale, exact).
-__device__ __forceinline__ void ld_fp4_block(uint32_t row, int g, uint32_t (&x)[8]) {
-    const uint2 c = ld_shared_v2(row + 8 * g);
-    const uint32_t s = e4m3_to_f16_pair(ld_shared_u8(row + kFp4Codes + g));
-    uint32_t f[4];
-    e2m1x8_to_f16(c.x, f);
+// The scales of blocks t and 4 + t of a row in shared memory, as an f16 pair.
+__device__ __forceinline__ uint32_t ld_fp4_scales(uint32_t row, int t) {
+    const uint2 sc = ld_shared_v2(row + kFp4Codes);
+    return e4m3x2_to_f16x2(static_cast<uint16_t>(prmt(sc.x, sc.y, 0x40u + 0x11u * t)));
+}
+
+// A lane's share of two V rows in shared memory: the codes of scale block g and
+// the two rows' scales of it as an f16 pair.
+struct Fp4Pair {
+    uint2 c0, c1;
+    uint32_t s;
+};
+__device__ __forceinline__ Fp4Pair ld_fp4_pair(uint32_t row0, uint32_t row1, int g) {
+    Fp4Pair v;
+    v.c0 = ld_shared_v2(row0 + 8 * g);
+    v.c1 = ld_shared_v2(row1 + 8 * g);
+    const uint32_t b0 = ld_shared_u8(row0 + kFp4Codes + g), b1 = ld_shared_u8(row1 + kFp4Codes + g);
+    v.s = e4m3x2_to_f16x2(static_cast<uint16_t>(b0 | (b1 << 8)));
+    return v;
+}
+
+// The values of dims 8w .. 8w + 7 of the block as f16 pairs (first row, second
+// row).  The rows' nibbles are interleaved first, two operations for four
+// dims, so that a converted byte is one dim of both rows; converting each row
+// and then regrouping halves costs four.
+__device__ __forceinline__ void fp4_pairs(const Fp4Pair &v, int w, uint32_t (&x)[8]) {
+    const uint32_t a = w ? v.c0.y : v.c0.x, b = w ? v.c1.y : v.c1.x;
+    const uint32_t even = (a & 0x0F0F0F0Fu) | ((b << 4) & 0xF0F0F0F0u);
+    const uint32_t odd = ((a >> 4) & 0x0F0F0F0Fu) | (b & 0xF0F0F0F0u);
+    uint32_t e[4], o[4];
+    e2m1x8_to_f16(even, e);
+    e2m1x8_to_f16(odd, o);
 #pragma unroll
-    for (int j = 0; j < 4; ++j) x[j] = mul_f16x2(f[j], s);
-    e2m1x8_to_f16(c.y, f);
-#pragma unroll
-    for (int j = 0; j < 4; ++j) x[4 + j] = mul_f16x2(f[j], s);
+    for (int j = 0; j < 4; ++j) {
+        x[2 * j] = mul_f16x2(e[j], v.s);
+        x[2 * j + 1] = mul_f16x2(o[j], v.s);
+    }
 }
 
 }  // namespace fkv
