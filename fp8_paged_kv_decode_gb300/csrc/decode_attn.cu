@@ -45,6 +45,7 @@
 
 #include <cmath>
 #include <mutex>
+#include <type_traits>
 
 #include "fp4_row.cuh"
 
@@ -63,10 +64,10 @@
 #endif
 // Computing warps of a 4-bit CTA and the CTAs an SM holds.
 #ifndef FKV_FP4_WARPS
-#define FKV_FP4_WARPS 4
+#define FKV_FP4_WARPS 2
 #endif
 #ifndef FKV_FP4_CTAS
-#define FKV_FP4_CTAS 2
+#define FKV_FP4_CTAS 4
 #endif
 #ifndef FKV_BF16_TILE
 #define FKV_BF16_TILE 64
@@ -702,7 +703,11 @@ paged_decode_attn_kernel(const AttnParams p, const __grid_constant__ CUtensorMap
     const int g = lane >> 2, t = lane & 3;
     const int w = blockIdx.x * kWarps + warp;
     const int S = p.S, Hkv = p.Hkv, G = p.G;
-    const int S_log = 31 - __clz(S);                   // page sizes are powers of two
+    // log2 of the page size, a power of two, for the 4-bit copies.  (The other
+    // formats divide: with shifts in their place the 64-request FP8 call took
+    // 389 us instead of 377, the 256-request one of 16-token pages 323 instead
+    // of 326.)
+    const int S_log = 31 - __clz(S);
 
     if (kWarps > 1 ? lane == 0 : threadIdx.x == 0) {
         for (int s = 0; s < NST; ++s) {
@@ -781,7 +786,9 @@ paged_decode_attn_kernel(const AttnParams p, const __grid_constant__ CUtensorMap
         grid_dep_launch();
         return;
     }
-    const int64_t n_tiles = hi - lo;
+    // (a warp's tiles fit 32 bits; the 4-bit kernel's loop counts in them)
+    using Count = std::conditional_t<kFp4, int, int64_t>;
+    const Count n_tiles = static_cast<Count>(hi - lo);
     // entries one shared-memory merge round holds (the idle stage ring: outputs,
     // statistics and weights of each; one entry per lane)
     const int merge_cap = min(32, (NST * Lay::kStageBytes) / (G * kD * 4 + ((G + 1) & ~1) * 8 + 32));
@@ -808,7 +815,7 @@ paged_decode_attn_kernel(const AttnParams p, const __grid_constant__ CUtensorMap
         pid_r = fr.r0;                                 // the first request's page-table row is known
         lseq = fr.sl0;
         lrow0 = fr.row0;
-        lneed = (lseq + S - 1) >> S_log;
+        lneed = (lseq + S - 1) / S;
         pbase = -1000;
     } else {
         cursor_init(L, p, lo, p.warp_req[w]);
@@ -882,14 +889,14 @@ paged_decode_attn_kernel(const AttnParams p, const __grid_constant__ CUtensorMap
             pid_r = L.r;
             lseq = __ldcg(p.seq_lens + L.r);
             lrow0 = __ldcg(p.indptr + L.r);
-            lneed = (lseq + S - 1) >> S_log;
+            lneed = (lseq + S - 1) / S;
             pbase = -1000;
         }
         const int tok0 = L.tt * kTile;
-        const int npg = S < kTile ? kTile >> S_log : 1;  // pages per tile (<= 4)
+        const int npg = S < kTile ? kTile / S : 1;       // pages per tile (<= 4)
         const int rows = S < kTile ? S : kTile;
-        const int pos0 = tok0 >> S_log;
-        const int rowoff = S < kTile ? 0 : tok0 & (S - 1);
+        const int pos0 = tok0 / S;
+        const int rowoff = S < kTile ? 0 : tok0 % S;
         int ids[4] = {-1, -1, -1, -1};
         bool bad = false;
         uint32_t bytes = 0;
@@ -1006,7 +1013,7 @@ paged_decode_attn_kernel(const AttnParams p, const __grid_constant__ CUtensorMap
     UnitGeom def_gm{0, 0};
     float def_vsc = 1.f;
 
-    for (int64_t i = 0; i < n_tiles; ++i) {
+    for (Count i = 0; i < n_tiles; ++i) {
         const int s = static_cast<int>(i % NST);
         const uint32_t parity = static_cast<uint32_t>((i / NST) & 1);
 
