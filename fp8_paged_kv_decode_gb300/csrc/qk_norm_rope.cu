@@ -5,17 +5,24 @@
 // with t = position * inv_freq per pair.  Each row is read and written once:
 // bound by memory at 512 bytes a head for prompts, by latency for decode steps.
 //
-// A block serves one token (or part of its heads): its threads first form the
-// token's cos and sin once, for all heads, in shared memory; then 16 threads
-// take a head row, 8 elements (16 bytes) each.
+// A warp serves one token, or part of its heads when there are few tokens.  16
+// lanes take a head row, 8 elements each, so that both elements of a pair are
+// in one lane: lane l holds elements 8l .. 8l + 7 where pairs are neighbours,
+// else the four elements 4l .. and their partners rotary_dim / 2 further.  The
+// weights are the same for every head, so they go into the rotation's
+// coefficients once per token:
+//   a' = rs (a wa cos - b wb sin),   b' = rs (b wb cos + a wa sin)
+// and a row costs its sum of squares, 12 products and the conversions.  Each
+// half-warp has four rows' loads in flight before it works on the first.
 #include <cmath>
 
 #include "fkv_common.cuh"
 
 namespace fkv {
 
-constexpr int kRopeBlock = 256;
-constexpr int kRopeRows = kRopeBlock / 16;     // head rows a block has in flight
+constexpr int kRopeBlock = 128;
+constexpr int kRopeUnroll = 4;                 // rows a half-warp has in flight
+constexpr int kRopeBatch = 2 * kRopeUnroll;    // rows of a warp's batch
 constexpr int kRopeMaxAxes = 8;
 
 struct RopeParams {
@@ -27,7 +34,7 @@ struct RopeParams {
     const float *inv_freq;
     const uint8_t *axis_map;
     uint32_t *err;
-    int32_t n_tokens, hq, heads, rows_per_block, n_axes, half, interleaved;
+    int32_t n_tokens, hq, heads, parts, rows_per_warp, n_axes, half;
     float eps, rot_scale;
 };
 
@@ -53,97 +60,148 @@ __device__ __forceinline__ float2 cos_sin_of(int32_t pos, float f) {
     return make_float2(c, s);
 }
 
-__device__ __forceinline__ void unpack8(const uint4 v, float (&x)[8]) {
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        x[2 * j] = __uint_as_float(w[j] << 16);
-        x[2 * j + 1] = __uint_as_float(w[j] & 0xFFFF0000u);
+__device__ __forceinline__ float2 bf16x2_to_f32(uint32_t w) {
+    return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
+}
+
+// A lane's 8 elements (or weights) as the first and second elements of its four
+// pairs.  d0, d1: its two groups of four elements, in units of four.
+template <bool kNeighbours>
+__device__ __forceinline__ void pairs_of(const uint2 u, const uint2 v, float (&a)[4], float (&b)[4]) {
+    const float2 u0 = bf16x2_to_f32(u.x), u1 = bf16x2_to_f32(u.y), v0 = bf16x2_to_f32(v.x), v1 = bf16x2_to_f32(v.y);
+    if (kNeighbours) {
+        a[0] = u0.x, b[0] = u0.y, a[1] = u1.x, b[1] = u1.y;
+        a[2] = v0.x, b[2] = v0.y, a[3] = v1.x, b[3] = v1.y;
+    } else {
+        a[0] = u0.x, a[1] = u0.y, a[2] = u1.x, a[3] = u1.y;
+        b[0] = v0.x, b[1] = v0.y, b[2] = v1.x, b[3] = v1.y;
     }
 }
 
+template <bool kNeighbours>
 __global__ void __launch_bounds__(kRopeBlock)
 qk_norm_rope_kernel(const RopeParams p) {
-    __shared__ float2 cs[64];
+    // (several parts only for few tokens: the warps fit 32 bits)
+    const uint32_t wid = blockIdx.x * (kRopeBlock / 32) + threadIdx.x / 32;
+    const uint32_t tok = p.parts == 1 ? wid : wid / p.parts;
+    const int64_t n = tok;
     grid_dep_wait();
     grid_dep_launch();
-    const int64_t n = blockIdx.x;
-    const int lane = threadIdx.x & 15;
-    const int first = blockIdx.y * p.rows_per_block;
-    const int last = min(p.heads, first + p.rows_per_block);
-    if (threadIdx.x < p.half) {
-        const int j = threadIdx.x;
-        const int axis = p.axis_map ? __ldg(p.axis_map + j) : 0;
-        float2 v = make_float2(1.f, 0.f);                      // an axis that is not there: unturned
-        if (axis < p.n_axes) {
-            v = cos_sin_of(__ldg(p.positions + static_cast<int64_t>(axis) * p.n_tokens + n), __ldg(p.inv_freq + j));
-            v.x *= p.rot_scale;
-            v.y *= p.rot_scale;
-        } else {
-            atomicOr(p.err, FKV_DEVERR_ROPE_AXIS);
-        }
-        cs[j] = v;
-    }
-    __syncthreads();
-    // this thread's 8 elements 8 lane .. 8 lane + 7 and where they turn
-    const bool turned = 8 * lane < 2 * p.half;
-    const int step = p.half >> 3;                              // lanes between the two parts of a pair
-    const bool upper = !p.interleaved && turned && lane >= step;
-    const int partner = p.interleaved || !turned ? lane : upper ? lane - step : lane + step;
-    float c[8], s[8];
+    if (n >= p.n_tokens) return;
+    const int first = static_cast<int>(wid - tok * p.parts) * p.rows_per_warp;
+    const int last = min(p.heads, first + p.rows_per_warp);
+    const int lane = threadIdx.x & 15, hw = (threadIdx.x >> 4) & 1;
+    // this lane's two groups of four elements; past rotary_dim they are not pairs
+    const int np = p.half >> 2;                                // lanes holding pairs
+    const bool turned = lane < np;
+    const int g0 = kNeighbours ? 2 * lane : turned ? lane : 2 * np + 2 * (lane - np);
+    const int g1 = kNeighbours || !turned ? g0 + 1 : lane + np;
+
+    const uint16_t *qrow = p.q + n * p.qs, *krow = p.k + n * p.ks;
+    uint2 u[kRopeUnroll], v[kRopeUnroll];
+    auto load = [&](int row0, int end, const uint16_t *src) {  // rows row0 + hw, + 2, ... below end
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        c[i] = 1.f;
-        s[i] = 0.f;
-        if (turned) {
-            const int j = p.interleaved ? 4 * lane + (i >> 1) : 8 * (upper ? lane - step : lane) + i;
-            const float2 v = cs[j];
-            c[i] = v.x;
-            // out = y c + partner's y s: the first of a pair takes -sin
-            s[i] = (p.interleaved ? (i & 1) != 0 : upper) ? v.y : -v.y;
-        }
-    }
-    for (int row = first + threadIdx.x / 16; row < last; row += kRopeRows) {
-        const bool is_k = row >= p.hq;
-        const int h = is_k ? row - p.hq : row;
-        const uint16_t *src = (is_k ? p.k + n * p.ks : p.q + n * p.qs) + h * 128;
-        uint16_t *dst = (is_k ? p.k_out + n * p.kos : p.q_out + n * p.qos) + h * 128;
-        const uint4 *w = is_k ? p.k_weight : p.q_weight;
-        const uint4 v = *(reinterpret_cast<const uint4 *>(src) + lane);
-        const unsigned mask = 0xFFFFu << (threadIdx.x & 16);
-        float x[8], y[8], z[8];
-        unpack8(v, x);
-        uint4 u;                                               // the partner's elements
-        const int from = (threadIdx.x & 16) + partner;
-        u.x = __shfl_sync(mask, v.x, from);
-        u.y = __shfl_sync(mask, v.y, from);
-        u.z = __shfl_sync(mask, v.z, from);
-        u.w = __shfl_sync(mask, v.w, from);
-        unpack8(u, z);
-        if (w) {
-            float ss = 0.f;
-#pragma unroll
-            for (int i = 0; i < 8; ++i) ss = fmaf(x[i], x[i], ss);
-#pragma unroll
-            for (int o = 1; o < 16; o <<= 1) ss += __shfl_xor_sync(mask, ss, o);
-            const float rs = rsqrtf(fmaf(ss, 1.f / 128.f, p.eps));
-            float wx[8], wz[8];
-            unpack8(__ldg(w + lane), wx);
-            unpack8(__ldg(w + partner), wz);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                x[i] = x[i] * rs * wx[i];
-                z[i] = z[i] * rs * wz[i];
+        for (int i = 0; i < kRopeUnroll; ++i) {
+            const int row = row0 + 2 * i + hw;
+            if (row < end) {
+                const uint2 *s = reinterpret_cast<const uint2 *>(src + static_cast<int64_t>(row) * 128);
+                u[i] = s[g0];
+                v[i] = s[g1];
             }
         }
+    };
+    const int q_end = min(last, p.hq), k_first = max(first, p.hq) - p.hq, k_end = last - p.hq;
+    if (first < q_end) load(first, q_end, qrow);
+    else load(k_first, k_end, krow);
+
+    // cos and sin of the lane's four pairs, two by each half-warp
+    float c[4], s[4];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const float other = p.interleaved ? x[i ^ 1] : z[i];
-            y[i] = turned ? fmaf(x[i], c[i], other * s[i]) : x[i];
+    for (int i = 0; i < 2; ++i) {
+        const int j = 4 * lane + 2 * hw + i;
+        float2 x = make_float2(1.f, 0.f);                      // an axis that is not there: unturned
+        if (turned) {
+            const int axis = p.axis_map ? __ldg(p.axis_map + j) : 0;
+            if (axis < p.n_axes) {
+                x = cos_sin_of(__ldg(p.positions + static_cast<int64_t>(axis) * p.n_tokens + n),
+                               __ldg(p.inv_freq + j));
+                x.x *= p.rot_scale;
+                x.y *= p.rot_scale;
+            } else {
+                atomicOr(p.err, FKV_DEVERR_ROPE_AXIS);
+            }
         }
-        *(reinterpret_cast<uint4 *>(dst) + lane) = make_uint4(pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]),
-                                                             pack_bf16x2(y[4], y[5]), pack_bf16x2(y[6], y[7]));
+        const float oc = __shfl_xor_sync(0xffffffffu, x.x, 16), os = __shfl_xor_sync(0xffffffffu, x.y, 16);
+        c[i] = hw ? oc : x.x;
+        s[i] = hw ? os : x.y;
+        c[2 + i] = hw ? x.x : oc;
+        s[2 + i] = hw ? x.y : os;
     }
+
+    // one kind of heads: its rows [row0, end), the first batch loaded already
+    auto run = [&](int row0, int end, const uint16_t *src, uint16_t *dst, const uint2 *weight) {
+        float ac[4], as[4], bc[4], bs[4];
+        if (weight) {
+            float wa[4], wb[4];
+            pairs_of<kNeighbours>(__ldg(weight + g0), __ldg(weight + g1), wa, wb);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                ac[i] = wa[i] * c[i];
+                as[i] = wa[i] * s[i];
+                bc[i] = wb[i] * c[i];
+                bs[i] = wb[i] * s[i];
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                ac[i] = bc[i] = c[i];
+                as[i] = bs[i] = s[i];
+            }
+        }
+        for (;; ) {
+#pragma unroll
+            for (int i = 0; i < kRopeUnroll; ++i) {
+                const int row = row0 + 2 * i + hw;
+                float a[4], b[4];
+                pairs_of<kNeighbours>(u[i], v[i], a, b);
+                float rs = 1.f;
+                if (weight) {
+                    float ss = 0.f;
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) ss = fmaf(a[e], a[e], fmaf(b[e], b[e], ss));
+#pragma unroll
+                    for (int o = 1; o < 16; o <<= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+                    rs = rsqrtf(fmaf(ss, 1.f / 128.f, p.eps));
+                }
+                float x[4], y[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    // a lane past rotary_dim keeps its elements apart: 0 times an
+                    // infinity in the other one would be a NaN
+                    x[e] = rs * (turned ? fmaf(a[e], ac[e], -b[e] * bs[e]) : a[e] * ac[e]);
+                    y[e] = rs * (turned ? fmaf(b[e], bc[e], a[e] * as[e]) : b[e] * bc[e]);
+                }
+                if (row < end) {
+                    uint2 *d = reinterpret_cast<uint2 *>(dst + static_cast<int64_t>(row) * 128);
+                    if (kNeighbours) {
+                        d[g0] = make_uint2(pack_bf16x2(x[0], y[0]), pack_bf16x2(x[1], y[1]));
+                        d[g1] = make_uint2(pack_bf16x2(x[2], y[2]), pack_bf16x2(x[3], y[3]));
+                    } else {
+                        d[g0] = make_uint2(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]));
+                        d[g1] = make_uint2(pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]));
+                    }
+                }
+            }
+            row0 += kRopeBatch;
+            if (row0 >= end) return;
+            load(row0, end, src);
+        }
+    };
+    if (first < q_end) {
+        run(first, q_end, qrow, p.q_out + n * p.qos, reinterpret_cast<const uint2 *>(p.q_weight));
+        if (k_first < k_end) load(k_first, k_end, krow);
+    }
+    if (k_first < k_end) run(k_first, k_end, krow, p.k_out + n * p.kos, reinterpret_cast<const uint2 *>(p.k_weight));
 }
 
 }  // namespace fkv
@@ -195,16 +253,21 @@ extern "C" fkv_status qk_norm_rope(const void *q, int64_t q_token_stride, int32_
     p.heads = num_q_heads + num_kv_heads;
     p.n_axes = n_axes;
     p.half = rotary_dim / 2;
-    p.interleaved = interleaved != 0;
     p.eps = eps;
     p.rot_scale = rot_scale;
-    // few tokens: several blocks share a token's heads
-    int parts = 1;
-    while (static_cast<int64_t>(n_tokens) * parts < 2 * sms && parts * kRopeRows < p.heads) ++parts;
-    p.rows_per_block = ((p.heads + parts - 1) / parts + kRopeRows - 1) / kRopeRows * kRopeRows;
-    parts = (p.heads + p.rows_per_block - 1) / p.rows_per_block;
-    const cudaError_t e = launch_pdl(qk_norm_rope_kernel, dim3(static_cast<unsigned>(n_tokens),
-                                                               static_cast<unsigned>(parts)),
-                                     dim3(kRopeBlock), 0, static_cast<cudaStream_t>(stream), p);
+    // A token's heads are shared out until there are 24 warps per SM, in whole
+    // batches: a warp with one batch pays its cos and sin for 8 rows.
+    const int most = (p.heads + kRopeBatch - 1) / kRopeBatch;
+    const int64_t want = (24 * static_cast<int64_t>(sms) + n_tokens - 1) / n_tokens;
+    const int parts = static_cast<int>(want < most ? want : most);
+    p.rows_per_warp = ((p.heads + parts - 1) / parts + kRopeBatch - 1) / kRopeBatch * kRopeBatch;
+    p.parts = (p.heads + p.rows_per_warp - 1) / p.rows_per_warp;
+    const int64_t blocks = (static_cast<int64_t>(n_tokens) * p.parts + kRopeBlock / 32 - 1) / (kRopeBlock / 32);
+    if (blocks > 0x7FFFFFFF) return FKV_ERR_UNSUPPORTED;
+    auto go = [&](auto kern) {
+        return launch_pdl(kern, dim3(static_cast<unsigned>(blocks)), dim3(kRopeBlock), 0,
+                          static_cast<cudaStream_t>(stream), p);
+    };
+    const cudaError_t e = interleaved ? go(qk_norm_rope_kernel<true>) : go(qk_norm_rope_kernel<false>);
     return e == cudaSuccess ? FKV_OK : FKV_ERR_CUDA;
 }
