@@ -90,10 +90,10 @@ __device__ __forceinline__ int64_t token_of(int64_t n_tokens, unsigned bx) {
     return n < n_tokens ? n : -1;
 }
 
-// Index of the (slot, KV head by) row in the pool, or -1: nothing
+// Element offset of the (slot, KV head by) row in the pool, or -1: nothing
 // to write (a padding slot, or one outside the pool, which is recorded).
-__device__ __forceinline__ int64_t slot_row(int64_t slot, int32_t num_pages, int32_t num_kv_heads,
-                                            int32_t page_size, int32_t page_shift, uint32_t *err, unsigned by) {
+__device__ __forceinline__ int64_t slot_offset(int64_t slot, int32_t num_pages, int32_t num_kv_heads,
+                                               int32_t page_size, int32_t page_shift, uint32_t *err, unsigned by) {
     if (slot < 0) return -1;                                      // padding token
     const int64_t page = page_shift >= 0 ? (slot >> page_shift) : slot / page_size;
     const int64_t off = slot - page * page_size;
@@ -101,14 +101,7 @@ __device__ __forceinline__ int64_t slot_row(int64_t slot, int32_t num_pages, int
         if ((threadIdx.x % kThreadsPerToken) == 0) atomicOr(err, FKV_DEVERR_APPEND_SLOT);
         return -1;
     }
-    return (page * num_kv_heads + by) * page_size + off;
-}
-
-// The same as the row's first element, for rows of kHeadDim elements.
-__device__ __forceinline__ int64_t slot_offset(int64_t slot, int32_t num_pages, int32_t num_kv_heads,
-                                               int32_t page_size, int32_t page_shift, uint32_t *err, unsigned by) {
-    const int64_t row = slot_row(slot, num_pages, num_kv_heads, page_size, page_shift, err, by);
-    return row < 0 ? -1 : row * kHeadDim;
+    return ((page * num_kv_heads + by) * page_size + off) * kHeadDim;
 }
 
 // The e4m3 codes of one thread's 16 bf16 elements (two uint4 of the row, in
@@ -286,35 +279,78 @@ kv_append_bf16_tag_check_kernel(const uint4 *__restrict__ k_new, const uint4 *__
 }
 
 // ---------------------------------------------------------------------------
-// The 4-bit cache.  The same threads and loads as the FP8 append: a thread's
-// 16 elements are one scale block, so the block's maximum, scale and codes need
-// no other thread.  Per (token, KV head): 512 bytes in, 144 out.
+// The 4-bit cache.  A thread's 16 elements are one scale block, so the block's
+// maximum, scale and codes need no other thread.  Per (token, KV head): 512
+// bytes in, 144 out.
+//
+// A block serves 32 tokens of one head's K or V, not both (as the FP8 append
+// does): pointers and scale are then the same for the block, and the encoding
+// (about 125 instructions for 16 elements) leaves little room for selecting
+// them per thread and for 64-bit addressing.
 // ---------------------------------------------------------------------------
+constexpr int kFp4Tokens = kBlock / kThreadsPerRow;            // 32
+
+struct Fp4Append {
+    const uint4 *k_new, *v_new;
+    const int64_t *slots;
+    const float *k_scale, *v_scale;
+    uint8_t *k_cache, *v_cache;
+    uint32_t *err;
+    uint64_t total_slots;       // pages x page_size
+    uint64_t page_bytes;        // one page's rows of all heads
+    uint32_t n_tokens, num_kv_heads, page_size;
+    int32_t page_shift;         // log2 of the page size, -1 if it is not a power of two
+    bool small;                 // total_slots and page_bytes fit 32 bits
+};
+
+// The quotients of two bf16 elements (x: the lower one), by div2_abs's sequence
+// with their signs left on: every step rounds to nearest, so a negative
+// element's quotient is the exact negative of its magnitude's (a zero's sign
+// aside, which the codes do not keep).
+__device__ __forceinline__ float2 div2(uint32_t word, uint64_t nb, uint64_t yy) {
+    uint64_t m, q0, r, q;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(m) : "r"(word << 16), "r"(word & 0xFFFF0000u));
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(q0) : "l"(m), "l"(yy));
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(q0), "l"(nb), "l"(m));
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(q) : "l"(r), "l"(yy), "l"(q0));
+    uint32_t lo, hi;
+    asm("mov.b64 {%0, %1}, %2;" : "=r"(lo), "=r"(hi) : "l"(q));
+    return make_float2(__uint_as_float(lo), __uint_as_float(hi));
+}
+
 // The 16 codes (8 bytes) and the scale byte of one block of bf16 elements, for
-// the KV head's scale g.  The quotients are IEEE divisions, by div2_abs where
-// its range holds (see there), with the sign put back on the quotient.
+// the KV head's scale g.  The quotients are IEEE divisions, by div2 where its
+// range holds (see div2_abs).
 __device__ __forceinline__ uint2 encode_fp4_16(const uint4 r0, const uint4 r1, float g, uint32_t &scale) {
     const uint32_t w[8] = {r0.x, r0.y, r0.z, r0.w, r1.x, r1.y, r1.z, r1.w};
-    uint32_t big = 0;                                          // largest |x| bit patterns, per half
+    uint32_t m = 0;                                            // largest |x| bit patterns, per half
 #pragma unroll
-    for (int j = 0; j < 8; ++j) big = max_u16x2(big, w[j] & 0x7FFF7FFFu);
-    big = max(big >> 16, big & 0xFFFFu);                       // a NaN's pattern is above every other
+    for (int j = 0; j < 8; ++j) m = max_u16x2(m, w[j] & 0x7FFF7FFFu);
+    const uint32_t big = max(m >> 16, m & 0xFFFFu);            // a NaN's pattern is above every other
     const float amax = __uint_as_float(big << 16);
-    scale = f32x2_to_e4m3x2(0.f, __fdiv_rn(amax, __fmul_rn(6.f, g))) & 0xFFu;
+    const float g6 = __fmul_rn(6.f, g);
+    const bool fast = recip_scale_ok(g6) && big <= 0x5F80u;    // |x| <= 2^64
+    float ratio;
+    if (fast) {
+        const float y = __frcp_rn(g6), q0 = __fmul_rn(amax, y);
+        ratio = __fmaf_rn(__fmaf_rn(q0, -g6, amax), y, q0);
+    } else {
+        ratio = __fdiv_rn(amax, g6);
+    }
+    scale = f32x2_to_e4m3x2(0.f, ratio) & 0xFFu;
     const uint32_t s16 = e4m3x2_to_f16x2(static_cast<uint16_t>(scale));
     const float d = __fmul_rn(__half2float(__ushort_as_half(static_cast<unsigned short>(s16 & 0xFFFFu))), g);
     if (!(d > 0.f)) return make_uint2(0u, 0u);                 // scale 0 or NaN
     uint32_t code[8];                                          // two codes each
-    if (recip_scale_ok(d) && big <= 0x5F80u) {                 // |x| <= 2^64
+    if (fast && recip_scale_ok(d)) {
         const float y = __frcp_rn(d);
         uint64_t nb, yy;
         asm("mov.b64 %0, {%1, %1};" : "=l"(nb) : "r"(__float_as_uint(-d)));
         asm("mov.b64 %0, {%1, %1};" : "=l"(yy) : "r"(__float_as_uint(y)));
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-            const float2 q = div2_abs(w[j], nb, yy);
-            code[j] = f32x2_to_e2m1x2(__uint_as_float(__float_as_uint(q.y) | (w[j] & 0x80000000u)),
-                                      __uint_as_float(__float_as_uint(q.x) | ((w[j] << 16) & 0x80000000u)));
+            const float2 q = div2(w[j], nb, yy);
+            code[j] = f32x2_to_e2m1x2(q.y, q.x);
         }
     } else {
 #pragma unroll
@@ -322,32 +358,39 @@ __device__ __forceinline__ uint2 encode_fp4_16(const uint4 r0, const uint4 r1, f
             code[j] = f32x2_to_e2m1x2(__fdiv_rn(__uint_as_float(w[j] & 0xFFFF0000u), d),
                                       __fdiv_rn(__uint_as_float(w[j] << 16), d));
     }
-    return make_uint2(code[0] | (code[1] << 8) | (code[2] << 16) | (code[3] << 24),
-                      code[4] | (code[5] << 8) | (code[6] << 16) | (code[7] << 24));
+    return make_uint2(prmt(prmt(code[0], code[1], 0x0040u), prmt(code[2], code[3], 0x0040u), 0x5410u),
+                      prmt(prmt(code[4], code[5], 0x0040u), prmt(code[6], code[7], 0x0040u), 0x5410u));
 }
 
-// One thread's share of the 4-bit append in block (bx, by).
-__device__ __forceinline__ void append_fp4_part(const uint4 *__restrict__ k_new, const uint4 *__restrict__ v_new,
-                                                const int64_t *__restrict__ slots, int64_t n_tokens,
-                                                const float *__restrict__ k_scale, const float *__restrict__ v_scale,
-                                                uint8_t *__restrict__ k_cache, uint8_t *__restrict__ v_cache,
-                                                int32_t num_pages, int32_t num_kv_heads, int32_t page_size,
-                                                int32_t page_shift, uint32_t *err, unsigned bx, unsigned by) {
-    const int64_t n = token_of(n_tokens, bx);
-    if (n < 0) return;
-    const int h = by;
-    const int sub = threadIdx.x % kThreadsPerToken;
-    const bool is_v = sub >= kThreadsPerRow;
-    const int chunk = sub % kThreadsPerRow;
-    const uint4 *src = (is_v ? v_new : k_new) + (n * num_kv_heads + h) * (kHeadDim / 8) + chunk * 2;
+// One thread's share of the 4-bit append: token group bx, `by` the head's K
+// (by < num_kv_heads) or V rows.
+__device__ __forceinline__ void append_fp4_part(const Fp4Append &p, unsigned bx, unsigned by) {
+    const uint32_t n = bx * kFp4Tokens + threadIdx.x / kThreadsPerRow;
+    if (n >= p.n_tokens) return;
+    const bool is_v = by >= p.num_kv_heads;
+    const uint32_t h = is_v ? by - p.num_kv_heads : by;
+    const uint32_t chunk = threadIdx.x % kThreadsPerRow;
+    const uint4 *src = (is_v ? p.v_new : p.k_new) + static_cast<uint64_t>(n) * (p.num_kv_heads * (kHeadDim / 8)) +
+                       (h * (kHeadDim / 8) + chunk * 2);
     const uint4 r0 = __ldcs(src), r1 = __ldcs(src + 1);        // in flight with the scale's and the slot's loads
-    const float g = __ldg((is_v ? v_scale : k_scale) + h);
-    const int64_t slot = __ldg(slots + n);
-    const int64_t row = slot_row(slot, num_pages, num_kv_heads, page_size, page_shift, err, by);
-    if (row < 0) return;
+    const float g = __ldg((is_v ? p.v_scale : p.k_scale) + h);
+    const int64_t slot = __ldg(p.slots + n);
+    if (static_cast<uint64_t>(slot) >= p.total_slots) {        // padding, or outside the pool: skip, record
+        if (slot >= 0 && chunk == 0) atomicOr(p.err, FKV_DEVERR_APPEND_SLOT);
+        return;
+    }
+    uint8_t *dst = is_v ? p.v_cache : p.k_cache;
+    if (p.small && p.page_shift >= 0) {
+        const uint32_t s = static_cast<uint32_t>(slot), page = s >> p.page_shift;
+        dst += static_cast<uint64_t>(page) * static_cast<uint32_t>(p.page_bytes) +
+               (h * p.page_size + (s - (page << p.page_shift))) * kFp4Row;
+    } else {
+        const uint64_t page = static_cast<uint64_t>(slot) / p.page_size;
+        dst += page * p.page_bytes +
+               (static_cast<uint64_t>(h) * p.page_size + (static_cast<uint64_t>(slot) - page * p.page_size)) * kFp4Row;
+    }
     uint32_t s;
     const uint2 codes = encode_fp4_16(r0, r1, g, s);
-    uint8_t *dst = (is_v ? v_cache : k_cache) + row * kFp4Row;
     __stcs(reinterpret_cast<uint2 *>(dst) + chunk, codes);
     // the row's 8 scale bytes: four lanes' bytes make a word (the 8 threads of a
     // row take the same branches, so their mask is whole)
@@ -359,27 +402,16 @@ __device__ __forceinline__ void append_fp4_part(const uint4 *__restrict__ k_new,
 }
 
 __global__ void __launch_bounds__(kBlock, FKV_APPEND_MIN_BLOCKS)
-kv_append_fp4_kernel(const uint4 *__restrict__ k_new, const uint4 *__restrict__ v_new,
-                     const int64_t *__restrict__ slots, int64_t n_tokens,
-                     const float *__restrict__ k_scale, const float *__restrict__ v_scale,
-                     uint8_t *__restrict__ k_cache, uint8_t *__restrict__ v_cache,
-                     int32_t num_pages, int32_t num_kv_heads, int32_t page_size, int32_t page_shift,
-                     uint32_t *err) {
+kv_append_fp4_kernel(const Fp4Append p) {
     grid_dep_wait();        // earlier readers of the pool (attention) have finished
     grid_dep_launch();
-    append_fp4_part(k_new, v_new, slots, n_tokens, k_scale, v_scale, k_cache, v_cache, num_pages, num_kv_heads,
-                    page_size, page_shift, err, blockIdx.x, blockIdx.y);
+    append_fp4_part(p, blockIdx.x, blockIdx.y);
 }
 
 // The 4-bit cache's step prologue in one launch, laid out like
 // kv_append_fp8_tag_check_kernel: check blocks first, then the append's.
 __global__ void __launch_bounds__(kBlock, FKV_APPEND_MIN_BLOCKS)
-kv_append_fp4_tag_check_kernel(const uint4 *__restrict__ k_new, const uint4 *__restrict__ v_new,
-                               const int64_t *__restrict__ slots, int64_t n_tokens,
-                               const float *__restrict__ k_scale, const float *__restrict__ v_scale,
-                               uint8_t *__restrict__ k_cache, uint8_t *__restrict__ v_cache,
-                               int32_t num_pages, int32_t num_kv_heads, int32_t page_size, int32_t page_shift,
-                               uint32_t *err, unsigned append_blocks_x,
+kv_append_fp4_tag_check_kernel(const Fp4Append p, unsigned append_blocks_x, int32_t num_pages,
                                const uint32_t *__restrict__ page_tags, const int32_t *__restrict__ page_indptr,
                                const int32_t *__restrict__ page_indices, const uint32_t *__restrict__ expected_tags,
                                int32_t batch, int64_t nnz, uint8_t *__restrict__ abort_mask) {
@@ -393,8 +425,7 @@ kv_append_fp4_tag_check_kernel(const uint4 *__restrict__ k_new, const uint4 *__r
         return;
     }
     const unsigned a = b - static_cast<unsigned>(batch);
-    append_fp4_part(k_new, v_new, slots, n_tokens, k_scale, v_scale, k_cache, v_cache, num_pages, num_kv_heads,
-                    page_size, page_shift, err, a % append_blocks_x, a / append_blocks_x);
+    append_fp4_part(p, a % append_blocks_x, a / append_blocks_x);
 }
 
 static fkv_status check_append_args(const void *k_new, const void *v_new, const int64_t *slot_mapping,
@@ -537,6 +568,32 @@ extern "C" fkv_status kv_append_bf16_tag_check(const void *k_new, const void *v_
     return e == cudaSuccess ? FKV_OK : FKV_ERR_CUDA;
 }
 
+static Fp4Append fp4_append(const void *k_new, const void *v_new, const int64_t *slot_mapping, int32_t n_tokens,
+                            const float *k_scale, const float *v_scale, uint8_t *k_cache, uint8_t *v_cache,
+                            int32_t num_pages, int32_t num_kv_heads, int32_t page_size, uint32_t *err) {
+    Fp4Append p;
+    p.k_new = static_cast<const uint4 *>(k_new);
+    p.v_new = static_cast<const uint4 *>(v_new);
+    p.slots = slot_mapping;
+    p.k_scale = k_scale;
+    p.v_scale = v_scale;
+    p.k_cache = k_cache;
+    p.v_cache = v_cache;
+    p.err = err;
+    p.total_slots = static_cast<uint64_t>(num_pages) * static_cast<uint32_t>(page_size);
+    p.page_bytes = static_cast<uint64_t>(num_kv_heads) * static_cast<uint32_t>(page_size) * kFp4Row;
+    p.n_tokens = static_cast<uint32_t>(n_tokens);
+    p.num_kv_heads = static_cast<uint32_t>(num_kv_heads);
+    p.page_size = static_cast<uint32_t>(page_size);
+    p.page_shift = page_shift_of(page_size);
+    p.small = p.total_slots <= 0xFFFFFFFFu && p.page_bytes <= 0xFFFFFFFFu;
+    return p;
+}
+
+static unsigned fp4_blocks_x(int32_t n_tokens) {
+    return static_cast<unsigned>((static_cast<int64_t>(n_tokens) + kFp4Tokens - 1) / kFp4Tokens);
+}
+
 extern "C" fkv_status kv_append_fp4(const void *k_new, const void *v_new, const int64_t *slot_mapping,
                                     int32_t n_tokens, const float *k_scale, const float *v_scale,
                                     uint8_t *k_cache, uint8_t *v_cache, int32_t num_pages,
@@ -544,15 +601,17 @@ extern "C" fkv_status kv_append_fp4(const void *k_new, const void *v_new, const 
                                     void *stream) {
     fkv_status st = check_append_args(k_new, v_new, slot_mapping, n_tokens, k_cache, v_cache, num_pages,
                                       num_kv_heads, page_size, head_dim);
-    if (st != FKV_OK || n_tokens == 0) return st;
+    if (st != FKV_OK) return st;
+    if (2 * static_cast<int64_t>(num_kv_heads) > 65535) return FKV_ERR_UNSUPPORTED;       // grid y
+    if (n_tokens == 0) return FKV_OK;
     if (!k_scale || !v_scale) return FKV_ERR_INVALID_ARG;
     uint32_t *err = device_error_word();
     if (!err) return FKV_ERR_CUDA;
-    const cudaError_t e = launch_pdl(kv_append_fp4_kernel, append_grid(n_tokens, num_kv_heads), dim3(kBlock), 0,
-                                     static_cast<cudaStream_t>(stream), static_cast<const uint4 *>(k_new),
-                                     static_cast<const uint4 *>(v_new), slot_mapping, static_cast<int64_t>(n_tokens),
-                                     k_scale, v_scale, k_cache, v_cache, num_pages, num_kv_heads, page_size,
-                                     page_shift_of(page_size), err);
+    const Fp4Append p = fp4_append(k_new, v_new, slot_mapping, n_tokens, k_scale, v_scale, k_cache, v_cache, num_pages,
+                                   num_kv_heads, page_size, err);
+    const cudaError_t e = launch_pdl(kv_append_fp4_kernel,
+                                     dim3(fp4_blocks_x(n_tokens), 2u * static_cast<unsigned>(num_kv_heads)),
+                                     dim3(kBlock), 0, static_cast<cudaStream_t>(stream), p);
     return e == cudaSuccess ? FKV_OK : FKV_ERR_CUDA;
 }
 
@@ -568,16 +627,19 @@ extern "C" fkv_status kv_append_fp4_tag_check(const void *k_new, const void *v_n
                                               num_kv_heads, page_size, head_dim, page_tags, page_indptr,
                                               page_indices, expected_tags, batch, nnz, abort_mask, gx, blocks);
     if (st != FKV_OK) return st;
+    if (2 * static_cast<int64_t>(num_kv_heads) > 65535) return FKV_ERR_UNSUPPORTED;       // as kv_append_fp4
     if (n_tokens > 0 && (!k_scale || !v_scale)) return FKV_ERR_INVALID_ARG;
+    const unsigned fx = fp4_blocks_x(n_tokens);
+    blocks = static_cast<int64_t>(fx) * 2 * num_kv_heads + batch;
+    if (blocks > 0x7FFFFFFF) return FKV_ERR_UNSUPPORTED;
     if (blocks == 0) return FKV_OK;
     uint32_t *err = device_error_word();
     if (!err) return FKV_ERR_CUDA;
+    const Fp4Append p = fp4_append(k_new, v_new, slot_mapping, n_tokens, k_scale, v_scale, k_cache, v_cache, num_pages,
+                                   num_kv_heads, page_size, err);
     const cudaError_t e = launch_pdl(kv_append_fp4_tag_check_kernel, dim3(static_cast<unsigned>(blocks)),
-                                     dim3(kBlock), 0, static_cast<cudaStream_t>(stream),
-                                     static_cast<const uint4 *>(k_new), static_cast<const uint4 *>(v_new),
-                                     slot_mapping, static_cast<int64_t>(n_tokens), k_scale, v_scale, k_cache,
-                                     v_cache, num_pages, num_kv_heads, page_size, page_shift_of(page_size), err,
-                                     static_cast<unsigned>(gx > 0 ? gx : 1), page_tags, page_indptr, page_indices,
-                                     expected_tags, batch, nnz, abort_mask);
+                                     dim3(kBlock), 0, static_cast<cudaStream_t>(stream), p, fx > 0 ? fx : 1u,
+                                     num_pages, page_tags, page_indptr, page_indices, expected_tags, batch, nnz,
+                                     abort_mask);
     return e == cudaSuccess ? FKV_OK : FKV_ERR_CUDA;
 }

@@ -6,16 +6,26 @@
 // copied).  e4m3 codes and e2m1 code * block scale are exact in f16, so the
 // product with the head's scale is the only fp32 rounding before bf16's.
 //
-// Layout as in the append: grid of (16-token groups, KV heads), 16 threads per
+// Layout as in the append: grid of (token groups, KV heads), 16 threads per
 // (token, head), 8 on its K row and 8 on its V row, 16 elements each, so a
 // 4-bit thread reads one scale block.  Bound by memory: per (token, KV head)
-// 512 bytes out and 144 (FP4), 256 (FP8) or 512 (BF16) in.
+// 512 bytes out and 144 (FP4), 256 (FP8) or 512 (BF16) in.  A 4-bit thread's
+// row takes 9 bytes of loads, far too few in flight to cover their latency, so
+// a thread takes kU tokens and has all their slots, then all their rows, in
+// flight together.
 #include "fp4_row.cuh"
 
 namespace fkv {
 
 constexpr int kGatherBlock = 256;
 constexpr int kGatherTokens = kGatherBlock / 16;
+#ifndef GATHER_U
+#define GATHER_U 4
+#endif
+#ifndef GATHER_ST
+#define GATHER_ST __stcs
+#endif
+constexpr int kGatherMany = GATHER_U;
 
 // Two f16 values times the head's scale, rounded to bf16.
 __device__ __forceinline__ uint32_t scaled_bf16x2(uint32_t f16x2, float g) {
@@ -24,7 +34,69 @@ __device__ __forceinline__ uint32_t scaled_bf16x2(uint32_t f16x2, float g) {
     return pack_bf16x2(__fmul_rn(f.x, g), __fmul_rn(f.y, g));
 }
 
+// The raw bytes of one thread's 16 elements, and their bf16 values.
+struct GatherRaw {
+    uint4 a, b;
+    uint32_t s;
+};
+
 template <int kKv>
+__device__ __forceinline__ GatherRaw gather_load(const uint8_t *cache, uint64_t row, int chunk) {
+    GatherRaw r{};
+    if (kKv == FKV_KV_BF16) {
+        const uint4 *src = reinterpret_cast<const uint4 *>(cache) + row * 16 + chunk * 2;
+        r.a = __ldg(src);
+        r.b = __ldg(src + 1);
+    } else if (kKv == FKV_KV_FP8_E4M3) {
+        r.a = __ldg(reinterpret_cast<const uint4 *>(cache + row * 128) + chunk);
+    } else {
+        const uint8_t *src = cache + row * kFp4Row;
+        const uint2 c = __ldg(reinterpret_cast<const uint2 *>(src) + chunk);
+        r.a.x = c.x;
+        r.a.y = c.y;
+        r.s = __ldg(src + kFp4Codes + chunk);
+    }
+    return r;
+}
+
+template <int kKv>
+__device__ __forceinline__ void gather_store(uint4 *dst, const GatherRaw &r, float g, bool live) {
+    uint4 r0 = make_uint4(0u, 0u, 0u, 0u), r1 = r0;
+    if (live) {
+        if (kKv == FKV_KV_BF16) {
+            r0 = r.a;
+            r1 = r.b;
+        } else {
+            uint32_t f[8];                                 // 16 values in f16, in order
+            if (kKv == FKV_KV_FP8_E4M3) {
+                const uint32_t w[4] = {r.a.x, r.a.y, r.a.z, r.a.w};
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    f[2 * j] = e4m3x2_to_f16x2(static_cast<uint16_t>(w[j] & 0xFFFFu));
+                    f[2 * j + 1] = e4m3x2_to_f16x2(static_cast<uint16_t>(w[j] >> 16));
+                }
+            } else {
+                const uint32_t s = e4m3_to_f16_pair(r.s);
+                uint32_t lo[4], hi[4];
+                e2m1x8_to_f16(r.a.x, lo);
+                e2m1x8_to_f16(r.a.y, hi);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    f[j] = mul_f16x2(lo[j], s);
+                    f[4 + j] = mul_f16x2(hi[j], s);
+                }
+            }
+            r0 = make_uint4(scaled_bf16x2(f[0], g), scaled_bf16x2(f[1], g), scaled_bf16x2(f[2], g),
+                            scaled_bf16x2(f[3], g));
+            r1 = make_uint4(scaled_bf16x2(f[4], g), scaled_bf16x2(f[5], g), scaled_bf16x2(f[6], g),
+                            scaled_bf16x2(f[7], g));
+        }
+    }
+    GATHER_ST(dst, r0);
+    GATHER_ST(dst + 1, r1);
+}
+
+template <int kKv, int kU>
 __global__ void __launch_bounds__(kGatherBlock)
 kv_gather_kernel(const uint8_t *__restrict__ k_cache, const uint8_t *__restrict__ v_cache,
                  const float *__restrict__ k_scale, const float *__restrict__ v_scale,
@@ -33,59 +105,35 @@ kv_gather_kernel(const uint8_t *__restrict__ k_cache, const uint8_t *__restrict_
                  int32_t page_shift, uint32_t *err) {
     grid_dep_wait();
     grid_dep_launch();
-    const int64_t n = static_cast<int64_t>(blockIdx.x) * kGatherTokens + threadIdx.x / 16;
-    if (n >= n_tokens) return;
+    const int64_t n0 = static_cast<int64_t>(blockIdx.x) * (kGatherTokens * kU) + threadIdx.x / 16;
     const int h = blockIdx.y;
     const bool is_v = (threadIdx.x & 8) != 0;
     const int chunk = threadIdx.x & 7;
-    const int64_t slot = __ldg(slots + n);
-    uint4 *dst = (is_v ? v_out : k_out) + (n * num_kv_heads + h) * 16 + chunk * 2;
-    uint4 r0 = make_uint4(0u, 0u, 0u, 0u), r1 = r0;
-    if (slot >= 0) {
-        const int64_t page = page_shift >= 0 ? (slot >> page_shift) : slot / page_size;
-        const int64_t off = slot - page * page_size;
-        if (page >= num_pages) {
-            if ((threadIdx.x & 15) == 0) atomicOr(err, FKV_DEVERR_GATHER_SLOT);
-        } else {
-            const uint8_t *cache = is_v ? v_cache : k_cache;
-            const int64_t row = (page * num_kv_heads + h) * page_size + off;
-            if (kKv == FKV_KV_BF16) {
-                const uint4 *src = reinterpret_cast<const uint4 *>(cache) + row * 16 + chunk * 2;
-                r0 = __ldg(src);
-                r1 = __ldg(src + 1);
-            } else {
-                const float g = __ldg((is_v ? v_scale : k_scale) + h);
-                uint32_t f[8];                             // 16 values in f16, in order
-                if (kKv == FKV_KV_FP8_E4M3) {
-                    const uint4 c = __ldg(reinterpret_cast<const uint4 *>(cache + row * 128) + chunk);
-                    const uint32_t w[4] = {c.x, c.y, c.z, c.w};
+    const uint8_t *cache = is_v ? v_cache : k_cache;
+    int64_t slot[kU];
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        f[2 * j] = e4m3x2_to_f16x2(static_cast<uint16_t>(w[j] & 0xFFFFu));
-                        f[2 * j + 1] = e4m3x2_to_f16x2(static_cast<uint16_t>(w[j] >> 16));
-                    }
-                } else {
-                    const uint8_t *src = cache + row * kFp4Row;
-                    const uint2 c = __ldg(reinterpret_cast<const uint2 *>(src) + chunk);
-                    const uint32_t s = e4m3_to_f16_pair(__ldg(src + kFp4Codes + chunk));
-                    uint32_t lo[4], hi[4];
-                    e2m1x8_to_f16(c.x, lo);
-                    e2m1x8_to_f16(c.y, hi);
+    for (int u = 0; u < kU; ++u) slot[u] = n0 + u * kGatherTokens < n_tokens ? __ldg(slots + n0 + u * kGatherTokens) : -1;
+    const float g = kKv == FKV_KV_BF16 ? 1.f : __ldg((is_v ? v_scale : k_scale) + h);
+    GatherRaw raw[kU];
+    bool live[kU];
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        f[j] = mul_f16x2(lo[j], s);
-                        f[4 + j] = mul_f16x2(hi[j], s);
-                    }
-                }
-                r0 = make_uint4(scaled_bf16x2(f[0], g), scaled_bf16x2(f[1], g), scaled_bf16x2(f[2], g),
-                                scaled_bf16x2(f[3], g));
-                r1 = make_uint4(scaled_bf16x2(f[4], g), scaled_bf16x2(f[5], g), scaled_bf16x2(f[6], g),
-                                scaled_bf16x2(f[7], g));
-            }
+    for (int u = 0; u < kU; ++u) {
+        raw[u] = GatherRaw{};
+        const int64_t page = page_shift >= 0 ? (slot[u] >> page_shift) : slot[u] / page_size;
+        live[u] = slot[u] >= 0 && page < num_pages;
+        if (live[u]) {
+            const uint32_t off = static_cast<uint32_t>(slot[u] - page * page_size);
+            raw[u] = gather_load<kKv>(
+                cache, (static_cast<uint64_t>(static_cast<uint32_t>(page)) * num_kv_heads + h) * page_size + off, chunk);
+        } else if (slot[u] >= 0 && (threadIdx.x & 15) == 0) {
+            atomicOr(err, FKV_DEVERR_GATHER_SLOT);
         }
     }
-    dst[0] = r0;
-    dst[1] = r1;
+    uint4 *out = (is_v ? v_out : k_out) + (static_cast<uint64_t>(n0) * num_kv_heads + h) * 16 + chunk * 2;
+#pragma unroll
+    for (int u = 0; u < kU; ++u)
+        if (n0 + u * kGatherTokens < n_tokens)
+            gather_store<kKv>(out + static_cast<uint64_t>(u) * kGatherTokens * num_kv_heads * 16, raw[u], g, live[u]);
 }
 
 }  // namespace fkv
@@ -108,7 +156,12 @@ extern "C" fkv_status kv_gather(const void *k_cache, const void *v_cache, int32_
     if (!err) return FKV_ERR_CUDA;
     int32_t shift = -1;
     if ((page_size & (page_size - 1)) == 0) shift = __builtin_ctz(static_cast<unsigned>(page_size));
-    const dim3 grid(static_cast<unsigned>((static_cast<int64_t>(n_tokens) + kGatherTokens - 1) / kGatherTokens),
+    // Several tokens per thread once the grid fills the GPU without that.
+    const int sms = device_sm_count();
+    const int64_t rows = static_cast<int64_t>(n_tokens) * num_kv_heads;
+    const bool many = rows >= static_cast<int64_t>(sms) * 8 * kGatherTokens * kGatherMany;
+    const int per = kGatherTokens * (many ? kGatherMany : 1);
+    const dim3 grid(static_cast<unsigned>((static_cast<int64_t>(n_tokens) + per - 1) / per),
                     static_cast<unsigned>(num_kv_heads));
     auto go = [&](auto kern) {
         return launch_pdl(kern, grid, dim3(kGatherBlock), 0, static_cast<cudaStream_t>(stream),
@@ -116,8 +169,11 @@ extern "C" fkv_status kv_gather(const void *k_cache, const void *v_cache, int32_
                           v_scale, slots, n_tokens, static_cast<uint4 *>(k_out), static_cast<uint4 *>(v_out),
                           num_pages, num_kv_heads, page_size, shift, err);
     };
-    const cudaError_t e = kv_dtype == FKV_KV_FP8_E4M3 ? go(kv_gather_kernel<FKV_KV_FP8_E4M3>)
-                          : kv_dtype == FKV_KV_BF16   ? go(kv_gather_kernel<FKV_KV_BF16>)
-                                                      : go(kv_gather_kernel<FKV_KV_FP4>);
+    auto pick = [&](auto few, auto several) { return many ? go(several) : go(few); };
+    const cudaError_t e =
+        kv_dtype == FKV_KV_FP8_E4M3
+            ? pick(kv_gather_kernel<FKV_KV_FP8_E4M3, 1>, kv_gather_kernel<FKV_KV_FP8_E4M3, kGatherMany>)
+        : kv_dtype == FKV_KV_BF16 ? pick(kv_gather_kernel<FKV_KV_BF16, 1>, kv_gather_kernel<FKV_KV_BF16, kGatherMany>)
+                                  : pick(kv_gather_kernel<FKV_KV_FP4, 1>, kv_gather_kernel<FKV_KV_FP4, kGatherMany>);
     return e == cudaSuccess ? FKV_OK : FKV_ERR_CUDA;
 }

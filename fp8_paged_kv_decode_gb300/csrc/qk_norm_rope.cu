@@ -79,7 +79,7 @@ __device__ __forceinline__ void pairs_of(const uint2 u, const uint2 v, float (&a
 }
 
 template <bool kNeighbours>
-__global__ void __launch_bounds__(kRopeBlock)
+__global__ void __launch_bounds__(kRopeBlock, 8)
 qk_norm_rope_kernel(const RopeParams p) {
     // (several parts only for few tokens: the warps fit 32 bits)
     const uint32_t wid = blockIdx.x * (kRopeBlock / 32) + threadIdx.x / 32;
@@ -164,6 +164,11 @@ qk_norm_rope_kernel(const RopeParams p) {
                 const int row = row0 + 2 * i + hw;
                 float a[4], b[4];
                 pairs_of<kNeighbours>(u[i], v[i], a, b);
+                if (row + kRopeBatch < end) {                  // the next batch's row, in flight from here on
+                    const uint2 *s = reinterpret_cast<const uint2 *>(src + static_cast<int64_t>(row + kRopeBatch) * 128);
+                    u[i] = s[g0];
+                    v[i] = s[g1];
+                }
                 float rs = 1.f;
                 if (weight) {
                     float ss = 0.f;
@@ -184,17 +189,16 @@ qk_norm_rope_kernel(const RopeParams p) {
                 if (row < end) {
                     uint2 *d = reinterpret_cast<uint2 *>(dst + static_cast<int64_t>(row) * 128);
                     if (kNeighbours) {
-                        d[g0] = make_uint2(pack_bf16x2(x[0], y[0]), pack_bf16x2(x[1], y[1]));
-                        d[g1] = make_uint2(pack_bf16x2(x[2], y[2]), pack_bf16x2(x[3], y[3]));
+                        __stcs(d + g0, make_uint2(pack_bf16x2(x[0], y[0]), pack_bf16x2(x[1], y[1])));
+                        __stcs(d + g1, make_uint2(pack_bf16x2(x[2], y[2]), pack_bf16x2(x[3], y[3])));
                     } else {
-                        d[g0] = make_uint2(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]));
-                        d[g1] = make_uint2(pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]));
+                        __stcs(d + g0, make_uint2(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3])));
+                        __stcs(d + g1, make_uint2(pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3])));
                     }
                 }
             }
             row0 += kRopeBatch;
             if (row0 >= end) return;
-            load(row0, end, src);
         }
     };
     if (first < q_end) {

@@ -132,9 +132,9 @@ FKV_API fkv_status kv_append_bf16(const void *k_new, const void *v_new,
  * For each block of 16 dims of a row, with g = scale[h]:
  *     s    = e4m3_rne_satfinite( fl32( max|x| / fl32(6 g) ) )
  *     D    = fl32( s * g )
- *     code = e2m1_rne_satfinite( fl32( x / D ) ),  sign kept on zeros;
+ *     code = e2m1_rne_satfinite( fl32( x / D ) );
  *            0 for the whole block when D is 0 or NaN
- * (IEEE divisions, ties to the even code).  Scales of kv_calibrate_scales fit:
+ * (IEEE divisions, ties to the even code; a zero code may carry either sign).  Scales of kv_calibrate_scales fit:
  * a block's s is then at most 74.7, so values up to six times the calibrated
  * maximum are still held without saturation.  An infinity saturates (its
  * block takes s = 448); a NaN makes its block's scale, and so its 16 values,
