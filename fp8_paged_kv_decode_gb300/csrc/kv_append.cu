@@ -283,12 +283,21 @@ kv_append_bf16_tag_check_kernel(const uint4 *__restrict__ k_new, const uint4 *__
 // maximum, scale and codes need no other thread.  Per (token, KV head): 512
 // bytes in, 144 out.
 //
-// A block serves 32 tokens of one head's K or V, not both (as the FP8 append
-// does): pointers and scale are then the same for the block, and the encoding
-// (about 125 instructions for 16 elements) leaves little room for selecting
-// them per thread and for 64-bit addressing.
+// Bound by memory in a prompt's write, but only just: the encoding takes some
+// 135 instructions for 16 elements.  So a block serves one head's K or V, not
+// both (as the FP8 append does): pointers and scale are then the same for the
+// block; addresses take 32-bit arithmetic where the pool allows it; and a
+// thread takes two tokens, for one reciprocal of the head's scale and 64 bytes
+// of loads in flight.  262144 tokens of 8 heads into running slots: 281 us laid
+// out as the FP8 append is, 245 with a block per K or V, 219 with two tokens a
+// thread (6.3 TB/s); four tokens 220, two at 4 or 5 resident blocks 255 and
+// 231.  Slots in random order cost the partly written sectors at both ends of
+// every 72-byte row: 296 us.
 // ---------------------------------------------------------------------------
-constexpr int kFp4Tokens = kBlock / kThreadsPerRow;            // 32
+constexpr int kFp4Rows = kBlock / kThreadsPerRow;              // rows of a block at a time: 32
+constexpr int kFp4Many = 2;                                    // tokens per thread of a large call
+// Resident blocks per SM: 40 registers with two tokens a thread, else 32.
+constexpr int fp4_min_blocks(int unroll) { return unroll == 1 ? 8 : 6; }
 
 struct Fp4Append {
     const uint4 *k_new, *v_new;
@@ -321,19 +330,22 @@ __device__ __forceinline__ float2 div2(uint32_t word, uint64_t nb, uint64_t yy) 
 // The 16 codes (8 bytes) and the scale byte of one block of bf16 elements, for
 // the KV head's scale g.  The quotients are IEEE divisions, by div2 where its
 // range holds (see div2_abs).
-__device__ __forceinline__ uint2 encode_fp4_16(const uint4 r0, const uint4 r1, float g, uint32_t &scale) {
+struct Fp4Scale {
+    float g, g6, y6;       // the head's scale, fl32(6 g) and its reciprocal
+};
+__device__ __forceinline__ uint2 encode_fp4_16(const uint4 r0, const uint4 r1, const Fp4Scale &hs, uint32_t &scale) {
+    const float g = hs.g, g6 = hs.g6;
     const uint32_t w[8] = {r0.x, r0.y, r0.z, r0.w, r1.x, r1.y, r1.z, r1.w};
     uint32_t m = 0;                                            // largest |x| bit patterns, per half
 #pragma unroll
     for (int j = 0; j < 8; ++j) m = max_u16x2(m, w[j] & 0x7FFF7FFFu);
     const uint32_t big = max(m >> 16, m & 0xFFFFu);            // a NaN's pattern is above every other
     const float amax = __uint_as_float(big << 16);
-    const float g6 = __fmul_rn(6.f, g);
     const bool fast = recip_scale_ok(g6) && big <= 0x5F80u;    // |x| <= 2^64
     float ratio;
     if (fast) {
-        const float y = __frcp_rn(g6), q0 = __fmul_rn(amax, y);
-        ratio = __fmaf_rn(__fmaf_rn(q0, -g6, amax), y, q0);
+        const float q0 = __fmul_rn(amax, hs.y6);
+        ratio = __fmaf_rn(__fmaf_rn(q0, -g6, amax), hs.y6, q0);
     } else {
         ratio = __fdiv_rn(amax, g6);
     }
@@ -364,53 +376,73 @@ __device__ __forceinline__ uint2 encode_fp4_16(const uint4 r0, const uint4 r1, f
 
 // One thread's share of the 4-bit append: token group bx, `by` the head's K
 // (by < num_kv_heads) or V rows.
+template <int kU>
 __device__ __forceinline__ void append_fp4_part(const Fp4Append &p, unsigned bx, unsigned by) {
-    const uint32_t n = bx * kFp4Tokens + threadIdx.x / kThreadsPerRow;
-    if (n >= p.n_tokens) return;
+    const uint32_t n0 = bx * (kFp4Rows * kU) + threadIdx.x / kThreadsPerRow;
     const bool is_v = by >= p.num_kv_heads;
     const uint32_t h = is_v ? by - p.num_kv_heads : by;
     const uint32_t chunk = threadIdx.x % kThreadsPerRow;
-    const uint4 *src = (is_v ? p.v_new : p.k_new) + static_cast<uint64_t>(n) * (p.num_kv_heads * (kHeadDim / 8)) +
+    const uint32_t row_words = p.num_kv_heads * (kHeadDim / 8);
+    const uint4 *src = (is_v ? p.v_new : p.k_new) + static_cast<uint64_t>(n0) * row_words +
                        (h * (kHeadDim / 8) + chunk * 2);
-    const uint4 r0 = __ldcs(src), r1 = __ldcs(src + 1);        // in flight with the scale's and the slot's loads
-    const float g = __ldg((is_v ? p.v_scale : p.k_scale) + h);
-    const int64_t slot = __ldg(p.slots + n);
-    if (static_cast<uint64_t>(slot) >= p.total_slots) {        // padding, or outside the pool: skip, record
-        if (slot >= 0 && chunk == 0) atomicOr(p.err, FKV_DEVERR_APPEND_SLOT);
-        return;
+    // every row, the scale and the slots are in flight together
+    uint4 r0[kU], r1[kU];
+    int64_t slot[kU];
+#pragma unroll
+    for (int u = 0; u < kU; ++u) {
+        slot[u] = -1;
+        if (n0 + u * kFp4Rows < p.n_tokens) {
+            const uint4 *s = src + static_cast<uint64_t>(u * kFp4Rows) * row_words;
+            r0[u] = __ldcs(s);
+            r1[u] = __ldcs(s + 1);
+            slot[u] = __ldg(p.slots + n0 + u * kFp4Rows);
+        }
     }
-    uint8_t *dst = is_v ? p.v_cache : p.k_cache;
-    if (p.small && p.page_shift >= 0) {
-        const uint32_t s = static_cast<uint32_t>(slot), page = s >> p.page_shift;
-        dst += static_cast<uint64_t>(page) * static_cast<uint32_t>(p.page_bytes) +
-               (h * p.page_size + (s - (page << p.page_shift))) * kFp4Row;
-    } else {
-        const uint64_t page = static_cast<uint64_t>(slot) / p.page_size;
-        dst += page * p.page_bytes +
-               (static_cast<uint64_t>(h) * p.page_size + (static_cast<uint64_t>(slot) - page * p.page_size)) * kFp4Row;
+    Fp4Scale hs;
+    hs.g = __ldg((is_v ? p.v_scale : p.k_scale) + h);
+    hs.g6 = __fmul_rn(6.f, hs.g);
+    hs.y6 = __frcp_rn(hs.g6);
+    uint8_t *pool = is_v ? p.v_cache : p.k_cache;
+#pragma unroll
+    for (int u = 0; u < kU; ++u) {
+        if (static_cast<uint64_t>(slot[u]) >= p.total_slots) { // padding, or outside the pool: skip, record
+            if (slot[u] >= 0 && chunk == 0) atomicOr(p.err, FKV_DEVERR_APPEND_SLOT);
+            continue;
+        }
+        uint8_t *dst = pool;
+        if (p.small && p.page_shift >= 0) {
+            const uint32_t s = static_cast<uint32_t>(slot[u]), page = s >> p.page_shift;
+            dst += static_cast<uint64_t>(page) * static_cast<uint32_t>(p.page_bytes) +
+                   (h * p.page_size + (s - (page << p.page_shift))) * kFp4Row;
+        } else {
+            const uint64_t s = static_cast<uint64_t>(slot[u]), page = s / p.page_size;
+            dst += page * p.page_bytes + (static_cast<uint64_t>(h) * p.page_size + (s - page * p.page_size)) * kFp4Row;
+        }
+        uint32_t s;
+        const uint2 codes = encode_fp4_16(r0[u], r1[u], hs, s);
+        __stcs(reinterpret_cast<uint2 *>(dst) + chunk, codes);
+        // the row's 8 scale bytes: four lanes' bytes make a word (the 8 threads of
+        // a row take the same branches, so their mask is whole)
+        const unsigned mask = 0xFFu << (threadIdx.x & 24u);
+        uint32_t word = s << (8 * (chunk & 3));
+        word |= __shfl_xor_sync(mask, word, 1);
+        word |= __shfl_xor_sync(mask, word, 2);
+        if ((chunk & 3) == 0) __stcs(reinterpret_cast<uint32_t *>(dst + kFp4Codes + chunk), word);
     }
-    uint32_t s;
-    const uint2 codes = encode_fp4_16(r0, r1, g, s);
-    __stcs(reinterpret_cast<uint2 *>(dst) + chunk, codes);
-    // the row's 8 scale bytes: four lanes' bytes make a word (the 8 threads of a
-    // row take the same branches, so their mask is whole)
-    const unsigned mask = 0xFFu << (threadIdx.x & 24u);
-    uint32_t word = s << (8 * (chunk & 3));
-    word |= __shfl_xor_sync(mask, word, 1);
-    word |= __shfl_xor_sync(mask, word, 2);
-    if ((chunk & 3) == 0) __stcs(reinterpret_cast<uint32_t *>(dst + kFp4Codes + chunk), word);
 }
 
-__global__ void __launch_bounds__(kBlock, FKV_APPEND_MIN_BLOCKS)
+template <int kU>
+__global__ void __launch_bounds__(kBlock, fp4_min_blocks(kU))
 kv_append_fp4_kernel(const Fp4Append p) {
     grid_dep_wait();        // earlier readers of the pool (attention) have finished
     grid_dep_launch();
-    append_fp4_part(p, blockIdx.x, blockIdx.y);
+    append_fp4_part<kU>(p, blockIdx.x, blockIdx.y);
 }
 
 // The 4-bit cache's step prologue in one launch, laid out like
-// kv_append_fp8_tag_check_kernel: check blocks first, then the append's.
-__global__ void __launch_bounds__(kBlock, FKV_APPEND_MIN_BLOCKS)
+// kv_append_fp8_tag_check_kernel: check blocks first, then the append's.  (A
+// decode step's call: one token per thread.)
+__global__ void __launch_bounds__(kBlock, fp4_min_blocks(1))
 kv_append_fp4_tag_check_kernel(const Fp4Append p, unsigned append_blocks_x, int32_t num_pages,
                                const uint32_t *__restrict__ page_tags, const int32_t *__restrict__ page_indptr,
                                const int32_t *__restrict__ page_indices, const uint32_t *__restrict__ expected_tags,
@@ -425,7 +457,7 @@ kv_append_fp4_tag_check_kernel(const Fp4Append p, unsigned append_blocks_x, int3
         return;
     }
     const unsigned a = b - static_cast<unsigned>(batch);
-    append_fp4_part(p, a % append_blocks_x, a / append_blocks_x);
+    append_fp4_part<1>(p, a % append_blocks_x, a / append_blocks_x);
 }
 
 static fkv_status check_append_args(const void *k_new, const void *v_new, const int64_t *slot_mapping,
@@ -590,8 +622,9 @@ static Fp4Append fp4_append(const void *k_new, const void *v_new, const int64_t 
     return p;
 }
 
-static unsigned fp4_blocks_x(int32_t n_tokens) {
-    return static_cast<unsigned>((static_cast<int64_t>(n_tokens) + kFp4Tokens - 1) / kFp4Tokens);
+static unsigned fp4_blocks_x(int32_t n_tokens, int unroll) {
+    const int64_t per = static_cast<int64_t>(kFp4Rows) * unroll;
+    return static_cast<unsigned>((n_tokens + per - 1) / per);
 }
 
 extern "C" fkv_status kv_append_fp4(const void *k_new, const void *v_new, const int64_t *slot_mapping,
@@ -609,9 +642,17 @@ extern "C" fkv_status kv_append_fp4(const void *k_new, const void *v_new, const 
     if (!err) return FKV_ERR_CUDA;
     const Fp4Append p = fp4_append(k_new, v_new, slot_mapping, n_tokens, k_scale, v_scale, k_cache, v_cache, num_pages,
                                    num_kv_heads, page_size, err);
-    const cudaError_t e = launch_pdl(kv_append_fp4_kernel,
-                                     dim3(fp4_blocks_x(n_tokens), 2u * static_cast<unsigned>(num_kv_heads)),
-                                     dim3(kBlock), 0, static_cast<cudaStream_t>(stream), p);
+    // Two tokens per thread once their blocks fill the GPU (262144 tokens of 8
+    // heads: 245 us with one, 219 with two; a step's 256 tokens: 1.7 and 2.2 us).
+    const int sms = device_sm_count();
+    if (sms <= 0) return FKV_ERR_CUDA;
+    const unsigned gy = 2u * static_cast<unsigned>(num_kv_heads);
+    const bool many = static_cast<int64_t>(fp4_blocks_x(n_tokens, kFp4Many)) * gy >= 6 * static_cast<int64_t>(sms);
+    auto go = [&](auto kern, int unroll) {
+        return launch_pdl(kern, dim3(fp4_blocks_x(n_tokens, unroll), gy), dim3(kBlock), 0,
+                          static_cast<cudaStream_t>(stream), p);
+    };
+    const cudaError_t e = many ? go(kv_append_fp4_kernel<kFp4Many>, kFp4Many) : go(kv_append_fp4_kernel<1>, 1);
     return e == cudaSuccess ? FKV_OK : FKV_ERR_CUDA;
 }
 
@@ -629,7 +670,7 @@ extern "C" fkv_status kv_append_fp4_tag_check(const void *k_new, const void *v_n
     if (st != FKV_OK) return st;
     if (2 * static_cast<int64_t>(num_kv_heads) > 65535) return FKV_ERR_UNSUPPORTED;       // as kv_append_fp4
     if (n_tokens > 0 && (!k_scale || !v_scale)) return FKV_ERR_INVALID_ARG;
-    const unsigned fx = fp4_blocks_x(n_tokens);
+    const unsigned fx = fp4_blocks_x(n_tokens, 1);
     blocks = static_cast<int64_t>(fx) * 2 * num_kv_heads + batch;
     if (blocks > 0x7FFFFFFF) return FKV_ERR_UNSUPPORTED;
     if (blocks == 0) return FKV_OK;

@@ -6,26 +6,21 @@
 // copied).  e4m3 codes and e2m1 code * block scale are exact in f16, so the
 // product with the head's scale is the only fp32 rounding before bf16's.
 //
-// Layout as in the append: grid of (token groups, KV heads), 16 threads per
-// (token, head), 8 on its K row and 8 on its V row, 16 elements each, so a
-// 4-bit thread reads one scale block.  Bound by memory: per (token, KV head)
-// 512 bytes out and 144 (FP4), 256 (FP8) or 512 (BF16) in.  A 4-bit thread's
-// row takes 9 bytes of loads, far too few in flight to cover their latency, so
-// a thread takes kU tokens and has all their slots, then all their rows, in
-// flight together.
+// Grid of (token groups, KV heads of K then of V): a block reads one head of one
+// pool, 8 threads to a row, 16 elements each, so a 4-bit thread reads one scale
+// block.  Bound by memory: per (token, KV head) 512 bytes out and 144 (FP4),
+// 256 (FP8) or 512 (BF16) in.  A 4-bit thread's row takes 9 bytes of loads, far
+// too few in flight to cover their latency, so a thread takes kU tokens and has
+// all their slots, then all their rows, in flight together.  262144 tokens of 8
+// heads: FP4 277 us with one token a thread, 233 with four (5.9 TB/s; three
+// 231, six 246, eight 259), FP8 288 and 253 (6.4 TB/s).
 #include "fp4_row.cuh"
 
 namespace fkv {
 
 constexpr int kGatherBlock = 256;
-constexpr int kGatherTokens = kGatherBlock / 16;
-#ifndef GATHER_U
-#define GATHER_U 4
-#endif
-#ifndef GATHER_ST
-#define GATHER_ST __stcs
-#endif
-constexpr int kGatherMany = GATHER_U;
+constexpr int kGatherTokens = kGatherBlock / 8;      // rows of a block at a time
+constexpr int kGatherMany = 4;                       // tokens per thread of a large call
 
 // Two f16 values times the head's scale, rounded to bf16.
 __device__ __forceinline__ uint32_t scaled_bf16x2(uint32_t f16x2, float g) {
@@ -92,48 +87,59 @@ __device__ __forceinline__ void gather_store(uint4 *dst, const GatherRaw &r, flo
                             scaled_bf16x2(f[7], g));
         }
     }
-    GATHER_ST(dst, r0);
-    GATHER_ST(dst + 1, r1);
+    __stcs(dst, r0);
+    __stcs(dst + 1, r1);
 }
+
+struct GatherParams {
+    const uint8_t *k_cache, *v_cache;
+    const float *k_scale, *v_scale;
+    const int64_t *slots;
+    uint4 *k_out, *v_out;
+    uint32_t *err;
+    uint64_t total_slots;       // pages x page_size
+    uint32_t n_tokens, num_kv_heads, page_size;
+    int32_t page_shift;         // log2 of the page size, -1 if it is not a power of two
+};
 
 template <int kKv, int kU>
 __global__ void __launch_bounds__(kGatherBlock)
-kv_gather_kernel(const uint8_t *__restrict__ k_cache, const uint8_t *__restrict__ v_cache,
-                 const float *__restrict__ k_scale, const float *__restrict__ v_scale,
-                 const int64_t *__restrict__ slots, int32_t n_tokens, uint4 *__restrict__ k_out,
-                 uint4 *__restrict__ v_out, int32_t num_pages, int32_t num_kv_heads, int32_t page_size,
-                 int32_t page_shift, uint32_t *err) {
+kv_gather_kernel(const GatherParams p) {
     grid_dep_wait();
     grid_dep_launch();
-    const int64_t n0 = static_cast<int64_t>(blockIdx.x) * (kGatherTokens * kU) + threadIdx.x / 16;
-    const int h = blockIdx.y;
-    const bool is_v = (threadIdx.x & 8) != 0;
-    const int chunk = threadIdx.x & 7;
-    const uint8_t *cache = is_v ? v_cache : k_cache;
+    const uint32_t n0 = blockIdx.x * (kGatherTokens * kU) + threadIdx.x / 8;
+    const bool is_v = blockIdx.y >= p.num_kv_heads;
+    const uint32_t h = is_v ? blockIdx.y - p.num_kv_heads : blockIdx.y;
+    const uint32_t chunk = threadIdx.x & 7;
+    const uint8_t *cache = is_v ? p.v_cache : p.k_cache;
     int64_t slot[kU];
 #pragma unroll
-    for (int u = 0; u < kU; ++u) slot[u] = n0 + u * kGatherTokens < n_tokens ? __ldg(slots + n0 + u * kGatherTokens) : -1;
-    const float g = kKv == FKV_KV_BF16 ? 1.f : __ldg((is_v ? v_scale : k_scale) + h);
+    for (int u = 0; u < kU; ++u) {
+        const uint32_t n = n0 + u * kGatherTokens;
+        slot[u] = n < p.n_tokens ? __ldg(p.slots + n) : -1;
+    }
+    const float g = kKv == FKV_KV_BF16 ? 1.f : __ldg((is_v ? p.v_scale : p.k_scale) + h);
     GatherRaw raw[kU];
-    bool live[kU];
 #pragma unroll
     for (int u = 0; u < kU; ++u) {
         raw[u] = GatherRaw{};
-        const int64_t page = page_shift >= 0 ? (slot[u] >> page_shift) : slot[u] / page_size;
-        live[u] = slot[u] >= 0 && page < num_pages;
-        if (live[u]) {
-            const uint32_t off = static_cast<uint32_t>(slot[u] - page * page_size);
+        const uint64_t s = static_cast<uint64_t>(slot[u]);
+        if (s < p.total_slots) {
+            const uint64_t page = p.page_shift >= 0 ? s >> p.page_shift : s / p.page_size;
+            const uint32_t off = static_cast<uint32_t>(s - page * p.page_size);
             raw[u] = gather_load<kKv>(
-                cache, (static_cast<uint64_t>(static_cast<uint32_t>(page)) * num_kv_heads + h) * page_size + off, chunk);
-        } else if (slot[u] >= 0 && (threadIdx.x & 15) == 0) {
-            atomicOr(err, FKV_DEVERR_GATHER_SLOT);
+                cache, (static_cast<uint64_t>(static_cast<uint32_t>(page)) * p.num_kv_heads + h) * p.page_size + off, chunk);
+        } else if (slot[u] >= 0 && chunk == 0) {
+            atomicOr(p.err, FKV_DEVERR_GATHER_SLOT);
         }
     }
-    uint4 *out = (is_v ? v_out : k_out) + (static_cast<uint64_t>(n0) * num_kv_heads + h) * 16 + chunk * 2;
+    const uint32_t row_words = p.num_kv_heads * 16;
+    uint4 *out = (is_v ? p.v_out : p.k_out) + static_cast<uint64_t>(n0) * row_words + (h * 16 + chunk * 2);
 #pragma unroll
     for (int u = 0; u < kU; ++u)
-        if (n0 + u * kGatherTokens < n_tokens)
-            gather_store<kKv>(out + static_cast<uint64_t>(u) * kGatherTokens * num_kv_heads * 16, raw[u], g, live[u]);
+        if (n0 + u * kGatherTokens < p.n_tokens)
+            gather_store<kKv>(out + static_cast<uint64_t>(u * kGatherTokens) * row_words, raw[u], g,
+                              static_cast<uint64_t>(slot[u]) < p.total_slots);
 }
 
 }  // namespace fkv
@@ -146,7 +152,7 @@ extern "C" fkv_status kv_gather(const void *k_cache, const void *v_cache, int32_
                                 int32_t head_dim, void *stream) {
     if (n_tokens < 0 || num_pages <= 0 || num_kv_heads <= 0 || page_size <= 0) return FKV_ERR_INVALID_ARG;
     if (kv_dtype != FKV_KV_FP8_E4M3 && kv_dtype != FKV_KV_BF16 && kv_dtype != FKV_KV_FP4) return FKV_ERR_INVALID_ARG;
-    if (head_dim != 128 || num_kv_heads > 65535) return FKV_ERR_UNSUPPORTED;
+    if (head_dim != 128 || num_kv_heads > 32767) return FKV_ERR_UNSUPPORTED;          // grid y: K and V heads
     if (n_tokens == 0) return FKV_OK;
     if (!k_cache || !v_cache || !slots || !k_out || !v_out) return FKV_ERR_INVALID_ARG;
     if (kv_dtype != FKV_KV_BF16 && (!k_scale || !v_scale)) return FKV_ERR_INVALID_ARG;
@@ -154,20 +160,30 @@ extern "C" fkv_status kv_gather(const void *k_cache, const void *v_cache, int32_
         return FKV_ERR_INVALID_ARG;
     uint32_t *err = device_error_word();
     if (!err) return FKV_ERR_CUDA;
-    int32_t shift = -1;
-    if ((page_size & (page_size - 1)) == 0) shift = __builtin_ctz(static_cast<unsigned>(page_size));
-    // Several tokens per thread once the grid fills the GPU without that.
     const int sms = device_sm_count();
-    const int64_t rows = static_cast<int64_t>(n_tokens) * num_kv_heads;
+    if (sms <= 0) return FKV_ERR_CUDA;
+    GatherParams p;
+    p.k_cache = static_cast<const uint8_t *>(k_cache);
+    p.v_cache = static_cast<const uint8_t *>(v_cache);
+    p.k_scale = k_scale;
+    p.v_scale = v_scale;
+    p.slots = slots;
+    p.k_out = static_cast<uint4 *>(k_out);
+    p.v_out = static_cast<uint4 *>(v_out);
+    p.err = err;
+    p.total_slots = static_cast<uint64_t>(num_pages) * static_cast<uint32_t>(page_size);
+    p.n_tokens = static_cast<uint32_t>(n_tokens);
+    p.num_kv_heads = static_cast<uint32_t>(num_kv_heads);
+    p.page_size = static_cast<uint32_t>(page_size);
+    p.page_shift = (page_size & (page_size - 1)) == 0 ? __builtin_ctz(p.page_size) : -1;
+    // Several tokens per thread once the grid fills the GPU without that.
+    const int64_t rows = 2 * static_cast<int64_t>(n_tokens) * num_kv_heads;
     const bool many = rows >= static_cast<int64_t>(sms) * 8 * kGatherTokens * kGatherMany;
     const int per = kGatherTokens * (many ? kGatherMany : 1);
     const dim3 grid(static_cast<unsigned>((static_cast<int64_t>(n_tokens) + per - 1) / per),
-                    static_cast<unsigned>(num_kv_heads));
+                    2u * static_cast<unsigned>(num_kv_heads));
     auto go = [&](auto kern) {
-        return launch_pdl(kern, grid, dim3(kGatherBlock), 0, static_cast<cudaStream_t>(stream),
-                          static_cast<const uint8_t *>(k_cache), static_cast<const uint8_t *>(v_cache), k_scale,
-                          v_scale, slots, n_tokens, static_cast<uint4 *>(k_out), static_cast<uint4 *>(v_out),
-                          num_pages, num_kv_heads, page_size, shift, err);
+        return launch_pdl(kern, grid, dim3(kGatherBlock), 0, static_cast<cudaStream_t>(stream), p);
     };
     auto pick = [&](auto few, auto several) { return many ? go(several) : go(few); };
     const cudaError_t e =
