@@ -4,20 +4,22 @@
 // Integer work: prefix sums over the requests (CSR rows, tokens, pages to take)
 // and then one independent entry per page-table cell and per token.  Two
 // launches: a single block scans the requests and leaves one record per request
-// in the workspace, then a grid fills the entries.  The fill reads only the
+// in the workspace, then a grid fills the entries, four neighbours to a thread
+// (one search for their request, 16-byte stores).  The fill reads only the
 // records, so the length and free-count outputs may be the inputs' own arrays.
-// Bytes: 16 per page-table entry (id and tag, in and out) and 12 per token; at
-// decode sizes both launches are bound by latency.
+// Bytes: 16 per page-table entry (id and tag, in and out) and 12 per token; both
+// launches are bound by latency: the scan's two block-wide steps, and the
+// fill's chain of search, record, page id, tag.
 #include "fkv_common.cuh"
 
 namespace fkv {
 
-constexpr int kTabThreads = 1024;
+constexpr int kTabThreads = 1024;               // most threads of the scan's block
 constexpr int kFillThreads = 256;
 constexpr int kListed = 1, kGranted = 2;        // record flags
 
-struct StepRecord {
-    int32_t cached, fresh;    // tokens held and new (0 when refused as invalid)
+struct alignas(16) StepRecord {
+    int32_t cached, have;     // tokens and pages held (0 for lengths that are not valid)
     int32_t top;              // free-list index of the request's first new page
     int32_t flags;
 };
@@ -37,93 +39,110 @@ struct StepParams {
     int32_t *positions, *free_left;
     StepRecord *rec;
     uint32_t *err;
-    int32_t batch, max_blocks, num_free, num_pages, page, nnz, n_tokens;
+    int32_t batch, max_blocks, num_free, num_pages, nnz, n_tokens;
+    uint32_t page;
+    int32_t page_shift;       // log2 of the page size, -1 if it is not a power of two
+    bool wide;                // the entry and token arrays are 16-byte aligned
 };
 
-__device__ __forceinline__ int32_t pages_of(int64_t tokens, int32_t page) {
-    return static_cast<int32_t>((tokens + page - 1) / page);
+// Pages that hold so many tokens (below 2^31).
+__device__ __forceinline__ int32_t pages_of(const StepParams &p, uint32_t tokens) {
+    const uint32_t up = tokens + (p.page - 1);                 // below 2^32
+    return static_cast<int32_t>(p.page_shift >= 0 ? up >> p.page_shift : up / p.page);
 }
 
-// Inclusive prefix sum over the block's threads, plus the block's total.
-__device__ __forceinline__ int64_t block_scan(int64_t v, int64_t &total, int64_t *s_warp) {
-    const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
+// Inclusive prefix sums of v[0 .. K - 1] over the block's threads and their
+// totals, with one barrier: every warp scans the warps' totals for itself.
+template <int K>
+__device__ __forceinline__ void block_scan(int64_t (&v)[K], int64_t (&total)[K], int64_t (*s_warp)[32]) {
+    const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5, warps = blockDim.x >> 5;
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const int64_t y = __shfl_up_sync(0xffffffffu, v, o);
-        if (lane >= o) v += y;
-    }
-    if (lane == 31) s_warp[wid] = v;
+    for (int o = 1; o < 32; o <<= 1)
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            const int64_t y = __shfl_up_sync(0xffffffffu, v[k], o);
+            if (lane >= o) v[k] += y;
+        }
+    if (lane == 31)
+#pragma unroll
+        for (int k = 0; k < K; ++k) s_warp[k][wid] = v[k];
     __syncthreads();
-    int64_t before = 0;
-    total = 0;
-    for (int i = 0; i < kTabThreads / 32; ++i) {
-        const int64_t x = s_warp[i];
-        if (i < wid) before += x;
-        total += x;
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+        const int64_t own = lane < warps ? s_warp[k][lane] : 0;
+        int64_t x = own;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
+            if (lane >= o) x += y;
+        }
+        v[k] += __shfl_sync(0xffffffffu, x - own, wid);
+        total[k] = __shfl_sync(0xffffffffu, x, 31);
     }
-    __syncthreads();                           // s_warp is free again
-    return before + v;
 }
 
 __global__ void __launch_bounds__(kTabThreads)
 step_plan_kernel(const StepParams p) {
+    __shared__ int64_t s_one[2][32], s_two[1][32];
+    __shared__ int s_used, s_refused;
+    if (threadIdx.x == 0) s_used = s_refused = 0;
     grid_dep_wait();
     grid_dep_launch();
-    __shared__ int64_t s_warp[kTabThreads / 32];
-    const int64_t free = min(max(*p.free_count, 0), p.num_free);
+    const int32_t free = min(max(*p.free_count, 0), p.num_free);
     int64_t rows = 0, toks = 0, taken = 0;     // sums over the requests before this chunk
-    bool any_refused = false;
-    for (int base = 0; base < p.batch; base += kTabThreads) {
+    int used = 0, refused = 0;
+    for (int base = 0; base < p.batch; base += blockDim.x) {
         const int r = base + threadIdx.x;
         const bool in = r < p.batch;
         const int32_t c = in ? p.cached[r] : 0, n = in ? p.fresh[r] : 0;
-        const int64_t len = static_cast<int64_t>(c) + n;
-        const bool valid = c >= 0 && n >= 0 && len <= 0x7FFFFFFF && pages_of(len, p.page) <= p.max_blocks;
-        const int32_t pages = valid ? pages_of(len, p.page) : 0;
-        const int32_t count = max(n, 0);
-        int64_t sum;
-        const int64_t row_end = rows + block_scan(pages, sum, s_warp);
-        rows += sum;
-        const int64_t tok_end = toks + block_scan(count, sum, s_warp);
-        toks += sum;
+        const bool lens = c >= 0 && n >= 0 && static_cast<uint32_t>(c) + static_cast<uint32_t>(n) <= 0x7FFFFFFFu;
+        const int32_t len = lens ? c + n : 0;
+        int32_t pages = pages_of(p, len);
+        const bool valid = lens && pages <= p.max_blocks;
+        if (!valid) pages = 0;
+        int64_t one[2] = {pages, max(n, 0)}, sum[2];
+        block_scan<2>(one, sum, s_one);
+        const int64_t row_end = rows + one[0], tok_end = toks + one[1];
+        rows += sum[0];
+        toks += sum[1];
         const bool fits = valid && row_end <= p.nnz && tok_end <= p.n_tokens;
-        const int32_t need = fits ? pages - pages_of(c, p.page) : 0;
-        const int64_t need_end = taken + block_scan(need, sum, s_warp);
-        taken += sum;
+        const int32_t need = fits ? pages - pages_of(p, c) : 0;
+        int64_t two[1] = {need}, sum2[1];
+        block_scan<1>(two, sum2, s_two);
+        const int64_t need_end = taken + two[0];
+        taken += sum2[0];
         const bool granted = fits && (need == 0 || need_end <= free);
         if (in) {
             p.page_indptr[r + 1] = static_cast<int32_t>(min(row_end, static_cast<int64_t>(p.nnz)));
             p.token_indptr[r + 1] = static_cast<int32_t>(min(tok_end, static_cast<int64_t>(p.n_tokens)));
-            p.step_lens[r] = granted ? static_cast<int32_t>(len) : 0;
-            p.cached_out[r] = granted ? static_cast<int32_t>(len) : c;
+            p.step_lens[r] = granted ? len : 0;
+            p.cached_out[r] = granted ? len : c;
             p.refused[r] = granted ? 0 : 1;
             StepRecord rec;
             rec.cached = valid ? c : 0;
-            rec.fresh = valid ? n : 0;
+            rec.have = valid ? pages_of(p, c) : 0;
             rec.top = granted ? static_cast<int32_t>(free - 1 - (need_end - need)) : -1;
             rec.flags = (valid ? kListed : 0) | (granted ? kGranted : 0);
-            p.rec[r] = rec;
+            *reinterpret_cast<int4 *>(p.rec + r) = *reinterpret_cast<const int4 *>(&rec);
+            // Pages are granted to every request up to the first that found too
+            // few: the last granted one's sum is what was taken.
+            if (granted && need > 0) used = max(used, static_cast<int>(need_end));
+            if (!granted) refused = 1;
         }
-        any_refused |= in && !granted;
     }
-    // pages granted: every request up to the first that found too few
-    const int refused = __syncthreads_or(any_refused);
-    __shared__ unsigned long long s_used;
-    if (threadIdx.x == 0) s_used = 0;
-    __syncthreads();
-    unsigned long long used = 0;
-    for (int r = threadIdx.x; r < p.batch; r += kTabThreads) {
-        const StepRecord rec = p.rec[r];
-        if (rec.flags & kGranted)
-            used += pages_of(static_cast<int64_t>(rec.cached) + rec.fresh, p.page) - pages_of(rec.cached, p.page);
+    used = __reduce_max_sync(0xffffffffu, used);
+    refused = __reduce_or_sync(0xffffffffu, refused);
+    __syncthreads();                           // s_used, s_refused are set (and an empty batch's too)
+    if ((threadIdx.x & 31) == 0) {
+        atomicMax(&s_used, used);              // whole numbers: any order gives the same
+        atomicOr(&s_refused, refused);
     }
-    atomicAdd(&s_used, used);                  // whole numbers: any order gives the same sum
     __syncthreads();
     if (threadIdx.x == 0) {
         p.page_indptr[0] = 0;
         p.token_indptr[0] = 0;
-        *p.free_left = static_cast<int32_t>(free - static_cast<int64_t>(s_used));
-        if (refused) atomicOr(p.err, FKV_DEVERR_TABLES);
+        *p.free_left = free - s_used;
+        if (s_refused) atomicOr(p.err, FKV_DEVERR_TABLES);
     }
 }
 
@@ -138,17 +157,21 @@ __device__ __forceinline__ int find_row(const int32_t *indptr, int batch, int32_
     return a;
 }
 
+__device__ __forceinline__ StepRecord load_record(const StepParams &p, int r) {
+    const int4 v = __ldg(reinterpret_cast<const int4 *>(p.rec + r));
+    return StepRecord{v.x, v.y, v.z, v.w};
+}
+
 // Page `col` of a request: from its table where it held it already, else from
 // the free list.  -1 (and the error bit) for an id outside the pool, -1 for a
 // page it was not granted.
 __device__ __forceinline__ int32_t page_at(const StepParams &p, const StepRecord &rec, int r, int32_t col) {
-    const int32_t have = pages_of(rec.cached, p.page);
     int32_t id;
-    if (col < have) {
+    if (col < rec.have) {
         id = __ldg(p.table + static_cast<int64_t>(r) * p.max_blocks + col);
     } else {
         if (!(rec.flags & kGranted)) return -1;
-        id = __ldg(p.free_pages + (rec.top - (col - have)));
+        id = __ldg(p.free_pages + (rec.top - (col - rec.have)));
     }
     if (id < 0 || id >= p.num_pages) {
         atomicOr(p.err, FKV_DEVERR_TABLES);
@@ -157,44 +180,118 @@ __device__ __forceinline__ int32_t page_at(const StepParams &p, const StepRecord
     return id;
 }
 
+// A thread's run of kRun neighbouring entries i .. of [0, end): the request of
+// the first by search, then onwards.
+constexpr int kRun = 4;
+
 __global__ void __launch_bounds__(kFillThreads)
 step_fill_kernel(const StepParams p) {
     grid_dep_wait();
     grid_dep_launch();
-    const int64_t stride = static_cast<int64_t>(gridDim.x) * kFillThreads;
-    const int64_t start = static_cast<int64_t>(blockIdx.x) * kFillThreads + threadIdx.x;
-    const int32_t rows = p.page_indptr[p.batch], toks = p.token_indptr[p.batch];
-    for (int64_t j = start; j < rows; j += stride) {
-        const int r = find_row(p.page_indptr, p.batch, static_cast<int32_t>(j));
-        const StepRecord rec = p.rec[r];
-        const int32_t col = static_cast<int32_t>(j) - p.page_indptr[r];
-        const int64_t cell = static_cast<int64_t>(r) * p.max_blocks + col;
-        const int32_t id = page_at(p, rec, r, col);
-        uint32_t tag = 0;
-        if (col < pages_of(rec.cached, p.page)) {
-            tag = p.table_tags[cell];
-        } else if (id >= 0) {
-            tag = __ldg(p.page_tags + id);
-            p.table_tags[cell] = tag;
-        }
-        if (col >= pages_of(rec.cached, p.page) && (rec.flags & kGranted)) p.table[cell] = id;
-        p.page_indices[j] = id;
-        p.expected[j] = tag;
-    }
-    for (int64_t i = start; i < p.n_tokens; i += stride) {
-        int64_t slot = -1;
-        int32_t pos = 0;
-        if (i < toks) {
-            const int r = find_row(p.token_indptr, p.batch, static_cast<int32_t>(i));
-            const StepRecord rec = p.rec[r];
-            if (rec.flags & kListed) {
-                pos = rec.cached + (static_cast<int32_t>(i) - p.token_indptr[r]);
-                const int32_t id = rec.flags & kGranted ? page_at(p, rec, r, pos / p.page) : -1;
-                if (id >= 0) slot = static_cast<int64_t>(id) * p.page + pos % p.page;
+    const int32_t rows = __ldg(p.page_indptr + p.batch), toks = __ldg(p.token_indptr + p.batch);
+    const uint32_t row_runs = (static_cast<uint32_t>(rows) + kRun - 1) / kRun;
+    const uint32_t tok_runs = (static_cast<uint32_t>(p.n_tokens) + kRun - 1) / kRun;
+    const uint32_t stride = gridDim.x * kFillThreads;
+    // runs of page-table entries first, then runs of tokens
+    for (uint64_t run = blockIdx.x * kFillThreads + threadIdx.x; run < static_cast<uint64_t>(row_runs) + tok_runs;
+         run += stride) {
+        if (run < row_runs) {
+            const int32_t j0 = static_cast<int32_t>(run) * kRun, m = min(kRun, rows - j0);
+            int r = find_row(p.page_indptr, p.batch, j0);
+            int32_t first = __ldg(p.page_indptr + r), next = __ldg(p.page_indptr + r + 1);
+            StepRecord rec = load_record(p, r);
+            int32_t id[kRun];
+            uint32_t tag[kRun];
+            int64_t cell[kRun];
+            bool fresh[kRun];
+#pragma unroll
+            for (int e = 0; e < kRun; ++e) {
+                const int32_t j = j0 + e;
+                id[e] = -1;
+                tag[e] = 0;
+                fresh[e] = false;
+                if (e >= m) continue;
+                if (j >= next) {
+                    do {                                       // requests without entries are passed over
+                        ++r;
+                        first = next;
+                        next = __ldg(p.page_indptr + r + 1);
+                    } while (j >= next);
+                    rec = load_record(p, r);
+                }
+                const int32_t col = j - first;
+                cell[e] = static_cast<int64_t>(r) * p.max_blocks + col;
+                id[e] = page_at(p, rec, r, col);
+                fresh[e] = col >= rec.have && (rec.flags & kGranted);
+                if (col < rec.have) tag[e] = __ldg(p.table_tags + cell[e]);
+                else if (id[e] >= 0) tag[e] = __ldg(p.page_tags + id[e]);
+            }
+#pragma unroll
+            for (int e = 0; e < kRun; ++e) {
+                if (!fresh[e]) continue;
+                p.table[cell[e]] = id[e];
+                if (id[e] >= 0) p.table_tags[cell[e]] = tag[e];
+            }
+            if (m == kRun && p.wide) {
+                reinterpret_cast<int4 *>(p.page_indices)[run] = make_int4(id[0], id[1], id[2], id[3]);
+                reinterpret_cast<uint4 *>(p.expected)[run] = make_uint4(tag[0], tag[1], tag[2], tag[3]);
+            } else {
+#pragma unroll
+                for (int e = 0; e < kRun; ++e) {
+                    if (e >= m) continue;
+                    p.page_indices[j0 + e] = id[e];
+                    p.expected[j0 + e] = tag[e];
+                }
+            }
+        } else {
+            const uint32_t run_t = static_cast<uint32_t>(run - row_runs);
+            const int32_t i0 = static_cast<int32_t>(run_t) * kRun, m = min(kRun, p.n_tokens - i0);
+            int64_t slot[kRun] = {-1, -1, -1, -1};
+            int32_t pos[kRun] = {0, 0, 0, 0};
+            if (i0 < toks) {
+                int r = find_row(p.token_indptr, p.batch, i0);
+                int32_t first = __ldg(p.token_indptr + r), next = __ldg(p.token_indptr + r + 1);
+                StepRecord rec = load_record(p, r);
+                int32_t col_at = -1, id = -1;                  // the page looked up last
+#pragma unroll
+                for (int e = 0; e < kRun; ++e) {
+                    const int32_t i = i0 + e;
+                    if (i >= toks) continue;
+                    if (i >= next) {
+                        do {
+                            ++r;
+                            first = next;
+                            next = __ldg(p.token_indptr + r + 1);
+                        } while (i >= next);
+                        rec = load_record(p, r);
+                        col_at = -1;
+                    }
+                    if (!(rec.flags & kListed)) continue;
+                    pos[e] = rec.cached + (i - first);
+                    if (!(rec.flags & kGranted)) continue;
+                    const uint32_t at = static_cast<uint32_t>(pos[e]);
+                    const uint32_t col = p.page_shift >= 0 ? at >> p.page_shift : at / p.page;
+                    if (static_cast<int32_t>(col) != col_at) {
+                        col_at = static_cast<int32_t>(col);
+                        id = page_at(p, rec, r, col_at);
+                    }
+                    if (id >= 0) slot[e] = static_cast<int64_t>(id) * p.page + (at - col * p.page);
+                }
+            }
+            if (m == kRun && p.wide) {
+                longlong2 *s = reinterpret_cast<longlong2 *>(p.slots) + 2 * static_cast<uint64_t>(run_t);
+                s[0] = make_longlong2(slot[0], slot[1]);
+                s[1] = make_longlong2(slot[2], slot[3]);
+                reinterpret_cast<int4 *>(p.positions)[run_t] = make_int4(pos[0], pos[1], pos[2], pos[3]);
+            } else {
+#pragma unroll
+                for (int e = 0; e < kRun; ++e) {
+                    if (e >= m) continue;
+                    p.slots[i0 + e] = slot[e];
+                    p.positions[i0 + e] = pos[e];
+                }
             }
         }
-        p.slots[i] = slot;
-        p.positions[i] = pos;
     }
 }
 
@@ -232,14 +329,17 @@ extern "C" fkv_status kv_step_tables(const int32_t *cached_lens, const int32_t *
     uint32_t *err = device_error_word();
     const int sms = device_sm_count();
     if (!err || sms <= 0) return FKV_ERR_CUDA;
+    const uint32_t page = static_cast<uint32_t>(page_size);
+    const bool wide = aligned16(page_indices) && aligned16(expected_tags) && aligned16(slot_mapping) && aligned16(positions);
     const StepParams p{cached_lens, new_lens, block_table, block_tags, free_pages, free_count, page_tags, step_lens,
                        cached_lens_out, refused, page_indptr, page_indices, expected_tags, token_indptr, slot_mapping,
                        positions, free_left, static_cast<StepRecord *>(workspace), err, batch, max_blocks, num_free,
-                       num_pages, page_size, nnz, n_tokens};
+                       num_pages, nnz, n_tokens, page, (page & (page - 1)) ? -1 : __builtin_ctz(page), wide};
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    if (launch_pdl(step_plan_kernel, dim3(1), dim3(kTabThreads), 0, st, p) != cudaSuccess) return FKV_ERR_CUDA;
-    const int64_t most = nnz > n_tokens ? nnz : n_tokens;
-    int64_t blocks = (most + kFillThreads - 1) / kFillThreads;
+    const unsigned scan = batch >= kTabThreads ? kTabThreads : batch <= 32 ? 32u : (static_cast<unsigned>(batch) + 31u) & ~31u;
+    if (launch_pdl(step_plan_kernel, dim3(1), dim3(scan), 0, st, p) != cudaSuccess) return FKV_ERR_CUDA;
+    const int64_t runs = (static_cast<int64_t>(nnz) + kRun - 1) / kRun + (static_cast<int64_t>(n_tokens) + kRun - 1) / kRun;
+    int64_t blocks = (runs + kFillThreads - 1) / kFillThreads;
     if (blocks > 8 * sms) blocks = 8 * sms;
     if (blocks == 0) return FKV_OK;
     return launch_pdl(step_fill_kernel, dim3(static_cast<unsigned>(blocks)), dim3(kFillThreads), 0, st, p) ==
