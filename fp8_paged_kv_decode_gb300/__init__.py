@@ -4,7 +4,10 @@ Thin Python binding over the C ABI in ``include/fkv.h`` (``libfkv.so``, built
 in-tree by ``_build.py``).  Every function here only checks tensor metadata and
 passes raw device pointers, sizes and the current CUDA stream to the library;
 all computation runs in the library's CUDA kernels.  There is no CPU path: if
-the library is missing or no GPU is present the calls raise.
+the library is missing or no GPU is present the calls raise.  The calls that a
+decode step makes with a 4-bit cache, and ``paged_decode_attn``, are marshalled
+by ``_fkv_bind.so`` (host C++, ``csrc/bind.cpp``): in Python their checks took
+4 to 9 us a call, more than some of the kernels.
 
 Entry points (same names as the C ABI):
   kv_append_fp8 / kv_append_bf16   write new tokens into the paged pools
@@ -65,6 +68,7 @@ NOALLOC_SCRATCH_BYTES = 16 << 20
 _HERE = os.path.dirname(os.path.abspath(__file__))
 _lock = threading.Lock()
 _lib = None
+_bind = None      # the compiled marshalling, once loaded
 
 
 class FkvError(RuntimeError):
@@ -140,6 +144,29 @@ def load_library():
         return lib
 
 
+def _load_bind():
+    """Load _fkv_bind.so and give it the library's entry points."""
+    global _bind
+    lib = load_library()
+    with _lock:
+        if _bind is None:
+            import importlib.machinery
+            import importlib.util
+
+            import torch  # noqa: F401  (its libraries, which the module links against)
+            path = os.path.join(_HERE, "_fkv_bind.so")
+            if not os.path.exists(path):
+                raise FkvError("_fkv_bind.so is not built; run fp8_paged_kv_decode_gb300._build.build()")
+            loader = importlib.machinery.ExtensionFileLoader("_fkv_bind", path)
+            mod = importlib.util.module_from_spec(importlib.util.spec_from_loader("_fkv_bind", loader))
+            loader.exec_module(mod)
+            mod.setup(FkvError, *(ctypes.cast(getattr(lib, f), ctypes.c_void_p).value for f in (
+                "fkv_status_string", "kv_append_fp4", "kv_append_fp4_tag_check", "kv_gather", "qk_norm_rope",
+                "kv_step_tables", "paged_decode_attn")))
+            _bind = mod
+        return _bind
+
+
 # ---------------------------------------------------------------------------
 # marshalling helpers
 # ---------------------------------------------------------------------------
@@ -179,21 +206,9 @@ def _is_byte_cache(t):
     return t.dtype in (torch.uint8, getattr(torch, "float8_e4m3fn", torch.uint8))
 
 
-# The checks of the calls below cost host time on every step, as much as their
-# kernels run at decode sizes; so they read each property once, and compare
-# without a call per condition.
 def _is_fp4_cache(t):
     import torch
     return t.dtype is torch.uint8 and t.shape[-1] == FP4_ROW_BYTES and t.dim() == 4
-
-
-def _here(*ts):
-    """Contiguous tensors of the current device (the one the call launches on)."""
-    import torch
-    cur = torch._C._cuda_getDevice() if torch.cuda.is_initialized() else None
-    for t in ts:
-        if t is not None and (t.get_device() != cur or not t.is_contiguous()):
-            raise FkvError("tensors must be contiguous CUDA tensors of the current device")
 
 
 # ---------------------------------------------------------------------------
@@ -313,100 +328,28 @@ def kv_calibrate_scales(k, v, k_scale, v_scale, stream=None):
                                               _stream(stream)), "kv_calibrate_scales")
 
 
-def _check_fp4_append(k_new, v_new, slot_mapping, k_scale, v_scale, k_cache, v_cache):
-    import torch
-    if not (k_new.dtype is torch.bfloat16 and v_new.dtype is torch.bfloat16):
-        raise FkvError("k_new/v_new must be bf16")
-    if slot_mapping.dtype is not torch.int64:
-        raise FkvError("slot_mapping must be int64")
-    shape = k_cache.shape
-    if not (_is_fp4_cache(k_cache) and v_cache.dtype is torch.uint8 and v_cache.shape == shape):
-        raise FkvError("FP4 caches must both be uint8 [P][Hkv][S][72]")
-    P, Hkv, S, _ = shape
-    if not (k_scale.dtype is torch.float32 and v_scale.dtype is torch.float32 and k_scale.numel() == Hkv
-            and v_scale.numel() == Hkv):
-        raise FkvError("scales must be float32 [Hkv]")
-    N = slot_mapping.numel()
-    want = (N, Hkv, HEAD_DIM)
-    if not (k_new.shape == want and v_new.shape == want):
-        raise FkvError("k_new/v_new must be [N][Hkv][128]")
-    return P, Hkv, S, N
-
-
 def kv_append_fp4(k_new, v_new, slot_mapping, k_scale, v_scale, k_cache, v_cache, stream=None):
     """Quantize bf16 ``k_new/v_new`` [N][Hkv][128] to e2m1 codes with an e4m3
     scale per 16 dims into ``k_cache/v_cache`` [P][Hkv][S][72] (uint8) at
     ``slot_mapping`` [N] (int64, <0 = skip).  The per-head fp32 scales are the
     ones an FP8 cache would use (``kv_calibrate_scales``)."""
-    _here(k_new, v_new, slot_mapping, k_scale, v_scale, k_cache, v_cache)
-    P, Hkv, S, N = _check_fp4_append(k_new, v_new, slot_mapping, k_scale, v_scale, k_cache, v_cache)
-    _raise(load_library().kv_append_fp4(
-        k_new.data_ptr(), v_new.data_ptr(), slot_mapping.data_ptr(), N, k_scale.data_ptr(), v_scale.data_ptr(),
-        k_cache.data_ptr(), v_cache.data_ptr(), P, Hkv, S, HEAD_DIM, _stream(stream)), "kv_append_fp4")
+    (_bind or _load_bind()).kv_append_fp4(k_new, v_new, slot_mapping, k_scale, v_scale, k_cache, v_cache, stream)
 
 
 def kv_append_fp4_tag_check(k_new, v_new, slot_mapping, k_scale, v_scale, k_cache, v_cache,
                             page_tags, page_indptr, page_indices, expected_tags, abort_mask, stream=None):
     """``kv_append_fp4`` then ``kv_page_tag_check`` (same arguments, same
     results) in one launch; ``page_tags`` has one entry per page of the pool."""
-    import torch
-    _here(k_new, v_new, slot_mapping, k_scale, v_scale, k_cache, v_cache, page_tags, page_indptr, page_indices,
-          expected_tags, abort_mask)
-    P, Hkv, S, N = _check_fp4_append(k_new, v_new, slot_mapping, k_scale, v_scale, k_cache, v_cache)
-    if not (page_tags.dtype in (torch.uint32, torch.int32) and expected_tags.dtype is page_tags.dtype):
-        raise FkvError("tags must be 32-bit, both of one dtype")
-    if page_tags.numel() != P:
-        raise FkvError("page_tags must have one entry per page of the pool")
-    if not (page_indptr.dtype is torch.int32 and page_indices.dtype is torch.int32):
-        raise FkvError("CSR must be int32")
-    B, nnz = page_indptr.numel() - 1, page_indices.numel()
-    if not (abort_mask.dtype is torch.uint8 and abort_mask.numel() == B and expected_tags.numel() == nnz):
-        raise FkvError("abort_mask must be uint8 [B], expected_tags parallel to page_indices")
-    _raise(load_library().kv_append_fp4_tag_check(
-        k_new.data_ptr(), v_new.data_ptr(), slot_mapping.data_ptr(), N, k_scale.data_ptr(), v_scale.data_ptr(),
-        k_cache.data_ptr(), v_cache.data_ptr(), P, Hkv, S, HEAD_DIM, page_tags.data_ptr(), page_indptr.data_ptr(),
-        page_indices.data_ptr(), expected_tags.data_ptr(), B, nnz, abort_mask.data_ptr(), _stream(stream)),
-        "kv_append_fp4_tag_check")
+    (_bind or _load_bind()).kv_append_fp4_tag_check(k_new, v_new, slot_mapping, k_scale, v_scale, k_cache, v_cache,
+                                                    page_tags, page_indptr, page_indices, expected_tags, abort_mask,
+                                                    stream)
 
 
 def kv_gather(k_cache, v_cache, slots, k_out, v_out, k_scale=None, v_scale=None, stream=None):
     """Cached tokens at ``slots`` [N] (int64; <0 gives zeros) as bf16
     ``k_out/v_out`` [N][Hkv][128].  Caches: FP8 uint8 / float8_e4m3fn or bf16
     [P][Hkv][S][128], or FP4 uint8 [P][Hkv][S][72]; scales fp32 [Hkv] unless bf16."""
-    import torch
-    _here(k_cache, v_cache, slots, k_out, v_out, k_scale, v_scale)
-    kv, D = _attn_cache(k_cache, v_cache, k_scale, v_scale)
-    shape = k_cache.shape
-    P, Hkv, S, _ = shape
-    if not (v_cache.shape == shape and v_cache.dtype is k_cache.dtype):
-        raise FkvError("k_cache and v_cache differ")
-    if kv != KV_BF16 and not (k_scale is not None and v_scale is not None and k_scale.dtype is torch.float32
-                              and v_scale.dtype is torch.float32 and k_scale.numel() == Hkv
-                              and v_scale.numel() == Hkv):
-        raise FkvError("scales must be float32 [Hkv]")
-    if slots.dtype is not torch.int64:
-        raise FkvError("slots must be int64")
-    N = slots.numel()
-    want = (N, Hkv, D)
-    if not (k_out.dtype is torch.bfloat16 and v_out.dtype is torch.bfloat16 and k_out.shape == want
-            and v_out.shape == want):
-        raise FkvError("k_out/v_out must be bf16 [N][Hkv][128]")
-    _raise(load_library().kv_gather(
-        k_cache.data_ptr(), v_cache.data_ptr(), kv, _ptr(k_scale), _ptr(v_scale), slots.data_ptr(), N,
-        k_out.data_ptr(), v_out.data_ptr(), P, Hkv, S, D, _stream(stream)), "kv_gather")
-
-
-def _head_rows(x, want, cur):
-    """The token stride of bf16 [N][H][128] whose head rows lie together."""
-    import torch
-    if not (x.dtype is torch.bfloat16 and x.get_device() == cur and x.shape == want):
-        raise FkvError("q/k and outputs must be bf16 [N][H][128] on the current device")
-    if want[0] == 0:
-        return want[1] * want[2]
-    a, b, c = x.stride()
-    if c != 1 or (b != want[2] and want[1] != 1):
-        raise FkvError("head rows must be contiguous")
-    return a if want[0] > 1 else want[1] * want[2]
+    (_bind or _load_bind()).kv_gather(k_cache, v_cache, slots, k_out, v_out, k_scale, v_scale, stream)
 
 
 def qk_norm_rope(q, k, positions, inv_freq, q_out, k_out, q_weight=None, k_weight=None, eps=1e-6, axis_map=None,
@@ -418,37 +361,8 @@ def qk_norm_rope(q, k, positions, inv_freq, q_out, k_out, q_weight=None, k_weigh
     ``inv_freq`` [R/2], R <= 128 a multiple of 16; pairs are (j, j + R/2), or
     (2j, 2j + 1) when ``interleaved``.  ``q_out``/``k_out`` may be q/k.
     ``k`` and ``k_out`` may be None."""
-    import torch
-    _here(positions, inv_freq, q_weight, k_weight, axis_map)
-    cur = positions.get_device()
-    N, Hq, D = q.shape
-    want = (N, Hq, D)
-    qs, qos = _head_rows(q, want, cur), _head_rows(q_out, want, cur)
-    if k is None:
-        if k_out is not None:
-            raise FkvError("k and k_out go together")
-        Hkv = ks = kos = 0
-    else:
-        if k_out is None or k.dim() != 3:
-            raise FkvError("k and k_out go together, both [N][Hkv][128]")
-        Hkv = k.shape[1]
-        want = (N, Hkv, D)
-        ks, kos = _head_rows(k, want, cur), _head_rows(k_out, want, cur)
-    for w in (q_weight, k_weight):
-        if w is not None and not (w.dtype is torch.bfloat16 and w.numel() == D):
-            raise FkvError("weights must be bf16 [128]")
-    pos_shape = positions.shape
-    if not (positions.dtype is torch.int32 and len(pos_shape) in (1, 2) and pos_shape[-1] == N):
-        raise FkvError("positions must be int32 [N] or [axes][N]")
-    half = inv_freq.numel()
-    if not (inv_freq.dtype is torch.float32 and inv_freq.dim() == 1):
-        raise FkvError("inv_freq must be float32 [R/2]")
-    if axis_map is not None and not (axis_map.dtype is torch.uint8 and axis_map.numel() == half):
-        raise FkvError("axis_map must be uint8 [R/2]")
-    _raise(load_library().qk_norm_rope(
-        q.data_ptr(), qs, Hq, _ptr(k), ks, Hkv, q_out.data_ptr(), qos, _ptr(k_out), kos, N, _ptr(q_weight),
-        _ptr(k_weight), float(eps), positions.data_ptr(), 1 if len(pos_shape) == 1 else pos_shape[0], inv_freq.data_ptr(),
-        _ptr(axis_map), 2 * half, 1 if interleaved else 0, float(rot_scale), D, _stream(stream)), "qk_norm_rope")
+    (_bind or _load_bind()).qk_norm_rope(q, k, positions, inv_freq, q_out, k_out, q_weight, k_weight, eps, axis_map,
+                                         interleaved, rot_scale, stream)
     return q_out, k_out
 
 
@@ -472,36 +386,10 @@ def kv_step_tables(cached_lens, new_lens, block_table, block_tags, free_pages, f
     refused uint8 and tags 32-bit; the capacities are the arrays' lengths.  For
     the next step pass ``cached_lens_out`` as ``cached_lens`` and ``free_left``
     as ``free_count`` (each may also be the same array in one call)."""
-    import torch
-    _here(cached_lens, new_lens, block_table, block_tags, free_pages, free_count, page_tags, step_lens,
-          cached_lens_out, refused, page_indptr, page_indices, expected_tags, token_indptr, slot_mapping, positions,
-          free_left, workspace)
-    for x in (cached_lens, new_lens, block_table, free_pages, free_count, step_lens, cached_lens_out, page_indptr,
-              page_indices, token_indptr, positions, free_left):
-        if x.dtype is not torch.int32:
-            raise FkvError("lengths, tables, free list, indptr, indices and positions must be int32")
-    tag = page_tags.dtype
-    if not ((tag is torch.int32 or tag is torch.uint32) and block_tags.dtype is tag and expected_tags.dtype is tag):
-        raise FkvError("tags must be 32-bit, of one dtype")
-    if not (slot_mapping.dtype is torch.int64 and refused.dtype is torch.uint8):
-        raise FkvError("slot_mapping must be int64, refused uint8")
-    B, nnz, n_tokens, n_free = cached_lens.numel(), page_indices.numel(), slot_mapping.numel(), free_pages.numel()
-    shape = block_table.shape
-    if not (len(shape) == 2 and shape[0] == B and block_tags.shape == shape):
-        raise FkvError("block_table and block_tags must be [B][max_blocks]")
-    if not (new_lens.numel() == B and step_lens.numel() == B and cached_lens_out.numel() == B
-            and refused.numel() == B and page_indptr.numel() == B + 1 and token_indptr.numel() == B + 1):
-        raise FkvError("one length per request, indptr arrays of B + 1")
-    if not (expected_tags.numel() == nnz and positions.numel() == n_tokens and free_count.numel() == 1
-            and free_left.numel() == 1):
-        raise FkvError("expected_tags parallel to page_indices, positions to slot_mapping; free counts of one value")
-    _raise(load_library().kv_step_tables(
-        cached_lens.data_ptr(), new_lens.data_ptr(), B, block_table.data_ptr(), block_tags.data_ptr(), shape[1],
-        free_pages.data_ptr(), n_free, free_count.data_ptr(), page_tags.data_ptr(), page_tags.numel(), int(page_size),
-        step_lens.data_ptr(), cached_lens_out.data_ptr(), refused.data_ptr(), page_indptr.data_ptr(),
-        page_indices.data_ptr(), expected_tags.data_ptr(), nnz, token_indptr.data_ptr(), slot_mapping.data_ptr(),
-        positions.data_ptr(), n_tokens, free_left.data_ptr(), workspace.data_ptr(), workspace.nbytes,
-        _stream(stream)), "kv_step_tables")
+    (_bind or _load_bind()).kv_step_tables(
+        cached_lens, new_lens, block_table, block_tags, free_pages, free_count, page_tags, page_size, step_lens,
+        cached_lens_out, refused, page_indptr, page_indices, expected_tags, token_indptr, slot_mapping, positions,
+        free_left, workspace, stream)
 
 
 def kv_page_realloc(page_tags, pages, new_tags, k_cache=None, v_cache=None, stream=None):
@@ -526,49 +414,6 @@ def kv_page_realloc(page_tags, pages, new_tags, k_cache=None, v_cache=None, stre
                                           _stream(stream)), "kv_page_realloc")
 
 
-def _attn_cache(k_cache, v_cache, k_scale, v_scale):
-    """The caches' format and head dim."""
-    import torch
-    if _is_fp4_cache(k_cache):
-        if not (v_cache.shape == k_cache.shape and v_cache.dtype is torch.uint8):
-            raise FkvError("k_cache and v_cache differ")
-        H = k_cache.shape[1]
-        if not (k_scale is not None and v_scale is not None and k_scale.dtype is torch.float32
-                and v_scale.dtype is torch.float32 and k_scale.numel() == H and v_scale.numel() == H):
-            raise FkvError("scales must be float32 [Hkv]")
-        return KV_FP4, HEAD_DIM
-    fp8 = _is_byte_cache(k_cache)
-    _need(fp8 or k_cache.dtype == torch.bfloat16, "cache must be uint8 (e4m3) or bf16")
-    return (KV_FP8_E4M3 if fp8 else KV_BF16), k_cache.shape[-1]
-
-
-def _check_attn(q, k_cache, v_cache, page_indptr, page_indices, seq_lens, out, workspace, k_scale, v_scale,
-                abort_mask):
-    import torch
-    for t in (q, k_cache, v_cache, page_indptr, page_indices, seq_lens, out, workspace, k_scale, v_scale, abort_mask):
-        if t is not None and not (t.is_cuda and t.is_contiguous()):
-            raise FkvError("tensors must be contiguous CUDA tensors")
-    kv, D2 = _attn_cache(k_cache, v_cache, k_scale, v_scale)
-    if not (q.dtype is torch.bfloat16 and out.dtype is torch.bfloat16):
-        raise FkvError("q/out must be bf16")
-    if seq_lens.dtype is not torch.int32:
-        raise FkvError("seq_lens must be int32")
-    if abort_mask is not None and abort_mask.dtype is not torch.uint8:
-        raise FkvError("abort_mask must be uint8")
-    shape = q.shape
-    B, Hq, D = shape
-    P, Hkv, S, _ = k_cache.shape
-    if not (out.shape == shape and D2 == D and page_indptr.numel() == B + 1):
-        raise FkvError("shape mismatch")
-    if kv == KV_FP4:
-        _here(q, k_cache, seq_lens)
-        if not (page_indptr.dtype is torch.int32 and page_indices.dtype is torch.int32 and seq_lens.numel() == B
-                and (abort_mask is None or abort_mask.numel() == B)):
-            raise FkvError("CSR must be int32, seq_lens and abort_mask [B]")
-    scales = (None, None) if kv == KV_BF16 else (_ptr(k_scale), _ptr(v_scale))
-    return kv, scales, B, Hq, P, Hkv, S, D
-
-
 def paged_decode_attn_workspace_size(batch, num_q_heads, num_kv_heads, head_dim=HEAD_DIM, kv_dtype=KV_FP8_E4M3):
     n = load_library().paged_decode_attn_workspace_size(batch, num_q_heads, num_kv_heads, head_dim, kv_dtype)
     _need(n > 0 or batch == 0, "unsupported shape for paged_decode_attn")
@@ -589,13 +434,8 @@ def paged_decode_attn(q, k_cache, v_cache, page_indptr, page_indices, seq_lens, 
     k_scale/v_scale fp32 [Hkv]) or bf16, or [P][Hkv][S][72] uint8 (FP4, with
     the same scales; workspace for KV_FP4); CSR page table int32; seq_lens int32
     [B]; abort_mask uint8 [B] or None (no tracker)."""
-    kv, scales, B, Hq, P, Hkv, S, D = _check_attn(q, k_cache, v_cache, page_indptr, page_indices, seq_lens, out,
-                                                  workspace, k_scale, v_scale, abort_mask)
-    _raise(load_library().paged_decode_attn(
-        q.data_ptr(), B, Hq, k_cache.data_ptr(), v_cache.data_ptr(), kv, *scales, P, Hkv, S, D,
-        page_indptr.data_ptr(), page_indices.data_ptr(), page_indices.numel(), seq_lens.data_ptr(), _ptr(abort_mask),
-        float(sm_scale), out.data_ptr(), workspace.data_ptr(), workspace.nbytes, _stream(stream)),
-        "paged_decode_attn")
+    (_bind or _load_bind()).paged_decode_attn(q, k_cache, v_cache, page_indptr, page_indices, seq_lens, sm_scale, out,
+                                              workspace, k_scale, v_scale, abort_mask, stream)
     return out
 
 
@@ -606,12 +446,27 @@ def paged_decode_attn_noalloc(q, k_cache, v_cache, page_indptr, page_indices, se
     ``NOALLOC_SCRATCH_BYTES`` inside the library (shared by all calls on a
     device, so calls must not overlap on the GPU).  Shapes needing more
     scratch raise FkvError (status ERR_SCRATCH_LIMIT)."""
-    kv, scales, B, Hq, P, Hkv, S, D = _check_attn(q, k_cache, v_cache, page_indptr, page_indices, seq_lens, out, None,
-                                                  k_scale, v_scale, abort_mask)
+    import torch
+    _dev(q, k_cache, v_cache, page_indptr, page_indices, seq_lens, out, k_scale, v_scale, abort_mask)
+    B, Hq, D = q.shape
+    P, Hkv, S, row = k_cache.shape
+    if _is_fp4_cache(k_cache):
+        kv, row = KV_FP4, HEAD_DIM
+    elif _is_byte_cache(k_cache):
+        kv = KV_FP8_E4M3
+    else:
+        _need(k_cache.dtype == torch.bfloat16, "cache must be uint8 (e4m3, or FP4 rows of 72) or bf16")
+        kv = KV_BF16
+    _need(kv != KV_FP4 or (_is_fp4_cache(v_cache) and v_cache.shape == k_cache.shape), "k_cache and v_cache differ")
+    _need(q.dtype == torch.bfloat16 and out.dtype == torch.bfloat16, "q/out must be bf16")
+    _need(seq_lens.dtype == torch.int32, "seq_lens must be int32")
+    _need(abort_mask is None or abort_mask.dtype == torch.uint8, "abort_mask must be uint8")
+    _need(tuple(out.shape) == (B, Hq, D) and row == D and page_indptr.numel() == B + 1, "shape mismatch")
     _raise(load_library().paged_decode_attn_noalloc(
-        q.data_ptr(), B, Hq, k_cache.data_ptr(), v_cache.data_ptr(), kv, *scales, P, Hkv, S, D,
-        page_indptr.data_ptr(), page_indices.data_ptr(), page_indices.numel(), seq_lens.data_ptr(), _ptr(abort_mask),
-        float(sm_scale), out.data_ptr(), _stream(stream)), "paged_decode_attn_noalloc")
+        _ptr(q), B, Hq, _ptr(k_cache), _ptr(v_cache), kv, _ptr(k_scale) if kv != KV_BF16 else None,
+        _ptr(v_scale) if kv != KV_BF16 else None, P, Hkv, S, D, _ptr(page_indptr), _ptr(page_indices),
+        page_indices.numel(), _ptr(seq_lens), _ptr(abort_mask), float(sm_scale), _ptr(out), _stream(stream)),
+        "paged_decode_attn_noalloc")
     return out
 
 

@@ -1,4 +1,5 @@
-"""Build libfkv.so in-tree with nvcc for sm_103a (GB300).
+"""Build libfkv.so in-tree with nvcc for sm_103a (GB300), and _fkv_bind.so, the
+Python binding's argument marshalling (host C++ against torch's headers).
 
 Each .cu file compiles to an object in parallel, then one shared library is
 linked.  No fast-math: the e4m3 quantisation relies on IEEE division.
@@ -14,6 +15,8 @@ PKG = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(PKG, "csrc")
 ROOT = os.path.dirname(PKG)
 LIB = os.path.join(PKG, "libfkv.so")
+BIND = os.path.join(PKG, "_fkv_bind.so")
+BIND_SOURCE = os.path.join(CSRC, "bind.cpp")
 BUILD_DIR = os.path.join(PKG, "_build")
 SOURCES = ["fkv_api.cu", "kv_append.cu", "tag_check.cu", "decode_attn.cu", "decode_attn_noalloc.cu", "page_realloc.cu",
            "kv_calibrate.cu", "selftest.cu", "kv_gather.cu", "qk_norm_rope.cu", "step_tables.cu"]
@@ -41,6 +44,20 @@ def _headers():
     return hs + [os.path.join(ROOT, "include", "fkv.h")]
 
 
+def _bind_command(out: str):
+    import sysconfig
+
+    import torch
+    from torch.utils.cpp_extension import include_paths
+    lib = os.path.join(os.path.dirname(torch.__file__), "lib")
+    cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc())))
+    inc = [*include_paths(), sysconfig.get_paths()["include"], os.path.join(cuda, "include")]
+    return [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
+            "-D_GLIBCXX_USE_CXX11_ABI=%d" % int(torch._C._GLIBCXX_USE_CXX11_ABI),
+            *[f for d in inc for f in ("-isystem", d)], BIND_SOURCE, "-o", out,
+            "-L", lib, "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda"]
+
+
 def build(force: bool = False, verbose: bool = False, extra_flags=(), out_lib: str = LIB,
           build_dir: str = BUILD_DIR) -> str:
     """Compile every source (only what changed) and link ``out_lib``."""
@@ -59,12 +76,17 @@ def build(force: bool = False, verbose: bool = False, extra_flags=(), out_lib: s
     def run(cmd):
         r = subprocess.run(cmd, capture_output=True, text=True)
         if r.returncode != 0:
-            raise RuntimeError("nvcc failed:\n%s\n%s%s" % (" ".join(cmd), r.stdout, r.stderr))
+            raise RuntimeError("compiling failed:\n%s\n%s%s" % (" ".join(cmd), r.stdout, r.stderr))
         if verbose and (r.stdout or r.stderr):
             print(r.stdout + r.stderr)
 
-    with cf.ThreadPoolExecutor(max_workers=len(SOURCES)) as ex:
-        list(ex.map(run, jobs))
+    bind = None
+    if out_lib == LIB and (force or _stale(BIND, [BIND_SOURCE, os.path.join(ROOT, "include", "fkv.h")])):
+        bind = BIND + ".tmp%d" % os.getpid()
+    with cf.ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
+        list(ex.map(run, ([_bind_command(bind)] if bind else []) + jobs))
+    if bind:
+        os.replace(bind, BIND)
     if force or jobs or _stale(out_lib, objs):
         tmp = out_lib + ".tmp%d" % os.getpid()
         run([exe, *ARCH, "-shared", "-o", tmp, *objs, "-lcudart"])

@@ -1136,7 +1136,7 @@ paged_decode_attn_kernel(const AttnParams p, const __grid_constant__ CUtensorMap
             // Steps of (block, word of 8 dims, M tile): 8 conversions, 8 products
             // and 2 MMAs each, which run on three pipes; each step converts for
             // the next one before its own MMAs, so that all three are fed.
-            uint2 kw[2 * MT];
+            uint2 kw[2 * MT] = {};
             uint32_t fa[2][4], fb[2][4];
             auto convert = [&](int step) {
                 const int blk = step / (2 * MT), wd = step / MT & 1, mt = step % MT, b = step & 1;
