@@ -62,12 +62,16 @@
 #ifndef FKV_FP4_STAGES
 #define FKV_FP4_STAGES 2
 #endif
-// Computing warps of a 4-bit CTA and the CTAs an SM holds.
+// Computing warps of a 4-bit CTA, and the CTAs an SM holds in the kernel's
+// instances for small and for large calls (large_fp4_call).
 #ifndef FKV_FP4_WARPS
 #define FKV_FP4_WARPS 2
 #endif
 #ifndef FKV_FP4_CTAS
 #define FKV_FP4_CTAS 4
+#endif
+#ifndef FKV_FP4_CTAS_LARGE
+#define FKV_FP4_CTAS_LARGE 6
 #endif
 #ifndef FKV_BF16_TILE
 #define FKV_BF16_TILE 64
@@ -109,7 +113,7 @@ constexpr uint32_t kFull = 0xffffffffu;
 #ifndef FKV_MIN_TILES_PER_WARP
 #define FKV_MIN_TILES_PER_WARP 12
 #endif
-constexpr int kNone = 0, kFinalDue = 1, kChunkDue = 2;   // merge duties of a warp
+constexpr int kNone = 0, kFinalDue = 1, kChunkDue = 2, kSecondDue = 3;   // merge duties of a warp
 constexpr int kChunk = FKV_MERGE_CHUNK;  // parts merged per first-level merge of a long unit
 constexpr int kMinTilesPerWarp = FKV_MIN_TILES_PER_WARP;   // small batches use fewer, longer warp ranges
 constexpr int kMinAlignedTiles = FKV_ALIGNED_MIN_TILES;
@@ -138,7 +142,6 @@ struct Cfg<FKV_KV_FP8_E4M3> {
     static constexpr int kHalves = 1;           // column blocks per token row
     static constexpr int kRow = 128;            // bytes of a token row in one column block
     static constexpr int kWarps = 1;            // computing warps per CTA
-    static constexpr int kMinCtas = 1;          // resident CTAs per SM the registers are held to
 };
 template <>
 struct Cfg<FKV_KV_BF16> {
@@ -147,7 +150,6 @@ struct Cfg<FKV_KV_BF16> {
     static constexpr int kHalves = 2;
     static constexpr int kRow = 128;
     static constexpr int kWarps = 1;
-    static constexpr int kMinCtas = 1;
 };
 template <>
 struct Cfg<FKV_KV_FP4> {
@@ -156,15 +158,19 @@ struct Cfg<FKV_KV_FP4> {
     static constexpr int kHalves = 1;
     static constexpr int kRow = FKV_FP4_ROW_BYTES;
     static constexpr int kWarps = FKV_FP4_WARPS;
-    static constexpr int kMinCtas = FKV_FP4_CTAS;
 };
 
-// Attention CTA: kWarps warps that each issue their copies and compute, on a
-// stage ring of their own, or (kWS, kWarps 1) a producer warp that issues copies
-// and a consumer warp that computes.
+// The kernel has two variants per format.  FP8 and BF16: one warp that issues
+// its copies and computes, or (kVar) a producer warp that issues copies and a
+// consumer warp that computes.  FP4: kWarps warps that each issue their copies
+// and compute, on a stage ring of their own, held to the registers of the
+// small-call or (kVar) of the large-call residency.
 template <int kKv>
-__host__ __device__ constexpr int attn_threads(bool ws) {
-    return ws ? 64 : 32 * Cfg<kKv>::kWarps;
+__host__ __device__ constexpr int attn_threads(bool var) {
+    return kKv != FKV_KV_FP4 && var ? 64 : 32 * Cfg<kKv>::kWarps;
+}
+__host__ __device__ constexpr int attn_min_ctas(int kv, bool var) {
+    return kv != FKV_KV_FP4 ? 1 : var ? FKV_FP4_CTAS_LARGE : FKV_FP4_CTAS;
 }
 
 template <int kKv>
@@ -671,12 +677,14 @@ __device__ bool merge_parts_smem(const AttnParams &p, uint32_t sbuf, int cap, ui
 // whole warps (place_aligned) when the live requests' tiles pass its test and
 // uses the even split otherwise.  Larger batches use the instance without
 // the option (their warps do not hold the requests' rows).
-template <int kKv, bool kWS, bool kAligned>
-__global__ void __launch_bounds__(attn_threads<kKv>(kWS), Cfg<kKv>::kMinCtas)
+template <int kKv, bool kVar, bool kAligned>
+__global__ void __launch_bounds__(attn_threads<kKv>(kVar), attn_min_ctas(kKv, kVar))
 paged_decode_attn_kernel(const AttnParams p, const __grid_constant__ CUtensorMap tmK,
                          const __grid_constant__ CUtensorMap tmV) {
     using Lay = Layout<kKv>;
     constexpr bool kFp8 = kKv == FKV_KV_FP8_E4M3, kFp4 = kKv == FKV_KV_FP4;
+    constexpr bool kWS = !kFp4 && kVar;                  // producer and consumer warp
+    constexpr bool kLarge = kFp4 && kVar;                // instance for large 4-bit calls
     constexpr bool kScaled = kFp8 || kFp4;               // codes with per-head scales, computed in f16
     constexpr int kTile = Lay::kTile;
     constexpr int NST = Lay::kStages;
@@ -1012,6 +1020,231 @@ paged_decode_attn_kernel(const AttnParams p, const __grid_constant__ CUtensorMap
     int def_stage = kNone, def_r = 0, def_h = 0;
     UnitGeom def_gm{0, 0};
     float def_vsc = 1.f;
+    int end_stage = kNone;  // large-call instance: the merge at the range end
+
+    // End of this warp's share of the unit at cursor C: the row itself, or a
+    // partial and its arrival.  range_end: it is the last of the warp's range.
+    auto finish_share = [&](bool range_end) __attribute__((always_inline)) {
+        float lt[2] = {l[0], l[1]};
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            lt[j] += __shfl_xor_sync(kFull, lt[j], 4);
+            lt[j] += __shfl_xor_sync(kFull, lt[j], 8);
+            lt[j] += __shfl_xor_sync(kFull, lt[j], 16);
+        }
+        const bool whole = seg_start == 0 && C.tt == C.nt - 1;
+        const int64_t u = static_cast<int64_t>(C.r) * Hkv + C.h;
+        // parts of a split unit that hold tiles (warps of its span with a
+        // non-empty range)
+        auto unit_parts = [&](const UnitGeom &gm) {
+            int n = gm.span;
+            if (maybe_empty) {
+                n = 0;
+                for (int64_t x = gm.wf; x < gm.wf + gm.span; ++x) n += warp_lo(x, T, nw) != warp_lo(x + 1, T, nw);
+            }
+            return n;
+        };
+        // The unit's final merge from this warp's registers plus the other
+        // parts' partials (at most two), loaded straight from L2: their
+        // statistics and the first one's outputs in one round trip, the
+        // second one's outputs in another.  This warp holds the unit's
+        // first part, so its registers are entry 0 of merge_parts_smem's
+        // definition and the other parts follow in index order; every
+        // step below is that definition's, with the same roundings, so the
+        // row's bytes equal those of the merge through the stage ring.
+        // The caller has acquired every other part.
+        auto merge_regs = [&](int64_t u) {
+            const int d0 = kScaled ? 16 * g : 8 * g, d1 = kScaled ? 16 * g + 8 : 64 + 8 * g;
+            int64_t x0 = 0, x1 = 0;                       // the other parts, in index order
+            int no = 0;
+            for (int64_t x = cgm.wf; x < cgm.wf + cgm.span; ++x) {
+                if (x == w || (maybe_empty && warp_lo(x, T, nw) == warp_lo(x + 1, T, nw))) continue;
+                if (no == 0) x0 = x;
+                else x1 = x;
+                ++no;
+            }
+            // lanes past the group's heads read a valid row and drop it
+            float2 ml[2][2];
+            float4 q[2][4];
+            auto load_rows = [&](int k) {
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    const int hd = min(2 * t + j, G - 1);
+                    const float4 *prow =
+                        reinterpret_cast<const float4 *>(p.part_o + ((u + (k ? x1 : x0)) * G + hd) * kD);
+                    q[j][0] = __ldcg(prow + d0 / 4);
+                    q[j][1] = __ldcg(prow + d0 / 4 + 1);
+                    q[j][2] = __ldcg(prow + d1 / 4);
+                    q[j][3] = __ldcg(prow + d1 / 4 + 1);
+                }
+            };
+#pragma unroll
+            for (int k = 0; k < 2; ++k)
+#pragma unroll
+                for (int j = 0; j < 2; ++j)
+                    ml[k][j] = k < no ? __ldcg(p.part_ml + (u + (k ? x1 : x0)) * p.GP + min(2 * t + j, G - 1))
+                                      : make_float2(-INFINITY, 0.f);
+            load_rows(0);
+            bool bad = unit_bad;
+            float v[2][16], w1[2], w2[2], Lj[2];
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                bad |= ml[0][j].y < 0.f || ml[1][j].y < 0.f;
+                const float mx = fmaxf(fmaxf(m[j], ml[0][j].x), ml[1][j].x);
+                const float w0 = m[j] == -INFINITY ? 0.f : ex2(m[j] - mx);
+                w1[j] = ml[0][j].x == -INFINITY ? 0.f : ex2(ml[0][j].x - mx);
+                w2[j] = ml[1][j].x == -INFINITY ? 0.f : ex2(ml[1][j].x - mx);
+                // the lanes' butterfly sum with entries at lanes 0, 1, 2 (zeros past them)
+                const float sl = __fadd_rn(__fadd_rn(__fmul_rn(w0, lt[j]), __fmul_rn(w1[j], ml[0][j].y)),
+                                           __fmul_rn(w2[j], ml[1][j].y));
+                Lj[j] = __fmaf_rn(0.f, 0.f, sl);
+#pragma unroll
+                for (int a = 0; a < 8; ++a) {
+                    v[j][2 * a] = __fmaf_rn(w0, o[a][j], 0.f);
+                    v[j][2 * a + 1] = __fmaf_rn(w0, o[a][2 + j], 0.f);
+                }
+            }
+            for (int k = 0; k < no; ++k) {
+                if (k == 1) load_rows(1);
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    const float qv[16] = {q[j][0].x, q[j][0].y, q[j][0].z, q[j][0].w, q[j][1].x, q[j][1].y,
+                                          q[j][1].z, q[j][1].w, q[j][2].x, q[j][2].y, q[j][2].z, q[j][2].w,
+                                          q[j][3].x, q[j][3].y, q[j][3].z, q[j][3].w};
+                    const float wk = k == 0 ? w1[j] : w2[j];
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) v[j][e] = __fmaf_rn(wk, qv[e], v[j][e]);
+                }
+            }
+            bad = __any_sync(kFull, bad);
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                const int hd = 2 * t + j;
+                if (hd >= G) continue;
+                const float f = __fdiv_rn(cvsc, Lj[j]);
+                __nv_bfloat16 *orow = p.out + (static_cast<int64_t>(C.r) * p.Hq + C.h * G + hd) * kD;
+                uint4 r0v = make_uint4(0u, 0u, 0u, 0u), r1v = make_uint4(0u, 0u, 0u, 0u);
+                if (!bad) {                                // fail closed: zeros, whatever the data
+                    r0v.x = pack_bf16x2(__fmul_rn(v[j][0], f), __fmul_rn(v[j][1], f));
+                    r0v.y = pack_bf16x2(__fmul_rn(v[j][2], f), __fmul_rn(v[j][3], f));
+                    r0v.z = pack_bf16x2(__fmul_rn(v[j][4], f), __fmul_rn(v[j][5], f));
+                    r0v.w = pack_bf16x2(__fmul_rn(v[j][6], f), __fmul_rn(v[j][7], f));
+                    r1v.x = pack_bf16x2(__fmul_rn(v[j][8], f), __fmul_rn(v[j][9], f));
+                    r1v.y = pack_bf16x2(__fmul_rn(v[j][10], f), __fmul_rn(v[j][11], f));
+                    r1v.z = pack_bf16x2(__fmul_rn(v[j][12], f), __fmul_rn(v[j][13], f));
+                    r1v.w = pack_bf16x2(__fmul_rn(v[j][14], f), __fmul_rn(v[j][15], f));
+                }
+                *reinterpret_cast<uint4 *>(orow + d0) = r0v;
+                *reinterpret_cast<uint4 *>(orow + d1) = r1v;
+            }
+        };
+        bool merged = false;
+#if FKV_TRY_LAST
+        // (not the 4-bit kernel, whose shorter ranges leave fewer such units: 66.4 us
+        // without it on 32 x 8192 tokens, 67.5 with it)
+        if (!kFp4 && !whole && seg_start == 0 && range_end && (maybe_empty || cgm.span <= kChunk) &&
+            unit_parts(cgm) <= 3) {
+            // This warp holds the unit's first part (the unit started in
+            // its range and runs to the range end).  The unit's other
+            // parts usually end early in their warps' ranges, so at this
+            // warp's range end they may all have arrived.  Then this warp
+            // is the last: it merges its registers with their partials,
+            // loaded straight from global memory (one round trip for a
+            // unit over two warps), and writes the row -- no partial of
+            // its own, no arrival.  Otherwise it publishes and arrives as
+            // below.  (Only the first part of a unit of at most three
+            // parts does this: merge_regs reproduces merge_parts_smem's
+            // arithmetic for that case.)
+            int known = 0;
+            if (lane == 0) known = ld_acquire_gpu(p.counters + u) == unit_parts(cgm) - 1;
+            merged = __shfl_sync(kFull, known, 0) != 0;
+            if (merged) {
+                __syncwarp();                              // lane 0's acquire covers the warp's loads
+                merge_regs(u);
+            }
+        }
+#endif
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            const int hd = 2 * t + j;
+            if (hd >= G || merged) continue;
+            // this lane's 16 dims of head hd, in ascending order
+            float v[16];
+#pragma unroll
+            for (int a = 0; a < 8; ++a) {
+                v[2 * a] = o[a][j];
+                v[2 * a + 1] = o[a][2 + j];
+            }
+            const int d0 = kScaled ? 16 * g : 8 * g;          // first run of dims
+            const int d1 = kScaled ? 16 * g + 8 : 64 + 8 * g; // second run (8 dims each)
+            if (whole) {
+                const float f = cvsc / lt[j];
+                __nv_bfloat16 *orow = p.out + (static_cast<int64_t>(C.r) * p.Hq + C.h * G + hd) * kD;
+                uint4 r0v = make_uint4(0u, 0u, 0u, 0u), r1v = make_uint4(0u, 0u, 0u, 0u);
+                if (!unit_bad) {                           // fail closed: zeros, whatever the data
+                    r0v.x = pack_bf16x2(v[0] * f, v[1] * f);
+                    r0v.y = pack_bf16x2(v[2] * f, v[3] * f);
+                    r0v.z = pack_bf16x2(v[4] * f, v[5] * f);
+                    r0v.w = pack_bf16x2(v[6] * f, v[7] * f);
+                    r1v.x = pack_bf16x2(v[8] * f, v[9] * f);
+                    r1v.y = pack_bf16x2(v[10] * f, v[11] * f);
+                    r1v.z = pack_bf16x2(v[12] * f, v[13] * f);
+                    r1v.w = pack_bf16x2(v[14] * f, v[15] * f);
+                }
+                *reinterpret_cast<uint4 *>(orow + d0) = r0v;
+                *reinterpret_cast<uint4 *>(orow + d1) = r1v;
+            } else {
+                const int64_t slot = u + w;
+                float *prow = p.part_o + (slot * G + hd) * kD;
+                __stcg(reinterpret_cast<float4 *>(prow + d0), make_float4(v[0], v[1], v[2], v[3]));
+                __stcg(reinterpret_cast<float4 *>(prow + d0 + 4), make_float4(v[4], v[5], v[6], v[7]));
+                __stcg(reinterpret_cast<float4 *>(prow + d1), make_float4(v[8], v[9], v[10], v[11]));
+                __stcg(reinterpret_cast<float4 *>(prow + d1 + 4), make_float4(v[12], v[13], v[14], v[15]));
+                if (g == 0) __stcg(p.part_ml + slot * p.GP + hd, make_float2(m[j], unit_bad ? -1.f : lt[j]));
+            }
+        }
+        if (!whole && !merged) {
+            // Merge without waiting: the last of the unit's warps to arrive
+            // merges.  Units split over more than kChunk warps merge in two
+            // levels (chunks of kChunk consecutive parts, then the chunks),
+            // so no single warp reads a long unit's partials serially.
+            // Arrivals are acquire-release atomics by lane 0 after a warp
+            // barrier: they publish this warp's partial and, for the last
+            // arriver, make every other part visible.
+            const UnitGeom &gm = cgm;
+            int stage = kNone;
+            __syncwarp();
+            if (maybe_empty || gm.span <= kChunk) {
+                const int nparts = unit_parts(gm);
+                int last = 0;
+                if (lane == 0) last = atomic_add_acq_rel_gpu(p.counters + u, 1) == nparts - 1;
+                stage = __shfl_sync(kFull, last, 0) ? kFinalDue : kNone;
+            } else {
+                // A one-part chunk (the unit's last warp, whose part ends early in
+                // its range) is already its own result: no first level.
+                const int csz = gm.csz(w);
+                int last = csz == 1;
+                if (csz > 1 && lane == 0)
+                    last = atomic_add_acq_rel_gpu(p.chunk_counters + (u + gm.wf + gm.c0(w)), 1) == csz - 1;
+                stage = __shfl_sync(kFull, last, 0) ? kChunkDue : kNone;
+            }
+            // at the range end the stage ring is idle: merge through it
+            if (stage != kNone && !range_end) {
+                // mid-range: the stream would stall for the merge, and a
+                // part ending just before this range's end can be the last
+                // to arrive, putting that stall on the call's critical path;
+                // owe it until the range end instead
+                def_stage = stage;
+                def_gm = gm;
+                def_r = C.r;
+                def_h = C.h;
+                def_vsc = cvsc;
+                stage = kNone;
+            }
+            if constexpr (kLarge) end_stage = stage;           // done below, with the owed one
+            else if (stage != kNone) merge_steps(stage, gm, C.r, C.h, cvsc);
+        }
+    };
 
     for (Count i = 0; i < n_tiles; ++i) {
         const int s = static_cast<int>(i % NST);
@@ -1359,227 +1592,56 @@ paged_decode_attn_kernel(const AttnParams p, const __grid_constant__ CUtensorMap
         }
 
         // ---- end of this warp's share of the unit ----
-        if (C.tt == C.nt - 1 || i == n_tiles - 1) {
-            float lt[2] = {l[0], l[1]};
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                lt[j] += __shfl_xor_sync(kFull, lt[j], 4);
-                lt[j] += __shfl_xor_sync(kFull, lt[j], 8);
-                lt[j] += __shfl_xor_sync(kFull, lt[j], 16);
-            }
-            const bool whole = seg_start == 0 && C.tt == C.nt - 1;
-            const int64_t u = static_cast<int64_t>(C.r) * Hkv + C.h;
-            // parts of a split unit that hold tiles (warps of its span with a
-            // non-empty range)
-            auto unit_parts = [&](const UnitGeom &gm) {
-                int n = gm.span;
-                if (maybe_empty) {
-                    n = 0;
-                    for (int64_t x = gm.wf; x < gm.wf + gm.span; ++x) n += warp_lo(x, T, nw) != warp_lo(x + 1, T, nw);
-                }
-                return n;
-            };
-            // The unit's final merge from this warp's registers plus the other
-            // parts' partials (at most two), loaded straight from L2: their
-            // statistics and the first one's outputs in one round trip, the
-            // second one's outputs in another.  This warp holds the unit's
-            // first part, so its registers are entry 0 of merge_parts_smem's
-            // definition and the other parts follow in index order; every
-            // step below is that definition's, with the same roundings, so the
-            // row's bytes equal those of the merge through the stage ring.
-            // The caller has acquired every other part.
-            auto merge_regs = [&](int64_t u) {
-                const int d0 = kScaled ? 16 * g : 8 * g, d1 = kScaled ? 16 * g + 8 : 64 + 8 * g;
-                int64_t x0 = 0, x1 = 0;                       // the other parts, in index order
-                int no = 0;
-                for (int64_t x = cgm.wf; x < cgm.wf + cgm.span; ++x) {
-                    if (x == w || (maybe_empty && warp_lo(x, T, nw) == warp_lo(x + 1, T, nw))) continue;
-                    if (no == 0) x0 = x;
-                    else x1 = x;
-                    ++no;
-                }
-                // lanes past the group's heads read a valid row and drop it
-                float2 ml[2][2];
-                float4 q[2][4];
-                auto load_rows = [&](int k) {
-#pragma unroll
-                    for (int j = 0; j < 2; ++j) {
-                        const int hd = min(2 * t + j, G - 1);
-                        const float4 *prow =
-                            reinterpret_cast<const float4 *>(p.part_o + ((u + (k ? x1 : x0)) * G + hd) * kD);
-                        q[j][0] = __ldcg(prow + d0 / 4);
-                        q[j][1] = __ldcg(prow + d0 / 4 + 1);
-                        q[j][2] = __ldcg(prow + d1 / 4);
-                        q[j][3] = __ldcg(prow + d1 / 4 + 1);
-                    }
-                };
-#pragma unroll
-                for (int k = 0; k < 2; ++k)
-#pragma unroll
-                    for (int j = 0; j < 2; ++j)
-                        ml[k][j] = k < no ? __ldcg(p.part_ml + (u + (k ? x1 : x0)) * p.GP + min(2 * t + j, G - 1))
-                                          : make_float2(-INFINITY, 0.f);
-                load_rows(0);
-                bool bad = unit_bad;
-                float v[2][16], w1[2], w2[2], Lj[2];
-#pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    bad |= ml[0][j].y < 0.f || ml[1][j].y < 0.f;
-                    const float mx = fmaxf(fmaxf(m[j], ml[0][j].x), ml[1][j].x);
-                    const float w0 = m[j] == -INFINITY ? 0.f : ex2(m[j] - mx);
-                    w1[j] = ml[0][j].x == -INFINITY ? 0.f : ex2(ml[0][j].x - mx);
-                    w2[j] = ml[1][j].x == -INFINITY ? 0.f : ex2(ml[1][j].x - mx);
-                    // the lanes' butterfly sum with entries at lanes 0, 1, 2 (zeros past them)
-                    const float sl = __fadd_rn(__fadd_rn(__fmul_rn(w0, lt[j]), __fmul_rn(w1[j], ml[0][j].y)),
-                                               __fmul_rn(w2[j], ml[1][j].y));
-                    Lj[j] = __fmaf_rn(0.f, 0.f, sl);
-#pragma unroll
-                    for (int a = 0; a < 8; ++a) {
-                        v[j][2 * a] = __fmaf_rn(w0, o[a][j], 0.f);
-                        v[j][2 * a + 1] = __fmaf_rn(w0, o[a][2 + j], 0.f);
-                    }
-                }
-                for (int k = 0; k < no; ++k) {
-                    if (k == 1) load_rows(1);
-#pragma unroll
-                    for (int j = 0; j < 2; ++j) {
-                        const float qv[16] = {q[j][0].x, q[j][0].y, q[j][0].z, q[j][0].w, q[j][1].x, q[j][1].y,
-                                              q[j][1].z, q[j][1].w, q[j][2].x, q[j][2].y, q[j][2].z, q[j][2].w,
-                                              q[j][3].x, q[j][3].y, q[j][3].z, q[j][3].w};
-                        const float wk = k == 0 ? w1[j] : w2[j];
-#pragma unroll
-                        for (int e = 0; e < 16; ++e) v[j][e] = __fmaf_rn(wk, qv[e], v[j][e]);
-                    }
-                }
-                bad = __any_sync(kFull, bad);
-#pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    const int hd = 2 * t + j;
-                    if (hd >= G) continue;
-                    const float f = __fdiv_rn(cvsc, Lj[j]);
-                    __nv_bfloat16 *orow = p.out + (static_cast<int64_t>(C.r) * p.Hq + C.h * G + hd) * kD;
-                    uint4 r0v = make_uint4(0u, 0u, 0u, 0u), r1v = make_uint4(0u, 0u, 0u, 0u);
-                    if (!bad) {                                // fail closed: zeros, whatever the data
-                        r0v.x = pack_bf16x2(__fmul_rn(v[j][0], f), __fmul_rn(v[j][1], f));
-                        r0v.y = pack_bf16x2(__fmul_rn(v[j][2], f), __fmul_rn(v[j][3], f));
-                        r0v.z = pack_bf16x2(__fmul_rn(v[j][4], f), __fmul_rn(v[j][5], f));
-                        r0v.w = pack_bf16x2(__fmul_rn(v[j][6], f), __fmul_rn(v[j][7], f));
-                        r1v.x = pack_bf16x2(__fmul_rn(v[j][8], f), __fmul_rn(v[j][9], f));
-                        r1v.y = pack_bf16x2(__fmul_rn(v[j][10], f), __fmul_rn(v[j][11], f));
-                        r1v.z = pack_bf16x2(__fmul_rn(v[j][12], f), __fmul_rn(v[j][13], f));
-                        r1v.w = pack_bf16x2(__fmul_rn(v[j][14], f), __fmul_rn(v[j][15], f));
-                    }
-                    *reinterpret_cast<uint4 *>(orow + d0) = r0v;
-                    *reinterpret_cast<uint4 *>(orow + d1) = r1v;
-                }
-            };
-            bool merged = false;
-#if FKV_TRY_LAST
-            if (!whole && seg_start == 0 && i == n_tiles - 1 && (maybe_empty || cgm.span <= kChunk) &&
-                unit_parts(cgm) <= 3) {
-                // This warp holds the unit's first part (the unit started in
-                // its range and runs to the range end).  The unit's other
-                // parts usually end early in their warps' ranges, so at this
-                // warp's range end they may all have arrived.  Then this warp
-                // is the last: it merges its registers with their partials,
-                // loaded straight from global memory (one round trip for a
-                // unit over two warps), and writes the row -- no partial of
-                // its own, no arrival.  Otherwise it publishes and arrives as
-                // below.  (Only the first part of a unit of at most three
-                // parts does this: merge_regs reproduces merge_parts_smem's
-                // arithmetic for that case.)
-                int known = 0;
-                if (lane == 0) known = ld_acquire_gpu(p.counters + u) == unit_parts(cgm) - 1;
-                merged = __shfl_sync(kFull, known, 0) != 0;
-                if (merged) {
-                    __syncwarp();                              // lane 0's acquire covers the warp's loads
-                    merge_regs(u);
-                }
-            }
-#endif
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                const int hd = 2 * t + j;
-                if (hd >= G || merged) continue;
-                // this lane's 16 dims of head hd, in ascending order
-                float v[16];
-#pragma unroll
-                for (int a = 0; a < 8; ++a) {
-                    v[2 * a] = o[a][j];
-                    v[2 * a + 1] = o[a][2 + j];
-                }
-                const int d0 = kScaled ? 16 * g : 8 * g;          // first run of dims
-                const int d1 = kScaled ? 16 * g + 8 : 64 + 8 * g; // second run (8 dims each)
-                if (whole) {
-                    const float f = cvsc / lt[j];
-                    __nv_bfloat16 *orow = p.out + (static_cast<int64_t>(C.r) * p.Hq + C.h * G + hd) * kD;
-                    uint4 r0v = make_uint4(0u, 0u, 0u, 0u), r1v = make_uint4(0u, 0u, 0u, 0u);
-                    if (!unit_bad) {                           // fail closed: zeros, whatever the data
-                        r0v.x = pack_bf16x2(v[0] * f, v[1] * f);
-                        r0v.y = pack_bf16x2(v[2] * f, v[3] * f);
-                        r0v.z = pack_bf16x2(v[4] * f, v[5] * f);
-                        r0v.w = pack_bf16x2(v[6] * f, v[7] * f);
-                        r1v.x = pack_bf16x2(v[8] * f, v[9] * f);
-                        r1v.y = pack_bf16x2(v[10] * f, v[11] * f);
-                        r1v.z = pack_bf16x2(v[12] * f, v[13] * f);
-                        r1v.w = pack_bf16x2(v[14] * f, v[15] * f);
-                    }
-                    *reinterpret_cast<uint4 *>(orow + d0) = r0v;
-                    *reinterpret_cast<uint4 *>(orow + d1) = r1v;
-                } else {
-                    const int64_t slot = u + w;
-                    float *prow = p.part_o + (slot * G + hd) * kD;
-                    __stcg(reinterpret_cast<float4 *>(prow + d0), make_float4(v[0], v[1], v[2], v[3]));
-                    __stcg(reinterpret_cast<float4 *>(prow + d0 + 4), make_float4(v[4], v[5], v[6], v[7]));
-                    __stcg(reinterpret_cast<float4 *>(prow + d1), make_float4(v[8], v[9], v[10], v[11]));
-                    __stcg(reinterpret_cast<float4 *>(prow + d1 + 4), make_float4(v[12], v[13], v[14], v[15]));
-                    if (g == 0) __stcg(p.part_ml + slot * p.GP + hd, make_float2(m[j], unit_bad ? -1.f : lt[j]));
-                }
-            }
-            if (!whole && !merged) {
-                // Merge without waiting: the last of the unit's warps to arrive
-                // merges.  Units split over more than kChunk warps merge in two
-                // levels (chunks of kChunk consecutive parts, then the chunks),
-                // so no single warp reads a long unit's partials serially.
-                // Arrivals are acquire-release atomics by lane 0 after a warp
-                // barrier: they publish this warp's partial and, for the last
-                // arriver, make every other part visible.
-                const UnitGeom &gm = cgm;
-                int stage = kNone;
-                __syncwarp();
-                if (maybe_empty || gm.span <= kChunk) {
-                    const int nparts = unit_parts(gm);
-                    int last = 0;
-                    if (lane == 0) last = atomic_add_acq_rel_gpu(p.counters + u, 1) == nparts - 1;
-                    stage = __shfl_sync(kFull, last, 0) ? kFinalDue : kNone;
-                } else {
-                    // A one-part chunk (the unit's last warp, whose part ends early in
-                    // its range) is already its own result: no first level.
-                    const int csz = gm.csz(w);
-                    int last = csz == 1;
-                    if (csz > 1 && lane == 0)
-                        last = atomic_add_acq_rel_gpu(p.chunk_counters + (u + gm.wf + gm.c0(w)), 1) == csz - 1;
-                    stage = __shfl_sync(kFull, last, 0) ? kChunkDue : kNone;
-                }
-                // at the range end the stage ring is idle: merge through it
-                if (stage != kNone && i < n_tiles - 1) {
-                    // mid-range: the stream would stall for the merge, and a
-                    // part ending just before this range's end can be the last
-                    // to arrive, putting that stall on the call's critical path;
-                    // owe it until the range end instead
-                    def_stage = stage;
-                    def_gm = gm;
-                    def_r = C.r;
-                    def_h = C.h;
-                    def_vsc = cvsc;
-                    stage = kNone;
-                }
-                if (stage != kNone) merge_steps(stage, gm, C.r, C.h, cvsc);
-            }
+        if constexpr (kLarge) {
+            if (i == n_tiles - 1) break;                   // finished below
+            if (C.tt == C.nt - 1) finish_share(false);
+        } else if (C.tt == C.nt - 1 || i == n_tiles - 1) {
+            finish_share(i == n_tiles - 1);
         }
         cursor_next(C, p);
     }
-    if (def_stage != kNone) merge_steps(def_stage, def_gm, def_r, def_h, def_vsc);
+    if constexpr (kLarge) {
+        // The large-call instance ends its range outside the loop, and merges with
+        // one copy of the merge (the steps of merge_steps, as a loop): what that
+        // holds then shares no registers with the loop's state, which fits 164 that
+        // way, three warps per scheduler, and spills at 168 otherwise.  It costs
+        // about 3 us at the end of a call, so a small one keeps them in the loop.
+        finish_share(true);
+        int stage = end_stage, r = C.r, h = C.h;
+        UnitGeom gm = cgm;
+        float vsc = cvsc;
+        bool owed = def_stage != kNone;
+        while (true) {
+            if (stage == kNone) {
+                if (!owed) break;
+                owed = false;
+                stage = def_stage;
+                gm = def_gm;
+                r = def_r;
+                h = def_h;
+                vsc = def_vsc;
+            }
+            __syncwarp();
+            const int64_t u = static_cast<int64_t>(r) * Hkv + h;
+            const bool chunk = stage == kChunkDue, second = stage == kSecondDue;
+            const int c0 = chunk ? gm.c0(w) : 0;
+            const int n = chunk ? gm.csz(w) : second ? gm.nch() : gm.span;
+            const int64_t at = u + gm.wf + c0;
+            if ((!chunk || n > 1) &&
+                !merge_parts_smem(p, sbase, merge_cap, merge_bar, merge_phase, nw, at, n, second ? kChunk : 1,
+                                  stage == kFinalDue && maybe_empty, gm.wf + c0, T, !chunk, r, h, vsc, at)) {
+                if (lane == 0) atomicOr(p.err, FKV_DEVERR_TIMEOUT);
+                stage = kNone;                                 // nothing more of this unit
+                continue;
+            }
+            __syncwarp();
+            int last = 0;
+            if (chunk && lane == 0) last = atomic_add_acq_rel_gpu(p.counters + u, 1) == gm.nch() - 1;
+            stage = __shfl_sync(kFull, last, 0) ? kSecondDue : kNone;
+        }
+    } else if (def_stage != kNone) {
+        merge_steps(def_stage, def_gm, def_r, def_h, def_vsc);
+    }
     grid_dep_launch();
 }
 
@@ -1590,7 +1652,7 @@ namespace {
 
 constexpr int kMaxDev = 64;
 std::mutex g_mu;
-// Resident CTAs per SM, [dev][kv_dtype][ws], with the id of the context in
+// Resident CTAs per SM, [dev][kv_dtype][variant], with the id of the context in
 // which the kernels' shared-memory limit was raised: a new context (after
 // cudaDeviceReset) loads the kernels again, so the attribute is set again.
 struct CtasPerSm {
@@ -1613,23 +1675,23 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
     return fn;
 }
 
-template <int kKv, bool kWS>
+template <int kKv, bool kVar>
 int ctas_per_sm() {
     int dev = -1;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDev) return 0;
     std::lock_guard<std::mutex> lk(g_mu);
-    CtasPerSm &c = g_ctas_per_sm[dev][kKv][kWS ? 1 : 0];
+    CtasPerSm &c = g_ctas_per_sm[dev][kKv][kVar ? 1 : 0];
     const unsigned long long ctx = current_context_id();
     if (!c.n || ctx == 0 || ctx != c.ctx_id) {
         const int smem = Layout<kKv>::kSmem;
-        if (cudaFuncSetAttribute(paged_decode_attn_kernel<kKv, kWS, false>,
+        if (cudaFuncSetAttribute(paged_decode_attn_kernel<kKv, kVar, false>,
                                  cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess ||
-            cudaFuncSetAttribute(paged_decode_attn_kernel<kKv, kWS, true>,
+            cudaFuncSetAttribute(paged_decode_attn_kernel<kKv, kVar, true>,
                                  cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
             return 0;
         int nb = 0;
-        if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&nb, paged_decode_attn_kernel<kKv, kWS, false>,
-                                                          attn_threads<kKv>(kWS), smem) != cudaSuccess ||
+        if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&nb, paged_decode_attn_kernel<kKv, kVar, false>,
+                                                          attn_threads<kKv>(kVar), smem) != cudaSuccess ||
             nb <= 0)
             return 0;
         c.n = nb < 16 ? nb : 16;
@@ -1640,16 +1702,13 @@ int ctas_per_sm() {
 
 // Computing warps of one launch (one per CTA).
 template <int kKv>
-int grid_warps_of(bool ws) {
-    if constexpr (kKv == FKV_KV_FP4)
-        return ws ? 0 : device_sm_count() * ctas_per_sm<kKv, false>() * Cfg<kKv>::kWarps;
-    else
-        return device_sm_count() * (ws ? ctas_per_sm<kKv, true>() : ctas_per_sm<kKv, false>());
+int grid_warps_of(bool var) {
+    return device_sm_count() * (var ? ctas_per_sm<kKv, true>() : ctas_per_sm<kKv, false>()) * Cfg<kKv>::kWarps;
 }
-int grid_warps(int kv, bool ws) {
-    return kv == FKV_KV_FP8_E4M3 ? grid_warps_of<FKV_KV_FP8_E4M3>(ws)
-           : kv == FKV_KV_BF16   ? grid_warps_of<FKV_KV_BF16>(ws)
-                                 : grid_warps_of<FKV_KV_FP4>(ws);
+int grid_warps(int kv, bool var) {
+    return kv == FKV_KV_FP8_E4M3 ? grid_warps_of<FKV_KV_FP8_E4M3>(var)
+           : kv == FKV_KV_BF16   ? grid_warps_of<FKV_KV_BF16>(var)
+                                 : grid_warps_of<FKV_KV_FP4>(var);
 }
 
 int tile_tokens(int kv) {
@@ -1666,22 +1725,31 @@ bool known_kv(int kv) { return kv == FKV_KV_FP8_E4M3 || kv == FKV_KV_BF16 || kv 
 #define FKV_WS_PAGE_LIMIT 64
 #endif
 bool use_ws(int page_size, int kv) {
-    if (kv == FKV_KV_FP4) return false;      // its untiled copies go out one per lane
     const int tile = tile_tokens(kv);
     return page_size < (FKV_WS_PAGE_LIMIT < tile ? FKV_WS_PAGE_LIMIT : tile);
 }
 
+// Tiles from which a 4-bit call is a large one, counted over the pages that the
+// page table lists (the lengths are on the device).  Requests of 8192 tokens, 64
+// query / 8 KV heads, small-call against large-call instance: 32 of them (33
+// thousand tiles) 65.9 and 67.3 us, 48 91.0 and 92.3, 64 116.9 and 116.5, 96 168.5
+// and 162.2; one request of 7168 tokens 17.7 and 21.2.
+#ifndef FKV_FP4_LARGE_TILES
+#define FKV_FP4_LARGE_TILES 60000
+#endif
+bool large_fp4_call(int64_t nnz, int page_size, int units_per_request) {
+    return nnz > static_cast<int64_t>(FKV_FP4_LARGE_TILES) * FKV_FP4_TILE / page_size / units_per_request;
+}
+
 template <int kKv>
-cudaError_t launch_attn(bool two_warp, bool aligned, dim3 grid, cudaStream_t st, const AttnParams &p, const CUtensorMap &tmK,
+cudaError_t launch_attn(bool var, bool aligned, dim3 grid, cudaStream_t st, const AttnParams &p, const CUtensorMap &tmK,
                         const CUtensorMap &tmV) {
-    auto go = [&](auto kern, bool ws) {
-        return launch_pdl(kern, grid, dim3(attn_threads<kKv>(ws)), Layout<kKv>::kSmem, st, p, tmK, tmV);
+    auto go = [&](auto kern) {
+        return launch_pdl(kern, grid, dim3(attn_threads<kKv>(var)), Layout<kKv>::kSmem, st, p, tmK, tmV);
     };
-    if constexpr (kKv != FKV_KV_FP4) if (two_warp)
-        return aligned ? go(paged_decode_attn_kernel<kKv, true, true>, true)
-                       : go(paged_decode_attn_kernel<kKv, true, false>, true);
-    return aligned ? go(paged_decode_attn_kernel<kKv, false, true>, false)
-                   : go(paged_decode_attn_kernel<kKv, false, false>, false);
+    if (var)
+        return aligned ? go(paged_decode_attn_kernel<kKv, true, true>) : go(paged_decode_attn_kernel<kKv, true, false>);
+    return aligned ? go(paged_decode_attn_kernel<kKv, false, true>) : go(paged_decode_attn_kernel<kKv, false, false>);
 }
 
 size_t align256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
@@ -1740,10 +1808,10 @@ extern "C" size_t paged_decode_attn_workspace_size(int32_t batch, int32_t num_q_
     if (head_dim != kD || !known_kv(kv_dtype)) return 0;
     const int R = group_split(num_q_heads / num_kv_heads);
     if (R == 0) return 0;
-    // sized for either CTA shape (the page size is not known here)
+    // sized for either variant (neither the page size nor the call's is known here)
     const int n1 = grid_warps(kv_dtype, false), n2 = grid_warps(kv_dtype, true);
     const int NW = n1 > n2 ? n1 : n2;
-    if (n1 <= 0 || (n2 <= 0 && kv_dtype != FKV_KV_FP4)) return 0;
+    if (n1 <= 0 || n2 <= 0) return 0;
     return ws_layout(batch, num_kv_heads * R, num_q_heads / num_kv_heads / R, NW).total;
 }
 
@@ -1772,8 +1840,8 @@ extern "C" fkv_status paged_decode_attn(const void *q, int32_t batch, int32_t nu
     if (!aligned16(q) || !aligned16(k_cache) || !aligned16(v_cache) || !aligned16(out) ||
         (reinterpret_cast<uintptr_t>(workspace) & 255u))
         return FKV_ERR_INVALID_ARG;
-    const bool two_warp = use_ws(page_size, kv_dtype);
-    const int NW = grid_warps(kv_dtype, two_warp);
+    const bool var = kv_dtype == FKV_KV_FP4 ? large_fp4_call(nnz, page_size, Hv) : use_ws(page_size, kv_dtype);
+    const int NW = grid_warps(kv_dtype, var);
     uint32_t *err = device_error_word();
     if (NW <= 0 || !err) return FKV_ERR_CUDA;
     const WsLayout wl = ws_layout(batch, Hv, G, NW);
@@ -1830,11 +1898,11 @@ extern "C" fkv_status paged_decode_attn(const void *q, int32_t batch, int32_t nu
     const bool aligned = FKV_ALIGNED_SCHEDULE && batch <= 64;
     const dim3 grid(kv_dtype == FKV_KV_FP4 ? NW / Cfg<FKV_KV_FP4>::kWarps : NW);
     if (fp8)
-        e = launch_attn<FKV_KV_FP8_E4M3>(two_warp, aligned, grid, st, p, tmK, tmV);
+        e = launch_attn<FKV_KV_FP8_E4M3>(var, aligned, grid, st, p, tmK, tmV);
     else if (kv_dtype == FKV_KV_BF16)
-        e = launch_attn<FKV_KV_BF16>(two_warp, aligned, grid, st, p, tmK, tmV);
+        e = launch_attn<FKV_KV_BF16>(var, aligned, grid, st, p, tmK, tmV);
     else
-        e = launch_attn<FKV_KV_FP4>(two_warp, aligned, grid, st, p, tmK, tmV);
+        e = launch_attn<FKV_KV_FP4>(var, aligned, grid, st, p, tmK, tmV);
     if (e != cudaSuccess) return FKV_ERR_CUDA;
     return FKV_OK;
 }

@@ -172,12 +172,19 @@ class Fp4Case:
         self.q = W.bf16_bits((q_std * rng.standard_normal((B, Hq, D))).astype(np.float32))
         self.sm = 1.0 / np.sqrt(D)
 
-    def gpu(self, seq=None, indices=None, mask=None, noalloc=False, indptr=None):
+    def gpu(self, seq=None, indices=None, mask=None, noalloc=False, indptr=None, large=False):
+        """large: a page table with room for so many pages that the call takes
+        the kernel's large-call instance (60000 tiles of 64 tokens and more)."""
         import torch
         import fp8_paged_kv_decode_gb300 as fkv
         out = torch.full((self.B, self.Hq, D), float("nan"), dtype=torch.bfloat16, device="cuda")
+        indices = self.indices if indices is None else indices
+        if large:
+            R = next(r for r in (1, 2, 4, 8) if (self.Hq // self.H) % r == 0 and self.Hq // self.H // r <= 8)
+            room = 60000 * 64 // (self.S * self.H * R) + 2
+            indices = np.concatenate([indices, np.zeros(max(0, room - len(indices)), np.int32)])
         args = [dev(self.q, dtype=torch.bfloat16), dev(self.kc), dev(self.vc), dev(self.indptr if indptr is None else indptr),
-                dev(self.indices if indices is None else indices), dev(self.seq if seq is None else np.asarray(seq, np.int32)), self.sm, out]
+                dev(indices), dev(self.seq if seq is None else np.asarray(seq, np.int32)), self.sm, out]
         kw = dict(k_scale=dev(self.ks), v_scale=dev(self.vs), abort_mask=None if mask is None else dev(np.asarray(mask, np.uint8)))
         if noalloc:
             fkv.paged_decode_attn_noalloc(*args, **kw)
@@ -199,25 +206,28 @@ class Fp4Case:
         assert (err[sel] <= tol[sel]).all(), (float((err - tol)[sel].max()), np.argwhere(err > tol)[:4])
 
 
+@pytest.mark.parametrize("large", [False, True])
 @pytest.mark.parametrize("B,Hq,H,S,seq", [
     (1, 1, 1, 16, [1]), (1, 8, 1, 64, [2]), (3, 6, 2, 16, [1, 15, 16]), (4, 16, 4, 32, [31, 32, 33, 64]),
     (5, 40, 8, 64, [63, 64, 65, 127, 129]), (2, 14, 2, 128, [1, 300]), (3, 8, 8, 128, [64, 65, 1000]),
     (2, 20, 2, 16, [700, 45]), (2, 64, 2, 64, [500, 90]), (1, 12, 4, 32, [9000]), (1, 4, 1, 16, [20000]),
     (64, 8, 2, 16, list(range(1, 65))), (65, 8, 2, 64, list(range(1, 650, 10))), (130, 4, 1, 32, list(range(1, 1301, 10))),
     (300, 2, 1, 16, [7 * (i % 40) + 1 for i in range(300)])])
-def test_attention(B, Hq, H, S, seq):
+def test_attention(B, Hq, H, S, seq, large):
     c = Fp4Case(B, Hq, H, S, seq, seed=B * 100 + Hq + S)
-    c.check(c.gpu())
+    c.check(c.gpu(large=large))
 
 
+@pytest.mark.parametrize("large", [False, True])
 @pytest.mark.parametrize("S", [16, 64, 128])
-def test_attention_peaky_softmax(S):
+def test_attention_peaky_softmax(S, large):
     c = Fp4Case(3, 8, 2, S, [200, 1, 777], seed=9, q_std=8.0)
-    c.check(c.gpu())
+    c.check(c.gpu(large=large))
 
 
+@pytest.mark.parametrize("large", [False, True])
 @pytest.mark.parametrize("S", [16, 64])
-def test_attention_fail_closed(S):
+def test_attention_fail_closed(S, large):
     import fp8_paged_kv_decode_gb300 as fkv
     c = Fp4Case(6, 8, 2, S, [100, 200, 50, 300, 80, 130], seed=11)
     seq = c.seq.copy()
@@ -225,13 +235,13 @@ def test_attention_fail_closed(S):
     seq[4] = 10 ** 6                                            # more tokens than its pages hold
     dead = [0, 1, 1, 0, 1, 0]
     fkv.device_error()
-    out = c.gpu(seq=seq, mask=[0, 1, 0, 0, 0, 0])
+    out = c.gpu(seq=seq, mask=[0, 1, 0, 0, 0, 0], large=large)
     c.check(out, seq=np.where(np.array(dead) > 0, 0, c.seq), dead=dead)
     assert (out.float().cpu().numpy()[np.array(dead) > 0] == 0).all() and fkv.device_error() == 0
     idx = c.indices.copy()
     idx[c.indptr[3] + 1] = c.P
     idx[c.indptr[5]] = -1
-    out = c.gpu(indices=idx)
+    out = c.gpu(indices=idx, large=large)
     assert fkv.device_error() == fkv.DEVERR_ATTN_PAGE
     got = out.float().cpu().numpy()
     assert (got[[3, 5]] == 0).all()
@@ -250,19 +260,30 @@ def test_attention_nan_block_reaches_its_dims_only():
     assert np.array_equal(bad, want)
 
 
+@pytest.mark.parametrize("large", [False, True])
 @pytest.mark.parametrize("B,S,seq", [(3, 16, [900, 5000, 64]), (40, 64, [64 * i + 3 for i in range(40)]), (140, 32, [300] * 140)])
-def test_attention_repeats_byte_for_byte(B, S, seq):
+def test_attention_repeats_byte_for_byte(B, S, seq, large):
     import torch
     c = Fp4Case(B, 16, 2, S, seq, seed=13)
-    first = c.gpu()
+    first = c.gpu(large=large)
     for _ in range(4):
-        assert torch.equal(first.view(torch.int16), c.gpu().view(torch.int16))
+        assert torch.equal(first.view(torch.int16), c.gpu(large=large).view(torch.int16))
 
 
 def test_attention_noalloc_is_the_same_call():
     import torch
     c = Fp4Case(5, 16, 4, 32, [10, 2000, 333, 64, 65], seed=14)
-    assert torch.equal(c.gpu().view(torch.int16), c.gpu(noalloc=True).view(torch.int16))
+    for large in (False, True):
+        assert torch.equal(c.gpu(large=large).view(torch.int16), c.gpu(noalloc=True, large=large).view(torch.int16))
+
+
+@pytest.mark.parametrize("B,Hq,H,S,seq", [(9, 32, 4, 64, [20000, 50000, 1, 33, 5000, 21000, 64, 9000, 12345]),
+                                          (66, 16, 4, 16, [2049] * 66), (3, 16, 2, 128, [90000, 129, 40001])])
+def test_attention_long(B, Hq, H, S, seq):
+    """Units over hundreds of warps, and warps over many units, in both instances."""
+    c = Fp4Case(B, Hq, H, S, seq, seed=B)
+    for large in (False, True):
+        c.check(c.gpu(large=large))
 
 
 def test_attention_shared_pages():
