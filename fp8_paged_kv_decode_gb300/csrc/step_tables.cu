@@ -43,6 +43,7 @@ struct StepParams {
     uint32_t page;
     int32_t page_shift;       // log2 of the page size, -1 if it is not a power of two
     bool wide;                // the entry and token arrays are 16-byte aligned
+    int32_t token_run;        // tokens of a thread's run: kRun, or 1 where requests have few each
 };
 
 // Pages that hold so many tokens (below 2^31).
@@ -180,9 +181,48 @@ __device__ __forceinline__ int32_t page_at(const StepParams &p, const StepRecord
     return id;
 }
 
-// A thread's run of kRun neighbouring entries i .. of [0, end): the request of
-// the first by search, then onwards.
+// A thread's run of neighbouring entries: the request of the first by search,
+// then onwards.  The following request's record is loaded with the first one's,
+// so a run that passes one border waits for nothing more.
 constexpr int kRun = 4;
+struct Walk {
+    int r;
+    int32_t first, next, next2;       // the request's entries are [first, next), its successor's [next, next2)
+    StepRecord rec, rec2;
+};
+__device__ __forceinline__ Walk walk_from(const StepParams &p, const int32_t *indptr, int32_t i) {
+    Walk w;
+    w.r = find_row(indptr, p.batch, i);
+    const int r2 = min(w.r + 1, p.batch - 1);
+    w.first = __ldg(indptr + w.r);
+    w.next = __ldg(indptr + w.r + 1);
+    w.next2 = __ldg(indptr + r2 + 1);
+    w.rec = load_record(p, w.r);
+    w.rec2 = load_record(p, r2);
+    return w;
+}
+// On to the request of entry i >= w.next.
+__device__ __forceinline__ void walk_on(const StepParams &p, const int32_t *indptr, Walk &w, int32_t i) {
+    ++w.r;
+    w.first = w.next;
+    w.next = w.next2;
+    w.rec = w.rec2;
+    if (i < w.next) {                                          // the successor's successor, should the run reach it
+        const int r2 = min(w.r + 1, p.batch - 1);
+        w.next2 = __ldg(indptr + r2 + 1);
+        w.rec2 = load_record(p, r2);
+        return;
+    }
+    do {                                                       // requests without entries are passed over
+        ++w.r;
+        w.first = w.next;
+        w.next = __ldg(indptr + w.r + 1);
+    } while (i >= w.next);
+    const int r2 = min(w.r + 1, p.batch - 1);
+    w.rec = load_record(p, w.r);
+    w.next2 = __ldg(indptr + r2 + 1);
+    w.rec2 = load_record(p, r2);
+}
 
 __global__ void __launch_bounds__(kFillThreads)
 step_fill_kernel(const StepParams p) {
@@ -190,16 +230,14 @@ step_fill_kernel(const StepParams p) {
     grid_dep_launch();
     const int32_t rows = __ldg(p.page_indptr + p.batch), toks = __ldg(p.token_indptr + p.batch);
     const uint32_t row_runs = (static_cast<uint32_t>(rows) + kRun - 1) / kRun;
-    const uint32_t tok_runs = (static_cast<uint32_t>(p.n_tokens) + kRun - 1) / kRun;
+    const uint32_t tok_runs = (static_cast<uint32_t>(p.n_tokens) + p.token_run - 1) / p.token_run;
     const uint32_t stride = gridDim.x * kFillThreads;
     // runs of page-table entries first, then runs of tokens
     for (uint64_t run = blockIdx.x * kFillThreads + threadIdx.x; run < static_cast<uint64_t>(row_runs) + tok_runs;
          run += stride) {
         if (run < row_runs) {
             const int32_t j0 = static_cast<int32_t>(run) * kRun, m = min(kRun, rows - j0);
-            int r = find_row(p.page_indptr, p.batch, j0);
-            int32_t first = __ldg(p.page_indptr + r), next = __ldg(p.page_indptr + r + 1);
-            StepRecord rec = load_record(p, r);
+            Walk w = walk_from(p, p.page_indptr, j0);
             int32_t id[kRun];
             uint32_t tag[kRun];
             int64_t cell[kRun];
@@ -211,19 +249,12 @@ step_fill_kernel(const StepParams p) {
                 tag[e] = 0;
                 fresh[e] = false;
                 if (e >= m) continue;
-                if (j >= next) {
-                    do {                                       // requests without entries are passed over
-                        ++r;
-                        first = next;
-                        next = __ldg(p.page_indptr + r + 1);
-                    } while (j >= next);
-                    rec = load_record(p, r);
-                }
-                const int32_t col = j - first;
-                cell[e] = static_cast<int64_t>(r) * p.max_blocks + col;
-                id[e] = page_at(p, rec, r, col);
-                fresh[e] = col >= rec.have && (rec.flags & kGranted);
-                if (col < rec.have) tag[e] = __ldg(p.table_tags + cell[e]);
+                if (j >= w.next) walk_on(p, p.page_indptr, w, j);
+                const int32_t col = j - w.first;
+                cell[e] = static_cast<int64_t>(w.r) * p.max_blocks + col;
+                id[e] = page_at(p, w.rec, w.r, col);
+                fresh[e] = col >= w.rec.have && (w.rec.flags & kGranted);
+                if (col < w.rec.have) tag[e] = __ldg(p.table_tags + cell[e]);
                 else if (id[e] >= 0) tag[e] = __ldg(p.page_tags + id[e]);
             }
 #pragma unroll
@@ -245,35 +276,28 @@ step_fill_kernel(const StepParams p) {
             }
         } else {
             const uint32_t run_t = static_cast<uint32_t>(run - row_runs);
-            const int32_t i0 = static_cast<int32_t>(run_t) * kRun, m = min(kRun, p.n_tokens - i0);
+            const int32_t i0 = static_cast<int32_t>(run_t) * p.token_run, m = min(p.token_run, p.n_tokens - i0);
             int64_t slot[kRun] = {-1, -1, -1, -1};
             int32_t pos[kRun] = {0, 0, 0, 0};
             if (i0 < toks) {
-                int r = find_row(p.token_indptr, p.batch, i0);
-                int32_t first = __ldg(p.token_indptr + r), next = __ldg(p.token_indptr + r + 1);
-                StepRecord rec = load_record(p, r);
+                Walk w = walk_from(p, p.token_indptr, i0);
                 int32_t col_at = -1, id = -1;                  // the page looked up last
 #pragma unroll
                 for (int e = 0; e < kRun; ++e) {
                     const int32_t i = i0 + e;
-                    if (i >= toks) continue;
-                    if (i >= next) {
-                        do {
-                            ++r;
-                            first = next;
-                            next = __ldg(p.token_indptr + r + 1);
-                        } while (i >= next);
-                        rec = load_record(p, r);
+                    if (e >= m || i >= toks) continue;
+                    if (i >= w.next) {
+                        walk_on(p, p.token_indptr, w, i);
                         col_at = -1;
                     }
-                    if (!(rec.flags & kListed)) continue;
-                    pos[e] = rec.cached + (i - first);
-                    if (!(rec.flags & kGranted)) continue;
+                    if (!(w.rec.flags & kListed)) continue;
+                    pos[e] = w.rec.cached + (i - w.first);
+                    if (!(w.rec.flags & kGranted)) continue;
                     const uint32_t at = static_cast<uint32_t>(pos[e]);
                     const uint32_t col = p.page_shift >= 0 ? at >> p.page_shift : at / p.page;
                     if (static_cast<int32_t>(col) != col_at) {
                         col_at = static_cast<int32_t>(col);
-                        id = page_at(p, rec, r, col_at);
+                        id = page_at(p, w.rec, w.r, col_at);
                     }
                     if (id >= 0) slot[e] = static_cast<int64_t>(id) * p.page + (at - col * p.page);
                 }
@@ -331,14 +355,16 @@ extern "C" fkv_status kv_step_tables(const int32_t *cached_lens, const int32_t *
     if (!err || sms <= 0) return FKV_ERR_CUDA;
     const uint32_t page = static_cast<uint32_t>(page_size);
     const bool wide = aligned16(page_indices) && aligned16(expected_tags) && aligned16(slot_mapping) && aligned16(positions);
+    // A decode step's tokens are each a request of their own: one to a thread.
+    const int32_t token_run = n_tokens <= kRun * static_cast<int64_t>(batch) ? 1 : kRun;
     const StepParams p{cached_lens, new_lens, block_table, block_tags, free_pages, free_count, page_tags, step_lens,
                        cached_lens_out, refused, page_indptr, page_indices, expected_tags, token_indptr, slot_mapping,
                        positions, free_left, static_cast<StepRecord *>(workspace), err, batch, max_blocks, num_free,
-                       num_pages, nnz, n_tokens, page, (page & (page - 1)) ? -1 : __builtin_ctz(page), wide};
+                       num_pages, nnz, n_tokens, page, (page & (page - 1)) ? -1 : __builtin_ctz(page), wide, token_run};
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     const unsigned scan = batch >= kTabThreads ? kTabThreads : batch <= 32 ? 32u : (static_cast<unsigned>(batch) + 31u) & ~31u;
     if (launch_pdl(step_plan_kernel, dim3(1), dim3(scan), 0, st, p) != cudaSuccess) return FKV_ERR_CUDA;
-    const int64_t runs = (static_cast<int64_t>(nnz) + kRun - 1) / kRun + (static_cast<int64_t>(n_tokens) + kRun - 1) / kRun;
+    const int64_t runs = (static_cast<int64_t>(nnz) + kRun - 1) / kRun + (static_cast<int64_t>(n_tokens) + token_run - 1) / token_run;
     int64_t blocks = (runs + kFillThreads - 1) / kFillThreads;
     if (blocks > 8 * sms) blocks = 8 * sms;
     if (blocks == 0) return FKV_OK;
