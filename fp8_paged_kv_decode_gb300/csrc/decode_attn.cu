@@ -1473,6 +1473,24 @@ paged_decode_attn_kernel(const AttnParams p, const __grid_constant__ CUtensorMap
         }
         float pr[MT][4];
         float ls[2] = {0.f, 0.f};
+        if constexpr (kFp4) {
+            // the same operations on the two columns at once (packed, each lane
+            // rounding as the scalar instruction does)
+            const uint64_t cf = pack2(cfac[0], cfac[1]), nm = pack2(-m[0], -m[1]);
+            uint64_t sum = pack2(0.f, 0.f);
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+                for (int c = 0; c < 4; c += 2) {
+                    const float2 z = unpack2(add2(mul2(pack2(sacc[mt][c], sacc[mt][c + 1]), cf), nm));
+                    pr[mt][c] = ex2(z.x);
+                    pr[mt][c + 1] = ex2(z.y);
+                    sum = add2(sum, pack2(pr[mt][c], pr[mt][c + 1]));
+                }
+            const float2 s2 = unpack2(sum);
+            ls[0] = s2.x;
+            ls[1] = s2.y;
+        } else {
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
@@ -1480,6 +1498,7 @@ paged_decode_attn_kernel(const AttnParams p, const __grid_constant__ CUtensorMap
                 pr[mt][c] = ex2(__fmul_rn(sacc[mt][c], cfac[c & 1]) - m[c & 1]);
                 ls[c & 1] += pr[mt][c];
             }
+        }
         l[0] = l[0] * alpha[0] + ls[0];
         l[1] = l[1] * alpha[1] + ls[1];
         // (the 4-bit kernel, nearer its issue limit, skips the products by 1 once
@@ -1834,6 +1853,9 @@ extern "C" fkv_status paged_decode_attn(const void *q, int32_t batch, int32_t nu
     if (!(sm_scale > 0.f) || !std::isfinite(sm_scale)) return FKV_ERR_INVALID_ARG;
     if (batch == 0) return FKV_OK;
     const bool fp8 = kv_dtype == FKV_KV_FP8_E4M3;
+    // a page's rows are counted in 32 bits by the 4-bit copies
+    if (kv_dtype == FKV_KV_FP4 && static_cast<int64_t>(num_kv_heads) * page_size * FKV_FP4_ROW_BYTES > 0x7FFFFFFF)
+        return FKV_ERR_UNSUPPORTED;
     if (!q || !k_cache || !v_cache || !page_indptr || !seq_lens || !out || !workspace) return FKV_ERR_INVALID_ARG;
     if (nnz > 0 && !page_indices) return FKV_ERR_INVALID_ARG;
     if (kv_dtype != FKV_KV_BF16 && (!k_scale || !v_scale)) return FKV_ERR_INVALID_ARG;

@@ -44,6 +44,28 @@ __device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
     return d;
 }
 
+// Two fp32 lanes in one register pair.
+__device__ __forceinline__ uint64_t pack2(float x, float y) {
+    uint64_t d;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "r"(__float_as_uint(x)), "r"(__float_as_uint(y)));
+    return d;
+}
+__device__ __forceinline__ float2 unpack2(uint64_t v) {
+    uint32_t x, y;
+    asm("mov.b64 {%0, %1}, %2;" : "=r"(x), "=r"(y) : "l"(v));
+    return make_float2(__uint_as_float(x), __uint_as_float(y));
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+    uint64_t d;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+    uint64_t d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+
 // One scale byte as an f16 pair (s, s).
 __device__ __forceinline__ uint32_t e4m3_to_f16_pair(uint32_t byte) {
     return e4m3x2_to_f16x2(static_cast<uint16_t>(prmt(byte, 0u, 0x4400u)));

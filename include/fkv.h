@@ -138,7 +138,8 @@ FKV_API fkv_status kv_append_bf16(const void *k_new, const void *v_new,
  * a block's s is then at most 74.7, so values up to six times the calibrated
  * maximum are still held without saturation.  An infinity saturates (its
  * block takes s = 448); a NaN makes its block's scale, and so its 16 values,
- * NaN.
+ * NaN.  A slot listed twice in one call ends with codes and scales of either
+ * token, block by block; num_kv_heads is at most 32767.
  */
 FKV_API fkv_status kv_append_fp4(const void *k_new, const void *v_new,
                          const int64_t *slot_mapping, int32_t n_tokens,
@@ -161,7 +162,7 @@ FKV_API fkv_status kv_append_fp4(const void *k_new, const void *v_new,
  *   k_scale, v_scale  fp32 [num_kv_heads]; ignored (may be NULL) for BF16
  *   slots          int64 [n_tokens], repeats allowed
  *   k_out, v_out   bf16 [n_tokens][num_kv_heads][head_dim], 16-byte aligned
- * n_tokens == 0 is a no-op.
+ * num_kv_heads is at most 32767.  n_tokens == 0 is a no-op.
  */
 FKV_API fkv_status kv_gather(const void *k_cache, const void *v_cache, int32_t kv_dtype,
                              const float *k_scale, const float *v_scale,
@@ -430,7 +431,10 @@ FKV_API size_t paged_decode_attn_workspace_size(int32_t batch, int32_t num_q_hea
  * written as zeros whatever those bytes hold (FKV_DEVERR_ATTN_PAGE is set).
  * Deterministic: the same call gives the same bytes every time (the split
  * over warps depends only on the live requests, and the merge of a split
- * (request, KV head) does not depend on which warp performs it or when).
+ * (request, KV head) does not depend on which warp performs it or when).  The
+ * 4-bit cache's split also depends on nnz: from 60000 tiles' worth of listed
+ * pages on (a tile is 64 tokens of one KV head) a call is spread over more
+ * warps, so the same rows under a longer page table may differ by rounding.
  * Supported: head_dim 128, page_size in {16, 32, 64, 128}, group size
  * G = num_q_heads / num_kv_heads in 1..8, or above 8 when G splits into R
  * equal groups of at most 8 with R a power of two up to 8 (10, 12, 16, 24,

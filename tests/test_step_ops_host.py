@@ -153,6 +153,9 @@ def test_attention_knows_the_format(lib):
     P = ctypes.c_void_p
     args = [None, 2, 8, None, None, 2, None, None, 4, 2, 16, 128, None, None, 0, None, None, 0.1, None, None, 0, P(0)]
     assert lib.paged_decode_attn(*args) == 1                   # FP4: null pointers
+    args[8:11] = [4, 300000, 128]
+    args[2] = 300000
+    assert lib.paged_decode_attn(*args) == 2                   # a page of 300000 heads' rows
     args[5] = 3
     assert lib.paged_decode_attn(*args) == 1                   # no such format
     assert lib.paged_decode_attn_workspace_size(2, 8, 2, 128, 3) == 0
