@@ -1,4 +1,4 @@
-// decode_attn.cu -- paged decode attention over an FP8 e4m3 (or BF16) cache.
+// decode_attn.cu -- paged decode attention over an FP8 e4m3, BF16 or 4-bit cache.
 //
 // What is computed: for each request r and query head i (KV head h = i / G)
 //     out[r][i] = sum_t softmax_t(sm_scale * q[r][i] . k_t) v_t
@@ -41,6 +41,26 @@
 //     do not depend on which warp merges it or when.  Rows of requests with
 //     no tiles (aborted, empty, malformed) are zero-filled by the warps, one
 //     request each.
+//
+// The 4-bit cache (rows of fp4_row.cuh).  A tile is 9.2 KB of K and V instead of
+// FP8's 16.4 KB, while its arithmetic is the same and a multiply per value for the
+// block scales comes on top, so this kernel is bound by issue, not by memory:
+// at the copy bandwidth a scheduler has about 1700 cycles for a tile, and the
+// conversions (256 e2m1 pairs, 2 cycles each), the scale products (beside them)
+// and 64 MMAs (8 cycles each, during which little else issues) take 1070 of
+// them before anything else.  Measured apart on 64 requests around 16k tokens:
+// copies alone 208 us, arithmetic alone 237, together 234 in the kernel as it is.
+// What it does for that:
+//  - tiles come as untiled bulk copies of whole rows (codes and scales lie
+//    together), one per page and pool, issued by different lanes, and cut to the
+//    rows in use: no tensor maps, no producer warp (270 -> 256 us);
+//  - V's nibbles are interleaved over two tokens before they are converted, two
+//    operations for four dims, instead of converting dim pairs and doubling the
+//    MMAs against half-empty operands (281 -> 270 us);
+//  - conversions for the next MMA group are issued before the current one's MMAs;
+//  - small calls run eight warps per SM with all the registers they want, large
+//    ones twelve in 160 registers (255 -> 236 us; see large_fp4_call), the
+//    softmax in packed two-lane arithmetic (236 -> 234 us).
 #include <cudaTypedefs.h>
 
 #include <cmath>

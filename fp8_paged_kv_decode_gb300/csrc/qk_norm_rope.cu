@@ -13,7 +13,11 @@
 // coefficients once per token:
 //   a' = rs (a wa cos - b wb sin),   b' = rs (b wb cos + a wa sin)
 // and a row costs its sum of squares, 12 products and the conversions.  Each
-// half-warp has four rows' loads in flight before it works on the first.
+// half-warp has four rows' loads in flight and asks for the next batch's row as
+// soon as it has unpacked one.  16411 tokens of 36 heads (302 MB): 118 us with a
+// block per token that formed cos and sin before its loads, 54 with a warp per
+// token, 51 with the rows asked for ahead, eight resident blocks and streaming
+// stores (5.9 TB/s); 64 tokens of 72 heads: 3.4, 2.7 and 2.7 us.
 #include <cmath>
 
 #include "fkv_common.cuh"

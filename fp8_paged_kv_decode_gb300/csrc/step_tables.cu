@@ -9,7 +9,10 @@
 // records, so the length and free-count outputs may be the inputs' own arrays.
 // Bytes: 16 per page-table entry (id and tag, in and out) and 12 per token; both
 // launches are bound by latency: the scan's two block-wide steps, and the
-// fill's chain of search, record, page id, tag.
+// fill's chain of search, record, page id, tag.  64 requests (20 thousand
+// entries) take 6.4 us, one request 4.7, 256 prompt chunks (524 thousand tokens)
+// 8.7; one launch of a cluster of eight blocks that scan for themselves took 6.8,
+// 4.8 and 33.6 us, and 9.1 against 6.0 on 64 requests of 1024 pages each.
 #include "fkv_common.cuh"
 
 namespace fkv {
