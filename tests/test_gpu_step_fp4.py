@@ -154,3 +154,45 @@ def test_on_a_side_stream():
     fkv.kv_gather(s.kc, s.vc, s.slots, ko, vo, k_scale=s.kst, v_scale=s.vst, stream=st)
     st.synchronize()
     assert torch.isfinite(vo).all() and vo.abs().amax() > 1
+
+
+def test_empty_calls():
+    """No tokens, no requests: nothing is launched that could touch anything."""
+    import torch
+    import fp8_paged_kv_decode_gb300 as fkv
+    z = lambda *s, dt=torch.bfloat16: torch.zeros(*s, dtype=dt, device="cuda")   # noqa: E731
+    kc, sc, none = z(2, 2, 16, ROW, dt=torch.uint8), z(2, dt=torch.float32) + 1, z(0, dt=torch.int64)
+    fkv.kv_append_fp4(z(0, 2, D), z(0, 2, D), none, sc, sc, kc, kc.clone())
+    fkv.kv_gather(kc, kc.clone(), none, z(0, 2, D), z(0, 2, D), k_scale=sc, v_scale=sc)
+    ptr = z(1, dt=torch.int32)
+    fkv.kv_append_fp4_tag_check(z(0, 2, D), z(0, 2, D), none, sc, sc, kc, kc.clone(), z(2, dt=torch.int32), ptr, z(0, dt=torch.int32), z(0, dt=torch.int32),
+                                z(0, dt=torch.uint8))
+    fkv.paged_decode_attn(z(0, 8, D), kc, kc.clone(), ptr, z(0, dt=torch.int32), z(0, dt=torch.int32), 0.1, z(0, 8, D), fkv.alloc_workspace(0, 8, 2, fkv.KV_FP4),
+                          k_scale=sc, v_scale=sc)
+    torch.cuda.synchronize()
+    assert (kc == 0).all()
+
+
+def test_two_layers_on_two_streams():
+    """Two layers' norms, appends and attention at once, a workspace each: the same bytes as one after the other."""
+    import torch
+    import fp8_paged_kv_decode_gb300 as fkv
+    a, b = (Step(9, 16, 4, 64, blocks=6, pool=54, nnz=54, seed=7) for _ in range(2))
+    for s in (a, b):
+        s.new.copy_(dev(np.arange(9, dtype=np.int32) * 30 + 1))
+        s.buffers(int((np.arange(9) * 30 + 1).sum()))
+        s.fill()
+        s.calls(attend=False)
+        s.new.fill_(1)
+        s.buffers(9)
+        s.fill()
+    torch.cuda.synchronize()
+    x, y = torch.cuda.Stream(), torch.cuda.Stream()
+    with torch.cuda.stream(x):
+        a.calls(attend=True)
+    with torch.cuda.stream(y):
+        b.calls(attend=True)
+    torch.cuda.synchronize()
+    assert torch.equal(a.out.view(torch.int16), b.out.view(torch.int16)) and torch.equal(a.kc, b.kc)
+    a.check()
+    assert fkv.device_error() == 0
