@@ -142,6 +142,13 @@ constexpr uint32_t kFull = 0xffffffffu;
 #endif
 constexpr int kNone = 0, kFinalDue = 1, kChunkDue = 2, kSecondDue = 3;   // merge duties of a warp
 constexpr int kChunk = FKV_MERGE_CHUNK;  // parts merged per first-level merge of a long unit
+// The same for the 4-bit cache, whose units span more warps (16 requests of 8192
+// tokens, eleven parts a unit: 44.2 us with 9, 40.0 with 12 or 16; one of 7168
+// tokens 16.9, 16.2 and 17.4; 33 ragged requests in a whole step 47.2, 47.8 and
+// 49.5; the others alike).
+#ifndef FKV_FP4_MERGE_CHUNK
+#define FKV_FP4_MERGE_CHUNK 12
+#endif
 constexpr int kMinTilesPerWarp = FKV_MIN_TILES_PER_WARP;   // small batches use fewer, longer warp ranges
 constexpr int kMinAlignedTiles = FKV_ALIGNED_MIN_TILES;
 // Batches of up to this many requests are scheduled by the attention warps
@@ -444,13 +451,14 @@ __device__ __forceinline__ int64_t scan_requests(const RequestInfo &ri, int b, i
 }
 
 // Where the parts of a split unit sit: its first warp and how many warps it
-// spans.  A unit over more than kChunk warps merges in chunks of kChunk
-// consecutive parts; c0 is the first part of warp w's chunk.
+// spans.  A unit over more than kC warps merges in chunks of kC consecutive
+// parts; c0 is the first part of warp w's chunk.
+template <int kC>
 struct UnitGeom {
     int wf, span;
-    __device__ int c0(int w) const { return ((w - wf) / kChunk) * kChunk; }
-    __device__ int csz(int w) const { return min(kChunk, span - c0(w)); }
-    __device__ int nch() const { return (span + kChunk - 1) / kChunk; }
+    __device__ int c0(int w) const { return ((w - wf) / kC) * kC; }
+    __device__ int csz(int w) const { return min(kC, span - c0(w)); }
+    __device__ int nch() const { return (span + kC - 1) / kC; }
 };
 
 // Schedule of a small batch (up to 64 requests, each lane holding two
@@ -467,9 +475,9 @@ struct UnitGeom {
 // others.  Past the test every count fits in 32 bits.  Warp w
 // gets tiles [lo, hi) (empty past the last unit's warps), the request holding
 // them, and its unit's warps.
-template <int kTile>
+template <int kTile, typename Geom>
 __device__ __forceinline__ bool place_aligned(const RequestInfo (&rc)[2], int64_t T, int NW, int Hkv, int w,
-                                              int64_t &lo, int64_t &hi, FirstRequest &fr, UnitGeom &gm) {
+                                              int64_t &lo, int64_t &hi, FirstRequest &fr, Geom &gm) {
     const int lane = threadIdx.x & 31;
     int live = (rc[0].tiles > 0) + (rc[1].tiles > 0);
 #pragma unroll
@@ -714,6 +722,8 @@ paged_decode_attn_kernel(const AttnParams p, const __grid_constant__ CUtensorMap
     constexpr bool kLarge = kFp4 && kVar;                // instance for large 4-bit calls
     constexpr bool kScaled = kFp8 || kFp4;               // codes with per-head scales, computed in f16
     constexpr int kTile = Lay::kTile;
+    constexpr int kCh = kFp4 ? FKV_FP4_MERGE_CHUNK : kChunk;
+    using Geom = UnitGeom<kCh>;
     constexpr int NST = Lay::kStages;
     constexpr int MT = kTile / 16;                       // 16-token MMA tiles per stage
     constexpr int NACC = MT >= 4 ? 1 : 2;                // independent QK accumulator chains per M tile
@@ -786,7 +796,7 @@ paged_decode_attn_kernel(const AttnParams p, const __grid_constant__ CUtensorMap
     bool aligned = false;          // small batch: every unit has whole warps
     int64_t lo = 0, hi = 0;
     FirstRequest afr;
-    UnitGeom agm{0, 0};            // the warp's unit, under the aligned schedule
+    Geom agm{0, 0};            // the warp's unit, under the aligned schedule
     // Up to 64 requests: one load of every request's row (two per lane) serves
     // both the total and the search for the first request.
     const bool cached = p.B <= 64;
@@ -1002,13 +1012,13 @@ paged_decode_attn_kernel(const AttnParams p, const __grid_constant__ CUtensorMap
         const int64_t nt = (p.prefix[r + 1] - base) / Hkv;
         const int64_t s0 = base + h * nt;
         const int64_t wf = warp_of_tile(s0, T, nw);
-        return UnitGeom{static_cast<int>(wf), static_cast<int>(warp_of_tile(s0 + nt - 1, T, nw) - wf + 1)};
+        return Geom{static_cast<int>(wf), static_cast<int>(warp_of_tile(s0 + nt - 1, T, nw) - wf + 1)};
     };
     // A merge this warp owes (kFinalDue: the single-level merge of a unit;
     // kChunkDue: the first level of a two-level merge, then the unit's
     // arrival and, if last, its second level), for unit (r, h), performed at
     // the end of the warp's range, where the stage ring is idle.
-    auto merge_steps = [&](int stage, const UnitGeom &gm, int r, int h, float vsc) {
+    auto merge_steps = [&](int stage, const Geom &gm, int r, int h, float vsc) {
         auto merge = [&](int64_t sl0, int cnt, int stride, bool me, int64_t wk0, bool fin, int64_t d) {
             if (merge_parts_smem(p, sbase, merge_cap, merge_bar, merge_phase, nw, sl0, cnt, stride, me, wk0, T,
                                  fin, r, h, vsc, d))
@@ -1029,7 +1039,7 @@ paged_decode_attn_kernel(const AttnParams p, const __grid_constant__ CUtensorMap
         if (lane == 0) last2 = atomic_add_acq_rel_gpu(p.counters + u, 1) == gm.nch() - 1;
         if (__shfl_sync(kFull, last2, 0)) {
             __syncwarp();
-            merge(u + gm.wf, gm.nch(), kChunk, false, gm.wf, true, 0);
+            merge(u + gm.wf, gm.nch(), kCh, false, gm.wf, true, 0);
         }
     };
 
@@ -1041,11 +1051,11 @@ paged_decode_attn_kernel(const AttnParams p, const __grid_constant__ CUtensorMap
     int cseq = 0, seg_start = 0;
     bool unit_bad = false;
     float cvsc = 1.f;       // the unit's V scale
-    UnitGeom cgm = agm;     // where the unit's parts sit, if it is split (span 0: not yet known)
+    Geom cgm = agm;     // where the unit's parts sit, if it is split (span 0: not yet known)
     // a merge this warp owes from the middle of its range: at most one, since
     // only the unit it started in can end there and be split
     int def_stage = kNone, def_r = 0, def_h = 0;
-    UnitGeom def_gm{0, 0};
+    Geom def_gm{0, 0};
     float def_vsc = 1.f;
     int end_stage = kNone;  // large-call instance: the merge at the range end
 
@@ -1063,7 +1073,7 @@ paged_decode_attn_kernel(const AttnParams p, const __grid_constant__ CUtensorMap
         const int64_t u = static_cast<int64_t>(C.r) * Hkv + C.h;
         // parts of a split unit that hold tiles (warps of its span with a
         // non-empty range)
-        auto unit_parts = [&](const UnitGeom &gm) {
+        auto unit_parts = [&](const Geom &gm) {
             int n = gm.span;
             if (maybe_empty) {
                 n = 0;
@@ -1169,7 +1179,7 @@ paged_decode_attn_kernel(const AttnParams p, const __grid_constant__ CUtensorMap
 #if FKV_TRY_LAST
         // (not the 4-bit kernel, whose shorter ranges leave fewer such units: 66.4 us
         // without it on 32 x 8192 tokens, 67.5 with it)
-        if (!kFp4 && !whole && seg_start == 0 && range_end && (maybe_empty || cgm.span <= kChunk) &&
+        if (!kFp4 && !whole && seg_start == 0 && range_end && (maybe_empty || cgm.span <= kCh) &&
             unit_parts(cgm) <= 3) {
             // This warp holds the unit's first part (the unit started in
             // its range and runs to the range end).  The unit's other
@@ -1232,16 +1242,16 @@ paged_decode_attn_kernel(const AttnParams p, const __grid_constant__ CUtensorMap
         }
         if (!whole && !merged) {
             // Merge without waiting: the last of the unit's warps to arrive
-            // merges.  Units split over more than kChunk warps merge in two
-            // levels (chunks of kChunk consecutive parts, then the chunks),
+            // merges.  Units split over more than kCh warps merge in two
+            // levels (chunks of kCh consecutive parts, then the chunks),
             // so no single warp reads a long unit's partials serially.
             // Arrivals are acquire-release atomics by lane 0 after a warp
             // barrier: they publish this warp's partial and, for the last
             // arriver, make every other part visible.
-            const UnitGeom &gm = cgm;
+            const Geom &gm = cgm;
             int stage = kNone;
             __syncwarp();
-            if (maybe_empty || gm.span <= kChunk) {
+            if (maybe_empty || gm.span <= kCh) {
                 const int nparts = unit_parts(gm);
                 int last = 0;
                 if (lane == 0) last = atomic_add_acq_rel_gpu(p.counters + u, 1) == nparts - 1;
@@ -1654,7 +1664,7 @@ paged_decode_attn_kernel(const AttnParams p, const __grid_constant__ CUtensorMap
         // about 3 us at the end of a call, so a small one keeps them in the loop.
         finish_share(true);
         int stage = end_stage, r = C.r, h = C.h;
-        UnitGeom gm = cgm;
+        Geom gm = cgm;
         float vsc = cvsc;
         bool owed = def_stage != kNone;
         while (true) {
@@ -1674,7 +1684,7 @@ paged_decode_attn_kernel(const AttnParams p, const __grid_constant__ CUtensorMap
             const int n = chunk ? gm.csz(w) : second ? gm.nch() : gm.span;
             const int64_t at = u + gm.wf + c0;
             if ((!chunk || n > 1) &&
-                !merge_parts_smem(p, sbase, merge_cap, merge_bar, merge_phase, nw, at, n, second ? kChunk : 1,
+                !merge_parts_smem(p, sbase, merge_cap, merge_bar, merge_phase, nw, at, n, second ? kCh : 1,
                                   stage == kFinalDue && maybe_empty, gm.wf + c0, T, !chunk, r, h, vsc, at)) {
                 if (lane == 0) atomicOr(p.err, FKV_DEVERR_TIMEOUT);
                 stage = kNone;                                 // nothing more of this unit
