@@ -182,7 +182,8 @@ FKV_API fkv_status kv_gather(const void *k_cache, const void *v_cache, int32_t k
  *     interleaved != 0; elements from rotary_dim on are y unchanged.
  * The angle keeps its low bits at far positions: the product is formed in two
  * fp32 words and reduced to a fraction of a turn before sin and cos (|theta|
- * below 2^31; below 2^20 it is off by about 2^-23 of a turn).
+ * below 2^31; below 2^20 it is off by about 2^-23 of a turn).  A normed row's
+ * sum of squares has to be a finite fp32 number (every |x| below 1.6e18 is).
  *
  *   q, k           bf16, token n's heads at q + n * q_token_stride (elements):
  *                  num_q_heads (num_kv_heads) rows of 128, contiguous; token
