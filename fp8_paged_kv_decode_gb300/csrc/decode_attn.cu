@@ -125,6 +125,7 @@ constexpr int kPlanSmemPrefix = 4096;    // requests whose prefix the plan searc
 constexpr uint64_t kWaitLimitNs = 2000000000ull;     // a copy that has not landed in 2 s has failed
 constexpr uint64_t kDrainLimitNs = 200000000ull;
 constexpr uint32_t kFull = 0xffffffffu;
+constexpr float kPTop = 15.f;            // log2 of the largest softmax weight held in f16 (its maximum is just below 2^16)
 #ifndef FKV_MERGE_CHUNK
 #define FKV_MERGE_CHUNK 9
 #endif
@@ -239,7 +240,7 @@ struct AttnParams {
     const int64_t *prefix;     // [B+1] tile prefix over requests (tiles x Hkv)
     const int32_t *warp_req;   // [NW + 1] request holding each warp's first tile; [NW] = warps with work
     float *part_o;             // [slots][G][D]   slots = B*Hkv + NW
-    float2 *part_ml;           // [slots][GP] (m in log2 units, l; l < 0 marks an invalid unit)
+    float2 *part_ml;           // [slots][GP] (m, the log2 reference of the part's weights, and l; l < 0 marks an invalid unit)
     int32_t *counters;         // [B*Hkv] arrivals per split unit (or per chunk of it)
     int32_t *chunk_counters;   // [slots] arrivals per first-level chunk, indexed by its first slot
     __nv_bfloat16 *out;
@@ -1496,15 +1497,20 @@ paged_decode_attn_kernel(const AttnParams p, const __grid_constant__ CUtensorMap
             mx[j] = fmaxf(mx[j], __shfl_xor_sync(kFull, mx[j], 16));
         }
         // Each logit is scaled with one rounded multiply, the same operation
-        // that forms the running maximum, so the largest logit gives exactly
-        // ex2(0) = 1 and every other one at most 1.  (A fused multiply-add
+        // that forms the running maximum, so the largest logit gives the largest
+        // weight, ex2(0) = 1 for BF16, and no other one more.  (A fused multiply-add
         // against the rounded maximum would leave the product's rounding error,
         // up to half an ulp of the logit: harmless for ordinary logits, but
         // past ~2^33 in log2 units that error overflows ex2.)
+        // FP8 and FP4 take their weights relative to kPTop below that maximum
+        // (rounded up, so the largest is at most 2^kPTop), which uses f16's upper
+        // range for P below: l and o carry the same factor, and m is the reference
+        // that both belong to, so nothing else knows of it.
         float alpha[2];
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
-            const float mnew = fmaxf(m[j], __fmul_rn(mx[j], cfac[j]));
+            const float top = __fmul_rn(mx[j], cfac[j]);
+            const float mnew = fmaxf(m[j], kScaled ? __fadd_ru(top, -kPTop) : top);
             alpha[j] = ex2(m[j] - mnew);
             m[j] = mnew;
         }
@@ -1549,9 +1555,14 @@ paged_decode_attn_kernel(const AttnParams p, const __grid_constant__ CUtensorMap
             o[a][3] *= alpha[1];
         }
         // P^T fragments: transpose (token, head) 8x8 blocks into (head, token).
-        // FP8: P in f16 (11-bit significand).  BF16: the MMA needs bf16 P, whose
-        // 8-bit significand alone would cost up to 2^-9 |v| in the output, so P
-        // is split into bf16 hi + lo parts and PV runs on both (16 bits).
+        // FP8 and FP4: P in f16, the type the codes convert to exactly; its 11-bit
+        // significand costs each weight at most 2^-11 of itself, an eighth of the
+        // output's own rounding.  P <= 2^kPTop keeps those bits down to 2^-29 of the
+        // largest weight and drops a weight only below 2^-40 (without the factor
+        // 2^-14 and 2^-25, where a token of large weight and small V, an attention
+        // sink, hid the other tokens).  BF16: the MMA needs bf16 P, whose 8-bit
+        // significand alone would cost up to 2^-8 of each weight, so P is split
+        // into bf16 hi + lo parts and PV runs on both (16 bits).
         uint32_t pb[MT][2], pl[MT][2];
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt) {
