@@ -69,6 +69,8 @@ _HERE = os.path.dirname(os.path.abspath(__file__))
 _lock = threading.Lock()
 _lib = None
 _bind = None      # the compiled marshalling, once loaded
+_BIND_CALLS = ("fkv_status_string", "kv_append_fp4", "kv_append_fp4_tag_check", "kv_gather", "qk_norm_rope", "kv_step_tables",
+               "paged_decode_attn")      # the entry points that it calls, in the order its setup takes them
 
 
 class FkvError(RuntimeError):
@@ -160,9 +162,7 @@ def _load_bind():
             loader = importlib.machinery.ExtensionFileLoader("_fkv_bind", path)
             mod = importlib.util.module_from_spec(importlib.util.spec_from_loader("_fkv_bind", loader))
             loader.exec_module(mod)
-            mod.setup(FkvError, *(ctypes.cast(getattr(lib, f), ctypes.c_void_p).value for f in (
-                "fkv_status_string", "kv_append_fp4", "kv_append_fp4_tag_check", "kv_gather", "qk_norm_rope",
-                "kv_step_tables", "paged_decode_attn")))
+            mod.setup(FkvError, *(ctypes.cast(getattr(lib, f), ctypes.c_void_p).value for f in _BIND_CALLS))
             _bind = mod
         return _bind
 
