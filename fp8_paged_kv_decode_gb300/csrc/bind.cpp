@@ -70,6 +70,7 @@ void *stream_of(PyObject *o, int dev) {
     need(h != nullptr, "stream must be a torch.cuda.Stream or a handle");
     void *s = PyLong_AsVoidPtr(h);
     Py_DECREF(h);
+    need(s || !PyErr_Occurred(), "stream must be a torch.cuda.Stream or a handle");
     return s;
 }
 double number(PyObject *o) {

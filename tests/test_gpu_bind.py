@@ -53,3 +53,19 @@ def test_the_interpreter_lock_is_released():
         for f in calls().values():
             f()
     assert check() == 1
+
+
+class OddStream:
+    cuda_stream = "not a handle"
+
+
+@pytest.mark.parametrize("stream", [2 ** 70, -2 ** 70, OddStream(), "a stream", object()], ids=str)
+def test_a_stream_that_is_none_is_refused(stream):
+    import fp8_paged_kv_decode_gb300 as fkv
+    check = ctypes.cast(ctypes.pythonapi.PyGILState_Check, ctypes.c_void_p).value      # (so that nothing is launched)
+    with entry_points(check):
+        for f in calls(stream=None).values():
+            f()
+        for f in calls(stream=stream).values():
+            with pytest.raises(fkv.FkvError, match="stream"):
+                f()
