@@ -192,7 +192,7 @@ int32_t cache_format(const at::Tensor &kc, const at::Tensor &vc, const at::Tenso
     need(bytes8(kc) && bytes8(vc), "cache must be uint8 (e4m3, or FP4 rows of 72) or bf16");
     need(ks && vs && is(*ks, kF32) && is(*vs, kF32) && ks->numel() >= kc.size(1) && vs->numel() >= kc.size(1),
          "scales must be float32 [Hkv]");
-    return kc.size(3) == FKV_FP4_ROW_BYTES ? FKV_KV_FP4 : FKV_KV_FP8_E4M3;
+    return is(kc, kU8) && is(vc, kU8) && kc.size(3) == FKV_FP4_ROW_BYTES ? FKV_KV_FP4 : FKV_KV_FP8_E4M3;
 }
 
 PyObject *py_gather(PyObject *, PyObject *const *a, Py_ssize_t n) {

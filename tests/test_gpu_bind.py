@@ -59,7 +59,7 @@ class OddStream:
     cuda_stream = "not a handle"
 
 
-@pytest.mark.parametrize("stream", [2 ** 70, -2 ** 70, OddStream(), "a stream", object()], ids=str)
+@pytest.mark.parametrize("stream", [2 ** 70, -2 ** 70, OddStream(), "a stream", object()], ids=["past64", "below64", "attribute", "text", "object"])
 def test_a_stream_that_is_none_is_refused(stream):
     import fp8_paged_kv_decode_gb300 as fkv
     check = ctypes.cast(ctypes.pythonapi.PyGILState_Check, ctypes.c_void_p).value      # (so that nothing is launched)
@@ -69,3 +69,27 @@ def test_a_stream_that_is_none_is_refused(stream):
         for f in calls(stream=stream).values():
             with pytest.raises(fkv.FkvError, match="stream"):
                 f()
+
+
+def test_only_uint8_rows_of_72_are_fp4():
+    """An e4m3 tensor's last dimension is its head_dim: 72 is not supported."""
+    import torch
+    import fp8_paged_kv_decode_gb300 as fkv
+    z = lambda *s, dt=torch.bfloat16: torch.zeros(*s, dtype=dt, device="cuda")   # noqa: E731
+    sc, k8 = z(2, dt=torch.float32) + 1, z(4, 2, 16, 72, dt=torch.uint8)
+    ke = k8.view(torch.float8_e4m3fn)
+    slots, ptr, idx, lens = z(3, dt=torch.int64), z(2, dt=torch.int32), z(1, dt=torch.int32), z(1, dt=torch.int32)
+    ws = fkv.alloc_workspace(1, 4, 2, fkv.KV_FP4)
+    for kc, vc in ((ke, ke), (ke, k8), (k8, ke)):
+        with pytest.raises(fkv.FkvError):
+            fkv.kv_gather(kc, vc, slots, z(3, 2, D), z(3, 2, D), sc, sc)
+        with pytest.raises(fkv.FkvError):
+            fkv.kv_gather(kc, vc, slots, z(3, 2, 72), z(3, 2, 72), sc, sc)
+        for d in (D, 72):
+            q = z(1, 4, d)
+            with pytest.raises(fkv.FkvError):
+                fkv.paged_decode_attn(q, kc, vc, ptr, idx, lens, 0.1, q.clone(), ws, k_scale=sc, v_scale=sc)
+            with pytest.raises(fkv.FkvError):
+                fkv.paged_decode_attn_noalloc(q, kc, vc, ptr, idx, lens, 0.1, q.clone(), k_scale=sc, v_scale=sc)
+    with pytest.raises(fkv.FkvError):
+        fkv.kv_page_realloc(z(4, dt=torch.int32), idx, idx.clone(), ke, ke)
