@@ -439,6 +439,35 @@ def paged_decode_attn(q, k_cache, v_cache, page_indptr, page_indices, seq_lens, 
     return out
 
 
+def _attn_args(q, k_cache, v_cache, page_indptr, page_indices, seq_lens, sm_scale, out, k_scale, v_scale, abort_mask):
+    """The checked C arguments of decode attention, up to ``out``."""
+    import torch
+    _dev(q, k_cache, v_cache, page_indptr, page_indices, seq_lens, out, k_scale, v_scale, abort_mask)
+    _need(q.dim() == 3 and k_cache.dim() == 4 and k_cache.shape == v_cache.shape, "q [B][Hq][128], caches of one shape")
+    B, Hq, D = q.shape
+    P, Hkv, S, row = k_cache.shape
+    if _is_fp4_cache(k_cache) and _is_fp4_cache(v_cache):
+        kv, row = KV_FP4, HEAD_DIM
+    elif k_cache.dtype == torch.bfloat16:
+        _need(v_cache.dtype == torch.bfloat16, "k_cache and v_cache types differ")
+        kv = KV_BF16
+    else:
+        _need(_is_byte_cache(k_cache) and _is_byte_cache(v_cache), "cache must be uint8 (e4m3, or FP4 rows of 72) or bf16")
+        kv = KV_FP8_E4M3
+    if kv == KV_BF16:
+        k_scale = v_scale = None
+    else:
+        for s in (k_scale, v_scale):
+            _need(s is not None and s.dtype == torch.float32 and s.numel() >= Hkv, "scales must be float32 [Hkv]")
+    _need(q.dtype == torch.bfloat16 and out.dtype == torch.bfloat16, "q/out must be bf16")
+    _need(page_indptr.dtype in (torch.int32, torch.uint32) and page_indices.dtype in (torch.int32, torch.uint32), "CSR must be int32")
+    _need(seq_lens.dtype == torch.int32 and seq_lens.numel() >= B, "seq_lens must be int32 [B]")
+    _need(abort_mask is None or (abort_mask.dtype == torch.uint8 and abort_mask.numel() >= B), "abort_mask must be uint8 [B]")
+    _need(tuple(out.shape) == (B, Hq, D) and row == D and page_indptr.numel() == B + 1, "shape mismatch")
+    return (_ptr(q), B, Hq, _ptr(k_cache), _ptr(v_cache), kv, _ptr(k_scale), _ptr(v_scale), P, Hkv, S, D, _ptr(page_indptr),
+            _ptr(page_indices), page_indices.numel(), _ptr(seq_lens), _ptr(abort_mask), float(sm_scale), _ptr(out))
+
+
 def paged_decode_attn_noalloc(q, k_cache, v_cache, page_indptr, page_indices, seq_lens, sm_scale, out,
                               k_scale=None, v_scale=None, abort_mask=None, stream=None):
     """``paged_decode_attn`` without a workspace argument, for callers that
@@ -446,27 +475,9 @@ def paged_decode_attn_noalloc(q, k_cache, v_cache, page_indptr, page_indices, se
     ``NOALLOC_SCRATCH_BYTES`` inside the library (shared by all calls on a
     device, so calls must not overlap on the GPU).  Shapes needing more
     scratch raise FkvError (status ERR_SCRATCH_LIMIT)."""
-    import torch
-    _dev(q, k_cache, v_cache, page_indptr, page_indices, seq_lens, out, k_scale, v_scale, abort_mask)
-    B, Hq, D = q.shape
-    P, Hkv, S, row = k_cache.shape
-    if _is_fp4_cache(k_cache):
-        kv, row = KV_FP4, HEAD_DIM
-    elif _is_byte_cache(k_cache):
-        kv = KV_FP8_E4M3
-    else:
-        _need(k_cache.dtype == torch.bfloat16, "cache must be uint8 (e4m3, or FP4 rows of 72) or bf16")
-        kv = KV_BF16
-    _need(kv != KV_FP4 or (_is_fp4_cache(v_cache) and v_cache.shape == k_cache.shape), "k_cache and v_cache differ")
-    _need(q.dtype == torch.bfloat16 and out.dtype == torch.bfloat16, "q/out must be bf16")
-    _need(seq_lens.dtype == torch.int32, "seq_lens must be int32")
-    _need(abort_mask is None or abort_mask.dtype == torch.uint8, "abort_mask must be uint8")
-    _need(tuple(out.shape) == (B, Hq, D) and row == D and page_indptr.numel() == B + 1, "shape mismatch")
     _raise(load_library().paged_decode_attn_noalloc(
-        _ptr(q), B, Hq, _ptr(k_cache), _ptr(v_cache), kv, _ptr(k_scale) if kv != KV_BF16 else None,
-        _ptr(v_scale) if kv != KV_BF16 else None, P, Hkv, S, D, _ptr(page_indptr), _ptr(page_indices),
-        page_indices.numel(), _ptr(seq_lens), _ptr(abort_mask), float(sm_scale), _ptr(out), _stream(stream)),
-        "paged_decode_attn_noalloc")
+        *_attn_args(q, k_cache, v_cache, page_indptr, page_indices, seq_lens, sm_scale, out, k_scale, v_scale, abort_mask),
+        _stream(stream)), "paged_decode_attn_noalloc")
     return out
 
 
