@@ -399,12 +399,16 @@ def kv_page_realloc(page_tags, pages, new_tags, k_cache=None, v_cache=None, stre
     _dev(page_tags, pages, new_tags, k_cache, v_cache)
     _need(page_tags.dtype in (torch.int32, torch.uint32) and new_tags.dtype == page_tags.dtype, "32-bit tags")
     _need(pages.dtype == torch.int32 and new_tags.numel() == pages.numel(), "pages int32, one new tag each")
+    _need(k_cache is not None or v_cache is None, "both pools, or neither")
     if k_cache is not None:
         _need(v_cache is not None and tuple(k_cache.shape) == tuple(v_cache.shape), "both pools, same shape")
+        _need(k_cache.dtype == v_cache.dtype or (_is_byte_cache(k_cache) and _is_byte_cache(v_cache)), "pools of one type")
         P, Hkv, S, D = k_cache.shape
+        _need(P >= page_tags.numel(), "the pools must have every page that has a tag")
         if _is_fp4_cache(k_cache):
             D, kv = HEAD_DIM, KV_FP4
         else:
+            _need(_is_byte_cache(k_cache) or k_cache.dtype == torch.bfloat16, "pools must be uint8 (e4m3, or FP4 rows of 72) or bf16")
             kv = KV_FP8_E4M3 if _is_byte_cache(k_cache) else KV_BF16
     else:
         Hkv = S = 0

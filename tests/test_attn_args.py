@@ -75,3 +75,17 @@ def test_noalloc_refusals(lib, kind, i):
     with pytest.raises(fkv.FkvError):
         fkv.paged_decode_attn_noalloc(**attn(kind, **over))
     assert not lib.calls
+
+
+@pytest.mark.parametrize("row,dt,fmt", [(72, "uint8", 2), (128, "uint8", 0), (128, "float8_e4m3fn", 0), (128, "bfloat16", 1)])
+def test_realloc_pools(lib, row, dt, fmt):
+    """A scrub writes whole pages of both pools, so both have to hold every tagged page in one format."""
+    tags, pages, new, pool = z(5, dt="int32"), z(2, dt="int32"), z(2, dt="int32"), z(5, 4, 16, row, dt=dt)
+    fkv.kv_page_realloc(tags, pages, new, pool, z(5, 4, 16, row, dt=dt), stream=0)
+    assert [c[1][7] for c in lib.calls] == [fmt]
+    for kc, vc in ((z(4, 4, 16, row, dt=dt), z(4, 4, 16, row, dt=dt)), (pool, z(4, 4, 16, row, dt=dt)), (pool, z(5, 4, 16, row, dt="float32")), (pool, None),
+                   (None, pool), (z(5, 4, 16, row, dt="float32"), z(5, 4, 16, row, dt="float32")),
+                   (pool, z(5, 4, 16, row, dt="uint8" if fmt == 1 else "bfloat16"))):
+        with pytest.raises(fkv.FkvError):
+            fkv.kv_page_realloc(tags, pages, new, kc, vc, stream=0)
+    assert len(lib.calls) == 1
