@@ -6,8 +6,10 @@ passes raw device pointers, sizes and the current CUDA stream to the library;
 all computation runs in the library's CUDA kernels.  There is no CPU path: if
 the library is missing or no GPU is present the calls raise.  The calls that a
 decode step makes with a 4-bit cache, and ``paged_decode_attn``, are marshalled
-by ``_fkv_bind.so`` (host C++, ``csrc/bind.cpp``): in Python their checks took
-4 to 9 us a call, more than some of the kernels.
+by the ``_fkv_bind`` module (host C++, ``csrc/bind.cpp``, built for one torch
+version): in Python their checks took 4 to 9 us a call, more than some of the
+kernels.  Without it ``paged_decode_attn`` and the calls that do not use it
+still run.
 
 Entry points (same names as the C ABI):
   kv_append_fp8 / kv_append_bf16   write new tokens into the paged pools
@@ -146,8 +148,9 @@ def load_library():
         return lib
 
 
-def _load_bind():
-    """Load _fkv_bind.so and give it the library's entry points."""
+def _load_bind(needed=True):
+    """Load the marshalling module for this torch and give it the library's
+    entry points.  Where it has not been built: an error, or None (not needed)."""
     global _bind
     lib = load_library()
     with _lock:
@@ -156,9 +159,13 @@ def _load_bind():
             import importlib.util
 
             import torch  # noqa: F401  (its libraries, which the module links against)
-            path = os.path.join(_HERE, "_fkv_bind.so")
+
+            from . import _build
+            path = _build.bind_path()
             if not os.path.exists(path):
-                raise FkvError("_fkv_bind.so is not built; run fp8_paged_kv_decode_gb300._build.build()")
+                if not needed:
+                    return None
+                raise FkvError("%s is not built; run fp8_paged_kv_decode_gb300._build.build()" % os.path.basename(path))
             loader = importlib.machinery.ExtensionFileLoader("_fkv_bind", path)
             mod = importlib.util.module_from_spec(importlib.util.spec_from_loader("_fkv_bind", loader))
             loader.exec_module(mod)
@@ -438,8 +445,15 @@ def paged_decode_attn(q, k_cache, v_cache, page_indptr, page_indices, seq_lens, 
     k_scale/v_scale fp32 [Hkv]) or bf16, or [P][Hkv][S][72] uint8 (FP4, with
     the same scales; workspace for KV_FP4); CSR page table int32; seq_lens int32
     [B]; abort_mask uint8 [B] or None (no tracker)."""
-    (_bind or _load_bind()).paged_decode_attn(q, k_cache, v_cache, page_indptr, page_indices, seq_lens, sm_scale, out,
-                                              workspace, k_scale, v_scale, abort_mask, stream)
+    bind = _bind or _load_bind(needed=False)
+    if bind is not None:
+        bind.paged_decode_attn(q, k_cache, v_cache, page_indptr, page_indices, seq_lens, sm_scale, out, workspace, k_scale,
+                               v_scale, abort_mask, stream)
+    else:               # not built for this torch: the library alone serves the call, at more host time
+        _dev(workspace)
+        _raise(load_library().paged_decode_attn(
+            *_attn_args(q, k_cache, v_cache, page_indptr, page_indices, seq_lens, sm_scale, out, k_scale, v_scale, abort_mask),
+            _ptr(workspace), workspace.numel() * workspace.element_size(), _stream(stream)), "paged_decode_attn")
     return out
 
 

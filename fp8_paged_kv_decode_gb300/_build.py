@@ -1,5 +1,6 @@
-"""Build libfkv.so in-tree with nvcc for sm_103a (GB300), and _fkv_bind.so, the
-Python binding's argument marshalling (host C++ against torch's headers).
+"""Build libfkv.so in-tree with nvcc for sm_103a (GB300), and the Python binding's
+argument marshalling (host C++ against torch's headers; one file per Python and
+torch, whose versions its name carries).
 
 Each .cu file compiles to an object in parallel, then one shared library is
 linked.  No fast-math: the e4m3 quantisation relies on IEEE division.
@@ -15,7 +16,6 @@ PKG = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(PKG, "csrc")
 ROOT = os.path.dirname(PKG)
 LIB = os.path.join(PKG, "libfkv.so")
-BIND = os.path.join(PKG, "_fkv_bind.so")
 BIND_SOURCE = os.path.join(CSRC, "bind.cpp")
 BUILD_DIR = os.path.join(PKG, "_build")
 SOURCES = ["fkv_api.cu", "kv_append.cu", "tag_check.cu", "decode_attn.cu", "decode_attn_noalloc.cu", "page_realloc.cu",
@@ -42,6 +42,15 @@ def _stale(out: str, deps) -> bool:
 def _headers():
     hs = [os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith((".cuh", ".h"))]
     return hs + [os.path.join(ROOT, "include", "fkv.h")]
+
+
+def bind_path() -> str:
+    """The marshalling module for this Python and torch (torch's C++ interface
+    changes with its version)."""
+    import sys
+
+    import torch
+    return os.path.join(PKG, "_fkv_bind.%s-torch-%s.so" % (sys.implementation.cache_tag, torch.__version__))
 
 
 def _bind_command(out: str):
@@ -80,13 +89,14 @@ def build(force: bool = False, verbose: bool = False, extra_flags=(), out_lib: s
         if verbose and (r.stdout or r.stderr):
             print(r.stdout + r.stderr)
 
-    bind = None
-    if out_lib == LIB and (force or _stale(BIND, [BIND_SOURCE, os.path.join(ROOT, "include", "fkv.h")])):
-        bind = BIND + ".tmp%d" % os.getpid()
+    # any libfkv.so is called through it, a variant's (out_lib) too
+    bind, bind_out = None, bind_path()
+    if (force and out_lib == LIB) or _stale(bind_out, [BIND_SOURCE, os.path.join(ROOT, "include", "fkv.h")]):
+        bind = bind_out + ".tmp%d" % os.getpid()
     with cf.ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
         list(ex.map(run, ([_bind_command(bind)] if bind else []) + jobs))
     if bind:
-        os.replace(bind, BIND)
+        os.replace(bind, bind_out)
     if force or jobs or _stale(out_lib, objs):
         tmp = out_lib + ".tmp%d" % os.getpid()
         run([exe, *ARCH, "-shared", "-o", tmp, *objs, "-lcudart"])

@@ -89,3 +89,51 @@ def test_realloc_pools(lib, row, dt, fmt):
         with pytest.raises(fkv.FkvError):
             fkv.kv_page_realloc(tags, pages, new, kc, vc, stream=0)
     assert len(lib.calls) == 1
+
+
+@pytest.fixture
+def no_module(monkeypatch, tmp_path):
+    """As after a change of torch: the marshalling module has not been built for it."""
+    from fp8_paged_kv_decode_gb300 import _build
+    monkeypatch.setattr(fkv, "_bind", None)
+    monkeypatch.setattr(_build, "bind_path", lambda: str(tmp_path / "_fkv_bind.none.so"))
+
+
+@pytest.mark.parametrize("kind", ["fp4", "fp8", "bf16"])
+def test_attention_needs_the_library_alone(lib, no_module, kind):
+    a, ws = attn(kind), z(1024, dt="uint8")
+    assert fkv.paged_decode_attn(**a, workspace=ws) is a["out"]
+    fkv.paged_decode_attn_noalloc(**a)
+    (n0, c0), (n1, c1) = lib.calls
+    assert n0 == "paged_decode_attn" and c0 == c1[:-1] + (ws.data_ptr(), 1024, 0)
+    with pytest.raises(fkv.FkvError, match="not built"):
+        fkv.kv_gather(a["k_cache"], a["v_cache"], a["seq_lens"], a["out"], a["out"])
+
+
+def test_the_module_belongs_to_one_torch(monkeypatch):
+    """Another torch version is another file, so that one built before is neither loaded nor taken as built."""
+    import torch
+    from fp8_paged_kv_decode_gb300 import _build
+    here = _build.bind_path()
+    assert here.endswith(".so") and str(torch.__version__) in here
+    monkeypatch.setattr(torch, "__version__", "99.0")
+    assert _build.bind_path() != here and _build._stale(_build.bind_path(), [])
+
+
+def test_a_variant_build_brings_the_module(monkeypatch, tmp_path):
+    """A library built elsewhere is called through the module too."""
+    from fp8_paged_kv_decode_gb300 import _build
+    ran = []
+
+    def run(cmd, **kw):
+        ran.append(cmd)
+        open(cmd[cmd.index("-o") + 1], "w").close()
+        return type("R", (), dict(returncode=0, stdout="", stderr=""))
+    monkeypatch.setattr(_build, "bind_path", lambda: str(tmp_path / "_fkv_bind.new.so"))
+    monkeypatch.setattr(_build.subprocess, "run", run)
+    out = str(tmp_path / "libvariant.so")
+    assert _build.build(out_lib=out, build_dir=str(tmp_path / "b")) == out
+    assert (tmp_path / "_fkv_bind.new.so").exists() and len(ran) == len(_build.SOURCES) + 2
+    n = len(ran)
+    _build.build(out_lib=out, build_dir=str(tmp_path / "b"), force=True)
+    assert len(ran) == n + len(_build.SOURCES) + 1               # and is not built again for it
