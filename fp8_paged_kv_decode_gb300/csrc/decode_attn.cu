@@ -861,7 +861,7 @@ paged_decode_attn_kernel(const AttnParams p, const __grid_constant__ CUtensorMap
         pid_r = fr.r0;                                 // the first request's page-table row is known
         lseq = fr.sl0;
         lrow0 = fr.row0;
-        lneed = (lseq + S - 1) / S;
+        lneed = static_cast<int>((static_cast<uint32_t>(lseq) + (S - 1)) / S);   // (the sum may pass 31 bits)
         pbase = -1000;
     } else {
         cursor_init(L, p, lo, p.warp_req[w]);
@@ -902,7 +902,7 @@ paged_decode_attn_kernel(const AttnParams p, const __grid_constant__ CUtensorMap
             pid_r = L.r;
             lseq = __ldcg(p.seq_lens + L.r);
             lrow0 = __ldcg(p.indptr + L.r);
-            lneed = (lseq + S - 1) >> S_log;
+            lneed = static_cast<int>((static_cast<uint32_t>(lseq) + (S - 1)) >> S_log);
             pbase = -1000;
         }
         const int tok0 = L.tt * kTile;
@@ -935,7 +935,7 @@ paged_decode_attn_kernel(const AttnParams p, const __grid_constant__ CUtensorMap
             pid_r = L.r;
             lseq = __ldcg(p.seq_lens + L.r);
             lrow0 = __ldcg(p.indptr + L.r);
-            lneed = (lseq + S - 1) / S;
+            lneed = static_cast<int>((static_cast<uint32_t>(lseq) + (S - 1)) / S);
             pbase = -1000;
         }
         const int tok0 = L.tt * kTile;
