@@ -118,11 +118,14 @@ def code_tokens(text):
     return "\n".join(out)
 
 
+KERNEL_SOURCES = ("decode_attn.cu", "fkv_common.cuh", "fp4_row.cuh")
+
+
 def kernel_source_hash(sources=None):
-    """Hash of the attention kernel's code (its two source files), which the
-    recorded ncu traffic figures are keyed to."""
+    """Hash of the attention kernel's code (its source file and the device
+    headers that it includes), which the recorded ncu traffic figures are keyed to."""
     h = hashlib.sha256()
-    for f in ("decode_attn.cu", "fkv_common.cuh"):
+    for f in KERNEL_SOURCES:
         if sources is None:
             with open(os.path.join(ROOT, "fp8_paged_kv_decode_gb300", "csrc", f)) as fh:
                 text = fh.read()
