@@ -48,8 +48,8 @@
 // at the copy bandwidth a scheduler has about 1700 cycles for a tile, and the
 // conversions (256 e2m1 pairs, 2 cycles each), the scale products (beside them)
 // and 64 MMAs (8 cycles each, during which little else issues) take 1070 of
-// them before anything else.  Measured apart on 64 requests around 16k tokens:
-// copies alone 208 us, arithmetic alone 237, together 234 in the kernel as it is.
+// them before anything else.  This kernel on 64 requests around 16k tokens: 234 us;
+// with its arithmetic left out 212, with its copies left out 223.
 // What it does for that:
 //  - tiles come as untiled bulk copies of whole rows (codes and scales lie
 //    together), one per page and pool, issued by different lanes, and cut to the
@@ -1670,9 +1670,10 @@ paged_decode_attn_kernel(const AttnParams p, const __grid_constant__ CUtensorMap
     if constexpr (kLarge) {
         // The large-call instance ends its range outside the loop, and merges with
         // one copy of the merge (the steps of merge_steps, as a loop): what that
-        // holds then shares no registers with the loop's state, which fits 164 that
-        // way, three warps per scheduler, and spills at 168 otherwise.  It costs
-        // about 3 us at the end of a call, so a small one keeps them in the loop.
+        // holds then shares no registers with the loop's state, which fits 160 that
+        // way, three warps per scheduler (168 at most), and spilled with the merge
+        // in the loop.  It costs about 3 us at the end of a call, so a small one
+        // keeps them in the loop.
         finish_share(true);
         int stage = end_stage, r = C.r, h = C.h;
         Geom gm = cgm;
@@ -1800,7 +1801,10 @@ bool use_ws(int page_size, int kv) {
 // page table lists (the lengths are on the device).  Requests of 8192 tokens, 64
 // query / 8 KV heads, small-call against large-call instance: 32 of them (33
 // thousand tiles) 65.9 and 67.3 us, 48 91.0 and 92.3, 64 116.9 and 116.5, 96 168.5
-// and 162.2; one request of 7168 tokens 17.7 and 21.2.
+// and 162.2; one request of 7168 tokens 17.7 and 21.2.  So short requests under a
+// table with room for many pay for it: under 100000 entries instead of their own,
+// one of 7168 tokens takes 21.3 us instead of 16.3, 16 of 8192 45.9 instead of
+// 40.5, 64 of 2048 48.3 instead of 42.0, 4 of 300 11.9 instead of 11.0.
 #ifndef FKV_FP4_LARGE_TILES
 #define FKV_FP4_LARGE_TILES 60000
 #endif

@@ -440,8 +440,9 @@ kv_append_fp4_kernel(const Fp4Append p) {
 }
 
 // The 4-bit cache's step prologue in one launch, laid out like
-// kv_append_fp8_tag_check_kernel: check blocks first, then the append's.  (A
-// decode step's call: one token per thread.)
+// kv_append_fp8_tag_check_kernel: check blocks first, then the append's.  Made for
+// a decode step's call, one token per thread: a prompt of 262144 tokens of 8 heads
+// takes 264 us through it, 220 through kv_append_fp4.
 __global__ void __launch_bounds__(kBlock, fp4_min_blocks(1))
 kv_append_fp4_tag_check_kernel(const Fp4Append p, unsigned append_blocks_x, int32_t num_pages,
                                const uint32_t *__restrict__ page_tags, const int32_t *__restrict__ page_indptr,

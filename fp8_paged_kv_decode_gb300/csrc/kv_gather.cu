@@ -13,7 +13,7 @@
 // too few in flight to cover their latency, so a thread takes kU tokens and has
 // all their slots, then all their rows, in flight together.  262144 tokens of 8
 // heads: FP4 277 us with one token a thread, 233 with four (5.9 TB/s; three
-// 231, six 246, eight 259), FP8 288 and 253 (6.4 TB/s).
+// 231, six 246, eight 259), FP8 288 and 253 (6.4 TB/s), BF16 327 with four (6.6 TB/s).
 #include "fp4_row.cuh"
 
 namespace fkv {

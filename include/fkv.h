@@ -183,7 +183,8 @@ FKV_API fkv_status kv_gather(const void *k_cache, const void *v_cache, int32_t k
  * The angle keeps its low bits at far positions: the product is formed in two
  * fp32 words and reduced to a fraction of a turn before sin and cos (|theta|
  * below 2^31; below 2^20 it is off by about 2^-23 of a turn).  A normed row's
- * sum of squares has to be a finite fp32 number (every |x| below 1.6e18 is).
+ * sum of squares has to be a finite fp32 number (every |x| below 1.6e18 is),
+ * and a normal one if eps is 0 (some |x| above 1.1e-19: squares of less vanish).
  *
  *   q, k           bf16, token n's heads at q + n * q_token_stride (elements):
  *                  num_q_heads (num_kv_heads) rows of 128, contiguous; token
@@ -195,7 +196,8 @@ FKV_API fkv_status kv_gather(const void *k_cache, const void *v_cache, int32_t k
  *   positions      int32 [n_axes][n_tokens]
  *   inv_freq       fp32 [rotary_dim / 2], finite
  *   axis_map       uint8 [rotary_dim / 2], each below n_axes (an entry that is
- *                  not leaves its pair unturned and sets FKV_DEVERR_ROPE_AXIS);
+ *                  not leaves its pair unturned, cos 1 and sin 0 without
+ *                  rot_scale, and sets FKV_DEVERR_ROPE_AXIS);
  *                  NULL: axis 0 for every pair.  n_axes is 1 .. 8
  *   rotary_dim     a multiple of 16, 16 .. 128
  * n_tokens == 0 is a no-op.
@@ -231,9 +233,11 @@ FKV_API fkv_status qk_norm_rope(const void *q, int64_t q_token_stride, int32_t n
  * them), no page is taken.  A request refused for the first two reasons has an
  * empty CSR row; otherwise missing pages are -1 with tag 0, which
  * kv_page_tag_check and paged_decode_attn reject.  Prefix sums that pass
- * n_tokens or nnz are cut to it.  A taken page id outside [0, num_pages), or
- * an existing one under a new token, makes its entries -1 and their slots -1
- * and sets FKV_DEVERR_TABLES.
+ * n_tokens or nnz are cut to it.  A listed page id outside [0, num_pages), taken
+ * or existing, makes its entries -1 and the slots of tokens on it -1 and sets
+ * FKV_DEVERR_TABLES (block_table gets the -1 of a taken one; an existing one's
+ * cell and tags are left).  A refused request's positions are c, c + 1, ...,
+ * or 0 where it was refused for one of the first two reasons.
  *
  *   cached_lens, new_lens  int32 [batch]
  *   block_table    int32 [batch][max_blocks], block_tags uint32, the same shape;
@@ -250,8 +254,9 @@ FKV_API fkv_status qk_norm_rope(const void *q, int64_t q_token_stride, int32_t n
  *   free_left      int32 [1], pages still free; may be free_count
  *   workspace      kv_step_tables_workspace_size(batch) bytes, 256-byte aligned,
  *                  not shared by calls that overlap on the GPU
- * The result depends only on the inputs (no atomics), and a call repeated on
- * the same inputs writes the same bytes.  batch == 0 still fills slot_mapping
+ * The result depends only on the inputs (its few atomics are integer maxima and
+ * ORs, the same in any order), and a call repeated on the same inputs writes the
+ * same bytes.  batch == 0 still fills slot_mapping
  * and positions, writes the two indptr's single 0 and free_left.
  */
 FKV_API size_t kv_step_tables_workspace_size(int32_t batch);
@@ -353,7 +358,8 @@ FKV_API fkv_status kv_append_bf16_tag_check(const void *k_new, const void *v_new
 /*
  * kv_append_fp4_tag_check -- the same one-launch prologue for a 4-bit cache:
  * kv_append_fp4 followed by kv_page_tag_check, with the arguments, results,
- * argument checks and rules of kv_append_fp8_tag_check.
+ * argument checks and rules of kv_append_fp8_tag_check.  It is made for a decode
+ * step; thousands of tokens are written faster by the two calls.
  */
 FKV_API fkv_status kv_append_fp4_tag_check(const void *k_new, const void *v_new,
                                    const int64_t *slot_mapping, int32_t n_tokens,
@@ -435,7 +441,12 @@ FKV_API size_t paged_decode_attn_workspace_size(int32_t batch, int32_t num_q_hea
  * (request, KV head) does not depend on which warp performs it or when).  The
  * 4-bit cache's split also depends on nnz: from 60000 tiles' worth of listed
  * pages on (a tile is 64 tokens of one KV head) a call is spread over more
- * warps, so the same rows under a longer page table may differ by rounding.
+ * warps, so the same rows under a longer page table may differ by rounding, and
+ * short requests under a table with room for many take up to 6 us longer: pass
+ * the nnz that a step can need, not the most that any may.
+ * Softmax weights and their sums are fp32; the product with V takes them as f16
+ * for FP8 and FP4 (each within 2^-11 of itself, down to 2^-29 of the largest
+ * weight of its part) and as two bf16 words for BF16.
  * Supported: head_dim 128, page_size in {16, 32, 64, 128}, group size
  * G = num_q_heads / num_kv_heads in 1..8, or above 8 when G splits into R
  * equal groups of at most 8 with R a power of two up to 8 (10, 12, 16, 24,
