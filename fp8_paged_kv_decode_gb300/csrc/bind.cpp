@@ -153,9 +153,9 @@ PyObject *py_append(PyObject *, PyObject *const *a, Py_ssize_t n) {
     return guarded("kv_append_fp4", n, 8, [&] {
         const Append p = append_args(a);
         return call(g_append, ptr(p.k), ptr(p.v), static_cast<const int64_t *>(ptr(p.slots)), p.n,
-                        static_cast<const float *>(ptr(p.ks)), static_cast<const float *>(ptr(p.vs)),
-                        static_cast<uint8_t *>(ptr(p.kc)), static_cast<uint8_t *>(ptr(p.vc)), p.pages, p.heads, p.page,
-                        128, stream_of(a[7], p.dev));
+                    static_cast<const float *>(ptr(p.ks)), static_cast<const float *>(ptr(p.vs)),
+                    static_cast<uint8_t *>(ptr(p.kc)), static_cast<uint8_t *>(ptr(p.vc)), p.pages, p.heads, p.page,
+                    128, stream_of(a[7], p.dev));
     });
 }
 
@@ -172,12 +172,12 @@ PyObject *py_append_check(PyObject *, PyObject *const *a, Py_ssize_t n) {
         need(batch >= 0 && is(*mask, kU8) && mask->numel() == batch && expected->numel() == nnz,
              "abort_mask must be uint8 [B], expected_tags parallel to page_indices");
         return call(g_append_check, ptr(p.k), ptr(p.v), static_cast<const int64_t *>(ptr(p.slots)), p.n,
-                              static_cast<const float *>(ptr(p.ks)), static_cast<const float *>(ptr(p.vs)),
-                              static_cast<uint8_t *>(ptr(p.kc)), static_cast<uint8_t *>(ptr(p.vc)), p.pages, p.heads,
-                              p.page, 128, static_cast<const uint32_t *>(ptr(tags)),
-                              static_cast<const int32_t *>(ptr(indptr)), static_cast<const int32_t *>(ptr(indices)),
-                              static_cast<const uint32_t *>(ptr(expected)), i32(batch), nnz,
-                              static_cast<uint8_t *>(ptr(mask)), stream_of(a[12], p.dev));
+                    static_cast<const float *>(ptr(p.ks)), static_cast<const float *>(ptr(p.vs)),
+                    static_cast<uint8_t *>(ptr(p.kc)), static_cast<uint8_t *>(ptr(p.vc)), p.pages, p.heads,
+                    p.page, 128, static_cast<const uint32_t *>(ptr(tags)),
+                    static_cast<const int32_t *>(ptr(indptr)), static_cast<const int32_t *>(ptr(indices)),
+                    static_cast<const uint32_t *>(ptr(expected)), i32(batch), nnz,
+                    static_cast<uint8_t *>(ptr(mask)), stream_of(a[12], p.dev));
     });
 }
 
@@ -207,8 +207,8 @@ PyObject *py_gather(PyObject *, PyObject *const *a, Py_ssize_t n) {
         need(is(*ko, kB16) && is(*vo, kB16) && shape3(*ko, rows, heads, dim) && shape3(*vo, rows, heads, dim),
              "k_out/v_out must be bf16 [N][Hkv][128]");
         return call(g_gather, ptr(kc), ptr(vc), kv, static_cast<const float *>(ptr(ks)), static_cast<const float *>(ptr(vs)),
-                        static_cast<const int64_t *>(ptr(slots)), i32(rows), ptr(ko), ptr(vo), i32(kc->size(0)),
-                        i32(heads), i32(kc->size(2)), i32(dim), stream_of(a[7], dev));
+                    static_cast<const int64_t *>(ptr(slots)), i32(rows), ptr(ko), ptr(vo), i32(kc->size(0)),
+                    i32(heads), i32(kc->size(2)), i32(dim), stream_of(a[7], dev));
     });
 }
 
@@ -242,10 +242,10 @@ PyObject *py_rope(PyObject *, PyObject *const *a, Py_ssize_t n) {
         const int inter = PyObject_IsTrue(a[10]);
         need(inter >= 0, "interleaved must be true or false");
         return call(g_rope, ptr(q), qs, i32(hq), ptr(k), ks, i32(hk), ptr(qo), qos, ptr(ko), kos, i32(rows), ptr(qw), ptr(kw),
-                      static_cast<float>(number(a[8])), static_cast<const int32_t *>(ptr(pos)),
-                      pos->dim() == 1 ? 1 : i32(pos->size(0)), static_cast<const float *>(ptr(freq)),
-                      static_cast<const uint8_t *>(ptr(map)), i32(2 * freq->numel()), inter,
-                      static_cast<float>(number(a[11])), i32(dim), stream_of(a[12], dev));
+                    static_cast<float>(number(a[8])), static_cast<const int32_t *>(ptr(pos)),
+                    pos->dim() == 1 ? 1 : i32(pos->size(0)), static_cast<const float *>(ptr(freq)),
+                    static_cast<const uint8_t *>(ptr(map)), i32(2 * freq->numel()), inter,
+                    static_cast<float>(number(a[11])), i32(dim), stream_of(a[12], dev));
     });
 }
 
@@ -276,9 +276,9 @@ PyObject *py_tables(PyObject *, PyObject *const *a, Py_ssize_t n) {
         const int64_t page = integer(a[7]);
         need(page > 0 && page <= 0x7FFFFFFF, "page_size must be positive");
         return call(g_tables, i(0), i(1), i32(batch), i(2), u(3), i32(t[2]->size(1)), i(4), i32(t[4]->numel()), i(5), u(6),
-                        i32(t[6]->numel()), static_cast<int32_t>(page), i(8), i(9), static_cast<uint8_t *>(ptr(t[10])),
-                        i(11), i(12), u(13), i32(t[12]->numel()), i(14), static_cast<int64_t *>(ptr(t[15])), i(16),
-                        i32(t[15]->numel()), i(17), ptr(t[18]), t[18]->nbytes(), stream_of(a[19], dev));
+                    i32(t[6]->numel()), static_cast<int32_t>(page), i(8), i(9), static_cast<uint8_t *>(ptr(t[10])),
+                    i(11), i(12), u(13), i32(t[12]->numel()), i(14), static_cast<int64_t *>(ptr(t[15])), i(16),
+                    i32(t[15]->numel()), i(17), ptr(t[18]), t[18]->nbytes(), stream_of(a[19], dev));
     });
 }
 
@@ -302,12 +302,12 @@ PyObject *py_attn(PyObject *, PyObject *const *a, Py_ssize_t n) {
              "shape mismatch");
         const bool scaled = kv != FKV_KV_BF16;
         return call(g_attn, ptr(q), i32(batch), i32(q->size(1)), ptr(kc), ptr(vc), kv,
-                      scaled ? static_cast<const float *>(ptr(ks)) : nullptr,
-                      scaled ? static_cast<const float *>(ptr(vs)) : nullptr, i32(kc->size(0)), i32(kc->size(1)),
-                      i32(kc->size(2)), i32(dim), static_cast<const int32_t *>(ptr(indptr)),
-                      static_cast<const int32_t *>(ptr(indices)), indices->numel(),
-                      static_cast<const int32_t *>(ptr(lens)), static_cast<const uint8_t *>(ptr(mask)),
-                      static_cast<float>(number(a[6])), ptr(out), ptr(ws), ws->nbytes(), stream_of(a[12], dev));
+                    scaled ? static_cast<const float *>(ptr(ks)) : nullptr,
+                    scaled ? static_cast<const float *>(ptr(vs)) : nullptr, i32(kc->size(0)), i32(kc->size(1)),
+                    i32(kc->size(2)), i32(dim), static_cast<const int32_t *>(ptr(indptr)),
+                    static_cast<const int32_t *>(ptr(indices)), indices->numel(),
+                    static_cast<const int32_t *>(ptr(lens)), static_cast<const uint8_t *>(ptr(mask)),
+                    static_cast<float>(number(a[6])), ptr(out), ptr(ws), ws->nbytes(), stream_of(a[12], dev));
     });
 }
 

@@ -138,8 +138,9 @@ FKV_API fkv_status kv_append_bf16(const void *k_new, const void *v_new,
  * a block's s is then at most 74.7, so values up to six times the calibrated
  * maximum are still held without saturation.  An infinity saturates (its
  * block takes s = 448); a NaN makes its block's scale, and so its 16 values,
- * NaN.  A slot listed twice in one call ends with codes and scales of either
- * token, block by block; num_kv_heads is at most 32767.
+ * NaN.  A slot listed twice in one call ends with a mix of the two tokens' rows
+ * (a block may hold one's codes under the other's scale): list each slot once.
+ * num_kv_heads is at most 32767.
  */
 FKV_API fkv_status kv_append_fp4(const void *k_new, const void *v_new,
                          const int64_t *slot_mapping, int32_t n_tokens,
