@@ -24,6 +24,10 @@ Entry points (same names as the C ABI):
   kv_page_realloc                  bump tags (and optionally zero pages) of reallocated pages
   paged_decode_attn                decode attention over the paged cache
   paged_decode_attn_workspace_size bytes of scratch paged_decode_attn needs
+  kv_append_rope                   qk_norm_rope and the append of a step's keys and values in one pass
+  paged_tree_attn                  attention of every request's tree of drafted tokens over the paged cache
+  paged_window_attn                decode attention over a sliding window and a few first tokens
+  kv_tree_commit                   the accepted drafted tokens' rows moved into place, left-over pages given back
 """
 from __future__ import annotations
 
@@ -40,6 +44,8 @@ __all__ = [
     "paged_decode_attn_workspace_size",
     "alloc_workspace",
     "paged_decode_attn_noalloc",
+    "kv_append_rope", "paged_tree_attn", "paged_tree_attn_workspace_size", "alloc_tree_workspace", "paged_window_attn",
+    "kv_tree_commit",
     "device_error", "kernels_per_call", "selftest_wait", "EXPORTED_SYMBOLS",
 ]
 
@@ -54,6 +60,7 @@ DEVERR_REALLOC_PAGE = 0x8
 DEVERR_GATHER_SLOT = 0x10
 DEVERR_TABLES = 0x20
 DEVERR_ROPE_AXIS = 0x40
+DEVERR_TREE = 0x80
 HEAD_DIM = 128
 
 EXPORTED_SYMBOLS = (
@@ -63,6 +70,7 @@ EXPORTED_SYMBOLS = (
     "fkv_kernels_per_call", "fkv_selftest_wait",
     "kv_append_fp4", "kv_append_fp4_tag_check", "kv_gather", "qk_norm_rope", "kv_step_tables",
     "kv_step_tables_workspace_size",
+    "kv_append_rope", "paged_tree_attn_workspace_size", "paged_tree_attn", "paged_window_attn", "kv_tree_commit",
 )
 ERR_SCRATCH_LIMIT = 4
 NOALLOC_SCRATCH_BYTES = 16 << 20
@@ -72,7 +80,8 @@ _lock = threading.Lock()
 _lib = None
 _bind = None      # the compiled marshalling, once loaded
 _BIND_CALLS = ("fkv_status_string", "kv_append_fp4", "kv_append_fp4_tag_check", "kv_gather", "qk_norm_rope", "kv_step_tables",
-               "paged_decode_attn")      # the entry points that it calls, in the order its setup takes them
+               "paged_decode_attn", "kv_append_rope", "paged_tree_attn", "paged_window_attn",
+               "kv_tree_commit")         # the entry points that it calls, in the order its setup takes them
 
 
 class FkvError(RuntimeError):
@@ -138,6 +147,20 @@ def load_library():
         lib.paged_decode_attn_noalloc.restype = ctypes.c_int
         lib.paged_decode_attn_noalloc.argtypes = [P, i32, i32, P, P, i32, P, P, i32, i32, i32, i32, P, P, i64, P, P,
                                                   f32, P, P]
+        lib.kv_append_rope.restype = ctypes.c_int
+        lib.kv_append_rope.argtypes = [P, i64, i32, P, i64, P, i64, i32, P, i64, i32, P, P, f32, P, i32, P, P, i32, i32, f32, P,
+                                       i32, P, P, P, P, i32, i32, i32, P]
+        lib.paged_tree_attn_workspace_size.restype = ctypes.c_size_t
+        lib.paged_tree_attn_workspace_size.argtypes = [i32, i32, i32, i32, i32, i32]
+        lib.paged_tree_attn.restype = ctypes.c_int
+        lib.paged_tree_attn.argtypes = [P, i32, i32, P, P, i32, P, P, i32, i32, i32, i32, P, P, i64, P, i32, P, P, i32, i32, i32,
+                                        P, f32, P, P, ctypes.c_size_t, P]
+        lib.paged_window_attn.restype = ctypes.c_int
+        lib.paged_window_attn.argtypes = [P, i32, i32, P, P, i32, P, P, i32, i32, i32, i32, P, P, i64, P, i32, i32, P, f32, P, P,
+                                          ctypes.c_size_t, P]
+        lib.kv_tree_commit.restype = ctypes.c_int
+        lib.kv_tree_commit.argtypes = [P, P, i32, i32, i32, i32, i32, P, P, i64, P, i32, P, i32, P, i32, P, P, P, P, i32, P, P, P,
+                                       P]
         lib.fkv_device_error.restype = ctypes.c_int
         lib.fkv_device_error.argtypes = [ctypes.POINTER(ctypes.c_uint32), i32]
         lib.fkv_kernels_per_call.restype = i32
@@ -497,6 +520,66 @@ def paged_decode_attn_noalloc(q, k_cache, v_cache, page_indptr, page_indices, se
         *_attn_args(q, k_cache, v_cache, page_indptr, page_indices, seq_lens, sm_scale, out, k_scale, v_scale, abort_mask),
         _stream(stream)), "paged_decode_attn_noalloc")
     return out
+
+
+def kv_append_rope(q, k, v, positions, inv_freq, slot_mapping, q_out, k_cache, v_cache, k_scale=None, v_scale=None,
+                   q_weight=None, k_weight=None, eps=1e-6, axis_map=None, interleaved=False, rot_scale=1.0, stream=None):
+    """``qk_norm_rope`` of ``q`` [N][Hq][128] (into ``q_out``) and ``k``, with ``k``
+    and ``v`` [N][Hkv][128] going into the cache at ``slot_mapping`` [N] (int64, <0 =
+    skip) in the same pass; the keys are rounded once.  q, k and v are bf16, heads
+    contiguous, any token stride that is a multiple of 8.  Caches: FP8 uint8 /
+    float8_e4m3fn or bf16 [P][Hkv][S][128], or FP4 uint8 [P][Hkv][S][72]; scales fp32
+    [Hkv] unless bf16.  ``q_out`` may be q; ``q`` and ``q_out`` may be None."""
+    (_bind or _load_bind()).kv_append_rope(q, k, v, positions, inv_freq, slot_mapping, q_out, k_cache, v_cache, k_scale, v_scale,
+                                           q_weight, k_weight, eps, axis_map, interleaved, rot_scale, stream)
+    return q_out
+
+
+def paged_tree_attn_workspace_size(n_tokens, batch, num_q_heads, num_kv_heads, head_dim=HEAD_DIM, kv_dtype=KV_FP8_E4M3):
+    n = load_library().paged_tree_attn_workspace_size(n_tokens, batch, num_q_heads, num_kv_heads, head_dim, kv_dtype)
+    _need(n > 0, "unsupported shape for paged_tree_attn")
+    return int(n)
+
+
+def alloc_tree_workspace(n_tokens, batch, num_q_heads, num_kv_heads, kv_dtype=KV_FP8_E4M3, device="cuda"):
+    """Scratch for ``paged_tree_attn`` of n_tokens drafted tokens, or ``paged_window_attn`` (n_tokens = batch)."""
+    import torch
+    n = paged_tree_attn_workspace_size(n_tokens, batch, num_q_heads, num_kv_heads, HEAD_DIM, kv_dtype)
+    return torch.empty(n, dtype=torch.uint8, device=device)
+
+
+def paged_tree_attn(q, k_cache, v_cache, page_indptr, page_indices, seq_lens, token_indptr, tree_mask, sm_scale, out, workspace,
+                    k_scale=None, v_scale=None, abort_mask=None, window=0, sinks=0, stream=None):
+    """Attention of drafted tokens: rows ``token_indptr[r]`` .. of ``q``/``out`` [N][Hq][128] are
+    request r's, whose drafted tokens are the last of its ``seq_lens[r]`` cached ones.  A row sees the
+    committed tokens before them (with ``window``: those less than that far behind its own depth, and
+    the first ``sinks``) and drafted token j if bit j of its ``tree_mask`` (int64 or uint64 [N] or
+    [N][words], up to 4 words) is set.  The other arguments are ``paged_decode_attn``'s;
+    workspace from ``alloc_tree_workspace``."""
+    (_bind or _load_bind()).paged_tree_attn(q, k_cache, v_cache, page_indptr, page_indices, seq_lens, token_indptr, tree_mask,
+                                            sm_scale, out, workspace, k_scale, v_scale, abort_mask, window, sinks, stream)
+    return out
+
+
+def paged_window_attn(q, k_cache, v_cache, page_indptr, page_indices, seq_lens, sm_scale, out, workspace, window, sinks=0,
+                      k_scale=None, v_scale=None, abort_mask=None, stream=None):
+    """``paged_decode_attn`` over each request's last ``window`` tokens and its first ``sinks``;
+    workspace from ``alloc_tree_workspace(B, B, ...)``."""
+    (_bind or _load_bind()).paged_window_attn(q, k_cache, v_cache, page_indptr, page_indices, seq_lens, sm_scale, out, workspace,
+                                              k_scale, v_scale, abort_mask, window, sinks, stream)
+    return out
+
+
+def kv_tree_commit(k_cache, v_cache, page_indptr, page_indices, seq_lens, token_indptr, accepted, accepted_counts, lens_out,
+                   abort_mask=None, free_pages=None, free_count=None, free_left=None, page_tags=None, stream=None):
+    """Moves the cache rows of each request's accepted drafted tokens (``accepted`` int32 [B][max],
+    strictly increasing indices, ``accepted_counts`` [B]) behind its committed ones and writes the kept
+    lengths to ``lens_out``.  With ``free_pages``, ``free_count`` and ``free_left`` (which may be
+    free_count) the pages past them go back onto ``kv_step_tables``' free list, their ``page_tags``
+    bumped where given.  Requests that are aborted or not valid are left as they are."""
+    (_bind or _load_bind()).kv_tree_commit(k_cache, v_cache, page_indptr, page_indices, seq_lens, token_indptr, accepted,
+                                           accepted_counts, lens_out, abort_mask, free_pages, free_count, free_left, page_tags,
+                                           stream)
 
 
 def device_error(clear: bool = True) -> int:

@@ -22,6 +22,10 @@ decltype(&kv_gather) g_gather = nullptr;
 decltype(&qk_norm_rope) g_rope = nullptr;
 decltype(&kv_step_tables) g_tables = nullptr;
 decltype(&paged_decode_attn) g_attn = nullptr;
+decltype(&kv_append_rope) g_append_rope = nullptr;
+decltype(&paged_tree_attn) g_tree = nullptr;
+decltype(&paged_window_attn) g_window = nullptr;
+decltype(&kv_tree_commit) g_commit = nullptr;
 
 struct Refused {
     const char *why;
@@ -311,15 +315,157 @@ PyObject *py_attn(PyObject *, PyObject *const *a, Py_ssize_t n) {
     });
 }
 
-// setup(FkvError, status_string, append, append_check, gather, rope, tables, attn): the exception and the C entry
-// points' addresses.
+// q, k, v, positions, inv_freq, slots, q_out, k_cache, v_cache, k_scale, v_scale, q_weight, k_weight, eps, axis_map,
+// interleaved, rot_scale, stream
+PyObject *py_append_rope(PyObject *, PyObject *const *a, Py_ssize_t n) {
+    return guarded("kv_append_rope", n, 18, [&] {
+        const at::Tensor *q = tensor(a[0], true), *k = tensor(a[1]), *v = tensor(a[2]), *pos = tensor(a[3]), *freq = tensor(a[4]),
+                         *slots = tensor(a[5]), *qo = tensor(a[6], true), *kc = tensor(a[7]), *vc = tensor(a[8]),
+                         *ks = tensor(a[9], true), *vs = tensor(a[10], true), *qw = tensor(a[11], true),
+                         *kw = tensor(a[12], true), *map = tensor(a[14], true);
+        const int dev = device_of(*kc);
+        here(dev, {pos, freq, slots, kc, vc, ks, vs, qw, kw, map});
+        const int32_t kv = cache_format(*kc, *vc, ks, vs);
+        need((q == nullptr) == (qo == nullptr) && (!q || q->dim() == 3), "q and q_out go together, both [N][Hq][128]");
+        need(is(*slots, kI64), "slot_mapping must be int64");
+        const int64_t rows = slots->numel(), hk = kc->size(1), dim = kv == FKV_KV_FP4 ? 128 : kc->size(3), hq = q ? q->size(1) : 0;
+        const int64_t qst = q ? head_rows(*q, dev, rows, hq, dim) : 0, qos = q ? head_rows(*qo, dev, rows, hq, dim) : 0;
+        const int64_t kst = head_rows(*k, dev, rows, hk, dim), vst = head_rows(*v, dev, rows, hk, dim);
+        for (const at::Tensor *w : {qw, kw}) need(!w || (is(*w, kB16) && w->numel() == dim), "weights must be bf16 [128]");
+        need(is(*pos, kI32) && (pos->dim() == 1 || pos->dim() == 2) && pos->size(-1) == rows,
+             "positions must be int32 [N] or [axes][N]");
+        need(is(*freq, kF32) && freq->dim() == 1, "inv_freq must be float32 [R/2]");
+        need(!map || (is(*map, kU8) && map->numel() == freq->numel()), "axis_map must be uint8 [R/2]");
+        const int inter = PyObject_IsTrue(a[15]);
+        need(inter >= 0, "interleaved must be true or false");
+        const bool scaled = kv != FKV_KV_BF16;
+        return call(g_append_rope, ptr(q), qst, i32(hq), ptr(k), kst, ptr(v), vst, i32(hk), ptr(qo), qos, i32(rows), ptr(qw), ptr(kw),
+                    static_cast<float>(number(a[13])), static_cast<const int32_t *>(ptr(pos)),
+                    pos->dim() == 1 ? 1 : i32(pos->size(0)), static_cast<const float *>(ptr(freq)),
+                    static_cast<const uint8_t *>(ptr(map)), i32(2 * freq->numel()), inter, static_cast<float>(number(a[16])),
+                    static_cast<const int64_t *>(ptr(slots)), kv, scaled ? static_cast<const float *>(ptr(ks)) : nullptr,
+                    scaled ? static_cast<const float *>(ptr(vs)) : nullptr, ptr(kc), ptr(vc), i32(kc->size(0)), i32(kc->size(2)),
+                    i32(dim), stream_of(a[17], dev));
+    });
+}
+
+// The arguments that tree and window attention share.
+struct Paged {
+    const at::Tensor *q, *kc, *vc, *indptr, *indices, *lens, *out, *ws, *ks, *vs, *mask;
+    int dev;
+    int32_t kv, batch, dim;
+};
+Paged paged_args(PyObject *q, PyObject *kc, PyObject *vc, PyObject *indptr, PyObject *indices, PyObject *lens, PyObject *out,
+                 PyObject *ws, PyObject *ks, PyObject *vs, PyObject *mask) {
+    Paged p{tensor(q), tensor(kc), tensor(vc), tensor(indptr), tensor(indices), tensor(lens), tensor(out), tensor(ws),
+            tensor(ks, true), tensor(vs, true), tensor(mask, true), 0, 0, 0, 0};
+    p.dev = device_of(*p.q);
+    here(p.dev, {p.q, p.kc, p.vc, p.indptr, p.indices, p.lens, p.out, p.ws, p.ks, p.vs, p.mask});
+    p.kv = cache_format(*p.kc, *p.vc, p.ks, p.vs);
+    need(is(*p.q, kB16) && is(*p.out, kB16), "q/out must be bf16");
+    need(is(*p.lens, kI32), "seq_lens must be int32");
+    need(!p.mask || is(*p.mask, kU8), "abort_mask must be uint8");
+    need(tag32(*p.indptr) && tag32(*p.indices), "CSR must be int32");
+    need(p.q->dim() == 3 && p.out->sizes() == p.q->sizes(), "shape mismatch");
+    need(p.indptr->numel() >= 1, "page_indptr has batch + 1 entries");
+    p.batch = i32(p.indptr->numel() - 1);
+    p.dim = i32(p.q->size(2));
+    need((p.kv == FKV_KV_FP4 ? 128 : p.kc->size(3)) == p.dim && p.lens->numel() == p.batch &&
+             (!p.mask || p.mask->numel() == p.batch),
+         "shape mismatch");
+    if (p.kv == FKV_KV_BF16) p.ks = p.vs = nullptr;
+    return p;
+}
+int32_t small(PyObject *o, const char *why) {
+    const int64_t v = integer(o);
+    need(v >= 0 && v <= 0x7FFFFFFF, why);
+    return static_cast<int32_t>(v);
+}
+
+// q, k_cache, v_cache, indptr, indices, seq_lens, token_indptr, tree_mask, sm_scale, out, workspace, k_scale, v_scale,
+// abort_mask, window, sinks, stream
+PyObject *py_tree(PyObject *, PyObject *const *a, Py_ssize_t n) {
+    return guarded("paged_tree_attn", n, 17, [&] {
+        const Paged p = paged_args(a[0], a[1], a[2], a[3], a[4], a[5], a[9], a[10], a[11], a[12], a[13]);
+        const at::Tensor *rows = tensor(a[6]), *mask = tensor(a[7]);
+        here(p.dev, {rows, mask});
+        need(is(*rows, kI32) && rows->numel() == p.batch + 1, "token_indptr must be int32 [B + 1]");
+        need((is(*mask, kI64) || is(*mask, ScalarType::UInt64)) && (mask->dim() == 1 || mask->dim() == 2) &&
+                 mask->size(0) == p.q->size(0) && (mask->dim() == 1 || mask->size(1) >= 1),
+             "tree_mask must be int64 or uint64 [N] or [N][words]");
+        return call(g_tree, ptr(p.q), i32(p.q->size(0)), i32(p.q->size(1)), ptr(p.kc), ptr(p.vc), p.kv,
+                    static_cast<const float *>(ptr(p.ks)), static_cast<const float *>(ptr(p.vs)), i32(p.kc->size(0)),
+                    i32(p.kc->size(1)), i32(p.kc->size(2)), p.dim, static_cast<const int32_t *>(ptr(p.indptr)),
+                    static_cast<const int32_t *>(ptr(p.indices)), p.indices->numel(), static_cast<const int32_t *>(ptr(p.lens)),
+                    p.batch, static_cast<const int32_t *>(ptr(rows)), static_cast<const uint64_t *>(ptr(mask)),
+                    mask->dim() == 1 ? 1 : i32(mask->size(1)), small(a[14], "window must not be negative"),
+                    small(a[15], "sinks must not be negative"), static_cast<const uint8_t *>(ptr(p.mask)),
+                    static_cast<float>(number(a[8])), ptr(p.out), ptr(p.ws), p.ws->nbytes(), stream_of(a[16], p.dev));
+    });
+}
+
+// q, k_cache, v_cache, indptr, indices, seq_lens, sm_scale, out, workspace, k_scale, v_scale, abort_mask, window, sinks,
+// stream
+PyObject *py_window(PyObject *, PyObject *const *a, Py_ssize_t n) {
+    return guarded("paged_window_attn", n, 15, [&] {
+        const Paged p = paged_args(a[0], a[1], a[2], a[3], a[4], a[5], a[7], a[8], a[9], a[10], a[11]);
+        need(p.q->size(0) == p.batch, "shape mismatch");
+        return call(g_window, ptr(p.q), p.batch, i32(p.q->size(1)), ptr(p.kc), ptr(p.vc), p.kv,
+                    static_cast<const float *>(ptr(p.ks)), static_cast<const float *>(ptr(p.vs)), i32(p.kc->size(0)),
+                    i32(p.kc->size(1)), i32(p.kc->size(2)), p.dim, static_cast<const int32_t *>(ptr(p.indptr)),
+                    static_cast<const int32_t *>(ptr(p.indices)), p.indices->numel(), static_cast<const int32_t *>(ptr(p.lens)),
+                    small(a[12], "window must be positive"), small(a[13], "sinks must not be negative"),
+                    static_cast<const uint8_t *>(ptr(p.mask)), static_cast<float>(number(a[6])), ptr(p.out), ptr(p.ws),
+                    p.ws->nbytes(), stream_of(a[14], p.dev));
+    });
+}
+
+// k_cache, v_cache, indptr, indices, seq_lens, token_indptr, accepted, counts, lens_out, abort_mask, free_pages, free_count,
+// free_left, page_tags, stream
+PyObject *py_commit(PyObject *, PyObject *const *a, Py_ssize_t n) {
+    return guarded("kv_tree_commit", n, 15, [&] {
+        const at::Tensor *kc = tensor(a[0]), *vc = tensor(a[1]), *indptr = tensor(a[2]), *indices = tensor(a[3]), *lens = tensor(a[4]),
+                         *rows = tensor(a[5]), *acc = tensor(a[6]), *counts = tensor(a[7]), *kept = tensor(a[8]),
+                         *mask = tensor(a[9], true), *pages = tensor(a[10], true), *have = tensor(a[11], true),
+                         *left = tensor(a[12], true), *tags = tensor(a[13], true);
+        const int dev = device_of(*kc);
+        here(dev, {kc, vc, indptr, indices, lens, rows, acc, counts, kept, mask, pages, have, left, tags});
+        need(kc->dim() == 4 && vc->sizes() == kc->sizes(), "k_cache and v_cache shapes differ");
+        const bool b16 = is(*kc, kB16);
+        need(b16 ? is(*vc, kB16) : bytes8(*kc) && bytes8(*vc), "caches must both be uint8 (e4m3, or FP4 rows of 72) or bf16");
+        const bool fp4 = is(*kc, kU8) && is(*vc, kU8) && kc->size(3) == FKV_FP4_ROW_BYTES;
+        for (const at::Tensor *t : {indptr, indices, lens, rows, acc, counts, kept})
+            need(is(*t, kI32), "CSR, lengths, token_indptr and accepted lists must be int32");
+        const int64_t batch = indptr->numel() - 1;
+        need(batch >= 0 && lens->numel() == batch && rows->numel() == batch + 1 && counts->numel() == batch &&
+                 kept->numel() == batch && acc->dim() == 2 && acc->size(0) == batch,
+             "one length, count and list per request, indptr arrays of B + 1");
+        need(!mask || (is(*mask, kU8) && mask->numel() == batch), "abort_mask must be uint8 [B]");
+        need((pages != nullptr) == (have != nullptr) && (pages != nullptr) == (left != nullptr) && (pages || !tags),
+             "free_pages, free_count and free_left go together");
+        for (const at::Tensor *t : {pages, have, left}) need(!t || is(*t, kI32), "the free list must be int32");
+        need(!pages || (have->numel() == 1 && left->numel() == 1), "free counts of one value");
+        need(!tags || (tag32(*tags) && tags->numel() == kc->size(0)), "page_tags must be 32-bit, one per page of the pool");
+        return call(g_commit, ptr(kc), ptr(vc), b16 ? FKV_KV_BF16 : fp4 ? FKV_KV_FP4 : FKV_KV_FP8_E4M3, i32(kc->size(0)),
+                    i32(kc->size(1)), i32(kc->size(2)), fp4 ? 128 : i32(kc->size(3)), static_cast<const int32_t *>(ptr(indptr)),
+                    static_cast<const int32_t *>(ptr(indices)), indices->numel(), static_cast<const int32_t *>(ptr(lens)), i32(batch),
+                    static_cast<const int32_t *>(ptr(rows)), 0x7FFFFFFF, static_cast<const int32_t *>(ptr(acc)), i32(acc->size(1)),
+                    static_cast<const int32_t *>(ptr(counts)), static_cast<const uint8_t *>(ptr(mask)),
+                    static_cast<int32_t *>(ptr(kept)), static_cast<int32_t *>(ptr(pages)), pages ? i32(pages->numel()) : 0,
+                    static_cast<const int32_t *>(ptr(have)), static_cast<int32_t *>(ptr(left)), static_cast<uint32_t *>(ptr(tags)),
+                    stream_of(a[14], dev));
+    });
+}
+
+// setup(FkvError, status_string, append, append_check, gather, rope, tables, attn, append_rope, tree, window, commit): the
+// exception and the C entry points' addresses.
 PyObject *py_setup(PyObject *, PyObject *const *a, Py_ssize_t n) {
-    if (n != 8) {
-        PyErr_SetString(PyExc_TypeError, "setup takes 8 arguments");
+    if (n != 12) {
+        PyErr_SetString(PyExc_TypeError, "setup takes 12 arguments");
         return nullptr;
     }
-    void *f[8] = {};
-    for (int i = 1; i < 8; ++i) {
+    void *f[12] = {};
+    for (int i = 1; i < 12; ++i) {
         f[i] = PyLong_AsVoidPtr(a[i]);
         if (!f[i]) {
             if (!PyErr_Occurred()) PyErr_SetString(PyExc_ValueError, "an entry point is missing");
@@ -336,6 +482,10 @@ PyObject *py_setup(PyObject *, PyObject *const *a, Py_ssize_t n) {
     g_rope = reinterpret_cast<decltype(g_rope)>(f[5]);
     g_tables = reinterpret_cast<decltype(g_tables)>(f[6]);
     g_attn = reinterpret_cast<decltype(g_attn)>(f[7]);
+    g_append_rope = reinterpret_cast<decltype(g_append_rope)>(f[8]);
+    g_tree = reinterpret_cast<decltype(g_tree)>(f[9]);
+    g_window = reinterpret_cast<decltype(g_window)>(f[10]);
+    g_commit = reinterpret_cast<decltype(g_commit)>(f[11]);
     Py_RETURN_NONE;
 }
 
@@ -347,6 +497,10 @@ PyMethodDef methods[] = {FKV_METHOD("setup", py_setup),
                          FKV_METHOD("qk_norm_rope", py_rope),
                          FKV_METHOD("kv_step_tables", py_tables),
                          FKV_METHOD("paged_decode_attn", py_attn),
+                         FKV_METHOD("kv_append_rope", py_append_rope),
+                         FKV_METHOD("paged_tree_attn", py_tree),
+                         FKV_METHOD("paged_window_attn", py_window),
+                         FKV_METHOD("kv_tree_commit", py_commit),
                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_fkv_bind", "Argument marshalling of a decode step's calls.", -1, methods,
                       nullptr, nullptr, nullptr, nullptr};

@@ -20,14 +20,13 @@
 // stores (5.9 TB/s); 64 tokens of 72 heads: 3.4, 2.7 and 2.7 us.
 #include <cmath>
 
-#include "fkv_common.cuh"
+#include "rope.cuh"
 
 namespace fkv {
 
 constexpr int kRopeBlock = 128;
 constexpr int kRopeUnroll = 4;                 // rows a half-warp has in flight
 constexpr int kRopeBatch = 2 * kRopeUnroll;    // rows of a warp's batch
-constexpr int kRopeMaxAxes = 8;
 
 struct RopeParams {
     const uint16_t *q, *k;          // bf16
@@ -41,32 +40,6 @@ struct RopeParams {
     int32_t n_tokens, hq, heads, parts, rows_per_warp, n_axes, half;
     float eps, rot_scale;
 };
-
-// cos and sin of pos * f.  The angle is formed in turns, pos * (f / 2 pi), with
-// 1 / (2 pi) and the products in two fp32 words: pos is split into two exact
-// 16-bit parts, each product's rounding error comes from one fma, and whole
-// turns leave before sin and cos see the rest.  With |pos * f| < 2^31 the angle
-// is off by less than 2^-18 of a turn; for |pos * f| < 2^20 by about 2^-23.
-__device__ __forceinline__ float2 cos_sin_of(int32_t pos, float f) {
-    const float inv_hi = 0.15915494f;                          // RN(1 / (2 pi))
-    const float inv_lo = 6.4206382e-09f;                       // 1 / (2 pi) - inv_hi
-    const float ch = f * inv_hi;
-    const float cl = fmaf(f, inv_lo, fmaf(f, inv_hi, -ch));
-    const int32_t lo16 = pos & 0xFFFF;
-    const float a = static_cast<float>(pos - lo16), b = static_cast<float>(lo16);
-    const float ha = a * ch, hb = b * ch;
-    float ea = fmaf(a, cl, fmaf(a, ch, -ha));
-    const float eb = fmaf(b, cl, fmaf(b, ch, -hb));
-    ea -= rintf(ea);                                           // |ha| past 2^24 leaves whole turns here
-    const float r = ((ha - rintf(ha)) + (hb - rintf(hb))) + (ea + eb);
-    float s, c;
-    sincospif(2.f * r, &s, &c);
-    return make_float2(c, s);
-}
-
-__device__ __forceinline__ float2 bf16x2_to_f32(uint32_t w) {
-    return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
-}
 
 // A lane's 8 elements (or weights) as the first and second elements of its four
 // pairs.  d0, d1: its two groups of four elements, in units of four.

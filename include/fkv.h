@@ -81,12 +81,14 @@ typedef enum {
 
 /* Bits of the sticky device error word. */
 #define FKV_DEVERR_APPEND_SLOT   0x1u  /* kv_append_*: slot beyond the pool, token skipped */
-#define FKV_DEVERR_ATTN_PAGE     0x2u  /* paged_decode_attn: page id outside [0, num_pages), row zeroed */
+#define FKV_DEVERR_ATTN_PAGE     0x2u  /* paged_*_attn: page id outside [0, num_pages), row zeroed */
 #define FKV_DEVERR_TIMEOUT       0x4u  /* a bounded wait on a copy gave up; the call's output is not valid */
 #define FKV_DEVERR_REALLOC_PAGE  0x8u  /* kv_page_realloc: a listed id is outside [0, num_pages), skipped */
 #define FKV_DEVERR_GATHER_SLOT   0x10u /* kv_gather: slot beyond the pool, its rows written as zeros */
 #define FKV_DEVERR_TABLES        0x20u /* kv_step_tables: a request was refused, or a free page id is outside [0, num_pages) */
-#define FKV_DEVERR_ROPE_AXIS     0x40u /* qk_norm_rope: an axis_map entry is not below n_axes, its pair was not turned */
+#define FKV_DEVERR_ROPE_AXIS     0x40u /* qk_norm_rope, kv_append_rope: an axis_map entry is not below n_axes, its pair was not turned */
+#define FKV_DEVERR_TREE          0x80u /* kv_tree_commit: a kept list or a drafted token's page is not valid (the request was left
+                                          as it was), or the free list has no room (no page was given back) */
 
 FKV_API const char *fkv_status_string(fkv_status s);
 
@@ -511,6 +513,150 @@ FKV_API fkv_status paged_decode_attn_noalloc(const void *q, int32_t batch, int32
                                      const int32_t *page_indptr, const int32_t *page_indices,
                                      int64_t nnz, const int32_t *seq_lens, const uint8_t *abort_mask,
                                      float sm_scale, void *out, void *stream);
+
+/*
+ * kv_append_rope -- qk_norm_rope and the append in one pass: the query heads are
+ * normed, turned and written as bf16, the key heads normed, turned and put into
+ * the cache, the value heads put into the cache as they are.  Norm and rotation
+ * are qk_norm_rope's; keys are quantised from their fp32 values, rounded once
+ * (qk_norm_rope followed by kv_append_* rounds them to bf16 in between):
+ *   FP8:  code = e4m3_rne_satfinite( x / scale[h] )
+ *   FP4:  kv_append_fp4's blocks and codes, with x for the bf16 element
+ *   BF16: bf16_rne(x)
+ * (a key's quotient is within an fp32 ulp of x / scale[h]; the values' codes are
+ * the bytes of kv_append_fp8, kv_append_bf16 or kv_append_fp4.)
+ *
+ *   q, k, v        bf16, token n's heads at q + n * q_token_stride (elements):
+ *                  rows of 128, contiguous; token strides are multiples of 8, so
+ *                  the three may lie in one projection's output.  q and q_out may
+ *                  be NULL with num_q_heads 0
+ *   q_out          bf16, with its own token stride; may be q itself (in place)
+ *                  but must not overlap q, k or v otherwise
+ *   q_weight ... rot_scale  as in qk_norm_rope
+ *   slot_mapping, k_scale, v_scale, k_cache, v_cache  as in kv_append_fp8, with
+ *                  pools of dtype kv_dtype; scales are ignored (may be NULL) for
+ *                  BF16.  A token whose slot is < 0 or whose page is >= num_pages
+ *                  (which sets FKV_DEVERR_APPEND_SLOT) still has its query heads
+ *                  turned.  List each slot once.
+ * num_kv_heads is at most 32767.  n_tokens == 0 is a no-op.
+ */
+FKV_API fkv_status kv_append_rope(const void *q, int64_t q_token_stride, int32_t num_q_heads,
+                                  const void *k, int64_t k_token_stride,
+                                  const void *v, int64_t v_token_stride, int32_t num_kv_heads,
+                                  void *q_out, int64_t q_out_token_stride, int32_t n_tokens,
+                                  const void *q_weight, const void *k_weight, float eps,
+                                  const int32_t *positions, int32_t n_axes, const float *inv_freq,
+                                  const uint8_t *axis_map, int32_t rotary_dim, int32_t interleaved,
+                                  float rot_scale, const int64_t *slot_mapping, int32_t kv_dtype,
+                                  const float *k_scale, const float *v_scale,
+                                  void *k_cache, void *v_cache, int32_t num_pages, int32_t page_size,
+                                  int32_t head_dim, void *stream);
+
+/*
+ * paged_tree_attn -- attention of drafted tokens over the paged cache.  Request r
+ * has n = token_indptr[r + 1] - token_indptr[r] drafted tokens (kv_step_tables'
+ * new tokens), already in the cache as the last n of its seq_lens[r] tokens; c =
+ * seq_lens[r] - n tokens are committed.  Its i-th query row sees
+ *   - drafted token j (position c + j) if bit j % 64 of word j / 64 of the row's
+ *     tree_mask is set: its ancestors in the tree, and itself;
+ *   - committed token t if window is 0, or t < sinks, or t > p - window with p =
+ *     c + max(0, bits set in its mask - 1), the position of its depth in the tree.
+ * and out = softmax(sm_scale * q . k) v over what it sees, as in paged_decode_attn.
+ * Bits of tokens that are not there are ignored.  A row that sees nothing is
+ * zeros.  What a row does not see has no part in it, whatever it holds (NaN,
+ * infinities).  Any order of the drafted tokens is taken; positions (depths) of
+ * siblings are the caller's, in kv_append_rope.
+ *
+ *   q, out         bf16 [n_tokens][num_q_heads][head_dim], rows of request r at
+ *                  token_indptr[r] ..; rows that are no request's are not written
+ *   token_indptr   int32 [batch + 1]
+ *   tree_mask      uint64 [n_tokens][mask_words], mask_words 1 .. 4
+ *   window, sinks  0 and 0: no window (sinks has no effect without one)
+ *   workspace      paged_tree_attn_workspace_size(...) bytes, 256-byte aligned, no
+ *                  initialisation needed, not shared by calls that overlap on
+ *                  the GPU (two captured graphs that may run at once need two)
+ *   the others     as in paged_decode_attn
+ * Fail closed: the rows of a request that is aborted, has a malformed CSR row, has
+ * n > seq_lens[r], n > 64 * mask_words, more tokens than its pages hold, or a page
+ * that it reads outside [0, num_pages) (FKV_DEVERR_ATTN_PAGE) are zeros.  token_indptr
+ * entries that are negative, decreasing or past n_tokens leave the request's rows
+ * unwritten.
+ * Deterministic: the same call gives the same bytes every time.
+ * Supported: head_dim 128, page_size in {16, 32, 64, 128}, up to 128 query heads
+ * per KV head.  batch == 0 or n_tokens == 0 is a no-op.
+ */
+FKV_API size_t paged_tree_attn_workspace_size(int32_t n_tokens, int32_t batch, int32_t num_q_heads,
+                                              int32_t num_kv_heads, int32_t head_dim, int32_t kv_dtype);
+FKV_API fkv_status paged_tree_attn(const void *q, int32_t n_tokens, int32_t num_q_heads,
+                                   const void *k_cache, const void *v_cache, int32_t kv_dtype,
+                                   const float *k_scale, const float *v_scale,
+                                   int32_t num_pages, int32_t num_kv_heads,
+                                   int32_t page_size, int32_t head_dim,
+                                   const int32_t *page_indptr, const int32_t *page_indices,
+                                   int64_t nnz, const int32_t *seq_lens, int32_t batch,
+                                   const int32_t *token_indptr, const uint64_t *tree_mask,
+                                   int32_t mask_words, int32_t window, int32_t sinks,
+                                   const uint8_t *abort_mask, float sm_scale, void *out,
+                                   void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * paged_window_attn -- decode attention over a sliding window and a few first
+ * tokens: paged_decode_attn's arguments and results, over the tokens
+ *     t < sinks  or  t >= seq_lens[r] - window
+ * of request r, whose query is its last token.  window >= 1, sinks >= 0.  Pages
+ * whose tokens are all outside are not read and may hold any id.  The workspace
+ * is paged_tree_attn_workspace_size(batch, batch, ...) bytes; limits, failing
+ * closed and determinism are paged_tree_attn's.
+ */
+FKV_API fkv_status paged_window_attn(const void *q, int32_t batch, int32_t num_q_heads,
+                                     const void *k_cache, const void *v_cache, int32_t kv_dtype,
+                                     const float *k_scale, const float *v_scale,
+                                     int32_t num_pages, int32_t num_kv_heads,
+                                     int32_t page_size, int32_t head_dim,
+                                     const int32_t *page_indptr, const int32_t *page_indices,
+                                     int64_t nnz, const int32_t *seq_lens, int32_t window, int32_t sinks,
+                                     const uint8_t *abort_mask, float sm_scale, void *out,
+                                     void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * kv_tree_commit -- after the drafted tokens of a step are verified: the kept ones'
+ * cache rows move to where the next step expects them.  With n, c as in
+ * paged_tree_attn and the kept path accepted[r][0 .. accepted_counts[r]) (indices of
+ * drafted tokens, strictly increasing: parents come before children):
+ *   - for i = 0, 1, ...: the K and V rows of position c + accepted[r][i] go to
+ *     position c + i (all KV heads);
+ *   - lens_out[r] = c + accepted_counts[r], the length kept for the next step;
+ *   - with free_pages: the request's pages past ceil(lens_out[r] / page_size) go
+ *     back onto the free list, their live tags bumped by one if page_tags is given
+ *     (holders of the old tag fail the check).  They are pushed so that the next
+ *     kv_step_tables takes them in the order in which this step did: request 0's
+ *     first one is on top.
+ * An aborted request, one with a malformed CSR row or token_indptr, and one with n >
+ * seq_lens[r] or more tokens than its pages hold is left as it is: no row moves,
+ * lens_out[r] is not written, no page goes back.  So is one whose list is not strictly
+ * increasing, leaves [0, n), or is longer than n or max_accepted, and one with a
+ * drafted token's page outside [0, num_pages); these set FKV_DEVERR_TREE.
+ *
+ *   k_cache, v_cache  pools of dtype kv_dtype; bytes of other rows are not touched
+ *   accepted       int32 [batch][max_accepted]; accepted_counts int32 [batch]
+ *   lens_out       int32 [batch], not seq_lens itself (kv_step_tables' cached_lens_out
+ *                  fits: it is already the length kept for requests left as they are)
+ *   free_pages     int32 [num_free], free_count int32 [1] (the entries in use), free_left
+ *                  int32 [1] (in use afterwards; may be free_count), page_tags uint32
+ *                  [num_pages] or NULL; or all NULL and num_free 0: no page goes back.
+ *                  Without room for all pages none goes back (FKV_DEVERR_TREE).
+ * A request's drafted positions must lie on pages of its own.  batch == 0 with a free
+ * list still writes free_left.
+ */
+FKV_API fkv_status kv_tree_commit(void *k_cache, void *v_cache, int32_t kv_dtype, int32_t num_pages,
+                                  int32_t num_kv_heads, int32_t page_size, int32_t head_dim,
+                                  const int32_t *page_indptr, const int32_t *page_indices, int64_t nnz,
+                                  const int32_t *seq_lens, int32_t batch, const int32_t *token_indptr,
+                                  int32_t n_tokens, const int32_t *accepted, int32_t max_accepted,
+                                  const int32_t *accepted_counts, const uint8_t *abort_mask,
+                                  int32_t *lens_out, int32_t *free_pages, int32_t num_free,
+                                  const int32_t *free_count, int32_t *free_left, uint32_t *page_tags,
+                                  void *stream);
 
 /*
  * fkv_device_error -- read (and optionally clear) the sticky device error word

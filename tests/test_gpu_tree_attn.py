@@ -1,0 +1,364 @@
+"""paged_tree_attn and paged_window_attn on the GPU against a dense softmax in 64 bits."""
+import numpy as np
+import pytest
+
+import draft_ref as T
+from fp8_paged_kv_decode_gb300 import workloads as W
+from gpu_util import bf16_out, dev
+
+pytestmark = pytest.mark.gpu
+D = 128
+KINDS = ["fp8", "bf16", "fp4"]
+
+
+class Case:
+    """Requests of c committed and n drafted tokens over scattered pages."""
+
+    def __init__(self, kind, Hq, H, S, ctx, n, seed, words=None, q_std=1.0, sets=None, spare=5):
+        rng = np.random.default_rng(seed)
+        self.kind, self.Hq, self.H, self.S, self.rng = kind, Hq, H, S, rng
+        self.ctx, self.n = np.asarray(ctx), np.asarray(n)
+        self.lens = (self.ctx + self.n).astype(np.int32)
+        self.tptr = np.concatenate([[0], np.cumsum(self.n)]).astype(np.int32)
+        pages = -(-self.lens.astype(np.int64) // S)
+        self.P = int(pages.sum()) + spare
+        self.ptr = np.concatenate([[0], np.cumsum(pages)]).astype(np.int32)
+        self.idx = rng.permutation(self.P)[:int(pages.sum())].astype(np.int32)
+        (self.kc, self.ks), (self.vc, self.vs) = T.pool(rng, kind, self.P, H, S), T.pool(rng, kind, self.P, H, S)
+        if kind == "bf16":
+            self.ks = self.vs = None
+        self.N = int(self.n.sum())
+        self.q = W.bf16_bits((q_std * rng.standard_normal((self.N, Hq, D))).astype(np.float32))
+        self.sets = sets if sets is not None else [m for k in self.n for m in T.random_tree(rng, int(k))]
+        self.words = words or max(1, -(-int(max(self.n, default=1)) // 64))
+        self.sm = 1.0 / np.sqrt(D)
+        self.dead = None
+
+    def ref(self, window=0, sinks=0):
+        return T.tree_attention(self.q, self.kc, self.vc, self.kind, self.ks, self.vs, self.ptr, self.idx, self.lens, self.tptr, self.sets, self.sm,
+                                window, sinks, self.dead, 64 * self.words)
+
+    def tensors(self):
+        import torch
+        b16 = dict(dtype=torch.bfloat16)
+        pool = (lambda a: dev(a, **b16)) if self.kind == "bf16" else dev
+        return dict(q=dev(self.q, **b16), k_cache=pool(self.kc), v_cache=pool(self.vc), page_indptr=dev(self.ptr), page_indices=dev(self.idx),
+                    seq_lens=dev(self.lens), sm_scale=self.sm, out=torch.full((self.N, self.Hq, D), float("nan"), device="cuda", **b16),
+                    workspace=self.workspace(), k_scale=None if self.ks is None else dev(self.ks), v_scale=None if self.vs is None else dev(self.vs),
+                    abort_mask=None if self.dead is None else dev(self.dead.astype(np.uint8)))
+
+    def workspace(self):
+        import fp8_paged_kv_decode_gb300 as fkv
+        ws = fkv.alloc_tree_workspace(self.N, len(self.lens), self.Hq, self.H, dict(fp8=fkv.KV_FP8_E4M3, bf16=fkv.KV_BF16, fp4=fkv.KV_FP4)[self.kind])
+        return ws.fill_(0xA5)                                       # no initialisation is needed
+
+    def tree(self, t=None, **k):
+        import fp8_paged_kv_decode_gb300 as fkv
+        t = t or self.tensors()
+        fkv.paged_tree_attn(**t, token_indptr=dev(self.tptr), tree_mask=dev(T.words_of(self.sets, self.words).view(np.int64)), **k)
+        return t["out"]
+
+    def window(self, t=None, **k):
+        import fp8_paged_kv_decode_gb300 as fkv
+        t = t or self.tensors()
+        fkv.paged_window_attn(**t, **k)
+        return t["out"]
+
+    def check(self, out, window=0, sinks=0):
+        want, vmax, written = self.ref(window, sinks)
+        got = bf16_out(out)
+        assert np.isnan(got[~written]).all()                        # rows of no request are not written
+        got, want, vmax = got[written], want[written], vmax[written]
+        assert np.array_equal(np.isnan(got), np.isnan(want)), np.argwhere(np.isnan(got) != np.isnan(want))[:4]
+        fine = np.isfinite(want) & np.isfinite(vmax)
+        # bf16's half step, 2^-8 of the value; a weight in 11 bits (f16), or two words of 8 (bf16), and the logit in
+        # fp32 (|z| < 40 over 128 products: 2^-24 * 40 * 12 < 2^-15) move the mean by at most 2^-11 + 2^-12 of max|v|,
+        # the normaliser included
+        err = np.abs(got - want)
+        tol = 2.0 ** -8 * np.abs(want) + (2.0 ** -11 + 2.0 ** -12) * vmax
+        with np.errstate(all="ignore"):
+            bad = (err > tol) & fine
+        assert not bad.any(), (int(bad.sum()), np.argwhere(bad)[:4].tolist(), float(err[fine].max()))
+        odd = ~np.isfinite(want)
+        assert np.array_equal(got[odd & ~np.isnan(want)], want[odd & ~np.isnan(want)])
+
+
+SHAPES = [  # q heads, KV heads, page, committed, drafted
+    (8, 2, 16, [0], [1]), (8, 2, 16, [1, 0, 15, 16, 17], [1, 3, 1, 16, 2]), (4, 4, 32, [5, 300, 127, 128, 129], [2, 7, 1, 4, 5]),
+    (64, 8, 64, [1000, 63, 64, 65], [8, 8, 8, 8]), (16, 2, 128, [511, 512, 513, 0], [16, 1, 17, 5]), (6, 2, 16, [40, 0, 333], [11, 1, 64]),
+    (24, 2, 32, [200, 77], [13, 3]), (40, 8, 64, [150, 700], [6, 9]), (16, 1, 64, [90], [61]), (5, 1, 128, [1300], [33]),
+    (128, 1, 16, [70, 20], [2, 1]), (64, 1, 32, [129], [5]), (8, 8, 64, [2000] * 3, [4, 0, 1])]
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("Hq,H,S,ctx,n", SHAPES)
+def test_trees(kind, Hq, H, S, ctx, n):
+    import fp8_paged_kv_decode_gb300 as fkv
+    fkv.device_error()
+    c = Case(kind, Hq, H, S, ctx, n, seed=Hq + S + len(ctx))
+    c.check(c.tree())
+    assert fkv.device_error() == 0
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("window,sinks", [(1, 0), (1, 3), (2, 0), (7, 1), (64, 4), (100, 130), (129, 16), (500, 0), (10 ** 9, 4), (2 ** 31 - 1, 2 ** 31 - 1)])
+def test_trees_with_a_window(kind, window, sinks):
+    c = Case(kind, 16, 2, 16, [0, 1, 40, 200, 333, 640, 1000], [3, 5, 12, 1, 20, 7, 9], seed=window % 1000 + sinks % 1000)
+    c.check(c.tree(window=window, sinks=sinks), window, sinks)
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("Hq,H,S", [(8, 2, 16), (4, 4, 32), (64, 8, 64), (16, 1, 128), (24, 2, 64)])
+@pytest.mark.parametrize("window,sinks", [(1, 0), (1, 1), (64, 4), (130, 0), (300, 200), (1024, 16), (2 ** 31 - 1, 0)])
+def test_windows(kind, Hq, H, S, window, sinks):
+    import fp8_paged_kv_decode_gb300 as fkv
+    fkv.device_error()
+    lens = np.array([1, 2, 63, 64, 65, 127, 128, 129, 130, 131, 256, 300, 1025, 1500])
+    c = Case(kind, Hq, H, S, lens - 1, np.ones(len(lens), int), seed=Hq + S, sets=[1] * len(lens))
+    c.check(c.window(window=window, sinks=sinks), window, sinks)
+    assert fkv.device_error() == 0
+
+
+@pytest.mark.parametrize("kind", KINDS)
+def test_many_drafted_tokens(kind):
+    """Up to 256, several words, query rows of several tiles."""
+    c = Case(kind, 8, 2, 32, [300, 10, 0, 129], [130, 64, 256, 65], seed=3)
+    assert c.words == 4
+    c.check(c.tree())
+    c.check(c.tree(window=90, sinks=5), 90, 5)
+
+
+@pytest.mark.parametrize("kind", KINDS)
+def test_long_contexts(kind):
+    """Units split over many blocks."""
+    c = Case(kind, 16, 2, 64, [9000, 30, 20001], [4, 2, 7], seed=5)
+    c.check(c.tree())
+    c.check(c.tree(window=6000, sinks=100), 6000, 100)
+
+
+@pytest.mark.parametrize("batch", [130, 700, 3000])
+def test_many_requests(batch):
+    rng = np.random.default_rng(batch)
+    c = Case("fp8", 4, 1, 16, rng.integers(0, 200, batch), rng.integers(0, 4, batch), seed=batch)
+    c.check(c.tree())
+    c = Case("fp4", 2, 2, 16, rng.integers(0, 90, batch), np.ones(batch, int), seed=batch, sets=[1] * batch)
+    c.check(c.window(window=33, sinks=2), 33, 2)
+
+
+@pytest.mark.parametrize("kind", KINDS)
+def test_masks_that_are_no_trees(kind):
+    """Rows that see nothing, not themselves, later tokens, or bits of tokens that are not there."""
+    ctx, n = [0, 0, 50, 130], [3, 70, 5, 4]
+    rng = np.random.default_rng(8)
+    sets = [0, 0b100, 0] + [int(rng.integers(0, 2 ** 62)) << 7 for _ in range(70)] + [0, 0b10, 0b11111, 2 ** 63, (2 ** 128 - 1)] + [2 ** 100, 0b1000, 0, 1]
+    c = Case(kind, 8, 2, 16, ctx, n, seed=9, sets=sets)
+    out = c.tree()
+    c.check(out)
+    assert (bf16_out(out)[[0, 2]] == 0).all()
+    c.check(c.tree(window=2, sinks=0), 2, 0)
+
+
+@pytest.mark.parametrize("kind", KINDS)
+def test_nan_and_infinity_where_rows_do_not_look(kind):
+    """A NaN or infinity in K or V reaches the rows that see its token, and no other."""
+    ctx, n, S = [37, 300, 5], [6, 9, 4], 16
+    c = Case(kind, 8, 2, S, ctx, n, seed=11)
+    nan = {"fp8": 0x7F, "bf16": 0x7FC0, "fp4": 0x7F}[kind]
+
+    def put(cache, r, t, d, value):
+        pg, off = c.idx[c.ptr[r] + t // S], t % S
+        cache[pg, :, off, 64 + d // 16 if kind == "fp4" else d] = value
+    put(c.vc, 0, 37 + 2, 5, nan)                                   # a drafted token's V
+    put(c.kc, 1, 300 + 4, 100, nan)                                # and K
+    put(c.vc, 1, 300 + 8, 77, nan)                                 # one that only itself sees
+    put(c.vc, 2, 5 + 1, 127, nan)
+    put(c.vc, 2, 5 + 3, 0, nan)
+    if kind == "bf16":
+        put(c.vc, 0, 37 + 4, 6, 0x7F80)
+        put(c.vc, 2, 5 + 2, 9, 0xFF80)
+    # slots past the last token, pages' ends
+    for r in range(3):
+        for t in range(ctx[r] + n[r], -(-(ctx[r] + n[r]) // S) * S):
+            put(c.kc, r, t, 3, nan)
+            put(c.vc, r, t, 50, nan)
+    c.check(c.tree())
+    # committed tokens that a window leaves out, for the deeper rows or for all
+    c = Case(kind, 8, 2, S, ctx, n, seed=12)
+    for t in range(280, 299):
+        put(c.vc, 1, t, t % 128, nan)
+    put(c.kc, 1, 100, 1, nan)
+    put(c.vc, 1, 100, 1, nan)
+    c.check(c.tree(window=12, sinks=3), 12, 3)
+    w = Case(kind, 8, 2, S, [300, 200], [1, 1], seed=13, sets=[1, 1])
+    for t in (0, 1, 3, 250, 289):
+        pg, off = w.idx[w.ptr[0] + t // S], t % S
+        w.kc[pg, :, off, -1] = w.vc[pg, :, off, -1] = nan
+    w.check(w.window(window=11, sinks=0), 11, 0)
+    w.check(w.window(window=12, sinks=1), 12, 1)                   # sees 289 and 0
+
+
+@pytest.mark.parametrize("kind", KINDS)
+def test_failing_closed(kind):
+    import fp8_paged_kv_decode_gb300 as fkv
+    fkv.device_error()
+    ctx, n = [100, 40, 70, 200, 30, 60, 90, 10], [5, 3, 8, 2, 4, 6, 7, 1]
+    c = Case(kind, 8, 2, 16, ctx, n, seed=14)
+    c.dead = np.array([0, 1, 0, 0, 0, 0, 0, 0])
+    c.lens[2] = 7                                                  # fewer tokens than drafted ones
+    c.lens[3] = 300                                                # more than its pages hold
+    c.lens[5] = 0
+    c.check(c.tree())
+    assert fkv.device_error() == 0
+    c.idx[c.ptr[4] + 1], c.idx[c.ptr[6] + 2] = c.P, -1              # pages outside the pool
+    out = c.tree()
+    c.check(out)
+    assert fkv.device_error() == fkv.DEVERR_ATTN_PAGE
+    got = bf16_out(out)
+    for r in (1, 2, 3, 4, 5, 6):
+        assert (got[c.tptr[r]:c.tptr[r + 1]] == 0).all()
+    assert (np.abs(got[:5]).max(-1) > 0).all()
+    c.ptr[1] = -4                                                  # requests 0 and 1
+    c.check(c.tree())
+    fkv.device_error()
+
+
+def test_page_outside_the_window_is_not_read():
+    import fp8_paged_kv_decode_gb300 as fkv
+    fkv.device_error()
+    c = Case("fp8", 8, 2, 16, [400, 500], [1, 1], seed=15, sets=[1, 1])
+    want = bf16_out(c.window(window=60, sinks=5))
+    c.idx[c.ptr[0] + 3:c.ptr[0] + 20] = -1
+    got = bf16_out(c.window(window=60, sinks=5))
+    assert np.array_equal(got, want) and fkv.device_error() == 0
+
+
+def test_rows_of_no_request():
+    """token_indptr that begins late, ends early or is out of order."""
+    c = Case("fp8", 8, 2, 16, [100, 40, 70, 20], [5, 3, 8, 4], seed=16)
+    c.tptr[0], c.tptr[4] = 2, 18                                   # rows 0, 1 and 18, 19 are nobody's
+    c.sets[2:5] = [1, 3, 7]
+    c.check(c.tree())
+    c = Case("fp8", 8, 2, 16, [100, 40, 70, 20], [5, 3, 8, 4], seed=16)
+    c.tptr[4] = 30                                                 # past the rows
+    c.check(c.tree())
+    c.tptr[:] = [0, 5, 3, 8, 12]                                   # decreasing; request 2's rows are 3 ..
+    c.n = np.array([5, 0, 5, 4])
+    t = c.tensors()
+    out = bf16_out(c.tree(t))
+    assert np.isfinite(out[:12]).all() and np.isnan(out[12:]).all()
+    c = Case("fp4", 8, 2, 16, [100, 40], [80, 3], seed=17, words=1)  # more drafted tokens than mask bits
+    c.check(c.tree())
+
+
+@pytest.mark.parametrize("kind", KINDS)
+def test_peaky_and_flat(kind):
+    """Logits of standard deviation 30: one token takes all; and queries of zeros: the mean."""
+    c = Case(kind, 8, 2, 64, [700, 1300], [5, 9], seed=18, q_std=30.0)
+    want, vmax, _ = c.ref()
+    got = bf16_out(c.tree())
+    # |z| up to 200: fp32 products and their sum leave 2^-24 * 200 * 12 < 2^-12 in an exponent of e, on both sides
+    assert (np.abs(got - want) <= 2.0 ** -8 * np.abs(want) + 2.0 ** -10 * vmax).all()
+    c.q[:] = 0
+    c.check(c.tree())
+
+
+def test_sink_tokens_hide_nothing():
+    """A token of large weight and zero V, the others 18 nats lower: they still make the output."""
+    for kind in ("fp8", "bf16"):
+        c = Case(kind, 8, 2, 64, [1500], [3], seed=19)
+        one = np.uint16(0x3F80) if kind == "bf16" else np.uint8(0x38)
+        c.q[:] = 0
+        c.q[..., 0] = W.bf16_bits(np.full((1,), 8.0, np.float32))[0]
+        c.kc[..., 0] = 0
+        if c.ks is not None:
+            c.ks[:], c.vs[:] = 1.0, 0.01
+        c.sm = 18.0 / 8.0
+        for t in (0, 700):
+            pg = c.idx[t // 64]
+            c.kc[pg, :, t % 64, 0], c.vc[pg, :, t % 64] = one, 0
+        want, vmax, _ = c.ref()
+        got = bf16_out(c.tree())
+        # every other weight is 2^-26 of the largest: f16 keeps it to 2^-29, so within 2^-3 of itself, and the average
+        # of some 1500 of one sign's rounding at worst the same
+        assert (np.abs(got - want) <= 2.0 ** -8 * np.abs(want) + 2.0 ** -3 * np.abs(want) + 2.0 ** -12 * 2.0 ** -26 * 1500 * vmax + 1e-12).all()
+        assert (np.abs(want).max(-1) > 0).all()
+
+
+def test_same_bytes_every_time_and_padding():
+    """Repeated calls, and the same requests beside an aborted one."""
+    import torch
+    c = Case("fp8", 64, 8, 64, [5000, 40, 900, 3000], [8, 3, 1, 12], seed=20)
+    t = c.tensors()
+    first = c.tree(t).clone()
+    flush = torch.empty(1 << 28, dtype=torch.uint8, device="cuda")
+    for i in range(10):
+        flush.fill_(i)
+        t["out"].fill_(float("nan"))
+        assert torch.equal(c.tree(t).view(torch.int16), first.view(torch.int16))
+
+
+def test_streams_graphs_and_workspaces():
+    """Two calls at once on streams and workspaces of their own; captured and replayed with changed inputs."""
+    import torch
+    a, b = Case("fp8", 32, 4, 64, [3000, 700], [8, 5], seed=21), Case("bf16", 16, 2, 32, [900, 2100, 5], [3, 9, 2], seed=22)
+    ta, tb = a.tensors(), b.tensors()
+    s1, s2 = torch.cuda.Stream(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    ga, gb = torch.cuda.CUDAGraph(), torch.cuda.CUDAGraph()
+    ma, mb = (dev(T.words_of(x.sets, x.words).view(np.int64)) for x in (a, b))
+    pa, pb = dev(a.tptr), dev(b.tptr)
+    import fp8_paged_kv_decode_gb300 as fkv
+    with torch.cuda.graph(ga):
+        fkv.paged_tree_attn(**ta, token_indptr=pa, tree_mask=ma)
+    with torch.cuda.graph(gb):
+        fkv.paged_tree_attn(**tb, token_indptr=pb, tree_mask=mb, window=500, sinks=4)
+    for k in range(3):
+        for x, t in ((a, ta), (b, tb)):
+            x.q = W.bf16_bits(x.rng.standard_normal(x.q.shape).astype(np.float32))
+            t["q"].copy_(dev(x.q, dtype=torch.bfloat16))
+            t["out"].fill_(float("nan"))
+        a.lens[0] = 3008 - 60 * k                                  # committed tokens change between replays
+        ta["seq_lens"].copy_(dev(a.lens))
+        torch.cuda.synchronize()
+        with torch.cuda.stream(s1):
+            ga.replay()
+        with torch.cuda.stream(s2):
+            gb.replay()
+        torch.cuda.synchronize()
+        a.check(ta["out"])
+        b.check(tb["out"], 500, 4)
+
+
+def test_float8_cache_and_uint64_mask():
+    import torch
+    import fp8_paged_kv_decode_gb300 as fkv
+    c = Case("fp8", 8, 2, 16, [100, 40], [5, 3], seed=23)
+    t = c.tensors()
+    t["k_cache"], t["v_cache"] = (t[x].view(torch.float8_e4m3fn) for x in ("k_cache", "v_cache"))
+    mask = dev(T.words_of(c.sets, 1)[:, 0].view(np.int64)).view(torch.uint64)
+    fkv.paged_tree_attn(**t, token_indptr=dev(c.tptr), tree_mask=mask)
+    c.check(t["out"])
+
+
+def test_python_refusals():
+    import torch
+    import fp8_paged_kv_decode_gb300 as fkv
+    c = Case("fp8", 8, 2, 16, [100, 40], [1, 1], seed=24, sets=[1, 1])
+    z = lambda *s, dt=torch.bfloat16: torch.zeros(*s, dtype=dt, device="cuda")   # noqa: E731
+    t = c.tensors()
+    tree = dict(t, token_indptr=dev(c.tptr), tree_mask=z(2, dt=torch.int64))
+    win = dict(t, window=4)
+    common = (dict(q=t["q"].float()), dict(out=z(2, 8, 64)), dict(out=z(3, 8, D)), dict(k_scale=None), dict(k_scale=z(1, dt=torch.float32)),
+              dict(seq_lens=z(2, dt=torch.int64)), dict(seq_lens=z(3, dt=torch.int32)), dict(abort_mask=z(2, dt=torch.int32)), dict(abort_mask=z(1, dt=torch.uint8)),
+              dict(page_indptr=z(2, dt=torch.int32)), dict(page_indices=z(9, dt=torch.int64)), dict(workspace=z(16, dt=torch.uint8)), dict(sm_scale=0.0),
+              dict(k_cache=t["k_cache"][:3]), dict(q=t["q"].cpu()), dict(q=z(2, D, 8).transpose(1, 2)), dict(sinks=-1), dict(window=-1), dict(window=2 ** 31),
+              dict(window=1.5))
+    for bad in common + (dict(token_indptr=z(2, dt=torch.int32)), dict(token_indptr=z(3, dt=torch.int64)), dict(tree_mask=z(2, dt=torch.int32)),
+                         dict(tree_mask=z(3, dt=torch.int64)), dict(tree_mask=z(2, 5, dt=torch.int64)), dict(tree_mask=z(2, 0, dt=torch.int64))):
+        with pytest.raises(fkv.FkvError):
+            fkv.paged_tree_attn(**dict(tree, **bad))
+    for bad in common + (dict(window=0), dict(q=z(3, 8, D), out=z(3, 8, D))):
+        with pytest.raises(fkv.FkvError):
+            fkv.paged_window_attn(**dict(win, **bad))
+    with pytest.raises(fkv.FkvError):
+        fkv.alloc_tree_workspace(2, 2, 7, 2)
