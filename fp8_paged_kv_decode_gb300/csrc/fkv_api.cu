@@ -112,9 +112,10 @@ extern "C" int32_t fkv_kernels_per_call(const char *entry_point) {
     if (e == "kv_append_fp8" || e == "kv_append_bf16" || e == "kv_page_tag_check" || e == "kv_page_realloc" ||
         e == "kv_append_fp8_tag_check" || e == "kv_append_bf16_tag_check" || e == "kv_append_fp4" ||
         e == "kv_append_fp4_tag_check" || e == "kv_gather" || e == "qk_norm_rope" ||
-        e == "kv_append_rope" || e == "kv_tree_commit" || e == "paged_tree_attn" || e == "paged_window_attn")
+        e == "kv_append_rope" || e == "kv_tree_commit")
         return 1;
     if (e == "paged_decode_attn" || e == "paged_decode_attn_noalloc") return 2;   // plan, split attention
+    if (e == "paged_tree_attn" || e == "paged_window_attn") return 2;             // attention, join
     if (e == "kv_step_tables") return 2;                                          // plan, fill
     if (e == "kv_calibrate_scales") return 2;                                     // amax, finalize
     return -1;

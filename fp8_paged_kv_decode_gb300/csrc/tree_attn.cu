@@ -1,21 +1,47 @@
 // tree_attn.cu -- attention of drafted tokens, and over a window, on the paged cache.
 //
 // Request r has n drafted tokens, the last n of its seq_lens[r] cached ones.  Each is
-// a query row that sees the committed tokens before them (all of them, or those of a
-// window and a few first ones) and the drafted tokens its mask names:
+// a query row (per query head) that sees the committed tokens before them (all of
+// them, or those of a window and a few first ones) and the drafted tokens its mask names:
 //     out[i][hq] = sum_t softmax_t(sm_scale * q[i][hq] . k_t) v_t   over t seen by i
 // A decode step over a window is the same with one token a request.
 //
-// One block of four warps per (row, query head): each warp takes every fourth token,
-// a lane four dims, with a running maximum and sum; the warps' sums are joined at the end.
+// The n drafted tokens of a request and the G query heads of a KV head share its K and V,
+// so a unit of work is (request, KV head, up to kR of their n G rows): products of
+// 128-token tiles with kR columns, on the fifth-generation tensor cores with tokens (or
+// dims) on M and rows on N,
+//     S^T = K Q^T  [128 tokens][kR],   O^T = V^T P^T  [128 dims][kR],
+// so that few rows cost little and K and V pass through once for all of them.  kR is 16,
+// 32, 64 or 128: the smallest that holds G times the call's mean n.
+//
+// One CTA per SM takes an equal share of all units' tiles (a unit may be cut; its parts are
+// joined by a second kernel).  Its warps:
+//   producer   a unit's geometry, and TMA copies of its pages into rings of K and V stages
+//   converters (FP8, FP4) K rows to f16 in tensor memory, V rows to f16 in shared memory,
+//              one token a thread; they also bring a unit's Q as f16 (BF16: as it is)
+//   issuer     the products, S of the next tile before O of this one
+//   softmax    two groups of four warps, each half of the columns, one token a thread:
+//              weights against a running reference, stored as the second product's operand
+// The reference of a column moves only when a weight would pass f16's range: a maximum is
+// put at 2^13, later ones may grow to 2^15.9, so sums are rescaled a few times per unit.
+#include <cudaTypedefs.h>
+
 #include <cmath>
+#include <cstddef>
+#include <mutex>
 
 #include "fp4_row.cuh"
+#include "umma.cuh"
 
 namespace fkv {
 
 constexpr int kTreeMaxWords = 4;               // 64-bit words of a row's mask
-constexpr int kTreeBlock = 128;
+constexpr int kTreeTok = 128;                  // tokens of a tile
+constexpr int kTreePoison = 10;                // tiles of a unit that hold tokens not seen by every row, at most (9)
+constexpr float kTreeTop = 13.f, kTreeMost = 15.9f;   // log2 of a moved reference's largest weight, and of any weight
+constexpr float kTreeNone = -3e38f;            // the reference of a column that has seen nothing
+constexpr uint64_t kTreeWaitNs = 2000000000ull;
+constexpr uint32_t kAll = 0xffffffffu;
 
 struct TreeParams {
     const __nv_bfloat16 *q;
@@ -27,146 +53,1188 @@ struct TreeParams {
     const uint8_t *abort_mask;
     __nv_bfloat16 *out;
     uint32_t *err;
+    float *part_o;                             // [2 grid][kR][128] sums of units that are cut
+    float2 *part_ml;                           // [2 grid][kR] their references and weights' sums (sum < 0: a bad page)
+    int4 *joins;                               // [grid] the unit whose last part a CTA has: first CTA (-1: none), token, tokens, KV head
     int64_t nnz;
-    int32_t batch, n_tokens, hq, hkv, pages, page_size, words, window, sinks;
+    int32_t batch, n_tokens, hq, hkv, group, pages, page_size, words, window, sinks;
     float scale_log2;
 };
 
-template <int kKv>
-__device__ __forceinline__ float4 load4(const uint8_t *cache, int64_t row, int lane) {
-    if (kKv == FKV_KV_BF16) {
-        const uint2 u = reinterpret_cast<const uint2 *>(cache + row * 256)[lane];
-        return make_float4(__uint_as_float(u.x << 16), __uint_as_float(u.x & 0xFFFF0000u), __uint_as_float(u.y << 16),
-                           __uint_as_float(u.y & 0xFFFF0000u));
+// ---------------------------------------------------------------------------
+// geometry
+// ---------------------------------------------------------------------------
+struct TreeRequest {
+    int32_t t0, n, len, row;                   // first query token, drafted and all tokens, first page-table entry
+    bool live, rows;                           // has work; its rows are rows of q
+};
+
+__device__ __forceinline__ TreeRequest tree_request(const TreeParams &p, int r) {
+    TreeRequest q{};
+    if (r >= p.batch) return q;
+    int t0 = r, t1 = r + 1;
+    if (p.token_indptr) {
+        t0 = __ldg(p.token_indptr + r);
+        t1 = __ldg(p.token_indptr + r + 1);
     }
-    uint32_t lo, hi;
-    float s = 1.f;
-    if (kKv == FKV_KV_FP8_E4M3) {
-        const uint32_t u = reinterpret_cast<const uint32_t *>(cache + row * 128)[lane];
-        lo = e4m3x2_to_f16x2(static_cast<uint16_t>(u & 0xFFFFu));
-        hi = e4m3x2_to_f16x2(static_cast<uint16_t>(u >> 16));
-    } else {
-        const uint8_t *r = cache + row * kFp4Row;
-        uint32_t f[4];
-        e2m1x8_to_f16(reinterpret_cast<const uint16_t *>(r)[lane], f);
-        lo = f[0];
-        hi = f[1];
-        const uint32_t s16 = e4m3x2_to_f16x2(r[kFp4Codes + lane / 4]);
-        s = __half2float(__ushort_as_half(static_cast<unsigned short>(s16 & 0xFFFFu)));
-    }
-    const float2 a = __half22float2(*reinterpret_cast<const __half2 *>(&lo)), b = __half22float2(*reinterpret_cast<const __half2 *>(&hi));
-    return make_float4(a.x * s, a.y * s, b.x * s, b.y * s);
+    const int32_t b = __ldg(p.indptr + r), e = __ldg(p.indptr + r + 1);
+    q.len = __ldg(p.seq_lens + r);
+    const bool alive = !p.abort_mask || __ldg(p.abort_mask + r) == 0;
+    q.t0 = t0;
+    q.row = b;
+    q.rows = t0 >= 0 && t1 >= t0 && t1 <= p.n_tokens;
+    q.n = q.rows ? t1 - t0 : 0;
+    q.live = q.n > 0 && alive && q.len >= q.n && q.n <= 64 * p.words && b >= 0 && e >= b && e <= p.nnz &&
+             static_cast<int64_t>(e - b) * p.page_size >= q.len;
+    return q;
 }
 
+// The tiles of a live request: those over the first tokens, if they lie apart, then those
+// from `start` on, the page of the first token that a row at depth 0 sees.
+struct TreeSpan {
+    int32_t start, sink_tiles, head, tiles;
+};
+__device__ __forceinline__ TreeSpan tree_span(const TreeParams &p, const TreeRequest &q) {
+    TreeSpan s{0, 0, 0, 0};
+    const int32_t ctx = q.len - q.n;
+    if (p.window && ctx >= p.window) {
+        const int32_t lo = ctx - p.window + 1;
+        s.start = lo - lo % p.page_size;
+        s.head = min(p.sinks, lo);
+        s.sink_tiles = (s.head + kTreeTok - 1) / kTreeTok;
+        if (s.start <= static_cast<int64_t>(s.sink_tiles) * kTreeTok) s = TreeSpan{0, 0, 0, 0};
+    }
+    s.tiles = s.sink_tiles + (q.len - s.start + kTreeTok - 1) / kTreeTok;
+    return s;
+}
+
+// What a CTA takes of a unit, from the producer to the others.
+struct TreeUnit {
+    int32_t tb, te;                            // its tiles; te < 0: there is no more work
+    int32_t tok0, ntok;                        // the rows' tokens
+    int32_t ctx, len;
+    int32_t start, sink_tiles, head;
+    int32_t full_lo;                           // the first position that every row sees
+    int32_t row, h;                            // first page-table entry, KV head
+    int32_t slot;                              // of its partial sums; -1: the whole unit is here
+    int32_t bad;                               // a page outside the pool
+};
+__device__ __forceinline__ uint32_t tile_at(const TreeUnit &u, int i) {
+    return i < u.sink_tiles ? static_cast<uint32_t>(i) * kTreeTok : u.start + static_cast<uint32_t>(i - u.sink_tiles) * kTreeTok;
+}
+__device__ __forceinline__ uint32_t tile_end(const TreeUnit &u, int i) { return i < u.sink_tiles ? u.head : u.len; }
+// Whether every row sees every token of the tile at t0.
+__device__ __forceinline__ bool tile_whole(const TreeUnit &u, const TreeParams &p, uint32_t t0) {
+    const uint32_t t1 = t0 + kTreeTok;
+    return t1 <= static_cast<uint32_t>(u.ctx) &&
+           (!p.window || t0 >= static_cast<uint32_t>(u.full_lo) || t1 <= static_cast<uint32_t>(p.sinks));
+}
+
+// ---------------------------------------------------------------------------
+// shared memory
+// ---------------------------------------------------------------------------
+template <int kKv, int kR>
+struct TreeCfg {
+    static constexpr bool kConv = kKv != FKV_KV_BF16;              // K and V become f16 here
+    static constexpr int kRowB = kKv == FKV_KV_FP8_E4M3 ? 128 : kKv == FKV_KV_BF16 ? 256 : kFp4Row;
+    static constexpr int kStageB = kTreeTok * kRowB;               // the K (or V) rows of a tile
+    static constexpr int kNK = kConv && (kR <= 64 || kKv == FKV_KV_FP4) ? 3 : 2;
+    static constexpr int kNV = kConv ? (kR <= 32 ? 4 : 3) : kR <= 64 ? 3 : 2;
+    static constexpr int kNP = kConv && kR <= 64 ? 2 : 1;          // weight buffers
+    static constexpr int kParts = kConv ? 1 : 2;                   // words of a weight
+    static constexpr int kHalves = kR > 64 ? 2 : 1;                // 64-column halves of a weight buffer
+    static constexpr int kPB = 16384 * kHalves;
+    static constexpr int kQB = kR * 256;
+    static constexpr int kV16 = kConv ? 32768 : 0;
+    static constexpr int kGroups = kR <= 64 ? 2 : 1;               // converter groups: K and V, or one for both
+    static constexpr int kThreads = 256 + 128 * kGroups + 64;
+    static constexpr int kND = kR <= 64 ? 4 : 2;                   // units in flight
+    static constexpr int kNC = kR / 2;                             // columns of a softmax group
+    // tensor memory columns: K f16 (two buffers), S (two), O
+    static constexpr int kTmS = kConv ? 128 : 0, kTmO = kTmS + 2 * kR;
+    static constexpr int kNVR = kConv ? 2 : kNV;                   // buffers between converters and issuer
+    static constexpr int kOffP = kQB, kOffV16 = kOffP + kNP * kParts * kPB, kOffK = kOffV16 + 2 * kV16;
+    static constexpr int kOffV = kOffK + kNK * kStageB, kOffCtrl = kOffV + kNV * kStageB;
+};
+
+template <int kKv, int kR>
+struct TreeCtrl {
+    using C = TreeCfg<kKv, kR>;
+    uint64_t kfull[C::kNK], kempty[C::kNK], vfull[C::kNV], vempty[C::kNV];
+    uint64_t k16full[2], k16empty[2], vready[C::kNVR], v16empty[2];
+    uint64_t sfull[2], sempty[2], pfull[C::kNP], pempty[C::kNP];
+    uint64_t qfull, qempty, oempty, drained;
+    uint64_t dfull[C::kND], dempty[C::kND], cfull[C::kND];
+    TreeUnit unit[C::kND];
+    alignas(16) float colscale[C::kND][kR];                        // a logit in log2 units per unit of S
+    alignas(16) float ref[kR];                                     // the columns' references, negated
+    int32_t redmax[2][4][16];
+    float lsum[kR <= 64 ? 2 * 4 * C::kNC : 1];                     // (kR = 128: in the weights' buffer)
+    uint32_t poison[C::kND][kTreePoison][4];                       // tokens whose V holds NaN or infinities
+    int64_t scan[18];                                             // one per warp
+    int64_t total, off0;
+    int32_t r0;
+    uint32_t tmem;
+    int32_t dead;
+};
+
+template <int kKv, int kR>
+constexpr int tree_smem() {
+    using C = TreeCfg<kKv, kR>;
+    using T = TreeCtrl<kKv, kR>;
+    static_assert(offsetof(T, colscale) % 16 == 0 && offsetof(T, ref) % 16 == 0 && C::kOffCtrl % 16 == 0, "read four at a time");
+    static_assert(C::kOffP % 1024 == 0 && C::kOffV16 % 1024 == 0 && C::kOffK % 1024 == 0 && C::kOffV % 1024 == 0,
+                  "swizzled buffers start on 1024 bytes");
+    return TreeCfg<kKv, kR>::kOffCtrl + static_cast<int>((sizeof(TreeCtrl<kKv, kR>) + 15) / 16 * 16);
+}
+
+struct Ring {                                  // a buffer of a ring and the parity of its current round
+    int i = 0;
+    uint32_t ph = 0;
+    template <int kN>
+    __device__ __forceinline__ void next() {
+        if (++i == kN) {
+            i = 0;
+            ph ^= 1;
+        }
+    }
+};
+
+// Waits for a phase, for at most kTreeWaitNs and until another thread has given up.
+__device__ __forceinline__ bool tree_wait(uint32_t bar, uint32_t parity, volatile int32_t *dead, uint32_t *err) {
+    if (mbar_try_wait(bar, parity)) return true;
+    const uint64_t t0 = globaltimer_ns();
+    for (uint32_t i = 1;; ++i) {
+        if (mbar_try_wait(bar, parity)) return true;
+        if ((i & 31u) == 0) {
+            if (*dead) return false;
+            if (globaltimer_ns() - t0 > kTreeWaitNs) {
+                *dead = 1;
+                atomicOr(err, FKV_DEVERR_TIMEOUT);
+                return false;
+            }
+        }
+    }
+}
+
+// Whether any of the 128 threads of a softmax group says so (a barrier of the group).
+__device__ __forceinline__ bool group_any(int id, bool x) {
+    uint32_t r;
+    asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\tbarrier.cta.red.or.pred q, %2, 128, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+                 : "=r"(r) : "r"(x ? 1u : 0u), "r"(id) : "memory");
+    return r != 0;
+}
+__device__ __forceinline__ void group_sync(int id) { asm volatile("barrier.cta.sync %0, 128;" ::"r"(id) : "memory"); }
+
+__device__ __forceinline__ void st_shared_v4(uint32_t addr, uint4 v) {
+    asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
+}
+
+// ---------------------------------------------------------------------------
+// which rows see a token
+// ---------------------------------------------------------------------------
+struct RowSight {
+    uint64_t word;                             // the row's mask word of the token asked for
+    int32_t lo;                                // its first committed token apart from the first ones
+};
+// Of drafted row `tok` (of the call), for tokens of mask word `w`.
+__device__ __forceinline__ RowSight row_sight(const TreeParams &p, const TreeUnit &u, int tok, int w) {
+    RowSight s{w == 0 ? 1ull : 0ull, 0};
+    int bits = 1;
+    if (p.mask) {
+        const uint64_t *m = p.mask + static_cast<int64_t>(tok) * p.words;
+        s.word = w < p.words ? __ldg(m + w) : 0ull;
+        if (p.window) {
+            bits = 0;
+            for (int i = 0; i < p.words; ++i) bits += __popcll(__ldg(m + i));
+        }
+    }
+    if (p.window) s.lo = static_cast<int32_t>(static_cast<int64_t>(u.ctx) + max(bits - 1, 0) - p.window + 1 > 0 ? static_cast<int64_t>(u.ctx) + max(bits - 1, 0) - p.window + 1 : 0);
+    return s;
+}
+__device__ __forceinline__ bool sees(const TreeParams &p, const TreeUnit &u, const RowSight &s, uint32_t t) {
+    if (t >= static_cast<uint32_t>(u.len)) return false;
+    if (t >= static_cast<uint32_t>(u.ctx)) return (s.word >> ((t - u.ctx) & 63)) & 1;
+    return !p.window || t < static_cast<uint32_t>(p.sinks) || t >= static_cast<uint32_t>(s.lo);
+}
+__device__ __forceinline__ int word_of(const TreeUnit &u, uint32_t t) {
+    return t >= static_cast<uint32_t>(u.ctx) ? static_cast<int>((t - u.ctx) >> 6) : 0;
+}
+// Bits of this group's columns whose rows see token t (rows past the unit's: unset).
+template <int kNC>
+__device__ __forceinline__ uint64_t seen_by(const TreeParams &p, const TreeUnit &u, int col0, uint32_t t) {
+    uint64_t v = 0;
+    const int w = word_of(u, t), G = p.group;
+    for (int i = col0 / G; i < u.ntok && i * G < col0 + kNC; ++i) {
+        if (sees(p, u, row_sight(p, u, u.tok0 + i, w), t)) {
+            const int a = max(i * G, col0) - col0, b = min((i + 1) * G, col0 + kNC) - col0;
+            v |= (b - a == 64 ? ~0ull : (1ull << (b - a)) - 1) << a;
+        }
+    }
+    return v;
+}
+
+// ---------------------------------------------------------------------------
+// rows of the cache as f16 (this thread's token)
+// ---------------------------------------------------------------------------
+__device__ __forceinline__ void e4m3x4_to_f16(uint32_t w, uint32_t &lo, uint32_t &hi) {
+    lo = e4m3x2_to_f16x2(static_cast<uint16_t>(w & 0xFFFFu));
+    hi = e4m3x2_to_f16x2(static_cast<uint16_t>(w >> 16));
+}
+// 64 values (half `hf`) of the row in a K or V stage, as f16 pairs.  kClean: NaN become
+// zeros, and `odd` says whether there were any.
+template <int kKv, bool kClean>
+__device__ __forceinline__ void half_row(uint32_t stage, int tok, int hf, uint32_t (&f)[32], bool &odd) {
+    if (kKv == FKV_KV_FP8_E4M3) {
+        const uint32_t row = stage + tok * 128;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+            const uint4 v = ld_shared_v4(row + (((4 * hf + c) ^ (tok & 7)) << 4));
+            uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                if (kClean) {
+                    const uint32_t nan = (((w[j] & 0x7F7F7F7Fu) + 0x01010101u) >> 7) & 0x01010101u;
+                    odd |= nan != 0;
+                    w[j] &= ~(nan * 0xFFu);
+                }
+                e4m3x4_to_f16(w[j], f[8 * c + 2 * j], f[8 * c + 2 * j + 1]);
+            }
+        }
+    } else {
+        const uint32_t row = stage + tok * kFp4Row;
+        const uint2 sc = ld_shared_v2(row + kFp4Codes);
+        const uint32_t s4 = hf ? sc.y : sc.x;
+#pragma unroll
+        for (int b = 0; b < 4; ++b) {
+            const uint2 c = ld_shared_v2(row + 32 * hf + 8 * b);
+            uint32_t byte = (s4 >> (8 * b)) & 0xFFu;
+            if (kClean && (byte & 0x7Fu) == 0x7Fu) {
+                odd = true;
+                byte = 0;
+            }
+            const uint32_t s = e4m3_to_f16_pair(byte);
+            uint32_t x[4], y[4];
+            e2m1x8_to_f16(c.x, x);
+            e2m1x8_to_f16(c.y, y);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                f[8 * b + j] = mul_f16x2(x[j], s);
+                f[8 * b + 4 + j] = mul_f16x2(y[j], s);
+            }
+        }
+    }
+}
+
+// A V row as f16 into a 128 x 128 operand buffer (MN-major, two halves of 64 dims).
+template <int kKv, bool kClean>
+__device__ __forceinline__ bool convert_v(uint32_t stage, uint32_t dst, int tok, bool valid) {
+    bool odd = false;
+#pragma unroll
+    for (int hf = 0; hf < 2; ++hf) {
+        uint32_t f[32];
+        if (!kClean || valid) {
+            half_row<kKv, kClean>(stage, tok, hf, f, odd);
+        } else {
+#pragma unroll
+            for (int j = 0; j < 32; ++j) f[j] = 0;
+        }
+#pragma unroll
+        for (int c = 0; c < 8; ++c)
+            st_shared_v4(dst + 16384 * hf + tok * 128 + ((c ^ (tok & 7)) << 4),
+                         make_uint4(f[4 * c], f[4 * c + 1], f[4 * c + 2], f[4 * c + 3]));
+    }
+    return odd;
+}
+
+// A bf16 V row in its stage: rows of no token and NaN or infinite elements become zeros.
+__device__ __forceinline__ bool clean_v(uint32_t stage, int tok, bool valid) {
+    bool odd = false;
+#pragma unroll 4
+    for (int c = 0; c < 16; ++c) {
+        const uint32_t a = stage + 16384 * (c >> 3) + tok * 128 + (((c & 7) ^ (tok & 7)) << 4);
+        uint4 v = ld_shared_v4(a);
+        uint32_t w[4] = {v.x, v.y, v.z, v.w};
+        bool change = !valid;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const uint32_t lo = (w[j] & 0x7F80u) == 0x7F80u ? 0xFFFFu : 0u, hi = (w[j] & 0x7F800000u) == 0x7F800000u ? 0xFFFF0000u : 0u;
+            if (valid && (lo | hi)) change = odd = true;
+            w[j] = valid ? w[j] & ~(lo | hi) : 0u;
+        }
+        if (change) st_shared_v4(a, make_uint4(w[0], w[1], w[2], w[3]));
+    }
+    return odd;
+}
+
+// A V value that is NaN or infinite, as the cache holds it; else 0.
 template <int kKv>
-__global__ void __launch_bounds__(kTreeBlock)
-tree_attn_kernel(const TreeParams p) {
+__device__ __forceinline__ float odd_value(const TreeParams &p, const TreeUnit &u, uint32_t t, int dim) {
+    const int64_t pg = __ldg(p.indices + u.row + t / p.page_size);
+    if (pg < 0 || pg >= p.pages) return 0.f;
+    const int64_t row = (pg * p.hkv + u.h) * p.page_size + t % p.page_size;
+    float v;
+    if (kKv == FKV_KV_BF16) {
+        v = __uint_as_float(static_cast<uint32_t>(reinterpret_cast<const uint16_t *>(p.v_cache)[row * 128 + dim]) << 16);
+    } else {
+        const uint32_t b = kKv == FKV_KV_FP8_E4M3 ? p.v_cache[row * 128 + dim] : p.v_cache[row * kFp4Row + kFp4Codes + dim / 16];
+        v = (b & 0x7Fu) == 0x7Fu ? __int_as_float(0x7FC00000) : 0.f;
+    }
+    return isfinite(v) ? 0.f : v;
+}
+
+// Sums over a warp's lanes of kN columns: half of them go to the lane kO away, then half of
+// those that are left, and so on; at the end a lane has kN / 32 columns (at least one).
+template <int kN, int kO, int kSize>
+__device__ __forceinline__ void spread_sums(float (&v)[kSize], int lane) {
+    if constexpr (kO > 0) {
+        constexpr int n = kN > 1 ? kN / 2 : 1;
+        if constexpr (kN > 1) {
+#pragma unroll
+            for (int j = 0; j < n; ++j) {
+                const float a = v[j], b = v[j + n];
+                const float got = __shfl_xor_sync(kAll, lane & kO ? a : b, kO);
+                v[j] = (lane & kO ? b : a) + got;
+            }
+        } else {
+            v[0] += __shfl_xor_sync(kAll, v[0], kO);
+        }
+        spread_sums<n, kO / 2>(v, lane);
+    }
+}
+
+// ---------------------------------------------------------------------------
+// the kernel
+// ---------------------------------------------------------------------------
+template <int kKv, int kR>
+__global__ void __launch_bounds__(TreeCfg<kKv, kR>::kThreads, 1)
+tree_attn_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV) {
+    using C = TreeCfg<kKv, kR>;
+    using Ctrl = TreeCtrl<kKv, kR>;
+    extern __shared__ __align__(1024) uint8_t smem[];
+    Ctrl &ct = *reinterpret_cast<Ctrl *>(smem + C::kOffCtrl);
+    const uint32_t base = smem_u32(smem);
+    const uint32_t sQ = base, sP = base + C::kOffP, sV16 = base + C::kOffV16, sK = base + C::kOffK, sV = base + C::kOffV;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    constexpr int kConvW = 8, kProdW = 8 + 4 * C::kGroups, kMmaW = kProdW + 1;
+    volatile int32_t *dead = &ct.dead;
+    auto bar = [&](uint64_t &b) { return smem_u32(&b); };
+    auto wait = [&](uint64_t &b, uint32_t parity) { return tree_wait(smem_u32(&b), parity, dead, p.err); };
+
+    if (tid == 0) {
+        constexpr int kKC = C::kConv ? 4 : 1;                      // who empties a stage: converter warps, or the issuer
+        for (int i = 0; i < C::kNK; ++i) mbar_init(bar(ct.kfull[i]), 1), mbar_init(bar(ct.kempty[i]), kKC);
+        for (int i = 0; i < C::kNV; ++i) mbar_init(bar(ct.vfull[i]), 1), mbar_init(bar(ct.vempty[i]), kKC);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(bar(ct.k16full[i]), 4), mbar_init(bar(ct.k16empty[i]), 1), mbar_init(bar(ct.v16empty[i]), 1);
+            mbar_init(bar(ct.sfull[i]), 1), mbar_init(bar(ct.sempty[i]), 8);
+        }
+        for (int i = 0; i < C::kNVR; ++i) mbar_init(bar(ct.vready[i]), 4);
+        for (int i = 0; i < C::kNP; ++i) mbar_init(bar(ct.pfull[i]), 8), mbar_init(bar(ct.pempty[i]), 1);
+        mbar_init(bar(ct.qfull), 4), mbar_init(bar(ct.qempty), 1), mbar_init(bar(ct.oempty), 8), mbar_init(bar(ct.drained), 1);
+        for (int i = 0; i < C::kND; ++i)
+            mbar_init(bar(ct.dfull[i]), 1), mbar_init(bar(ct.dempty[i]), 8 + 4 * C::kGroups + 1), mbar_init(bar(ct.cfull[i]), 4);
+        ct.dead = 0;
+        ct.r0 = p.batch;
+        fence_mbar_init();
+    }
+    if (warp == kMmaW) tmem_alloc(smem_u32(&ct.tmem), 512);
+    if (C::kConv && kKv == FKV_KV_FP8_E4M3 && warp == kProdW && lane == 0) prefetch_tensormap(&tmK), prefetch_tensormap(&tmV);
+
+    grid_dep_wait();                                               // lengths, tables and cache of earlier kernels
+    // ---- this CTA's share: the tiles of all units, counted by the whole block ----
+    const int tpt = kR / p.group;                                  // tokens of a unit's rows
+    const int per = (p.batch + C::kThreads - 1) / C::kThreads;
+    auto tiles_of = [&](const TreeRequest &q) -> int64_t {
+        return q.live ? static_cast<int64_t>(tree_span(p, q).tiles) * ((q.n + tpt - 1) / tpt) * p.hkv : 0;
+    };
+    int64_t mine = 0;
+    for (int i = 0; i < per; ++i) {
+        const int r = tid * per + i;
+        if (r < p.batch) mine += tiles_of(tree_request(p, r));
+    }
+    int64_t incl = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int64_t y = __shfl_up_sync(kAll, incl, o);
+        if (lane >= o) incl += y;
+    }
+    if (lane == 31) ct.scan[warp] = incl;
+    __syncthreads();
+    int64_t before = 0, T = 0;
+    for (int w = 0; w < C::kThreads / 32; ++w) {
+        const int64_t x = ct.scan[w];
+        if (w < warp) before += x;
+        T += x;
+    }
+    const int64_t grid = T < static_cast<int64_t>(gridDim.x) ? (T > 0 ? T : 1) : gridDim.x;
+    const int64_t g0 = blockIdx.x < grid ? T * blockIdx.x / grid : T, g1 = blockIdx.x < grid ? T * (blockIdx.x + 1) / grid : T;
+    incl += before;
+    if (g0 < g1 && incl - mine <= g0 && g0 < incl) {
+        int64_t at = incl - mine;
+        int r = tid * per;
+        for (;; ++r) {
+            const int64_t x = tiles_of(tree_request(p, r));
+            if (g0 < at + x) break;
+            at += x;
+        }
+        ct.r0 = r;
+        ct.off0 = g0 - at;
+    }
+    umma_fence_before();
+    __syncthreads();
+    umma_fence_after();
+    const uint32_t tmem = ct.tmem;
+    grid_dep_launch();
+
+    if (warp == kProdW) {
+        // ==== producer ====
+        const uint64_t once = l2_policy_evict_first(), again = l2_policy_evict_normal();
+        int r = ct.r0;
+        int64_t off = ct.off0, left = g1 - g0;
+        int4 join = make_int4(-1, 0, 0, 0);
+        TreeRequest cur = tree_request(p, r), nxt = tree_request(p, r + 1);
+        Ring d, k, v;
+        bool ok = true;
+        const int npg = kTreeTok / p.page_size;
+        while (left > 0 && ok) {
+            const TreeSpan sp = tree_span(p, cur);
+            const int mt = (cur.n + tpt - 1) / tpt, units = mt * p.hkv;
+            const uint64_t policy = mt > 1 ? again : once;
+            for (int ui = static_cast<int>(off / sp.tiles), tb = static_cast<int>(off % sp.tiles); ui < units && left > 0 && ok; ++ui, tb = 0) {
+                const int te = left < sp.tiles - tb ? tb + static_cast<int>(left) : sp.tiles;
+                const int h = ui / mt, m = ui - h * mt;
+                ok = wait(ct.dempty[d.i], d.ph ^ 1);
+                if (!ok) break;
+                TreeUnit u;
+                u.tb = tb;
+                u.te = te;
+                u.tok0 = cur.t0 + m * tpt;
+                u.ntok = min(tpt, cur.n - m * tpt);
+                u.ctx = cur.len - cur.n;
+                u.len = cur.len;
+                u.start = sp.start;
+                u.sink_tiles = sp.sink_tiles;
+                u.head = sp.head;
+                const int64_t far = static_cast<int64_t>(cur.len) - p.window;
+                u.full_lo = p.window && far > 0 ? static_cast<int32_t>(far) : 0;
+                u.row = cur.row;
+                u.h = h;
+                u.slot = tb == 0 && te == sp.tiles ? -1 : 2 * static_cast<int>(blockIdx.x) + (tb == 0 ? 1 : 0);
+                u.bad = 0;
+                if (lane == 0) ct.unit[d.i] = u;
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar(ct.dfull[d.i]));
+                if (tb > 0 && te == sp.tiles) {
+                    // the last part of a unit that other CTAs began: its first tile's CTA
+                    const int64_t first = g1 - left - tb;
+                    join = make_int4(static_cast<int>(((first + 1) * grid + T - 1) / T - 1), u.tok0, u.ntok, h);
+                }
+                auto page = [&](int i) -> int32_t {                // this lane's page of tile i; -1: none to copy
+                    const uint32_t t = tile_at(u, i) + static_cast<uint32_t>(lane) * p.page_size;
+                    return lane < npg && t < tile_end(u, i) ? __ldg(p.indices + u.row + t / p.page_size) : -1;
+                };
+                int32_t pg_next = page(tb);
+                for (int i = tb; i < te; ++i) {
+                    int32_t pg = pg_next;
+                    const bool has = lane < npg && tile_at(u, i) + static_cast<uint32_t>(lane) * p.page_size < tile_end(u, i);
+                    if (i + 1 < te) pg_next = page(i + 1);
+                    if (__any_sync(kAll, has && static_cast<uint32_t>(pg) >= static_cast<uint32_t>(p.pages))) {
+                        if (static_cast<uint32_t>(pg) >= static_cast<uint32_t>(p.pages)) pg = 0;   // never dereferenced: the unit's rows become zeros
+                        if (lane == 0) {
+                            *const_cast<volatile int32_t *>(&ct.unit[d.i].bad) = 1;
+                            atomicOr(p.err, FKV_DEVERR_ATTN_PAGE);
+                        }
+                    }
+                    const uint32_t bytes = __popc(__ballot_sync(kAll, has)) * p.page_size * C::kRowB;
+                    auto copy = [&](uint64_t &full, uint32_t dst, const CUtensorMap *tm, const uint8_t *cache) {
+                        if (lane == 0) mbar_arrive_expect_tx(bar(full), bytes);
+                        __syncwarp();
+                        if (!has) return;
+                        if (kKv == FKV_KV_FP4) {
+                            const uint32_t sz = p.page_size * kFp4Row;
+                            bulk_load_hint(dst + lane * sz, cache + (static_cast<int64_t>(pg) * p.hkv + h) * sz, sz, bar(full), policy);
+                        } else {
+                            tma_load_4d(dst + lane * p.page_size * 128, tm, bar(full), 0, 0, h, pg, policy);
+                            if (kKv == FKV_KV_BF16) tma_load_4d(dst + 16384 + lane * p.page_size * 128, tm, bar(full), 64, 0, h, pg, policy);
+                        }
+                    };
+                    ok = wait(ct.kempty[k.i], k.ph ^ 1);
+                    if (!ok) break;
+                    copy(ct.kfull[k.i], sK + k.i * C::kStageB, &tmK, p.k_cache);
+                    k.template next<C::kNK>();
+                    ok = wait(ct.vempty[v.i], v.ph ^ 1);
+                    if (!ok) break;
+                    copy(ct.vfull[v.i], sV + v.i * C::kStageB, &tmV, p.v_cache);
+                    v.template next<C::kNV>();
+                }
+                left -= te - tb;
+                d.template next<C::kND>();
+            }
+            off = 0;
+            if (left > 0 && ok) {
+                do {
+                    ++r;
+                    cur = nxt;
+                    nxt = tree_request(p, r + 1);
+                } while (r < p.batch && !cur.live);
+                if (r >= p.batch) break;
+            }
+        }
+        if (ok && wait(ct.dempty[d.i], d.ph ^ 1)) {
+            if (lane == 0) {
+                ct.unit[d.i].te = -1;
+                mbar_arrive(bar(ct.dfull[d.i]));
+            }
+        }
+        if (lane == 0) p.joins[blockIdx.x] = join;
+        __syncwarp();
+        // after a wait that gave up, the copies in flight still land in this CTA's memory
+        if (*dead) {
+            const uint64_t t0 = globaltimer_ns();
+            while (globaltimer_ns() - t0 < 200000000ull) __nanosleep(1000);
+        }
+    } else if (warp == kMmaW) {
+        // ==== issuer ====
+        if (lane == 0) {
+            constexpr bool kB16 = !C::kConv;
+            constexpr uint32_t idS = umma_idesc(kB16, false, false, 128, kR), idO = umma_idesc(kB16, true, true, 128, kR);
+            Ring dq, dv, kr, s, vr, pr;                            // units of S and of O, K buffers, S, V buffers, weights
+            int sq = 0, sqe = 0, so = 0, soe = 0;                  // tiles left to do: next and end
+            uint32_t nq = 0, no = 0;                               // units begun
+            bool ok = true, more = true;
+            auto step_s = [&]() {                                  // S of the next tile, if there is one
+                if (!more || !ok) return;
+                if (sq == sqe) {
+                    if (!(ok = wait(ct.dfull[dq.i], dq.ph))) return;
+                    sq = *const_cast<volatile int32_t *>(&ct.unit[dq.i].tb);
+                    sqe = *const_cast<volatile int32_t *>(&ct.unit[dq.i].te);
+                    if (sqe < 0) {
+                        more = false;
+                        return;
+                    }
+                    dq.template next<C::kND>();
+                    if (!(ok = wait(ct.qfull, nq & 1))) return;
+                    ++nq;
+                }
+                if (!(ok = wait(kB16 ? ct.kfull[kr.i] : ct.k16full[kr.i], kr.ph) && wait(ct.sempty[s.i], s.ph ^ 1))) return;
+                umma_fence_after();
+                const uint32_t dst = tmem + C::kTmS + s.i * kR;
+#pragma unroll
+                for (int kk = 0; kk < 8; ++kk) {
+                    const uint64_t b = umma_desc(sQ + (kk >> 2) * (kR * 128) + (kk & 3) * 32, 16, 1024);
+                    if (kB16)
+                        umma_ss(dst, umma_desc(sK + kr.i * C::kStageB + (kk >> 2) * 16384 + (kk & 3) * 32, 16, 1024), b, idS, kk > 0);
+                    else
+                        umma_ts(dst, tmem + kr.i * 64 + kk * 8, b, idS, kk > 0);
+                }
+                umma_commit(bar(ct.sfull[s.i]));
+                umma_commit(bar(kB16 ? ct.kempty[kr.i] : ct.k16empty[kr.i]));
+                if (++sq == sqe) umma_commit(bar(ct.qempty));
+                kr.template next<kB16 ? C::kNK : 2>();
+                s.template next<2>();
+            };
+            step_s();
+            while (ok && (more || so != soe || dv.i != dq.i || dv.ph != dq.ph)) {
+                step_s();
+                if (!ok) break;
+                const bool first = so == soe;                      // of a unit: it starts its sums anew
+                if (first) {
+                    if (dv.i == dq.i && dv.ph == dq.ph) break;     // no unit left
+                    so = *const_cast<volatile int32_t *>(&ct.unit[dv.i].tb);
+                    soe = *const_cast<volatile int32_t *>(&ct.unit[dv.i].te);
+                    if (no && !(ok = wait(ct.oempty, (no - 1) & 1))) break;
+                    ++no;
+                }
+                if (!(ok = wait(ct.pfull[pr.i], pr.ph) && wait(ct.vready[vr.i], vr.ph))) break;
+                umma_fence_after();
+#pragma unroll
+                for (int w = 0; w < C::kParts; ++w) {
+#pragma unroll
+                    for (int kk = 0; kk < 8; ++kk) {
+                        const uint32_t va = C::kConv ? sV16 + vr.i * C::kV16 : sV + vr.i * C::kStageB;
+                        umma_ss(tmem + C::kTmO, umma_desc(va + kk * 2048, 16384, 1024),
+                                umma_desc(sP + (pr.i * C::kParts + w) * C::kPB + kk * 2048, 16384, 1024), idO, !first || w > 0 || kk > 0);
+                    }
+                }
+                umma_commit(bar(ct.pempty[pr.i]));
+                umma_commit(bar(C::kConv ? ct.v16empty[vr.i & 1] : ct.vempty[vr.i]));
+                pr.template next<C::kNP>();
+                vr.template next<C::kNVR>();
+                if (++so == soe) {
+                    mbar_arrive(bar(ct.dempty[dv.i]));
+                    dv.template next<C::kND>();
+                }
+            }
+            umma_commit(bar(ct.drained));                          // nothing is in flight when the block ends
+            mbar_wait_bounded(bar(ct.drained), 0, kTreeWaitNs);
+        }
+        __syncwarp();
+    } else if (warp >= kConvW) {
+        // ==== converters ====
+        const int grp = (warp - kConvW) >> 2, ctid = tid - 256 - 128 * grp, cw = ctid >> 5;
+        const bool do_k = grp == 0, do_v = C::kGroups == 1 || grp == 1;
+        const uint32_t tlane = static_cast<uint32_t>(32 * cw) << 16;
+        Ring d, k, kb, v, vb;
+        uint32_t nu = 0;
+        while (true) {
+            if (!wait(ct.dfull[d.i], d.ph)) break;
+            const TreeUnit u = ct.unit[d.i];
+            if (u.te < 0) break;
+            if (do_k) {
+                // ---- the unit's Q ----
+                if (!wait(ct.qempty, (nu & 1) ^ 1)) break;
+                constexpr int kU = kR / 8 < 8 ? kR / 8 : 8;
+                const int c16 = ctid & 15;
+                const float ks = C::kConv ? __ldg(p.k_scale + u.h) : 1.f;
+#pragma unroll
+                for (int r8 = 0; r8 < kR / 8; r8 += kU) {
+                    uint4 x[kU];
+#pragma unroll
+                    for (int i = 0; i < kU; ++i) {
+                        const int row = (r8 + i) * 8 + (ctid >> 4), tk = row / p.group;
+                        x[i] = make_uint4(0u, 0u, 0u, 0u);
+                        if (tk < u.ntok)
+                            x[i] = __ldg(reinterpret_cast<const uint4 *>(
+                                             p.q + (static_cast<int64_t>(u.tok0 + tk) * p.hq + u.h * p.group + (row - tk * p.group)) * 128) + c16);
+                    }
+#pragma unroll
+                    for (int i = 0; i < kU; ++i) {
+                        const int row = (r8 + i) * 8 + (ctid >> 4);
+                        float cs = p.scale_log2;
+                        if (C::kConv) {
+                            // f16 with a power of two per row that puts its largest element into [2^14, 2^15)
+                            uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+                            uint32_t big = 0;
+#pragma unroll
+                            for (int j = 0; j < 4; ++j) big = max(big, max(w[j] & 0x7FFFu, (w[j] >> 16) & 0x7FFFu));
+#pragma unroll
+                            for (int o = 1; o < 16; o <<= 1) big = max(big, __shfl_xor_sync(kAll, big, o));
+                            int e = static_cast<int>(big >> 7);
+                            if (e == 0 || e == 255) e = 141;       // zeros, infinities and NaN stay what they are
+                            e = max(e, 15);
+                            const float up = __uint_as_float(static_cast<uint32_t>(268 - e) << 23), down = __uint_as_float(static_cast<uint32_t>(e - 14) << 23);
+                            cs = cs * ks * down;
+#pragma unroll
+                            for (int j = 0; j < 4; ++j)
+                                w[j] = pack_f16x2(__uint_as_float(w[j] << 16) * up, __uint_as_float(w[j] & 0xFFFF0000u) * up);
+                            x[i] = make_uint4(w[0], w[1], w[2], w[3]);
+                        }
+                        st_shared_v4(sQ + (c16 >> 3) * (kR * 128) + row * 128 + (((c16 & 7) ^ (row & 7)) << 4), x[i]);
+                        if (c16 == 0) ct.colscale[d.i][row] = cs;
+                    }
+                }
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) {
+                    mbar_arrive(bar(ct.qfull));
+                    mbar_arrive(bar(ct.cfull[d.i]));
+                }
+            }
+            ++nu;
+            bool ok = true;
+            int odd_tiles = 0;
+            for (int i = u.tb; i < u.te && ok; ++i) {
+                if (do_k && C::kConv) {
+                    // ---- K: f16 rows in tensor memory ----
+                    if (!(ok = wait(ct.kfull[k.i], k.ph) && wait(ct.k16empty[kb.i], kb.ph ^ 1))) break;
+                    umma_fence_after();
+                    bool none = false;
+#pragma unroll
+                    for (int hf = 0; hf < 2; ++hf) {
+                        uint32_t f[32];
+                        half_row<C::kConv ? kKv : FKV_KV_FP8_E4M3, false>(sK + k.i * C::kStageB, ctid, hf, f, none);
+                        tmem_store(tmem + tlane + kb.i * 64 + 32 * hf, f);
+                    }
+                    tmem_store_wait();
+                    umma_fence_before();
+                    __syncwarp();
+                    if (lane == 0) {
+                        mbar_arrive(bar(ct.k16full[kb.i]));
+                        mbar_arrive(bar(ct.kempty[k.i]));
+                    }
+                    k.template next<C::kNK>();
+                    kb.template next<2>();
+                }
+                if (do_v) {
+                    // ---- V: f16 rows in an operand buffer ----
+                    if (!(ok = wait(ct.vfull[v.i], v.ph))) break;
+                    const uint32_t t0 = tile_at(u, i), t = t0 + ctid;
+                    const bool whole = tile_whole(u, p, t0), valid = t < tile_end(u, i);
+                    bool odd = false;
+                    if (C::kConv) {
+                        if (!(ok = wait(ct.v16empty[vb.i & 1], vb.ph ^ 1))) break;
+                        const uint32_t dst = sV16 + vb.i * C::kV16, src = sV + v.i * C::kStageB;
+                        if (whole) convert_v<C::kConv ? kKv : FKV_KV_FP8_E4M3, false>(src, dst, ctid, true);
+                        else odd = convert_v<C::kConv ? kKv : FKV_KV_FP8_E4M3, true>(src, dst, ctid, valid);
+                    } else if (!whole) {
+                        odd = clean_v(sV + v.i * C::kStageB, ctid, valid);
+                    }
+                    if (!whole) {
+                        const uint32_t m = __ballot_sync(kAll, odd);
+                        if (lane == 0) *const_cast<volatile uint32_t *>(&ct.poison[d.i][min(odd_tiles, kTreePoison - 1)][cw]) = m;
+                        ++odd_tiles;
+                    }
+                    if (C::kConv || !whole) fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) {
+                        mbar_arrive(bar(ct.vready[vb.i]));
+                        if (C::kConv) mbar_arrive(bar(ct.vempty[v.i]));
+                    }
+                    v.template next<C::kNV>();
+                    vb.template next<C::kNVR>();
+                }
+            }
+            if (!ok) break;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(ct.dempty[d.i]));
+            d.template next<C::kND>();
+        }
+        // ---- rows of requests without work ----
+        if (grp == 0) {
+            __syncwarp();
+            for (int r = blockIdx.x; r < p.batch; r += gridDim.x) {
+                const TreeRequest q = tree_request(p, r);
+                if (!q.rows || q.live) continue;
+                uint4 *o = reinterpret_cast<uint4 *>(p.out + static_cast<int64_t>(q.t0) * p.hq * 128);
+                const int64_t words = static_cast<int64_t>(q.n) * p.hq * 16;
+                for (int64_t i = ctid; i < words; i += 128) o[i] = make_uint4(0u, 0u, 0u, 0u);
+            }
+        }
+    } else {
+        // ==== softmax ====
+        constexpr int kNC = C::kNC, kCh = kNC < 32 ? kNC : 32, kChunks = kNC / kCh;
+        const int g = warp >> 2, wq = warp & 3, tok = tid & 127, col0 = g * kNC, barrier = 1 + g;
+        const uint32_t tlane = static_cast<uint32_t>(32 * wq) << 16;
+        const uint32_t sref = smem_u32(ct.ref) + 4 * col0;
+        Ring d, s, pr, last;                                       // units, S buffers, weight buffers; the last one handed over
+        bool bad = false;                                          // this thread's waits
+        float sum[kNC];
+        while (true) {
+            bad |= !wait(ct.dfull[d.i], d.ph);
+            if (group_any(barrier, bad)) break;
+            const TreeUnit u = ct.unit[d.i];
+            if (u.te < 0) break;
+            if (tok < kNC) ct.ref[col0 + tok] = -kTreeNone;
+#pragma unroll
+            for (int j = 0; j < kNC; ++j) sum[j] = 0.f;
+            bad |= !wait(ct.cfull[d.i], d.ph);
+            group_sync(barrier);
+            const uint32_t scs = smem_u32(ct.colscale[d.i]) + 4 * col0;
+            int odd_tiles = 0;
+            bool quit = false;
+            for (int i = u.tb; i < u.te; ++i) {
+                const uint32_t t0 = tile_at(u, i);
+                const bool whole = tile_whole(u, p, t0);
+                const uint64_t see = whole ? ~0ull : seen_by<kNC>(p, u, col0, t0 + tok);
+                odd_tiles += whole ? 0 : 1;
+                bad |= !wait(ct.sfull[s.i], s.ph);
+                umma_fence_after();
+                const uint32_t ts = tmem + tlane + C::kTmS + s.i * kR + col0;
+                float x[kCh];
+                // the exponents of kCh columns, relative to their references; unseen ones -infinity
+                auto exponents = [&](int ch) {
+                    tmem_load(ts + ch * kCh, x);
+#pragma unroll
+                    for (int j = 0; j < kCh; j += 4) {
+                        const float4 c4 = ld_shared_f4(scs + 4 * (ch * kCh + j)), r4 = ld_shared_f4(sref + 4 * (ch * kCh + j));
+                        // rounded products, as the references': a fused one would leave their rounding, up to 2^9 at
+                        // logits of 1e10, in the exponent
+                        const float2 a = unpack2(add2(mul2(pack2(x[j], x[j + 1]), pack2(c4.x, c4.y)), pack2(r4.x, r4.y)));
+                        const float2 b = unpack2(add2(mul2(pack2(x[j + 2], x[j + 3]), pack2(c4.z, c4.w)), pack2(r4.z, r4.w)));
+                        x[j] = a.x, x[j + 1] = a.y, x[j + 2] = b.x, x[j + 3] = b.y;
+                    }
+                    if (!whole) {
+#pragma unroll
+                        for (int j = 0; j < kCh; ++j)
+                            if (!((see >> (ch * kCh + j)) & 1)) x[j] = -INFINITY;
+                    }
+                };
+                float most = -INFINITY;
+#pragma unroll
+                for (int ch = kChunks - 1; ch >= 0; --ch) {
+                    exponents(ch);
+#pragma unroll
+                    for (int j = 0; j < kCh; ++j) most = fmaxf(most, x[j]);
+                }
+                if (group_any(barrier, most > kTreeMost || bad)) {
+                    if (group_any(barrier, bad)) {
+                        quit = true;
+                        break;
+                    }
+                    // ---- move the references of the columns that need it ----
+                    if (i > u.tb) bad |= !wait(ct.pempty[last.i], last.ph);      // the sums so far are complete
+                    umma_fence_after();
+                    constexpr int kSl = kNC < 16 ? kNC : 16;
+#pragma unroll
+                    for (int c = 0; c < kNC; c += kSl) {
+                        float y[kSl];
+                        tmem_load(ts + c, y);
+#pragma unroll
+                        for (int j = 0; j < kSl; ++j) {
+                            float z = __fmul_rn(y[j], *reinterpret_cast<const float *>(&ct.colscale[d.i][col0 + c + j]));
+                            if (!((see >> (c + j)) & 1)) z = -INFINITY;
+                            const int key = __float_as_int(z) ^ ((__float_as_int(z) >> 31) & 0x7FFFFFFF);   // ordered as the floats
+                            const int top = __reduce_max_sync(kAll, key);
+                            if (lane == 0) ct.redmax[g][wq][j] = top;
+                        }
+                        group_sync(barrier);
+                        float up[kSl], ref[kSl];
+                        bool any = false;
+#pragma unroll
+                        for (int j = 0; j < kSl; ++j) {
+                            const int key = max(max(ct.redmax[g][0][j], ct.redmax[g][1][j]), max(ct.redmax[g][2][j], ct.redmax[g][3][j]));
+                            const float z = __int_as_float(key ^ ((key >> 31) & 0x7FFFFFFF)), was = -ct.ref[col0 + c + j];
+                            const bool move = z - was > kTreeMost;
+                            ref[j] = move ? z - kTreeTop : was;
+                            up[j] = move ? ex2(was - ref[j]) : 1.f;
+                            any |= move;
+                            sum[c + j] *= up[j];
+                        }
+                        group_sync(barrier);                       // the old references are read
+                        if (tok < kSl) {
+#pragma unroll
+                            for (int j = 0; j < kSl; ++j)
+                                if (tok == j) ct.ref[col0 + c + j] = -ref[j];
+                        }
+                        if (any && i > u.tb) {
+                            const uint32_t to = tmem + tlane + C::kTmO + col0 + c;
+                            tmem_load(to, y);
+                            uint32_t o[8];
+#pragma unroll
+                            for (int b = 0; b < kSl; b += 8) {
+#pragma unroll
+                                for (int j = 0; j < 8; ++j) o[j] = __float_as_uint(y[b + j] * up[b + j]);
+                                tmem_store(to + b, o);
+                            }
+                            tmem_store_wait();
+                        }
+                    }
+                    umma_fence_before();
+                    group_sync(barrier);                           // the new references are there
+                    exponents(0);
+                }
+                // ---- weights ----
+                bad |= !wait(ct.pempty[pr.i], pr.ph ^ 1);
+#pragma unroll
+                for (int ch = 0; ch < kChunks; ++ch) {
+                    if (ch > 0) exponents(ch);                     // (chunk 0 was the last of the first pass)
+#pragma unroll
+                    for (int j = 0; j < kCh; ++j) {
+                        x[j] = ex2(x[j]);
+                        sum[ch * kCh + j] += x[j];
+                    }
+#pragma unroll
+                    for (int j = 0; j < kCh; j += 8) {
+                        const int col = col0 + ch * kCh + j;
+                        const uint32_t at = sP + pr.i * C::kParts * C::kPB + (col >> 6) * 16384 + tok * 128 + ((((col & 63) >> 3) ^ (tok & 7)) << 4);
+                        if (C::kConv) {
+                            st_shared_v4(at, make_uint4(pack_f16x2(x[j], x[j + 1]), pack_f16x2(x[j + 2], x[j + 3]),
+                                                        pack_f16x2(x[j + 4], x[j + 5]), pack_f16x2(x[j + 6], x[j + 7])));
+                        } else {
+                            // two bf16 words: one alone would round a weight by up to 2^-8
+                            uint32_t hi[4], lo[4];
+#pragma unroll
+                            for (int b = 0; b < 4; ++b) {
+                                const float e = x[j + 2 * b], f = x[j + 2 * b + 1];
+                                hi[b] = pack_bf16x2(e, f);
+                                lo[b] = pack_bf16x2(e - __uint_as_float(hi[b] << 16), f - __uint_as_float(hi[b] & 0xFFFF0000u));
+                            }
+                            st_shared_v4(at, make_uint4(hi[0], hi[1], hi[2], hi[3]));
+                            st_shared_v4(at + C::kPB, make_uint4(lo[0], lo[1], lo[2], lo[3]));
+                        }
+                    }
+                }
+                umma_fence_before();
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) {
+                    mbar_arrive(bar(ct.sempty[s.i]));
+                    mbar_arrive(bar(ct.pfull[pr.i]));
+                }
+                last = pr;
+                pr.template next<C::kNP>();
+                s.template next<2>();
+            }
+            if (quit) break;
+            // ---- end of this CTA's part of the unit ----
+            // sums over the tokens: halves of the columns go to the other lanes, step by step
+            spread_sums<kNC, 16>(sum, lane);
+            bad |= !wait(ct.pempty[last.i], last.ph);              // all products are done, the weights' buffers free
+            if (group_any(barrier, bad)) break;
+            umma_fence_after();
+            float *ls = kR <= 64 ? ct.lsum + g * 4 * kNC : reinterpret_cast<float *>(smem + C::kOffP + 16384 * g);
+            constexpr int kPer = kNC >= 32 ? kNC / 32 : 1, kSpan = kNC >= 32 ? 1 : 32 / kNC;   // columns a lane has; lanes with the same
+            if (lane % kSpan == 0) {
+#pragma unroll
+                for (int j = 0; j < kPer; ++j) ls[wq * kNC + (lane / kSpan) * kPer + j] = sum[j];
+            }
+            group_sync(barrier);
+            const bool wrong = *const_cast<volatile int32_t *>(&ct.unit[d.i].bad) != 0;
+            const float vs = C::kConv ? __ldg(p.v_scale + u.h) : 1.f;
+            const int dim = 32 * wq + lane;
+            bool anyodd = false;
+            for (int k = 0; k < min(odd_tiles, kTreePoison); ++k)
+                for (int w = 0; w < 4; ++w) anyodd |= *const_cast<volatile uint32_t *>(&ct.poison[d.i][k][w]) != 0;
+            constexpr int kE = kNC < 16 ? kNC : 16;
+#pragma unroll
+            for (int c = 0; c < kNC; c += kE) {
+                float y[kE];
+                tmem_load(tmem + tlane + C::kTmO + col0 + c, y);
+                if (anyodd) {
+                    // NaN and infinities of V that not every row sees: left out of the product, here for those who do
+                    int k = 0;
+                    for (int i = u.tb; i < u.te; ++i) {
+                        const uint32_t t0 = tile_at(u, i);
+                        if (tile_whole(u, p, t0)) continue;
+                        for (int b = 0; b < kTreeTok; ++b) {
+                            if (!((*const_cast<volatile uint32_t *>(&ct.poison[d.i][min(k, kTreePoison - 1)][b >> 5]) >> (b & 31)) & 1)) continue;
+                            const float add = odd_value<kKv>(p, u, t0 + b, dim);
+                            const uint64_t see = seen_by<kNC>(p, u, col0, t0 + b);
+#pragma unroll
+                            for (int j = 0; j < kE; ++j)
+                                if ((see >> (c + j)) & 1) y[j] += add;
+                        }
+                        ++k;
+                    }
+                }
+#pragma unroll
+                for (int j = 0; j < kE; ++j) {
+                    const int col = c + j, row = col0 + col, tk = row / p.group;
+                    const float l = (ls[col] + ls[kNC + col]) + (ls[2 * kNC + col] + ls[3 * kNC + col]);
+                    if (tk >= u.ntok) continue;
+                    if (u.slot >= 0) {
+                        const int64_t at = static_cast<int64_t>(u.slot) * kR + row;
+                        p.part_o[at * 128 + dim] = y[j];
+                        if (dim == 0) p.part_ml[at] = make_float2(-ct.ref[row], wrong ? -1.f : l);
+                    } else {
+                        const float o = wrong || l == 0.f ? 0.f : y[j] * (vs / l);
+                        p.out[(static_cast<int64_t>(u.tok0 + tk) * p.hq + u.h * p.group + (row - tk * p.group)) * 128 + dim] = __float2bfloat16_rn(o);
+                    }
+                }
+            }
+            umma_fence_before();
+            group_sync(barrier);                                   // references and sums are read
+            if (lane == 0) {
+                mbar_arrive(bar(ct.oempty));
+                mbar_arrive(bar(ct.dempty[d.i]));
+            }
+            d.template next<C::kND>();
+        }
+        __syncwarp();
+    }
+    umma_fence_before();
+    __syncthreads();
+    if (warp == kMmaW) {
+        umma_fence_after();
+        tmem_free(tmem, 512);
+    }
+}
+
+// ---------------------------------------------------------------------------
+// joining the parts of a unit that is cut
+// ---------------------------------------------------------------------------
+// Block (c, y): rows 8y .. of the unit whose last part CTA c had, a warp each.  The parts
+// are CTA c0's last one and the first ones of c0 + 1 .. c.
+__global__ void __launch_bounds__(256)
+tree_join_kernel(const TreeParams p, int rows) {
     grid_dep_wait();
     grid_dep_launch();
-    const int row = blockIdx.x, hq = blockIdx.y, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    // the request of this row: the last one whose rows begin at or before it
-    int r = row, t0 = row, t1 = row + 1;
-    if (p.token_indptr) {
-        int lo = 0, hi = p.batch;
-        while (hi - lo > 1) {
-            const int mid = (lo + hi) / 2;
-            if (p.token_indptr[mid] <= row) lo = mid;
-            else hi = mid;
-        }
-        r = lo;
-        t0 = p.token_indptr[r];
-        t1 = p.token_indptr[r + 1];
-        if (t0 < 0 || row < t0 || row >= t1 || t1 > p.n_tokens) return;      // no request's row
+    const int c = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int4 j = p.joins[c];
+    const int c0 = j.x, row = blockIdx.y * 8 + warp, tk = row / p.group;
+    if (c0 < 0 || tk >= j.z) return;
+    const int parts = c - c0 + 1;
+    auto slot = [&](int i) { return static_cast<int64_t>(i == 0 ? 2 * c0 + 1 : 2 * (c0 + i)) * rows + row; };
+    float top = -INFINITY;
+    bool wrong = false;
+    for (int i = lane; i < parts; i += 32) {
+        const float2 ml = p.part_ml[slot(i)];
+        wrong |= ml.y < 0.f;
+        if (ml.y != 0.f) top = fmaxf(top, ml.x);
     }
-    const int n = t1 - t0, len = p.seq_lens[r];
-    const int32_t b = p.indptr[r], e = p.indptr[r + 1];
-    bool ok = (!p.abort_mask || !p.abort_mask[r]) && len >= n && n <= 64 * p.words && b >= 0 && e >= b && e <= p.nnz &&
-              static_cast<int64_t>(e - b) * p.page_size >= len;
-    const int ctx = len - n;
-    uint64_t m[kTreeMaxWords] = {1, 0, 0, 0};
-    if (p.mask)
-        for (int w = 0; w < kTreeMaxWords; ++w) m[w] = w < p.words ? p.mask[static_cast<int64_t>(row) * p.words + w] : 0;
-    int depth = -1;
-    for (int w = 0; w < kTreeMaxWords; ++w) depth += __popcll(m[w]);
-    if (depth < 0) depth = 0;
-    const int64_t lo64 = p.window ? static_cast<int64_t>(ctx) + depth - p.window + 1 : 0;
-    const int lo = lo64 < 0 ? 0 : lo64 > ctx ? ctx : static_cast<int>(lo64);
-    const int head = p.window ? min(p.sinks, lo) : 0;
-    const int h = hq / (p.hq / p.hkv);
-    const __nv_bfloat16 *q = p.q + (static_cast<int64_t>(row) * p.hq + hq) * 128 + 4 * lane;
-    const float4 qv = make_float4(__bfloat162float(q[0]), __bfloat162float(q[1]), __bfloat162float(q[2]), __bfloat162float(q[3]));
-    const float ks = kKv == FKV_KV_BF16 ? 1.f : p.k_scale[h], vs = kKv == FKV_KV_BF16 ? 1.f : p.v_scale[h];
-    const float c = p.scale_log2 * ks;
-    float top = -INFINITY, sum = 0.f;
-    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-    bool bad = false;
-    if (ok) {
-        const int seen = head + len - lo;
-        for (int i = warp; i < seen; i += kTreeBlock / 32) {
-            const int t = i < head ? i : lo + i - head, j = t - ctx;
-            const int pg = p.indices[b + t / p.page_size];
-            if (pg < 0 || pg >= p.pages) {
-                bad = true;
-                continue;
-            }
-            if (j >= 0 && !((m[j >> 6] >> (j & 63)) & 1)) continue;
-            const int64_t at = (static_cast<int64_t>(pg) * p.hkv + h) * p.page_size + t % p.page_size;
-            const float4 k = load4<kKv>(p.k_cache, at, lane), v = load4<kKv>(p.v_cache, at, lane);
-            float z = qv.x * k.x + qv.y * k.y + qv.z * k.z + qv.w * k.w;
 #pragma unroll
-            for (int x = 16; x; x >>= 1) z += __shfl_xor_sync(0xffffffffu, z, x);
-            z *= c;
-            if (z > top) {
-                const float f = exp2f(top - z);
-                sum *= f;
-                o.x *= f, o.y *= f, o.z *= f, o.w *= f;
-                top = z;
-            }
-            const float w = z == -INFINITY ? 0.f : exp2f(z - top);
-            sum += w;
-            o.x = fmaf(w, v.x, o.x), o.y = fmaf(w, v.y, o.y), o.z = fmaf(w, v.z, o.z), o.w = fmaf(w, v.w, o.w);
+    for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(kAll, top, o));
+    wrong = __any_sync(kAll, wrong);
+    float l = 0.f;
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (!wrong) {
+#pragma unroll 4
+        for (int i = 0; i < parts; ++i) {
+            const int64_t at = slot(i);
+            const float2 ml = p.part_ml[at];
+            const float4 x = reinterpret_cast<const float4 *>(p.part_o + at * 128)[lane];
+            if (ml.y == 0.f) continue;                             // it saw nothing
+            const float f = ex2(ml.x - top);
+            l = fmaf(f, ml.y, l);
+            o.x = fmaf(f, x.x, o.x), o.y = fmaf(f, x.y, o.y), o.z = fmaf(f, x.z, o.z), o.w = fmaf(f, x.w, o.w);
         }
     }
-    __shared__ float4 s_o[kTreeBlock];
-    __shared__ float s_top[kTreeBlock / 32], s_sum[kTreeBlock / 32];
-    __shared__ int s_bad;
-    if (threadIdx.x == 0) s_bad = 0;
-    __syncthreads();
-    if (bad && lane == 0) s_bad = 1;
-    s_o[threadIdx.x] = o;
-    if (lane == 0) s_top[warp] = top, s_sum[warp] = sum;
-    __syncthreads();
-    if (warp) return;
-    float all = -INFINITY, den = 0.f;
-    for (int w = 0; w < kTreeBlock / 32; ++w) all = fmaxf(all, s_top[w]);
-    float4 num = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int w = 0; w < kTreeBlock / 32; ++w) {
-        const float f = s_sum[w] == 0.f ? 0.f : exp2f(s_top[w] - all);
-        const float4 x = s_o[32 * w + lane];
-        if (s_sum[w] == 0.f) continue;
-        den = fmaf(f, s_sum[w], den);
-        num.x = fmaf(f, x.x, num.x), num.y = fmaf(f, x.y, num.y), num.z = fmaf(f, x.z, num.z), num.w = fmaf(f, x.w, num.w);
-    }
-    if (s_bad && lane == 0) atomicOr(p.err, FKV_DEVERR_ATTN_PAGE);
-    const float g = s_bad || den == 0.f ? 0.f : vs / den;
-    if (g == 0.f) num = make_float4(0.f, 0.f, 0.f, 0.f);
+    const float g = l == 0.f ? 0.f : (p.v_scale ? __ldg(p.v_scale + j.w) : 1.f) / l;
+    if (l == 0.f) o = make_float4(0.f, 0.f, 0.f, 0.f);
     uint2 w;
-    w.x = pack_bf16x2(num.x * g, num.y * g);
-    w.y = pack_bf16x2(num.z * g, num.w * g);
-    reinterpret_cast<uint2 *>(p.out + (static_cast<int64_t>(row) * p.hq + hq) * 128)[lane] = w;
+    w.x = pack_bf16x2(o.x * g, o.y * g);
+    w.y = pack_bf16x2(o.z * g, o.w * g);
+    reinterpret_cast<uint2 *>(p.out + (static_cast<int64_t>(j.y + tk) * p.hq + j.w * p.group + (row - tk * p.group)) * 128)[lane] = w;
 }
 
+// ---------------------------------------------------------------------------
+// host side
+// ---------------------------------------------------------------------------
 namespace {
+
+constexpr int kMaxDev = 64;
+std::mutex g_mu;
+unsigned long long g_ready[kMaxDev][3][4];                         // the context in which an instance's shared memory was set
+
+PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
+    static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
+    static std::once_flag once;
+    std::call_once(once, [] {
+        void *f = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &q) == cudaSuccess &&
+            q == cudaDriverEntryPointSuccess)
+            fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(f);
+    });
+    return fn;
+}
+
+// A pool as a 4-D tensor; a box is a page's rows of one KV head (BF16: 64 of their dims).
+bool page_map(CUtensorMap *m, const void *pool, bool fp8, int P, int Hkv, int S) {
+    const auto enc = encode_fn();
+    if (!enc) return false;
+    const cuuint64_t row = fp8 ? 128 : 256;
+    const cuuint64_t dims[4] = {128, static_cast<cuuint64_t>(S), static_cast<cuuint64_t>(Hkv), static_cast<cuuint64_t>(P)};
+    const cuuint64_t strides[3] = {row, row * S, row * S * Hkv};
+    const cuuint32_t box[4] = {fp8 ? 128u : 64u, static_cast<cuuint32_t>(S), 1u, 1u}, step[4] = {1u, 1u, 1u, 1u};
+    return enc(m, fp8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void *>(pool), dims, strides, box,
+               step, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
 
 bool known_kv(int kv) { return kv == FKV_KV_FP8_E4M3 || kv == FKV_KV_BF16 || kv == FKV_KV_FP4; }
 
-fkv_status run(TreeParams p, int kv, void *stream) {
-    const dim3 grid(static_cast<unsigned>(p.n_tokens), static_cast<unsigned>(p.hq));
-    auto go = [&](auto kern) { return launch_pdl(kern, grid, dim3(kTreeBlock), 0, static_cast<cudaStream_t>(stream), p); };
-    const cudaError_t e = kv == FKV_KV_FP8_E4M3 ? go(tree_attn_kernel<FKV_KV_FP8_E4M3>)
-                          : kv == FKV_KV_BF16   ? go(tree_attn_kernel<FKV_KV_BF16>)
-                                                : go(tree_attn_kernel<FKV_KV_FP4>);
-    return e == cudaSuccess ? FKV_OK : FKV_ERR_CUDA;
+// Rows of a unit: the smallest instance that holds the query heads of the requests' mean
+// number of tokens.
+int rows_of(int64_t n_tokens, int64_t batch, int64_t group) {
+    const int64_t want = group * ((n_tokens + batch - 1) / (batch > 0 ? batch : 1));
+    for (int r = 16; r < 128; r *= 2)
+        if (want <= r) return r;
+    return 128;
+}
+
+size_t align256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
+struct TreeWs {
+    size_t joins, ml, o, total;
+};
+TreeWs tree_ws(int sms, int rows) {
+    TreeWs w;
+    w.joins = 0;
+    w.ml = align256(sizeof(int4) * sms);
+    w.o = align256(w.ml + sizeof(float2) * 2 * sms * rows);
+    w.total = align256(w.o + sizeof(float) * 128 * 2 * sms * rows);
+    return w;
+}
+
+template <int kKv, int kR>
+fkv_status launch_tree(const TreeParams &p, int sms, const CUtensorMap &tmK, const CUtensorMap &tmV, cudaStream_t st) {
+    constexpr int smem = tree_smem<kKv, kR>();
+    static_assert(smem <= 232448, "shared memory of a CTA");
+    int dev = -1;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDev) return FKV_ERR_CUDA;
+    {
+        std::lock_guard<std::mutex> lk(g_mu);
+        constexpr int ri = kR == 16 ? 0 : kR == 32 ? 1 : kR == 64 ? 2 : 3;
+        const unsigned long long ctx = current_context_id();
+        if (ctx == 0 || g_ready[dev][kKv][ri] != ctx) {
+            if (cudaFuncSetAttribute(tree_attn_kernel<kKv, kR>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
+                return FKV_ERR_CUDA;
+            g_ready[dev][kKv][ri] = current_context_id();
+        }
+    }
+    if (launch_pdl(tree_attn_kernel<kKv, kR>, dim3(sms), dim3(TreeCfg<kKv, kR>::kThreads), smem, st, p, tmK, tmV) != cudaSuccess)
+        return FKV_ERR_CUDA;
+    return launch_pdl(tree_join_kernel, dim3(sms, kR / 8), dim3(256), 0, st, p, kR) == cudaSuccess ? FKV_OK : FKV_ERR_CUDA;
+}
+
+template <int kKv>
+fkv_status launch_rows(int rows, const TreeParams &p, int sms, const CUtensorMap &tmK, const CUtensorMap &tmV, cudaStream_t st) {
+    return rows == 16   ? launch_tree<kKv, 16>(p, sms, tmK, tmV, st)
+           : rows == 32 ? launch_tree<kKv, 32>(p, sms, tmK, tmV, st)
+           : rows == 64 ? launch_tree<kKv, 64>(p, sms, tmK, tmV, st)
+                        : launch_tree<kKv, 128>(p, sms, tmK, tmV, st);
+}
+
+// Both calls.  tree: rows and masks per drafted token; else one token a request.
+fkv_status attend(bool tree, const void *q, int32_t n_tokens, int32_t num_q_heads, const void *k_cache, const void *v_cache,
+                  int32_t kv_dtype, const float *k_scale, const float *v_scale, int32_t num_pages, int32_t num_kv_heads,
+                  int32_t page_size, int32_t head_dim, const int32_t *page_indptr, const int32_t *page_indices, int64_t nnz,
+                  const int32_t *seq_lens, int32_t batch, const int32_t *token_indptr, const uint64_t *tree_mask,
+                  int32_t mask_words, int32_t window, int32_t sinks, const uint8_t *abort_mask, float sm_scale, void *out,
+                  void *workspace, size_t workspace_bytes, void *stream) {
+    if (n_tokens < 0 || batch < 0 || num_q_heads <= 0 || num_kv_heads <= 0 || num_pages <= 0 || nnz < 0) return FKV_ERR_INVALID_ARG;
+    if (num_q_heads % num_kv_heads || window < 0 || sinks < 0 || mask_words < 1) return FKV_ERR_INVALID_ARG;
+    if (!known_kv(kv_dtype)) return FKV_ERR_INVALID_ARG;
+    if (head_dim != 128 || num_q_heads / num_kv_heads > 128 || mask_words > kTreeMaxWords) return FKV_ERR_UNSUPPORTED;
+    if (page_size != 16 && page_size != 32 && page_size != 64 && page_size != 128) return FKV_ERR_UNSUPPORTED;
+    if (!(sm_scale > 0.f) || !std::isfinite(sm_scale)) return FKV_ERR_INVALID_ARG;
+    if (batch == 0 || n_tokens == 0) return FKV_OK;
+    // a page's rows are counted in 32 bits by the 4-bit copies
+    if (kv_dtype == FKV_KV_FP4 && static_cast<int64_t>(num_kv_heads) * page_size * FKV_FP4_ROW_BYTES > 0x7FFFFFFF)
+        return FKV_ERR_UNSUPPORTED;
+    if (!q || !k_cache || !v_cache || !page_indptr || !seq_lens || !out || !workspace) return FKV_ERR_INVALID_ARG;
+    if (tree && (!token_indptr || !tree_mask)) return FKV_ERR_INVALID_ARG;
+    if (nnz > 0 && !page_indices) return FKV_ERR_INVALID_ARG;
+    if (kv_dtype != FKV_KV_BF16 && (!k_scale || !v_scale)) return FKV_ERR_INVALID_ARG;
+    if (!aligned16(q) || !aligned16(k_cache) || !aligned16(v_cache) || !aligned16(out) ||
+        (reinterpret_cast<uintptr_t>(workspace) & 255u))
+        return FKV_ERR_INVALID_ARG;
+    uint32_t *err = device_error_word();
+    const int sms = device_sm_count();
+    if (!err || sms <= 0) return FKV_ERR_CUDA;
+    const int group = num_q_heads / num_kv_heads, rows = rows_of(n_tokens, batch, group);
+    const TreeWs w = tree_ws(sms, rows);
+    if (workspace_bytes < w.total) return FKV_ERR_INVALID_ARG;
+    CUtensorMap tmK = {}, tmV = {};                                // unused by the 4-bit cache's untiled copies
+    const bool fp8 = kv_dtype == FKV_KV_FP8_E4M3;
+    if (kv_dtype != FKV_KV_FP4 && (!page_map(&tmK, k_cache, fp8, num_pages, num_kv_heads, page_size) ||
+                                   !page_map(&tmV, v_cache, fp8, num_pages, num_kv_heads, page_size)))
+        return FKV_ERR_CUDA;
+    uint8_t *ws = static_cast<uint8_t *>(workspace);
+    TreeParams p;
+    p.q = static_cast<const __nv_bfloat16 *>(q);
+    p.k_cache = static_cast<const uint8_t *>(k_cache);
+    p.v_cache = static_cast<const uint8_t *>(v_cache);
+    p.k_scale = kv_dtype == FKV_KV_BF16 ? nullptr : k_scale;
+    p.v_scale = kv_dtype == FKV_KV_BF16 ? nullptr : v_scale;
+    p.indptr = page_indptr;
+    p.indices = page_indices;
+    p.seq_lens = seq_lens;
+    p.token_indptr = tree ? token_indptr : nullptr;
+    p.mask = tree ? tree_mask : nullptr;
+    p.abort_mask = abort_mask;
+    p.out = static_cast<__nv_bfloat16 *>(out);
+    p.err = err;
+    p.joins = reinterpret_cast<int4 *>(ws + w.joins);
+    p.part_ml = reinterpret_cast<float2 *>(ws + w.ml);
+    p.part_o = reinterpret_cast<float *>(ws + w.o);
+    p.nnz = nnz;
+    p.batch = batch;
+    p.n_tokens = n_tokens;
+    p.hq = num_q_heads;
+    p.hkv = num_kv_heads;
+    p.group = group;
+    p.pages = num_pages;
+    p.page_size = page_size;
+    p.words = mask_words;
+    p.window = window;
+    p.sinks = sinks;
+    p.scale_log2 = sm_scale * 1.4426950408889634f;
+    const cudaStream_t st = static_cast<cudaStream_t>(stream);
+    return fp8                         ? launch_rows<FKV_KV_FP8_E4M3>(rows, p, sms, tmK, tmV, st)
+           : kv_dtype == FKV_KV_BF16 ? launch_rows<FKV_KV_BF16>(rows, p, sms, tmK, tmV, st)
+                                     : launch_rows<FKV_KV_FP4>(rows, p, sms, tmK, tmV, st);
 }
 
 }  // namespace
@@ -178,7 +1246,8 @@ extern "C" size_t paged_tree_attn_workspace_size(int32_t n_tokens, int32_t batch
                                                  int32_t head_dim, int32_t kv_dtype) {
     if (n_tokens < 0 || batch < 0 || num_q_heads <= 0 || num_kv_heads <= 0 || num_q_heads % num_kv_heads) return 0;
     if (head_dim != 128 || !known_kv(kv_dtype) || num_q_heads / num_kv_heads > 128) return 0;
-    return 256;
+    const int sms = device_sm_count();
+    return sms <= 0 ? 0 : tree_ws(sms, rows_of(n_tokens, batch, num_q_heads / num_kv_heads)).total;
 }
 
 extern "C" fkv_status paged_tree_attn(const void *q, int32_t n_tokens, int32_t num_q_heads, const void *k_cache,
@@ -189,51 +1258,9 @@ extern "C" fkv_status paged_tree_attn(const void *q, int32_t n_tokens, int32_t n
                                       const uint64_t *tree_mask, int32_t mask_words, int32_t window, int32_t sinks,
                                       const uint8_t *abort_mask, float sm_scale, void *out, void *workspace,
                                       size_t workspace_bytes, void *stream) {
-    const bool tree = token_indptr || tree_mask || mask_words;
-    if (n_tokens < 0 || batch < 0 || num_q_heads <= 0 || num_kv_heads <= 0 || num_pages <= 0 || nnz < 0) return FKV_ERR_INVALID_ARG;
-    if (num_q_heads % num_kv_heads || window < 0 || sinks < 0) return FKV_ERR_INVALID_ARG;
-    if (!known_kv(kv_dtype)) return FKV_ERR_INVALID_ARG;
-    if (head_dim != 128 || num_q_heads / num_kv_heads > 128 || mask_words > kTreeMaxWords) return FKV_ERR_UNSUPPORTED;
-    if (page_size != 16 && page_size != 32 && page_size != 64 && page_size != 128) return FKV_ERR_UNSUPPORTED;
-    if (!(sm_scale > 0.f) || !std::isfinite(sm_scale) || mask_words < (tree ? 1 : 0)) return FKV_ERR_INVALID_ARG;
-    if (batch == 0 || n_tokens == 0) return FKV_OK;
-    if (!q || !k_cache || !v_cache || !page_indptr || !seq_lens || !out || !workspace) return FKV_ERR_INVALID_ARG;
-    if (tree ? !token_indptr || !tree_mask : n_tokens != batch) return FKV_ERR_INVALID_ARG;
-    if (nnz > 0 && !page_indices) return FKV_ERR_INVALID_ARG;
-    if (kv_dtype != FKV_KV_BF16 && (!k_scale || !v_scale)) return FKV_ERR_INVALID_ARG;
-    if (!aligned16(q) || !aligned16(k_cache) || !aligned16(v_cache) || !aligned16(out) ||
-        (reinterpret_cast<uintptr_t>(workspace) & 255u))
-        return FKV_ERR_INVALID_ARG;
-    uint32_t *err = device_error_word();
-    if (!err) return FKV_ERR_CUDA;
-    if (workspace_bytes < paged_tree_attn_workspace_size(n_tokens, batch, num_q_heads, num_kv_heads, head_dim, kv_dtype))
-        return FKV_ERR_INVALID_ARG;
-    TreeParams p;
-    p.q = static_cast<const __nv_bfloat16 *>(q);
-    p.k_cache = static_cast<const uint8_t *>(k_cache);
-    p.v_cache = static_cast<const uint8_t *>(v_cache);
-    p.k_scale = k_scale;
-    p.v_scale = v_scale;
-    p.indptr = page_indptr;
-    p.indices = page_indices;
-    p.seq_lens = seq_lens;
-    p.token_indptr = token_indptr;
-    p.mask = tree_mask;
-    p.abort_mask = abort_mask;
-    p.out = static_cast<__nv_bfloat16 *>(out);
-    p.err = err;
-    p.nnz = nnz;
-    p.batch = batch;
-    p.n_tokens = n_tokens;
-    p.hq = num_q_heads;
-    p.hkv = num_kv_heads;
-    p.pages = num_pages;
-    p.page_size = page_size;
-    p.words = tree ? mask_words : 1;
-    p.window = window;
-    p.sinks = sinks;
-    p.scale_log2 = sm_scale * 1.4426950408889634f;
-    return run(p, kv_dtype, stream);
+    return attend(true, q, n_tokens, num_q_heads, k_cache, v_cache, kv_dtype, k_scale, v_scale, num_pages, num_kv_heads, page_size,
+                  head_dim, page_indptr, page_indices, nnz, seq_lens, batch, token_indptr, tree_mask, mask_words, window, sinks,
+                  abort_mask, sm_scale, out, workspace, workspace_bytes, stream);
 }
 
 extern "C" fkv_status paged_window_attn(const void *q, int32_t batch, int32_t num_q_heads, const void *k_cache,
@@ -243,7 +1270,7 @@ extern "C" fkv_status paged_window_attn(const void *q, int32_t batch, int32_t nu
                                         const int32_t *seq_lens, int32_t window, int32_t sinks, const uint8_t *abort_mask,
                                         float sm_scale, void *out, void *workspace, size_t workspace_bytes, void *stream) {
     if (window <= 0) return FKV_ERR_INVALID_ARG;
-    return paged_tree_attn(q, batch, num_q_heads, k_cache, v_cache, kv_dtype, k_scale, v_scale, num_pages, num_kv_heads,
-                           page_size, head_dim, page_indptr, page_indices, nnz, seq_lens, batch, nullptr, nullptr, 0, window,
-                           sinks, abort_mask, sm_scale, out, workspace, workspace_bytes, stream);
+    return attend(false, q, batch, num_q_heads, k_cache, v_cache, kv_dtype, k_scale, v_scale, num_pages, num_kv_heads, page_size,
+                  head_dim, page_indptr, page_indices, nnz, seq_lens, batch, nullptr, nullptr, 1, window, sinks, abort_mask, sm_scale,
+                  out, workspace, workspace_bytes, stream);
 }
