@@ -147,7 +147,13 @@ struct TreeCfg {
     static constexpr int kQB = kR * 256;
     static constexpr int kV16 = kConv ? 32768 : 0;
     static constexpr int kGroups = kR <= 64 ? 2 : 1;               // converter groups: K and V, or one for both
-    static constexpr int kThreads = 256 + 128 * kGroups + 64;
+    // Softmax warps with many columns take registers of the others: of a thread, at launch, then
+    // of the three kinds of warps (no more in all than at launch; whole groups of four warps).
+    static constexpr bool kShift = kR > 32;
+    static constexpr int kThreads = 256 + 128 * kGroups + (kShift ? 128 : 64);     // softmax, converters, producer and issuer
+    static constexpr int kRegs = kGroups == 2 ? 96 : 128;
+    static constexpr int kRegsSoft = kGroups == 2 ? 128 : 176, kRegsConv = kGroups == 2 ? 80 : 88, kRegsRest = kGroups == 2 ? 64 : 72;
+    static_assert(2 * kRegsSoft + kGroups * kRegsConv + kRegsRest <= (2 + kGroups + 1) * kRegs, "the block's registers");
     static constexpr int kND = kR <= 64 ? 4 : 2;                   // units in flight
     static constexpr int kNC = kR / 2;                             // columns of a softmax group
     // tensor memory columns: K f16 (two buffers), S (two), O
@@ -168,10 +174,10 @@ struct TreeCtrl {
     TreeUnit unit[C::kND];
     alignas(16) float colscale[C::kND][kR];                        // a logit in log2 units per unit of S
     alignas(16) float ref[kR];                                     // the columns' references, negated
-    int32_t redmax[2][4][16];
+    int32_t redmax[2][4][8];
     float lsum[kR <= 64 ? 2 * 4 * C::kNC : 1];                     // (kR = 128: in the weights' buffer)
     uint32_t poison[C::kND][kTreePoison][4];                       // tokens whose V holds NaN or infinities
-    int64_t scan[18];                                             // one per warp
+    int64_t scan[20];                                             // one per warp
     int64_t total, off0;
     int32_t r0;
     uint32_t tmem;
@@ -200,21 +206,23 @@ struct Ring {                                  // a buffer of a ring and the par
     }
 };
 
-// Waits for a phase, for at most kTreeWaitNs and until another thread has given up.
+// Waits for a phase, for at most kTreeWaitNs and until another thread has given up.  The
+// timer is read after a few thousand cycles only: reading it takes about a microsecond.
 __device__ __forceinline__ bool tree_wait(uint32_t bar, uint32_t parity, volatile int32_t *dead, uint32_t *err) {
-    if (mbar_try_wait(bar, parity)) return true;
-    const uint64_t t0 = globaltimer_ns();
-    for (uint32_t i = 1;; ++i) {
+#pragma unroll 1
+    for (int i = 0; i < 256; ++i)
         if (mbar_try_wait(bar, parity)) return true;
-        if ((i & 31u) == 0) {
-            if (*dead) return false;
-            if (globaltimer_ns() - t0 > kTreeWaitNs) {
-                *dead = 1;
-                atomicOr(err, FKV_DEVERR_TIMEOUT);
-                return false;
-            }
+    const uint64_t t0 = globaltimer_ns();
+#pragma unroll 1
+    while (!*dead) {
+        for (int i = 0; i < 64; ++i)
+            if (mbar_try_wait(bar, parity)) return true;
+        if (globaltimer_ns() - t0 > kTreeWaitNs) {
+            *dead = 1;
+            atomicOr(err, FKV_DEVERR_TIMEOUT);
         }
     }
+    return false;
 }
 
 // Whether any of the 128 threads of a softmax group says so (a barrier of the group).
@@ -487,7 +495,9 @@ tree_attn_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmK, co
     const uint32_t tmem = ct.tmem;
     grid_dep_launch();
 
-    if (warp == kProdW) {
+    if (warp >= kProdW) {
+        if constexpr (C::kShift) regs_down<C::kRegsRest>();
+        if (warp == kProdW) {
         // ==== producer ====
         const uint64_t once = l2_policy_evict_first(), again = l2_policy_evict_normal();
         int r = ct.r0;
@@ -594,84 +604,94 @@ tree_attn_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmK, co
             const uint64_t t0 = globaltimer_ns();
             while (globaltimer_ns() - t0 < 200000000ull) __nanosleep(1000);
         }
-    } else if (warp == kMmaW) {
+        } else if (warp == kMmaW) {
         // ==== issuer ====
-        if (lane == 0) {
-            constexpr bool kB16 = !C::kConv;
-            constexpr uint32_t idS = umma_idesc(kB16, false, false, 128, kR), idO = umma_idesc(kB16, true, true, 128, kR);
-            Ring dq, dv, kr, s, vr, pr;                            // units of S and of O, K buffers, S, V buffers, weights
-            int sq = 0, sqe = 0, so = 0, soe = 0;                  // tiles left to do: next and end
-            uint32_t nq = 0, no = 0;                               // units begun
-            bool ok = true, more = true;
-            auto step_s = [&]() {                                  // S of the next tile, if there is one
-                if (!more || !ok) return;
-                if (sq == sqe) {
-                    if (!(ok = wait(ct.dfull[dq.i], dq.ph))) return;
-                    sq = *const_cast<volatile int32_t *>(&ct.unit[dq.i].tb);
-                    sqe = *const_cast<volatile int32_t *>(&ct.unit[dq.i].te);
-                    if (sqe < 0) {
-                        more = false;
-                        return;
-                    }
-                    dq.template next<C::kND>();
-                    if (!(ok = wait(ct.qfull, nq & 1))) return;
-                    ++nq;
+        // The whole warp waits, one lane issues: products and commits come from the same thread.
+        constexpr bool kB16 = !C::kConv;
+        constexpr uint32_t idS = umma_idesc(kB16, false, false, 128, kR), idO = umma_idesc(kB16, true, true, 128, kR);
+        constexpr uint32_t kHi = umma_desc_hi(1024);
+        const uint32_t lQ = umma_desc_lo(sQ, 16), lK = umma_desc_lo(sK, 16), lP = umma_desc_lo(sP, 16384),
+                       lV = umma_desc_lo(C::kConv ? sV16 : sV, 16384);
+        constexpr uint32_t kVStep = (C::kConv ? C::kV16 : C::kStageB) / 16;
+        Ring dq, dv, kr, s, vr, pr;                                // units of S and of O, K buffers, S, V buffers, weights
+        int sq = 0, sqe = 0, so = 0, soe = 0;                      // tiles left to do: next and end
+        uint32_t nq = 0, no = 0;                                   // units begun
+        bool ok = true, more = true;
+        auto step_s = [&]() {                                      // S of the next tile, if there is one
+            if (!more || !ok) return;
+            if (sq == sqe) {
+                if (!(ok = wait(ct.dfull[dq.i], dq.ph))) return;
+                sq = *const_cast<volatile int32_t *>(&ct.unit[dq.i].tb);
+                sqe = *const_cast<volatile int32_t *>(&ct.unit[dq.i].te);
+                if (sqe < 0) {
+                    more = false;
+                    return;
                 }
-                if (!(ok = wait(kB16 ? ct.kfull[kr.i] : ct.k16full[kr.i], kr.ph) && wait(ct.sempty[s.i], s.ph ^ 1))) return;
-                umma_fence_after();
-                const uint32_t dst = tmem + C::kTmS + s.i * kR;
+                dq.template next<C::kND>();
+                if (!(ok = wait(ct.qfull, nq & 1))) return;
+                ++nq;
+            }
+            if (!(ok = wait(kB16 ? ct.kfull[kr.i] : ct.k16full[kr.i], kr.ph) && wait(ct.sempty[s.i], s.ph ^ 1))) return;
+            umma_fence_after();
+            const uint32_t dst = tmem + C::kTmS + s.i * kR, ta = tmem + kr.i * 64, la = lK + kr.i * (C::kStageB / 16);
+            ++sq;
+            __syncwarp();
+            if (elect_one()) {
 #pragma unroll
                 for (int kk = 0; kk < 8; ++kk) {
-                    const uint64_t b = umma_desc(sQ + (kk >> 2) * (kR * 128) + (kk & 3) * 32, 16, 1024);
-                    if (kB16)
-                        umma_ss(dst, umma_desc(sK + kr.i * C::kStageB + (kk >> 2) * 16384 + (kk & 3) * 32, 16, 1024), b, idS, kk > 0);
-                    else
-                        umma_ts(dst, tmem + kr.i * 64 + kk * 8, b, idS, kk > 0);
+                    const uint64_t b = umma_desc(lQ + (kk >> 2) * (kR * 8) + (kk & 3) * 2, kHi);
+                    if (kB16) umma_ss(dst, umma_desc(la + (kk >> 2) * 1024 + (kk & 3) * 2, kHi), b, idS, kk > 0);
+                    else umma_ts(dst, ta + kk * 8, b, idS, kk > 0);
                 }
                 umma_commit(bar(ct.sfull[s.i]));
                 umma_commit(bar(kB16 ? ct.kempty[kr.i] : ct.k16empty[kr.i]));
-                if (++sq == sqe) umma_commit(bar(ct.qempty));
-                kr.template next<kB16 ? C::kNK : 2>();
-                s.template next<2>();
-            };
+                if (sq == sqe) umma_commit(bar(ct.qempty));
+            }
+            __syncwarp();
+            kr.template next<kB16 ? C::kNK : 2>();
+            s.template next<2>();
+        };
+        step_s();
+        while (ok) {
             step_s();
-            while (ok && (more || so != soe || dv.i != dq.i || dv.ph != dq.ph)) {
-                step_s();
-                if (!ok) break;
-                const bool first = so == soe;                      // of a unit: it starts its sums anew
-                if (first) {
-                    if (dv.i == dq.i && dv.ph == dq.ph) break;     // no unit left
-                    so = *const_cast<volatile int32_t *>(&ct.unit[dv.i].tb);
-                    soe = *const_cast<volatile int32_t *>(&ct.unit[dv.i].te);
-                    if (no && !(ok = wait(ct.oempty, (no - 1) & 1))) break;
-                    ++no;
-                }
-                if (!(ok = wait(ct.pfull[pr.i], pr.ph) && wait(ct.vready[vr.i], vr.ph))) break;
-                umma_fence_after();
+            if (!ok) break;
+            const bool first = so == soe;                          // of a unit: it starts its sums anew
+            if (first) {
+                if (dv.i == dq.i && dv.ph == dq.ph) break;         // no unit left
+                so = *const_cast<volatile int32_t *>(&ct.unit[dv.i].tb);
+                soe = *const_cast<volatile int32_t *>(&ct.unit[dv.i].te);
+                if (no && !(ok = wait(ct.oempty, (no - 1) & 1))) break;
+                ++no;
+            }
+            if (!(ok = wait(ct.vready[vr.i], vr.ph) && wait(ct.pfull[pr.i], pr.ph))) break;
+            umma_fence_after();
+            const uint32_t lv = lV + vr.i * kVStep, lp = lP + pr.i * (C::kParts * C::kPB / 16);
+            ++so;
+            __syncwarp();
+            if (elect_one()) {
 #pragma unroll
                 for (int w = 0; w < C::kParts; ++w) {
 #pragma unroll
-                    for (int kk = 0; kk < 8; ++kk) {
-                        const uint32_t va = C::kConv ? sV16 + vr.i * C::kV16 : sV + vr.i * C::kStageB;
-                        umma_ss(tmem + C::kTmO, umma_desc(va + kk * 2048, 16384, 1024),
-                                umma_desc(sP + (pr.i * C::kParts + w) * C::kPB + kk * 2048, 16384, 1024), idO, !first || w > 0 || kk > 0);
-                    }
+                    for (int kk = 0; kk < 8; ++kk)
+                        umma_ss(tmem + C::kTmO, umma_desc(lv + kk * 128, kHi), umma_desc(lp + w * (C::kPB / 16) + kk * 128, kHi), idO,
+                                !first || w > 0 || kk > 0);
                 }
                 umma_commit(bar(ct.pempty[pr.i]));
                 umma_commit(bar(C::kConv ? ct.v16empty[vr.i & 1] : ct.vempty[vr.i]));
-                pr.template next<C::kNP>();
-                vr.template next<C::kNVR>();
-                if (++so == soe) {
-                    mbar_arrive(bar(ct.dempty[dv.i]));
-                    dv.template next<C::kND>();
-                }
+                if (so == soe) mbar_arrive(bar(ct.dempty[dv.i]));
             }
-            umma_commit(bar(ct.drained));                          // nothing is in flight when the block ends
-            mbar_wait_bounded(bar(ct.drained), 0, kTreeWaitNs);
+            __syncwarp();
+            pr.template next<C::kNP>();
+            vr.template next<C::kNVR>();
+            if (so == soe) dv.template next<C::kND>();
         }
+        if (elect_one()) umma_commit(bar(ct.drained));             // nothing is in flight when the block ends
         __syncwarp();
+        mbar_wait_bounded(bar(ct.drained), 0, kTreeWaitNs);
+        }
     } else if (warp >= kConvW) {
         // ==== converters ====
+        if constexpr (C::kShift) regs_down<C::kRegsConv>();
         const int grp = (warp - kConvW) >> 2, ctid = tid - 256 - 128 * grp, cw = ctid >> 5;
         const bool do_k = grp == 0, do_v = C::kGroups == 1 || grp == 1;
         const uint32_t tlane = static_cast<uint32_t>(32 * cw) << 16;
@@ -803,6 +823,7 @@ tree_attn_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmK, co
         }
     } else {
         // ==== softmax ====
+        if constexpr (C::kShift) regs_up<C::kRegsSoft>();
         constexpr int kNC = C::kNC, kCh = kNC < 32 ? kNC : 32, kChunks = kNC / kCh;
         const int g = warp >> 2, wq = warp & 3, tok = tid & 127, col0 = g * kNC, barrier = 1 + g;
         const uint32_t tlane = static_cast<uint32_t>(32 * wq) << 16;
@@ -865,7 +886,7 @@ tree_attn_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmK, co
                     // ---- move the references of the columns that need it ----
                     if (i > u.tb) bad |= !wait(ct.pempty[last.i], last.ph);      // the sums so far are complete
                     umma_fence_after();
-                    constexpr int kSl = kNC < 16 ? kNC : 16;
+                    constexpr int kSl = 8;
 #pragma unroll
                     for (int c = 0; c < kNC; c += kSl) {
                         float y[kSl];
@@ -976,7 +997,7 @@ tree_attn_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmK, co
             bool anyodd = false;
             for (int k = 0; k < min(odd_tiles, kTreePoison); ++k)
                 for (int w = 0; w < 4; ++w) anyodd |= *const_cast<volatile uint32_t *>(&ct.poison[d.i][k][w]) != 0;
-            constexpr int kE = kNC < 16 ? kNC : 16;
+            constexpr int kE = 8;
 #pragma unroll
             for (int c = 0; c < kNC; c += kE) {
                 float y[kE];

@@ -66,10 +66,22 @@ __device__ __forceinline__ void tmem_store_wait() { asm volatile("tcgen05.wait::
 // chunk c ^ (r % 8).  K-major (a row holds 64 elements of K): `stride` from 8 rows to the
 // next 8, `lead` unused.  MN-major (a row holds 64 elements of M or N): `lead` to the next
 // 64 of them, `stride` from 8 K rows to the next 8.
-__device__ __forceinline__ uint64_t umma_desc(uint32_t addr, uint32_t lead, uint32_t stride) {
-    return static_cast<uint64_t>((addr >> 4) & 0x3FFFu) | (static_cast<uint64_t>(lead >> 4) << 16) |
-           (static_cast<uint64_t>(stride >> 4) << 32) | (1ull << 46) | (2ull << 61);
+// A descriptor's upper word is a constant, its lower one moves with the address by sixteenths
+// of bytes: one addition a product, on the issuing thread's critical path.
+__host__ __device__ constexpr uint32_t umma_desc_hi(uint32_t stride) { return (stride >> 4) | (1u << 14) | (2u << 29); }
+__device__ __forceinline__ uint32_t umma_desc_lo(uint32_t addr, uint32_t lead) { return ((addr >> 4) & 0x3FFFu) | ((lead >> 4) << 16); }
+__device__ __forceinline__ uint64_t umma_desc(uint32_t lo, uint32_t hi) { return (static_cast<uint64_t>(hi) << 32) | lo; }
+// One lane of the (converged) warp, always the same.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t r;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r) :: "memory");
+    return r != 0;
 }
+// Registers of the warps of a group of four: given back to, or taken from, the block's.
+template <int kN>
+__device__ __forceinline__ void regs_down() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kN)); }
+template <int kN>
+__device__ __forceinline__ void regs_up() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kN)); }
 // f16 (bf16: `bf16`) operands, fp32 accumulators; *_mn: that operand is MN-major.
 __host__ __device__ constexpr uint32_t umma_idesc(bool bf16, bool a_mn, bool b_mn, int m, int n) {
     return (1u << 4) | (bf16 ? (1u << 7) | (1u << 10) : 0u) | (a_mn ? 1u << 15 : 0u) | (b_mn ? 1u << 16 : 0u) |
