@@ -38,7 +38,7 @@ namespace fkv {
 constexpr int kTreeMaxWords = 4;               // 64-bit words of a row's mask
 constexpr int kTreeTok = 128;                  // tokens of a tile
 constexpr int kTreePoison = 10;                // tiles of a unit that hold tokens not seen by every row, at most (9)
-constexpr float kTreeTop = 13.f, kTreeMost = 15.9f;   // log2 of a moved reference's largest weight, and of any weight
+constexpr float kTreeTop = 10.f, kTreeMost = 15.9f;   // log2 of a moved reference's largest weight, and of any weight
 constexpr float kTreeNone = -3e38f;            // the reference of a column that has seen nothing
 constexpr uint64_t kTreeWaitNs = 2000000000ull;
 constexpr uint32_t kAll = 0xffffffffu;
@@ -138,28 +138,34 @@ struct TreeCfg {
     static constexpr bool kConv = kKv != FKV_KV_BF16;              // K and V become f16 here
     static constexpr int kRowB = kKv == FKV_KV_FP8_E4M3 ? 128 : kKv == FKV_KV_BF16 ? 256 : kFp4Row;
     static constexpr int kStageB = kTreeTok * kRowB;               // the K (or V) rows of a tile
+    // The softmax groups take turns, a tile each, with sums and references of their own; with
+    // 128 rows, whose sums fill the tensor memory once, each takes half of the rows of every tile.
+    static constexpr bool kTurns = kR <= 64;
     static constexpr int kNK = kConv && (kR <= 64 || kKv == FKV_KV_FP4) ? 3 : 2;
-    static constexpr int kNV = kConv ? (kR <= 32 ? 4 : 3) : kR <= 64 ? 3 : 2;
-    static constexpr int kNP = kConv && kR <= 64 ? 2 : 1;          // weight buffers
+    static constexpr int kNV = kConv ? (kR <= 32 ? 4 : 3) : kR <= 32 ? 3 : 2;
+    static constexpr int kNP = kTurns ? 2 : 1;                     // weight buffers
     static constexpr int kParts = kConv ? 1 : 2;                   // words of a weight
     static constexpr int kHalves = kR > 64 ? 2 : 1;                // 64-column halves of a weight buffer
-    static constexpr int kPB = 16384 * kHalves;
+    static constexpr int kPW = kR <= 32 ? 64 : 16384 * kHalves;    // from a weight's first word to its second
+    static constexpr int kPB = kR <= 32 ? 16384 : kParts * kPW;    // a weight buffer
     static constexpr int kQB = kR * 256;
     static constexpr int kV16 = kConv ? 32768 : 0;
-    static constexpr int kGroups = kR <= 64 ? 2 : 1;               // converter groups: K and V, or one for both
+    static constexpr int kGroups = kConv && kR <= 32 ? 2 : 1;      // converter groups: K and V, or one for both
     // Softmax warps with many columns take registers of the others: of a thread, at launch, then
     // of the three kinds of warps (no more in all than at launch; whole groups of four warps).
-    static constexpr bool kShift = kR > 32;
-    static constexpr int kThreads = 256 + 128 * kGroups + (kShift ? 128 : 64);     // softmax, converters, producer and issuer
+    static constexpr bool kShift = kR >= 64 || kGroups * kR == 64;
+    static constexpr int kThreads = 256 + 128 * kGroups + 128;     // softmax, converters; producer, two issuers, an idle warp
     static constexpr int kRegs = kGroups == 2 ? 96 : 128;
-    static constexpr int kRegsSoft = kGroups == 2 ? 128 : 176, kRegsConv = kGroups == 2 ? 80 : 88, kRegsRest = kGroups == 2 ? 64 : 72;
+    static constexpr int kRegsSoft = kGroups == 2 ? 112 : 168, kRegsConv = kGroups == 2 ? 80 : 96, kRegsRest = kGroups == 2 ? 80 : 80;
     static_assert(2 * kRegsSoft + kGroups * kRegsConv + kRegsRest <= (2 + kGroups + 1) * kRegs, "the block's registers");
     static constexpr int kND = kR <= 64 ? 4 : 2;                   // units in flight
-    static constexpr int kNC = kR / 2;                             // columns of a softmax group
-    // tensor memory columns: K f16 (two buffers), S (two), O
+    static constexpr int kNC = kTurns ? kR : kR / 2;               // columns of a softmax thread
+    static constexpr int kNS = kTurns ? 4 : 8;                     // softmax warps of a tile
+    // tensor memory columns: K f16 (two buffers), S (two), O (one per group that takes turns)
     static constexpr int kTmS = kConv ? 128 : 0, kTmO = kTmS + 2 * kR;
+    static_assert(kTmO + (kTurns ? 2 : 1) * kR <= 512, "tensor memory");
     static constexpr int kNVR = kConv ? 2 : kNV;                   // buffers between converters and issuer
-    static constexpr int kOffP = kQB, kOffV16 = kOffP + kNP * kParts * kPB, kOffK = kOffV16 + 2 * kV16;
+    static constexpr int kOffP = kQB, kOffV16 = kOffP + kNP * kPB, kOffK = kOffV16 + 2 * kV16;
     static constexpr int kOffV = kOffK + kNK * kStageB, kOffCtrl = kOffV + kNV * kStageB;
 };
 
@@ -169,13 +175,17 @@ struct TreeCtrl {
     uint64_t kfull[C::kNK], kempty[C::kNK], vfull[C::kNV], vempty[C::kNV];
     uint64_t k16full[2], k16empty[2], vready[C::kNVR], v16empty[2];
     uint64_t sfull[2], sempty[2], pfull[C::kNP], pempty[C::kNP];
-    uint64_t qfull, qempty, oempty, drained;
+    uint64_t qfull, qempty, oempty, drained[2];
     uint64_t dfull[C::kND], dempty[C::kND], cfull[C::kND];
     TreeUnit unit[C::kND];
     alignas(16) float colscale[C::kND][kR];                        // a logit in log2 units per unit of S
-    alignas(16) float ref[kR];                                     // the columns' references, negated
-    int32_t redmax[2][4][8];
-    float lsum[kR <= 64 ? 2 * 4 * C::kNC : 1];                     // (kR = 128: in the weights' buffer)
+    // [unit's parity][group] where the groups take turns: the columns' references, negated, and
+    // their warps' sums (or maxima); a moved reference's factor; the factors of the two groups' sums
+    static constexpr int kU = C::kTurns ? 2 : 1;
+    alignas(16) float ref[kU][kU][kR];
+    alignas(16) float red[kU][2][4][C::kTurns ? kR : 8];
+    alignas(16) float up[2][C::kTurns ? kR : 4];
+    alignas(16) float2 part[C::kTurns ? kR : 2];
     uint32_t poison[C::kND][kTreePoison][4];                       // tokens whose V holds NaN or infinities
     int64_t scan[20];                                             // one per warp
     int64_t total, off0;
@@ -188,7 +198,7 @@ template <int kKv, int kR>
 constexpr int tree_smem() {
     using C = TreeCfg<kKv, kR>;
     using T = TreeCtrl<kKv, kR>;
-    static_assert(offsetof(T, colscale) % 16 == 0 && offsetof(T, ref) % 16 == 0 && C::kOffCtrl % 16 == 0, "read four at a time");
+    static_assert(offsetof(T, colscale) % 16 == 0 && offsetof(T, ref) % 16 == 0 && offsetof(T, up) % 16 == 0 && offsetof(T, part) % 16 == 0 && C::kOffCtrl % 16 == 0, "read four at a time");
     static_assert(C::kOffP % 1024 == 0 && C::kOffV16 % 1024 == 0 && C::kOffK % 1024 == 0 && C::kOffV % 1024 == 0,
                   "swizzled buffers start on 1024 bytes");
     return TreeCfg<kKv, kR>::kOffCtrl + static_cast<int>((sizeof(TreeCtrl<kKv, kR>) + 15) / 16 * 16);
@@ -230,6 +240,12 @@ __device__ __forceinline__ bool group_any(int id, bool x) {
     uint32_t r;
     asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\tbarrier.cta.red.or.pred q, %2, 128, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
                  : "=r"(r) : "r"(x ? 1u : 0u), "r"(id) : "memory");
+    return r != 0;
+}
+__device__ __forceinline__ bool both_any(bool x) {             // the same for both groups
+    uint32_t r;
+    asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\tbarrier.cta.red.or.pred q, 3, 256, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+                 : "=r"(r) : "r"(x ? 1u : 0u) : "memory");
     return r != 0;
 }
 __device__ __forceinline__ void group_sync(int id) { asm volatile("barrier.cta.sync %0, 128;" ::"r"(id) : "memory"); }
@@ -391,23 +407,22 @@ __device__ __forceinline__ float odd_value(const TreeParams &p, const TreeUnit &
     return isfinite(v) ? 0.f : v;
 }
 
-// Sums over a warp's lanes of kN columns: half of them go to the lane kO away, then half of
+// kN columns reduced over a warp's lanes: half of them go to the lane kO away, then half of
 // those that are left, and so on; at the end a lane has kN / 32 columns (at least one).
-template <int kN, int kO, int kSize>
-__device__ __forceinline__ void spread_sums(float (&v)[kSize], int lane) {
+template <int kN, int kO, int kSize, typename Op>
+__device__ __forceinline__ void spread(float (&v)[kSize], int lane, Op op) {
     if constexpr (kO > 0) {
         constexpr int n = kN > 1 ? kN / 2 : 1;
         if constexpr (kN > 1) {
 #pragma unroll
             for (int j = 0; j < n; ++j) {
                 const float a = v[j], b = v[j + n];
-                const float got = __shfl_xor_sync(kAll, lane & kO ? a : b, kO);
-                v[j] = (lane & kO ? b : a) + got;
+                v[j] = op(lane & kO ? b : a, __shfl_xor_sync(kAll, lane & kO ? a : b, kO));
             }
         } else {
-            v[0] += __shfl_xor_sync(kAll, v[0], kO);
+            v[0] = op(v[0], __shfl_xor_sync(kAll, v[0], kO));
         }
-        spread_sums<n, kO / 2>(v, lane);
+        spread<n, kO / 2>(v, lane, op);
     }
 }
 
@@ -424,7 +439,7 @@ tree_attn_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmK, co
     const uint32_t base = smem_u32(smem);
     const uint32_t sQ = base, sP = base + C::kOffP, sV16 = base + C::kOffV16, sK = base + C::kOffK, sV = base + C::kOffV;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    constexpr int kConvW = 8, kProdW = 8 + 4 * C::kGroups, kMmaW = kProdW + 1;
+    constexpr int kConvW = 8, kProdW = 8 + 4 * C::kGroups, kMmaW = kProdW + 1, kMmaW2 = kProdW + 2;
     volatile int32_t *dead = &ct.dead;
     auto bar = [&](uint64_t &b) { return smem_u32(&b); };
     auto wait = [&](uint64_t &b, uint32_t parity) { return tree_wait(smem_u32(&b), parity, dead, p.err); };
@@ -435,13 +450,13 @@ tree_attn_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmK, co
         for (int i = 0; i < C::kNV; ++i) mbar_init(bar(ct.vfull[i]), 1), mbar_init(bar(ct.vempty[i]), kKC);
         for (int i = 0; i < 2; ++i) {
             mbar_init(bar(ct.k16full[i]), 4), mbar_init(bar(ct.k16empty[i]), 1), mbar_init(bar(ct.v16empty[i]), 1);
-            mbar_init(bar(ct.sfull[i]), 1), mbar_init(bar(ct.sempty[i]), 8);
+            mbar_init(bar(ct.sfull[i]), 1), mbar_init(bar(ct.sempty[i]), C::kNS);
         }
         for (int i = 0; i < C::kNVR; ++i) mbar_init(bar(ct.vready[i]), 4);
-        for (int i = 0; i < C::kNP; ++i) mbar_init(bar(ct.pfull[i]), 8), mbar_init(bar(ct.pempty[i]), 1);
-        mbar_init(bar(ct.qfull), 4), mbar_init(bar(ct.qempty), 1), mbar_init(bar(ct.oempty), 8), mbar_init(bar(ct.drained), 1);
+        for (int i = 0; i < C::kNP; ++i) mbar_init(bar(ct.pfull[i]), C::kNS), mbar_init(bar(ct.pempty[i]), 1);
+        mbar_init(bar(ct.qfull), 4), mbar_init(bar(ct.qempty), 1), mbar_init(bar(ct.oempty), 8), mbar_init(bar(ct.drained[0]), 1), mbar_init(bar(ct.drained[1]), 1);
         for (int i = 0; i < C::kND; ++i)
-            mbar_init(bar(ct.dfull[i]), 1), mbar_init(bar(ct.dempty[i]), 8 + 4 * C::kGroups + 1), mbar_init(bar(ct.cfull[i]), 4);
+            mbar_init(bar(ct.dfull[i]), 1), mbar_init(bar(ct.dempty[i]), 8 + 4 * C::kGroups + 2), mbar_init(bar(ct.cfull[i]), 4);
         ct.dead = 0;
         ct.r0 = p.batch;
         fence_mbar_init();
@@ -604,90 +619,88 @@ tree_attn_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmK, co
             const uint64_t t0 = globaltimer_ns();
             while (globaltimer_ns() - t0 < 200000000ull) __nanosleep(1000);
         }
-        } else if (warp == kMmaW) {
-        // ==== issuer ====
-        // The whole warp waits, one lane issues: products and commits come from the same thread.
+        } else if (warp == kMmaW || warp == kMmaW2) {
+        // ==== issuers: S = K Q^T, and O += V^T P^T ====
+        // A whole warp waits, one lane issues: products and commits come from the same thread.
         constexpr bool kB16 = !C::kConv;
-        constexpr uint32_t idS = umma_idesc(kB16, false, false, 128, kR), idO = umma_idesc(kB16, true, true, 128, kR);
         constexpr uint32_t kHi = umma_desc_hi(1024);
-        const uint32_t lQ = umma_desc_lo(sQ, 16), lK = umma_desc_lo(sK, 16), lP = umma_desc_lo(sP, 16384),
-                       lV = umma_desc_lo(C::kConv ? sV16 : sV, 16384);
-        constexpr uint32_t kVStep = (C::kConv ? C::kV16 : C::kStageB) / 16;
-        Ring dq, dv, kr, s, vr, pr;                                // units of S and of O, K buffers, S, V buffers, weights
-        int sq = 0, sqe = 0, so = 0, soe = 0;                      // tiles left to do: next and end
-        uint32_t nq = 0, no = 0;                                   // units begun
-        bool ok = true, more = true;
-        auto step_s = [&]() {                                      // S of the next tile, if there is one
-            if (!more || !ok) return;
-            if (sq == sqe) {
-                if (!(ok = wait(ct.dfull[dq.i], dq.ph))) return;
-                sq = *const_cast<volatile int32_t *>(&ct.unit[dq.i].tb);
-                sqe = *const_cast<volatile int32_t *>(&ct.unit[dq.i].te);
-                if (sqe < 0) {
-                    more = false;
-                    return;
-                }
-                dq.template next<C::kND>();
-                if (!(ok = wait(ct.qfull, nq & 1))) return;
-                ++nq;
-            }
-            if (!(ok = wait(kB16 ? ct.kfull[kr.i] : ct.k16full[kr.i], kr.ph) && wait(ct.sempty[s.i], s.ph ^ 1))) return;
-            umma_fence_after();
-            const uint32_t dst = tmem + C::kTmS + s.i * kR, ta = tmem + kr.i * 64, la = lK + kr.i * (C::kStageB / 16);
-            ++sq;
-            __syncwarp();
-            if (elect_one()) {
+        Ring d;
+        bool ok = true;
+        if (warp == kMmaW) {
+            constexpr uint32_t id = umma_idesc(kB16, false, false, 128, kR);
+            const uint32_t lQ = umma_desc_lo(sQ, 16), lK = umma_desc_lo(sK, 16);
+            Ring k, sb;
+            for (uint32_t units = 0; ok; ++units) {
+                if (!(ok = wait(ct.dfull[d.i], d.ph))) break;
+                const int tb = *const_cast<volatile int32_t *>(&ct.unit[d.i].tb), te = *const_cast<volatile int32_t *>(&ct.unit[d.i].te);
+                if (te < 0) break;
+                __syncwarp();
+                if (elect_one()) mbar_arrive(bar(ct.dempty[d.i]));
+                d.template next<C::kND>();
+                if (!(ok = wait(ct.qfull, units & 1))) break;
+                for (int i = tb; i < te; ++i) {
+                    if (!(ok = wait(kB16 ? ct.kfull[k.i] : ct.k16full[k.i], k.ph) && wait(ct.sempty[sb.i], sb.ph ^ 1))) break;
+                    umma_fence_after();
+                    const uint32_t dst = tmem + C::kTmS + sb.i * kR, ta = tmem + k.i * 64, la = lK + k.i * (C::kStageB / 16);
+                    __syncwarp();
+                    if (elect_one()) {
 #pragma unroll
-                for (int kk = 0; kk < 8; ++kk) {
-                    const uint64_t b = umma_desc(lQ + (kk >> 2) * (kR * 8) + (kk & 3) * 2, kHi);
-                    if (kB16) umma_ss(dst, umma_desc(la + (kk >> 2) * 1024 + (kk & 3) * 2, kHi), b, idS, kk > 0);
-                    else umma_ts(dst, ta + kk * 8, b, idS, kk > 0);
+                        for (int kk = 0; kk < 8; ++kk) {
+                            const uint64_t b = umma_desc(lQ + (kk >> 2) * (kR * 8) + (kk & 3) * 2, kHi);
+                            if (kB16) umma_ss(dst, umma_desc(la + (kk >> 2) * 1024 + (kk & 3) * 2, kHi), b, id, kk > 0);
+                            else umma_ts(dst, ta + kk * 8, b, id, kk > 0);
+                        }
+                        umma_commit(bar(ct.sfull[sb.i]));
+                        umma_commit(bar(kB16 ? ct.kempty[k.i] : ct.k16empty[k.i]));
+                        if (i + 1 == te) umma_commit(bar(ct.qempty));
+                    }
+                    __syncwarp();
+                    k.template next<kB16 ? C::kNK : 2>();
+                    sb.template next<2>();
                 }
-                umma_commit(bar(ct.sfull[s.i]));
-                umma_commit(bar(kB16 ? ct.kempty[kr.i] : ct.k16empty[kr.i]));
-                if (sq == sqe) umma_commit(bar(ct.qempty));
             }
-            __syncwarp();
-            kr.template next<kB16 ? C::kNK : 2>();
-            s.template next<2>();
-        };
-        step_s();
-        while (ok) {
-            step_s();
-            if (!ok) break;
-            const bool first = so == soe;                          // of a unit: it starts its sums anew
-            if (first) {
-                if (dv.i == dq.i && dv.ph == dq.ph) break;         // no unit left
-                so = *const_cast<volatile int32_t *>(&ct.unit[dv.i].tb);
-                soe = *const_cast<volatile int32_t *>(&ct.unit[dv.i].te);
-                if (no && !(ok = wait(ct.oempty, (no - 1) & 1))) break;
-                ++no;
-            }
-            if (!(ok = wait(ct.vready[vr.i], vr.ph) && wait(ct.pfull[pr.i], pr.ph))) break;
-            umma_fence_after();
-            const uint32_t lv = lV + vr.i * kVStep, lp = lP + pr.i * (C::kParts * C::kPB / 16);
-            ++so;
-            __syncwarp();
-            if (elect_one()) {
+        } else {
+            constexpr uint32_t id = umma_idesc(kB16, true, true, 128, kR);
+            const uint32_t lP = umma_desc_lo(sP, 16384), lV = umma_desc_lo(C::kConv ? sV16 : sV, 16384);
+            constexpr uint32_t kVStep = (C::kConv ? C::kV16 : C::kStageB) / 16;
+            Ring v, pb;
+            for (uint32_t units = 0; ok; ++units) {
+                if (!(ok = wait(ct.dfull[d.i], d.ph))) break;
+                const int tb = *const_cast<volatile int32_t *>(&ct.unit[d.i].tb), te = *const_cast<volatile int32_t *>(&ct.unit[d.i].te);
+                if (te < 0) break;
+                __syncwarp();
+                if (elect_one()) mbar_arrive(bar(ct.dempty[d.i]));
+                d.template next<C::kND>();
+                if (units && !(ok = wait(ct.oempty, (units - 1) & 1))) break;
+                for (int i = tb; i < te; ++i) {
+                    if (!(ok = wait(ct.vready[v.i], v.ph) && wait(ct.pfull[pb.i], pb.ph))) break;
+                    umma_fence_after();
+                    const uint32_t lv = lV + v.i * kVStep, lp = lP + pb.i * (C::kPB / 16);
+                    const uint32_t dst = tmem + C::kTmO + (C::kTurns ? pb.i * kR : 0);
+                    const bool first = i < tb + (C::kTurns ? 2 : 1);       // of a unit and a group: its sums start anew
+                    __syncwarp();
+                    if (elect_one()) {
 #pragma unroll
-                for (int w = 0; w < C::kParts; ++w) {
+                        for (int w = 0; w < C::kParts; ++w) {
 #pragma unroll
-                    for (int kk = 0; kk < 8; ++kk)
-                        umma_ss(tmem + C::kTmO, umma_desc(lv + kk * 128, kHi), umma_desc(lp + w * (C::kPB / 16) + kk * 128, kHi), idO,
-                                !first || w > 0 || kk > 0);
+                            for (int kk = 0; kk < 8; ++kk)
+                                umma_ss(dst, umma_desc(lv + kk * 128, kHi), umma_desc(lp + w * (C::kPW / 16) + kk * 128, kHi), id,
+                                        !first || w > 0 || kk > 0);
+                        }
+                        umma_commit(bar(ct.pempty[pb.i]));
+                        umma_commit(bar(C::kConv ? ct.v16empty[v.i & 1] : ct.vempty[v.i]));
+                    }
+                    __syncwarp();
+                    pb.template next<C::kNP>();
+                    v.template next<C::kNVR>();
                 }
-                umma_commit(bar(ct.pempty[pr.i]));
-                umma_commit(bar(C::kConv ? ct.v16empty[vr.i & 1] : ct.vempty[vr.i]));
-                if (so == soe) mbar_arrive(bar(ct.dempty[dv.i]));
             }
-            __syncwarp();
-            pr.template next<C::kNP>();
-            vr.template next<C::kNVR>();
-            if (so == soe) dv.template next<C::kND>();
         }
-        if (elect_one()) umma_commit(bar(ct.drained));             // nothing is in flight when the block ends
+        uint64_t &drained = ct.drained[warp - kMmaW];              // nothing is in flight when the block ends
         __syncwarp();
-        mbar_wait_bounded(bar(ct.drained), 0, kTreeWaitNs);
+        if (elect_one()) umma_commit(bar(drained));
+        __syncwarp();
+        mbar_wait_bounded(bar(drained), 0, kTreeWaitNs);
         }
     } else if (warp >= kConvW) {
         // ==== converters ====
@@ -824,36 +837,55 @@ tree_attn_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmK, co
     } else {
         // ==== softmax ====
         if constexpr (C::kShift) regs_up<C::kRegsSoft>();
+        constexpr bool kTurns = C::kTurns;
         constexpr int kNC = C::kNC, kCh = kNC < 32 ? kNC : 32, kChunks = kNC / kCh;
-        const int g = warp >> 2, wq = warp & 3, tok = tid & 127, col0 = g * kNC, barrier = 1 + g;
+        const int g = warp >> 2, wq = warp & 3, tok = tid & 127, barrier = 1 + g;
+        const int col0 = kTurns ? 0 : g * kNC;                     // this thread's columns begin here
         const uint32_t tlane = static_cast<uint32_t>(32 * wq) << 16;
-        const uint32_t sref = smem_u32(ct.ref) + 4 * col0;
-        Ring d, s, pr, last;                                       // units, S buffers, weight buffers; the last one handed over
+        const uint32_t tO = tmem + tlane + C::kTmO;
+        const uint32_t sPw = sP + (kTurns ? g * C::kPB : 0) + (col0 >> 6) * 16384 + tok * 128;
+        Ring d;
+        int sb = kTurns ? g : 0;                                   // S buffer, and the rounds of it and of the weights' buffer
+        uint32_t sph = 0, pph = 0, turn = 0, par = 0;              // (turn: whose the next tile is; par: the unit's parity)
         bool bad = false;                                          // this thread's waits
         float sum[kNC];
         while (true) {
             bad |= !wait(ct.dfull[d.i], d.ph);
-            if (group_any(barrier, bad)) break;
+            if (kTurns ? both_any(bad) : group_any(barrier, bad)) break;
             const TreeUnit u = ct.unit[d.i];
             if (u.te < 0) break;
-            if (tok < kNC) ct.ref[col0 + tok] = -kTreeNone;
+            float *const refs = kTurns ? ct.ref[par % Ctrl::kU][g % Ctrl::kU] : ct.ref[0][0];
+            const uint32_t sref = smem_u32(refs) + 4 * col0;
+            if (tok < kNC) refs[col0 + tok] = -kTreeNone;
 #pragma unroll
             for (int j = 0; j < kNC; ++j) sum[j] = 0.f;
             bad |= !wait(ct.cfull[d.i], d.ph);
             group_sync(barrier);
             const uint32_t scs = smem_u32(ct.colscale[d.i]) + 4 * col0;
-            int odd_tiles = 0;
-            bool quit = false;
-            for (int i = u.tb; i < u.te; ++i) {
+            bool quit = false, had = false;                        // had: a tile of this unit
+            for (int i = kTurns ? u.tb + static_cast<int>((g ^ turn) & 1) : u.tb; i < u.te; i += kTurns ? 2 : 1) {
                 const uint32_t t0 = tile_at(u, i);
                 const bool whole = tile_whole(u, p, t0);
                 const uint64_t see = whole ? ~0ull : seen_by<kNC>(p, u, col0, t0 + tok);
-                odd_tiles += whole ? 0 : 1;
-                bad |= !wait(ct.sfull[s.i], s.ph);
+                bad |= !wait(ct.sfull[sb], sph);
                 umma_fence_after();
-                const uint32_t ts = tmem + tlane + C::kTmS + s.i * kR + col0;
+                const uint32_t ts = tmem + tlane + C::kTmS + sb * kR + col0;
                 float x[kCh];
-                // the exponents of kCh columns, relative to their references; unseen ones -infinity
+                // kCh columns' logits in log2 units; less their references, unseen ones -infinity
+                auto logits = [&](int ch) {
+                    tmem_load(ts + ch * kCh, x);
+#pragma unroll
+                    for (int j = 0; j < kCh; j += 4) {
+                        const float4 c4 = ld_shared_f4(scs + 4 * (ch * kCh + j));
+                        const float2 a = unpack2(mul2(pack2(x[j], x[j + 1]), pack2(c4.x, c4.y))), b = unpack2(mul2(pack2(x[j + 2], x[j + 3]), pack2(c4.z, c4.w)));
+                        x[j] = a.x, x[j + 1] = a.y, x[j + 2] = b.x, x[j + 3] = b.y;
+                    }
+                    if (!whole) {
+#pragma unroll
+                        for (int j = 0; j < kCh; ++j)
+                            if (!((see >> (ch * kCh + j)) & 1)) x[j] = -INFINITY;
+                    }
+                };
                 auto exponents = [&](int ch) {
                     tmem_load(ts + ch * kCh, x);
 #pragma unroll
@@ -875,8 +907,10 @@ tree_attn_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmK, co
 #pragma unroll
                 for (int ch = kChunks - 1; ch >= 0; --ch) {
                     exponents(ch);
+                    float m4[4] = {x[0], x[1], x[2], x[3]};
 #pragma unroll
-                    for (int j = 0; j < kCh; ++j) most = fmaxf(most, x[j]);
+                    for (int j = 4; j < kCh; ++j) m4[j & 3] = fmaxf(m4[j & 3], x[j]);
+                    most = fmaxf(most, fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])));
                 }
                 if (group_any(barrier, most > kTreeMost || bad)) {
                     if (group_any(barrier, bad)) {
@@ -884,71 +918,121 @@ tree_attn_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmK, co
                         break;
                     }
                     // ---- move the references of the columns that need it ----
-                    if (i > u.tb) bad |= !wait(ct.pempty[last.i], last.ph);      // the sums so far are complete
+                    const int buf = kTurns ? g : 0;
+                    if (had) bad |= !wait(ct.pempty[buf], pph ^ 1);              // the sums so far are complete
                     umma_fence_after();
-                    constexpr int kSl = 8;
+                    if constexpr (kTurns) {
+                        float(*const red)[kR] = ct.red[par % Ctrl::kU][g];
 #pragma unroll
-                    for (int c = 0; c < kNC; c += kSl) {
-                        float y[kSl];
-                        tmem_load(ts + c, y);
-#pragma unroll
-                        for (int j = 0; j < kSl; ++j) {
-                            float z = __fmul_rn(y[j], *reinterpret_cast<const float *>(&ct.colscale[d.i][col0 + c + j]));
-                            if (!((see >> (c + j)) & 1)) z = -INFINITY;
-                            const int key = __float_as_int(z) ^ ((__float_as_int(z) >> 31) & 0x7FFFFFFF);   // ordered as the floats
-                            const int top = __reduce_max_sync(kAll, key);
-                            if (lane == 0) ct.redmax[g][wq][j] = top;
+                        for (int ch = 0; ch < kChunks; ++ch) {
+                            logits(ch);
+                            spread<kCh, 16>(x, lane, [](float a, float b) { return fmaxf(a, b); });
+                            constexpr int kSpan = 32 / kCh;
+                            if (lane % kSpan == 0) red[wq][ch * kCh + lane / kSpan] = x[0];
                         }
                         group_sync(barrier);
-                        float up[kSl], ref[kSl];
-                        bool any = false;
-#pragma unroll
-                        for (int j = 0; j < kSl; ++j) {
-                            const int key = max(max(ct.redmax[g][0][j], ct.redmax[g][1][j]), max(ct.redmax[g][2][j], ct.redmax[g][3][j]));
-                            const float z = __int_as_float(key ^ ((key >> 31) & 0x7FFFFFFF)), was = -ct.ref[col0 + c + j];
-                            const bool move = z - was > kTreeMost;
-                            ref[j] = move ? z - kTreeTop : was;
-                            up[j] = move ? ex2(was - ref[j]) : 1.f;
-                            any |= move;
-                            sum[c + j] *= up[j];
+                        bool move = false;
+                        if (tok < kNC) {
+                            const float z = fmaxf(fmaxf(red[0][tok], red[1][tok]), fmaxf(red[2][tok], red[3][tok])), was = -refs[tok];
+                            move = z - was > kTreeMost;
+                            const float ref = move ? z - kTreeTop : was;
+                            refs[tok] = -ref;
+                            ct.up[g][tok] = move ? ex2(was - ref) : 1.f;
                         }
-                        group_sync(barrier);                       // the old references are read
-                        if (tok < kSl) {
+                        const bool any = group_any(barrier, move);
+                        const uint32_t sup = smem_u32(ct.up[g]);
+                        if (any && had) {
 #pragma unroll
-                            for (int j = 0; j < kSl; ++j)
-                                if (tok == j) ct.ref[col0 + c + j] = -ref[j];
-                        }
-                        if (any && i > u.tb) {
-                            const uint32_t to = tmem + tlane + C::kTmO + col0 + c;
-                            tmem_load(to, y);
-                            uint32_t o[8];
+                            for (int j = 0; j < kNC; j += 4) {
+                                const float4 f = ld_shared_f4(sup + 4 * j);
+                                sum[j] *= f.x, sum[j + 1] *= f.y, sum[j + 2] *= f.z, sum[j + 3] *= f.w;
+                            }
 #pragma unroll
-                            for (int b = 0; b < kSl; b += 8) {
+                            for (int c = 0; c < kNC; c += 8) {
+                                float y[8];
+                                uint32_t o[8];
+                                tmem_load(tO + g * kR + c, y);
 #pragma unroll
-                                for (int j = 0; j < 8; ++j) o[j] = __float_as_uint(y[b + j] * up[b + j]);
-                                tmem_store(to + b, o);
+                                for (int j = 0; j < 8; j += 4) {
+                                    const float4 f = ld_shared_f4(sup + 4 * (c + j));
+                                    o[j] = __float_as_uint(y[j] * f.x), o[j + 1] = __float_as_uint(y[j + 1] * f.y);
+                                    o[j + 2] = __float_as_uint(y[j + 2] * f.z), o[j + 3] = __float_as_uint(y[j + 3] * f.w);
+                                }
+                                tmem_store(tO + g * kR + c, o);
                             }
                             tmem_store_wait();
+                            umma_fence_before();
                         }
+                    } else {
+                        float(*const red)[8] = ct.red[0][g];
+#pragma unroll
+                        for (int c = 0; c < kNC; c += 8) {
+                            float y[8];
+                            tmem_load(ts + c, y);
+#pragma unroll
+                            for (int j = 0; j < 8; ++j) {
+                                float z = __fmul_rn(y[j], ct.colscale[d.i][col0 + c + j]);
+                                if (!((see >> (c + j)) & 1)) z = -INFINITY;
+                                const int key = __float_as_int(z) ^ ((__float_as_int(z) >> 31) & 0x7FFFFFFF);   // ordered as the floats
+                                const int top = __reduce_max_sync(kAll, key);
+                                if (lane == 0) red[wq][j] = __int_as_float(top ^ ((top >> 31) & 0x7FFFFFFF));
+                            }
+                            group_sync(barrier);
+                            float up[8], ref[8];
+                            bool any = false;
+#pragma unroll
+                            for (int j = 0; j < 8; ++j) {
+                                const float z = fmaxf(fmaxf(red[0][j], red[1][j]), fmaxf(red[2][j], red[3][j])), was = -refs[col0 + c + j];
+                                const bool move = z - was > kTreeMost;
+                                ref[j] = move ? z - kTreeTop : was;
+                                up[j] = move ? ex2(was - ref[j]) : 1.f;
+                                any |= move;
+                                sum[c + j] *= up[j];
+                            }
+                            group_sync(barrier);                   // the old references and the maxima are read
+#pragma unroll
+                            for (int j = 0; j < 8; ++j)
+                                if (tok == j) refs[col0 + c + j] = -ref[j];
+                            if (any && had) {
+                                uint32_t o[8];
+                                tmem_load(tO + col0 + c, y);
+#pragma unroll
+                                for (int j = 0; j < 8; ++j) o[j] = __float_as_uint(y[j] * up[j]);
+                                tmem_store(tO + col0 + c, o);
+                                tmem_store_wait();
+                            }
+                        }
+                        umma_fence_before();
+                        group_sync(barrier);                       // the new references are there
                     }
-                    umma_fence_before();
-                    group_sync(barrier);                           // the new references are there
                     exponents(0);
                 }
                 // ---- weights ----
-                bad |= !wait(ct.pempty[pr.i], pr.ph ^ 1);
+                if (kChunks == 1) {                                // S is read
+                    umma_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(bar(ct.sempty[sb]));
+                }
+                bad |= !wait(ct.pempty[kTurns ? g : 0], pph ^ 1);
 #pragma unroll
                 for (int ch = 0; ch < kChunks; ++ch) {
-                    if (ch > 0) exponents(ch);                     // (chunk 0 was the last of the first pass)
+                    if (ch > 0) {                                  // (chunk 0 was the last of the first pass)
+                        exponents(ch);
+                        umma_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(bar(ct.sempty[sb]));
+                    }
 #pragma unroll
-                    for (int j = 0; j < kCh; ++j) {
+                    for (int j = 0; j < kCh; j += 2) {
                         x[j] = ex2(x[j]);
-                        sum[ch * kCh + j] += x[j];
+                        x[j + 1] = ex2(x[j + 1]);
+                        const float2 t = unpack2(add2(pack2(sum[ch * kCh + j], sum[ch * kCh + j + 1]), pack2(x[j], x[j + 1])));
+                        sum[ch * kCh + j] = t.x;
+                        sum[ch * kCh + j + 1] = t.y;
                     }
 #pragma unroll
                     for (int j = 0; j < kCh; j += 8) {
-                        const int col = col0 + ch * kCh + j;
-                        const uint32_t at = sP + pr.i * C::kParts * C::kPB + (col >> 6) * 16384 + tok * 128 + ((((col & 63) >> 3) ^ (tok & 7)) << 4);
+                        const uint32_t at = sPw + (((ch * kCh + j) >> 3) ^ (tok & 7)) * 16;
                         if (C::kConv) {
                             st_shared_v4(at, make_uint4(pack_f16x2(x[j], x[j + 1]), pack_f16x2(x[j + 2], x[j + 3]),
                                                         pack_f16x2(x[j + 4], x[j + 5]), pack_f16x2(x[j + 6], x[j + 7])));
@@ -962,47 +1046,88 @@ tree_attn_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmK, co
                                 lo[b] = pack_bf16x2(e - __uint_as_float(hi[b] << 16), f - __uint_as_float(hi[b] & 0xFFFF0000u));
                             }
                             st_shared_v4(at, make_uint4(hi[0], hi[1], hi[2], hi[3]));
-                            st_shared_v4(at + C::kPB, make_uint4(lo[0], lo[1], lo[2], lo[3]));
+                            st_shared_v4(C::kPW < 128 ? sPw + ((((ch * kCh + j) >> 3) + C::kPW / 16) ^ (tok & 7)) * 16 : at + C::kPW,
+                                         make_uint4(lo[0], lo[1], lo[2], lo[3]));
                         }
                     }
                 }
-                umma_fence_before();
                 fence_proxy_async_smem();
                 __syncwarp();
-                if (lane == 0) {
-                    mbar_arrive(bar(ct.sempty[s.i]));
-                    mbar_arrive(bar(ct.pfull[pr.i]));
-                }
-                last = pr;
-                pr.template next<C::kNP>();
-                s.template next<2>();
+                if (lane == 0) mbar_arrive(bar(ct.pfull[kTurns ? g : 0]));
+                had = true;
+                pph ^= 1;
+                if (kTurns) sph ^= 1;
+                else if ((sb ^= 1) == 0) sph ^= 1;
             }
-            if (quit) break;
+            if (quit && !kTurns) break;                            // (groups that take turns leave together, below)
+            turn += u.te - u.tb;
             // ---- end of this CTA's part of the unit ----
-            // sums over the tokens: halves of the columns go to the other lanes, step by step
-            spread_sums<kNC, 16>(sum, lane);
-            bad |= !wait(ct.pempty[last.i], last.ph);              // all products are done, the weights' buffers free
-            if (group_any(barrier, bad)) break;
-            umma_fence_after();
-            float *ls = kR <= 64 ? ct.lsum + g * 4 * kNC : reinterpret_cast<float *>(smem + C::kOffP + 16384 * g);
-            constexpr int kPer = kNC >= 32 ? kNC / 32 : 1, kSpan = kNC >= 32 ? 1 : 32 / kNC;   // columns a lane has; lanes with the same
+            // sums over the tokens; the groups' sums joined; a group writes half of the columns
+            constexpr int kHalf = kR / 2, kPer = kNC >= 32 ? kNC / 32 : 1, kSpan = kNC >= 32 ? 1 : 32 / kNC;
+            spread<kNC, 16>(sum, lane, [](float a, float b) { return a + b; });
+            if (had) bad |= !wait(ct.pempty[kTurns ? g : 0], pph ^ 1);     // all products are done, the weights' buffer is free
+            float *const ls = kTurns ? &ct.red[par % Ctrl::kU][g][0][0] : reinterpret_cast<float *>(smem + C::kOffP + 16384 * g);
             if (lane % kSpan == 0) {
 #pragma unroll
                 for (int j = 0; j < kPer; ++j) ls[wq * kNC + (lane / kSpan) * kPer + j] = sum[j];
             }
+            if (kTurns ? both_any(bad) : group_any(barrier, bad)) break;
+            umma_fence_after();
+            const bool wrong = *const_cast<volatile int32_t *>(&ct.unit[d.i].bad) != 0, cut = u.slot >= 0;
+            float2 *const part = kTurns ? ct.part + g * kHalf : reinterpret_cast<float2 *>(smem + C::kOffP + 16384 * g + 1024);
+            const int c0 = g * kHalf;                              // the columns this group writes
+            if (tok < kHalf) {
+                float l[2] = {0.f, 0.f}, m[2] = {kTreeNone, kTreeNone};
+#pragma unroll
+                for (int k = 0; k < (kTurns ? 2 : 1); ++k) {
+                    const float *x = kTurns ? &ct.red[par % Ctrl::kU][k][0][0] + c0 + tok : ls + tok;
+                    l[k] = (x[0] + x[kNC]) + (x[2 * kNC] + x[3 * kNC]);
+                    m[k] = -(kTurns ? ct.ref[par % Ctrl::kU][k % Ctrl::kU][c0 + tok] : refs[c0 + tok]);
+                }
+                const float top = l[0] == 0.f ? m[1] : l[1] == 0.f ? m[0] : fmaxf(m[0], m[1]);
+                float f[2];
+#pragma unroll
+                for (int k = 0; k < 2; ++k) f[k] = l[k] == 0.f ? 0.f : ex2(m[k] - top);
+                const float all = f[0] * l[0] + f[1] * l[1];
+                if (cut) {
+                    if (tok + c0 < u.ntok * p.group)
+                        p.part_ml[static_cast<int64_t>(u.slot) * kR + c0 + tok] = make_float2(top, wrong ? -1.f : all);
+                } else {
+                    const float vs = C::kConv ? __ldg(p.v_scale + u.h) : 1.f;
+                    const float n = wrong || all == 0.f ? 0.f : vs / all;
+                    f[0] *= n;
+                    f[1] *= n;
+                }
+                part[tok] = make_float2(f[0], f[1]);
+            }
             group_sync(barrier);
-            const bool wrong = *const_cast<volatile int32_t *>(&ct.unit[d.i].bad) != 0;
-            const float vs = C::kConv ? __ldg(p.v_scale + u.h) : 1.f;
+            const bool both = u.te - u.tb > 1;                     // which groups had tiles
+            const bool had0 = !kTurns || both || had == (g == 0), had1 = kTurns && (both || had == (g == 1));
             const int dim = 32 * wq + lane;
             bool anyodd = false;
-            for (int k = 0; k < min(odd_tiles, kTreePoison); ++k)
-                for (int w = 0; w < 4; ++w) anyodd |= *const_cast<volatile uint32_t *>(&ct.poison[d.i][k][w]) != 0;
-            constexpr int kE = 8;
+            int odd_tiles = 0;
+            for (int i = u.tb; i < u.te; ++i)
+                if (!tile_whole(u, p, tile_at(u, i))) {
+                    for (int w = 0; w < 4; ++w) anyodd |= *const_cast<volatile uint32_t *>(&ct.poison[d.i][min(odd_tiles, kTreePoison - 1)][w]) != 0;
+                    ++odd_tiles;
+                }
+            int tk = c0 / p.group, hr = c0 - tk * p.group;         // of the column: token and query head
+            __nv_bfloat16 *out = p.out + (static_cast<int64_t>(u.tok0 + tk) * p.hq + u.h * p.group + hr) * 128 + dim;
+            float *po = p.part_o + (static_cast<int64_t>(cut ? u.slot : 0) * kR + c0) * 128 + dim;
+            const int64_t skip = static_cast<int64_t>(p.hq - p.group) * 128;
+#pragma unroll 1
+            for (int c = 0; c < kHalf && tk < u.ntok; c += 8) {
+                float y[8], z[8];
+                if (had0) tmem_load(tO + c0 + c, y);
+                if (had1) tmem_load(tO + kR + c0 + c, z);
 #pragma unroll
-            for (int c = 0; c < kNC; c += kE) {
-                float y[kE];
-                tmem_load(tmem + tlane + C::kTmO + col0 + c, y);
-                if (anyodd) {
+                for (int j = 0; j < 8; ++j) {
+                    const float2 f = part[c + j];
+                    float v = had0 ? y[j] * f.x : 0.f;
+                    if (had1) v = fmaf(z[j], f.y, v);
+                    y[j] = !cut && f.x == 0.f && f.y == 0.f ? 0.f : v;
+                }
+                if (anyodd && !wrong) {
                     // NaN and infinities of V that not every row sees: left out of the product, here for those who do
                     int k = 0;
                     for (int i = u.tb; i < u.te; ++i) {
@@ -1011,35 +1136,36 @@ tree_attn_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmK, co
                         for (int b = 0; b < kTreeTok; ++b) {
                             if (!((*const_cast<volatile uint32_t *>(&ct.poison[d.i][min(k, kTreePoison - 1)][b >> 5]) >> (b & 31)) & 1)) continue;
                             const float add = odd_value<kKv>(p, u, t0 + b, dim);
-                            const uint64_t see = seen_by<kNC>(p, u, col0, t0 + b);
+                            const uint64_t see = seen_by<8>(p, u, c0 + c, t0 + b);
 #pragma unroll
-                            for (int j = 0; j < kE; ++j)
-                                if ((see >> (c + j)) & 1) y[j] += add;
+                            for (int j = 0; j < 8; ++j)
+                                if ((see >> j) & 1) y[j] += add;
                         }
                         ++k;
                     }
                 }
 #pragma unroll
-                for (int j = 0; j < kE; ++j) {
-                    const int col = c + j, row = col0 + col, tk = row / p.group;
-                    const float l = (ls[col] + ls[kNC + col]) + (ls[2 * kNC + col] + ls[3 * kNC + col]);
-                    if (tk >= u.ntok) continue;
-                    if (u.slot >= 0) {
-                        const int64_t at = static_cast<int64_t>(u.slot) * kR + row;
-                        p.part_o[at * 128 + dim] = y[j];
-                        if (dim == 0) p.part_ml[at] = make_float2(-ct.ref[row], wrong ? -1.f : l);
-                    } else {
-                        const float o = wrong || l == 0.f ? 0.f : y[j] * (vs / l);
-                        p.out[(static_cast<int64_t>(u.tok0 + tk) * p.hq + u.h * p.group + (row - tk * p.group)) * 128 + dim] = __float2bfloat16_rn(o);
+                for (int j = 0; j < 8; ++j) {
+                    if (tk < u.ntok) {
+                        if (cut) po[j * 128] = y[j];
+                        else *out = __float2bfloat16_rn(y[j]);
+                    }
+                    out += 128;
+                    if (++hr == p.group) {
+                        hr = 0;
+                        ++tk;
+                        out += skip;
                     }
                 }
+                po += 8 * 128;
             }
             umma_fence_before();
-            group_sync(barrier);                                   // references and sums are read
+            group_sync(barrier);                                   // references, sums and products are read
             if (lane == 0) {
                 mbar_arrive(bar(ct.oempty));
                 mbar_arrive(bar(ct.dempty[d.i]));
             }
+            ++par;
             d.template next<C::kND>();
         }
         __syncwarp();
