@@ -29,6 +29,7 @@
 #include <cmath>
 #include <cstddef>
 #include <mutex>
+#include <type_traits>
 
 #include "fp4_row.cuh"
 #include "umma.cuh"
@@ -118,6 +119,7 @@ struct TreeUnit {
     int32_t row, h;                            // first page-table entry, KV head
     int32_t slot;                              // of its partial sums; -1: the whole unit is here
     int32_t bad;                               // a page outside the pool
+    int32_t odd;                               // NaN or infinities in V that not every row sees
 };
 __device__ __forceinline__ uint32_t tile_at(const TreeUnit &u, int i) {
     return i < u.sink_tiles ? static_cast<uint32_t>(i) * kTreeTok : u.start + static_cast<uint32_t>(i - u.sink_tiles) * kTreeTok;
@@ -141,28 +143,28 @@ struct TreeCfg {
     // The softmax groups take turns, a tile each, with sums and references of their own; with
     // 128 rows, whose sums fill the tensor memory once, each takes half of the rows of every tile.
     static constexpr bool kTurns = kR <= 64;
-    static constexpr int kNK = kConv && (kR <= 64 || kKv == FKV_KV_FP4) ? 3 : 2;
-    static constexpr int kNV = kConv ? (kR <= 32 ? 4 : 3) : kR <= 32 ? 3 : 2;
+    // V as f16 goes into tensor memory where that has room; with 128 rows into shared memory.
+    static constexpr bool kVT = kConv && kTurns;
+    static constexpr int kNK = kKv == FKV_KV_FP4 ? (kTurns ? 8 : 3) : kVT ? 5 : 2;
+    static constexpr int kNV = kKv == FKV_KV_FP4 ? (kTurns ? 8 : 3) : kVT ? 5 : kConv || kR <= 32 ? 3 : 2;
     static constexpr int kNP = kTurns ? 2 : 1;                     // weight buffers
     static constexpr int kParts = kConv ? 1 : 2;                   // words of a weight
     static constexpr int kHalves = kR > 64 ? 2 : 1;                // 64-column halves of a weight buffer
     static constexpr int kPW = kR <= 32 ? 64 : 16384 * kHalves;    // from a weight's first word to its second
     static constexpr int kPB = kR <= 32 ? 16384 : kParts * kPW;    // a weight buffer
     static constexpr int kQB = kR * 256;
-    static constexpr int kV16 = kConv ? 32768 : 0;
-    static constexpr int kGroups = kConv && kR <= 32 ? 2 : 1;      // converter groups: K and V, or one for both
-    // Softmax warps with many columns take registers of the others: of a thread, at launch, then
+    static constexpr int kV16 = kConv && !kVT ? 32768 : 0;
+        // Softmax warps with many columns take registers of the others: of a thread, at launch, then
     // of the three kinds of warps (no more in all than at launch; whole groups of four warps).
-    static constexpr bool kShift = kR >= 64 || kGroups * kR == 64;
-    static constexpr int kThreads = 256 + 128 * kGroups + 128;     // softmax, converters; producer, two issuers, an idle warp
-    static constexpr int kRegs = kGroups == 2 ? 96 : 128;
-    static constexpr int kRegsSoft = kGroups == 2 ? 112 : 168, kRegsConv = kGroups == 2 ? 80 : 96, kRegsRest = kGroups == 2 ? 80 : 80;
-    static_assert(2 * kRegsSoft + kGroups * kRegsConv + kRegsRest <= (2 + kGroups + 1) * kRegs, "the block's registers");
+    static constexpr bool kShift = kR >= 32;
+    static constexpr int kThreads = 512;                           // softmax, converters; producer, two issuers, an idle warp
+    static constexpr int kRegsSoft = kR >= 64 ? 176 : 152, kRegsConv = kR >= 64 ? 88 : 104, kRegsRest = kR >= 64 ? 72 : 104;
+    static_assert(2 * kRegsSoft + kRegsConv + kRegsRest <= 65536 / 128, "the block's registers");
     static constexpr int kND = kR <= 64 ? 4 : 2;                   // units in flight
     static constexpr int kNC = kTurns ? kR : kR / 2;               // columns of a softmax thread
     static constexpr int kNS = kTurns ? 4 : 8;                     // softmax warps of a tile
-    // tensor memory columns: K f16 (two buffers), S (two), O (one per group that takes turns)
-    static constexpr int kTmS = kConv ? 128 : 0, kTmO = kTmS + 2 * kR;
+    // tensor memory columns: K f16 (two buffers), V f16 (two), S (two), O (one per group that takes turns)
+    static constexpr int kTmV = 128, kTmS = kVT ? 256 : kConv ? 128 : 0, kTmO = kTmS + 2 * kR;
     static_assert(kTmO + (kTurns ? 2 : 1) * kR <= 512, "tensor memory");
     static constexpr int kNVR = kConv ? 2 : kNV;                   // buffers between converters and issuer
     static constexpr int kOffP = kQB, kOffV16 = kOffP + kNP * kPB, kOffK = kOffV16 + 2 * kV16;
@@ -187,7 +189,7 @@ struct TreeCtrl {
     alignas(16) float up[2][C::kTurns ? kR : 4];
     alignas(16) float2 part[C::kTurns ? kR : 2];
     uint32_t poison[C::kND][kTreePoison][4];                       // tokens whose V holds NaN or infinities
-    int64_t scan[20];                                             // one per warp
+    int64_t scan[16];                                             // one per warp
     int64_t total, off0;
     int32_t r0;
     uint32_t tmem;
@@ -216,23 +218,25 @@ struct Ring {                                  // a buffer of a ring and the par
     }
 };
 
-// Waits for a phase, for at most kTreeWaitNs and until another thread has given up.  The
-// timer is read after a few thousand cycles only: reading it takes about a microsecond.
-__device__ __forceinline__ bool tree_wait(uint32_t bar, uint32_t parity, volatile int32_t *dead, uint32_t *err) {
+// Waits for a phase.  After kTreeWaitNs without it the call has failed: that is recorded, and
+// from then on no wait of the block waits, so that it ends soon, with outputs that are not
+// valid.  (The plain test sleeps in hardware for a while; the form with a time hint is a loop
+// of its own that takes issue slots from the warps that work.)
+__device__ __forceinline__ void tree_wait(uint32_t bar, uint32_t parity, volatile int32_t *dead, uint32_t *err) {
+    if (mbar_try_wait(bar, parity)) return;
+    uint64_t t0 = 0;
 #pragma unroll 1
-    for (int i = 0; i < 256; ++i)
-        if (mbar_try_wait(bar, parity)) return true;
-    const uint64_t t0 = globaltimer_ns();
-#pragma unroll 1
-    while (!*dead) {
-        for (int i = 0; i < 64; ++i)
-            if (mbar_try_wait(bar, parity)) return true;
-        if (globaltimer_ns() - t0 > kTreeWaitNs) {
-            *dead = 1;
-            atomicOr(err, FKV_DEVERR_TIMEOUT);
+    for (uint32_t i = 1; !mbar_try_wait(bar, parity); ++i) {
+        if ((i & 255u) == 0) {
+            const uint64_t now = globaltimer_ns();
+            if (t0 == 0) t0 = now;
+            if (now - t0 > kTreeWaitNs) {
+                *dead = 1;
+                atomicOr(err, FKV_DEVERR_TIMEOUT);
+            }
+            if (*dead) return;
         }
     }
-    return false;
 }
 
 // Whether any of the 128 threads of a softmax group says so (a barrier of the group).
@@ -252,6 +256,12 @@ __device__ __forceinline__ void group_sync(int id) { asm volatile("barrier.cta.s
 
 __device__ __forceinline__ void st_shared_v4(uint32_t addr, uint4 v) {
     asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
+}
+
+__device__ __forceinline__ uint32_t ld_shared_u16(uint32_t addr) {
+    uint16_t v;
+    asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(addr));
+    return v;
 }
 
 // ---------------------------------------------------------------------------
@@ -305,39 +315,31 @@ __device__ __forceinline__ void e4m3x4_to_f16(uint32_t w, uint32_t &lo, uint32_t
     lo = e4m3x2_to_f16x2(static_cast<uint16_t>(w & 0xFFFFu));
     hi = e4m3x2_to_f16x2(static_cast<uint16_t>(w >> 16));
 }
-// 64 values (half `hf`) of the row in a K or V stage, as f16 pairs.  kClean: NaN become
-// zeros, and `odd` says whether there were any.
-template <int kKv, bool kClean>
-__device__ __forceinline__ void half_row(uint32_t stage, int tok, int hf, uint32_t (&f)[32], bool &odd) {
+// 64 values (half `hf`) of the row in a K or V stage, as f16 pairs.
+template <int kKv>
+__device__ __forceinline__ void half_row(uint32_t stage, int tok, int hf, uint32_t (&f)[32]) {
     if (kKv == FKV_KV_FP8_E4M3) {
         const uint32_t row = stage + tok * 128;
+        uint4 v[4];                                                // all on their way before one is converted
+#pragma unroll
+        for (int c = 0; c < 4; ++c) v[c] = ld_shared_v4(row + (((4 * hf + c) ^ (tok & 7)) << 4));
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
-            const uint4 v = ld_shared_v4(row + (((4 * hf + c) ^ (tok & 7)) << 4));
-            uint32_t w[4] = {v.x, v.y, v.z, v.w};
+            const uint32_t w[4] = {v[c].x, v[c].y, v[c].z, v[c].w};
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                if (kClean) {
-                    const uint32_t nan = (((w[j] & 0x7F7F7F7Fu) + 0x01010101u) >> 7) & 0x01010101u;
-                    odd |= nan != 0;
-                    w[j] &= ~(nan * 0xFFu);
-                }
-                e4m3x4_to_f16(w[j], f[8 * c + 2 * j], f[8 * c + 2 * j + 1]);
-            }
+            for (int j = 0; j < 4; ++j) e4m3x4_to_f16(w[j], f[8 * c + 2 * j], f[8 * c + 2 * j + 1]);
         }
     } else {
         const uint32_t row = stage + tok * kFp4Row;
         const uint2 sc = ld_shared_v2(row + kFp4Codes);
         const uint32_t s4 = hf ? sc.y : sc.x;
+        uint2 cs[4];
+#pragma unroll
+        for (int b = 0; b < 4; ++b) cs[b] = ld_shared_v2(row + 32 * hf + 8 * b);
 #pragma unroll
         for (int b = 0; b < 4; ++b) {
-            const uint2 c = ld_shared_v2(row + 32 * hf + 8 * b);
-            uint32_t byte = (s4 >> (8 * b)) & 0xFFu;
-            if (kClean && (byte & 0x7Fu) == 0x7Fu) {
-                odd = true;
-                byte = 0;
-            }
-            const uint32_t s = e4m3_to_f16_pair(byte);
+            const uint2 c = cs[b];
+            const uint32_t s = e4m3_to_f16_pair((s4 >> (8 * b)) & 0xFFu);
             uint32_t x[4], y[4];
             e2m1x8_to_f16(c.x, x);
             e2m1x8_to_f16(c.y, y);
@@ -351,42 +353,110 @@ __device__ __forceinline__ void half_row(uint32_t stage, int tok, int hf, uint32
 }
 
 // A V row as f16 into a 128 x 128 operand buffer (MN-major, two halves of 64 dims).
-template <int kKv, bool kClean>
-__device__ __forceinline__ bool convert_v(uint32_t stage, uint32_t dst, int tok, bool valid) {
-    bool odd = false;
-#pragma unroll
+template <int kKv>
+__device__ __forceinline__ void convert_v(uint32_t stage, uint32_t dst, int tok) {
+#pragma unroll 1
     for (int hf = 0; hf < 2; ++hf) {
         uint32_t f[32];
-        if (!kClean || valid) {
-            half_row<kKv, kClean>(stage, tok, hf, f, odd);
-        } else {
-#pragma unroll
-            for (int j = 0; j < 32; ++j) f[j] = 0;
-        }
+        half_row<kKv>(stage, tok, hf, f);
 #pragma unroll
         for (int c = 0; c < 8; ++c)
             st_shared_v4(dst + 16384 * hf + tok * 128 + ((c ^ (tok & 7)) << 4),
                          make_uint4(f[4 * c], f[4 * c + 1], f[4 * c + 2], f[4 * c + 3]));
     }
-    return odd;
 }
 
-// A bf16 V row in its stage: rows of no token and NaN or infinite elements become zeros.
+// The V rows of a stage as f16 into tensor memory: dims on lanes, two tokens a column, from
+// column `dst` (of this warp's 32 lanes).  Thread l takes dims 4 (l / 4) .. + 3 of the warp's
+// 32 and tokens 8k + 2 (l % 4) + {0, 1}, the places of the .16x128b store: lane 16b + 8h + r
+// holds dim 4r + 2b + h.  Two tokens' codes are interleaved before they are converted, so a
+// converted pair is one dim of both.
+template <int kKv>
+__device__ __forceinline__ void convert_v_tmem(uint32_t stage, uint32_t dst, int cw, int lane) {
+    const int g = lane >> 2, t = lane & 3;
+    uint32_t r0, r1;                                               // this thread's codes of tokens 2t and 2t + 1
+    if (kKv == FKV_KV_FP8_E4M3) {
+        const int c = 2 * cw + (g >> 2);
+        r0 = stage + 2 * t * 128 + ((c ^ (2 * t)) << 4) + 4 * (g & 3);
+        r1 = stage + (2 * t + 1) * 128 + ((c ^ (2 * t + 1)) << 4) + 4 * (g & 3);
+    } else {
+        r0 = stage + 2 * t * kFp4Row + 16 * cw + 2 * g;
+        r1 = r0 + kFp4Row;
+    }
+    const uint32_t s0 = stage + 2 * t * kFp4Row + kFp4Codes + 2 * cw + (g >> 2);
+#pragma unroll 1
+    for (int hf = 0; hf < 2; ++hf) {
+        uint32_t a[16], b[16], in[8][2], sin[8][2];                // all loads on their way before one word is converted
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            const int row = 64 * hf + 8 * k;
+            if (kKv == FKV_KV_FP8_E4M3) {
+                in[k][0] = ld_shared_u32(r0 + row * 128), in[k][1] = ld_shared_u32(r1 + row * 128);
+            } else {
+                in[k][0] = ld_shared_u16(r0 + row * kFp4Row), in[k][1] = ld_shared_u16(r1 + row * kFp4Row);
+                sin[k][0] = ld_shared_u8(s0 + row * kFp4Row), sin[k][1] = ld_shared_u8(s0 + (row + 1) * kFp4Row);
+            }
+        }
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            const uint32_t w[2] = {in[k][0], in[k][1]};
+            if (kKv == FKV_KV_FP8_E4M3) {
+                const uint32_t x = prmt(w[0], w[1], 0x5140), y = prmt(w[0], w[1], 0x7362);
+                e4m3x4_to_f16(x, a[2 * k], a[2 * k + 1]);
+                e4m3x4_to_f16(y, b[2 * k], b[2 * k + 1]);
+            } else {
+                // byte 0: dim 0 of both tokens, byte 1: dim 2; and dims 1 and 3
+                const uint32_t even = (w[0] & 0x0F0Fu) | ((w[1] << 4) & 0xF0F0u), odd = ((w[0] >> 4) & 0x0F0Fu) | (w[1] & 0xF0F0u);
+                uint32_t f[4];
+                e2m1x8_to_f16(even | (odd << 16), f);
+                const uint32_t s = e4m3x2_to_f16x2(static_cast<uint16_t>(sin[k][0] | (sin[k][1] << 8)));
+                a[2 * k] = mul_f16x2(f[0], s);
+                a[2 * k + 1] = mul_f16x2(f[2], s);
+                b[2 * k] = mul_f16x2(f[1], s);
+                b[2 * k + 1] = mul_f16x2(f[3], s);
+            }
+        }
+        tmem_store_rows(dst + 32 * hf, a);
+        tmem_store_rows(dst + (16u << 16) + 32 * hf, b);
+    }
+}
+
+// A V row in its stage, of a tile that not every row sees whole: rows of no token, NaN and
+// infinities become zeros, since a weight of zero would not take them out of a product.
+// Returns whether there were NaN or infinities.  A pass of its own over these few tiles keeps
+// the conversions small: with both forms of them in the loop every tile paid for the tests
+// (64 requests, window of 4096: 173 us, 120 without).
+template <int kKv>
 __device__ __forceinline__ bool clean_v(uint32_t stage, int tok, bool valid) {
     bool odd = false;
-#pragma unroll 4
-    for (int c = 0; c < 16; ++c) {
+    constexpr int kSteps = kKv == FKV_KV_BF16 ? 16 : 8;
+#pragma unroll 1
+    for (int c = 0; c < kSteps; ++c) {
+        if (kKv == FKV_KV_FP4) {
+            const uint32_t a = stage + tok * kFp4Row + 8 * c;
+            if (!valid) {
+                st_shared_v2_zero(a);
+                if (c == 0) st_shared_v2_zero(stage + tok * kFp4Row + kFp4Codes);
+            } else if ((ld_shared_u8(stage + tok * kFp4Row + kFp4Codes + c) & 0x7Fu) == 0x7Fu) {
+                odd = true;                                        // codes of zero under a scale of zero
+                asm volatile("st.shared.u8 [%0], %1;" ::"r"(stage + tok * kFp4Row + kFp4Codes + c), "r"(0u) : "memory");
+            }
+            continue;
+        }
         const uint32_t a = stage + 16384 * (c >> 3) + tok * 128 + (((c & 7) ^ (tok & 7)) << 4);
-        uint4 v = ld_shared_v4(a);
-        uint32_t w[4] = {v.x, v.y, v.z, v.w};
-        bool change = !valid;
+        const uint4 v = ld_shared_v4(a);
+        uint32_t w[4] = {v.x, v.y, v.z, v.w}, bad = 0;
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            const uint32_t lo = (w[j] & 0x7F80u) == 0x7F80u ? 0xFFFFu : 0u, hi = (w[j] & 0x7F800000u) == 0x7F800000u ? 0xFFFF0000u : 0u;
-            if (valid && (lo | hi)) change = odd = true;
-            w[j] = valid ? w[j] & ~(lo | hi) : 0u;
+            uint32_t m;                                            // the bits of what is no number
+            if (kKv == FKV_KV_BF16) m = ((w[j] & 0x7F80u) == 0x7F80u ? 0xFFFFu : 0u) | ((w[j] & 0x7F800000u) == 0x7F800000u ? 0xFFFF0000u : 0u);
+            else m = ((((w[j] & 0x7F7F7F7Fu) + 0x01010101u) >> 7) & 0x01010101u) * 0xFFu;
+            if (!valid) m = 0xFFFFFFFFu;
+            else odd |= m != 0;
+            bad |= m;
+            w[j] &= ~m;
         }
-        if (change) st_shared_v4(a, make_uint4(w[0], w[1], w[2], w[3]));
+        if (bad) st_shared_v4(a, make_uint4(w[0], w[1], w[2], w[3]));
     }
     return odd;
 }
@@ -439,10 +509,10 @@ tree_attn_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmK, co
     const uint32_t base = smem_u32(smem);
     const uint32_t sQ = base, sP = base + C::kOffP, sV16 = base + C::kOffV16, sK = base + C::kOffK, sV = base + C::kOffV;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    constexpr int kConvW = 8, kProdW = 8 + 4 * C::kGroups, kMmaW = kProdW + 1, kMmaW2 = kProdW + 2;
+    constexpr int kConvW = 8, kProdW = 12, kMmaW = kProdW + 1, kMmaW2 = kProdW + 2;
     volatile int32_t *dead = &ct.dead;
     auto bar = [&](uint64_t &b) { return smem_u32(&b); };
-    auto wait = [&](uint64_t &b, uint32_t parity) { return tree_wait(smem_u32(&b), parity, dead, p.err); };
+    auto wait = [&](uint64_t &b, uint32_t parity) { tree_wait(smem_u32(&b), parity, dead, p.err); };
 
     if (tid == 0) {
         constexpr int kKC = C::kConv ? 4 : 1;                      // who empties a stage: converter warps, or the issuer
@@ -456,7 +526,7 @@ tree_attn_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmK, co
         for (int i = 0; i < C::kNP; ++i) mbar_init(bar(ct.pfull[i]), C::kNS), mbar_init(bar(ct.pempty[i]), 1);
         mbar_init(bar(ct.qfull), 4), mbar_init(bar(ct.qempty), 1), mbar_init(bar(ct.oempty), 8), mbar_init(bar(ct.drained[0]), 1), mbar_init(bar(ct.drained[1]), 1);
         for (int i = 0; i < C::kND; ++i)
-            mbar_init(bar(ct.dfull[i]), 1), mbar_init(bar(ct.dempty[i]), 8 + 4 * C::kGroups + 2), mbar_init(bar(ct.cfull[i]), 4);
+            mbar_init(bar(ct.dfull[i]), 1), mbar_init(bar(ct.dempty[i]), 8 + 4 + 2), mbar_init(bar(ct.cfull[i]), 4);
         ct.dead = 0;
         ct.r0 = p.batch;
         fence_mbar_init();
@@ -520,17 +590,16 @@ tree_attn_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmK, co
         int4 join = make_int4(-1, 0, 0, 0);
         TreeRequest cur = tree_request(p, r), nxt = tree_request(p, r + 1);
         Ring d, k, v;
-        bool ok = true;
         const int npg = kTreeTok / p.page_size;
-        while (left > 0 && ok) {
+        while (left > 0 && !*dead) {
             const TreeSpan sp = tree_span(p, cur);
             const int mt = (cur.n + tpt - 1) / tpt, units = mt * p.hkv;
             const uint64_t policy = mt > 1 ? again : once;
-            for (int ui = static_cast<int>(off / sp.tiles), tb = static_cast<int>(off % sp.tiles); ui < units && left > 0 && ok; ++ui, tb = 0) {
+            for (int ui = static_cast<int>(off / sp.tiles), tb = static_cast<int>(off % sp.tiles); ui < units && left > 0; ++ui, tb = 0) {
                 const int te = left < sp.tiles - tb ? tb + static_cast<int>(left) : sp.tiles;
                 const int h = ui / mt, m = ui - h * mt;
-                ok = wait(ct.dempty[d.i], d.ph ^ 1);
-                if (!ok) break;
+                wait(ct.dempty[d.i], d.ph ^ 1);
+                if (*dead) break;                                  // others may still read what is there
                 TreeUnit u;
                 u.tb = tb;
                 u.te = te;
@@ -546,8 +615,9 @@ tree_attn_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmK, co
                 u.row = cur.row;
                 u.h = h;
                 u.slot = tb == 0 && te == sp.tiles ? -1 : 2 * static_cast<int>(blockIdx.x) + (tb == 0 ? 1 : 0);
-                u.bad = 0;
+                u.bad = u.odd = 0;
                 if (lane == 0) ct.unit[d.i] = u;
+                for (int i = lane; i < 4 * kTreePoison; i += 32) (&ct.poison[d.i][0][0])[i] = 0;
                 __syncwarp();
                 if (lane == 0) mbar_arrive(bar(ct.dfull[d.i]));
                 if (tb > 0 && te == sp.tiles) {
@@ -584,12 +654,10 @@ tree_attn_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmK, co
                             if (kKv == FKV_KV_BF16) tma_load_4d(dst + 16384 + lane * p.page_size * 128, tm, bar(full), 64, 0, h, pg, policy);
                         }
                     };
-                    ok = wait(ct.kempty[k.i], k.ph ^ 1);
-                    if (!ok) break;
+                    wait(ct.kempty[k.i], k.ph ^ 1);
                     copy(ct.kfull[k.i], sK + k.i * C::kStageB, &tmK, p.k_cache);
                     k.template next<C::kNK>();
-                    ok = wait(ct.vempty[v.i], v.ph ^ 1);
-                    if (!ok) break;
+                    wait(ct.vempty[v.i], v.ph ^ 1);
                     copy(ct.vfull[v.i], sV + v.i * C::kStageB, &tmV, p.v_cache);
                     v.template next<C::kNV>();
                 }
@@ -597,7 +665,7 @@ tree_attn_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmK, co
                 d.template next<C::kND>();
             }
             off = 0;
-            if (left > 0 && ok) {
+            if (left > 0) {
                 do {
                     ++r;
                     cur = nxt;
@@ -606,11 +674,10 @@ tree_attn_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmK, co
                 if (r >= p.batch) break;
             }
         }
-        if (ok && wait(ct.dempty[d.i], d.ph ^ 1)) {
-            if (lane == 0) {
-                ct.unit[d.i].te = -1;
-                mbar_arrive(bar(ct.dfull[d.i]));
-            }
+        wait(ct.dempty[d.i], d.ph ^ 1);
+        if (lane == 0 && !*dead) {
+            ct.unit[d.i].te = -1;
+            mbar_arrive(bar(ct.dfull[d.i]));
         }
         if (lane == 0) p.joins[blockIdx.x] = join;
         __syncwarp();
@@ -625,21 +692,21 @@ tree_attn_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmK, co
         constexpr bool kB16 = !C::kConv;
         constexpr uint32_t kHi = umma_desc_hi(1024);
         Ring d;
-        bool ok = true;
         if (warp == kMmaW) {
             constexpr uint32_t id = umma_idesc(kB16, false, false, 128, kR);
             const uint32_t lQ = umma_desc_lo(sQ, 16), lK = umma_desc_lo(sK, 16);
             Ring k, sb;
-            for (uint32_t units = 0; ok; ++units) {
-                if (!(ok = wait(ct.dfull[d.i], d.ph))) break;
+            for (uint32_t units = 0;; ++units) {
+                wait(ct.dfull[d.i], d.ph);
                 const int tb = *const_cast<volatile int32_t *>(&ct.unit[d.i].tb), te = *const_cast<volatile int32_t *>(&ct.unit[d.i].te);
-                if (te < 0) break;
+                if (te < 0 || *dead) break;
                 __syncwarp();
                 if (elect_one()) mbar_arrive(bar(ct.dempty[d.i]));
                 d.template next<C::kND>();
-                if (!(ok = wait(ct.qfull, units & 1))) break;
+                wait(ct.qfull, units & 1);
                 for (int i = tb; i < te; ++i) {
-                    if (!(ok = wait(kB16 ? ct.kfull[k.i] : ct.k16full[k.i], k.ph) && wait(ct.sempty[sb.i], sb.ph ^ 1))) break;
+                    wait(kB16 ? ct.kfull[k.i] : ct.k16full[k.i], k.ph);
+                    wait(ct.sempty[sb.i], sb.ph ^ 1);
                     umma_fence_after();
                     const uint32_t dst = tmem + C::kTmS + sb.i * kR, ta = tmem + k.i * 64, la = lK + k.i * (C::kStageB / 16);
                     __syncwarp();
@@ -660,20 +727,21 @@ tree_attn_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmK, co
                 }
             }
         } else {
-            constexpr uint32_t id = umma_idesc(kB16, true, true, 128, kR);
+            constexpr uint32_t id = umma_idesc(kB16, !C::kVT, true, 128, kR);
             const uint32_t lP = umma_desc_lo(sP, 16384), lV = umma_desc_lo(C::kConv ? sV16 : sV, 16384);
             constexpr uint32_t kVStep = (C::kConv ? C::kV16 : C::kStageB) / 16;
             Ring v, pb;
-            for (uint32_t units = 0; ok; ++units) {
-                if (!(ok = wait(ct.dfull[d.i], d.ph))) break;
+            for (uint32_t units = 0;; ++units) {
+                wait(ct.dfull[d.i], d.ph);
                 const int tb = *const_cast<volatile int32_t *>(&ct.unit[d.i].tb), te = *const_cast<volatile int32_t *>(&ct.unit[d.i].te);
-                if (te < 0) break;
+                if (te < 0 || *dead) break;
                 __syncwarp();
                 if (elect_one()) mbar_arrive(bar(ct.dempty[d.i]));
                 d.template next<C::kND>();
-                if (units && !(ok = wait(ct.oempty, (units - 1) & 1))) break;
+                if (units) wait(ct.oempty, (units - 1) & 1);
                 for (int i = tb; i < te; ++i) {
-                    if (!(ok = wait(ct.vready[v.i], v.ph) && wait(ct.pfull[pb.i], pb.ph))) break;
+                    wait(ct.vready[v.i], v.ph);
+                    wait(ct.pfull[pb.i], pb.ph);
                     umma_fence_after();
                     const uint32_t lv = lV + v.i * kVStep, lp = lP + pb.i * (C::kPB / 16);
                     const uint32_t dst = tmem + C::kTmO + (C::kTurns ? pb.i * kR : 0);
@@ -683,9 +751,12 @@ tree_attn_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmK, co
 #pragma unroll
                         for (int w = 0; w < C::kParts; ++w) {
 #pragma unroll
-                            for (int kk = 0; kk < 8; ++kk)
-                                umma_ss(dst, umma_desc(lv + kk * 128, kHi), umma_desc(lp + w * (C::kPW / 16) + kk * 128, kHi), id,
-                                        !first || w > 0 || kk > 0);
+                            for (int kk = 0; kk < 8; ++kk) {
+                                const uint64_t b = umma_desc(lp + w * (C::kPW / 16) + kk * 128, kHi);
+                                const bool add = !first || w > 0 || kk > 0;
+                                if (C::kVT) umma_ts(dst, tmem + C::kTmV + v.i * 64 + kk * 8, b, id, add);
+                                else umma_ss(dst, umma_desc(lv + kk * 128, kHi), b, id, add);
+                            }
                         }
                         umma_commit(bar(ct.pempty[pb.i]));
                         umma_commit(bar(C::kConv ? ct.v16empty[v.i & 1] : ct.vempty[v.i]));
@@ -705,18 +776,17 @@ tree_attn_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmK, co
     } else if (warp >= kConvW) {
         // ==== converters ====
         if constexpr (C::kShift) regs_down<C::kRegsConv>();
-        const int grp = (warp - kConvW) >> 2, ctid = tid - 256 - 128 * grp, cw = ctid >> 5;
-        const bool do_k = grp == 0, do_v = C::kGroups == 1 || grp == 1;
+        const int ctid = tid - 256, cw = ctid >> 5;
         const uint32_t tlane = static_cast<uint32_t>(32 * cw) << 16;
         Ring d, k, kb, v, vb;
         uint32_t nu = 0;
         while (true) {
-            if (!wait(ct.dfull[d.i], d.ph)) break;
+            wait(ct.dfull[d.i], d.ph);
             const TreeUnit u = ct.unit[d.i];
-            if (u.te < 0) break;
-            if (do_k) {
+            if (u.te < 0 || *dead) break;
+            {
                 // ---- the unit's Q ----
-                if (!wait(ct.qempty, (nu & 1) ^ 1)) break;
+                wait(ct.qempty, (nu & 1) ^ 1);
                 constexpr int kU = kR / 8 < 8 ? kR / 8 : 8;
                 const int c16 = ctid & 15;
                 const float ks = C::kConv ? __ldg(p.k_scale + u.h) : 1.f;
@@ -765,18 +835,17 @@ tree_attn_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmK, co
                 }
             }
             ++nu;
-            bool ok = true;
             int odd_tiles = 0;
-            for (int i = u.tb; i < u.te && ok; ++i) {
-                if (do_k && C::kConv) {
+            for (int i = u.tb; i < u.te; ++i) {
+                if constexpr (C::kConv) {
                     // ---- K: f16 rows in tensor memory ----
-                    if (!(ok = wait(ct.kfull[k.i], k.ph) && wait(ct.k16empty[kb.i], kb.ph ^ 1))) break;
+                    wait(ct.kfull[k.i], k.ph);
+                    wait(ct.k16empty[kb.i], kb.ph ^ 1);
                     umma_fence_after();
-                    bool none = false;
-#pragma unroll
+#pragma unroll 1
                     for (int hf = 0; hf < 2; ++hf) {
                         uint32_t f[32];
-                        half_row<C::kConv ? kKv : FKV_KV_FP8_E4M3, false>(sK + k.i * C::kStageB, ctid, hf, f, none);
+                        half_row<C::kConv ? kKv : FKV_KV_FP8_E4M3>(sK + k.i * C::kStageB, ctid, hf, f);
                         tmem_store(tmem + tlane + kb.i * 64 + 32 * hf, f);
                     }
                     tmem_store_wait();
@@ -789,26 +858,31 @@ tree_attn_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmK, co
                     k.template next<C::kNK>();
                     kb.template next<2>();
                 }
-                if (do_v) {
-                    // ---- V: f16 rows in an operand buffer ----
-                    if (!(ok = wait(ct.vfull[v.i], v.ph))) break;
-                    const uint32_t t0 = tile_at(u, i), t = t0 + ctid;
-                    const bool whole = tile_whole(u, p, t0), valid = t < tile_end(u, i);
-                    bool odd = false;
-                    if (C::kConv) {
-                        if (!(ok = wait(ct.v16empty[vb.i & 1], vb.ph ^ 1))) break;
-                        const uint32_t dst = sV16 + vb.i * C::kV16, src = sV + v.i * C::kStageB;
-                        if (whole) convert_v<C::kConv ? kKv : FKV_KV_FP8_E4M3, false>(src, dst, ctid, true);
-                        else odd = convert_v<C::kConv ? kKv : FKV_KV_FP8_E4M3, true>(src, dst, ctid, valid);
-                    } else if (!whole) {
-                        odd = clean_v(sV + v.i * C::kStageB, ctid, valid);
-                    }
+                {
+                    // ---- V: f16 in tensor memory, or rows in an operand buffer; BF16 as it lies ----
+                    wait(ct.vfull[v.i], v.ph);
+                    const uint32_t t0 = tile_at(u, i), end = tile_end(u, i), n = end > t0 ? end - t0 : 0;
+                    const uint32_t src = sV + v.i * C::kStageB;
+                    const bool whole = tile_whole(u, p, t0);
                     if (!whole) {
-                        const uint32_t m = __ballot_sync(kAll, odd);
-                        if (lane == 0) *const_cast<volatile uint32_t *>(&ct.poison[d.i][min(odd_tiles, kTreePoison - 1)][cw]) = m;
+                        if (clean_v<kKv>(src, ctid, static_cast<uint32_t>(ctid) < n)) {
+                            atomicOr(&ct.poison[d.i][min(odd_tiles, kTreePoison - 1)][ctid >> 5], 1u << (ctid & 31));
+                            *const_cast<volatile int32_t *>(&ct.unit[d.i].odd) = 1;
+                        }
+                        if (C::kConv) group_sync(3 + 1);           // the converters: a warp reads other warps' tokens
                         ++odd_tiles;
                     }
-                    if (C::kConv || !whole) fence_proxy_async_smem();
+                    constexpr int kF = C::kConv ? kKv : FKV_KV_FP8_E4M3;
+                    if (C::kConv) wait(ct.v16empty[vb.i & 1], vb.ph ^ 1);
+                    if constexpr (C::kVT) {
+                        umma_fence_after();
+                        convert_v_tmem<kF>(src, tmem + tlane + C::kTmV + vb.i * 64, cw, lane);
+                        tmem_store_wait();
+                        umma_fence_before();
+                    } else {
+                        if constexpr (C::kConv) convert_v<kF>(src, sV16 + vb.i * C::kV16, ctid);
+                    }
+                    if ((C::kConv && !C::kVT) || !whole) fence_proxy_async_smem();
                     __syncwarp();
                     if (lane == 0) {
                         mbar_arrive(bar(ct.vready[vb.i]));
@@ -818,13 +892,12 @@ tree_attn_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmK, co
                     vb.template next<C::kNVR>();
                 }
             }
-            if (!ok) break;
             __syncwarp();
             if (lane == 0) mbar_arrive(bar(ct.dempty[d.i]));
             d.template next<C::kND>();
         }
         // ---- rows of requests without work ----
-        if (grp == 0) {
+        {
             __syncwarp();
             for (int r = blockIdx.x; r < p.batch; r += gridDim.x) {
                 const TreeRequest q = tree_request(p, r);
@@ -838,7 +911,7 @@ tree_attn_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmK, co
         // ==== softmax ====
         if constexpr (C::kShift) regs_up<C::kRegsSoft>();
         constexpr bool kTurns = C::kTurns;
-        constexpr int kNC = C::kNC, kCh = kNC < 32 ? kNC : 32, kChunks = kNC / kCh;
+        constexpr int kNC = C::kNC, kLd = kNC < 32 ? kNC : 32;     // columns of a thread, and of a load
         const int g = warp >> 2, wq = warp & 3, tok = tid & 127, barrier = 1 + g;
         const int col0 = kTurns ? 0 : g * kNC;                     // this thread's columns begin here
         const uint32_t tlane = static_cast<uint32_t>(32 * wq) << 16;
@@ -847,11 +920,10 @@ tree_attn_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmK, co
         Ring d;
         int sb = kTurns ? g : 0;                                   // S buffer, and the rounds of it and of the weights' buffer
         uint32_t sph = 0, pph = 0, turn = 0, par = 0;              // (turn: whose the next tile is; par: the unit's parity)
-        bool bad = false;                                          // this thread's waits
         float sum[kNC];
         while (true) {
-            bad |= !wait(ct.dfull[d.i], d.ph);
-            if (kTurns ? both_any(bad) : group_any(barrier, bad)) break;
+            wait(ct.dfull[d.i], d.ph);
+            if (kTurns ? both_any(*dead != 0) : group_any(barrier, *dead != 0)) break;
             const TreeUnit u = ct.unit[d.i];
             if (u.te < 0) break;
             float *const refs = kTurns ? ct.ref[par % Ctrl::kU][g % Ctrl::kU] : ct.ref[0][0];
@@ -859,76 +931,63 @@ tree_attn_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmK, co
             if (tok < kNC) refs[col0 + tok] = -kTreeNone;
 #pragma unroll
             for (int j = 0; j < kNC; ++j) sum[j] = 0.f;
-            bad |= !wait(ct.cfull[d.i], d.ph);
+            wait(ct.cfull[d.i], d.ph);
             group_sync(barrier);
             const uint32_t scs = smem_u32(ct.colscale[d.i]) + 4 * col0;
-            bool quit = false, had = false;                        // had: a tile of this unit
+            bool had = false;                                      // a tile of this unit
             for (int i = kTurns ? u.tb + static_cast<int>((g ^ turn) & 1) : u.tb; i < u.te; i += kTurns ? 2 : 1) {
                 const uint32_t t0 = tile_at(u, i);
                 const bool whole = tile_whole(u, p, t0);
                 const uint64_t see = whole ? ~0ull : seen_by<kNC>(p, u, col0, t0 + tok);
-                bad |= !wait(ct.sfull[sb], sph);
+                wait(ct.sfull[sb], sph);
                 umma_fence_after();
                 const uint32_t ts = tmem + tlane + C::kTmS + sb * kR + col0;
-                float x[kCh];
-                // kCh columns' logits in log2 units; less their references, unseen ones -infinity
-                auto logits = [&](int ch) {
-                    tmem_load(ts + ch * kCh, x);
+                float x[kNC];
+                // the columns' logits in log2 units, less their references where kLess; unseen ones -infinity
+                auto logits = [&](auto less) {
+                    constexpr bool kLess = decltype(less)::value;
 #pragma unroll
-                    for (int j = 0; j < kCh; j += 4) {
-                        const float4 c4 = ld_shared_f4(scs + 4 * (ch * kCh + j));
-                        const float2 a = unpack2(mul2(pack2(x[j], x[j + 1]), pack2(c4.x, c4.y))), b = unpack2(mul2(pack2(x[j + 2], x[j + 3]), pack2(c4.z, c4.w)));
-                        x[j] = a.x, x[j + 1] = a.y, x[j + 2] = b.x, x[j + 3] = b.y;
+                    for (int c = 0; c < kNC; c += kLd) tmem_load(ts + c, *reinterpret_cast<float(*)[kLd]>(&x[c]));
+#pragma unroll
+                    for (int j = 0; j < kNC; j += 4) {
+                        const float4 c4 = ld_shared_f4(scs + 4 * j);
+                        uint64_t a = mul2(pack2(x[j], x[j + 1]), pack2(c4.x, c4.y)), b = mul2(pack2(x[j + 2], x[j + 3]), pack2(c4.z, c4.w));
+                        if (kLess) {
+                            // rounded products, as the references': a fused one would leave their rounding, up to 2^9
+                            // at logits of 1e10, in the exponent
+                            const float4 r4 = ld_shared_f4(sref + 4 * j);
+                            a = add2(a, pack2(r4.x, r4.y));
+                            b = add2(b, pack2(r4.z, r4.w));
+                        }
+                        const float2 e = unpack2(a), f = unpack2(b);
+                        x[j] = e.x, x[j + 1] = e.y, x[j + 2] = f.x, x[j + 3] = f.y;
                     }
                     if (!whole) {
+                        asm volatile("" ::: "memory");             // a branch: as selects every tile would pay for them
 #pragma unroll
-                        for (int j = 0; j < kCh; ++j)
-                            if (!((see >> (ch * kCh + j)) & 1)) x[j] = -INFINITY;
+                        for (int j = 0; j < kNC; ++j)
+                            if (!((see >> j) & 1)) x[j] = -INFINITY;
                     }
                 };
-                auto exponents = [&](int ch) {
-                    tmem_load(ts + ch * kCh, x);
-#pragma unroll
-                    for (int j = 0; j < kCh; j += 4) {
-                        const float4 c4 = ld_shared_f4(scs + 4 * (ch * kCh + j)), r4 = ld_shared_f4(sref + 4 * (ch * kCh + j));
-                        // rounded products, as the references': a fused one would leave their rounding, up to 2^9 at
-                        // logits of 1e10, in the exponent
-                        const float2 a = unpack2(add2(mul2(pack2(x[j], x[j + 1]), pack2(c4.x, c4.y)), pack2(r4.x, r4.y)));
-                        const float2 b = unpack2(add2(mul2(pack2(x[j + 2], x[j + 3]), pack2(c4.z, c4.w)), pack2(r4.z, r4.w)));
-                        x[j] = a.x, x[j + 1] = a.y, x[j + 2] = b.x, x[j + 3] = b.y;
-                    }
-                    if (!whole) {
-#pragma unroll
-                        for (int j = 0; j < kCh; ++j)
-                            if (!((see >> (ch * kCh + j)) & 1)) x[j] = -INFINITY;
-                    }
-                };
-                float most = -INFINITY;
-#pragma unroll
-                for (int ch = kChunks - 1; ch >= 0; --ch) {
-                    exponents(ch);
+                for (int tries = 0;; ++tries) {                    // (a second time only where logits are so large that a reference is rounded)
+                    logits(std::true_type{});
                     float m4[4] = {x[0], x[1], x[2], x[3]};
 #pragma unroll
-                    for (int j = 4; j < kCh; ++j) m4[j & 3] = fmaxf(m4[j & 3], x[j]);
-                    most = fmaxf(most, fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])));
-                }
-                if (group_any(barrier, most > kTreeMost || bad)) {
-                    if (group_any(barrier, bad)) {
-                        quit = true;
-                        break;
-                    }
+                    for (int j = 4; j < kNC; ++j) m4[j & 3] = fmaxf(m4[j & 3], x[j]);
+                    const float most = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
+                    if (!group_any(barrier, most > kTreeMost) || tries == 4) break;
                     // ---- move the references of the columns that need it ----
                     const int buf = kTurns ? g : 0;
-                    if (had) bad |= !wait(ct.pempty[buf], pph ^ 1);              // the sums so far are complete
+                    if (had) wait(ct.pempty[buf], pph ^ 1);                      // the sums so far are complete
                     umma_fence_after();
                     if constexpr (kTurns) {
                         float(*const red)[kR] = ct.red[par % Ctrl::kU][g];
+                        logits(std::false_type{});
+                        spread<kNC, 16>(x, lane, [](float a, float b) { return fmaxf(a, b); });
+                        constexpr int kHas = kNC >= 32 ? kNC / 32 : 1, kSame = kNC >= 32 ? 1 : 32 / kNC;
+                        if (lane % kSame == 0) {
 #pragma unroll
-                        for (int ch = 0; ch < kChunks; ++ch) {
-                            logits(ch);
-                            spread<kCh, 16>(x, lane, [](float a, float b) { return fmaxf(a, b); });
-                            constexpr int kSpan = 32 / kCh;
-                            if (lane % kSpan == 0) red[wq][ch * kCh + lane / kSpan] = x[0];
+                            for (int j = 0; j < kHas; ++j) red[wq][(lane / kSame) * kHas + j] = x[j];
                         }
                         group_sync(barrier);
                         bool move = false;
@@ -1005,50 +1064,37 @@ tree_attn_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmK, co
                         umma_fence_before();
                         group_sync(barrier);                       // the new references are there
                     }
-                    exponents(0);
                 }
                 // ---- weights ----
-                if (kChunks == 1) {                                // S is read
-                    umma_fence_before();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(bar(ct.sempty[sb]));
-                }
-                bad |= !wait(ct.pempty[kTurns ? g : 0], pph ^ 1);
+                umma_fence_before();                               // S is read
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar(ct.sempty[sb]));
+                wait(ct.pempty[kTurns ? g : 0], pph ^ 1);
 #pragma unroll
-                for (int ch = 0; ch < kChunks; ++ch) {
-                    if (ch > 0) {                                  // (chunk 0 was the last of the first pass)
-                        exponents(ch);
-                        umma_fence_before();
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(bar(ct.sempty[sb]));
+                for (int j = 0; j < kNC; j += 8) {
+#pragma unroll
+                    for (int k = j; k < j + 8; k += 2) {
+                        x[k] = ex2(x[k]);
+                        x[k + 1] = ex2(x[k + 1]);
+                        const float2 t = unpack2(add2(pack2(sum[k], sum[k + 1]), pack2(x[k], x[k + 1])));
+                        sum[k] = t.x;
+                        sum[k + 1] = t.y;
                     }
+                    const uint32_t at = sPw + ((j >> 3) ^ (tok & 7)) * 16;
+                    if (C::kConv) {
+                        st_shared_v4(at, make_uint4(pack_f16x2(x[j], x[j + 1]), pack_f16x2(x[j + 2], x[j + 3]),
+                                                    pack_f16x2(x[j + 4], x[j + 5]), pack_f16x2(x[j + 6], x[j + 7])));
+                    } else {
+                        // two bf16 words: one alone would round a weight by up to 2^-8
+                        uint32_t hi[4], lo[4];
 #pragma unroll
-                    for (int j = 0; j < kCh; j += 2) {
-                        x[j] = ex2(x[j]);
-                        x[j + 1] = ex2(x[j + 1]);
-                        const float2 t = unpack2(add2(pack2(sum[ch * kCh + j], sum[ch * kCh + j + 1]), pack2(x[j], x[j + 1])));
-                        sum[ch * kCh + j] = t.x;
-                        sum[ch * kCh + j + 1] = t.y;
-                    }
-#pragma unroll
-                    for (int j = 0; j < kCh; j += 8) {
-                        const uint32_t at = sPw + (((ch * kCh + j) >> 3) ^ (tok & 7)) * 16;
-                        if (C::kConv) {
-                            st_shared_v4(at, make_uint4(pack_f16x2(x[j], x[j + 1]), pack_f16x2(x[j + 2], x[j + 3]),
-                                                        pack_f16x2(x[j + 4], x[j + 5]), pack_f16x2(x[j + 6], x[j + 7])));
-                        } else {
-                            // two bf16 words: one alone would round a weight by up to 2^-8
-                            uint32_t hi[4], lo[4];
-#pragma unroll
-                            for (int b = 0; b < 4; ++b) {
-                                const float e = x[j + 2 * b], f = x[j + 2 * b + 1];
-                                hi[b] = pack_bf16x2(e, f);
-                                lo[b] = pack_bf16x2(e - __uint_as_float(hi[b] << 16), f - __uint_as_float(hi[b] & 0xFFFF0000u));
-                            }
-                            st_shared_v4(at, make_uint4(hi[0], hi[1], hi[2], hi[3]));
-                            st_shared_v4(C::kPW < 128 ? sPw + ((((ch * kCh + j) >> 3) + C::kPW / 16) ^ (tok & 7)) * 16 : at + C::kPW,
-                                         make_uint4(lo[0], lo[1], lo[2], lo[3]));
+                        for (int b = 0; b < 4; ++b) {
+                            const float e = x[j + 2 * b], f = x[j + 2 * b + 1];
+                            hi[b] = pack_bf16x2(e, f);
+                            lo[b] = pack_bf16x2(e - __uint_as_float(hi[b] << 16), f - __uint_as_float(hi[b] & 0xFFFF0000u));
                         }
+                        st_shared_v4(at, make_uint4(hi[0], hi[1], hi[2], hi[3]));
+                        st_shared_v4(C::kPW < 128 ? sPw + (((j >> 3) + C::kPW / 16) ^ (tok & 7)) * 16 : at + C::kPW, make_uint4(lo[0], lo[1], lo[2], lo[3]));
                     }
                 }
                 fence_proxy_async_smem();
@@ -1059,19 +1105,19 @@ tree_attn_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmK, co
                 if (kTurns) sph ^= 1;
                 else if ((sb ^= 1) == 0) sph ^= 1;
             }
-            if (quit && !kTurns) break;                            // (groups that take turns leave together, below)
             turn += u.te - u.tb;
             // ---- end of this CTA's part of the unit ----
             // sums over the tokens; the groups' sums joined; a group writes half of the columns
             constexpr int kHalf = kR / 2, kPer = kNC >= 32 ? kNC / 32 : 1, kSpan = kNC >= 32 ? 1 : 32 / kNC;
             spread<kNC, 16>(sum, lane, [](float a, float b) { return a + b; });
-            if (had) bad |= !wait(ct.pempty[kTurns ? g : 0], pph ^ 1);     // all products are done, the weights' buffer is free
+            if (had) wait(ct.pempty[kTurns ? g : 0], pph ^ 1);             // all products are done, the weights' buffer is free
             float *const ls = kTurns ? &ct.red[par % Ctrl::kU][g][0][0] : reinterpret_cast<float *>(smem + C::kOffP + 16384 * g);
             if (lane % kSpan == 0) {
 #pragma unroll
                 for (int j = 0; j < kPer; ++j) ls[wq * kNC + (lane / kSpan) * kPer + j] = sum[j];
             }
-            if (kTurns ? both_any(bad) : group_any(barrier, bad)) break;
+            if (kTurns) both_any(false);
+            else group_sync(barrier);
             umma_fence_after();
             const bool wrong = *const_cast<volatile int32_t *>(&ct.unit[d.i].bad) != 0, cut = u.slot >= 0;
             float2 *const part = kTurns ? ct.part + g * kHalf : reinterpret_cast<float2 *>(smem + C::kOffP + 16384 * g + 1024);
@@ -1103,14 +1149,9 @@ tree_attn_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmK, co
             group_sync(barrier);
             const bool both = u.te - u.tb > 1;                     // which groups had tiles
             const bool had0 = !kTurns || both || had == (g == 0), had1 = kTurns && (both || had == (g == 1));
-            const int dim = 32 * wq + lane;
-            bool anyodd = false;
-            int odd_tiles = 0;
-            for (int i = u.tb; i < u.te; ++i)
-                if (!tile_whole(u, p, tile_at(u, i))) {
-                    for (int w = 0; w < 4; ++w) anyodd |= *const_cast<volatile uint32_t *>(&ct.poison[d.i][min(odd_tiles, kTreePoison - 1)][w]) != 0;
-                    ++odd_tiles;
-                }
+            // the dim of this thread's lane (convert_v_tmem)
+            const int dim = 32 * wq + (C::kVT ? 4 * (lane & 7) + 2 * (lane >> 4) + ((lane >> 3) & 1) : lane);
+            const bool anyodd = *const_cast<volatile int32_t *>(&ct.unit[d.i].odd) != 0;
             int tk = c0 / p.group, hr = c0 - tk * p.group;         // of the column: token and query head
             __nv_bfloat16 *out = p.out + (static_cast<int64_t>(u.tok0 + tk) * p.hq + u.h * p.group + hr) * 128 + dim;
             float *po = p.part_o + (static_cast<int64_t>(cut ? u.slot : 0) * kR + c0) * 128 + dim;

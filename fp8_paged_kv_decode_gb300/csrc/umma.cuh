@@ -56,6 +56,12 @@ __device__ __forceinline__ void tmem_store(uint32_t addr, const uint32_t (&r)[32
 __device__ __forceinline__ void tmem_store(uint32_t addr, const uint32_t (&r)[8]) {
     asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(addr), FKV_I8(r, 0) : "memory");
 }
+// 16 lanes of 32 columns (.16x128b.x8): register 2k is lane l / 4, column 4k + l % 4 of this
+// thread l, register 2k + 1 the same of lane 8 + l / 4.
+__device__ __forceinline__ void tmem_store_rows(uint32_t addr, const uint32_t (&r)[16]) {
+    asm volatile("tcgen05.st.sync.aligned.16x128b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};"
+                 ::"r"(addr), FKV_I16(r, 0) : "memory");
+}
 #undef FKV_I4
 #undef FKV_I8
 #undef FKV_I16
