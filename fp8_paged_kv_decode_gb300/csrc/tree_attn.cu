@@ -34,6 +34,9 @@
 #include "fp4_row.cuh"
 #include "umma.cuh"
 
+#ifndef FKV_TWO
+#define FKV_TWO 32
+#endif
 namespace fkv {
 
 constexpr int kTreeMaxWords = 4;               // 64-bit words of a row's mask
@@ -41,7 +44,8 @@ constexpr int kTreeTok = 128;                  // tokens of a tile
 constexpr int kTreePoison = 10;                // tiles of a unit that hold tokens not seen by every row, at most (9)
 constexpr float kTreeTop = 10.f, kTreeMost = 15.9f;   // log2 of a moved reference's largest weight, and of any weight
 constexpr float kTreeNone = -3e38f;            // the reference of a column that has seen nothing
-constexpr uint64_t kTreeWaitNs = 2000000000ull;
+constexpr int kTreeTests = 1 << 24;
+constexpr uint64_t kTreeDrainNs = 2000000000ull;
 constexpr uint32_t kAll = 0xffffffffu;
 
 struct TreeParams {
@@ -154,12 +158,15 @@ struct TreeCfg {
     static constexpr int kPB = kR <= 32 ? 16384 : kParts * kPW;    // a weight buffer
     static constexpr int kQB = kR * 256;
     static constexpr int kV16 = kConv && !kVT ? 32768 : 0;
-        // Softmax warps with many columns take registers of the others: of a thread, at launch, then
+        static constexpr int kGroups = kConv && kR <= FKV_TWO ? 2 : 1;      // converter groups: K and V, or one for both
+    // Softmax warps with many columns take registers of the others: of a thread, at launch, then
     // of the three kinds of warps (no more in all than at launch; whole groups of four warps).
     static constexpr bool kShift = kR >= 32;
-    static constexpr int kThreads = 512;                           // softmax, converters; producer, two issuers, an idle warp
-    static constexpr int kRegsSoft = kR >= 64 ? 176 : 152, kRegsConv = kR >= 64 ? 88 : 104, kRegsRest = kR >= 64 ? 72 : 104;
-    static_assert(2 * kRegsSoft + kRegsConv + kRegsRest <= 65536 / 128, "the block's registers");
+    static constexpr int kThreads = 256 + 128 * kGroups + 128;     // softmax, converters; producer, two issuers, an idle warp
+    static constexpr int kRegs = kGroups == 2 ? 96 : 128;
+    static constexpr int kRegsSoft = kGroups == 2 ? 120 : kR >= 64 ? 176 : 152, kRegsConv = kGroups == 2 ? 80 : kR >= 64 ? 88 : 104,
+                         kRegsRest = kGroups == 2 ? 80 : kR >= 64 ? 72 : 104;
+    static_assert(2 * kRegsSoft + kGroups * kRegsConv + kRegsRest <= kThreads / 128 * kRegs, "the block's registers");
     static constexpr int kND = kR <= 64 ? 4 : 2;                   // units in flight
     static constexpr int kNC = kTurns ? kR : kR / 2;               // columns of a softmax thread
     static constexpr int kNS = kTurns ? 4 : 8;                     // softmax warps of a tile
@@ -189,7 +196,7 @@ struct TreeCtrl {
     alignas(16) float up[2][C::kTurns ? kR : 4];
     alignas(16) float2 part[C::kTurns ? kR : 2];
     uint32_t poison[C::kND][kTreePoison][4];                       // tokens whose V holds NaN or infinities
-    int64_t scan[16];                                             // one per warp
+    int64_t scan[20];                                             // one per warp
     int64_t total, off0;
     int32_t r0;
     uint32_t tmem;
@@ -218,19 +225,16 @@ struct Ring {                                  // a buffer of a ring and the par
     }
 };
 
-// Waits for a phase.  After kTreeWaitNs without it the call has failed: that is recorded, and
-// from then on no wait of the block waits, so that it ends soon, with outputs that are not
-// valid.  (The plain test sleeps in hardware for a while; the form with a time hint is a loop
-// of its own that takes issue slots from the warps that work.)
+// Waits for a phase.  After kTreeTests tests without it (each sleeps in hardware for a while;
+// some seconds in all) the call has failed: that is recorded, and from then on no wait of the
+// block waits, so that it ends soon, with outputs that are not valid.
 __device__ __forceinline__ void tree_wait(uint32_t bar, uint32_t parity, volatile int32_t *dead, uint32_t *err) {
-    if (mbar_try_wait(bar, parity)) return;
-    uint64_t t0 = 0;
+    if (__builtin_expect(mbar_try_wait(bar, parity), 1)) return;
+    int left = kTreeTests;
 #pragma unroll 1
-    for (uint32_t i = 1; !mbar_try_wait(bar, parity); ++i) {
-        if ((i & 255u) == 0) {
-            const uint64_t now = globaltimer_ns();
-            if (t0 == 0) t0 = now;
-            if (now - t0 > kTreeWaitNs) {
+    while (!mbar_try_wait(bar, parity)) {
+        if (__builtin_expect((--left & 0xFFF) == 0, 0)) {
+            if (left <= 0) {
                 *dead = 1;
                 atomicOr(err, FKV_DEVERR_TIMEOUT);
             }
@@ -509,7 +513,7 @@ tree_attn_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmK, co
     const uint32_t base = smem_u32(smem);
     const uint32_t sQ = base, sP = base + C::kOffP, sV16 = base + C::kOffV16, sK = base + C::kOffK, sV = base + C::kOffV;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    constexpr int kConvW = 8, kProdW = 12, kMmaW = kProdW + 1, kMmaW2 = kProdW + 2;
+    constexpr int kConvW = 8, kProdW = 8 + 4 * C::kGroups, kMmaW = kProdW + 1, kMmaW2 = kProdW + 2;
     volatile int32_t *dead = &ct.dead;
     auto bar = [&](uint64_t &b) { return smem_u32(&b); };
     auto wait = [&](uint64_t &b, uint32_t parity) { tree_wait(smem_u32(&b), parity, dead, p.err); };
@@ -526,7 +530,7 @@ tree_attn_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmK, co
         for (int i = 0; i < C::kNP; ++i) mbar_init(bar(ct.pfull[i]), C::kNS), mbar_init(bar(ct.pempty[i]), 1);
         mbar_init(bar(ct.qfull), 4), mbar_init(bar(ct.qempty), 1), mbar_init(bar(ct.oempty), 8), mbar_init(bar(ct.drained[0]), 1), mbar_init(bar(ct.drained[1]), 1);
         for (int i = 0; i < C::kND; ++i)
-            mbar_init(bar(ct.dfull[i]), 1), mbar_init(bar(ct.dempty[i]), 8 + 4 + 2), mbar_init(bar(ct.cfull[i]), 4);
+            mbar_init(bar(ct.dfull[i]), 1), mbar_init(bar(ct.dempty[i]), 8 + 4 * C::kGroups + 2), mbar_init(bar(ct.cfull[i]), 4);
         ct.dead = 0;
         ct.r0 = p.batch;
         fence_mbar_init();
@@ -771,12 +775,13 @@ tree_attn_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmK, co
         __syncwarp();
         if (elect_one()) umma_commit(bar(drained));
         __syncwarp();
-        mbar_wait_bounded(bar(drained), 0, kTreeWaitNs);
+        mbar_wait_bounded(bar(drained), 0, kTreeDrainNs);
         }
     } else if (warp >= kConvW) {
         // ==== converters ====
         if constexpr (C::kShift) regs_down<C::kRegsConv>();
-        const int ctid = tid - 256, cw = ctid >> 5;
+        const int ctid = tid & 127, cw = ctid >> 5;
+        const bool do_k = C::kGroups == 1 || tid < 384, do_v = C::kGroups == 1 || tid >= 384;
         const uint32_t tlane = static_cast<uint32_t>(32 * cw) << 16;
         Ring d, k, kb, v, vb;
         uint32_t nu = 0;
@@ -784,7 +789,7 @@ tree_attn_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmK, co
             wait(ct.dfull[d.i], d.ph);
             const TreeUnit u = ct.unit[d.i];
             if (u.te < 0 || *dead) break;
-            {
+            if (do_k) {
                 // ---- the unit's Q ----
                 wait(ct.qempty, (nu & 1) ^ 1);
                 constexpr int kU = kR / 8 < 8 ? kR / 8 : 8;
@@ -837,7 +842,7 @@ tree_attn_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmK, co
             ++nu;
             int odd_tiles = 0;
             for (int i = u.tb; i < u.te; ++i) {
-                if constexpr (C::kConv) {
+                if (C::kConv && do_k) {
                     // ---- K: f16 rows in tensor memory ----
                     wait(ct.kfull[k.i], k.ph);
                     wait(ct.k16empty[kb.i], kb.ph ^ 1);
@@ -858,13 +863,13 @@ tree_attn_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmK, co
                     k.template next<C::kNK>();
                     kb.template next<2>();
                 }
-                {
+                if (do_v) {
                     // ---- V: f16 in tensor memory, or rows in an operand buffer; BF16 as it lies ----
                     wait(ct.vfull[v.i], v.ph);
                     const uint32_t t0 = tile_at(u, i), end = tile_end(u, i), n = end > t0 ? end - t0 : 0;
                     const uint32_t src = sV + v.i * C::kStageB;
                     const bool whole = tile_whole(u, p, t0);
-                    if (!whole) {
+                    if (__builtin_expect(!whole, 0)) {
                         if (clean_v<kKv>(src, ctid, static_cast<uint32_t>(ctid) < n)) {
                             atomicOr(&ct.poison[d.i][min(odd_tiles, kTreePoison - 1)][ctid >> 5], 1u << (ctid & 31));
                             *const_cast<volatile int32_t *>(&ct.unit[d.i].odd) = 1;
@@ -897,7 +902,7 @@ tree_attn_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmK, co
             d.template next<C::kND>();
         }
         // ---- rows of requests without work ----
-        {
+        if (do_k) {
             __syncwarp();
             for (int r = blockIdx.x; r < p.batch; r += gridDim.x) {
                 const TreeRequest q = tree_request(p, r);
@@ -938,7 +943,8 @@ tree_attn_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmK, co
             for (int i = kTurns ? u.tb + static_cast<int>((g ^ turn) & 1) : u.tb; i < u.te; i += kTurns ? 2 : 1) {
                 const uint32_t t0 = tile_at(u, i);
                 const bool whole = tile_whole(u, p, t0);
-                const uint64_t see = whole ? ~0ull : seen_by<kNC>(p, u, col0, t0 + tok);
+                uint64_t see = ~0ull;
+                if (__builtin_expect(!whole, 0)) see = seen_by<kNC>(p, u, col0, t0 + tok);
                 wait(ct.sfull[sb], sph);
                 umma_fence_after();
                 const uint32_t ts = tmem + tlane + C::kTmS + sb * kR + col0;
@@ -962,7 +968,7 @@ tree_attn_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmK, co
                         const float2 e = unpack2(a), f = unpack2(b);
                         x[j] = e.x, x[j + 1] = e.y, x[j + 2] = f.x, x[j + 3] = f.y;
                     }
-                    if (!whole) {
+                    if (__builtin_expect(!whole, 0)) {
                         asm volatile("" ::: "memory");             // a branch: as selects every tile would pay for them
 #pragma unroll
                         for (int j = 0; j < kNC; ++j)
@@ -975,7 +981,7 @@ tree_attn_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmK, co
 #pragma unroll
                     for (int j = 4; j < kNC; ++j) m4[j & 3] = fmaxf(m4[j & 3], x[j]);
                     const float most = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
-                    if (!group_any(barrier, most > kTreeMost) || tries == 4) break;
+                    if (__builtin_expect(!group_any(barrier, most > kTreeMost) || tries == 4, 1)) break;
                     // ---- move the references of the columns that need it ----
                     const int buf = kTurns ? g : 0;
                     if (had) wait(ct.pempty[buf], pph ^ 1);                      // the sums so far are complete
@@ -1168,7 +1174,7 @@ tree_attn_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmK, co
                     if (had1) v = fmaf(z[j], f.y, v);
                     y[j] = !cut && f.x == 0.f && f.y == 0.f ? 0.f : v;
                 }
-                if (anyodd && !wrong) {
+                if (__builtin_expect(anyodd && !wrong, 0)) {
                     // NaN and infinities of V that not every row sees: left out of the product, here for those who do
                     int k = 0;
                     for (int i = u.tb; i < u.te; ++i) {
