@@ -34,9 +34,6 @@
 #include "fp4_row.cuh"
 #include "umma.cuh"
 
-#ifndef FKV_TWO
-#define FKV_TWO 32
-#endif
 namespace fkv {
 
 constexpr int kTreeMaxWords = 4;               // 64-bit words of a row's mask
@@ -119,7 +116,7 @@ struct TreeUnit {
     int32_t tok0, ntok;                        // the rows' tokens
     int32_t ctx, len;
     int32_t start, sink_tiles, head;
-    int32_t full_lo;                           // the first position that every row sees
+    int32_t whole[3];                          // tiles [0, whole[0]) and [whole[1], whole[2]) are seen by every row
     int32_t row, h;                            // first page-table entry, KV head
     int32_t slot;                              // of its partial sums; -1: the whole unit is here
     int32_t bad;                               // a page outside the pool
@@ -129,12 +126,8 @@ __device__ __forceinline__ uint32_t tile_at(const TreeUnit &u, int i) {
     return i < u.sink_tiles ? static_cast<uint32_t>(i) * kTreeTok : u.start + static_cast<uint32_t>(i - u.sink_tiles) * kTreeTok;
 }
 __device__ __forceinline__ uint32_t tile_end(const TreeUnit &u, int i) { return i < u.sink_tiles ? u.head : u.len; }
-// Whether every row sees every token of the tile at t0.
-__device__ __forceinline__ bool tile_whole(const TreeUnit &u, const TreeParams &p, uint32_t t0) {
-    const uint32_t t1 = t0 + kTreeTok;
-    return t1 <= static_cast<uint32_t>(u.ctx) &&
-           (!p.window || t0 >= static_cast<uint32_t>(u.full_lo) || t1 <= static_cast<uint32_t>(p.sinks));
-}
+// Whether every row sees every token of tile i.
+__device__ __forceinline__ bool tile_whole(const TreeUnit &u, int i) { return i < u.whole[0] || (i >= u.whole[1] && i < u.whole[2]); }
 
 // ---------------------------------------------------------------------------
 // shared memory
@@ -158,7 +151,7 @@ struct TreeCfg {
     static constexpr int kPB = kR <= 32 ? 16384 : kParts * kPW;    // a weight buffer
     static constexpr int kQB = kR * 256;
     static constexpr int kV16 = kConv && !kVT ? 32768 : 0;
-        static constexpr int kGroups = kConv && kR <= FKV_TWO ? 2 : 1;      // converter groups: K and V, or one for both
+        static constexpr int kGroups = kConv && kR <= 32 ? 2 : 1;      // converter groups: K and V, or one for both
     // Softmax warps with many columns take registers of the others: of a thread, at launch, then
     // of the three kinds of warps (no more in all than at launch; whole groups of four warps).
     static constexpr bool kShift = kR >= 32;
@@ -187,7 +180,8 @@ struct TreeCtrl {
     uint64_t qfull, qempty, oempty, drained[2];
     uint64_t dfull[C::kND], dempty[C::kND], cfull[C::kND];
     TreeUnit unit[C::kND];
-    alignas(16) float colscale[C::kND][kR];                        // a logit in log2 units per unit of S
+    float colscale[C::kND];                                        // a logit in log2 units per unit of S
+    uint32_t qmax[C::kND];                                         // the largest |q| of the unit, as bf16 bits
     // [unit's parity][group] where the groups take turns: the columns' references, negated, and
     // their warps' sums (or maxima); a moved reference's factor; the factors of the two groups' sums
     static constexpr int kU = C::kTurns ? 2 : 1;
@@ -207,7 +201,7 @@ template <int kKv, int kR>
 constexpr int tree_smem() {
     using C = TreeCfg<kKv, kR>;
     using T = TreeCtrl<kKv, kR>;
-    static_assert(offsetof(T, colscale) % 16 == 0 && offsetof(T, ref) % 16 == 0 && offsetof(T, up) % 16 == 0 && offsetof(T, part) % 16 == 0 && C::kOffCtrl % 16 == 0, "read four at a time");
+    static_assert(offsetof(T, ref) % 16 == 0 && offsetof(T, up) % 16 == 0 && offsetof(T, part) % 16 == 0 && C::kOffCtrl % 16 == 0, "read four at a time");
     static_assert(C::kOffP % 1024 == 0 && C::kOffV16 % 1024 == 0 && C::kOffK % 1024 == 0 && C::kOffV % 1024 == 0,
                   "swizzled buffers start on 1024 bytes");
     return TreeCfg<kKv, kR>::kOffCtrl + static_cast<int>((sizeof(TreeCtrl<kKv, kR>) + 15) / 16 * 16);
@@ -371,58 +365,75 @@ __device__ __forceinline__ void convert_v(uint32_t stage, uint32_t dst, int tok)
 }
 
 // The V rows of a stage as f16 into tensor memory: dims on lanes, two tokens a column, from
-// column `dst` (of this warp's 32 lanes).  Thread l takes dims 4 (l / 4) .. + 3 of the warp's
-// 32 and tokens 8k + 2 (l % 4) + {0, 1}, the places of the .16x128b store: lane 16b + 8h + r
-// holds dim 4r + 2b + h.  Two tokens' codes are interleaved before they are converted, so a
-// converted pair is one dim of both.
+// column `dst` (of this warp's 32 lanes, dims 32 cw ..).  Thread l holds, of tokens 8k + 2 (l % 4)
+// and the next one, the places of the .16x128b store: register 2k of the lower (upper) 16 lanes
+// is lane l / 4, register 2k + 1 lane 8 + l / 4.  The two tokens' codes are interleaved before
+// they are converted, so that a converted pair is one dim of both.
+// FP8: a transposing load brings two dims of both tokens; lane 16b + 8h + r is dim 16b + 2r + h.
+// FP4: rows of 72 bytes cannot be loaded so (every other one starts in the middle of 16
+// bytes): two bytes a token, four dims; lane 16b + 8h + r is dim 4r + 2b + h.
 template <int kKv>
 __device__ __forceinline__ void convert_v_tmem(uint32_t stage, uint32_t dst, int cw, int lane) {
-    const int g = lane >> 2, t = lane & 3;
-    uint32_t r0, r1;                                               // this thread's codes of tokens 2t and 2t + 1
-    if (kKv == FKV_KV_FP8_E4M3) {
-        const int c = 2 * cw + (g >> 2);
-        r0 = stage + 2 * t * 128 + ((c ^ (2 * t)) << 4) + 4 * (g & 3);
-        r1 = stage + (2 * t + 1) * 128 + ((c ^ (2 * t + 1)) << 4) + 4 * (g & 3);
-    } else {
-        r0 = stage + 2 * t * kFp4Row + 16 * cw + 2 * g;
-        r1 = r0 + kFp4Row;
+    if constexpr (kKv == FKV_KV_FP8_E4M3) {
+        const uint32_t row = stage + lane * 128;                   // of 32 tokens at a time
+#pragma unroll 1
+        for (int hf = 0; hf < 2; ++hf) {
+            uint32_t in[2][8];
+#pragma unroll
+            for (int b = 0; b < 2; ++b) {
+                const uint32_t at = row + hf * 8192 + (((2 * cw + b) ^ (lane & 7)) << 4);
+#pragma unroll
+                for (int q = 0; q < 2; ++q)
+                    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+                                 : "=r"(in[b][4 * q]), "=r"(in[b][4 * q + 1]), "=r"(in[b][4 * q + 2]), "=r"(in[b][4 * q + 3])
+                                 : "r"(at + q * 4096));
+            }
+#pragma unroll
+            for (int b = 0; b < 2; ++b) {
+                uint32_t f[16];
+#pragma unroll
+                for (int k = 0; k < 8; ++k) e4m3x4_to_f16(prmt(in[b][k], 0u, 0x3120u), f[2 * k], f[2 * k + 1]);
+                tmem_store_rows(dst + (static_cast<uint32_t>(16 * b) << 16) + 32 * hf, f);
+            }
+        }
+        return;
     }
-    const uint32_t s0 = stage + 2 * t * kFp4Row + kFp4Codes + 2 * cw + (g >> 2);
+    const int g = lane >> 2, t = lane & 3;
+    const uint32_t r0 = stage + 2 * t * kFp4Row + 16 * cw + 2 * g, s0 = stage + 2 * t * kFp4Row + kFp4Codes + 2 * cw + (g >> 2);
 #pragma unroll 1
     for (int hf = 0; hf < 2; ++hf) {
         uint32_t a[16], b[16], in[8][2], sin[8][2];                // all loads on their way before one word is converted
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
-            const int row = 64 * hf + 8 * k;
-            if (kKv == FKV_KV_FP8_E4M3) {
-                in[k][0] = ld_shared_u32(r0 + row * 128), in[k][1] = ld_shared_u32(r1 + row * 128);
-            } else {
-                in[k][0] = ld_shared_u16(r0 + row * kFp4Row), in[k][1] = ld_shared_u16(r1 + row * kFp4Row);
-                sin[k][0] = ld_shared_u8(s0 + row * kFp4Row), sin[k][1] = ld_shared_u8(s0 + (row + 1) * kFp4Row);
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                in[k][j] = ld_shared_u16(r0 + (64 * hf + 8 * k + j) * kFp4Row);
+                sin[k][j] = ld_shared_u8(s0 + (64 * hf + 8 * k + j) * kFp4Row);
             }
         }
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
-            const uint32_t w[2] = {in[k][0], in[k][1]};
-            if (kKv == FKV_KV_FP8_E4M3) {
-                const uint32_t x = prmt(w[0], w[1], 0x5140), y = prmt(w[0], w[1], 0x7362);
-                e4m3x4_to_f16(x, a[2 * k], a[2 * k + 1]);
-                e4m3x4_to_f16(y, b[2 * k], b[2 * k + 1]);
-            } else {
-                // byte 0: dim 0 of both tokens, byte 1: dim 2; and dims 1 and 3
-                const uint32_t even = (w[0] & 0x0F0Fu) | ((w[1] << 4) & 0xF0F0u), odd = ((w[0] >> 4) & 0x0F0Fu) | (w[1] & 0xF0F0u);
-                uint32_t f[4];
-                e2m1x8_to_f16(even | (odd << 16), f);
-                const uint32_t s = e4m3x2_to_f16x2(static_cast<uint16_t>(sin[k][0] | (sin[k][1] << 8)));
-                a[2 * k] = mul_f16x2(f[0], s);
-                a[2 * k + 1] = mul_f16x2(f[2], s);
-                b[2 * k] = mul_f16x2(f[1], s);
-                b[2 * k + 1] = mul_f16x2(f[3], s);
-            }
+            // byte 0: dim 0 of both tokens, byte 1: dim 2; and dims 1 and 3
+            const uint32_t w0 = in[k][0], w1 = in[k][1];
+            const uint32_t even = (w0 & 0x0F0Fu) | ((w1 << 4) & 0xF0F0u), odd = ((w0 >> 4) & 0x0F0Fu) | (w1 & 0xF0F0u);
+            uint32_t f[4];
+            e2m1x8_to_f16(even | (odd << 16), f);
+            const uint32_t s = e4m3x2_to_f16x2(static_cast<uint16_t>(sin[k][0] | (sin[k][1] << 8)));
+            a[2 * k] = mul_f16x2(f[0], s);
+            a[2 * k + 1] = mul_f16x2(f[2], s);
+            b[2 * k] = mul_f16x2(f[1], s);
+            b[2 * k + 1] = mul_f16x2(f[3], s);
         }
         tmem_store_rows(dst + 32 * hf, a);
         tmem_store_rows(dst + (16u << 16) + 32 * hf, b);
     }
+}
+// The dim of a lane of O (within its warp's 32).
+template <int kKv, bool kVT>
+__device__ __forceinline__ int dim_of_lane(int lane) {
+    if (!kVT) return lane;
+    const int b = lane >> 4, h = (lane >> 3) & 1, r = lane & 7;
+    return kKv == FKV_KV_FP8_E4M3 ? 16 * b + 2 * r + h : 4 * r + 2 * b + h;
 }
 
 // A V row in its stage, of a tile that not every row sees whole: rows of no token, NaN and
@@ -614,13 +625,16 @@ tree_attn_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmK, co
                 u.start = sp.start;
                 u.sink_tiles = sp.sink_tiles;
                 u.head = sp.head;
-                const int64_t far = static_cast<int64_t>(cur.len) - p.window;
-                u.full_lo = p.window && far > 0 ? static_cast<int32_t>(far) : 0;
+                // whole tiles: of committed tokens, and within every row's window or among the first tokens
+                const int32_t far = p.window && cur.len > p.window ? cur.len - p.window : 0;      // the deepest row's first token, at most
+                u.whole[2] = u.ctx > sp.start ? sp.sink_tiles + (u.ctx - sp.start) / kTreeTok : 0;
+                u.whole[1] = sp.sink_tiles + (far > sp.start ? (far - sp.start + kTreeTok - 1) / kTreeTok : 0);
+                u.whole[0] = p.window ? min(sp.sink_tiles ? sp.sink_tiles : u.whole[2], min(p.sinks, u.ctx) / kTreeTok) : 0;
                 u.row = cur.row;
                 u.h = h;
                 u.slot = tb == 0 && te == sp.tiles ? -1 : 2 * static_cast<int>(blockIdx.x) + (tb == 0 ? 1 : 0);
                 u.bad = u.odd = 0;
-                if (lane == 0) ct.unit[d.i] = u;
+                if (lane == 0) ct.unit[d.i] = u, ct.qmax[d.i] = 0;
                 for (int i = lane; i < 4 * kTreePoison; i += 32) (&ct.poison[d.i][0][0])[i] = 0;
                 __syncwarp();
                 if (lane == 0) mbar_arrive(bar(ct.dfull[d.i]));
@@ -792,12 +806,10 @@ tree_attn_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmK, co
             if (do_k) {
                 // ---- the unit's Q ----
                 wait(ct.qempty, (nu & 1) ^ 1);
-                constexpr int kU = kR / 8 < 8 ? kR / 8 : 8;
+                constexpr int kU = kR / 8 < 8 ? kR / 8 : 8;        // rows of a thread at a time
                 const int c16 = ctid & 15;
-                const float ks = C::kConv ? __ldg(p.k_scale + u.h) : 1.f;
-#pragma unroll
-                for (int r8 = 0; r8 < kR / 8; r8 += kU) {
-                    uint4 x[kU];
+                uint4 x[kU];
+                auto load = [&](int r8) {
 #pragma unroll
                     for (int i = 0; i < kU; ++i) {
                         const int row = (r8 + i) * 8 + (ctid >> 4), tk = row / p.group;
@@ -806,32 +818,50 @@ tree_attn_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmK, co
                             x[i] = __ldg(reinterpret_cast<const uint4 *>(
                                              p.q + (static_cast<int64_t>(u.tok0 + tk) * p.hq + u.h * p.group + (row - tk * p.group)) * 128) + c16);
                     }
+                };
+                float up = 1.f, cs = p.scale_log2;
+                if (C::kConv) {
+                    // f16 with a power of two that puts the unit's largest finite element into [2^14, 2^15): elements
+                    // down to 2^-32 of it stay exact
+                    uint32_t big = 0;
+#pragma unroll 1
+                    for (int r8 = 0; r8 < kR / 8; r8 += kU) {
+                        load(r8);
+#pragma unroll
+                        for (int i = 0; i < kU; ++i) {
+                            const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+#pragma unroll
+                            for (int j = 0; j < 4; ++j) {
+                                const uint32_t lo = w[j] & 0x7FFFu, hi = (w[j] >> 16) & 0x7FFFu;
+                                big = max(big, max(lo < 0x7F80u ? lo : 0u, hi < 0x7F80u ? hi : 0u));
+                            }
+                        }
+                    }
+                    big = __reduce_max_sync(kAll, big);
+                    if (lane == 0) atomicMax(&ct.qmax[d.i], big);
+                    group_sync(4);
+                    int e = static_cast<int>(*const_cast<volatile uint32_t *>(&ct.qmax[d.i]) >> 7);
+                    e = max(e == 0 ? 141 : e, 15);
+                    up = __uint_as_float(static_cast<uint32_t>(268 - e) << 23);
+                    cs = cs * __ldg(p.k_scale + u.h) * __uint_as_float(static_cast<uint32_t>(e - 14) << 23);
+                }
+#pragma unroll 1
+                for (int r8 = 0; r8 < kR / 8; r8 += kU) {
+                    if (!C::kConv || kU < kR / 8) load(r8);
 #pragma unroll
                     for (int i = 0; i < kU; ++i) {
                         const int row = (r8 + i) * 8 + (ctid >> 4);
-                        float cs = p.scale_log2;
                         if (C::kConv) {
-                            // f16 with a power of two per row that puts its largest element into [2^14, 2^15)
                             uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
-                            uint32_t big = 0;
-#pragma unroll
-                            for (int j = 0; j < 4; ++j) big = max(big, max(w[j] & 0x7FFFu, (w[j] >> 16) & 0x7FFFu));
-#pragma unroll
-                            for (int o = 1; o < 16; o <<= 1) big = max(big, __shfl_xor_sync(kAll, big, o));
-                            int e = static_cast<int>(big >> 7);
-                            if (e == 0 || e == 255) e = 141;       // zeros, infinities and NaN stay what they are
-                            e = max(e, 15);
-                            const float up = __uint_as_float(static_cast<uint32_t>(268 - e) << 23), down = __uint_as_float(static_cast<uint32_t>(e - 14) << 23);
-                            cs = cs * ks * down;
 #pragma unroll
                             for (int j = 0; j < 4; ++j)
                                 w[j] = pack_f16x2(__uint_as_float(w[j] << 16) * up, __uint_as_float(w[j] & 0xFFFF0000u) * up);
                             x[i] = make_uint4(w[0], w[1], w[2], w[3]);
                         }
                         st_shared_v4(sQ + (c16 >> 3) * (kR * 128) + row * 128 + (((c16 & 7) ^ (row & 7)) << 4), x[i]);
-                        if (c16 == 0) ct.colscale[d.i][row] = cs;
                     }
                 }
+                if (ctid == 0) ct.colscale[d.i] = cs;
                 fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0) {
@@ -866,15 +896,14 @@ tree_attn_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmK, co
                 if (do_v) {
                     // ---- V: f16 in tensor memory, or rows in an operand buffer; BF16 as it lies ----
                     wait(ct.vfull[v.i], v.ph);
-                    const uint32_t t0 = tile_at(u, i), end = tile_end(u, i), n = end > t0 ? end - t0 : 0;
                     const uint32_t src = sV + v.i * C::kStageB;
-                    const bool whole = tile_whole(u, p, t0);
+                    const bool whole = tile_whole(u, i);
                     if (__builtin_expect(!whole, 0)) {
-                        if (clean_v<kKv>(src, ctid, static_cast<uint32_t>(ctid) < n)) {
+                        if (clean_v<kKv>(src, ctid, tile_at(u, i) + ctid < tile_end(u, i))) {
                             atomicOr(&ct.poison[d.i][min(odd_tiles, kTreePoison - 1)][ctid >> 5], 1u << (ctid & 31));
                             *const_cast<volatile int32_t *>(&ct.unit[d.i].odd) = 1;
                         }
-                        if (C::kConv) group_sync(3 + 1);           // the converters: a warp reads other warps' tokens
+                        if (C::kConv) group_sync(5);               // a warp reads tokens of other warps too
                         ++odd_tiles;
                     }
                     constexpr int kF = C::kConv ? kKv : FKV_KV_FP8_E4M3;
@@ -938,13 +967,13 @@ tree_attn_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmK, co
             for (int j = 0; j < kNC; ++j) sum[j] = 0.f;
             wait(ct.cfull[d.i], d.ph);
             group_sync(barrier);
-            const uint32_t scs = smem_u32(ct.colscale[d.i]) + 4 * col0;
+            const float cs = *const_cast<volatile float *>(&ct.colscale[d.i]);
+            const uint64_t cs2 = pack2(cs, cs);
             bool had = false;                                      // a tile of this unit
             for (int i = kTurns ? u.tb + static_cast<int>((g ^ turn) & 1) : u.tb; i < u.te; i += kTurns ? 2 : 1) {
-                const uint32_t t0 = tile_at(u, i);
-                const bool whole = tile_whole(u, p, t0);
+                const bool whole = tile_whole(u, i);
                 uint64_t see = ~0ull;
-                if (__builtin_expect(!whole, 0)) see = seen_by<kNC>(p, u, col0, t0 + tok);
+                if (__builtin_expect(!whole, 0)) see = seen_by<kNC>(p, u, col0, tile_at(u, i) + tok);
                 wait(ct.sfull[sb], sph);
                 umma_fence_after();
                 const uint32_t ts = tmem + tlane + C::kTmS + sb * kR + col0;
@@ -956,8 +985,7 @@ tree_attn_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmK, co
                     for (int c = 0; c < kNC; c += kLd) tmem_load(ts + c, *reinterpret_cast<float(*)[kLd]>(&x[c]));
 #pragma unroll
                     for (int j = 0; j < kNC; j += 4) {
-                        const float4 c4 = ld_shared_f4(scs + 4 * j);
-                        uint64_t a = mul2(pack2(x[j], x[j + 1]), pack2(c4.x, c4.y)), b = mul2(pack2(x[j + 2], x[j + 3]), pack2(c4.z, c4.w));
+                        uint64_t a = mul2(pack2(x[j], x[j + 1]), cs2), b = mul2(pack2(x[j + 2], x[j + 3]), cs2);
                         if (kLess) {
                             // rounded products, as the references': a fused one would leave their rounding, up to 2^9
                             // at logits of 1e10, in the exponent
@@ -1036,7 +1064,7 @@ tree_attn_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmK, co
                             tmem_load(ts + c, y);
 #pragma unroll
                             for (int j = 0; j < 8; ++j) {
-                                float z = __fmul_rn(y[j], ct.colscale[d.i][col0 + c + j]);
+                                float z = __fmul_rn(y[j], cs);
                                 if (!((see >> (c + j)) & 1)) z = -INFINITY;
                                 const int key = __float_as_int(z) ^ ((__float_as_int(z) >> 31) & 0x7FFFFFFF);   // ordered as the floats
                                 const int top = __reduce_max_sync(kAll, key);
@@ -1095,9 +1123,12 @@ tree_attn_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmK, co
                         uint32_t hi[4], lo[4];
 #pragma unroll
                         for (int b = 0; b < 4; ++b) {
-                            const float e = x[j + 2 * b], f = x[j + 2 * b + 1];
-                            hi[b] = pack_bf16x2(e, f);
-                            lo[b] = pack_bf16x2(e - __uint_as_float(hi[b] << 16), f - __uint_as_float(hi[b] & 0xFFFF0000u));
+                            // the first word cut off, the second rounded: 2^-17 of a weight are left out
+                            const uint32_t e = __float_as_uint(x[j + 2 * b]), f = __float_as_uint(x[j + 2 * b + 1]);
+                            hi[b] = prmt(e, f, 0x7632);
+                            const float2 r = unpack2(add2(pack2(x[j + 2 * b], x[j + 2 * b + 1]),
+                                                          pack2(__uint_as_float((e & 0xFFFF0000u) ^ 0x80000000u), __uint_as_float((f & 0xFFFF0000u) ^ 0x80000000u))));
+                            lo[b] = pack_bf16x2(r.x, r.y);
                         }
                         st_shared_v4(at, make_uint4(hi[0], hi[1], hi[2], hi[3]));
                         st_shared_v4(C::kPW < 128 ? sPw + (((j >> 3) + C::kPW / 16) ^ (tok & 7)) * 16 : at + C::kPW, make_uint4(lo[0], lo[1], lo[2], lo[3]));
@@ -1156,7 +1187,7 @@ tree_attn_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmK, co
             const bool both = u.te - u.tb > 1;                     // which groups had tiles
             const bool had0 = !kTurns || both || had == (g == 0), had1 = kTurns && (both || had == (g == 1));
             // the dim of this thread's lane (convert_v_tmem)
-            const int dim = 32 * wq + (C::kVT ? 4 * (lane & 7) + 2 * (lane >> 4) + ((lane >> 3) & 1) : lane);
+            const int dim = 32 * wq + dim_of_lane<kKv, C::kVT>(lane);
             const bool anyodd = *const_cast<volatile int32_t *>(&ct.unit[d.i].odd) != 0;
             int tk = c0 / p.group, hr = c0 - tk * p.group;         // of the column: token and query head
             __nv_bfloat16 *out = p.out + (static_cast<int64_t>(u.tok0 + tk) * p.hq + u.h * p.group + hr) * 128 + dim;
@@ -1179,7 +1210,7 @@ tree_attn_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmK, co
                     int k = 0;
                     for (int i = u.tb; i < u.te; ++i) {
                         const uint32_t t0 = tile_at(u, i);
-                        if (tile_whole(u, p, t0)) continue;
+                        if (tile_whole(u, i)) continue;
                         for (int b = 0; b < kTreeTok; ++b) {
                             if (!((*const_cast<volatile uint32_t *>(&ct.poison[d.i][min(k, kTreePoison - 1)][b >> 5]) >> (b & 31)) & 1)) continue;
                             const float add = odd_value<kKv>(p, u, t0 + b, dim);
