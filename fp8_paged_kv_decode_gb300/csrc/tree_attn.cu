@@ -31,103 +31,15 @@
 #include <mutex>
 #include <type_traits>
 
-#include "fp4_row.cuh"
+#include "tree_attn.cuh"
 #include "umma.cuh"
 
 namespace fkv {
 
-constexpr int kTreeMaxWords = 4;               // 64-bit words of a row's mask
 constexpr int kTreeTok = 128;                  // tokens of a tile
 constexpr int kTreePoison = 10;                // tiles of a unit that hold tokens not seen by every row, at most (9)
-constexpr float kTreeTop = 10.f, kTreeMost = 15.9f;   // log2 of a moved reference's largest weight, and of any weight
-constexpr float kTreeNone = -3e38f;            // the reference of a column that has seen nothing
 constexpr int kTreeTests = 1 << 24;
 constexpr uint64_t kTreeDrainNs = 2000000000ull;
-constexpr uint32_t kAll = 0xffffffffu;
-
-struct TreeParams {
-    const __nv_bfloat16 *q;
-    const uint8_t *k_cache, *v_cache;
-    const float *k_scale, *v_scale;
-    const int32_t *indptr, *indices, *seq_lens;
-    const int32_t *token_indptr;               // nullptr: one token a request
-    const uint64_t *mask;                      // nullptr: a row sees itself
-    const uint8_t *abort_mask;
-    __nv_bfloat16 *out;
-    uint32_t *err;
-    float *part_o;                             // [2 grid][kR][128] sums of units that are cut
-    float2 *part_ml;                           // [2 grid][kR] their references and weights' sums (sum < 0: a bad page)
-    int4 *joins;                               // [grid] the unit whose last part a CTA has: first CTA (-1: none), token, tokens, KV head
-    int64_t nnz;
-    int32_t batch, n_tokens, hq, hkv, group, pages, page_size, words, window, sinks;
-    float scale_log2;
-};
-
-// ---------------------------------------------------------------------------
-// geometry
-// ---------------------------------------------------------------------------
-struct TreeRequest {
-    int32_t t0, n, len, row;                   // first query token, drafted and all tokens, first page-table entry
-    bool live, rows;                           // has work; its rows are rows of q
-};
-
-__device__ __forceinline__ TreeRequest tree_request(const TreeParams &p, int r) {
-    TreeRequest q{};
-    if (r >= p.batch) return q;
-    int t0 = r, t1 = r + 1;
-    if (p.token_indptr) {
-        t0 = __ldg(p.token_indptr + r);
-        t1 = __ldg(p.token_indptr + r + 1);
-    }
-    const int32_t b = __ldg(p.indptr + r), e = __ldg(p.indptr + r + 1);
-    q.len = __ldg(p.seq_lens + r);
-    const bool alive = !p.abort_mask || __ldg(p.abort_mask + r) == 0;
-    q.t0 = t0;
-    q.row = b;
-    q.rows = t0 >= 0 && t1 >= t0 && t1 <= p.n_tokens;
-    q.n = q.rows ? t1 - t0 : 0;
-    q.live = q.n > 0 && alive && q.len >= q.n && q.n <= 64 * p.words && b >= 0 && e >= b && e <= p.nnz &&
-             static_cast<int64_t>(e - b) * p.page_size >= q.len;
-    return q;
-}
-
-// The tiles of a live request: those over the first tokens, if they lie apart, then those
-// from `start` on, the page of the first token that a row at depth 0 sees.
-struct TreeSpan {
-    int32_t start, sink_tiles, head, tiles;
-};
-__device__ __forceinline__ TreeSpan tree_span(const TreeParams &p, const TreeRequest &q) {
-    TreeSpan s{0, 0, 0, 0};
-    const int32_t ctx = q.len - q.n;
-    if (p.window && ctx >= p.window) {
-        const int32_t lo = ctx - p.window + 1;
-        s.start = lo - lo % p.page_size;
-        s.head = min(p.sinks, lo);
-        s.sink_tiles = (s.head + kTreeTok - 1) / kTreeTok;
-        if (s.start <= static_cast<int64_t>(s.sink_tiles) * kTreeTok) s = TreeSpan{0, 0, 0, 0};
-    }
-    s.tiles = s.sink_tiles + (q.len - s.start + kTreeTok - 1) / kTreeTok;
-    return s;
-}
-
-// What a CTA takes of a unit, from the producer to the others.
-struct TreeUnit {
-    int32_t tb, te;                            // its tiles; te < 0: there is no more work
-    int32_t tok0, ntok;                        // the rows' tokens
-    int32_t ctx, len;
-    int32_t start, sink_tiles, head;
-    int32_t whole[3];                          // tiles [0, whole[0]) and [whole[1], whole[2]) are seen by every row
-    int32_t row, h;                            // first page-table entry, KV head
-    int32_t slot;                              // of its partial sums; -1: the whole unit is here
-    int32_t bad;                               // a page outside the pool
-    int32_t odd;                               // NaN or infinities in V that not every row sees
-};
-__device__ __forceinline__ uint32_t tile_at(const TreeUnit &u, int i) {
-    return i < u.sink_tiles ? static_cast<uint32_t>(i) * kTreeTok : u.start + static_cast<uint32_t>(i - u.sink_tiles) * kTreeTok;
-}
-__device__ __forceinline__ uint32_t tile_end(const TreeUnit &u, int i) { return i < u.sink_tiles ? u.head : u.len; }
-// Whether every row sees every token of tile i.
-__device__ __forceinline__ bool tile_whole(const TreeUnit &u, int i) { return i < u.whole[0] || (i >= u.whole[1] && i < u.whole[2]); }
 
 // ---------------------------------------------------------------------------
 // shared memory
@@ -190,9 +102,7 @@ struct TreeCtrl {
     alignas(16) float up[2][C::kTurns ? kR : 4];
     alignas(16) float2 part[C::kTurns ? kR : 2];
     uint32_t poison[C::kND][kTreePoison][4];                       // tokens whose V holds NaN or infinities
-    int64_t scan[20];                                             // one per warp
-    int64_t total, off0;
-    int32_t r0;
+    TreeShares<C::kThreads, 1> shares;
     uint32_t tmem;
     int32_t dead;
 };
@@ -252,46 +162,12 @@ __device__ __forceinline__ bool both_any(bool x) {             // the same for b
 }
 __device__ __forceinline__ void group_sync(int id) { asm volatile("barrier.cta.sync %0, 128;" ::"r"(id) : "memory"); }
 
-__device__ __forceinline__ void st_shared_v4(uint32_t addr, uint4 v) {
-    asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
-}
-
 __device__ __forceinline__ uint32_t ld_shared_u16(uint32_t addr) {
     uint16_t v;
     asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(addr));
     return v;
 }
 
-// ---------------------------------------------------------------------------
-// which rows see a token
-// ---------------------------------------------------------------------------
-struct RowSight {
-    uint64_t word;                             // the row's mask word of the token asked for
-    int32_t lo;                                // its first committed token apart from the first ones
-};
-// Of drafted row `tok` (of the call), for tokens of mask word `w`.
-__device__ __forceinline__ RowSight row_sight(const TreeParams &p, const TreeUnit &u, int tok, int w) {
-    RowSight s{w == 0 ? 1ull : 0ull, 0};
-    int bits = 1;
-    if (p.mask) {
-        const uint64_t *m = p.mask + static_cast<int64_t>(tok) * p.words;
-        s.word = w < p.words ? __ldg(m + w) : 0ull;
-        if (p.window) {
-            bits = 0;
-            for (int i = 0; i < p.words; ++i) bits += __popcll(__ldg(m + i));
-        }
-    }
-    if (p.window) s.lo = static_cast<int32_t>(static_cast<int64_t>(u.ctx) + max(bits - 1, 0) - p.window + 1 > 0 ? static_cast<int64_t>(u.ctx) + max(bits - 1, 0) - p.window + 1 : 0);
-    return s;
-}
-__device__ __forceinline__ bool sees(const TreeParams &p, const TreeUnit &u, const RowSight &s, uint32_t t) {
-    if (t >= static_cast<uint32_t>(u.len)) return false;
-    if (t >= static_cast<uint32_t>(u.ctx)) return (s.word >> ((t - u.ctx) & 63)) & 1;
-    return !p.window || t < static_cast<uint32_t>(p.sinks) || t >= static_cast<uint32_t>(s.lo);
-}
-__device__ __forceinline__ int word_of(const TreeUnit &u, uint32_t t) {
-    return t >= static_cast<uint32_t>(u.ctx) ? static_cast<int>((t - u.ctx) >> 6) : 0;
-}
 // Bits of this group's columns whose rows see token t (rows past the unit's: unset).
 template <int kNC>
 __device__ __forceinline__ uint64_t seen_by(const TreeParams &p, const TreeUnit &u, int col0, uint32_t t) {
@@ -309,10 +185,6 @@ __device__ __forceinline__ uint64_t seen_by(const TreeParams &p, const TreeUnit 
 // ---------------------------------------------------------------------------
 // rows of the cache as f16 (this thread's token)
 // ---------------------------------------------------------------------------
-__device__ __forceinline__ void e4m3x4_to_f16(uint32_t w, uint32_t &lo, uint32_t &hi) {
-    lo = e4m3x2_to_f16x2(static_cast<uint16_t>(w & 0xFFFFu));
-    hi = e4m3x2_to_f16x2(static_cast<uint16_t>(w >> 16));
-}
 // 64 values (half `hf`) of the row in a K or V stage, as f16 pairs.
 template <int kKv>
 __device__ __forceinline__ void half_row(uint32_t stage, int tok, int hf, uint32_t (&f)[32]) {
@@ -436,62 +308,6 @@ __device__ __forceinline__ int dim_of_lane(int lane) {
     return kKv == FKV_KV_FP8_E4M3 ? 16 * b + 2 * r + h : 4 * r + 2 * b + h;
 }
 
-// A V row in its stage, of a tile that not every row sees whole: rows of no token, NaN and
-// infinities become zeros, since a weight of zero would not take them out of a product.
-// Returns whether there were NaN or infinities.  A pass of its own over these few tiles keeps
-// the conversions small: with both forms of them in the loop every tile paid for the tests
-// (64 requests, window of 4096: 173 us, 120 without).
-template <int kKv>
-__device__ __forceinline__ bool clean_v(uint32_t stage, int tok, bool valid) {
-    bool odd = false;
-    constexpr int kSteps = kKv == FKV_KV_BF16 ? 16 : 8;
-#pragma unroll 1
-    for (int c = 0; c < kSteps; ++c) {
-        if (kKv == FKV_KV_FP4) {
-            const uint32_t a = stage + tok * kFp4Row + 8 * c;
-            if (!valid) {
-                st_shared_v2_zero(a);
-                if (c == 0) st_shared_v2_zero(stage + tok * kFp4Row + kFp4Codes);
-            } else if ((ld_shared_u8(stage + tok * kFp4Row + kFp4Codes + c) & 0x7Fu) == 0x7Fu) {
-                odd = true;                                        // codes of zero under a scale of zero
-                asm volatile("st.shared.u8 [%0], %1;" ::"r"(stage + tok * kFp4Row + kFp4Codes + c), "r"(0u) : "memory");
-            }
-            continue;
-        }
-        const uint32_t a = stage + 16384 * (c >> 3) + tok * 128 + (((c & 7) ^ (tok & 7)) << 4);
-        const uint4 v = ld_shared_v4(a);
-        uint32_t w[4] = {v.x, v.y, v.z, v.w}, bad = 0;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            uint32_t m;                                            // the bits of what is no number
-            if (kKv == FKV_KV_BF16) m = ((w[j] & 0x7F80u) == 0x7F80u ? 0xFFFFu : 0u) | ((w[j] & 0x7F800000u) == 0x7F800000u ? 0xFFFF0000u : 0u);
-            else m = ((((w[j] & 0x7F7F7F7Fu) + 0x01010101u) >> 7) & 0x01010101u) * 0xFFu;
-            if (!valid) m = 0xFFFFFFFFu;
-            else odd |= m != 0;
-            bad |= m;
-            w[j] &= ~m;
-        }
-        if (bad) st_shared_v4(a, make_uint4(w[0], w[1], w[2], w[3]));
-    }
-    return odd;
-}
-
-// A V value that is NaN or infinite, as the cache holds it; else 0.
-template <int kKv>
-__device__ __forceinline__ float odd_value(const TreeParams &p, const TreeUnit &u, uint32_t t, int dim) {
-    const int64_t pg = __ldg(p.indices + u.row + t / p.page_size);
-    if (pg < 0 || pg >= p.pages) return 0.f;
-    const int64_t row = (pg * p.hkv + u.h) * p.page_size + t % p.page_size;
-    float v;
-    if (kKv == FKV_KV_BF16) {
-        v = __uint_as_float(static_cast<uint32_t>(reinterpret_cast<const uint16_t *>(p.v_cache)[row * 128 + dim]) << 16);
-    } else {
-        const uint32_t b = kKv == FKV_KV_FP8_E4M3 ? p.v_cache[row * 128 + dim] : p.v_cache[row * kFp4Row + kFp4Codes + dim / 16];
-        v = (b & 0x7Fu) == 0x7Fu ? __int_as_float(0x7FC00000) : 0.f;
-    }
-    return isfinite(v) ? 0.f : v;
-}
-
 // kN columns reduced over a warp's lanes: half of them go to the lane kO away, then half of
 // those that are left, and so on; at the end a lane has kN / 32 columns (at least one).
 template <int kN, int kO, int kSize, typename Op>
@@ -543,52 +359,15 @@ tree_attn_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmK, co
         for (int i = 0; i < C::kND; ++i)
             mbar_init(bar(ct.dfull[i]), 1), mbar_init(bar(ct.dempty[i]), 8 + 4 * C::kGroups + 2), mbar_init(bar(ct.cfull[i]), 4);
         ct.dead = 0;
-        ct.r0 = p.batch;
         fence_mbar_init();
     }
     if (warp == kMmaW) tmem_alloc(smem_u32(&ct.tmem), 512);
     if (C::kConv && kKv == FKV_KV_FP8_E4M3 && warp == kProdW && lane == 0) prefetch_tensormap(&tmK), prefetch_tensormap(&tmV);
 
     grid_dep_wait();                                               // lengths, tables and cache of earlier kernels
-    // ---- this CTA's share: the tiles of all units, counted by the whole block ----
     const int tpt = kR / p.group;                                  // tokens of a unit's rows
-    const int per = (p.batch + C::kThreads - 1) / C::kThreads;
-    auto tiles_of = [&](const TreeRequest &q) -> int64_t {
-        return q.live ? static_cast<int64_t>(tree_span(p, q).tiles) * ((q.n + tpt - 1) / tpt) * p.hkv : 0;
-    };
-    int64_t mine = 0;
-    for (int i = 0; i < per; ++i) {
-        const int r = tid * per + i;
-        if (r < p.batch) mine += tiles_of(tree_request(p, r));
-    }
-    int64_t incl = mine;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const int64_t y = __shfl_up_sync(kAll, incl, o);
-        if (lane >= o) incl += y;
-    }
-    if (lane == 31) ct.scan[warp] = incl;
-    __syncthreads();
-    int64_t before = 0, T = 0;
-    for (int w = 0; w < C::kThreads / 32; ++w) {
-        const int64_t x = ct.scan[w];
-        if (w < warp) before += x;
-        T += x;
-    }
-    const int64_t grid = T < static_cast<int64_t>(gridDim.x) ? (T > 0 ? T : 1) : gridDim.x;
-    const int64_t g0 = blockIdx.x < grid ? T * blockIdx.x / grid : T, g1 = blockIdx.x < grid ? T * (blockIdx.x + 1) / grid : T;
-    incl += before;
-    if (g0 < g1 && incl - mine <= g0 && g0 < incl) {
-        int64_t at = incl - mine;
-        int r = tid * per;
-        for (;; ++r) {
-            const int64_t x = tiles_of(tree_request(p, r));
-            if (g0 < at + x) break;
-            at += x;
-        }
-        ct.r0 = r;
-        ct.off0 = g0 - at;
-    }
+    const TreeTotal total = tree_shares<kTreeTok, C::kThreads, 1>(p, tpt, ct.shares);
+    const int64_t g0 = total.begin(blockIdx.x), g1 = total.begin(blockIdx.x + 1);
     umma_fence_before();
     __syncthreads();
     umma_fence_after();
@@ -600,14 +379,14 @@ tree_attn_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmK, co
         if (warp == kProdW) {
         // ==== producer ====
         const uint64_t once = l2_policy_evict_first(), again = l2_policy_evict_normal();
-        int r = ct.r0;
-        int64_t off = ct.off0, left = g1 - g0;
+        int r = ct.shares.r[0];
+        int64_t off = ct.shares.off[0], left = g1 - g0;
         int4 join = make_int4(-1, 0, 0, 0);
         TreeRequest cur = tree_request(p, r), nxt = tree_request(p, r + 1);
         Ring d, k, v;
         const int npg = kTreeTok / p.page_size;
         while (left > 0 && !*dead) {
-            const TreeSpan sp = tree_span(p, cur);
+            const TreeSpan sp = tree_span<kTreeTok>(p, cur);
             const int mt = (cur.n + tpt - 1) / tpt, units = mt * p.hkv;
             const uint64_t policy = mt > 1 ? again : once;
             for (int ui = static_cast<int>(off / sp.tiles), tb = static_cast<int>(off % sp.tiles); ui < units && left > 0; ++ui, tb = 0) {
@@ -625,11 +404,7 @@ tree_attn_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmK, co
                 u.start = sp.start;
                 u.sink_tiles = sp.sink_tiles;
                 u.head = sp.head;
-                // whole tiles: of committed tokens, and within every row's window or among the first tokens
-                const int32_t far = p.window && cur.len > p.window ? cur.len - p.window : 0;      // the deepest row's first token, at most
-                u.whole[2] = u.ctx > sp.start ? sp.sink_tiles + (u.ctx - sp.start) / kTreeTok : 0;
-                u.whole[1] = sp.sink_tiles + (far > sp.start ? (far - sp.start + kTreeTok - 1) / kTreeTok : 0);
-                u.whole[0] = p.window ? min(sp.sink_tiles ? sp.sink_tiles : u.whole[2], min(p.sinks, u.ctx) / kTreeTok) : 0;
+                unit_whole<kTreeTok>(p, u);
                 u.row = cur.row;
                 u.h = h;
                 u.slot = tb == 0 && te == sp.tiles ? -1 : 2 * static_cast<int>(blockIdx.x) + (tb == 0 ? 1 : 0);
@@ -640,17 +415,16 @@ tree_attn_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmK, co
                 if (lane == 0) mbar_arrive(bar(ct.dfull[d.i]));
                 if (tb > 0 && te == sp.tiles) {
                     // the last part of a unit that other CTAs began: its first tile's CTA
-                    const int64_t first = g1 - left - tb;
-                    join = make_int4(static_cast<int>(((first + 1) * grid + T - 1) / T - 1), u.tok0, u.ntok, h);
+                    join = make_int4(static_cast<int>(total.of(g1 - left - tb)), u.tok0, u.ntok, h);
                 }
                 auto page = [&](int i) -> int32_t {                // this lane's page of tile i; -1: none to copy
-                    const uint32_t t = tile_at(u, i) + static_cast<uint32_t>(lane) * p.page_size;
+                    const uint32_t t = tile_at<kTreeTok>(u, i) + static_cast<uint32_t>(lane) * p.page_size;
                     return lane < npg && t < tile_end(u, i) ? __ldg(p.indices + u.row + t / p.page_size) : -1;
                 };
                 int32_t pg_next = page(tb);
                 for (int i = tb; i < te; ++i) {
                     int32_t pg = pg_next;
-                    const bool has = lane < npg && tile_at(u, i) + static_cast<uint32_t>(lane) * p.page_size < tile_end(u, i);
+                    const bool has = lane < npg && tile_at<kTreeTok>(u, i) + static_cast<uint32_t>(lane) * p.page_size < tile_end(u, i);
                     if (i + 1 < te) pg_next = page(i + 1);
                     if (__any_sync(kAll, has && static_cast<uint32_t>(pg) >= static_cast<uint32_t>(p.pages))) {
                         if (static_cast<uint32_t>(pg) >= static_cast<uint32_t>(p.pages)) pg = 0;   // never dereferenced: the unit's rows become zeros
@@ -899,7 +673,7 @@ tree_attn_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmK, co
                     const uint32_t src = sV + v.i * C::kStageB;
                     const bool whole = tile_whole(u, i);
                     if (__builtin_expect(!whole, 0)) {
-                        if (clean_v<kKv>(src, ctid, tile_at(u, i) + ctid < tile_end(u, i))) {
+                        if (clean_v<kKv>(src, ctid, tile_at<kTreeTok>(u, i) + ctid < tile_end(u, i))) {
                             atomicOr(&ct.poison[d.i][min(odd_tiles, kTreePoison - 1)][ctid >> 5], 1u << (ctid & 31));
                             *const_cast<volatile int32_t *>(&ct.unit[d.i].odd) = 1;
                         }
@@ -973,7 +747,7 @@ tree_attn_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmK, co
             for (int i = kTurns ? u.tb + static_cast<int>((g ^ turn) & 1) : u.tb; i < u.te; i += kTurns ? 2 : 1) {
                 const bool whole = tile_whole(u, i);
                 uint64_t see = ~0ull;
-                if (__builtin_expect(!whole, 0)) see = seen_by<kNC>(p, u, col0, tile_at(u, i) + tok);
+                if (__builtin_expect(!whole, 0)) see = seen_by<kNC>(p, u, col0, tile_at<kTreeTok>(u, i) + tok);
                 wait(ct.sfull[sb], sph);
                 umma_fence_after();
                 const uint32_t ts = tmem + tlane + C::kTmS + sb * kR + col0;
@@ -1209,7 +983,7 @@ tree_attn_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmK, co
                     // NaN and infinities of V that not every row sees: left out of the product, here for those who do
                     int k = 0;
                     for (int i = u.tb; i < u.te; ++i) {
-                        const uint32_t t0 = tile_at(u, i);
+                        const uint32_t t0 = tile_at<kTreeTok>(u, i);
                         if (tile_whole(u, i)) continue;
                         for (int b = 0; b < kTreeTok; ++b) {
                             if (!((*const_cast<volatile uint32_t *>(&ct.poison[d.i][min(k, kTreePoison - 1)][b >> 5]) >> (b & 31)) & 1)) continue;
@@ -1259,48 +1033,126 @@ tree_attn_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmK, co
 // ---------------------------------------------------------------------------
 // joining the parts of a unit that is cut
 // ---------------------------------------------------------------------------
-// Block (c, y): rows 8y .. of the unit whose last part CTA c had, a warp each.  The parts
-// are CTA c0's last one and the first ones of c0 + 1 .. c.
-__global__ void __launch_bounds__(256)
+// Block (c, y): rows 8y .. of the unit whose last part share c had.  The parts are share c0's
+// last one and the first ones of c0 + 1 .. c.  Up to 16 parts: a warp joins a row, 8 loads in
+// flight.  A few requests alone are cut into a hundred parts, and a warp that read them
+// in turn made their joining the longest part of the call (batch of 4, up to 64k tokens: 30 us,
+// 13 now): there each warp first sums parts w, w + 8, ... of four rows.
+constexpr int kJoinWarps = 8;
+
+__global__ void __launch_bounds__(32 * kJoinWarps, 4)
 tree_join_kernel(const TreeParams p, int rows) {
+    __shared__ __align__(16) float4 part_o[kJoinWarps][4][32];
+    __shared__ float part_l[kJoinWarps][4], tops[8];
+    __shared__ int wrong[8];
     grid_dep_wait();
     grid_dep_launch();
     const int c = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int4 j = p.joins[c];
-    const int c0 = j.x, row = blockIdx.y * 8 + warp, tk = row / p.group;
-    if (c0 < 0 || tk >= j.z) return;
+    const int c0 = j.x, row0 = blockIdx.y * 8, n = min(8, j.z * p.group - row0);
+    if (c0 < 0 || n <= 0) return;
     const int parts = c - c0 + 1;
-    auto slot = [&](int i) { return static_cast<int64_t>(i == 0 ? 2 * c0 + 1 : 2 * (c0 + i)) * rows + row; };
+    const float vs = p.v_scale ? __ldg(p.v_scale + j.w) : 1.f;
+    auto slot = [&](int i) { return static_cast<int64_t>(i == 0 ? 2 * c0 + 1 : 2 * (c0 + i)) * rows + row0; };
+    auto put = [&](int r, bool none, float l, float4 o) {
+        const int row = row0 + r, tk = row / p.group;
+        none |= l == 0.f;
+        const float g = none ? 0.f : vs / l;
+        if (none) o = make_float4(0.f, 0.f, 0.f, 0.f);
+        uint2 w;
+        w.x = pack_bf16x2(o.x * g, o.y * g);
+        w.y = pack_bf16x2(o.z * g, o.w * g);
+        reinterpret_cast<uint2 *>(p.out + (static_cast<int64_t>(j.y + tk) * p.hq + j.w * p.group + (row - tk * p.group)) * 128)[lane] = w;
+    };
     float top = -INFINITY;
-    bool wrong = false;
-    for (int i = lane; i < parts; i += 32) {
-        const float2 ml = p.part_ml[slot(i)];
-        wrong |= ml.y < 0.f;
+    bool bad = false;
+    if (parts <= 2 * kJoinWarps) {
+        if (warp >= n) return;
+        const float2 ml = lane < parts ? p.part_ml[slot(lane) + warp] : make_float2(0.f, 0.f);
+        float4 x[8], o = make_float4(0.f, 0.f, 0.f, 0.f);
+        auto load = [&](int b) {
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+                if (b + k < parts) x[k] = reinterpret_cast<const float4 *>(p.part_o + (slot(b + k) + warp) * 128)[lane];
+        };
+        load(0);
+        if (ml.y != 0.f) top = ml.x;                               // 0: it saw nothing
+#pragma unroll
+        for (int d = 8; d; d >>= 1) top = fmaxf(top, __shfl_xor_sync(kAll, top, d));
+        bad = __any_sync(kAll, ml.y < 0.f);
+        const float f = ml.y == 0.f ? 0.f : ex2(ml.x - top);
+        float l = 0.f;
+        for (int b = 0;;) {
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                const float fk = __shfl_sync(kAll, f, b + k), y = __shfl_sync(kAll, ml.y, b + k);
+                if (y == 0.f) continue;
+                l = fmaf(fk, y, l);
+                o.x = fmaf(fk, x[k].x, o.x), o.y = fmaf(fk, x[k].y, o.y), o.z = fmaf(fk, x[k].z, o.z), o.w = fmaf(fk, x[k].w, o.w);
+            }
+            if ((b += 8) >= parts) break;
+            load(b);
+        }
+        put(warp, bad, l, o);
+        return;
+    }
+    for (int i = lane; i < parts && warp < n; i += 32) {
+        const float2 ml = p.part_ml[slot(i) + warp];
+        bad |= ml.y < 0.f;
         if (ml.y != 0.f) top = fmaxf(top, ml.x);
     }
 #pragma unroll
-    for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(kAll, top, o));
-    wrong = __any_sync(kAll, wrong);
-    float l = 0.f;
-    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (!wrong) {
-#pragma unroll 4
-        for (int i = 0; i < parts; ++i) {
-            const int64_t at = slot(i);
-            const float2 ml = p.part_ml[at];
-            const float4 x = reinterpret_cast<const float4 *>(p.part_o + at * 128)[lane];
-            if (ml.y == 0.f) continue;                             // it saw nothing
-            const float f = ex2(ml.x - top);
+    for (int d = 16; d; d >>= 1) top = fmaxf(top, __shfl_xor_sync(kAll, top, d));
+    bad = __any_sync(kAll, bad);
+    if (lane == 0) {
+        tops[warp] = top;
+        wrong[warp] = bad;
+    }
+#pragma unroll 1
+    for (int r0 = 0; r0 < n; r0 += 4) {
+        __syncthreads();
+        float4 o[4];
+        float l = 0.f;                                             // lane r: row r0 + r's
+#pragma unroll
+        for (int r = 0; r < 4; ++r) o[r] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 1
+        for (int i = warp; i < parts; i += kJoinWarps) {
+            const int64_t at = slot(i) + r0;
+            float4 x[4];
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+                if (r0 + r < n) x[r] = reinterpret_cast<const float4 *>(p.part_o + (at + r) * 128)[lane];
+            const float2 ml = lane < 4 && r0 + lane < n ? p.part_ml[at + lane] : make_float2(0.f, 0.f);
+            const float f = ml.y == 0.f ? 0.f : ex2(ml.x - tops[r0 + (lane & 3)]);
             l = fmaf(f, ml.y, l);
-            o.x = fmaf(f, x.x, o.x), o.y = fmaf(f, x.y, o.y), o.z = fmaf(f, x.z, o.z), o.w = fmaf(f, x.w, o.w);
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                const float fr = __shfl_sync(kAll, f, r);
+                if (__shfl_sync(kAll, ml.y, r) == 0.f) continue;
+                o[r].x = fmaf(fr, x[r].x, o[r].x), o[r].y = fmaf(fr, x[r].y, o[r].y);
+                o[r].z = fmaf(fr, x[r].z, o[r].z), o[r].w = fmaf(fr, x[r].w, o[r].w);
+            }
+        }
+#pragma unroll
+        for (int r = 0; r < 4; ++r) part_o[warp][r][lane] = o[r];
+        if (lane < 4) part_l[warp][lane] = l;
+        __syncthreads();
+        if (warp < 4 && r0 + warp < n) {
+            float4 all = make_float4(0.f, 0.f, 0.f, 0.f);
+            l = 0.f;
+#pragma unroll
+            for (int w = 0; w < kJoinWarps; ++w) {
+                const float4 x = part_o[w][warp][lane];
+                all.x += x.x, all.y += x.y, all.z += x.z, all.w += x.w;
+                l += part_l[w][warp];
+            }
+            put(r0 + warp, wrong[r0 + warp], l, all);
         }
     }
-    const float g = l == 0.f ? 0.f : (p.v_scale ? __ldg(p.v_scale + j.w) : 1.f) / l;
-    if (l == 0.f) o = make_float4(0.f, 0.f, 0.f, 0.f);
-    uint2 w;
-    w.x = pack_bf16x2(o.x * g, o.y * g);
-    w.y = pack_bf16x2(o.z * g, o.w * g);
-    reinterpret_cast<uint2 *>(p.out + (static_cast<int64_t>(j.y + tk) * p.hq + j.w * p.group + (row - tk * p.group)) * 128)[lane] = w;
+}
+
+cudaError_t launch_tree_join(const TreeParams &p, int shares, int rows, cudaStream_t st) {
+    return launch_pdl(tree_join_kernel, dim3(shares, rows / 8), dim3(32 * kJoinWarps), 0, st, p, rows);
 }
 
 // ---------------------------------------------------------------------------
@@ -1325,14 +1177,14 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
     return fn;
 }
 
-// A pool as a 4-D tensor; a box is a page's rows of one KV head (BF16: 64 of their dims).
-bool page_map(CUtensorMap *m, const void *pool, bool fp8, int P, int Hkv, int S) {
+// A pool as a 4-D tensor; a box is a page's rows of one KV head, `rows` at most (BF16: 64 of their dims).
+bool page_map(CUtensorMap *m, const void *pool, bool fp8, int P, int Hkv, int S, int rows) {
     const auto enc = encode_fn();
     if (!enc) return false;
     const cuuint64_t row = fp8 ? 128 : 256;
     const cuuint64_t dims[4] = {128, static_cast<cuuint64_t>(S), static_cast<cuuint64_t>(Hkv), static_cast<cuuint64_t>(P)};
     const cuuint64_t strides[3] = {row, row * S, row * S * Hkv};
-    const cuuint32_t box[4] = {fp8 ? 128u : 64u, static_cast<cuuint32_t>(S), 1u, 1u}, step[4] = {1u, 1u, 1u, 1u};
+    const cuuint32_t box[4] = {fp8 ? 128u : 64u, static_cast<cuuint32_t>(S < rows ? S : rows), 1u, 1u}, step[4] = {1u, 1u, 1u, 1u};
     return enc(m, fp8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void *>(pool), dims, strides, box,
                step, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
@@ -1349,16 +1201,23 @@ int rows_of(int64_t n_tokens, int64_t batch, int64_t group) {
     return 128;
 }
 
+// Which kernel.  Up to 32 rows over FP8 or FP4 the products are little work, and the hand-overs of a tile from warp to warp
+// cost more than they save: a window of 4096 over FP8 takes 98 us instead of 115, one of 1024 over 16-token FP4 pages 101
+// instead of 176, 64 requests around 16k tokens with up to 4 drafted (32 rows) 457 instead of 486 (batch of 16: 145, 140).
+// BF16 needs no conversions and is read by the tensor cores as it lies.
+bool small_call(int kv, int rows) { return kv != FKV_KV_BF16 && rows <= 32; }
+
 size_t align256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
 struct TreeWs {
     size_t joins, ml, o, total;
 };
-TreeWs tree_ws(int sms, int rows) {
+TreeWs tree_ws(int sms, int kv, int rows) {
+    const size_t shares = small_call(kv, rows) ? tree_small_shares(sms) : sms;
     TreeWs w;
     w.joins = 0;
-    w.ml = align256(sizeof(int4) * sms);
-    w.o = align256(w.ml + sizeof(float2) * 2 * sms * rows);
-    w.total = align256(w.o + sizeof(float) * 128 * 2 * sms * rows);
+    w.ml = align256(sizeof(int4) * shares);
+    w.o = align256(w.ml + sizeof(float2) * 2 * shares * rows);
+    w.total = align256(w.o + sizeof(float) * 128 * 2 * shares * rows);
     return w;
 }
 
@@ -1380,15 +1239,16 @@ fkv_status launch_tree(const TreeParams &p, int sms, const CUtensorMap &tmK, con
     }
     if (launch_pdl(tree_attn_kernel<kKv, kR>, dim3(sms), dim3(TreeCfg<kKv, kR>::kThreads), smem, st, p, tmK, tmV) != cudaSuccess)
         return FKV_ERR_CUDA;
-    return launch_pdl(tree_join_kernel, dim3(sms, kR / 8), dim3(256), 0, st, p, kR) == cudaSuccess ? FKV_OK : FKV_ERR_CUDA;
+    return launch_tree_join(p, sms, kR, st) == cudaSuccess ? FKV_OK : FKV_ERR_CUDA;
 }
 
 template <int kKv>
 fkv_status launch_rows(int rows, const TreeParams &p, int sms, const CUtensorMap &tmK, const CUtensorMap &tmV, cudaStream_t st) {
-    return rows == 16   ? launch_tree<kKv, 16>(p, sms, tmK, tmV, st)
-           : rows == 32 ? launch_tree<kKv, 32>(p, sms, tmK, tmV, st)
-           : rows == 64 ? launch_tree<kKv, 64>(p, sms, tmK, tmV, st)
-                        : launch_tree<kKv, 128>(p, sms, tmK, tmV, st);
+    if constexpr (kKv == FKV_KV_BF16) {                            // few rows of the other types: tree_attn_small.cu
+        if (rows == 16) return launch_tree<kKv, 16>(p, sms, tmK, tmV, st);
+        if (rows == 32) return launch_tree<kKv, 32>(p, sms, tmK, tmV, st);
+    }
+    return rows == 64 ? launch_tree<kKv, 64>(p, sms, tmK, tmV, st) : launch_tree<kKv, 128>(p, sms, tmK, tmV, st);
 }
 
 // Both calls.  tree: rows and masks per drafted token; else one token a request.
@@ -1419,12 +1279,14 @@ fkv_status attend(bool tree, const void *q, int32_t n_tokens, int32_t num_q_head
     const int sms = device_sm_count();
     if (!err || sms <= 0) return FKV_ERR_CUDA;
     const int group = num_q_heads / num_kv_heads, rows = rows_of(n_tokens, batch, group);
-    const TreeWs w = tree_ws(sms, rows);
+    const TreeWs w = tree_ws(sms, kv_dtype, rows);
+    const bool small = small_call(kv_dtype, rows);
+    const int box = small ? kTreeSmallTok : kTreeTok;
     if (workspace_bytes < w.total) return FKV_ERR_INVALID_ARG;
     CUtensorMap tmK = {}, tmV = {};                                // unused by the 4-bit cache's untiled copies
     const bool fp8 = kv_dtype == FKV_KV_FP8_E4M3;
-    if (kv_dtype != FKV_KV_FP4 && (!page_map(&tmK, k_cache, fp8, num_pages, num_kv_heads, page_size) ||
-                                   !page_map(&tmV, v_cache, fp8, num_pages, num_kv_heads, page_size)))
+    if (kv_dtype != FKV_KV_FP4 && (!page_map(&tmK, k_cache, fp8, num_pages, num_kv_heads, page_size, box) ||
+                                   !page_map(&tmV, v_cache, fp8, num_pages, num_kv_heads, page_size, box)))
         return FKV_ERR_CUDA;
     uint8_t *ws = static_cast<uint8_t *>(workspace);
     TreeParams p;
@@ -1457,6 +1319,7 @@ fkv_status attend(bool tree, const void *q, int32_t n_tokens, int32_t num_q_head
     p.sinks = sinks;
     p.scale_log2 = sm_scale * 1.4426950408889634f;
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
+    if (small) return launch_tree_small(p, kv_dtype, rows, sms, tmK, tmV, st);
     return fp8                         ? launch_rows<FKV_KV_FP8_E4M3>(rows, p, sms, tmK, tmV, st)
            : kv_dtype == FKV_KV_BF16 ? launch_rows<FKV_KV_BF16>(rows, p, sms, tmK, tmV, st)
                                      : launch_rows<FKV_KV_FP4>(rows, p, sms, tmK, tmV, st);
@@ -1472,7 +1335,7 @@ extern "C" size_t paged_tree_attn_workspace_size(int32_t n_tokens, int32_t batch
     if (n_tokens < 0 || batch < 0 || num_q_heads <= 0 || num_kv_heads <= 0 || num_q_heads % num_kv_heads) return 0;
     if (head_dim != 128 || !known_kv(kv_dtype) || num_q_heads / num_kv_heads > 128) return 0;
     const int sms = device_sm_count();
-    return sms <= 0 ? 0 : tree_ws(sms, rows_of(n_tokens, batch, num_q_heads / num_kv_heads)).total;
+    return sms <= 0 ? 0 : tree_ws(sms, kv_dtype, rows_of(n_tokens, batch, num_q_heads / num_kv_heads)).total;
 }
 
 extern "C" fkv_status paged_tree_attn(const void *q, int32_t n_tokens, int32_t num_q_heads, const void *k_cache,

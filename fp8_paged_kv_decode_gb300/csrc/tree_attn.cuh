@@ -1,0 +1,291 @@
+// tree_attn.cuh -- what the kernels of tree and window attention share: which tiles a
+// request has, which rows see a token, equal shares of all tiles, and the joining of units
+// that several shares have parts of.
+//
+// The n drafted tokens of a request and the G query heads of a KV head read the same K and V:
+// a unit is (request, KV head, rows of some of its drafted tokens), a tile kTok of the tokens
+// that its rows see.  The tiles of all units, laid end to end, are cut into equal shares.
+#pragma once
+
+#include "fp4_row.cuh"
+
+namespace fkv {
+
+constexpr int kTreeMaxWords = 4;               // 64-bit words of a row's mask
+constexpr float kTreeTop = 10.f, kTreeMost = 15.9f;   // log2 of a moved reference's largest weight, and of any weight
+constexpr float kTreeNone = -3e38f;            // the reference of a row that has seen nothing
+constexpr uint32_t kAll = 0xffffffffu;
+
+struct TreeParams {
+    const __nv_bfloat16 *q;
+    const uint8_t *k_cache, *v_cache;
+    const float *k_scale, *v_scale;
+    const int32_t *indptr, *indices, *seq_lens;
+    const int32_t *token_indptr;               // nullptr: one token a request
+    const uint64_t *mask;                      // nullptr: a row sees itself
+    const uint8_t *abort_mask;
+    __nv_bfloat16 *out;
+    uint32_t *err;
+    // [2 shares][rows][128], [2 shares][rows]: sums of units that are cut, their references and weights' sums (sum < 0: a
+    // bad page); [shares] the unit whose last part a share has: first share (-1: none), token, tokens, KV head
+    float *part_o;
+    float2 *part_ml;
+    int4 *joins;
+    int64_t nnz;
+    int32_t batch, n_tokens, hq, hkv, group, pages, page_size, words, window, sinks;
+    float scale_log2;
+};
+
+// ---------------------------------------------------------------------------
+// geometry
+// ---------------------------------------------------------------------------
+struct TreeRequest {
+    int32_t t0, n, len, row;                   // first query token, drafted and all tokens, first page-table entry
+    bool live, rows;                           // has work; its rows are rows of q
+};
+
+__device__ __forceinline__ TreeRequest tree_request(const TreeParams &p, int r) {
+    TreeRequest q{};
+    if (r >= p.batch) return q;
+    int t0 = r, t1 = r + 1;
+    if (p.token_indptr) {
+        t0 = __ldg(p.token_indptr + r);
+        t1 = __ldg(p.token_indptr + r + 1);
+    }
+    const int32_t b = __ldg(p.indptr + r), e = __ldg(p.indptr + r + 1);
+    q.len = __ldg(p.seq_lens + r);
+    const bool alive = !p.abort_mask || __ldg(p.abort_mask + r) == 0;
+    q.t0 = t0;
+    q.row = b;
+    q.rows = t0 >= 0 && t1 >= t0 && t1 <= p.n_tokens;
+    q.n = q.rows ? t1 - t0 : 0;
+    q.live = q.n > 0 && alive && q.len >= q.n && q.n <= 64 * p.words && b >= 0 && e >= b && e <= p.nnz &&
+             static_cast<int64_t>(e - b) * p.page_size >= q.len;
+    return q;
+}
+
+// The tiles of a live request: those over the first tokens, if they lie apart, then those
+// from `start` on, the page of the first token that a row at depth 0 sees.
+struct TreeSpan {
+    int32_t start, sink_tiles, head, tiles;
+};
+template <int kTok>                            // tokens of a tile
+__device__ __forceinline__ TreeSpan tree_span(const TreeParams &p, const TreeRequest &q) {
+    TreeSpan s{0, 0, 0, 0};
+    const int32_t ctx = q.len - q.n;
+    if (p.window && ctx >= p.window) {
+        const int32_t lo = ctx - p.window + 1;
+        s.start = lo - lo % p.page_size;
+        s.head = min(p.sinks, lo);
+        s.sink_tiles = (s.head + kTok - 1) / kTok;
+        if (s.start <= static_cast<int64_t>(s.sink_tiles) * kTok) s = TreeSpan{0, 0, 0, 0};
+    }
+    s.tiles = s.sink_tiles + (q.len - s.start - 1) / kTok + 1;
+    return s;
+}
+
+// What a share has of a unit.
+struct TreeUnit {
+    int32_t tb, te;                            // its tiles; te < 0: there is no more work
+    int32_t tok0, ntok;                        // the rows' tokens
+    int32_t ctx, len;
+    int32_t start, sink_tiles, head;
+    int32_t whole[3];                          // tiles [0, whole[0]) and [whole[1], whole[2]) are seen by every row
+    int32_t row, h;                            // first page-table entry, KV head
+    int32_t slot;                              // of its partial sums; -1: the whole unit is here
+    int32_t bad;                               // a page outside the pool
+    int32_t odd;                               // NaN or infinities in V that not every row sees
+};
+template <int kTok>
+__device__ __forceinline__ uint32_t tile_at(const TreeUnit &u, int i) {
+    return i < u.sink_tiles ? static_cast<uint32_t>(i) * kTok : u.start + static_cast<uint32_t>(i - u.sink_tiles) * kTok;
+}
+__device__ __forceinline__ uint32_t tile_end(const TreeUnit &u, int i) { return i < u.sink_tiles ? u.head : u.len; }
+// Sets u.whole, with the unit's spans and lengths in place: tiles of committed tokens that lie
+// within every row's window, or among the first tokens.
+template <int kTok>
+__device__ __forceinline__ void unit_whole(const TreeParams &p, TreeUnit &u) {
+    const int32_t far = p.window && u.len > p.window ? u.len - p.window : 0;       // the deepest row's first token, at most
+    u.whole[2] = u.ctx > u.start ? u.sink_tiles + (u.ctx - u.start) / kTok : 0;
+    u.whole[1] = u.sink_tiles + (far > u.start ? (far - u.start + kTok - 1) / kTok : 0);
+    u.whole[0] = p.window ? min(u.sink_tiles ? u.sink_tiles : u.whole[2], min(p.sinks, u.ctx) / kTok) : 0;
+}
+// Whether every row sees every token of tile i.
+__device__ __forceinline__ bool tile_whole(const TreeUnit &u, int i) { return i < u.whole[0] || (i >= u.whole[1] && i < u.whole[2]); }
+
+// ---------------------------------------------------------------------------
+// which rows see a token
+// ---------------------------------------------------------------------------
+struct RowSight {
+    uint64_t word;                             // the row's mask word of the token asked for
+    int32_t lo;                                // its first committed token apart from the first ones
+};
+// Of drafted row `tok` (of the call), for tokens of mask word `w`.
+__device__ __forceinline__ RowSight row_sight(const TreeParams &p, const TreeUnit &u, int tok, int w) {
+    RowSight s{w == 0 ? 1ull : 0ull, 0};
+    int bits = 1;
+    if (p.mask) {
+        const uint64_t *m = p.mask + static_cast<int64_t>(tok) * p.words;
+        s.word = w < p.words ? __ldg(m + w) : 0ull;
+        if (p.window) {
+            bits = 0;
+            for (int i = 0; i < p.words; ++i) bits += __popcll(__ldg(m + i));
+        }
+    }
+    if (p.window) s.lo = static_cast<int32_t>(static_cast<int64_t>(u.ctx) + max(bits - 1, 0) - p.window + 1 > 0 ? static_cast<int64_t>(u.ctx) + max(bits - 1, 0) - p.window + 1 : 0);
+    return s;
+}
+__device__ __forceinline__ bool sees(const TreeParams &p, const TreeUnit &u, const RowSight &s, uint32_t t) {
+    if (t >= static_cast<uint32_t>(u.len)) return false;
+    if (t >= static_cast<uint32_t>(u.ctx)) return (s.word >> ((t - u.ctx) & 63)) & 1;
+    return !p.window || t < static_cast<uint32_t>(p.sinks) || t >= static_cast<uint32_t>(s.lo);
+}
+__device__ __forceinline__ int word_of(const TreeUnit &u, uint32_t t) {
+    return t >= static_cast<uint32_t>(u.ctx) ? static_cast<int>((t - u.ctx) >> 6) : 0;
+}
+// ---------------------------------------------------------------------------
+// values
+// ---------------------------------------------------------------------------
+__device__ __forceinline__ void st_shared_v4(uint32_t addr, uint4 v) {
+    asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
+}
+
+__device__ __forceinline__ void e4m3x4_to_f16(uint32_t w, uint32_t &lo, uint32_t &hi) {
+    lo = e4m3x2_to_f16x2(static_cast<uint16_t>(w & 0xFFFFu));
+    hi = e4m3x2_to_f16x2(static_cast<uint16_t>(w >> 16));
+}
+// A V value that is NaN or infinite, as the cache holds it; else 0.
+template <int kKv>
+__device__ __forceinline__ float odd_value(const TreeParams &p, const TreeUnit &u, uint32_t t, int dim) {
+    const int64_t pg = __ldg(p.indices + u.row + t / p.page_size);
+    if (pg < 0 || pg >= p.pages) return 0.f;
+    const int64_t row = (pg * p.hkv + u.h) * p.page_size + t % p.page_size;
+    float v;
+    if (kKv == FKV_KV_BF16) {
+        v = __uint_as_float(static_cast<uint32_t>(reinterpret_cast<const uint16_t *>(p.v_cache)[row * 128 + dim]) << 16);
+    } else {
+        const uint32_t b = kKv == FKV_KV_FP8_E4M3 ? p.v_cache[row * 128 + dim] : p.v_cache[row * kFp4Row + kFp4Codes + dim / 16];
+        v = (b & 0x7Fu) == 0x7Fu ? __int_as_float(0x7FC00000) : 0.f;
+    }
+    return isfinite(v) ? 0.f : v;
+}
+
+// A V row in its stage, of a tile that not every row sees whole: rows of no token, NaN and
+// infinities become zeros, since a weight of zero would not take them out of a product.
+// Returns whether there were NaN or infinities.  A pass of its own over these few tiles keeps
+// the conversions small: with both forms of them in the loop every tile paid for the tests
+// (64 requests, window of 4096: 173 us, 120 without).
+template <int kKv>
+__device__ __forceinline__ bool clean_v(uint32_t stage, int tok, bool valid) {
+    bool odd = false;
+    constexpr int kSteps = kKv == FKV_KV_BF16 ? 16 : 8;
+#pragma unroll 1
+    for (int c = 0; c < kSteps; ++c) {
+        if (kKv == FKV_KV_FP4) {
+            const uint32_t a = stage + tok * kFp4Row + 8 * c;
+            if (!valid) {
+                st_shared_v2_zero(a);
+                if (c == 0) st_shared_v2_zero(stage + tok * kFp4Row + kFp4Codes);
+            } else if ((ld_shared_u8(stage + tok * kFp4Row + kFp4Codes + c) & 0x7Fu) == 0x7Fu) {
+                odd = true;                                        // codes of zero under a scale of zero
+                asm volatile("st.shared.u8 [%0], %1;" ::"r"(stage + tok * kFp4Row + kFp4Codes + c), "r"(0u) : "memory");
+            }
+            continue;
+        }
+        const uint32_t a = stage + 16384 * (c >> 3) + tok * 128 + (((c & 7) ^ (tok & 7)) << 4);
+        const uint4 v = ld_shared_v4(a);
+        uint32_t w[4] = {v.x, v.y, v.z, v.w}, bad = 0;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            uint32_t m;                                            // the bits of what is no number
+            if (kKv == FKV_KV_BF16) m = ((w[j] & 0x7F80u) == 0x7F80u ? 0xFFFFu : 0u) | ((w[j] & 0x7F800000u) == 0x7F800000u ? 0xFFFF0000u : 0u);
+            else m = ((((w[j] & 0x7F7F7F7Fu) + 0x01010101u) >> 7) & 0x01010101u) * 0xFFu;
+            if (!valid) m = 0xFFFFFFFFu;
+            else odd |= m != 0;
+            bad |= m;
+            w[j] &= ~m;
+        }
+        if (bad) st_shared_v4(a, make_uint4(w[0], w[1], w[2], w[3]));
+    }
+    return odd;
+}
+
+// ---------------------------------------------------------------------------
+// shares
+// ---------------------------------------------------------------------------
+// A block has kParts shares: k gridDim + blockIdx, so that few shares are spread over all
+// blocks.  The whole block counts the tiles; where a share begins is found by the thread that
+// counted the request.
+template <int kThreads, int kParts>
+struct TreeShares {
+    int64_t scan[kThreads / 32];                                   // one per warp
+    int64_t off[kParts];                                           // the share's first tile within its request
+    int32_t r[kParts];                                             // that request; batch: nothing to do
+};
+struct TreeTotal {
+    int64_t tiles, used;                                           // shares that get tiles
+    __device__ __forceinline__ int64_t begin(int64_t share) const { return share < used ? tiles * share / used : tiles; }
+    // The share that has tile t.
+    __device__ __forceinline__ int64_t of(int64_t t) const { return ((t + 1) * used + tiles - 1) / tiles - 1; }
+};
+template <int kTok, int kThreads, int kParts>
+__device__ __forceinline__ TreeTotal tree_shares(const TreeParams &p, int tpt, TreeShares<kThreads, kParts> &sh) {
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int per = (p.batch + kThreads - 1) / kThreads;
+    if (tid < kParts) sh.r[tid] = p.batch;
+    TreeTotal t{0, 1};
+    int64_t at = 0;
+    // twice the same loop: what this thread's requests have, then where shares begin in them
+    for (int pass = 0; pass < 2; ++pass) {
+        int64_t mine = 0;
+#pragma unroll 1
+        for (int i = 0; i < per; ++i) {
+            const int r = tid * per + i;
+            if (r >= p.batch) break;
+            const TreeRequest q = tree_request(p, r);
+            if (!q.live) continue;
+            const int64_t x = static_cast<int64_t>(tree_span<kTok>(p, q).tiles) * ((q.n + tpt - 1) / tpt) * p.hkv;
+            if (pass) {
+#pragma unroll 1
+                for (int k = 0; k < kParts; ++k) {
+                    const int64_t share = static_cast<int64_t>(k) * gridDim.x + blockIdx.x, g0 = t.begin(share);
+                    if (share < t.used && g0 >= at + mine && g0 < at + mine + x) {
+                        sh.r[k] = r;
+                        sh.off[k] = g0 - at - mine;
+                    }
+                }
+            }
+            mine += x;
+        }
+        if (pass) break;
+        int64_t incl = mine;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int64_t y = __shfl_up_sync(kAll, incl, o);
+            if (lane >= o) incl += y;
+        }
+        if (lane == 31) sh.scan[warp] = incl;
+        __syncthreads();
+        at = incl - mine;
+#pragma unroll 1
+        for (int w = 0; w < kThreads / 32; ++w) {
+            if (w < warp) at += sh.scan[w];
+            t.tiles += sh.scan[w];
+        }
+        const int64_t most = static_cast<int64_t>(kParts) * gridDim.x;
+        t.used = t.tiles < 1 ? 1 : t.tiles < most ? t.tiles : most;
+    }
+    return t;
+}
+
+// ---------------------------------------------------------------------------
+// the other parts of a call (host)
+// ---------------------------------------------------------------------------
+// Joins the parts of cut units (tree_attn.cu).
+cudaError_t launch_tree_join(const TreeParams &p, int shares, int rows, cudaStream_t st);
+// The kernel of few rows a unit (tree_attn_small.cu): 16 or 32, FP8 or FP4.
+int tree_small_shares(int sms);
+constexpr int kTreeSmallTok = 32;              // its tiles' tokens
+fkv_status launch_tree_small(const TreeParams &p, int kv, int rows, int sms, const CUtensorMap &tmK, const CUtensorMap &tmV, cudaStream_t st);
+
+}  // namespace fkv
