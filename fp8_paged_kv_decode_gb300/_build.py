@@ -20,7 +20,8 @@ BIND_SOURCE = os.path.join(CSRC, "bind.cpp")
 BUILD_DIR = os.path.join(PKG, "_build")
 SOURCES = ["fkv_api.cu", "kv_append.cu", "tag_check.cu", "decode_attn.cu", "decode_attn_noalloc.cu", "page_realloc.cu",
            "kv_calibrate.cu", "selftest.cu", "kv_gather.cu", "qk_norm_rope.cu", "step_tables.cu",
-           "kv_append_rope.cu", "tree_attn.cu", "tree_attn_small.cu", "tree_commit.cu"]
+           "kv_append_rope.cu", "tree_attn.cu", "tree_attn_small.cu", "tree_attn_wide.cu",
+           "tree_commit.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden",
               "--expt-relaxed-constexpr", "-I", os.path.join(ROOT, "include")]

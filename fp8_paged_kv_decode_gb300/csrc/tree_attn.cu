@@ -36,11 +36,6 @@
 
 namespace fkv {
 
-constexpr int kTreeTok = 128;                  // tokens of a tile
-constexpr int kTreePoison = 10;                // tiles of a unit that hold tokens not seen by every row, at most (9)
-constexpr int kTreeTests = 1 << 24;
-constexpr uint64_t kTreeDrainNs = 2000000000ull;
-
 // ---------------------------------------------------------------------------
 // shared memory
 // ---------------------------------------------------------------------------
@@ -115,36 +110,6 @@ constexpr int tree_smem() {
     static_assert(C::kOffP % 1024 == 0 && C::kOffV16 % 1024 == 0 && C::kOffK % 1024 == 0 && C::kOffV % 1024 == 0,
                   "swizzled buffers start on 1024 bytes");
     return TreeCfg<kKv, kR>::kOffCtrl + static_cast<int>((sizeof(TreeCtrl<kKv, kR>) + 15) / 16 * 16);
-}
-
-struct Ring {                                  // a buffer of a ring and the parity of its current round
-    int i = 0;
-    uint32_t ph = 0;
-    template <int kN>
-    __device__ __forceinline__ void next() {
-        if (++i == kN) {
-            i = 0;
-            ph ^= 1;
-        }
-    }
-};
-
-// Waits for a phase.  After kTreeTests tests without it (each sleeps in hardware for a while;
-// some seconds in all) the call has failed: that is recorded, and from then on no wait of the
-// block waits, so that it ends soon, with outputs that are not valid.
-__device__ __forceinline__ void tree_wait(uint32_t bar, uint32_t parity, volatile int32_t *dead, uint32_t *err) {
-    if (__builtin_expect(mbar_try_wait(bar, parity), 1)) return;
-    int left = kTreeTests;
-#pragma unroll 1
-    while (!mbar_try_wait(bar, parity)) {
-        if (__builtin_expect((--left & 0xFFF) == 0, 0)) {
-            if (left <= 0) {
-                *dead = 1;
-                atomicOr(err, FKV_DEVERR_TIMEOUT);
-            }
-            if (*dead) return;
-        }
-    }
 }
 
 // Whether any of the 128 threads of a softmax group says so (a barrier of the group).
@@ -1194,11 +1159,11 @@ bool known_kv(int kv) { return kv == FKV_KV_FP8_E4M3 || kv == FKV_KV_BF16 || kv 
 
 // Rows of a unit: the smallest instance that holds the query heads of the requests' mean
 // number of tokens.
-int rows_of(int64_t n_tokens, int64_t batch, int64_t group) {
+int rows_of(int kv, int64_t n_tokens, int64_t batch, int64_t group) {
     const int64_t want = group * ((n_tokens + batch - 1) / (batch > 0 ? batch : 1));
     for (int r = 16; r < 128; r *= 2)
         if (want <= r) return r;
-    return 128;
+    return kv == FKV_KV_BF16 && want > 128 ? kTreeWideRows : 128;
 }
 
 // Which kernel.  Up to 32 rows over FP8 or FP4 the products are little work, and the hand-overs of a tile from warp to warp
@@ -1278,7 +1243,7 @@ fkv_status attend(bool tree, const void *q, int32_t n_tokens, int32_t num_q_head
     uint32_t *err = device_error_word();
     const int sms = device_sm_count();
     if (!err || sms <= 0) return FKV_ERR_CUDA;
-    const int group = num_q_heads / num_kv_heads, rows = rows_of(n_tokens, batch, group);
+    const int group = num_q_heads / num_kv_heads, rows = rows_of(kv_dtype, n_tokens, batch, group);
     const TreeWs w = tree_ws(sms, kv_dtype, rows);
     const bool small = small_call(kv_dtype, rows);
     const int box = small ? kTreeSmallTok : kTreeTok;
@@ -1320,6 +1285,7 @@ fkv_status attend(bool tree, const void *q, int32_t n_tokens, int32_t num_q_head
     p.scale_log2 = sm_scale * 1.4426950408889634f;
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
     if (small) return launch_tree_small(p, kv_dtype, rows, sms, tmK, tmV, st);
+    if (rows == kTreeWideRows) return launch_tree_wide(p, sms, tmK, tmV, st);
     return fp8                         ? launch_rows<FKV_KV_FP8_E4M3>(rows, p, sms, tmK, tmV, st)
            : kv_dtype == FKV_KV_BF16 ? launch_rows<FKV_KV_BF16>(rows, p, sms, tmK, tmV, st)
                                      : launch_rows<FKV_KV_FP4>(rows, p, sms, tmK, tmV, st);
@@ -1335,7 +1301,7 @@ extern "C" size_t paged_tree_attn_workspace_size(int32_t n_tokens, int32_t batch
     if (n_tokens < 0 || batch < 0 || num_q_heads <= 0 || num_kv_heads <= 0 || num_q_heads % num_kv_heads) return 0;
     if (head_dim != 128 || !known_kv(kv_dtype) || num_q_heads / num_kv_heads > 128) return 0;
     const int sms = device_sm_count();
-    return sms <= 0 ? 0 : tree_ws(sms, kv_dtype, rows_of(n_tokens, batch, num_q_heads / num_kv_heads)).total;
+    return sms <= 0 ? 0 : tree_ws(sms, kv_dtype, rows_of(kv_dtype, n_tokens, batch, num_q_heads / num_kv_heads)).total;
 }
 
 extern "C" fkv_status paged_tree_attn(const void *q, int32_t n_tokens, int32_t num_q_heads, const void *k_cache,

@@ -143,6 +143,37 @@ __device__ __forceinline__ bool sees(const TreeParams &p, const TreeUnit &u, con
 __device__ __forceinline__ int word_of(const TreeUnit &u, uint32_t t) {
     return t >= static_cast<uint32_t>(u.ctx) ? static_cast<int>((t - u.ctx) >> 6) : 0;
 }
+// Which of the 32 tokens from t0 on row `tok` (of the call; -1: none) sees.
+__device__ __forceinline__ uint32_t seen_of(const TreeParams &p, const TreeUnit &u, int tok, uint32_t t0) {
+    if (tok < 0) return 0u;
+    auto below = [t0](int64_t x) {                                 // tokens before x
+        const int64_t d = x - t0;
+        return d >= 32 ? kAll : d <= 0 ? 0u : (1u << d) - 1u;
+    };
+    const int64_t at = static_cast<int64_t>(t0) - u.ctx;           // of the drafted tokens
+    uint64_t lo = 0, hi = 0;                                       // the mask words of tokens at and at + 32
+    int bits = 1;
+    if (p.mask) {
+        const uint64_t *m = p.mask + static_cast<int64_t>(tok) * p.words;
+        bits = 0;
+#pragma unroll
+        for (int i = 0; i < kTreeMaxWords; ++i) {
+            const uint64_t w = i < p.words ? __ldg(m + i) : 0ull;
+            bits += __popcll(w);
+            if (at >= 64 * i && at < 64 * i + 64) lo = w;
+            if (at + 63 >= 64 * i && at + 63 < 64 * i + 64) hi = w;
+        }
+    } else {
+        lo = at >= 0 && at < 64 ? 1ull : 0ull;
+        hi = at + 63 >= 0 && at + 63 < 64 ? 1ull : 0ull;
+    }
+    const int sh = static_cast<int>(at & 63);
+    const uint32_t drafted = static_cast<uint32_t>((lo >> sh) | (sh ? hi << (64 - sh) : 0ull));
+    uint32_t old = below(u.ctx);
+    if (p.window) old &= below(p.sinks) | ~below(static_cast<int64_t>(u.ctx) + max(bits - 1, 0) - p.window + 1);
+    return (old | (drafted & ~below(u.ctx))) & below(u.len);
+}
+
 // ---------------------------------------------------------------------------
 // values
 // ---------------------------------------------------------------------------
@@ -279,10 +310,51 @@ __device__ __forceinline__ TreeTotal tree_shares(const TreeParams &p, int tpt, T
 }
 
 // ---------------------------------------------------------------------------
+// the kernels on the tensor cores' own memory (tree_attn.cu, tree_attn_wide.cu)
+// ---------------------------------------------------------------------------
+constexpr int kTreeTok = 128;                  // tokens of a tile
+constexpr int kTreePoison = 10;                // tiles of a unit that hold tokens not seen by every row, at most (9)
+constexpr int kTreeTests = 1 << 24;
+constexpr uint64_t kTreeDrainNs = 2000000000ull;
+
+struct Ring {                                  // a buffer of a ring and the parity of its current round
+    int i = 0;
+    uint32_t ph = 0;
+    template <int kN>
+    __device__ __forceinline__ void next() {
+        if (++i == kN) {
+            i = 0;
+            ph ^= 1;
+        }
+    }
+};
+
+// Waits for a phase.  After kTreeTests tests without it (each sleeps in hardware for a while;
+// some seconds in all) the call has failed: that is recorded, and from then on no wait of the
+// block waits, so that it ends soon, with outputs that are not valid.
+__device__ __forceinline__ void tree_wait(uint32_t bar, uint32_t parity, volatile int32_t *dead, uint32_t *err) {
+    if (__builtin_expect(mbar_try_wait(bar, parity), 1)) return;
+    int left = kTreeTests;
+#pragma unroll 1
+    while (!mbar_try_wait(bar, parity)) {
+        if (__builtin_expect((--left & 0xFFF) == 0, 0)) {
+            if (left <= 0) {
+                *dead = 1;
+                atomicOr(err, FKV_DEVERR_TIMEOUT);
+            }
+            if (*dead) return;
+        }
+    }
+}
+
+// ---------------------------------------------------------------------------
 // the other parts of a call (host)
 // ---------------------------------------------------------------------------
 // Joins the parts of cut units (tree_attn.cu).
 cudaError_t launch_tree_join(const TreeParams &p, int shares, int rows, cudaStream_t st);
+// The kernel of more than 128 rows a unit, BF16 (tree_attn_wide.cu).
+constexpr int kTreeWideRows = 256;
+fkv_status launch_tree_wide(const TreeParams &p, int sms, const CUtensorMap &tmK, const CUtensorMap &tmV, cudaStream_t st);
 // The kernel of few rows a unit (tree_attn_small.cu): 16 or 32, FP8 or FP4.
 int tree_small_shares(int sms);
 constexpr int kTreeSmallTok = 32;              // its tiles' tokens

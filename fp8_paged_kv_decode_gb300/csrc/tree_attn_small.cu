@@ -68,37 +68,6 @@ __device__ __forceinline__ void k_fragments(uint32_t tile, int row, int g, int t
     }
 }
 
-// Which of the 32 tokens from t0 on row `tok` (of the call; -1: none) sees.
-__device__ __forceinline__ uint32_t seen_of(const TreeParams &p, const TreeUnit &u, int tok, uint32_t t0) {
-    if (tok < 0) return 0u;
-    auto below = [t0](int64_t x) {                                 // tokens before x
-        const int64_t d = x - t0;
-        return d >= 32 ? kAll : d <= 0 ? 0u : (1u << d) - 1u;
-    };
-    const int64_t at = static_cast<int64_t>(t0) - u.ctx;           // of the drafted tokens
-    uint64_t lo = 0, hi = 0;                                       // the mask words of tokens at and at + 32
-    int bits = 1;
-    if (p.mask) {
-        const uint64_t *m = p.mask + static_cast<int64_t>(tok) * p.words;
-        bits = 0;
-#pragma unroll
-        for (int i = 0; i < kTreeMaxWords; ++i) {
-            const uint64_t w = i < p.words ? __ldg(m + i) : 0ull;
-            bits += __popcll(w);
-            if (at >= 64 * i && at < 64 * i + 64) lo = w;
-            if (at + 63 >= 64 * i && at + 63 < 64 * i + 64) hi = w;
-        }
-    } else {
-        lo = at >= 0 && at < 64 ? 1ull : 0ull;
-        hi = at + 63 >= 0 && at + 63 < 64 ? 1ull : 0ull;
-    }
-    const int sh = static_cast<int>(at & 63);
-    const uint32_t drafted = static_cast<uint32_t>((lo >> sh) | (sh ? hi << (64 - sh) : 0ull));
-    uint32_t old = below(u.ctx);
-    if (p.window) old &= below(p.sinks) | ~below(static_cast<int64_t>(u.ctx) + max(bits - 1, 0) - p.window + 1);
-    return (old | (drafted & ~below(u.ctx))) & below(u.len);
-}
-
 template <int kKv, int kMB>
 __global__ void __launch_bounds__(SmallCfg<kKv, kMB>::kThreads, 1)
 tree_small_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV) {

@@ -1,0 +1,473 @@
+// tree_attn_wide.cu -- tree attention of many rows (more than 128 a KV head), BF16 cache.
+//
+// Here the products themselves are the work, so rows go on M: S = Q K^T and O += P V, both
+// 128 x 128 x 128, of two blocks of 128 rows that share every K and V tile.  A row is then a
+// lane of tensor memory and one thread of a softmax group: its reference, its sum and its
+// mask are that thread's own, no barrier or shuffle joins threads, and P replaces S where it
+// lies, as the second product's operand in tensor memory.  While one block's weights are
+// computed, the other's products run.
+//
+// Weights are two BF16 words (the first truncated, the second rounded): 16 bits of them, as
+// one word's 8 would be the largest error of the call.  So a tile costs a block three products
+// of 256 cycles and 16384 exponentials of 1024 cycles an SM; shared memory, which the tensor
+// cores read S's two operands and V twice from, about 1300.
+//
+// One CTA per SM, 12 warps: two softmax groups of four, a producer (a unit's geometry; K and V
+// tiles by turns into one ring of 32 KB stages), an issuer, two idle ones.
+#include <cudaTypedefs.h>
+
+#include <mutex>
+
+#include "tree_attn.cuh"
+#include "umma.cuh"
+
+namespace fkv {
+
+namespace wide {
+constexpr int kThreads = 384, kStages = 5, kStageB = 32768, kDesc = 4;
+constexpr int kQB = 32768;                                         // a block's Q
+constexpr int kOffRing = 2 * kQB, kOffCtrl = kOffRing + kStages * kStageB;
+constexpr int kProdW = 8, kMmaW = 9;
+// Registers of a thread at launch, then of the softmax warps, which hold a row's 128 logits, and of the others.
+constexpr int kRegs = 168, kRegsSoft = 216, kRegsRest = 72;
+static_assert(2 * kRegsSoft + kRegsRest <= kThreads / 128 * kRegs, "the block's registers");
+
+struct Ctrl {
+    uint64_t full[kStages], empty[kStages];
+    uint64_t qready[2], sfull[2], pready[2], odone[2];
+    uint64_t dfull[kDesc], dempty[kDesc], drained;
+    TreeUnit unit[kDesc];
+    uint32_t poison[kDesc][kTreePoison][4];                        // tokens whose V holds NaN or infinities
+    TreeShares<kThreads, 1> shares;
+    uint32_t tmem;
+    int32_t dead;
+};
+constexpr int kSmem = kOffCtrl + (static_cast<int>(sizeof(Ctrl)) + 15) / 16 * 16;
+static_assert(kSmem <= 232448, "shared memory of a CTA");
+
+// K's and V's places in the ring they share: every other stage each.
+struct Turn {
+    int i;
+    uint32_t ph = 0;
+    __device__ __forceinline__ void next() {
+        if ((i += 2) >= kStages) {
+            i -= kStages;
+            ph ^= 1;
+        }
+    }
+};
+}  // namespace wide
+
+__global__ void __launch_bounds__(wide::kThreads, 1)
+tree_wide_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV) {
+    using namespace wide;
+    extern __shared__ __align__(1024) uint8_t smem[];
+    Ctrl &ct = *reinterpret_cast<Ctrl *>(smem + kOffCtrl);
+    const uint32_t sQ = smem_u32(smem), sRing = sQ + kOffRing;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    volatile int32_t *dead = &ct.dead;
+    auto bar = [&](uint64_t &b) { return smem_u32(&b); };
+    auto wait = [&](uint64_t &b, uint32_t parity) { tree_wait(smem_u32(&b), parity, dead, p.err); };
+    if (tid == 0) {
+        for (int i = 0; i < kStages; ++i) mbar_init(bar(ct.full[i]), 1), mbar_init(bar(ct.empty[i]), 1);
+        for (int i = 0; i < 2; ++i)
+            mbar_init(bar(ct.qready[i]), 4), mbar_init(bar(ct.sfull[i]), 1), mbar_init(bar(ct.pready[i]), 4), mbar_init(bar(ct.odone[i]), 1);
+        for (int i = 0; i < kDesc; ++i) mbar_init(bar(ct.dfull[i]), 1), mbar_init(bar(ct.dempty[i]), 8 + 1);
+        mbar_init(bar(ct.drained), 1);
+        ct.dead = 0;
+        fence_mbar_init();
+    }
+    if (warp == kMmaW) tmem_alloc(smem_u32(&ct.tmem), 512);
+    if (warp == kProdW && lane == 0) prefetch_tensormap(&tmK), prefetch_tensormap(&tmV);
+
+    grid_dep_wait();                                               // lengths, tables and cache of earlier kernels
+    const int tpt = kTreeWideRows / p.group;                       // tokens of a unit's rows
+    const TreeTotal total = tree_shares<kTreeTok, kThreads, 1>(p, tpt, ct.shares);
+    umma_fence_before();
+    __syncthreads();
+    umma_fence_after();
+    const uint32_t tmem = ct.tmem;
+    grid_dep_launch();
+
+    if (warp >= kProdW) {
+        regs_down<kRegsRest>();
+        if (warp == kProdW) {
+        // ==== producer ====
+        const int64_t g1 = total.begin(blockIdx.x + 1);
+        int r = ct.shares.r[0];
+        int64_t off = ct.shares.off[0], left = g1 - total.begin(blockIdx.x);
+        int4 join = make_int4(-1, 0, 0, 0);
+        Ring d;
+        Turn k{0}, v{1};
+        const int npg = kTreeTok / p.page_size;
+        const uint64_t policy = l2_policy_evict_normal();
+        for (; left > 0 && r < p.batch && !*dead; ++r, off = 0) {
+            const TreeRequest q = tree_request(p, r);
+            if (!q.live) continue;
+            const TreeSpan sp = tree_span<kTreeTok>(p, q);
+            const int mt = (q.n + tpt - 1) / tpt, units = mt * p.hkv;
+            for (int ui = static_cast<int>(off / sp.tiles), tb = static_cast<int>(off % sp.tiles); ui < units && left > 0; ++ui, tb = 0) {
+                wait(ct.dempty[d.i], d.ph ^ 1);
+                if (*dead) break;                                  // others may still read what is there
+                TreeUnit u;
+                const int m = ui % mt;
+                u.tb = tb;
+                u.te = left < sp.tiles - tb ? tb + static_cast<int>(left) : sp.tiles;
+                u.tok0 = q.t0 + m * tpt;
+                u.ntok = min(tpt, q.n - m * tpt);
+                u.ctx = q.len - q.n;
+                u.len = q.len;
+                u.start = sp.start;
+                u.sink_tiles = sp.sink_tiles;
+                u.head = sp.head;
+                unit_whole<kTreeTok>(p, u);
+                u.row = q.row;
+                u.h = ui / mt;
+                u.slot = tb == 0 && u.te == sp.tiles ? -1 : 2 * static_cast<int>(blockIdx.x) + (tb == 0 ? 1 : 0);
+                u.bad = u.odd = 0;
+                if (lane == 0) ct.unit[d.i] = u;
+                for (int i = lane; i < 4 * kTreePoison; i += 32) (&ct.poison[d.i][0][0])[i] = 0;
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar(ct.dfull[d.i]));
+                // the last part of a unit that other CTAs began: its first tile's CTA
+                if (tb > 0 && u.te == sp.tiles) join = make_int4(static_cast<int>(total.of(g1 - left - tb)), u.tok0, u.ntok, u.h);
+                auto page = [&](int i) -> int32_t {                // this lane's page of tile i; -1: none to copy
+                    const uint32_t t = tile_at<kTreeTok>(u, i) + static_cast<uint32_t>(lane) * p.page_size;
+                    return lane < npg && t < tile_end(u, i) ? __ldg(p.indices + u.row + t / p.page_size) : -1;
+                };
+                int32_t pg_next = page(tb);
+                for (int i = tb; i < u.te; ++i) {
+                    int32_t pg = pg_next;
+                    const bool has = lane < npg && tile_at<kTreeTok>(u, i) + static_cast<uint32_t>(lane) * p.page_size < tile_end(u, i);
+                    if (i + 1 < u.te) pg_next = page(i + 1);
+                    if (__any_sync(kAll, has && static_cast<uint32_t>(pg) >= static_cast<uint32_t>(p.pages))) {
+                        if (static_cast<uint32_t>(pg) >= static_cast<uint32_t>(p.pages)) pg = 0;   // never dereferenced: the unit's rows become zeros
+                        if (lane == 0) {
+                            *const_cast<volatile int32_t *>(&ct.unit[d.i].bad) = 1;
+                            atomicOr(p.err, FKV_DEVERR_ATTN_PAGE);
+                        }
+                    }
+                    const uint32_t bytes = __popc(__ballot_sync(kAll, has)) * p.page_size * 256;
+                    auto copy = [&](Turn &at, const CUtensorMap *tm) {
+                        wait(ct.empty[at.i], at.ph ^ 1);
+                        const uint32_t dst = sRing + at.i * kStageB + lane * p.page_size * 128, full = bar(ct.full[at.i]);
+                        if (lane == 0) mbar_arrive_expect_tx(full, bytes);
+                        __syncwarp();
+                        if (has) {
+                            tma_load_4d(dst, tm, full, 0, 0, u.h, pg, policy);
+                            tma_load_4d(dst + 16384, tm, full, 64, 0, u.h, pg, policy);
+                        }
+                        __syncwarp();
+                        at.next();
+                    };
+                    copy(k, &tmK);
+                    copy(v, &tmV);
+                }
+                left -= u.te - u.tb;
+                d.template next<kDesc>();
+            }
+        }
+        wait(ct.dempty[d.i], d.ph ^ 1);
+        if (lane == 0 && !*dead) {
+            ct.unit[d.i].te = -1;
+            mbar_arrive(bar(ct.dfull[d.i]));
+        }
+        if (lane == 0) p.joins[blockIdx.x] = join;
+        __syncwarp();
+        // after a wait that gave up, the copies in flight still land in this CTA's memory
+        if (*dead) {
+            const uint64_t t0 = globaltimer_ns();
+            while (globaltimer_ns() - t0 < 200000000ull) __nanosleep(1000);
+        }
+        } else if (warp == kMmaW) {
+        // ==== issuer ====
+        constexpr uint32_t kHi = umma_desc_hi(1024);
+        constexpr uint32_t idS = umma_idesc(true, false, false, 128, 128), idO = umma_idesc(true, false, true, 128, 128);
+        const uint32_t lQ = umma_desc_lo(sQ, 16), lK = umma_desc_lo(sRing, 16), lV = umma_desc_lo(sRing, 16384);
+        Ring d;
+        Turn k{0}, v{1};
+        uint32_t nq[2] = {0, 0}, np[2] = {0, 0};
+        while (true) {
+            wait(ct.dfull[d.i], d.ph);
+            const int tb = *const_cast<volatile int32_t *>(&ct.unit[d.i].tb), te = *const_cast<volatile int32_t *>(&ct.unit[d.i].te);
+            const int blocks = *const_cast<volatile int32_t *>(&ct.unit[d.i].ntok) * p.group > 128 ? 2 : 1;
+            if (__any_sync(kAll, te < 0 || *dead)) break;
+            if (elect_one()) mbar_arrive(bar(ct.dempty[d.i]));
+            d.template next<kDesc>();
+            for (int i = tb - 1; i < te; ++i) {
+                // O of tile i, then S of the tile after it, block after block
+                const int vi = v.i;
+#pragma unroll
+                for (int g = 0; g < 2; ++g) {
+                    if (g == blocks) break;
+                    if (i >= tb) {
+                        if (g == 0) wait(ct.full[v.i], v.ph);
+                        wait(ct.pready[g], np[g]++ & 1);
+                        umma_fence_after();
+                        __syncwarp();
+                        if (elect_one()) {
+#pragma unroll
+                            for (int kk = 0; kk < 16; ++kk)
+                                umma_ts(tmem + 256 + 128 * g, tmem + 128 * g + kk * 8, umma_desc(lV + vi * (kStageB / 16) + (kk & 7) * 128, kHi), idO,
+                                        i > tb || kk > 0);
+                            umma_commit(bar(ct.odone[g]));
+                            if (g + 1 == blocks) umma_commit(bar(ct.empty[vi]));
+                        }
+                        __syncwarp();
+                    }
+                    if (i + 1 < te) {
+                        if (i < tb) wait(ct.qready[g], nq[g]++ & 1);
+                        if (g == 0) wait(ct.full[k.i], k.ph);
+                        if (np[g]) wait(ct.odone[g], (np[g] - 1) & 1);     // S takes the place of the weights that O was made of
+                        umma_fence_after();
+                        __syncwarp();
+                        if (elect_one()) {
+#pragma unroll
+                            for (int kk = 0; kk < 8; ++kk) {
+                                const uint32_t at = (kk >> 2) * 1024 + (kk & 3) * 2;
+                                umma_ss(tmem + 128 * g, umma_desc(lQ + g * (kQB / 16) + at, kHi), umma_desc(lK + k.i * (kStageB / 16) + at, kHi), idS, kk > 0);
+                            }
+                            umma_commit(bar(ct.sfull[g]));
+                            if (g + 1 == blocks) umma_commit(bar(ct.empty[k.i]));
+                        }
+                        __syncwarp();
+                    }
+                }
+                if (i >= tb) v.next();
+                if (i + 1 < te) k.next();
+            }
+        }
+        __syncwarp();
+        if (elect_one()) umma_commit(bar(ct.drained));             // nothing is in flight when the block ends
+        __syncwarp();
+        mbar_wait_bounded(bar(ct.drained), 0, kTreeDrainNs);
+        }
+    } else {
+        // ==== softmax ====
+        regs_up<kRegsSoft>();
+        const int g = warp >> 2, gtid = tid & 127;
+        const uint32_t tlane = static_cast<uint32_t>(32 * (warp & 3)) << 16;
+        const uint32_t tS = tmem + tlane + 128 * g, tO = tmem + tlane + 256 + 128 * g;
+        const int row = 128 * g + gtid, rtok = row / p.group, rhead = row - rtok * p.group;    // this thread's row of a unit
+        const float c = p.scale_log2;
+        Ring d;
+        Turn v{1};
+        uint32_t n = 0;                                            // tiles of this block so far
+        auto load_q = [&](const TreeUnit &u) {
+            const int c16 = gtid & 15;
+#pragma unroll 1
+            for (int r8 = 0; r8 < 16; r8 += 8) {
+                uint4 x[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const int rr = 128 * g + (r8 + i) * 8 + (gtid >> 4), tk = rr / p.group;
+                    x[i] = make_uint4(0u, 0u, 0u, 0u);
+                    if (tk < u.ntok)
+                        x[i] = __ldg(reinterpret_cast<const uint4 *>(
+                                         p.q + (static_cast<int64_t>(u.tok0 + tk) * p.hq + u.h * p.group + (rr - tk * p.group)) * 128) + c16);
+                }
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const int rr = (r8 + i) * 8 + (gtid >> 4);
+                    st_shared_v4(sQ + g * kQB + (c16 >> 3) * 16384 + rr * 128 + (((c16 & 7) ^ (rr & 7)) << 4), x[i]);
+                }
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(ct.qready[g]));
+        };
+        wait(ct.dfull[0], 0);
+        if (!*dead && ct.unit[0].te >= 0 && 128 * g < ct.unit[0].ntok * p.group) load_q(ct.unit[0]);
+        while (true) {
+            const TreeUnit &u = ct.unit[d.i];
+            const int tb = u.tb, te = u.te;
+            if (__any_sync(kAll, te < 0 || *dead)) break;
+            const bool mine = 128 * g < u.ntok * p.group;
+            const int tok = rtok < u.ntok ? u.tok0 + rtok : -1;    // the row's token (of the call)
+            float ref = kTreeNone, l = 0.f;
+            int odd_tiles = 0;
+#pragma unroll 1
+            for (int i = tb; i < te && mine; ++i) {
+                wait(ct.sfull[g], n & 1);
+                umma_fence_after();
+                float s[4][32];
+#pragma unroll
+                for (int b = 0; b < 4; ++b) tmem_load(tS + 32 * b, s[b]);
+                const bool whole = tile_whole(u, i);
+                if (__builtin_expect(!whole, 0)) {
+                    const uint32_t t0 = tile_at<kTreeTok>(u, i);
+#pragma unroll
+                    for (int b = 0; b < 4; ++b) {
+                        const uint32_t see = seen_of(p, u, tok, t0 + 32 * b);
+#pragma unroll
+                        for (int j = 0; j < 32; ++j)
+                            if (!((see >> j) & 1)) s[b][j] = -INFINITY;
+                    }
+                }
+                float top = -INFINITY;
+#pragma unroll
+                for (int b = 0; b < 4; ++b)
+#pragma unroll
+                    for (int j = 0; j < 32; j += 2) top = fmaxf(top, fmaxf(s[b][j], s[b][j + 1]));
+                top *= c;
+                const bool move = top - ref > kTreeMost;
+                if (__builtin_expect(__any_sync(kAll, move), 0)) {
+                    const float to = move ? top - kTreeTop : ref, f = ex2(ref - to);
+                    if (i > tb) {
+                        wait(ct.odone[g], (n - 1) & 1);
+                        umma_fence_after();
+#pragma unroll 1
+                        for (int b = 0; b < 4; ++b) {
+                            float o[32];
+                            uint32_t w[32];
+                            tmem_load(tO + 32 * b, o);
+#pragma unroll
+                            for (int j = 0; j < 32; ++j) w[j] = __float_as_uint(move ? o[j] * f : o[j]);
+                            tmem_store(tO + 32 * b, w);
+                        }
+                    }
+                    if (move) l *= f;
+                    ref = to;
+                }
+                float l4[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                for (int hf = 0; hf < 2; ++hf) {
+                    uint32_t hi[32], lo[32];
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) {
+                        const float *x = &s[2 * hf + (j >> 4)][2 * (j & 15)];
+                        const float a = ex2(fmaf(x[0], c, -ref)), b = ex2(fmaf(x[1], c, -ref));
+                        l4[j & 1] += a;
+                        l4[2 + (j & 1)] += b;
+                        hi[j] = prmt(__float_as_uint(a), __float_as_uint(b), 0x7632u);
+                        lo[j] = pack_bf16x2(a - __uint_as_float(__float_as_uint(a) & 0xFFFF0000u), b - __uint_as_float(__float_as_uint(b) & 0xFFFF0000u));
+                    }
+                    tmem_store(tS + 32 * hf, hi);
+                    tmem_store(tS + 64 + 32 * hf, lo);
+                }
+                l += (l4[0] + l4[1]) + (l4[2] + l4[3]);
+                if (__builtin_expect(!whole, 0)) {
+                    if (g == 0) {                                  // both blocks' products with V come after this block's weights
+                        wait(ct.full[v.i], v.ph);
+                        if (clean_v<FKV_KV_BF16>(sRing + v.i * kStageB, gtid, tile_at<kTreeTok>(u, i) + gtid < tile_end(u, i))) {
+                            atomicOr(&ct.poison[d.i][min(odd_tiles, kTreePoison - 1)][gtid >> 5], 1u << (gtid & 31));
+                            *const_cast<volatile int32_t *>(&ct.unit[d.i].odd) = 1;
+                        }
+                        fence_proxy_async_smem();
+                    }
+                    ++odd_tiles;
+                }
+                tmem_store_wait();
+                umma_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar(ct.pready[g]));
+                ++n;
+                v.next();
+            }
+            // the next unit's Q, while the last products run
+            Ring e = d;
+            e.template next<kDesc>();
+            wait(ct.dfull[e.i], e.ph);
+            if (__any_sync(kAll, *dead != 0)) break;
+            const int nte = *const_cast<volatile int32_t *>(&ct.unit[e.i].te);
+            if (nte >= 0 && 128 * g < ct.unit[e.i].ntok * p.group) load_q(ct.unit[e.i]);
+            if (mine) {
+                wait(ct.odone[g], (n - 1) & 1);
+                umma_fence_after();
+                const bool wrong = *const_cast<volatile int32_t *>(&ct.unit[d.i].bad) != 0, cut = u.slot >= 0;
+                const int64_t at = static_cast<int64_t>(u.slot) * kTreeWideRows + row;
+                const float f = wrong || l == 0.f ? 0.f : 1.f / l;
+                __nv_bfloat16 *const out = p.out + (static_cast<int64_t>(tok) * p.hq + u.h * p.group + rhead) * 128;
+                if (cut && tok >= 0) p.part_ml[at] = make_float2(ref, wrong ? -1.f : l);
+#pragma unroll 1
+                for (int b = 0; b < 4; ++b) {
+                    float o[32];
+                    tmem_load(tO + 32 * b, o);
+                    if (tok < 0) continue;
+                    if (cut) {
+                        float4 *dst = reinterpret_cast<float4 *>(p.part_o + at * 128 + 32 * b);
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) dst[j] = make_float4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
+                    } else {
+                        uint4 *dst = reinterpret_cast<uint4 *>(out + 32 * b);
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            uint32_t w[4];
+#pragma unroll
+                            for (int x = 0; x < 4; ++x) w[x] = f == 0.f ? 0u : pack_bf16x2(o[8 * j + 2 * x] * f, o[8 * j + 2 * x + 1] * f);
+                            dst[j] = make_uint4(w[0], w[1], w[2], w[3]);
+                        }
+                    }
+                }
+                umma_fence_before();
+                if (__builtin_expect(*const_cast<volatile int32_t *>(&ct.unit[d.i].odd) && !wrong && tok >= 0, 0)) {
+                    // NaN and infinities of V that not every row sees: left out of the product, here for those who do
+                    int k = 0;
+#pragma unroll 1
+                    for (int i = tb; i < te; ++i) {
+                        if (tile_whole(u, i)) continue;
+                        const uint32_t t0 = tile_at<kTreeTok>(u, i);
+#pragma unroll 1
+                        for (int b = 0; b < kTreeTok; ++b) {
+                            if (!((*const_cast<volatile uint32_t *>(&ct.poison[d.i][min(k, kTreePoison - 1)][b >> 5]) >> (b & 31)) & 1)) continue;
+                            if (!sees(p, u, row_sight(p, u, tok, word_of(u, t0 + b)), t0 + b)) continue;
+#pragma unroll 1
+                            for (int dim = 0; dim < 128; ++dim) {
+                                const float add = odd_value<FKV_KV_BF16>(p, u, t0 + b, dim);
+                                if (add == 0.f) continue;
+                                if (cut) p.part_o[at * 128 + dim] += add;
+                                else out[dim] = __float2bfloat16_rn(__bfloat162float(out[dim]) + add);
+                            }
+                        }
+                        ++k;
+                    }
+                }
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(ct.dempty[d.i]));
+            d = e;
+        }
+        // ---- rows of requests without work ----
+        __syncwarp();
+        for (int r = blockIdx.x; r < p.batch; r += gridDim.x) {
+            const TreeRequest q = tree_request(p, r);
+            if (!q.rows || q.live) continue;
+            uint4 *o = reinterpret_cast<uint4 *>(p.out + static_cast<int64_t>(q.t0) * p.hq * 128);
+            const int64_t words = static_cast<int64_t>(q.n) * p.hq * 16;
+            for (int64_t i = tid; i < words; i += 256) o[i] = make_uint4(0u, 0u, 0u, 0u);
+        }
+        __syncwarp();
+    }
+    umma_fence_before();
+    __syncthreads();
+    if (warp == kMmaW) {
+        umma_fence_after();
+        tmem_free(tmem, 512);
+    }
+}
+
+// ---------------------------------------------------------------------------
+// host side
+// ---------------------------------------------------------------------------
+namespace {
+constexpr int kMaxDev = 64;
+std::mutex g_mu;
+unsigned long long g_ready[kMaxDev];                               // the context in which the kernel's shared memory was set
+}  // namespace
+
+fkv_status launch_tree_wide(const TreeParams &p, int sms, const CUtensorMap &tmK, const CUtensorMap &tmV, cudaStream_t st) {
+    int dev = -1;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDev) return FKV_ERR_CUDA;
+    {
+        std::lock_guard<std::mutex> lk(g_mu);
+        const unsigned long long ctx = current_context_id();
+        if (ctx == 0 || g_ready[dev] != ctx) {
+            if (cudaFuncSetAttribute(tree_wide_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, wide::kSmem) != cudaSuccess) return FKV_ERR_CUDA;
+            g_ready[dev] = current_context_id();
+        }
+    }
+    if (launch_pdl(tree_wide_kernel, dim3(sms), dim3(wide::kThreads), wide::kSmem, st, p, tmK, tmV) != cudaSuccess) return FKV_ERR_CUDA;
+    return launch_tree_join(p, sms, kTreeWideRows, st) == cudaSuccess ? FKV_OK : FKV_ERR_CUDA;
+}
+
+}  // namespace fkv

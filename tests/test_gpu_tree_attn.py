@@ -362,3 +362,71 @@ def test_python_refusals():
             fkv.paged_window_attn(**dict(win, **bad))
     with pytest.raises(fkv.FkvError):
         fkv.alloc_tree_workspace(2, 2, 7, 2)
+
+
+WIDE = [  # 128 to 1300 rows of a KV head, in units of 128 and 256
+    (16, 1, 16, [90, 0, 1000], [9, 30, 17]), (32, 1, 32, [130, 255, 256], [5, 8, 64]), (48, 2, 64, [700, 3], [11, 6]),
+    (128, 1, 128, [400, 127], [2, 3]), (20, 4, 16, [4000, 60], [33, 61]), (8, 8, 64, [500, 30], [256, 200]), (127, 1, 32, [77], [10])]
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("Hq,H,S,ctx,n", WIDE)
+def test_wide_units(kind, Hq, H, S, ctx, n):
+    import fp8_paged_kv_decode_gb300 as fkv
+    fkv.device_error()
+    c = Case(kind, Hq, H, S, ctx, n, seed=Hq + S)
+    out = c.tree()
+    c.check(out)
+    first = out.clone()
+    assert fkv.device_error() == 0
+    for window, sinks in ((1, 0), (70, 3), (200, 130), (3000, 1)):
+        c.check(c.tree(window=window, sinks=sinks), window, sinks)
+    assert (c.tree().view(-1).view(dtype=first.dtype) == first.view(-1)).all()
+
+
+@pytest.mark.parametrize("kind", KINDS)
+def test_wide_units_of_odd_values_and_bad_requests(kind):
+    """NaN and infinities where some rows do not look, bad pages, requests without work, rows that see nothing."""
+    import fp8_paged_kv_decode_gb300 as fkv
+    fkv.device_error()
+    ctx, n, S = [37, 300, 5, 600], [16, 29, 24, 20], 16
+    c = Case(kind, 32, 2, S, ctx, n, seed=31)
+    nan = {"fp8": 0x7F, "bf16": 0x7FC0, "fp4": 0x7F}[kind]
+
+    def put(cache, r, t, d, value):
+        pg, off = c.idx[c.ptr[r] + t // S], t % S
+        cache[pg, :, off, 64 + d // 16 if kind == "fp4" else d] = value
+    put(c.vc, 0, 37 + 2, 5, nan)
+    put(c.kc, 1, 300 + 4, 100, nan)
+    put(c.vc, 1, 300 + 8, 77, nan)
+    put(c.vc, 2, 5 + 23, 127, nan)
+    if kind == "bf16":
+        put(c.vc, 0, 37 + 4, 6, 0x7F80)
+        put(c.vc, 0, 37 + 7, 6, 0xFF80)
+        put(c.vc, 3, 600 + 9, 9, 0xFF80)
+    for r in range(4):
+        for t in range(ctx[r] + n[r], -(-(ctx[r] + n[r]) // S) * S):
+            put(c.kc, r, t, 3, nan)
+            put(c.vc, r, t, 50, nan)
+    c.check(c.tree())
+    c.sets[3], c.sets[20], c.sets[50] = 0, 0, 1 << 23
+    c.check(c.tree())
+    c.check(c.tree(window=13, sinks=2), 13, 2)
+    c = Case(kind, 32, 2, S, ctx, n, seed=32)
+    c.idx[c.ptr[1] + 7] = c.P
+    c.dead = np.array([0, 0, 1, 0])
+    out = c.tree()
+    c.check(out)
+    assert fkv.device_error() == fkv.DEVERR_ATTN_PAGE
+    got = bf16_out(out)
+    assert (got[c.tptr[1]:c.tptr[3]] == 0).all() and (np.abs(got[:c.tptr[1]]).max(-1) > 0).all()
+
+
+@pytest.mark.parametrize("kind", KINDS)
+def test_few_requests_in_many_parts(kind):
+    """A hundred parts of a unit, joined by all warps of a block; rows past the unit's in the last eight."""
+    c = Case(kind, 6, 1, 64, [30000, 9], [3, 1], seed=33)
+    c.check(c.tree())
+    c.check(c.tree(window=20000, sinks=70), 20000, 70)
+    c = Case(kind, 5, 1, 16, [40000], [1], seed=34, sets=[1])
+    c.check(c.window(window=39000, sinks=3), 39000, 3)
