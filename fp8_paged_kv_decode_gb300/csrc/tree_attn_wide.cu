@@ -7,13 +7,20 @@
 // lies, as the second product's operand in tensor memory.  While one block's weights are
 // computed, the other's products run.
 //
-// Weights are two BF16 words (the first truncated, the second rounded): 16 bits of them, as
-// one word's 8 would be the largest error of the call.  So a tile costs a block three products
-// of 256 cycles and 16384 exponentials of 1024 cycles an SM; shared memory, which the tensor
-// cores read S's two operands and V twice from, about 1300.
+// Weights are two BF16 words (the first truncated, the second what is left, rounded): 16 bits
+// of them, as one word's 8 would be the largest error of the call.  So a tile costs a block 24
+// products of 128 x 128 x 16, 80 cycles each at the rate of a large matrix product, and 16384
+// exponentials, 1024 cycles of an SM.
 //
-// One CTA per SM, 12 warps: two softmax groups of four, a producer (a unit's geometry; K and V
-// tiles by turns into one ring of 32 KB stages), an issuer, two idle ones.
+// 16 requests of 8192 tokens, 61 drafted, 64 query heads on 8: 320 us, 475 with tokens on M
+// (tree_attn.cu), 140 at the rate of a large product were a weight one word, 220 as it is.  What
+// is left is a block's chain, weights after S after O, which two blocks hide only in part.
+// Tried: S of half tiles, so that the softmax begins earlier, 424 us (the tensor cores drain
+// between products of different shapes); O of half tiles and an issuer that takes whichever
+// block is ready, 386; all 128 logits of a row in registers with the others' given up, 348.
+//
+// One CTA per SM, 10 warps: two softmax groups of four, a producer (a unit's geometry; K and V
+// tiles by turns into one ring of 32 KB stages), an issuer.
 #include <cudaTypedefs.h>
 
 #include <mutex>
@@ -24,13 +31,10 @@
 namespace fkv {
 
 namespace wide {
-constexpr int kThreads = 384, kStages = 5, kStageB = 32768, kDesc = 4;
+constexpr int kThreads = 320, kStages = 5, kStageB = 32768, kDesc = 4;
 constexpr int kQB = 32768;                                         // a block's Q
 constexpr int kOffRing = 2 * kQB, kOffCtrl = kOffRing + kStages * kStageB;
 constexpr int kProdW = 8, kMmaW = 9;
-// Registers of a thread at launch, then of the softmax warps, which hold a row's 128 logits, and of the others.
-constexpr int kRegs = 168, kRegsSoft = 216, kRegsRest = 72;
-static_assert(2 * kRegsSoft + kRegsRest <= kThreads / 128 * kRegs, "the block's registers");
 
 struct Ctrl {
     uint64_t full[kStages], empty[kStages];
@@ -56,6 +60,27 @@ struct Turn {
         }
     }
 };
+
+// Two fp32 operations an instruction.
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+    float2 r;
+    asm("{\n\t.reg .b64 a, b, c, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tmov.b64 c, {%6, %7};\n\tfma.rn.f32x2 d, a, b, c;\n\tmov.b64 {%0, %1}, d;\n\t}"
+        : "=f"(r.x), "=f"(r.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+    return r;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+    float2 r;
+    asm("{\n\t.reg .b64 a, b, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tadd.rn.f32x2 d, a, b;\n\tmov.b64 {%0, %1}, d;\n\t}"
+        : "=f"(r.x), "=f"(r.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return r;
+}
+// Two weights as two BF16 words each: the first truncated, the second what is left, rounded.
+__device__ __forceinline__ void split(float a, float b, uint32_t &hi, uint32_t &lo) {
+    const uint32_t x = __float_as_uint(a), y = __float_as_uint(b);
+    hi = prmt(x, y, 0x7632u);
+    const float2 r = add2(make_float2(a, b), make_float2(__uint_as_float((x & 0xFFFF0000u) ^ 0x80000000u), __uint_as_float((y & 0xFFFF0000u) ^ 0x80000000u)));
+    lo = pack_bf16x2(r.x, r.y);
+}
 }  // namespace wide
 
 __global__ void __launch_bounds__(wide::kThreads, 1)
@@ -90,7 +115,6 @@ tree_wide_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmK, co
     grid_dep_launch();
 
     if (warp >= kProdW) {
-        regs_down<kRegsRest>();
         if (warp == kProdW) {
         // ==== producer ====
         const int64_t g1 = total.begin(blockIdx.x + 1);
@@ -186,7 +210,7 @@ tree_wide_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmK, co
         const uint32_t lQ = umma_desc_lo(sQ, 16), lK = umma_desc_lo(sRing, 16), lV = umma_desc_lo(sRing, 16384);
         Ring d;
         Turn k{0}, v{1};
-        uint32_t nq[2] = {0, 0}, np[2] = {0, 0};
+        uint32_t nq[2] = {0, 0}, np[2] = {0, 0};                   // units and tiles of a block so far
         while (true) {
             wait(ct.dfull[d.i], d.ph);
             const int tb = *const_cast<volatile int32_t *>(&ct.unit[d.i].tb), te = *const_cast<volatile int32_t *>(&ct.unit[d.i].te);
@@ -196,7 +220,6 @@ tree_wide_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmK, co
             d.template next<kDesc>();
             for (int i = tb - 1; i < te; ++i) {
                 // O of tile i, then S of the tile after it, block after block
-                const int vi = v.i;
 #pragma unroll
                 for (int g = 0; g < 2; ++g) {
                     if (g == blocks) break;
@@ -208,10 +231,10 @@ tree_wide_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmK, co
                         if (elect_one()) {
 #pragma unroll
                             for (int kk = 0; kk < 16; ++kk)
-                                umma_ts(tmem + 256 + 128 * g, tmem + 128 * g + kk * 8, umma_desc(lV + vi * (kStageB / 16) + (kk & 7) * 128, kHi), idO,
-                                        i > tb || kk > 0);
+                                umma_ts(tmem + 256 + 128 * g, tmem + 128 * g + kk * 8,
+                                        umma_desc(lV + v.i * (kStageB / 16) + ((kk & 3) + 4 * (kk >> 3)) * 128, kHi), idO, i > tb || kk > 0);
                             umma_commit(bar(ct.odone[g]));
-                            if (g + 1 == blocks) umma_commit(bar(ct.empty[vi]));
+                            if (g + 1 == blocks) umma_commit(bar(ct.empty[v.i]));
                         }
                         __syncwarp();
                     }
@@ -244,7 +267,6 @@ tree_wide_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmK, co
         }
     } else {
         // ==== softmax ====
-        regs_up<kRegsSoft>();
         const int g = warp >> 2, gtid = tid & 127;
         const uint32_t tlane = static_cast<uint32_t>(32 * (warp & 3)) << 16;
         const uint32_t tS = tmem + tlane + 128 * g, tO = tmem + tlane + 256 + 128 * g;
@@ -290,62 +312,79 @@ tree_wide_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmK, co
             for (int i = tb; i < te && mine; ++i) {
                 wait(ct.sfull[g], n & 1);
                 umma_fence_after();
-                float s[4][32];
-#pragma unroll
-                for (int b = 0; b < 4; ++b) tmem_load(tS + 32 * b, s[b]);
+                // 64 logits at a time, their weights' two words in their place
                 const bool whole = tile_whole(u, i);
-                if (__builtin_expect(!whole, 0)) {
-                    const uint32_t t0 = tile_at<kTreeTok>(u, i);
-#pragma unroll
-                    for (int b = 0; b < 4; ++b) {
-                        const uint32_t see = seen_of(p, u, tok, t0 + 32 * b);
-#pragma unroll
-                        for (int j = 0; j < 32; ++j)
-                            if (!((see >> j) & 1)) s[b][j] = -INFINITY;
-                    }
-                }
-                float top = -INFINITY;
-#pragma unroll
-                for (int b = 0; b < 4; ++b)
-#pragma unroll
-                    for (int j = 0; j < 32; j += 2) top = fmaxf(top, fmaxf(s[b][j], s[b][j + 1]));
-                top *= c;
-                const bool move = top - ref > kTreeMost;
-                if (__builtin_expect(__any_sync(kAll, move), 0)) {
-                    const float to = move ? top - kTreeTop : ref, f = ex2(ref - to);
-                    if (i > tb) {
-                        wait(ct.odone[g], (n - 1) & 1);
-                        umma_fence_after();
+                float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll 1
-                        for (int b = 0; b < 4; ++b) {
-                            float o[32];
-                            uint32_t w[32];
-                            tmem_load(tO + 32 * b, o);
+                for (int at = 0; at < 128; at += 64) {
+                    float s[64];
+                    tmem_load(tS + at, s);
+                    if (__builtin_expect(!whole, 0)) {
+                        const uint32_t t0 = tile_at<kTreeTok>(u, i) + at;
+                        const uint64_t see = seen_of(p, u, tok, t0) | static_cast<uint64_t>(seen_of(p, u, tok, t0 + 32)) << 32;
 #pragma unroll
-                            for (int j = 0; j < 32; ++j) w[j] = __float_as_uint(move ? o[j] * f : o[j]);
-                            tmem_store(tO + 32 * b, w);
-                        }
+                        for (int j = 0; j < 64; ++j)
+                            if (!((see >> j) & 1)) s[j] = -INFINITY;
                     }
-                    if (move) l *= f;
-                    ref = to;
-                }
-                float l4[4] = {0.f, 0.f, 0.f, 0.f};
+                    float top = -INFINITY;
 #pragma unroll
-                for (int hf = 0; hf < 2; ++hf) {
+                    for (int j = 0; j < 64; j += 2) top = fmaxf(top, fmaxf(s[j], s[j + 1]));
+                    top *= c;
+                    const bool move = top - ref > kTreeMost;
+                    if (__builtin_expect(__any_sync(kAll, move), 0)) {
+                        // the sums so far, and the weights of the tile's first half, are scaled to the new reference
+                        const float to = move ? top - kTreeTop : ref, f = move ? ex2(ref - to) : 1.f;
+                        if (i > tb) {
+                            wait(ct.odone[g], (n - 1) & 1);
+                            umma_fence_after();
+#pragma unroll 1
+                            for (int b = 0; b < 128; b += 32) {
+                                float o[32];
+                                uint32_t w[32];
+                                tmem_load(tO + b, o);
+#pragma unroll
+                                for (int j = 0; j < 32; ++j) w[j] = __float_as_uint(move ? o[j] * f : o[j]);
+                                tmem_store(tO + b, w);
+                            }
+                        }
+                        if (at) {
+                            tmem_store_wait();
+#pragma unroll 1
+                            for (int b = 0; b < 32; b += 8) {
+                                float hi[8], lo[8];
+                                uint32_t wh[8], wl[8];
+                                tmem_load(tS + b, hi);
+                                tmem_load(tS + 32 + b, lo);
+#pragma unroll
+                                for (int j = 0; j < 8; ++j) {
+                                    const uint32_t x = __float_as_uint(hi[j]), y = __float_as_uint(lo[j]);
+                                    const float v0 = (__uint_as_float(x << 16) + __uint_as_float(y << 16)) * f;
+                                    const float v1 = (__uint_as_float(x & 0xFFFF0000u) + __uint_as_float(y & 0xFFFF0000u)) * f;
+                                    split(v0, v1, wh[j], wl[j]);
+                                }
+                                tmem_store(tS + b, wh);
+                                tmem_store(tS + 32 + b, wl);
+                            }
+                        }
+                        l *= f;
+                        sum[0].x *= f, sum[0].y *= f, sum[1].x *= f, sum[1].y *= f;
+                        ref = to;
+                    }
+                    const float2 c2 = make_float2(c, c), r2 = make_float2(-ref, -ref);
                     uint32_t hi[32], lo[32];
 #pragma unroll
                     for (int j = 0; j < 32; ++j) {
-                        const float *x = &s[2 * hf + (j >> 4)][2 * (j & 15)];
-                        const float a = ex2(fmaf(x[0], c, -ref)), b = ex2(fmaf(x[1], c, -ref));
-                        l4[j & 1] += a;
-                        l4[2 + (j & 1)] += b;
-                        hi[j] = prmt(__float_as_uint(a), __float_as_uint(b), 0x7632u);
-                        lo[j] = pack_bf16x2(a - __uint_as_float(__float_as_uint(a) & 0xFFFF0000u), b - __uint_as_float(__float_as_uint(b) & 0xFFFF0000u));
+                        float2 x = fma2(make_float2(s[2 * j], s[2 * j + 1]), c2, r2);
+                        x.x = ex2(x.x);
+                        x.y = ex2(x.y);
+                        sum[j & 1] = add2(sum[j & 1], x);
+                        split(x.x, x.y, hi[j], lo[j]);
                     }
-                    tmem_store(tS + 32 * hf, hi);
-                    tmem_store(tS + 64 + 32 * hf, lo);
+                    tmem_store(tS + at, hi);
+                    tmem_store(tS + at + 32, lo);
                 }
-                l += (l4[0] + l4[1]) + (l4[2] + l4[3]);
+                sum[0] = add2(sum[0], sum[1]);
+                l += sum[0].x + sum[0].y;
                 if (__builtin_expect(!whole, 0)) {
                     if (g == 0) {                                  // both blocks' products with V come after this block's weights
                         wait(ct.full[v.i], v.ph);

@@ -27,13 +27,19 @@ __device__ __forceinline__ void umma_fence_after() { asm volatile("tcgen05.fence
 // part of it, so that no use is scheduled before it).
 template <int kN>
 __device__ __forceinline__ void tmem_load(uint32_t addr, float (&r)[kN]) {
-    static_assert(kN == 8 || kN == 16 || kN == 32, "8, 16 or 32 columns");
+    static_assert(kN == 8 || kN == 16 || kN == 32 || kN == 64, "8, 16, 32 or 64 columns");
     if constexpr (kN == 8) {
         asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];\n\t"
                      "tcgen05.wait::ld.sync.aligned;" : FKV_R8(r, 0) : "r"(addr) : "memory");
     } else if constexpr (kN == 16) {
         asm volatile("tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n\t"
                      "tcgen05.wait::ld.sync.aligned;" : FKV_R16(r, 0) : "r"(addr) : "memory");
+    } else if constexpr (kN == 64) {
+        asm volatile("tcgen05.ld.sync.aligned.32x32b.x64.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+                     "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,"
+                     "%32,%33,%34,%35,%36,%37,%38,%39,%40,%41,%42,%43,%44,%45,%46,%47,"
+                     "%48,%49,%50,%51,%52,%53,%54,%55,%56,%57,%58,%59,%60,%61,%62,%63}, [%64];\n\t"
+                     "tcgen05.wait::ld.sync.aligned;" : FKV_R16(r, 0), FKV_R16(r, 16), FKV_R16(r, 32), FKV_R16(r, 48) : "r"(addr) : "memory");
     } else {
         asm volatile("tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
                      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];\n\t"

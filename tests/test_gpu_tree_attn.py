@@ -430,3 +430,21 @@ def test_few_requests_in_many_parts(kind):
     c.check(c.tree(window=20000, sinks=70), 20000, 70)
     c = Case(kind, 5, 1, 16, [40000], [1], seed=34, sets=[1])
     c.check(c.window(window=39000, sinks=3), 39000, 3)
+
+
+@pytest.mark.parametrize("kind", ["fp8", "bf16"])
+def test_wide_units_of_rising_logits(kind):
+    """Logits that grow along the tokens, by 150 nats in all and again: references move in either half of a tile."""
+    c = Case(kind, 16, 1, 64, [900, 333], [12, 17], seed=35)
+    one = np.uint16(0x3F80) if kind == "bf16" else np.uint8(0x38)
+    c.kc[..., 0], c.sm = 0, 0.3
+    if c.ks is not None:
+        c.ks[:] = 1.0
+    for r in range(2):
+        for t in range(49, int(c.lens[r]), 50):                        # 1, 2, 4, ... 128 times the query's first dim
+            c.kc[c.idx[c.ptr[r] + t // 64], :, t % 64, 0] = one + (t // 50 % 8 << (7 if kind == "bf16" else 3))
+    c.q[..., 0] = W.bf16_bits(np.full((1,), 4.0, np.float32))[0]
+    want, vmax, _ = c.ref()
+    got = bf16_out(c.tree())
+    # |z| up to 200: fp32 products and their sum leave 2^-24 * 200 * 12 < 2^-12 in an exponent of e, on both sides
+    assert (np.abs(got - want) <= 2.0 ** -8 * np.abs(want) + 2.0 ** -10 * vmax).all()
