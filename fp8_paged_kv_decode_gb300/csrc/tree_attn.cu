@@ -7,23 +7,35 @@
 // A decode step over a window is the same with one token a request.
 //
 // The n drafted tokens of a request and the G query heads of a KV head share its K and V,
-// so a unit of work is (request, KV head, up to kR of their n G rows): products of
-// 128-token tiles with kR columns, on the fifth-generation tensor cores with tokens (or
-// dims) on M and rows on N,
-//     S^T = K Q^T  [128 tokens][kR],   O^T = V^T P^T  [128 dims][kR],
-// so that few rows cost little and K and V pass through once for all of them.  kR is 16,
-// 32, 64 or 128: the smallest that holds G times the call's mean n.
+// so a unit of work is (request, KV head, up to kR of their n G rows).  Three kernels, by the
+// rows that G times the call's mean n come to, so that few rows cost little and K and V pass
+// through once for all of them:
+//   here               BF16 up to 128 rows, FP8 and FP4 33 and more: products of 128-token tiles
+//                      with kR = 16, 32, 64 or 128 columns, on the fifth-generation tensor
+//                      cores, tokens (or dims) on M and rows on N,
+//                          S^T = K Q^T  [128 tokens][kR],   O^T = V^T P^T  [128 dims][kR]
+//   tree_attn_small.cu FP8 and FP4 up to 32 rows
+//   tree_attn_wide.cu  BF16 beyond 128 rows
 //
 // One CTA per SM takes an equal share of all units' tiles (a unit may be cut; its parts are
 // joined by a second kernel).  Its warps:
 //   producer   a unit's geometry, and TMA copies of its pages into rings of K and V stages
-//   converters (FP8, FP4) K rows to f16 in tensor memory, V rows to f16 in shared memory,
-//              one token a thread; they also bring a unit's Q as f16 (BF16: as it is)
-//   issuer     the products, S of the next tile before O of this one
-//   softmax    two groups of four warps, each half of the columns, one token a thread:
-//              weights against a running reference, stored as the second product's operand
+//   converters (FP8, FP4) K rows to f16 in tensor memory, V rows to f16 in tensor memory (128
+//              rows, whose sums leave no room there: in shared memory); a unit's Q as f16,
+//              scaled by one power of two (BF16: as it is)
+//   issuers    a warp for S, one for O
+//   softmax    two groups of four warps, one token a thread: weights against a running
+//              reference, stored as the second product's operand.  Up to 64 rows the groups
+//              take turns at tiles, with references and sums of their own that are joined at a
+//              unit's end; with 128 each takes half of the columns
 // The reference of a column moves only when a weight would pass f16's range: a maximum is
-// put at 2^13, later ones may grow to 2^15.9, so sums are rescaled a few times per unit.
+// put at 2^10, later ones may grow to 2^15.9, so sums are rescaled a few times per unit.
+// FP8 and FP4 weights are one f16 word, BF16 ones two BF16 words.
+//
+// Few rows over BF16 are bound by memory (8 requests, window of 32768: 86 us, 93% of a copy's
+// rate); 64 requests around 16k tokens, 8 drafted, over FP8 nearly so (565 to 650 us from run to
+// run, 66 to 77%): there a tile's way through five kinds of warps, and the instruction cache
+// that their code shares, cost what is missing.
 #include <cudaTypedefs.h>
 
 #include <cmath>
@@ -58,15 +70,14 @@ struct TreeCfg {
     static constexpr int kPB = kR <= 32 ? 16384 : kParts * kPW;    // a weight buffer
     static constexpr int kQB = kR * 256;
     static constexpr int kV16 = kConv && !kVT ? 32768 : 0;
-        static constexpr int kGroups = kConv && kR <= 32 ? 2 : 1;      // converter groups: K and V, or one for both
+    static_assert(!kConv || kR >= 64, "fewer rows of FP8 and FP4: tree_attn_small.cu");
     // Softmax warps with many columns take registers of the others: of a thread, at launch, then
     // of the three kinds of warps (no more in all than at launch; whole groups of four warps).
     static constexpr bool kShift = kR >= 32;
-    static constexpr int kThreads = 256 + 128 * kGroups + 128;     // softmax, converters; producer, two issuers, an idle warp
-    static constexpr int kRegs = kGroups == 2 ? 96 : 128;
-    static constexpr int kRegsSoft = kGroups == 2 ? 120 : kR >= 64 ? 176 : 152, kRegsConv = kGroups == 2 ? 80 : kR >= 64 ? 88 : 104,
-                         kRegsRest = kGroups == 2 ? 80 : kR >= 64 ? 72 : 104;
-    static_assert(2 * kRegsSoft + kGroups * kRegsConv + kRegsRest <= kThreads / 128 * kRegs, "the block's registers");
+    static constexpr int kThreads = 512;                           // softmax 256, converters 128; producer, two issuers, an idle warp
+    static constexpr int kRegs = 128;
+    static constexpr int kRegsSoft = kR >= 64 ? 176 : 152, kRegsConv = kR >= 64 ? 88 : 104, kRegsRest = kR >= 64 ? 72 : 104;
+    static_assert(2 * kRegsSoft + kRegsConv + kRegsRest <= kThreads / 128 * kRegs, "the block's registers");
     static constexpr int kND = kR <= 64 ? 4 : 2;                   // units in flight
     static constexpr int kNC = kTurns ? kR : kR / 2;               // columns of a softmax thread
     static constexpr int kNS = kTurns ? 4 : 8;                     // softmax warps of a tile
@@ -305,7 +316,7 @@ tree_attn_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmK, co
     const uint32_t base = smem_u32(smem);
     const uint32_t sQ = base, sP = base + C::kOffP, sV16 = base + C::kOffV16, sK = base + C::kOffK, sV = base + C::kOffV;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    constexpr int kConvW = 8, kProdW = 8 + 4 * C::kGroups, kMmaW = kProdW + 1, kMmaW2 = kProdW + 2;
+    constexpr int kConvW = 8, kProdW = 12, kMmaW = kProdW + 1, kMmaW2 = kProdW + 2;
     volatile int32_t *dead = &ct.dead;
     auto bar = [&](uint64_t &b) { return smem_u32(&b); };
     auto wait = [&](uint64_t &b, uint32_t parity) { tree_wait(smem_u32(&b), parity, dead, p.err); };
@@ -322,7 +333,7 @@ tree_attn_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmK, co
         for (int i = 0; i < C::kNP; ++i) mbar_init(bar(ct.pfull[i]), C::kNS), mbar_init(bar(ct.pempty[i]), 1);
         mbar_init(bar(ct.qfull), 4), mbar_init(bar(ct.qempty), 1), mbar_init(bar(ct.oempty), 8), mbar_init(bar(ct.drained[0]), 1), mbar_init(bar(ct.drained[1]), 1);
         for (int i = 0; i < C::kND; ++i)
-            mbar_init(bar(ct.dfull[i]), 1), mbar_init(bar(ct.dempty[i]), 8 + 4 * C::kGroups + 2), mbar_init(bar(ct.cfull[i]), 4);
+            mbar_init(bar(ct.dfull[i]), 1), mbar_init(bar(ct.dempty[i]), 8 + 4 + 2), mbar_init(bar(ct.cfull[i]), 4);
         ct.dead = 0;
         fence_mbar_init();
     }
@@ -534,7 +545,6 @@ tree_attn_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmK, co
         // ==== converters ====
         if constexpr (C::kShift) regs_down<C::kRegsConv>();
         const int ctid = tid & 127, cw = ctid >> 5;
-        const bool do_k = C::kGroups == 1 || tid < 384, do_v = C::kGroups == 1 || tid >= 384;
         const uint32_t tlane = static_cast<uint32_t>(32 * cw) << 16;
         Ring d, k, kb, v, vb;
         uint32_t nu = 0;
@@ -542,76 +552,74 @@ tree_attn_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmK, co
             wait(ct.dfull[d.i], d.ph);
             const TreeUnit u = ct.unit[d.i];
             if (u.te < 0 || *dead) break;
-            if (do_k) {
-                // ---- the unit's Q ----
-                wait(ct.qempty, (nu & 1) ^ 1);
-                constexpr int kU = kR / 8 < 8 ? kR / 8 : 8;        // rows of a thread at a time
-                const int c16 = ctid & 15;
-                uint4 x[kU];
-                auto load = [&](int r8) {
+            // ---- the unit's Q ----
+            wait(ct.qempty, (nu & 1) ^ 1);
+            constexpr int kU = kR / 8 < 8 ? kR / 8 : 8;        // rows of a thread at a time
+            const int c16 = ctid & 15;
+            uint4 x[kU];
+            auto load = [&](int r8) {
 #pragma unroll
-                    for (int i = 0; i < kU; ++i) {
-                        const int row = (r8 + i) * 8 + (ctid >> 4), tk = row / p.group;
-                        x[i] = make_uint4(0u, 0u, 0u, 0u);
-                        if (tk < u.ntok)
-                            x[i] = __ldg(reinterpret_cast<const uint4 *>(
-                                             p.q + (static_cast<int64_t>(u.tok0 + tk) * p.hq + u.h * p.group + (row - tk * p.group)) * 128) + c16);
-                    }
-                };
-                float up = 1.f, cs = p.scale_log2;
-                if (C::kConv) {
-                    // f16 with a power of two that puts the unit's largest finite element into [2^14, 2^15): elements
-                    // down to 2^-32 of it stay exact
-                    uint32_t big = 0;
-#pragma unroll 1
-                    for (int r8 = 0; r8 < kR / 8; r8 += kU) {
-                        load(r8);
-#pragma unroll
-                        for (int i = 0; i < kU; ++i) {
-                            const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
-#pragma unroll
-                            for (int j = 0; j < 4; ++j) {
-                                const uint32_t lo = w[j] & 0x7FFFu, hi = (w[j] >> 16) & 0x7FFFu;
-                                big = max(big, max(lo < 0x7F80u ? lo : 0u, hi < 0x7F80u ? hi : 0u));
-                            }
-                        }
-                    }
-                    big = __reduce_max_sync(kAll, big);
-                    if (lane == 0) atomicMax(&ct.qmax[d.i], big);
-                    group_sync(4);
-                    int e = static_cast<int>(*const_cast<volatile uint32_t *>(&ct.qmax[d.i]) >> 7);
-                    e = max(e == 0 ? 141 : e, 15);
-                    up = __uint_as_float(static_cast<uint32_t>(268 - e) << 23);
-                    cs = cs * __ldg(p.k_scale + u.h) * __uint_as_float(static_cast<uint32_t>(e - 14) << 23);
+                for (int i = 0; i < kU; ++i) {
+                    const int row = (r8 + i) * 8 + (ctid >> 4), tk = row / p.group;
+                    x[i] = make_uint4(0u, 0u, 0u, 0u);
+                    if (tk < u.ntok)
+                        x[i] = __ldg(reinterpret_cast<const uint4 *>(
+                                         p.q + (static_cast<int64_t>(u.tok0 + tk) * p.hq + u.h * p.group + (row - tk * p.group)) * 128) + c16);
                 }
+            };
+            float up = 1.f, cs = p.scale_log2;
+            if (C::kConv) {
+                // f16 with a power of two that puts the unit's largest finite element into [2^14, 2^15): elements
+                // down to 2^-32 of it stay exact
+                uint32_t big = 0;
 #pragma unroll 1
                 for (int r8 = 0; r8 < kR / 8; r8 += kU) {
-                    if (!C::kConv || kU < kR / 8) load(r8);
+                    load(r8);
 #pragma unroll
                     for (int i = 0; i < kU; ++i) {
-                        const int row = (r8 + i) * 8 + (ctid >> 4);
-                        if (C::kConv) {
-                            uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+                        const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
 #pragma unroll
-                            for (int j = 0; j < 4; ++j)
-                                w[j] = pack_f16x2(__uint_as_float(w[j] << 16) * up, __uint_as_float(w[j] & 0xFFFF0000u) * up);
-                            x[i] = make_uint4(w[0], w[1], w[2], w[3]);
+                        for (int j = 0; j < 4; ++j) {
+                            const uint32_t lo = w[j] & 0x7FFFu, hi = (w[j] >> 16) & 0x7FFFu;
+                            big = max(big, max(lo < 0x7F80u ? lo : 0u, hi < 0x7F80u ? hi : 0u));
                         }
-                        st_shared_v4(sQ + (c16 >> 3) * (kR * 128) + row * 128 + (((c16 & 7) ^ (row & 7)) << 4), x[i]);
                     }
                 }
-                if (ctid == 0) ct.colscale[d.i] = cs;
-                fence_proxy_async_smem();
-                __syncwarp();
-                if (lane == 0) {
-                    mbar_arrive(bar(ct.qfull));
-                    mbar_arrive(bar(ct.cfull[d.i]));
+                big = __reduce_max_sync(kAll, big);
+                if (lane == 0) atomicMax(&ct.qmax[d.i], big);
+                group_sync(4);
+                int e = static_cast<int>(*const_cast<volatile uint32_t *>(&ct.qmax[d.i]) >> 7);
+                e = max(e == 0 ? 141 : e, 15);
+                up = __uint_as_float(static_cast<uint32_t>(268 - e) << 23);
+                cs = cs * __ldg(p.k_scale + u.h) * __uint_as_float(static_cast<uint32_t>(e - 14) << 23);
+            }
+#pragma unroll 1
+            for (int r8 = 0; r8 < kR / 8; r8 += kU) {
+                if (!C::kConv || kU < kR / 8) load(r8);
+#pragma unroll
+                for (int i = 0; i < kU; ++i) {
+                    const int row = (r8 + i) * 8 + (ctid >> 4);
+                    if (C::kConv) {
+                        uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+#pragma unroll
+                        for (int j = 0; j < 4; ++j)
+                            w[j] = pack_f16x2(__uint_as_float(w[j] << 16) * up, __uint_as_float(w[j] & 0xFFFF0000u) * up);
+                        x[i] = make_uint4(w[0], w[1], w[2], w[3]);
+                    }
+                    st_shared_v4(sQ + (c16 >> 3) * (kR * 128) + row * 128 + (((c16 & 7) ^ (row & 7)) << 4), x[i]);
                 }
+            }
+            if (ctid == 0) ct.colscale[d.i] = cs;
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+                mbar_arrive(bar(ct.qfull));
+                mbar_arrive(bar(ct.cfull[d.i]));
             }
             ++nu;
             int odd_tiles = 0;
             for (int i = u.tb; i < u.te; ++i) {
-                if (C::kConv && do_k) {
+                if (C::kConv) {
                     // ---- K: f16 rows in tensor memory ----
                     wait(ct.kfull[k.i], k.ph);
                     wait(ct.k16empty[kb.i], kb.ph ^ 1);
@@ -632,53 +640,49 @@ tree_attn_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmK, co
                     k.template next<C::kNK>();
                     kb.template next<2>();
                 }
-                if (do_v) {
-                    // ---- V: f16 in tensor memory, or rows in an operand buffer; BF16 as it lies ----
-                    wait(ct.vfull[v.i], v.ph);
-                    const uint32_t src = sV + v.i * C::kStageB;
-                    const bool whole = tile_whole(u, i);
-                    if (__builtin_expect(!whole, 0)) {
-                        if (clean_v<kKv>(src, ctid, tile_at<kTreeTok>(u, i) + ctid < tile_end(u, i))) {
-                            atomicOr(&ct.poison[d.i][min(odd_tiles, kTreePoison - 1)][ctid >> 5], 1u << (ctid & 31));
-                            *const_cast<volatile int32_t *>(&ct.unit[d.i].odd) = 1;
-                        }
-                        if (C::kConv) group_sync(5);               // a warp reads tokens of other warps too
-                        ++odd_tiles;
+                // ---- V: f16 in tensor memory, or rows in an operand buffer; BF16 as it lies ----
+                wait(ct.vfull[v.i], v.ph);
+                const uint32_t src = sV + v.i * C::kStageB;
+                const bool whole = tile_whole(u, i);
+                if (__builtin_expect(!whole, 0)) {
+                    if (clean_v<kKv>(src, ctid, tile_at<kTreeTok>(u, i) + ctid < tile_end(u, i))) {
+                        atomicOr(&ct.poison[d.i][min(odd_tiles, kTreePoison - 1)][ctid >> 5], 1u << (ctid & 31));
+                        *const_cast<volatile int32_t *>(&ct.unit[d.i].odd) = 1;
                     }
-                    constexpr int kF = C::kConv ? kKv : FKV_KV_FP8_E4M3;
-                    if (C::kConv) wait(ct.v16empty[vb.i & 1], vb.ph ^ 1);
-                    if constexpr (C::kVT) {
-                        umma_fence_after();
-                        convert_v_tmem<kF>(src, tmem + tlane + C::kTmV + vb.i * 64, cw, lane);
-                        tmem_store_wait();
-                        umma_fence_before();
-                    } else {
-                        if constexpr (C::kConv) convert_v<kF>(src, sV16 + vb.i * C::kV16, ctid);
-                    }
-                    if ((C::kConv && !C::kVT) || !whole) fence_proxy_async_smem();
-                    __syncwarp();
-                    if (lane == 0) {
-                        mbar_arrive(bar(ct.vready[vb.i]));
-                        if (C::kConv) mbar_arrive(bar(ct.vempty[v.i]));
-                    }
-                    v.template next<C::kNV>();
-                    vb.template next<C::kNVR>();
+                    if (C::kConv) group_sync(5);               // a warp reads tokens of other warps too
+                    ++odd_tiles;
                 }
+                constexpr int kF = C::kConv ? kKv : FKV_KV_FP8_E4M3;
+                if (C::kConv) wait(ct.v16empty[vb.i & 1], vb.ph ^ 1);
+                if constexpr (C::kVT) {
+                    umma_fence_after();
+                    convert_v_tmem<kF>(src, tmem + tlane + C::kTmV + vb.i * 64, cw, lane);
+                    tmem_store_wait();
+                    umma_fence_before();
+                } else {
+                    if constexpr (C::kConv) convert_v<kF>(src, sV16 + vb.i * C::kV16, ctid);
+                }
+                if ((C::kConv && !C::kVT) || !whole) fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) {
+                    mbar_arrive(bar(ct.vready[vb.i]));
+                    if (C::kConv) mbar_arrive(bar(ct.vempty[v.i]));
+                }
+                v.template next<C::kNV>();
+                vb.template next<C::kNVR>();
             }
             __syncwarp();
             if (lane == 0) mbar_arrive(bar(ct.dempty[d.i]));
             d.template next<C::kND>();
         }
         // ---- rows of requests without work ----
-        if (do_k) {
-            __syncwarp();
-            for (int r = blockIdx.x; r < p.batch; r += gridDim.x) {
-                const TreeRequest q = tree_request(p, r);
-                if (!q.rows || q.live) continue;
-                uint4 *o = reinterpret_cast<uint4 *>(p.out + static_cast<int64_t>(q.t0) * p.hq * 128);
-                const int64_t words = static_cast<int64_t>(q.n) * p.hq * 16;
-                for (int64_t i = ctid; i < words; i += 128) o[i] = make_uint4(0u, 0u, 0u, 0u);
-            }
+        __syncwarp();
+        for (int r = blockIdx.x; r < p.batch; r += gridDim.x) {
+            const TreeRequest q = tree_request(p, r);
+            if (!q.rows || q.live) continue;
+            uint4 *o = reinterpret_cast<uint4 *>(p.out + static_cast<int64_t>(q.t0) * p.hq * 128);
+            const int64_t words = static_cast<int64_t>(q.n) * p.hq * 16;
+            for (int64_t i = ctid; i < words; i += 128) o[i] = make_uint4(0u, 0u, 0u, 0u);
         }
     } else {
         // ==== softmax ====
