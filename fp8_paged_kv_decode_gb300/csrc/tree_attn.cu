@@ -38,6 +38,7 @@
 // that their code shares, cost what is missing.
 #include <cudaTypedefs.h>
 
+#include <algorithm>
 #include <cmath>
 #include <cstddef>
 #include <mutex>
@@ -1305,7 +1306,12 @@ extern "C" size_t paged_tree_attn_workspace_size(int32_t n_tokens, int32_t batch
     if (n_tokens < 0 || batch < 0 || num_q_heads <= 0 || num_kv_heads <= 0 || num_q_heads % num_kv_heads) return 0;
     if (head_dim != 128 || !known_kv(kv_dtype) || num_q_heads / num_kv_heads > 128) return 0;
     const int sms = device_sm_count();
-    return sms <= 0 ? 0 : tree_ws(sms, kv_dtype, rows_of(kv_dtype, n_tokens, batch, num_q_heads / num_kv_heads)).total;
+    // of any call of up to n_tokens tokens, however many requests they are of: fewer rows can mean more shares
+    const int group = num_q_heads / num_kv_heads, most = rows_of(kv_dtype, n_tokens, 1, group);
+    size_t need = 0;
+    for (int rows = rows_of(kv_dtype, 1, 1, group); rows <= most && sms > 0; rows *= 2)
+        need = std::max(need, tree_ws(sms, kv_dtype, rows).total);
+    return need;
 }
 
 extern "C" fkv_status paged_tree_attn(const void *q, int32_t n_tokens, int32_t num_q_heads, const void *k_cache,

@@ -77,7 +77,7 @@ __device__ __forceinline__ TreeSpan tree_span(const TreeParams &p, const TreeReq
         const int32_t lo = ctx - p.window + 1;
         s.start = lo - lo % p.page_size;
         s.head = min(p.sinks, lo);
-        s.sink_tiles = (s.head + kTok - 1) / kTok;
+        s.sink_tiles = s.head / kTok + (s.head % kTok != 0);
         if (s.start <= static_cast<int64_t>(s.sink_tiles) * kTok) s = TreeSpan{0, 0, 0, 0};
     }
     s.tiles = s.sink_tiles + (q.len - s.start - 1) / kTok + 1;
@@ -107,7 +107,7 @@ template <int kTok>
 __device__ __forceinline__ void unit_whole(const TreeParams &p, TreeUnit &u) {
     const int32_t far = p.window && u.len > p.window ? u.len - p.window : 0;       // the deepest row's first token, at most
     u.whole[2] = u.ctx > u.start ? u.sink_tiles + (u.ctx - u.start) / kTok : 0;
-    u.whole[1] = u.sink_tiles + (far > u.start ? (far - u.start + kTok - 1) / kTok : 0);
+    u.whole[1] = u.sink_tiles + (far > u.start ? (far - u.start - 1) / kTok + 1 : 0);
     u.whole[0] = p.window ? min(u.sink_tiles ? u.sink_tiles : u.whole[2], min(p.sinks, u.ctx) / kTok) : 0;
 }
 // Whether every row sees every token of tile i.

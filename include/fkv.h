@@ -564,7 +564,9 @@ FKV_API fkv_status kv_append_rope(const void *q, int64_t q_token_stride, int32_t
  * and out = softmax(sm_scale * q . k) v over what it sees, as in paged_decode_attn.
  * Bits of tokens that are not there are ignored.  A row that sees nothing is
  * zeros.  What a row does not see has no part in it, whatever it holds (NaN,
- * infinities).  Any order of the drafted tokens is taken; positions (depths) of
+ * infinities; but infinite V that every row of a request sees may give NaN).  Query
+ * elements down to 2^-32 of the largest among the rows of a KV head are exact over FP8
+ * and FP4, BF16 ones always.  Any order of the drafted tokens is taken; positions (depths) of
  * siblings are the caller's, in kv_append_rope.
  *
  *   q, out         bf16 [n_tokens][num_q_heads][head_dim], rows of request r at
@@ -574,14 +576,15 @@ FKV_API fkv_status kv_append_rope(const void *q, int64_t q_token_stride, int32_t
  *   window, sinks  0 and 0: no window (sinks has no effect without one)
  *   workspace      paged_tree_attn_workspace_size(...) bytes, 256-byte aligned, no
  *                  initialisation needed, not shared by calls that overlap on
- *                  the GPU (two captured graphs that may run at once need two)
+ *                  the GPU (two captured graphs that may run at once need two); one
+ *                  of more tokens fits a call of fewer
  *   the others     as in paged_decode_attn
  * Fail closed: the rows of a request that is aborted, has a malformed CSR row, has
  * n > seq_lens[r], n > 64 * mask_words, more tokens than its pages hold, or a page
  * that it reads outside [0, num_pages) (FKV_DEVERR_ATTN_PAGE) are zeros.  token_indptr
  * entries that are negative, decreasing or past n_tokens leave the request's rows
  * unwritten.
- * Deterministic: the same call gives the same bytes every time.
+ * Deterministic: the same call gives the same bytes every time.  Two launches.
  * Supported: head_dim 128, page_size in {16, 32, 64, 128}, up to 128 query heads
  * per KV head.  batch == 0 or n_tokens == 0 is a no-op.
  */

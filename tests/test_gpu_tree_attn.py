@@ -448,3 +448,46 @@ def test_wide_units_of_rising_logits(kind):
     got = bf16_out(c.tree())
     # |z| up to 200: fp32 products and their sum leave 2^-24 * 200 * 12 < 2^-12 in an exponent of e, on both sides
     assert (np.abs(got - want) <= 2.0 ** -8 * np.abs(want) + 2.0 ** -10 * vmax).all()
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("tree", [False, True])
+@pytest.mark.parametrize("window,sinks", [(300, 40), (1000, 0), (1, 200)])
+def test_lengths_near_the_largest(kind, tree, window, sinks):
+    """Requests of up to 2^31 - 1 tokens whose window and first tokens are those of short ones: the same outputs."""
+    import torch
+    S, long = 128, 2 ** 31 - 1
+    n = 3 if tree else 1
+    tail = [long % S + 9 * S, 77 + 9 * S]                             # the short requests: 2 first pages, the others the window's
+    c = Case(kind, 4, 1, S, [x - n for x in tail], [n, n], seed=36, sets=None if tree else [1, 1])
+    call = c.tree if tree else c.window
+    c.check(call(window=window, sinks=sinks), window, sinks)
+    lens = np.array([long, 2 ** 30 + 77], np.int64)
+    pages = -(-lens // S)
+    ptr = np.concatenate([[0], np.cumsum(pages)]).astype(np.int32)
+    idx = torch.zeros(int(ptr[-1]), dtype=torch.int32, device="cuda")
+    for r in range(2):
+        row = c.idx[c.ptr[r]:c.ptr[r + 1]]
+        idx[int(ptr[r]):int(ptr[r]) + 2] = dev(row[:2])
+        idx[int(ptr[r + 1]) - len(row) + 2:int(ptr[r + 1])] = dev(row[2:])
+    t = c.tensors()
+    t.update(page_indptr=dev(ptr), page_indices=idx, seq_lens=dev(lens.astype(np.int32)))
+    c.check(call(t, window=window, sinks=sinks), window, sinks)
+    if window == 1:                                                    # first tokens without end: all of the short request's
+        t = c.tensors()
+        c.check(call(t, window=1, sinks=2 ** 31 - 1), 1, 2 ** 31 - 1)
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("Hq,H", [(8, 2), (64, 8), (24, 1), (100, 1)])
+def test_a_workspace_of_more_tokens_fits_fewer(kind, Hq, H):
+    import fp8_paged_kv_decode_gb300 as fkv
+    kv = dict(fp8=fkv.KV_FP8_E4M3, bf16=fkv.KV_BF16, fp4=fkv.KV_FP4)[kind]
+    sizes = [fkv.paged_tree_attn_workspace_size(n, b, Hq, H, kv_dtype=kv) for n in (1, 2, 7, 30, 64, 300, 5000) for b in (1, 3, 64)]
+    assert sizes == sorted(sizes)
+    ws = fkv.alloc_tree_workspace(500, 64, Hq, H, kv)
+    for ctx, n in (([40], [1]), ([30, 5], [1, 3]), ([200], [33]), ([100], [60]), ([9] * 30, [1] * 30)):
+        c = Case(kind, Hq, H, 16, ctx, n, seed=37)
+        t = c.tensors()
+        t["workspace"] = ws
+        c.check(c.tree(t))
