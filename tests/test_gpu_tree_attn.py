@@ -458,7 +458,7 @@ def test_lengths_near_the_largest(kind, tree, window, sinks):
     import torch
     S, long = 128, 2 ** 31 - 1
     n = 3 if tree else 1
-    tail = [long % S + 9 * S, 77 + 9 * S]                             # the short requests: 2 first pages, the others the window's
+    tail = [long % S + 9 * S, 77 + 9 * S]                             # the short requests
     c = Case(kind, 4, 1, S, [x - n for x in tail], [n, n], seed=36, sets=None if tree else [1, 1])
     call = c.tree if tree else c.window
     c.check(call(window=window, sinks=sinks), window, sinks)
@@ -468,8 +468,8 @@ def test_lengths_near_the_largest(kind, tree, window, sinks):
     idx = torch.zeros(int(ptr[-1]), dtype=torch.int32, device="cuda")
     for r in range(2):
         row = c.idx[c.ptr[r]:c.ptr[r + 1]]
-        idx[int(ptr[r]):int(ptr[r]) + 2] = dev(row[:2])
-        idx[int(ptr[r + 1]) - len(row) + 2:int(ptr[r + 1])] = dev(row[2:])
+        idx[int(ptr[r]):int(ptr[r]) + 2] = dev(row[:2])                # the first tokens' pages, and at the end all of them
+        idx[int(ptr[r + 1]) - len(row):int(ptr[r + 1])] = dev(row)
     t = c.tensors()
     t.update(page_indptr=dev(ptr), page_indices=idx, seq_lens=dev(lens.astype(np.int32)))
     c.check(call(t, window=window, sinks=sinks), window, sinks)
@@ -491,3 +491,42 @@ def test_a_workspace_of_more_tokens_fits_fewer(kind, Hq, H):
         t = c.tensors()
         t["workspace"] = ws
         c.check(c.tree(t))
+
+
+def test_two_graphs_of_other_kernels_at_once():
+    """A window over a 4-bit cache and wide trees over BF16, replayed on two streams with lengths that change, and eagerly
+    on a third; the first replay's state does not reach the next."""
+    import torch
+    import fp8_paged_kv_decode_gb300 as fkv
+    a = Case("fp4", 32, 8, 16, [3000] * 40, [1] * 40, seed=41, sets=[1] * 40)
+    b = Case("bf16", 32, 2, 64, [2500, 300, 5], [20, 31, 11], seed=42)
+    e = Case("fp8", 16, 2, 32, [900, 2100, 5], [3, 4, 2], seed=43)
+    ta, tb, te = a.tensors(), b.tensors(), e.tensors()
+    pb, mb = dev(b.tptr), dev(T.words_of(b.sets, b.words).view(np.int64))
+    pe, me = dev(e.tptr), dev(T.words_of(e.sets, e.words).view(np.int64))
+    s1, s2, s3 = (torch.cuda.Stream() for _ in range(3))
+    torch.cuda.synchronize()
+    ga, gb = torch.cuda.CUDAGraph(), torch.cuda.CUDAGraph()
+    with torch.cuda.graph(ga):
+        fkv.paged_window_attn(**ta, window=777, sinks=5)
+    with torch.cuda.graph(gb):
+        fkv.paged_tree_attn(**tb, token_indptr=pb, tree_mask=mb)
+    for k in range(4):
+        for x, t in ((a, ta), (b, tb), (e, te)):
+            x.q = W.bf16_bits(x.rng.standard_normal(x.q.shape).astype(np.float32))
+            t["q"].copy_(dev(x.q, dtype=torch.bfloat16))
+            t["out"].fill_(float("nan"))
+        a.lens[:] = [3001 - (37 * k * i) % 3000 for i in range(40)]
+        b.lens[0] = 2520 - 800 * k
+        ta["seq_lens"].copy_(dev(a.lens))
+        tb["seq_lens"].copy_(dev(b.lens))
+        torch.cuda.synchronize()
+        with torch.cuda.stream(s1):
+            ga.replay()
+        with torch.cuda.stream(s2):
+            gb.replay()
+        fkv.paged_tree_attn(**te, token_indptr=pe, tree_mask=me, window=50, sinks=1, stream=s3.cuda_stream)
+        torch.cuda.synchronize()
+        a.check(ta["out"], 777, 5)
+        b.check(tb["out"])
+        e.check(te["out"], 50, 1)
