@@ -10,12 +10,12 @@
 // so a unit of work is (request, KV head, up to kR of their n G rows).  Three kernels, by the
 // rows that G times the call's mean n come to, so that few rows cost little and K and V pass
 // through once for all of them:
-//   here               BF16 up to 128 rows, FP8 and FP4 33 and more: products of 128-token tiles
+//   here               BF16 up to 128 rows, FP8 and FP4 33 to 128: products of 128-token tiles
 //                      with kR = 16, 32, 64 or 128 columns, on the fifth-generation tensor
 //                      cores, tokens (or dims) on M and rows on N,
 //                          S^T = K Q^T  [128 tokens][kR],   O^T = V^T P^T  [128 dims][kR]
 //   tree_attn_small.cu FP8 and FP4 up to 32 rows
-//   tree_attn_wide.cu  BF16 beyond 128 rows
+//   tree_attn_wide.cu  more
 //
 // One CTA per SM takes an equal share of all units' tiles (a unit may be cut; its parts are
 // joined by a second kernel).  Its warps:
@@ -160,59 +160,8 @@ __device__ __forceinline__ uint64_t seen_by(const TreeParams &p, const TreeUnit 
 }
 
 // ---------------------------------------------------------------------------
-// rows of the cache as f16 (this thread's token)
+// V as f16 in tensor memory
 // ---------------------------------------------------------------------------
-// 64 values (half `hf`) of the row in a K or V stage, as f16 pairs.
-template <int kKv>
-__device__ __forceinline__ void half_row(uint32_t stage, int tok, int hf, uint32_t (&f)[32]) {
-    if (kKv == FKV_KV_FP8_E4M3) {
-        const uint32_t row = stage + tok * 128;
-        uint4 v[4];                                                // all on their way before one is converted
-#pragma unroll
-        for (int c = 0; c < 4; ++c) v[c] = ld_shared_v4(row + (((4 * hf + c) ^ (tok & 7)) << 4));
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-            const uint32_t w[4] = {v[c].x, v[c].y, v[c].z, v[c].w};
-#pragma unroll
-            for (int j = 0; j < 4; ++j) e4m3x4_to_f16(w[j], f[8 * c + 2 * j], f[8 * c + 2 * j + 1]);
-        }
-    } else {
-        const uint32_t row = stage + tok * kFp4Row;
-        const uint2 sc = ld_shared_v2(row + kFp4Codes);
-        const uint32_t s4 = hf ? sc.y : sc.x;
-        uint2 cs[4];
-#pragma unroll
-        for (int b = 0; b < 4; ++b) cs[b] = ld_shared_v2(row + 32 * hf + 8 * b);
-#pragma unroll
-        for (int b = 0; b < 4; ++b) {
-            const uint2 c = cs[b];
-            const uint32_t s = e4m3_to_f16_pair((s4 >> (8 * b)) & 0xFFu);
-            uint32_t x[4], y[4];
-            e2m1x8_to_f16(c.x, x);
-            e2m1x8_to_f16(c.y, y);
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                f[8 * b + j] = mul_f16x2(x[j], s);
-                f[8 * b + 4 + j] = mul_f16x2(y[j], s);
-            }
-        }
-    }
-}
-
-// A V row as f16 into a 128 x 128 operand buffer (MN-major, two halves of 64 dims).
-template <int kKv>
-__device__ __forceinline__ void convert_v(uint32_t stage, uint32_t dst, int tok) {
-#pragma unroll 1
-    for (int hf = 0; hf < 2; ++hf) {
-        uint32_t f[32];
-        half_row<kKv>(stage, tok, hf, f);
-#pragma unroll
-        for (int c = 0; c < 8; ++c)
-            st_shared_v4(dst + 16384 * hf + tok * 128 + ((c ^ (tok & 7)) << 4),
-                         make_uint4(f[4 * c], f[4 * c + 1], f[4 * c + 2], f[4 * c + 3]));
-    }
-}
-
 // The V rows of a stage as f16 into tensor memory: dims on lanes, two tokens a column, from
 // column `dst` (of this warp's 32 lanes, dims 32 cw ..).  Thread l holds, of tokens 8k + 2 (l % 4)
 // and the next one, the places of the .16x128b store: register 2k of the lower (upper) 16 lanes
@@ -661,7 +610,7 @@ tree_attn_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmK, co
                     tmem_store_wait();
                     umma_fence_before();
                 } else {
-                    if constexpr (C::kConv) convert_v<kF>(src, sV16 + vb.i * C::kV16, ctid);
+                    if constexpr (C::kConv) convert_row<kF>(src, sV16 + vb.i * C::kV16, ctid);
                 }
                 if ((C::kConv && !C::kVT) || !whole) fence_proxy_async_smem();
                 __syncwarp();
@@ -1164,11 +1113,11 @@ bool known_kv(int kv) { return kv == FKV_KV_FP8_E4M3 || kv == FKV_KV_BF16 || kv 
 
 // Rows of a unit: the smallest instance that holds the query heads of the requests' mean
 // number of tokens.
-int rows_of(int kv, int64_t n_tokens, int64_t batch, int64_t group) {
+int rows_of(int64_t n_tokens, int64_t batch, int64_t group) {
     const int64_t want = group * ((n_tokens + batch - 1) / (batch > 0 ? batch : 1));
     for (int r = 16; r < 128; r *= 2)
         if (want <= r) return r;
-    return kv == FKV_KV_BF16 && want > 128 ? kTreeWideRows : 128;
+    return want > 128 ? kTreeWideRows : 128;
 }
 
 // Which kernel.  Up to 32 rows over FP8 or FP4 the products are little work, and the hand-overs of a tile from warp to warp
@@ -1248,7 +1197,7 @@ fkv_status attend(bool tree, const void *q, int32_t n_tokens, int32_t num_q_head
     uint32_t *err = device_error_word();
     const int sms = device_sm_count();
     if (!err || sms <= 0) return FKV_ERR_CUDA;
-    const int group = num_q_heads / num_kv_heads, rows = rows_of(kv_dtype, n_tokens, batch, group);
+    const int group = num_q_heads / num_kv_heads, rows = rows_of(n_tokens, batch, group);
     const TreeWs w = tree_ws(sms, kv_dtype, rows);
     const bool small = small_call(kv_dtype, rows);
     const int box = small ? kTreeSmallTok : kTreeTok;
@@ -1290,7 +1239,7 @@ fkv_status attend(bool tree, const void *q, int32_t n_tokens, int32_t num_q_head
     p.scale_log2 = sm_scale * 1.4426950408889634f;
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
     if (small) return launch_tree_small(p, kv_dtype, rows, sms, tmK, tmV, st);
-    if (rows == kTreeWideRows) return launch_tree_wide(p, sms, tmK, tmV, st);
+    if (rows == kTreeWideRows) return launch_tree_wide(p, kv_dtype, sms, tmK, tmV, st);
     return fp8                         ? launch_rows<FKV_KV_FP8_E4M3>(rows, p, sms, tmK, tmV, st)
            : kv_dtype == FKV_KV_BF16 ? launch_rows<FKV_KV_BF16>(rows, p, sms, tmK, tmV, st)
                                      : launch_rows<FKV_KV_FP4>(rows, p, sms, tmK, tmV, st);
@@ -1307,9 +1256,9 @@ extern "C" size_t paged_tree_attn_workspace_size(int32_t n_tokens, int32_t batch
     if (head_dim != 128 || !known_kv(kv_dtype) || num_q_heads / num_kv_heads > 128) return 0;
     const int sms = device_sm_count();
     // of any call of up to n_tokens tokens, however many requests they are of: fewer rows can mean more shares
-    const int group = num_q_heads / num_kv_heads, most = rows_of(kv_dtype, n_tokens, 1, group);
+    const int group = num_q_heads / num_kv_heads, most = rows_of(n_tokens, 1, group);
     size_t need = 0;
-    for (int rows = rows_of(kv_dtype, 1, 1, group); rows <= most && sms > 0; rows *= 2)
+    for (int rows = rows_of(1, 1, group); rows <= most && sms > 0; rows *= 2)
         need = std::max(need, tree_ws(sms, kv_dtype, rows).total);
     return need;
 }

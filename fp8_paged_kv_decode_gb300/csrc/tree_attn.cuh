@@ -348,13 +348,67 @@ __device__ __forceinline__ void tree_wait(uint32_t bar, uint32_t parity, volatil
 }
 
 // ---------------------------------------------------------------------------
+// rows of the cache as f16 (this thread's token)
+// ---------------------------------------------------------------------------
+// 64 values (half `hf`) of the row in a K or V stage, as f16 pairs.
+template <int kKv>
+__device__ __forceinline__ void half_row(uint32_t stage, int tok, int hf, uint32_t (&f)[32]) {
+    if (kKv == FKV_KV_FP8_E4M3) {
+        const uint32_t row = stage + tok * 128;
+        uint4 v[4];                                                // all on their way before one is converted
+#pragma unroll
+        for (int c = 0; c < 4; ++c) v[c] = ld_shared_v4(row + (((4 * hf + c) ^ (tok & 7)) << 4));
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+            const uint32_t w[4] = {v[c].x, v[c].y, v[c].z, v[c].w};
+#pragma unroll
+            for (int j = 0; j < 4; ++j) e4m3x4_to_f16(w[j], f[8 * c + 2 * j], f[8 * c + 2 * j + 1]);
+        }
+    } else {
+        const uint32_t row = stage + tok * kFp4Row;
+        const uint2 sc = ld_shared_v2(row + kFp4Codes);
+        const uint32_t s4 = hf ? sc.y : sc.x;
+        uint2 cs[4];
+#pragma unroll
+        for (int b = 0; b < 4; ++b) cs[b] = ld_shared_v2(row + 32 * hf + 8 * b);
+#pragma unroll
+        for (int b = 0; b < 4; ++b) {
+            const uint2 c = cs[b];
+            const uint32_t s = e4m3_to_f16_pair((s4 >> (8 * b)) & 0xFFu);
+            uint32_t x[4], y[4];
+            e2m1x8_to_f16(c.x, x);
+            e2m1x8_to_f16(c.y, y);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                f[8 * b + j] = mul_f16x2(x[j], s);
+                f[8 * b + 4 + j] = mul_f16x2(y[j], s);
+            }
+        }
+    }
+}
+
+// A row as f16 into a 128 x 128 operand buffer (two halves of 64 dims; of V MN-major, of K K-major).
+template <int kKv>
+__device__ __forceinline__ void convert_row(uint32_t stage, uint32_t dst, int tok) {
+#pragma unroll 1
+    for (int hf = 0; hf < 2; ++hf) {
+        uint32_t f[32];
+        half_row<kKv>(stage, tok, hf, f);
+#pragma unroll
+        for (int c = 0; c < 8; ++c)
+            st_shared_v4(dst + 16384 * hf + tok * 128 + ((c ^ (tok & 7)) << 4),
+                         make_uint4(f[4 * c], f[4 * c + 1], f[4 * c + 2], f[4 * c + 3]));
+    }
+}
+
+// ---------------------------------------------------------------------------
 // the other parts of a call (host)
 // ---------------------------------------------------------------------------
 // Joins the parts of cut units (tree_attn.cu).
 cudaError_t launch_tree_join(const TreeParams &p, int shares, int rows, cudaStream_t st);
-// The kernel of more than 128 rows a unit, BF16 (tree_attn_wide.cu).
+// The kernel of more than 128 rows a unit (tree_attn_wide.cu).
 constexpr int kTreeWideRows = 256;
-fkv_status launch_tree_wide(const TreeParams &p, int sms, const CUtensorMap &tmK, const CUtensorMap &tmV, cudaStream_t st);
+fkv_status launch_tree_wide(const TreeParams &p, int kv, int sms, const CUtensorMap &tmK, const CUtensorMap &tmV, cudaStream_t st);
 // The kernel of few rows a unit (tree_attn_small.cu): 16 or 32, FP8 or FP4.
 int tree_small_shares(int sms);
 constexpr int kTreeSmallTok = 32;              // its tiles' tokens

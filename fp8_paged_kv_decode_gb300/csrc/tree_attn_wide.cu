@@ -1,4 +1,4 @@
-// tree_attn_wide.cu -- tree attention of many rows (more than 128 a KV head), BF16 cache.
+// tree_attn_wide.cu -- tree attention of many rows (more than 128 a KV head).
 //
 // Here the products themselves are the work, so rows go on M: S = Q K^T and O += P V, both
 // 128 x 128 x 128, of two blocks of 128 rows that share every K and V tile.  A row is then a
@@ -7,7 +7,7 @@
 // lies, as the second product's operand in tensor memory.  While one block's weights are
 // computed, the other's products run.
 //
-// Weights are two BF16 words (the first truncated, the second what is left, rounded): 16 bits
+// Over BF16 weights are two words (the first truncated, the second what is left, rounded): 16 bits
 // of them, as one word's 8 would be the largest error of the call.  So a tile costs a block 24
 // products of 128 x 128 x 16, 80 cycles each at the rate of a large matrix product, and 16384
 // exponentials, 1024 cycles of an SM.
@@ -31,28 +31,43 @@
 namespace fkv {
 
 namespace wide {
-constexpr int kThreads = 320, kStages = 5, kStageB = 32768, kDesc = 4;
-constexpr int kQB = 32768;                                         // a block's Q
-constexpr int kOffRing = 2 * kQB, kOffCtrl = kOffRing + kStages * kStageB;
-constexpr int kProdW = 8, kMmaW = 9;
+constexpr int kDesc = 4;
+constexpr int kQB = 32768, kStageB = 32768;                        // a block's Q; a K or V tile as an operand
+constexpr int kProdW = 8, kMmaW = 9, kConvW = 10;
 
+template <int kKv>
+struct Cfg {
+    static constexpr bool kConv = kKv != FKV_KV_BF16;              // K and V become f16 here
+    static constexpr int kThreads = kConv ? 448 : 320;
+    static constexpr int kStages = kConv ? 4 : 5;                  // of operands, K's and V's by turns
+    static constexpr int kRowB = kKv == FKV_KV_FP8_E4M3 ? 128 : kKv == FKV_KV_BF16 ? 256 : kFp4Row;
+    static constexpr int kRaw = !kConv ? 1 : kKv == FKV_KV_FP4 ? 3 : 2, kRawB = kConv ? kTreeTok * kRowB : 0;     // of rows as they lie in the cache
+    static constexpr int kOffRing = 2 * kQB, kOffRaw = kOffRing + kStages * kStageB, kOffCtrl = kOffRaw + kRaw * kRawB;
+};
+template <int kKv>
 struct Ctrl {
-    uint64_t full[kStages], empty[kStages];
+    using C = Cfg<kKv>;
+    uint64_t full[C::kStages], empty[C::kStages], rfull[C::kRaw], rempty[C::kRaw];
     uint64_t qready[2], sfull[2], pready[2], odone[2];
     uint64_t dfull[kDesc], dempty[kDesc], drained;
     TreeUnit unit[kDesc];
     uint32_t poison[kDesc][kTreePoison][4];                        // tokens whose V holds NaN or infinities
-    TreeShares<kThreads, 1> shares;
+    TreeShares<C::kThreads, 1> shares;
     uint32_t tmem;
     int32_t dead;
 };
-constexpr int kSmem = kOffCtrl + (static_cast<int>(sizeof(Ctrl)) + 15) / 16 * 16;
-static_assert(kSmem <= 232448, "shared memory of a CTA");
+template <int kKv>
+constexpr int smem_bytes() {
+    constexpr int n = Cfg<kKv>::kOffCtrl + (static_cast<int>(sizeof(Ctrl<kKv>)) + 15) / 16 * 16;
+    static_assert(n <= 232448, "shared memory of a CTA");
+    return n;
+}
 
 // K's and V's places in the ring they share: every other stage each.
 struct Turn {
     int i;
     uint32_t ph = 0;
+    template <int kStages>
     __device__ __forceinline__ void next() {
         if ((i += 2) >= kStages) {
             i -= kStages;
@@ -83,39 +98,41 @@ __device__ __forceinline__ void split(float a, float b, uint32_t &hi, uint32_t &
 }
 }  // namespace wide
 
-__global__ void __launch_bounds__(wide::kThreads, 1)
+template <int kKv>
+__global__ void __launch_bounds__(wide::Cfg<kKv>::kThreads, 1)
 tree_wide_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV) {
     using namespace wide;
+    using C = Cfg<kKv>;
     extern __shared__ __align__(1024) uint8_t smem[];
-    Ctrl &ct = *reinterpret_cast<Ctrl *>(smem + kOffCtrl);
-    const uint32_t sQ = smem_u32(smem), sRing = sQ + kOffRing;
+    Ctrl<kKv> &ct = *reinterpret_cast<Ctrl<kKv> *>(smem + C::kOffCtrl);
+    const uint32_t sQ = smem_u32(smem), sRing = sQ + C::kOffRing, sRaw = sQ + C::kOffRaw;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     volatile int32_t *dead = &ct.dead;
     auto bar = [&](uint64_t &b) { return smem_u32(&b); };
     auto wait = [&](uint64_t &b, uint32_t parity) { tree_wait(smem_u32(&b), parity, dead, p.err); };
     if (tid == 0) {
-        for (int i = 0; i < kStages; ++i) mbar_init(bar(ct.full[i]), 1), mbar_init(bar(ct.empty[i]), 1);
+        for (int i = 0; i < C::kStages; ++i) mbar_init(bar(ct.full[i]), C::kConv ? 4 : 1), mbar_init(bar(ct.empty[i]), 1);
+        for (int i = 0; i < C::kRaw; ++i) mbar_init(bar(ct.rfull[i]), 1), mbar_init(bar(ct.rempty[i]), 4);
         for (int i = 0; i < 2; ++i)
             mbar_init(bar(ct.qready[i]), 4), mbar_init(bar(ct.sfull[i]), 1), mbar_init(bar(ct.pready[i]), 4), mbar_init(bar(ct.odone[i]), 1);
-        for (int i = 0; i < kDesc; ++i) mbar_init(bar(ct.dfull[i]), 1), mbar_init(bar(ct.dempty[i]), 8 + 1);
+        for (int i = 0; i < kDesc; ++i) mbar_init(bar(ct.dfull[i]), 1), mbar_init(bar(ct.dempty[i]), 8 + 1 + (C::kConv ? 4 : 0));
         mbar_init(bar(ct.drained), 1);
         ct.dead = 0;
         fence_mbar_init();
     }
     if (warp == kMmaW) tmem_alloc(smem_u32(&ct.tmem), 512);
-    if (warp == kProdW && lane == 0) prefetch_tensormap(&tmK), prefetch_tensormap(&tmV);
+    if (kKv != FKV_KV_FP4 && warp == kProdW && lane == 0) prefetch_tensormap(&tmK), prefetch_tensormap(&tmV);
 
     grid_dep_wait();                                               // lengths, tables and cache of earlier kernels
     const int tpt = kTreeWideRows / p.group;                       // tokens of a unit's rows
-    const TreeTotal total = tree_shares<kTreeTok, kThreads, 1>(p, tpt, ct.shares);
+    const TreeTotal total = tree_shares<kTreeTok, C::kThreads, 1>(p, tpt, ct.shares);
     umma_fence_before();
     __syncthreads();
     umma_fence_after();
     const uint32_t tmem = ct.tmem;
     grid_dep_launch();
 
-    if (warp >= kProdW) {
-        if (warp == kProdW) {
+    if (warp == kProdW) {
         // ==== producer ====
         const int64_t g1 = total.begin(blockIdx.x + 1);
         int r = ct.shares.r[0];
@@ -123,6 +140,7 @@ tree_wide_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmK, co
         int4 join = make_int4(-1, 0, 0, 0);
         Ring d;
         Turn k{0}, v{1};
+        Ring raw;
         const int npg = kTreeTok / p.page_size;
         const uint64_t policy = l2_policy_evict_normal();
         for (; left > 0 && r < p.batch && !*dead; ++r, off = 0) {
@@ -171,21 +189,36 @@ tree_wide_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmK, co
                             atomicOr(p.err, FKV_DEVERR_ATTN_PAGE);
                         }
                     }
-                    const uint32_t bytes = __popc(__ballot_sync(kAll, has)) * p.page_size * 256;
-                    auto copy = [&](Turn &at, const CUtensorMap *tm) {
-                        wait(ct.empty[at.i], at.ph ^ 1);
-                        const uint32_t dst = sRing + at.i * kStageB + lane * p.page_size * 128, full = bar(ct.full[at.i]);
-                        if (lane == 0) mbar_arrive_expect_tx(full, bytes);
+                    const uint32_t bytes = __popc(__ballot_sync(kAll, has)) * p.page_size * C::kRowB;
+                    auto copy = [&](uint64_t &full, uint32_t dst, const CUtensorMap *tm, const uint8_t *cache) {
+                        if (lane == 0) mbar_arrive_expect_tx(bar(full), bytes);
                         __syncwarp();
                         if (has) {
-                            tma_load_4d(dst, tm, full, 0, 0, u.h, pg, policy);
-                            tma_load_4d(dst + 16384, tm, full, 64, 0, u.h, pg, policy);
+                            if (kKv == FKV_KV_FP4) {
+                                const uint32_t sz = p.page_size * kFp4Row;
+                                bulk_load_hint(dst + lane * sz, cache + (static_cast<int64_t>(pg) * p.hkv + u.h) * sz, sz, bar(full), policy);
+                            } else {
+                                tma_load_4d(dst + lane * p.page_size * 128, tm, bar(full), 0, 0, u.h, pg, policy);
+                                if (kKv == FKV_KV_BF16) tma_load_4d(dst + 16384 + lane * p.page_size * 128, tm, bar(full), 64, 0, u.h, pg, policy);
+                            }
                         }
                         __syncwarp();
-                        at.next();
                     };
-                    copy(k, &tmK);
-                    copy(v, &tmV);
+#pragma unroll
+                    for (int kv = 0; kv < 2; ++kv) {
+                        const CUtensorMap *tm = kv ? &tmV : &tmK;
+                        const uint8_t *cache = kv ? p.v_cache : p.k_cache;
+                        if constexpr (C::kConv) {
+                            wait(ct.rempty[raw.i], raw.ph ^ 1);
+                            copy(ct.rfull[raw.i], sRaw + raw.i * C::kRawB, tm, cache);
+                            raw.template next<C::kRaw>();
+                        } else {
+                            Turn &at = kv ? v : k;
+                            wait(ct.empty[at.i], at.ph ^ 1);
+                            copy(ct.full[at.i], sRing + at.i * kStageB, tm, cache);
+                            at.template next<C::kStages>();
+                        }
+                    }
                 }
                 left -= u.te - u.tb;
                 d.template next<kDesc>();
@@ -203,10 +236,54 @@ tree_wide_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmK, co
             const uint64_t t0 = globaltimer_ns();
             while (globaltimer_ns() - t0 < 200000000ull) __nanosleep(1000);
         }
-        } else if (warp == kMmaW) {
+    } else if (C::kConv && warp >= kConvW) {
+        // ==== converters: rows to f16 operands, a token a thread ====
+        constexpr int kF = C::kConv ? kKv : FKV_KV_FP8_E4M3;
+        const int ctid = tid - 32 * kConvW;
+        Ring d, raw;
+        Turn k{0}, v{1};
+        while (true) {
+            wait(ct.dfull[d.i], d.ph);
+            const TreeUnit &u = ct.unit[d.i];
+            const int tb = u.tb, te = u.te;
+            if (__any_sync(kAll, te < 0 || *dead)) break;
+            int odd_tiles = 0;
+#pragma unroll 1
+            for (int i = tb; i < te; ++i) {
+#pragma unroll 1
+                for (int kv = 0; kv < 2; ++kv) {
+                    Turn &at = kv ? v : k;
+                    const uint32_t src = sRaw + raw.i * C::kRawB;
+                    wait(ct.rfull[raw.i], raw.ph);
+                    if (__builtin_expect(kv && !tile_whole(u, i), 0)) {
+                        if (clean_v<kKv>(src, ctid, tile_at<kTreeTok>(u, i) + ctid < tile_end(u, i))) {
+                            atomicOr(&ct.poison[d.i][min(odd_tiles, kTreePoison - 1)][ctid >> 5], 1u << (ctid & 31));
+                            *const_cast<volatile int32_t *>(&ct.unit[d.i].odd) = 1;
+                        }
+                        ++odd_tiles;
+                    }
+                    wait(ct.empty[at.i], at.ph ^ 1);
+                    convert_row<kF>(src, sRing + at.i * kStageB, ctid);
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) {
+                        mbar_arrive(bar(ct.full[at.i]));
+                        mbar_arrive(bar(ct.rempty[raw.i]));
+                    }
+                    at.template next<C::kStages>();
+                    raw.template next<C::kRaw>();
+                }
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(ct.dempty[d.i]));
+            d.template next<kDesc>();
+        }
+        __syncwarp();
+    } else if (warp == kMmaW) {
         // ==== issuer ====
         constexpr uint32_t kHi = umma_desc_hi(1024);
-        constexpr uint32_t idS = umma_idesc(true, false, false, 128, 128), idO = umma_idesc(true, false, true, 128, 128);
+        constexpr uint32_t idS = umma_idesc(!C::kConv, false, false, 128, 128), idO = umma_idesc(!C::kConv, false, true, 128, 128);
+        constexpr int kO = C::kConv ? 8 : 16;                      // products of O: 16 tokens of a word each
         const uint32_t lQ = umma_desc_lo(sQ, 16), lK = umma_desc_lo(sRing, 16), lV = umma_desc_lo(sRing, 16384);
         Ring d;
         Turn k{0}, v{1};
@@ -230,9 +307,12 @@ tree_wide_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmK, co
                         __syncwarp();
                         if (elect_one()) {
 #pragma unroll
-                            for (int kk = 0; kk < 16; ++kk)
-                                umma_ts(tmem + 256 + 128 * g, tmem + 128 * g + kk * 8,
-                                        umma_desc(lV + v.i * (kStageB / 16) + ((kk & 3) + 4 * (kk >> 3)) * 128, kHi), idO, i > tb || kk > 0);
+                            for (int kk = 0; kk < kO; ++kk) {
+                                // half a tile's weights: 32 columns a word, from column 0 or 64
+                                const int half = kk / (kO / 2), word = C::kConv ? 0 : (kk >> 2) & 1, step = kk & 3;
+                                umma_ts(tmem + 256 + 128 * g, tmem + 128 * g + 64 * half + 32 * word + 8 * step,
+                                        umma_desc(lV + v.i * (kStageB / 16) + (4 * half + step) * 128, kHi), idO, i > tb || kk > 0);
+                            }
                             umma_commit(bar(ct.odone[g]));
                             if (g + 1 == blocks) umma_commit(bar(ct.empty[v.i]));
                         }
@@ -256,33 +336,35 @@ tree_wide_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmK, co
                         __syncwarp();
                     }
                 }
-                if (i >= tb) v.next();
-                if (i + 1 < te) k.next();
+                if (i >= tb) v.template next<C::kStages>();
+                if (i + 1 < te) k.template next<C::kStages>();
             }
         }
         __syncwarp();
         if (elect_one()) umma_commit(bar(ct.drained));             // nothing is in flight when the block ends
         __syncwarp();
         mbar_wait_bounded(bar(ct.drained), 0, kTreeDrainNs);
-        }
     } else {
         // ==== softmax ====
         const int g = warp >> 2, gtid = tid & 127;
         const uint32_t tlane = static_cast<uint32_t>(32 * (warp & 3)) << 16;
         const uint32_t tS = tmem + tlane + 128 * g, tO = tmem + tlane + 256 + 128 * g;
         const int row = 128 * g + gtid, rtok = row / p.group, rhead = row - rtok * p.group;    // this thread's row of a unit
-        const float c = p.scale_log2;
+        float c = p.scale_log2, c_next = c;                        // a logit in log2 units per unit of S
         Ring d;
         Turn v{1};
         uint32_t n = 0;                                            // tiles of this block so far
         auto load_q = [&](const TreeUnit &u) {
-            const int c16 = gtid & 15;
+            // the warp's own rows, two at a time; f16 with a power of two that puts a row's largest element into
+            // [2^14, 2^15) (BF16: as it is)
+            const int c16 = lane & 15;
+            const float ks = C::kConv ? __ldg(p.k_scale + u.h) : 1.f;
 #pragma unroll 1
             for (int r8 = 0; r8 < 16; r8 += 8) {
                 uint4 x[8];
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
-                    const int rr = 128 * g + (r8 + i) * 8 + (gtid >> 4), tk = rr / p.group;
+                    const int rr = 128 * g + 32 * (warp & 3) + 2 * (r8 + i) + (lane >> 4), tk = rr / p.group;
                     x[i] = make_uint4(0u, 0u, 0u, 0u);
                     if (tk < u.ntok)
                         x[i] = __ldg(reinterpret_cast<const uint4 *>(
@@ -290,7 +372,24 @@ tree_wide_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmK, co
                 }
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
-                    const int rr = (r8 + i) * 8 + (gtid >> 4);
+                    const int rr = 32 * (warp & 3) + 2 * (r8 + i) + (lane >> 4);
+                    if constexpr (C::kConv) {
+                        uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w}, big = 0;
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) big = max(big, max(w[j] & 0x7FFFu, (w[j] >> 16) & 0x7FFFu));
+#pragma unroll
+                        for (int o = 1; o < 16; o <<= 1) big = max(big, __shfl_xor_sync(kAll, big, o));
+                        int e = static_cast<int>(big >> 7);
+                        if (e == 0 || e == 255) e = 141;           // zeros, infinities and NaN stay what they are
+                        e = max(e, 15);
+                        // (the scale's sign goes to Q, and a scale of zero is next to nothing: -infinity times it is itself)
+                        const float up = copysignf(__uint_as_float(static_cast<uint32_t>(268 - e) << 23), ks);
+                        const float down = __shfl_sync(kAll, __uint_as_float(static_cast<uint32_t>(e - 14) << 23), 16 * (lane & 1));
+                        if (lane >> 1 == r8 + i) c_next = p.scale_log2 * (ks == 0.f ? 1e-30f : fabsf(ks)) * down;
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) w[j] = pack_f16x2(__uint_as_float(w[j] << 16) * up, __uint_as_float(w[j] & 0xFFFF0000u) * up);
+                        x[i] = make_uint4(w[0], w[1], w[2], w[3]);
+                    }
                     st_shared_v4(sQ + g * kQB + (c16 >> 3) * 16384 + rr * 128 + (((c16 & 7) ^ (rr & 7)) << 4), x[i]);
                 }
             }
@@ -308,6 +407,7 @@ tree_wide_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmK, co
             const int tok = rtok < u.ntok ? u.tok0 + rtok : -1;    // the row's token (of the call)
             float ref = kTreeNone, l = 0.f;
             int odd_tiles = 0;
+            c = c_next;
 #pragma unroll 1
             for (int i = tb; i < te && mine; ++i) {
                 wait(ct.sfull[g], n & 1);
@@ -324,7 +424,7 @@ tree_wide_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmK, co
                         const uint64_t see = seen_of(p, u, tok, t0) | static_cast<uint64_t>(seen_of(p, u, tok, t0 + 32)) << 32;
 #pragma unroll
                         for (int j = 0; j < 64; ++j)
-                            if (!((see >> j) & 1)) s[j] = -INFINITY;
+                            if (!((see >> j) & 1)) s[j] = -INFINITY;   // (c is above zero)
                     }
                     float top = -INFINITY;
 #pragma unroll
@@ -351,19 +451,29 @@ tree_wide_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmK, co
                             tmem_store_wait();
 #pragma unroll 1
                             for (int b = 0; b < 32; b += 8) {
-                                float hi[8], lo[8];
-                                uint32_t wh[8], wl[8];
+                                float hi[8];
+                                uint32_t wh[8];
                                 tmem_load(tS + b, hi);
-                                tmem_load(tS + 32 + b, lo);
+                                if constexpr (C::kConv) {
 #pragma unroll
-                                for (int j = 0; j < 8; ++j) {
-                                    const uint32_t x = __float_as_uint(hi[j]), y = __float_as_uint(lo[j]);
-                                    const float v0 = (__uint_as_float(x << 16) + __uint_as_float(y << 16)) * f;
-                                    const float v1 = (__uint_as_float(x & 0xFFFF0000u) + __uint_as_float(y & 0xFFFF0000u)) * f;
-                                    split(v0, v1, wh[j], wl[j]);
+                                    for (int j = 0; j < 8; ++j) {
+                                        const uint32_t x = __float_as_uint(hi[j]);
+                                        const float2 y = __half22float2(*reinterpret_cast<const __half2 *>(&x));
+                                        wh[j] = pack_f16x2(y.x * f, y.y * f);
+                                    }
+                                } else {
+                                    float lo[8];
+                                    uint32_t wl[8];
+                                    tmem_load(tS + 32 + b, lo);
+#pragma unroll
+                                    for (int j = 0; j < 8; ++j) {
+                                        const uint32_t x = __float_as_uint(hi[j]), y = __float_as_uint(lo[j]);
+                                        split((__uint_as_float(x << 16) + __uint_as_float(y << 16)) * f,
+                                              (__uint_as_float(x & 0xFFFF0000u) + __uint_as_float(y & 0xFFFF0000u)) * f, wh[j], wl[j]);
+                                    }
+                                    tmem_store(tS + 32 + b, wl);
                                 }
                                 tmem_store(tS + b, wh);
-                                tmem_store(tS + 32 + b, wl);
                             }
                         }
                         l *= f;
@@ -371,24 +481,25 @@ tree_wide_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmK, co
                         ref = to;
                     }
                     const float2 c2 = make_float2(c, c), r2 = make_float2(-ref, -ref);
-                    uint32_t hi[32], lo[32];
+                    uint32_t hi[32], lo[C::kConv ? 1 : 32];
 #pragma unroll
                     for (int j = 0; j < 32; ++j) {
                         float2 x = fma2(make_float2(s[2 * j], s[2 * j + 1]), c2, r2);
                         x.x = ex2(x.x);
                         x.y = ex2(x.y);
                         sum[j & 1] = add2(sum[j & 1], x);
-                        split(x.x, x.y, hi[j], lo[j]);
+                        if constexpr (C::kConv) hi[j] = pack_f16x2(x.x, x.y);
+                        else split(x.x, x.y, hi[j], lo[j]);
                     }
                     tmem_store(tS + at, hi);
-                    tmem_store(tS + at + 32, lo);
+                    if constexpr (!C::kConv) tmem_store(tS + at + 32, lo);
                 }
                 sum[0] = add2(sum[0], sum[1]);
                 l += sum[0].x + sum[0].y;
-                if (__builtin_expect(!whole, 0)) {
+                if (__builtin_expect(!C::kConv && !whole, 0)) {
                     if (g == 0) {                                  // both blocks' products with V come after this block's weights
                         wait(ct.full[v.i], v.ph);
-                        if (clean_v<FKV_KV_BF16>(sRing + v.i * kStageB, gtid, tile_at<kTreeTok>(u, i) + gtid < tile_end(u, i))) {
+                        if (clean_v<kKv>(sRing + v.i * kStageB, gtid, tile_at<kTreeTok>(u, i) + gtid < tile_end(u, i))) {
                             atomicOr(&ct.poison[d.i][min(odd_tiles, kTreePoison - 1)][gtid >> 5], 1u << (gtid & 31));
                             *const_cast<volatile int32_t *>(&ct.unit[d.i].odd) = 1;
                         }
@@ -401,7 +512,7 @@ tree_wide_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmK, co
                 __syncwarp();
                 if (lane == 0) mbar_arrive(bar(ct.pready[g]));
                 ++n;
-                v.next();
+                if (!C::kConv) v.template next<C::kStages>();
             }
             // the next unit's Q, while the last products run
             Ring e = d;
@@ -415,7 +526,7 @@ tree_wide_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmK, co
                 umma_fence_after();
                 const bool wrong = *const_cast<volatile int32_t *>(&ct.unit[d.i].bad) != 0, cut = u.slot >= 0;
                 const int64_t at = static_cast<int64_t>(u.slot) * kTreeWideRows + row;
-                const float f = wrong || l == 0.f ? 0.f : 1.f / l;
+                const float f = wrong || l == 0.f ? 0.f : (C::kConv ? __ldg(p.v_scale + u.h) : 1.f) / l;
                 __nv_bfloat16 *const out = p.out + (static_cast<int64_t>(tok) * p.hq + u.h * p.group + rhead) * 128;
                 if (cut && tok >= 0) p.part_ml[at] = make_float2(ref, wrong ? -1.f : l);
 #pragma unroll 1
@@ -452,7 +563,7 @@ tree_wide_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmK, co
                             if (!sees(p, u, row_sight(p, u, tok, word_of(u, t0 + b)), t0 + b)) continue;
 #pragma unroll 1
                             for (int dim = 0; dim < 128; ++dim) {
-                                const float add = odd_value<FKV_KV_BF16>(p, u, t0 + b, dim);
+                                const float add = odd_value<kKv>(p, u, t0 + b, dim);
                                 if (add == 0.f) continue;
                                 if (cut) p.part_o[at * 128 + dim] += add;
                                 else out[dim] = __float2bfloat16_rn(__bfloat162float(out[dim]) + add);
@@ -491,22 +602,30 @@ tree_wide_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmK, co
 namespace {
 constexpr int kMaxDev = 64;
 std::mutex g_mu;
-unsigned long long g_ready[kMaxDev];                               // the context in which the kernel's shared memory was set
-}  // namespace
+unsigned long long g_ready[kMaxDev][3];                            // the context in which an instance's shared memory was set
 
-fkv_status launch_tree_wide(const TreeParams &p, int sms, const CUtensorMap &tmK, const CUtensorMap &tmV, cudaStream_t st) {
+template <int kKv>
+fkv_status launch(const TreeParams &p, int sms, const CUtensorMap &tmK, const CUtensorMap &tmV, cudaStream_t st) {
+    constexpr int smem = wide::smem_bytes<kKv>();
     int dev = -1;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDev) return FKV_ERR_CUDA;
     {
         std::lock_guard<std::mutex> lk(g_mu);
         const unsigned long long ctx = current_context_id();
-        if (ctx == 0 || g_ready[dev] != ctx) {
-            if (cudaFuncSetAttribute(tree_wide_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, wide::kSmem) != cudaSuccess) return FKV_ERR_CUDA;
-            g_ready[dev] = current_context_id();
+        if (ctx == 0 || g_ready[dev][kKv] != ctx) {
+            if (cudaFuncSetAttribute(tree_wide_kernel<kKv>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess) return FKV_ERR_CUDA;
+            g_ready[dev][kKv] = current_context_id();
         }
     }
-    if (launch_pdl(tree_wide_kernel, dim3(sms), dim3(wide::kThreads), wide::kSmem, st, p, tmK, tmV) != cudaSuccess) return FKV_ERR_CUDA;
+    if (launch_pdl(tree_wide_kernel<kKv>, dim3(sms), dim3(wide::Cfg<kKv>::kThreads), smem, st, p, tmK, tmV) != cudaSuccess) return FKV_ERR_CUDA;
     return launch_tree_join(p, sms, kTreeWideRows, st) == cudaSuccess ? FKV_OK : FKV_ERR_CUDA;
+}
+}  // namespace
+
+fkv_status launch_tree_wide(const TreeParams &p, int kv, int sms, const CUtensorMap &tmK, const CUtensorMap &tmV, cudaStream_t st) {
+    return kv == FKV_KV_BF16         ? launch<FKV_KV_BF16>(p, sms, tmK, tmV, st)
+           : kv == FKV_KV_FP8_E4M3 ? launch<FKV_KV_FP8_E4M3>(p, sms, tmK, tmV, st)
+                                   : launch<FKV_KV_FP4>(p, sms, tmK, tmV, st);
 }
 
 }  // namespace fkv

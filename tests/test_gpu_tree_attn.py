@@ -530,3 +530,15 @@ def test_two_graphs_of_other_kernels_at_once():
         a.check(ta["out"], 777, 5)
         b.check(tb["out"])
         e.check(te["out"], 50, 1)
+
+
+@pytest.mark.parametrize("kind", ["fp8", "fp4"])
+@pytest.mark.parametrize("Hq,n", [(2, [3, 1]), (16, [3, 3]), (16, [7, 6]), (16, [40, 30])])
+def test_head_scales_of_zero_and_below(kind, Hq, n):
+    """16, 32 to 64, 128 and 256 rows a unit: a K scale of zero makes all logits equal, one below zero turns them around."""
+    for ks in (0.0, -1.0):
+        c = Case(kind, Hq, 2, 16, [70, 300], n, seed=44)
+        c.ks[0] *= ks
+        c.vs[1] = -c.vs[1]
+        c.check(c.tree())
+        c.check(c.tree(window=60, sinks=2), 60, 2)
