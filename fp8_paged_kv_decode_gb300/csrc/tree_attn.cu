@@ -1239,7 +1239,7 @@ fkv_status attend(bool tree, const void *q, int32_t n_tokens, int32_t num_q_head
     p.scale_log2 = sm_scale * 1.4426950408889634f;
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
     if (small) return launch_tree_small(p, kv_dtype, rows, sms, tmK, tmV, st);
-    if (rows == kTreeWideRows) return launch_tree_wide(p, kv_dtype, sms, tmK, tmV, st);
+    if (rows >= 128) return launch_tree_wide(p, kv_dtype, rows, sms, tmK, tmV, st);
     return fp8                         ? launch_rows<FKV_KV_FP8_E4M3>(rows, p, sms, tmK, tmV, st)
            : kv_dtype == FKV_KV_BF16 ? launch_rows<FKV_KV_BF16>(rows, p, sms, tmK, tmV, st)
                                      : launch_rows<FKV_KV_FP4>(rows, p, sms, tmK, tmV, st);

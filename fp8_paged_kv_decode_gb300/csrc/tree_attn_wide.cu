@@ -48,7 +48,7 @@ template <int kKv>
 struct Ctrl {
     using C = Cfg<kKv>;
     uint64_t full[C::kStages], empty[C::kStages], rfull[C::kRaw], rempty[C::kRaw];
-    uint64_t qready[2], sfull[2], pready[2], odone[2];
+    uint64_t qready[2], sfull[2], pready[2], odone[2], xready[2], xdone[2];
     uint64_t dfull[kDesc], dempty[kDesc], drained;
     TreeUnit unit[kDesc];
     uint32_t poison[kDesc][kTreePoison][4];                        // tokens whose V holds NaN or infinities
@@ -100,7 +100,7 @@ __device__ __forceinline__ void split(float a, float b, uint32_t &hi, uint32_t &
 
 template <int kKv>
 __global__ void __launch_bounds__(wide::Cfg<kKv>::kThreads, 1)
-tree_wide_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV) {
+tree_wide_kernel(const TreeParams p, int rows, const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV) {
     using namespace wide;
     using C = Cfg<kKv>;
     extern __shared__ __align__(1024) uint8_t smem[];
@@ -114,7 +114,8 @@ tree_wide_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmK, co
         for (int i = 0; i < C::kStages; ++i) mbar_init(bar(ct.full[i]), C::kConv ? 4 : 1), mbar_init(bar(ct.empty[i]), 1);
         for (int i = 0; i < C::kRaw; ++i) mbar_init(bar(ct.rfull[i]), 1), mbar_init(bar(ct.rempty[i]), 4);
         for (int i = 0; i < 2; ++i)
-            mbar_init(bar(ct.qready[i]), 4), mbar_init(bar(ct.sfull[i]), 1), mbar_init(bar(ct.pready[i]), 4), mbar_init(bar(ct.odone[i]), 1);
+            mbar_init(bar(ct.qready[i]), 4), mbar_init(bar(ct.sfull[i]), 1), mbar_init(bar(ct.pready[i]), 4), mbar_init(bar(ct.odone[i]), 1),
+            mbar_init(bar(ct.xready[i]), 4), mbar_init(bar(ct.xdone[i]), 4);
         for (int i = 0; i < kDesc; ++i) mbar_init(bar(ct.dfull[i]), 1), mbar_init(bar(ct.dempty[i]), 8 + 1 + (C::kConv ? 4 : 0));
         mbar_init(bar(ct.drained), 1);
         ct.dead = 0;
@@ -124,7 +125,7 @@ tree_wide_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmK, co
     if (kKv != FKV_KV_FP4 && warp == kProdW && lane == 0) prefetch_tensormap(&tmK), prefetch_tensormap(&tmV);
 
     grid_dep_wait();                                               // lengths, tables and cache of earlier kernels
-    const int tpt = kTreeWideRows / p.group;                       // tokens of a unit's rows
+    const int tpt = rows / p.group;                                // tokens of a unit's rows
     const TreeTotal total = tree_shares<kTreeTok, C::kThreads, 1>(p, tpt, ct.shares);
     umma_fence_before();
     __syncthreads();
@@ -287,7 +288,45 @@ tree_wide_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmK, co
         const uint32_t lQ = umma_desc_lo(sQ, 16), lK = umma_desc_lo(sRing, 16), lV = umma_desc_lo(sRing, 16384);
         Ring d;
         Turn k{0}, v{1};
-        uint32_t nq[2] = {0, 0}, np[2] = {0, 0};                   // units and tiles of a block so far
+        uint32_t nq = 0, np = 0, any = 0;                          // bit g: parity of block g's units and tiles so far; had tiles
+        auto put_s = [&](int g, int q, bool last) {                // S of stage k.i with Q block q
+            if ((any >> g) & 1) wait(ct.odone[g], ((np >> g) & 1) ^ 1);    // it takes the place of the weights that O was made of
+            umma_fence_after();
+            __syncwarp();
+            if (elect_one()) {
+#pragma unroll
+                for (int kk = 0; kk < 8; ++kk) {
+                    const uint32_t at = (kk >> 2) * 1024 + (kk & 3) * 2;
+                    umma_ss(tmem + 128 * g, umma_desc(lQ + q * (kQB / 16) + at, kHi), umma_desc(lK + k.i * (kStageB / 16) + at, kHi), idS, kk > 0);
+                }
+                umma_commit(bar(ct.sfull[g]));
+                if (last) umma_commit(bar(ct.empty[k.i]));
+            }
+            __syncwarp();
+        };
+        auto put_o = [&](int g, bool add, bool last) {             // O of stage v.i
+            wait(ct.pready[g], (np >> g) & 1);
+            np ^= 1u << g;
+            any |= 1u << g;
+            umma_fence_after();
+            __syncwarp();
+            if (elect_one()) {
+#pragma unroll
+                for (int kk = 0; kk < kO; ++kk) {
+                    // half a tile's weights: 32 columns a word, from column 0 or 64
+                    const int half = kk / (kO / 2), word = C::kConv ? 0 : (kk >> 2) & 1, step = kk & 3;
+                    umma_ts(tmem + 256 + 128 * g, tmem + 128 * g + 64 * half + 32 * word + 8 * step,
+                            umma_desc(lV + v.i * (kStageB / 16) + (4 * half + step) * 128, kHi), idO, add || kk > 0);
+                }
+                umma_commit(bar(ct.odone[g]));
+                if (last) umma_commit(bar(ct.empty[v.i]));
+            }
+            __syncwarp();
+        };
+        auto q_there = [&](int g) {
+            wait(ct.qready[g], (nq >> g) & 1);
+            nq ^= 1u << g;
+        };
         while (true) {
             wait(ct.dfull[d.i], d.ph);
             const int tb = *const_cast<volatile int32_t *>(&ct.unit[d.i].tb), te = *const_cast<volatile int32_t *>(&ct.unit[d.i].te);
@@ -295,49 +334,34 @@ tree_wide_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmK, co
             if (__any_sync(kAll, te < 0 || *dead)) break;
             if (elect_one()) mbar_arrive(bar(ct.dempty[d.i]));
             d.template next<kDesc>();
-            for (int i = tb - 1; i < te; ++i) {
-                // O of tile i, then S of the tile after it, block after block
+            // S runs ahead of O by a tile of each softmax group
+            const int ahead = 3 - blocks;
+#pragma unroll 1
+            for (int j = 0; j < te - tb + ahead; ++j) {
+                const bool o = j >= ahead, sn = j < te - tb;
+                if (o) wait(ct.full[v.i], v.ph);
+                if (blocks == 2) {
+                    // O of a tile, then S of the next one, block after block
 #pragma unroll
-                for (int g = 0; g < 2; ++g) {
-                    if (g == blocks) break;
-                    if (i >= tb) {
-                        if (g == 0) wait(ct.full[v.i], v.ph);
-                        wait(ct.pready[g], np[g]++ & 1);
-                        umma_fence_after();
-                        __syncwarp();
-                        if (elect_one()) {
-#pragma unroll
-                            for (int kk = 0; kk < kO; ++kk) {
-                                // half a tile's weights: 32 columns a word, from column 0 or 64
-                                const int half = kk / (kO / 2), word = C::kConv ? 0 : (kk >> 2) & 1, step = kk & 3;
-                                umma_ts(tmem + 256 + 128 * g, tmem + 128 * g + 64 * half + 32 * word + 8 * step,
-                                        umma_desc(lV + v.i * (kStageB / 16) + (4 * half + step) * 128, kHi), idO, i > tb || kk > 0);
-                            }
-                            umma_commit(bar(ct.odone[g]));
-                            if (g + 1 == blocks) umma_commit(bar(ct.empty[v.i]));
+                    for (int g = 0; g < 2; ++g) {
+                        if (o) put_o(g, j > 1, g == 1);
+                        if (sn) {
+                            if (j == 0) q_there(g);
+                            if (g == 0) wait(ct.full[k.i], k.ph);
+                            put_s(g, g, g == 1);
                         }
-                        __syncwarp();
                     }
-                    if (i + 1 < te) {
-                        if (i < tb) wait(ct.qready[g], nq[g]++ & 1);
-                        if (g == 0) wait(ct.full[k.i], k.ph);
-                        if (np[g]) wait(ct.odone[g], (np[g] - 1) & 1);     // S takes the place of the weights that O was made of
-                        umma_fence_after();
-                        __syncwarp();
-                        if (elect_one()) {
-#pragma unroll
-                            for (int kk = 0; kk < 8; ++kk) {
-                                const uint32_t at = (kk >> 2) * 1024 + (kk & 3) * 2;
-                                umma_ss(tmem + 128 * g, umma_desc(lQ + g * (kQB / 16) + at, kHi), umma_desc(lK + k.i * (kStageB / 16) + at, kHi), idS, kk > 0);
-                            }
-                            umma_commit(bar(ct.sfull[g]));
-                            if (g + 1 == blocks) umma_commit(bar(ct.empty[k.i]));
-                        }
-                        __syncwarp();
+                } else {
+                    // one block: its tiles by turns to the softmax groups
+                    if (o) put_o(j & 1, j > 3, true);
+                    if (sn) {
+                        if (j == 0) q_there(0);
+                        wait(ct.full[k.i], k.ph);
+                        put_s(j & 1, 0, true);
                     }
                 }
-                if (i >= tb) v.template next<C::kStages>();
-                if (i + 1 < te) k.template next<C::kStages>();
+                if (o) v.template next<C::kStages>();
+                if (sn) k.template next<C::kStages>();
             }
         }
         __syncwarp();
@@ -349,22 +373,22 @@ tree_wide_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmK, co
         const int g = warp >> 2, gtid = tid & 127;
         const uint32_t tlane = static_cast<uint32_t>(32 * (warp & 3)) << 16;
         const uint32_t tS = tmem + tlane + 128 * g, tO = tmem + tlane + 256 + 128 * g;
-        const int row = 128 * g + gtid, rtok = row / p.group, rhead = row - rtok * p.group;    // this thread's row of a unit
         float c = p.scale_log2, c_next = c;                        // a logit in log2 units per unit of S
         Ring d;
         Turn v{1};
-        uint32_t n = 0;                                            // tiles of this block so far
+        uint32_t n = 0, n_other = 0, n_turns = 0;                  // tiles of this group and the other, units in turns so far
         auto load_q = [&](const TreeUnit &u) {
             // the warp's own rows, two at a time; f16 with a power of two that puts a row's largest element into
             // [2^14, 2^15) (BF16: as it is)
-            const int c16 = lane & 15;
+            const bool alone = u.ntok * p.group <= 128;            // one block, which group 0 loads
+            const int c16 = lane & 15, row0 = (alone ? 0 : 128 * g) + 32 * (warp & 3) + (lane >> 4);
             const float ks = C::kConv ? __ldg(p.k_scale + u.h) : 1.f;
 #pragma unroll 1
             for (int r8 = 0; r8 < 16; r8 += 8) {
                 uint4 x[8];
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
-                    const int rr = 128 * g + 32 * (warp & 3) + 2 * (r8 + i) + (lane >> 4), tk = rr / p.group;
+                    const int rr = row0 + 2 * (r8 + i), tk = rr / p.group;
                     x[i] = make_uint4(0u, 0u, 0u, 0u);
                     if (tk < u.ntok)
                         x[i] = __ldg(reinterpret_cast<const uint4 *>(
@@ -372,7 +396,7 @@ tree_wide_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmK, co
                 }
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
-                    const int rr = 32 * (warp & 3) + 2 * (r8 + i) + (lane >> 4);
+                    const int rr = (row0 & 127) + 2 * (r8 + i);
                     if constexpr (C::kConv) {
                         uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w}, big = 0;
 #pragma unroll
@@ -390,26 +414,32 @@ tree_wide_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmK, co
                         for (int j = 0; j < 4; ++j) w[j] = pack_f16x2(__uint_as_float(w[j] << 16) * up, __uint_as_float(w[j] & 0xFFFF0000u) * up);
                         x[i] = make_uint4(w[0], w[1], w[2], w[3]);
                     }
-                    st_shared_v4(sQ + g * kQB + (c16 >> 3) * 16384 + rr * 128 + (((c16 & 7) ^ (rr & 7)) << 4), x[i]);
+                    if (!alone || g == 0) st_shared_v4(sQ + g * kQB + (c16 >> 3) * 16384 + rr * 128 + (((c16 & 7) ^ (rr & 7)) << 4), x[i]);
                 }
             }
             fence_proxy_async_smem();
             __syncwarp();
-            if (lane == 0) mbar_arrive(bar(ct.qready[g]));
+            if (lane == 0 && (!alone || g == 0)) mbar_arrive(bar(ct.qready[g]));
         };
         wait(ct.dfull[0], 0);
-        if (!*dead && ct.unit[0].te >= 0 && 128 * g < ct.unit[0].ntok * p.group) load_q(ct.unit[0]);
+        if (!__any_sync(kAll, *dead || ct.unit[0].te < 0)) load_q(ct.unit[0]);
         while (true) {
             const TreeUnit &u = ct.unit[d.i];
             const int tb = u.tb, te = u.te;
             if (__any_sync(kAll, te < 0 || *dead)) break;
-            const bool mine = 128 * g < u.ntok * p.group;
+            const bool turns = u.ntok * p.group <= 128;            // one block: its tiles by turns
+            const int row = turns ? gtid : 128 * g + gtid, rtok = row / p.group, rhead = row - rtok * p.group;
             const int tok = rtok < u.ntok ? u.tok0 + rtok : -1;    // the row's token (of the call)
             float ref = kTreeNone, l = 0.f;
             int odd_tiles = 0;
             c = c_next;
 #pragma unroll 1
-            for (int i = tb; i < te && mine; ++i) {
+            for (int i = tb; i < te; ++i) {
+                if (turns && ((i - tb - g) & 1)) {
+                    odd_tiles += !tile_whole(u, i);
+                    if (!C::kConv) v.template next<C::kStages>();
+                    continue;
+                }
                 wait(ct.sfull[g], n & 1);
                 umma_fence_after();
                 // 64 logits at a time, their weights' two words in their place
@@ -434,7 +464,7 @@ tree_wide_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmK, co
                     if (__builtin_expect(__any_sync(kAll, move), 0)) {
                         // the sums so far, and the weights of the tile's first half, are scaled to the new reference
                         const float to = move ? top - kTreeTop : ref, f = move ? ex2(ref - to) : 1.f;
-                        if (i > tb) {
+                        if (i > tb + turns) {
                             wait(ct.odone[g], (n - 1) & 1);
                             umma_fence_after();
 #pragma unroll 1
@@ -497,7 +527,7 @@ tree_wide_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmK, co
                 sum[0] = add2(sum[0], sum[1]);
                 l += sum[0].x + sum[0].y;
                 if (__builtin_expect(!C::kConv && !whole, 0)) {
-                    if (g == 0) {                                  // both blocks' products with V come after this block's weights
+                    if (g == 0 || turns) {                         // of two blocks both products with V come after block 0's weights
                         wait(ct.full[v.i], v.ph);
                         if (clean_v<kKv>(sRing + v.i * kStageB, gtid, tile_at<kTreeTok>(u, i) + gtid < tile_end(u, i))) {
                             atomicOr(&ct.poison[d.i][min(odd_tiles, kTreePoison - 1)][gtid >> 5], 1u << (gtid & 31));
@@ -514,37 +544,71 @@ tree_wide_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmK, co
                 ++n;
                 if (!C::kConv) v.template next<C::kStages>();
             }
-            // the next unit's Q, while the last products run
+            const int mine = turns ? (te - tb + 1 - g) / 2 : te - tb, others = turns ? (te - tb + g) / 2 : te - tb;
+            n_other += others;
             Ring e = d;
             e.template next<kDesc>();
-            wait(ct.dfull[e.i], e.ph);
-            if (__any_sync(kAll, *dead != 0)) break;
-            const int nte = *const_cast<volatile int32_t *>(&ct.unit[e.i].te);
-            if (nte >= 0 && 128 * g < ct.unit[e.i].ntok * p.group) load_q(ct.unit[e.i]);
-            if (mine) {
-                wait(ct.odone[g], (n - 1) & 1);
+            auto next_q = [&] {
+                wait(ct.dfull[e.i], e.ph);
+                if (!__any_sync(kAll, *dead || *const_cast<volatile int32_t *>(&ct.unit[e.i].te) < 0)) load_q(ct.unit[e.i]);
+            };
+            if (!turns) next_q();                                  // while the last products run
+            {
+                if (mine) wait(ct.odone[g], (n - 1) & 1);
+                float f = 1.f, f_other = 0.f;                      // of this group's sums and the other's
+                if (turns) {
+                    // one row is this thread's and the other group's; Q's second block lends the room
+                    float2 *x = reinterpret_cast<float2 *>(smem + kQB);
+                    if (others) wait(ct.odone[g ^ 1], (n_other - 1) & 1);
+                    x[128 * g + gtid] = make_float2(ref, l);
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(bar(ct.xready[g]));
+                    wait(ct.xready[g ^ 1], n_turns & 1);
+                    const volatile float2 *theirs = x + 128 * (g ^ 1) + gtid;
+                    const float2 y = make_float2(theirs->x, theirs->y);
+                    const float top = l == 0.f ? y.x : y.y == 0.f ? ref : fmaxf(ref, y.x);
+                    f = l == 0.f ? 0.f : ex2(ref - top);
+                    f_other = y.y == 0.f ? 0.f : ex2(y.x - top);
+                    // (the same sum in both groups)
+                    l = g ? f_other * y.y + f * l : f * l + f_other * y.y;
+                    ref = top;
+                }
                 umma_fence_after();
                 const bool wrong = *const_cast<volatile int32_t *>(&ct.unit[d.i].bad) != 0, cut = u.slot >= 0;
-                const int64_t at = static_cast<int64_t>(u.slot) * kTreeWideRows + row;
-                const float f = wrong || l == 0.f ? 0.f : (C::kConv ? __ldg(p.v_scale + u.h) : 1.f) / l;
+                const int64_t at = static_cast<int64_t>(u.slot) * rows + row;
+                const int d0 = turns ? 64 * g : 0, d1 = turns ? d0 + 64 : 128;     // the dims that this thread writes
                 __nv_bfloat16 *const out = p.out + (static_cast<int64_t>(tok) * p.hq + u.h * p.group + rhead) * 128;
-                if (cut && tok >= 0) p.part_ml[at] = make_float2(ref, wrong ? -1.f : l);
+                if (cut) {
+                    if (tok >= 0 && d0 == 0) p.part_ml[at] = make_float2(ref, wrong ? -1.f : l);
+                } else {
+                    const float norm = wrong || l == 0.f ? 0.f : (C::kConv ? __ldg(p.v_scale + u.h) : 1.f) / l;
+                    f *= norm;
+                    f_other *= norm;
+                }
 #pragma unroll 1
-                for (int b = 0; b < 4; ++b) {
+                for (int b = d0; b < d1; b += 32) {
                     float o[32];
-                    tmem_load(tO + 32 * b, o);
+                    tmem_load(tO + b, o);
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) o[j] = f == 0.f ? 0.f : o[j] * f;
+                    if (turns) {
+                        float z[32];
+                        tmem_load(tmem + tlane + 256 + 128 * (g ^ 1) + b, z);
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) o[j] += f_other == 0.f ? 0.f : z[j] * f_other;
+                    }
                     if (tok < 0) continue;
                     if (cut) {
-                        float4 *dst = reinterpret_cast<float4 *>(p.part_o + at * 128 + 32 * b);
+                        float4 *dst = reinterpret_cast<float4 *>(p.part_o + at * 128 + b);
 #pragma unroll
                         for (int j = 0; j < 8; ++j) dst[j] = make_float4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
                     } else {
-                        uint4 *dst = reinterpret_cast<uint4 *>(out + 32 * b);
+                        uint4 *dst = reinterpret_cast<uint4 *>(out + b);
 #pragma unroll
                         for (int j = 0; j < 4; ++j) {
                             uint32_t w[4];
 #pragma unroll
-                            for (int x = 0; x < 4; ++x) w[x] = f == 0.f ? 0u : pack_bf16x2(o[8 * j + 2 * x] * f, o[8 * j + 2 * x + 1] * f);
+                            for (int x = 0; x < 4; ++x) w[x] = pack_bf16x2(o[8 * j + 2 * x], o[8 * j + 2 * x + 1]);
                             dst[j] = make_uint4(w[0], w[1], w[2], w[3]);
                         }
                     }
@@ -562,7 +626,7 @@ tree_wide_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmK, co
                             if (!((*const_cast<volatile uint32_t *>(&ct.poison[d.i][min(k, kTreePoison - 1)][b >> 5]) >> (b & 31)) & 1)) continue;
                             if (!sees(p, u, row_sight(p, u, tok, word_of(u, t0 + b)), t0 + b)) continue;
 #pragma unroll 1
-                            for (int dim = 0; dim < 128; ++dim) {
+                            for (int dim = d0; dim < d1; ++dim) {
                                 const float add = odd_value<kKv>(p, u, t0 + b, dim);
                                 if (add == 0.f) continue;
                                 if (cut) p.part_o[at * 128 + dim] += add;
@@ -574,6 +638,13 @@ tree_wide_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmK, co
                 }
             }
             __syncwarp();
+            if (turns) {
+                // both groups have read each other's sums
+                if (lane == 0) mbar_arrive(bar(ct.xdone[g]));
+                wait(ct.xdone[g ^ 1], n_turns & 1);
+                ++n_turns;
+                next_q();
+            }
             if (lane == 0) mbar_arrive(bar(ct.dempty[d.i]));
             d = e;
         }
@@ -605,7 +676,7 @@ std::mutex g_mu;
 unsigned long long g_ready[kMaxDev][3];                            // the context in which an instance's shared memory was set
 
 template <int kKv>
-fkv_status launch(const TreeParams &p, int sms, const CUtensorMap &tmK, const CUtensorMap &tmV, cudaStream_t st) {
+fkv_status launch(const TreeParams &p, int rows, int sms, const CUtensorMap &tmK, const CUtensorMap &tmV, cudaStream_t st) {
     constexpr int smem = wide::smem_bytes<kKv>();
     int dev = -1;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDev) return FKV_ERR_CUDA;
@@ -617,15 +688,16 @@ fkv_status launch(const TreeParams &p, int sms, const CUtensorMap &tmK, const CU
             g_ready[dev][kKv] = current_context_id();
         }
     }
-    if (launch_pdl(tree_wide_kernel<kKv>, dim3(sms), dim3(wide::Cfg<kKv>::kThreads), smem, st, p, tmK, tmV) != cudaSuccess) return FKV_ERR_CUDA;
-    return launch_tree_join(p, sms, kTreeWideRows, st) == cudaSuccess ? FKV_OK : FKV_ERR_CUDA;
+    if (launch_pdl(tree_wide_kernel<kKv>, dim3(sms), dim3(wide::Cfg<kKv>::kThreads), smem, st, p, rows, tmK, tmV) != cudaSuccess)
+        return FKV_ERR_CUDA;
+    return launch_tree_join(p, sms, rows, st) == cudaSuccess ? FKV_OK : FKV_ERR_CUDA;
 }
 }  // namespace
 
-fkv_status launch_tree_wide(const TreeParams &p, int kv, int sms, const CUtensorMap &tmK, const CUtensorMap &tmV, cudaStream_t st) {
-    return kv == FKV_KV_BF16         ? launch<FKV_KV_BF16>(p, sms, tmK, tmV, st)
-           : kv == FKV_KV_FP8_E4M3 ? launch<FKV_KV_FP8_E4M3>(p, sms, tmK, tmV, st)
-                                   : launch<FKV_KV_FP4>(p, sms, tmK, tmV, st);
+fkv_status launch_tree_wide(const TreeParams &p, int kv, int rows, int sms, const CUtensorMap &tmK, const CUtensorMap &tmV, cudaStream_t st) {
+    return kv == FKV_KV_BF16         ? launch<FKV_KV_BF16>(p, rows, sms, tmK, tmV, st)
+           : kv == FKV_KV_FP8_E4M3 ? launch<FKV_KV_FP8_E4M3>(p, rows, sms, tmK, tmV, st)
+                                   : launch<FKV_KV_FP4>(p, rows, sms, tmK, tmV, st);
 }
 
 }  // namespace fkv
