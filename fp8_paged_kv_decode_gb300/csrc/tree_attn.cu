@@ -10,8 +10,8 @@
 // so a unit of work is (request, KV head, up to kR of their n G rows).  Three kernels, by the
 // rows that G times the call's mean n come to, so that few rows cost little and K and V pass
 // through once for all of them:
-//   here               BF16 up to 128 rows, FP8 and FP4 33 to 128: products of 128-token tiles
-//                      with kR = 16, 32, 64 or 128 columns, on the fifth-generation tensor
+//   here               BF16 up to 64 rows, FP8 and FP4 33 to 64: products of 128-token tiles
+//                      with kR = 16, 32 or 64 columns, on the fifth-generation tensor
 //                      cores, tokens (or dims) on M and rows on N,
 //                          S^T = K Q^T  [128 tokens][kR],   O^T = V^T P^T  [128 dims][kR]
 //   tree_attn_small.cu FP8 and FP4 up to 32 rows
@@ -20,14 +20,12 @@
 // One CTA per SM takes an equal share of all units' tiles (a unit may be cut; its parts are
 // joined by a second kernel).  Its warps:
 //   producer   a unit's geometry, and TMA copies of its pages into rings of K and V stages
-//   converters (FP8, FP4) K rows to f16 in tensor memory, V rows to f16 in tensor memory (128
-//              rows, whose sums leave no room there: in shared memory); a unit's Q as f16,
-//              scaled by one power of two (BF16: as it is)
+//   converters (FP8, FP4) K and V rows to f16 in tensor memory; a unit's Q as f16, scaled by
+//              one power of two (BF16: as it is)
 //   issuers    a warp for S, one for O
 //   softmax    two groups of four warps, one token a thread: weights against a running
-//              reference, stored as the second product's operand.  Up to 64 rows the groups
-//              take turns at tiles, with references and sums of their own that are joined at a
-//              unit's end; with 128 each takes half of the columns
+//              reference, stored as the second product's operand.  The groups take turns at
+//              tiles, with references and sums of their own that are joined at a unit's end
 // The reference of a column moves only when a weight would pass f16's range: a maximum is
 // put at 2^10, later ones may grow to 2^15.9, so sums are rescaled a few times per unit.
 // FP8 and FP4 weights are one f16 word, BF16 ones two BF16 words.
@@ -57,21 +55,13 @@ struct TreeCfg {
     static constexpr bool kConv = kKv != FKV_KV_BF16;              // K and V become f16 here
     static constexpr int kRowB = kKv == FKV_KV_FP8_E4M3 ? 128 : kKv == FKV_KV_BF16 ? 256 : kFp4Row;
     static constexpr int kStageB = kTreeTok * kRowB;               // the K (or V) rows of a tile
-    // The softmax groups take turns, a tile each, with sums and references of their own; with
-    // 128 rows, whose sums fill the tensor memory once, each takes half of the rows of every tile.
-    static constexpr bool kTurns = kR <= 64;
-    // V as f16 goes into tensor memory where that has room; with 128 rows into shared memory.
-    static constexpr bool kVT = kConv && kTurns;
-    static constexpr int kNK = kKv == FKV_KV_FP4 ? (kTurns ? 8 : 3) : kVT ? 5 : 2;
-    static constexpr int kNV = kKv == FKV_KV_FP4 ? (kTurns ? 8 : 3) : kVT ? 5 : kConv || kR <= 32 ? 3 : 2;
-    static constexpr int kNP = kTurns ? 2 : 1;                     // weight buffers
+    static constexpr int kNK = kKv == FKV_KV_FP4 ? 8 : kConv ? 5 : 2;
+    static constexpr int kNV = kKv == FKV_KV_FP4 ? 8 : kConv ? 5 : kR <= 32 ? 3 : 2;
     static constexpr int kParts = kConv ? 1 : 2;                   // words of a weight
-    static constexpr int kHalves = kR > 64 ? 2 : 1;                // 64-column halves of a weight buffer
-    static constexpr int kPW = kR <= 32 ? 64 : 16384 * kHalves;    // from a weight's first word to its second
+    static constexpr int kPW = kR <= 32 ? 64 : 16384;              // from a weight's first word to its second
     static constexpr int kPB = kR <= 32 ? 16384 : kParts * kPW;    // a weight buffer
     static constexpr int kQB = kR * 256;
-    static constexpr int kV16 = kConv && !kVT ? 32768 : 0;
-    static_assert(!kConv || kR >= 64, "fewer rows of FP8 and FP4: tree_attn_small.cu");
+    static_assert(kR <= 64 && (!kConv || kR == 64), "fewer rows of FP8 and FP4: tree_attn_small.cu; more: tree_attn_wide.cu");
     // Softmax warps with many columns take registers of the others: of a thread, at launch, then
     // of the three kinds of warps (no more in all than at launch; whole groups of four warps).
     static constexpr bool kShift = kR >= 32;
@@ -79,14 +69,12 @@ struct TreeCfg {
     static constexpr int kRegs = 128;
     static constexpr int kRegsSoft = kR >= 64 ? 176 : 152, kRegsConv = kR >= 64 ? 88 : 104, kRegsRest = kR >= 64 ? 72 : 104;
     static_assert(2 * kRegsSoft + kRegsConv + kRegsRest <= kThreads / 128 * kRegs, "the block's registers");
-    static constexpr int kND = kR <= 64 ? 4 : 2;                   // units in flight
-    static constexpr int kNC = kTurns ? kR : kR / 2;               // columns of a softmax thread
-    static constexpr int kNS = kTurns ? 4 : 8;                     // softmax warps of a tile
-    // tensor memory columns: K f16 (two buffers), V f16 (two), S (two), O (one per group that takes turns)
-    static constexpr int kTmV = 128, kTmS = kVT ? 256 : kConv ? 128 : 0, kTmO = kTmS + 2 * kR;
-    static_assert(kTmO + (kTurns ? 2 : 1) * kR <= 512, "tensor memory");
+    static constexpr int kND = 4;                                  // units in flight
+    // tensor memory columns: K f16 (two buffers), V f16 (two), S and O (one per softmax group)
+    static constexpr int kTmV = 128, kTmS = kConv ? 256 : 0, kTmO = kTmS + 2 * kR;
+    static_assert(kTmO + 2 * kR <= 512, "tensor memory");
     static constexpr int kNVR = kConv ? 2 : kNV;                   // buffers between converters and issuer
-    static constexpr int kOffP = kQB, kOffV16 = kOffP + kNP * kPB, kOffK = kOffV16 + 2 * kV16;
+    static constexpr int kOffP = kQB, kOffK = kOffP + 2 * kPB;
     static constexpr int kOffV = kOffK + kNK * kStageB, kOffCtrl = kOffV + kNV * kStageB;
 };
 
@@ -95,19 +83,18 @@ struct TreeCtrl {
     using C = TreeCfg<kKv, kR>;
     uint64_t kfull[C::kNK], kempty[C::kNK], vfull[C::kNV], vempty[C::kNV];
     uint64_t k16full[2], k16empty[2], vready[C::kNVR], v16empty[2];
-    uint64_t sfull[2], sempty[2], pfull[C::kNP], pempty[C::kNP];
+    uint64_t sfull[2], sempty[2], pfull[2], pempty[2];
     uint64_t qfull, qempty, oempty, drained[2];
     uint64_t dfull[C::kND], dempty[C::kND], cfull[C::kND];
     TreeUnit unit[C::kND];
     float colscale[C::kND];                                        // a logit in log2 units per unit of S
     uint32_t qmax[C::kND];                                         // the largest |q| of the unit, as bf16 bits
-    // [unit's parity][group] where the groups take turns: the columns' references, negated, and
-    // their warps' sums (or maxima); a moved reference's factor; the factors of the two groups' sums
-    static constexpr int kU = C::kTurns ? 2 : 1;
-    alignas(16) float ref[kU][kU][kR];
-    alignas(16) float red[kU][2][4][C::kTurns ? kR : 8];
-    alignas(16) float up[2][C::kTurns ? kR : 4];
-    alignas(16) float2 part[C::kTurns ? kR : 2];
+    // [unit's parity][group]: the columns' references, negated, and their warps' sums (or maxima);
+    // a moved reference's factor; the factors of the two groups' sums
+    alignas(16) float ref[2][2][kR];
+    alignas(16) float red[2][2][4][kR];
+    alignas(16) float up[2][kR];
+    alignas(16) float2 part[kR];
     uint32_t poison[C::kND][kTreePoison][4];                       // tokens whose V holds NaN or infinities
     TreeShares<C::kThreads, 1> shares;
     uint32_t tmem;
@@ -119,7 +106,7 @@ constexpr int tree_smem() {
     using C = TreeCfg<kKv, kR>;
     using T = TreeCtrl<kKv, kR>;
     static_assert(offsetof(T, ref) % 16 == 0 && offsetof(T, up) % 16 == 0 && offsetof(T, part) % 16 == 0 && C::kOffCtrl % 16 == 0, "read four at a time");
-    static_assert(C::kOffP % 1024 == 0 && C::kOffV16 % 1024 == 0 && C::kOffK % 1024 == 0 && C::kOffV % 1024 == 0,
+    static_assert(C::kOffP % 1024 == 0 && C::kOffK % 1024 == 0 && C::kOffV % 1024 == 0,
                   "swizzled buffers start on 1024 bytes");
     return TreeCfg<kKv, kR>::kOffCtrl + static_cast<int>((sizeof(TreeCtrl<kKv, kR>) + 15) / 16 * 16);
 }
@@ -227,9 +214,9 @@ __device__ __forceinline__ void convert_v_tmem(uint32_t stage, uint32_t dst, int
     }
 }
 // The dim of a lane of O (within its warp's 32).
-template <int kKv, bool kVT>
+template <int kKv>
 __device__ __forceinline__ int dim_of_lane(int lane) {
-    if (!kVT) return lane;
+    if (kKv == FKV_KV_BF16) return lane;
     const int b = lane >> 4, h = (lane >> 3) & 1, r = lane & 7;
     return kKv == FKV_KV_FP8_E4M3 ? 16 * b + 2 * r + h : 4 * r + 2 * b + h;
 }
@@ -264,7 +251,7 @@ tree_attn_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmK, co
     extern __shared__ __align__(1024) uint8_t smem[];
     Ctrl &ct = *reinterpret_cast<Ctrl *>(smem + C::kOffCtrl);
     const uint32_t base = smem_u32(smem);
-    const uint32_t sQ = base, sP = base + C::kOffP, sV16 = base + C::kOffV16, sK = base + C::kOffK, sV = base + C::kOffV;
+    const uint32_t sQ = base, sP = base + C::kOffP, sK = base + C::kOffK, sV = base + C::kOffV;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     constexpr int kConvW = 8, kProdW = 12, kMmaW = kProdW + 1, kMmaW2 = kProdW + 2;
     volatile int32_t *dead = &ct.dead;
@@ -277,10 +264,10 @@ tree_attn_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmK, co
         for (int i = 0; i < C::kNV; ++i) mbar_init(bar(ct.vfull[i]), 1), mbar_init(bar(ct.vempty[i]), kKC);
         for (int i = 0; i < 2; ++i) {
             mbar_init(bar(ct.k16full[i]), 4), mbar_init(bar(ct.k16empty[i]), 1), mbar_init(bar(ct.v16empty[i]), 1);
-            mbar_init(bar(ct.sfull[i]), 1), mbar_init(bar(ct.sempty[i]), C::kNS);
+            mbar_init(bar(ct.sfull[i]), 1), mbar_init(bar(ct.sempty[i]), 4);
         }
         for (int i = 0; i < C::kNVR; ++i) mbar_init(bar(ct.vready[i]), 4);
-        for (int i = 0; i < C::kNP; ++i) mbar_init(bar(ct.pfull[i]), C::kNS), mbar_init(bar(ct.pempty[i]), 1);
+        for (int i = 0; i < 2; ++i) mbar_init(bar(ct.pfull[i]), 4), mbar_init(bar(ct.pempty[i]), 1);
         mbar_init(bar(ct.qfull), 4), mbar_init(bar(ct.qempty), 1), mbar_init(bar(ct.oempty), 8), mbar_init(bar(ct.drained[0]), 1), mbar_init(bar(ct.drained[1]), 1);
         for (int i = 0; i < C::kND; ++i)
             mbar_init(bar(ct.dfull[i]), 1), mbar_init(bar(ct.dempty[i]), 8 + 4 + 2), mbar_init(bar(ct.cfull[i]), 4);
@@ -445,9 +432,8 @@ tree_attn_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmK, co
                 }
             }
         } else {
-            constexpr uint32_t id = umma_idesc(kB16, !C::kVT, true, 128, kR);
-            const uint32_t lP = umma_desc_lo(sP, 16384), lV = umma_desc_lo(C::kConv ? sV16 : sV, 16384);
-            constexpr uint32_t kVStep = (C::kConv ? C::kV16 : C::kStageB) / 16;
+            constexpr uint32_t id = umma_idesc(kB16, kB16, true, 128, kR);
+            const uint32_t lP = umma_desc_lo(sP, 16384), lV = umma_desc_lo(sV, 16384);
             Ring v, pb;
             for (uint32_t units = 0;; ++units) {
                 wait(ct.dfull[d.i], d.ph);
@@ -461,9 +447,9 @@ tree_attn_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmK, co
                     wait(ct.vready[v.i], v.ph);
                     wait(ct.pfull[pb.i], pb.ph);
                     umma_fence_after();
-                    const uint32_t lv = lV + v.i * kVStep, lp = lP + pb.i * (C::kPB / 16);
-                    const uint32_t dst = tmem + C::kTmO + (C::kTurns ? pb.i * kR : 0);
-                    const bool first = i < tb + (C::kTurns ? 2 : 1);       // of a unit and a group: its sums start anew
+                    const uint32_t lv = lV + v.i * (C::kStageB / 16), lp = lP + pb.i * (C::kPB / 16);
+                    const uint32_t dst = tmem + C::kTmO + pb.i * kR;
+                    const bool first = i < tb + 2;                        // of a unit and a group: its sums start anew
                     __syncwarp();
                     if (elect_one()) {
 #pragma unroll
@@ -472,7 +458,7 @@ tree_attn_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmK, co
                             for (int kk = 0; kk < 8; ++kk) {
                                 const uint64_t b = umma_desc(lp + w * (C::kPW / 16) + kk * 128, kHi);
                                 const bool add = !first || w > 0 || kk > 0;
-                                if (C::kVT) umma_ts(dst, tmem + C::kTmV + v.i * 64 + kk * 8, b, id, add);
+                                if (C::kConv) umma_ts(dst, tmem + C::kTmV + v.i * 64 + kk * 8, b, id, add);
                                 else umma_ss(dst, umma_desc(lv + kk * 128, kHi), b, id, add);
                             }
                         }
@@ -480,7 +466,7 @@ tree_attn_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmK, co
                         umma_commit(bar(C::kConv ? ct.v16empty[v.i & 1] : ct.vempty[v.i]));
                     }
                     __syncwarp();
-                    pb.template next<C::kNP>();
+                    pb.template next<2>();
                     v.template next<C::kNVR>();
                 }
             }
@@ -590,7 +576,7 @@ tree_attn_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmK, co
                     k.template next<C::kNK>();
                     kb.template next<2>();
                 }
-                // ---- V: f16 in tensor memory, or rows in an operand buffer; BF16 as it lies ----
+                // ---- V: f16 in tensor memory; BF16 as it lies ----
                 wait(ct.vfull[v.i], v.ph);
                 const uint32_t src = sV + v.i * C::kStageB;
                 const bool whole = tile_whole(u, i);
@@ -604,15 +590,13 @@ tree_attn_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmK, co
                 }
                 constexpr int kF = C::kConv ? kKv : FKV_KV_FP8_E4M3;
                 if (C::kConv) wait(ct.v16empty[vb.i & 1], vb.ph ^ 1);
-                if constexpr (C::kVT) {
+                if constexpr (C::kConv) {
                     umma_fence_after();
                     convert_v_tmem<kF>(src, tmem + tlane + C::kTmV + vb.i * 64, cw, lane);
                     tmem_store_wait();
                     umma_fence_before();
-                } else {
-                    if constexpr (C::kConv) convert_row<kF>(src, sV16 + vb.i * C::kV16, ctid);
                 }
-                if ((C::kConv && !C::kVT) || !whole) fence_proxy_async_smem();
+                if (!whole) fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0) {
                     mbar_arrive(bar(ct.vready[vb.i]));
@@ -637,25 +621,22 @@ tree_attn_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmK, co
     } else {
         // ==== softmax ====
         if constexpr (C::kShift) regs_up<C::kRegsSoft>();
-        constexpr bool kTurns = C::kTurns;
-        constexpr int kNC = C::kNC, kLd = kNC < 32 ? kNC : 32;     // columns of a thread, and of a load
+        constexpr int kNC = kR, kLd = kNC < 32 ? kNC : 32;     // columns of a thread, and of a load
         const int g = warp >> 2, wq = warp & 3, tok = tid & 127, barrier = 1 + g;
-        const int col0 = kTurns ? 0 : g * kNC;                     // this thread's columns begin here
         const uint32_t tlane = static_cast<uint32_t>(32 * wq) << 16;
         const uint32_t tO = tmem + tlane + C::kTmO;
-        const uint32_t sPw = sP + (kTurns ? g * C::kPB : 0) + (col0 >> 6) * 16384 + tok * 128;
+        const uint32_t sPw = sP + g * C::kPB + tok * 128;
         Ring d;
-        int sb = kTurns ? g : 0;                                   // S buffer, and the rounds of it and of the weights' buffer
-        uint32_t sph = 0, pph = 0, turn = 0, par = 0;              // (turn: whose the next tile is; par: the unit's parity)
+        uint32_t ph = 0, turn = 0, par = 0;                        // rounds of the group's buffers, whose the next tile is, the unit's parity
         float sum[kNC];
         while (true) {
             wait(ct.dfull[d.i], d.ph);
-            if (kTurns ? both_any(*dead != 0) : group_any(barrier, *dead != 0)) break;
+            if (both_any(*dead != 0)) break;
             const TreeUnit u = ct.unit[d.i];
             if (u.te < 0) break;
-            float *const refs = kTurns ? ct.ref[par % Ctrl::kU][g % Ctrl::kU] : ct.ref[0][0];
-            const uint32_t sref = smem_u32(refs) + 4 * col0;
-            if (tok < kNC) refs[col0 + tok] = -kTreeNone;
+            float *const refs = ct.ref[par & 1][g];
+            const uint32_t sref = smem_u32(refs);
+            if (tok < kNC) refs[tok] = -kTreeNone;
 #pragma unroll
             for (int j = 0; j < kNC; ++j) sum[j] = 0.f;
             wait(ct.cfull[d.i], d.ph);
@@ -663,13 +644,13 @@ tree_attn_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmK, co
             const float cs = *const_cast<volatile float *>(&ct.colscale[d.i]);
             const uint64_t cs2 = pack2(cs, cs);
             bool had = false;                                      // a tile of this unit
-            for (int i = kTurns ? u.tb + static_cast<int>((g ^ turn) & 1) : u.tb; i < u.te; i += kTurns ? 2 : 1) {
+            for (int i = u.tb + static_cast<int>((g ^ turn) & 1); i < u.te; i += 2) {
                 const bool whole = tile_whole(u, i);
                 uint64_t see = ~0ull;
-                if (__builtin_expect(!whole, 0)) see = seen_by<kNC>(p, u, col0, tile_at<kTreeTok>(u, i) + tok);
-                wait(ct.sfull[sb], sph);
+                if (__builtin_expect(!whole, 0)) see = seen_by<kNC>(p, u, 0, tile_at<kTreeTok>(u, i) + tok);
+                wait(ct.sfull[g], ph);
                 umma_fence_after();
-                const uint32_t ts = tmem + tlane + C::kTmS + sb * kR + col0;
+                const uint32_t ts = tmem + tlane + C::kTmS + g * kR;
                 float x[kNC];
                 // the columns' logits in log2 units, less their references where kLess; unseen ones -infinity
                 auto logits = [&](auto less) {
@@ -704,99 +685,55 @@ tree_attn_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmK, co
                     const float most = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
                     if (__builtin_expect(!group_any(barrier, most > kTreeMost) || tries == 4, 1)) break;
                     // ---- move the references of the columns that need it ----
-                    const int buf = kTurns ? g : 0;
-                    if (had) wait(ct.pempty[buf], pph ^ 1);                      // the sums so far are complete
+                    if (had) wait(ct.pempty[g], ph ^ 1);                      // the sums so far are complete
                     umma_fence_after();
-                    if constexpr (kTurns) {
-                        float(*const red)[kR] = ct.red[par % Ctrl::kU][g];
-                        logits(std::false_type{});
-                        spread<kNC, 16>(x, lane, [](float a, float b) { return fmaxf(a, b); });
-                        constexpr int kHas = kNC >= 32 ? kNC / 32 : 1, kSame = kNC >= 32 ? 1 : 32 / kNC;
-                        if (lane % kSame == 0) {
+                    float(*const red)[kR] = ct.red[par & 1][g];
+                    logits(std::false_type{});
+                    spread<kNC, 16>(x, lane, [](float a, float b) { return fmaxf(a, b); });
+                    constexpr int kHas = kNC >= 32 ? kNC / 32 : 1, kSame = kNC >= 32 ? 1 : 32 / kNC;
+                    if (lane % kSame == 0) {
 #pragma unroll
-                            for (int j = 0; j < kHas; ++j) red[wq][(lane / kSame) * kHas + j] = x[j];
+                        for (int j = 0; j < kHas; ++j) red[wq][(lane / kSame) * kHas + j] = x[j];
+                    }
+                    group_sync(barrier);
+                    bool move = false;
+                    if (tok < kNC) {
+                        const float z = fmaxf(fmaxf(red[0][tok], red[1][tok]), fmaxf(red[2][tok], red[3][tok])), was = -refs[tok];
+                        move = z - was > kTreeMost;
+                        const float ref = move ? z - kTreeTop : was;
+                        refs[tok] = -ref;
+                        ct.up[g][tok] = move ? ex2(was - ref) : 1.f;
+                    }
+                    const bool any = group_any(barrier, move);
+                    const uint32_t sup = smem_u32(ct.up[g]);
+                    if (any && had) {
+#pragma unroll
+                        for (int j = 0; j < kNC; j += 4) {
+                            const float4 f = ld_shared_f4(sup + 4 * j);
+                            sum[j] *= f.x, sum[j + 1] *= f.y, sum[j + 2] *= f.z, sum[j + 3] *= f.w;
                         }
-                        group_sync(barrier);
-                        bool move = false;
-                        if (tok < kNC) {
-                            const float z = fmaxf(fmaxf(red[0][tok], red[1][tok]), fmaxf(red[2][tok], red[3][tok])), was = -refs[tok];
-                            move = z - was > kTreeMost;
-                            const float ref = move ? z - kTreeTop : was;
-                            refs[tok] = -ref;
-                            ct.up[g][tok] = move ? ex2(was - ref) : 1.f;
-                        }
-                        const bool any = group_any(barrier, move);
-                        const uint32_t sup = smem_u32(ct.up[g]);
-                        if (any && had) {
-#pragma unroll
-                            for (int j = 0; j < kNC; j += 4) {
-                                const float4 f = ld_shared_f4(sup + 4 * j);
-                                sum[j] *= f.x, sum[j + 1] *= f.y, sum[j + 2] *= f.z, sum[j + 3] *= f.w;
-                            }
-#pragma unroll
-                            for (int c = 0; c < kNC; c += 8) {
-                                float y[8];
-                                uint32_t o[8];
-                                tmem_load(tO + g * kR + c, y);
-#pragma unroll
-                                for (int j = 0; j < 8; j += 4) {
-                                    const float4 f = ld_shared_f4(sup + 4 * (c + j));
-                                    o[j] = __float_as_uint(y[j] * f.x), o[j + 1] = __float_as_uint(y[j + 1] * f.y);
-                                    o[j + 2] = __float_as_uint(y[j + 2] * f.z), o[j + 3] = __float_as_uint(y[j + 3] * f.w);
-                                }
-                                tmem_store(tO + g * kR + c, o);
-                            }
-                            tmem_store_wait();
-                            umma_fence_before();
-                        }
-                    } else {
-                        float(*const red)[8] = ct.red[0][g];
 #pragma unroll
                         for (int c = 0; c < kNC; c += 8) {
                             float y[8];
-                            tmem_load(ts + c, y);
+                            uint32_t o[8];
+                            tmem_load(tO + g * kR + c, y);
 #pragma unroll
-                            for (int j = 0; j < 8; ++j) {
-                                float z = __fmul_rn(y[j], cs);
-                                if (!((see >> (c + j)) & 1)) z = -INFINITY;
-                                const int key = __float_as_int(z) ^ ((__float_as_int(z) >> 31) & 0x7FFFFFFF);   // ordered as the floats
-                                const int top = __reduce_max_sync(kAll, key);
-                                if (lane == 0) red[wq][j] = __int_as_float(top ^ ((top >> 31) & 0x7FFFFFFF));
+                            for (int j = 0; j < 8; j += 4) {
+                                const float4 f = ld_shared_f4(sup + 4 * (c + j));
+                                o[j] = __float_as_uint(y[j] * f.x), o[j + 1] = __float_as_uint(y[j + 1] * f.y);
+                                o[j + 2] = __float_as_uint(y[j + 2] * f.z), o[j + 3] = __float_as_uint(y[j + 3] * f.w);
                             }
-                            group_sync(barrier);
-                            float up[8], ref[8];
-                            bool any = false;
-#pragma unroll
-                            for (int j = 0; j < 8; ++j) {
-                                const float z = fmaxf(fmaxf(red[0][j], red[1][j]), fmaxf(red[2][j], red[3][j])), was = -refs[col0 + c + j];
-                                const bool move = z - was > kTreeMost;
-                                ref[j] = move ? z - kTreeTop : was;
-                                up[j] = move ? ex2(was - ref[j]) : 1.f;
-                                any |= move;
-                                sum[c + j] *= up[j];
-                            }
-                            group_sync(barrier);                   // the old references and the maxima are read
-#pragma unroll
-                            for (int j = 0; j < 8; ++j)
-                                if (tok == j) refs[col0 + c + j] = -ref[j];
-                            if (any && had) {
-                                uint32_t o[8];
-                                tmem_load(tO + col0 + c, y);
-#pragma unroll
-                                for (int j = 0; j < 8; ++j) o[j] = __float_as_uint(y[j] * up[j]);
-                                tmem_store(tO + col0 + c, o);
-                                tmem_store_wait();
-                            }
+                            tmem_store(tO + g * kR + c, o);
                         }
+                        tmem_store_wait();
                         umma_fence_before();
-                        group_sync(barrier);                       // the new references are there
                     }
                 }
                 // ---- weights ----
                 umma_fence_before();                               // S is read
                 __syncwarp();
-                if (lane == 0) mbar_arrive(bar(ct.sempty[sb]));
-                wait(ct.pempty[kTurns ? g : 0], pph ^ 1);
+                if (lane == 0) mbar_arrive(bar(ct.sempty[g]));
+                wait(ct.pempty[g], ph ^ 1);
 #pragma unroll
                 for (int j = 0; j < kNC; j += 8) {
 #pragma unroll
@@ -829,36 +766,33 @@ tree_attn_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmK, co
                 }
                 fence_proxy_async_smem();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(bar(ct.pfull[kTurns ? g : 0]));
+                if (lane == 0) mbar_arrive(bar(ct.pfull[g]));
                 had = true;
-                pph ^= 1;
-                if (kTurns) sph ^= 1;
-                else if ((sb ^= 1) == 0) sph ^= 1;
+                ph ^= 1;
             }
             turn += u.te - u.tb;
             // ---- end of this CTA's part of the unit ----
             // sums over the tokens; the groups' sums joined; a group writes half of the columns
             constexpr int kHalf = kR / 2, kPer = kNC >= 32 ? kNC / 32 : 1, kSpan = kNC >= 32 ? 1 : 32 / kNC;
             spread<kNC, 16>(sum, lane, [](float a, float b) { return a + b; });
-            if (had) wait(ct.pempty[kTurns ? g : 0], pph ^ 1);             // all products are done, the weights' buffer is free
-            float *const ls = kTurns ? &ct.red[par % Ctrl::kU][g][0][0] : reinterpret_cast<float *>(smem + C::kOffP + 16384 * g);
+            if (had) wait(ct.pempty[g], ph ^ 1);                           // all products are done, the weights' buffer is free
+            float *const ls = &ct.red[par & 1][g][0][0];
             if (lane % kSpan == 0) {
 #pragma unroll
                 for (int j = 0; j < kPer; ++j) ls[wq * kNC + (lane / kSpan) * kPer + j] = sum[j];
             }
-            if (kTurns) both_any(false);
-            else group_sync(barrier);
+            both_any(false);
             umma_fence_after();
             const bool wrong = *const_cast<volatile int32_t *>(&ct.unit[d.i].bad) != 0, cut = u.slot >= 0;
-            float2 *const part = kTurns ? ct.part + g * kHalf : reinterpret_cast<float2 *>(smem + C::kOffP + 16384 * g + 1024);
+            float2 *const part = ct.part + g * kHalf;
             const int c0 = g * kHalf;                              // the columns this group writes
             if (tok < kHalf) {
                 float l[2] = {0.f, 0.f}, m[2] = {kTreeNone, kTreeNone};
 #pragma unroll
-                for (int k = 0; k < (kTurns ? 2 : 1); ++k) {
-                    const float *x = kTurns ? &ct.red[par % Ctrl::kU][k][0][0] + c0 + tok : ls + tok;
+                for (int k = 0; k < 2; ++k) {
+                    const float *x = &ct.red[par & 1][k][0][0] + c0 + tok;
                     l[k] = (x[0] + x[kNC]) + (x[2 * kNC] + x[3 * kNC]);
-                    m[k] = -(kTurns ? ct.ref[par % Ctrl::kU][k % Ctrl::kU][c0 + tok] : refs[c0 + tok]);
+                    m[k] = -ct.ref[par & 1][k][c0 + tok];
                 }
                 const float top = l[0] == 0.f ? m[1] : l[1] == 0.f ? m[0] : fmaxf(m[0], m[1]);
                 float f[2];
@@ -878,9 +812,9 @@ tree_attn_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmK, co
             }
             group_sync(barrier);
             const bool both = u.te - u.tb > 1;                     // which groups had tiles
-            const bool had0 = !kTurns || both || had == (g == 0), had1 = kTurns && (both || had == (g == 1));
+            const bool had0 = both || had == (g == 0), had1 = both || had == (g == 1);
             // the dim of this thread's lane (convert_v_tmem)
-            const int dim = 32 * wq + dim_of_lane<kKv, C::kVT>(lane);
+            const int dim = 32 * wq + dim_of_lane<kKv>(lane);
             const bool anyodd = *const_cast<volatile int32_t *>(&ct.unit[d.i].odd) != 0;
             int tk = c0 / p.group, hr = c0 - tk * p.group;         // of the column: token and query head
             __nv_bfloat16 *out = p.out + (static_cast<int64_t>(u.tok0 + tk) * p.hq + u.h * p.group + hr) * 128 + dim;
@@ -1081,7 +1015,7 @@ namespace {
 
 constexpr int kMaxDev = 64;
 std::mutex g_mu;
-unsigned long long g_ready[kMaxDev][3][4];                         // the context in which an instance's shared memory was set
+unsigned long long g_ready[kMaxDev][3][3];                         // the context in which an instance's shared memory was set
 
 PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
     static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
@@ -1113,6 +1047,9 @@ bool known_kv(int kv) { return kv == FKV_KV_FP8_E4M3 || kv == FKV_KV_BF16 || kv 
 
 // Rows of a unit: the smallest instance that holds the query heads of the requests' mean
 // number of tokens.
+// From 128 rows on they lie on M (tree_attn_wide.cu): with 128 that is 126 us instead of 145 over BF16, 117 instead of
+// 130 over FP8 and 103 instead of 130 over FP4 (16 requests of 8192 tokens, 16 drafted); with 64, half of M, 801 instead
+// of 603 (FP8, 64 requests around 16k, 8 drafted).
 int rows_of(int64_t n_tokens, int64_t batch, int64_t group) {
     const int64_t want = group * ((n_tokens + batch - 1) / (batch > 0 ? batch : 1));
     for (int r = 16; r < 128; r *= 2)
@@ -1148,7 +1085,7 @@ fkv_status launch_tree(const TreeParams &p, int sms, const CUtensorMap &tmK, con
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDev) return FKV_ERR_CUDA;
     {
         std::lock_guard<std::mutex> lk(g_mu);
-        constexpr int ri = kR == 16 ? 0 : kR == 32 ? 1 : kR == 64 ? 2 : 3;
+        constexpr int ri = kR == 16 ? 0 : kR == 32 ? 1 : 2;
         const unsigned long long ctx = current_context_id();
         if (ctx == 0 || g_ready[dev][kKv][ri] != ctx) {
             if (cudaFuncSetAttribute(tree_attn_kernel<kKv, kR>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
@@ -1167,7 +1104,7 @@ fkv_status launch_rows(int rows, const TreeParams &p, int sms, const CUtensorMap
         if (rows == 16) return launch_tree<kKv, 16>(p, sms, tmK, tmV, st);
         if (rows == 32) return launch_tree<kKv, 32>(p, sms, tmK, tmV, st);
     }
-    return rows == 64 ? launch_tree<kKv, 64>(p, sms, tmK, tmV, st) : launch_tree<kKv, 128>(p, sms, tmK, tmV, st);
+    return launch_tree<kKv, 64>(p, sms, tmK, tmV, st);
 }
 
 // Both calls.  tree: rows and masks per drafted token; else one token a request.

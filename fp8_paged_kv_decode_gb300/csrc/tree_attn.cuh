@@ -406,7 +406,7 @@ __device__ __forceinline__ void convert_row(uint32_t stage, uint32_t dst, int to
 // ---------------------------------------------------------------------------
 // Joins the parts of cut units (tree_attn.cu).
 cudaError_t launch_tree_join(const TreeParams &p, int shares, int rows, cudaStream_t st);
-// The kernel of more than 128 rows a unit (tree_attn_wide.cu).
+// The kernel of 128 or 256 rows a unit (tree_attn_wide.cu).
 constexpr int kTreeWideRows = 256;
 fkv_status launch_tree_wide(const TreeParams &p, int kv, int rows, int sms, const CUtensorMap &tmK, const CUtensorMap &tmV, cudaStream_t st);
 // The kernel of few rows a unit (tree_attn_small.cu): 16 or 32, FP8 or FP4.
