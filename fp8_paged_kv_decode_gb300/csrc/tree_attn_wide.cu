@@ -1,26 +1,28 @@
-// tree_attn_wide.cu -- tree attention of many rows (more than 128 a KV head).
+// tree_attn_wide.cu -- tree attention of many rows (65 and more a KV head).
 //
 // Here the products themselves are the work, so rows go on M: S = Q K^T and O += P V, both
-// 128 x 128 x 128, of two blocks of 128 rows that share every K and V tile.  A row is then a
-// lane of tensor memory and one thread of a softmax group: its reference, its sum and its
-// mask are that thread's own, no barrier or shuffle joins threads, and P replaces S where it
-// lies, as the second product's operand in tensor memory.  While one block's weights are
-// computed, the other's products run.
+// 128 x 128 x 128.  A row is then a lane of tensor memory and one thread of a softmax group:
+// its reference, its sum and its mask are that thread's own, no barrier or shuffle joins
+// threads, and P replaces S where it lies, as the second product's operand in tensor memory.
+// While one softmax group computes weights, the other's products run: with more than 128 rows
+// the groups have a block of 128 rows each and share every K and V tile; with fewer they take
+// one block's tiles by turns, with references and sums of their own that are joined at the end.
 //
-// Over BF16 weights are two words (the first truncated, the second what is left, rounded): 16 bits
-// of them, as one word's 8 would be the largest error of the call.  So a tile costs a block 24
-// products of 128 x 128 x 16, 80 cycles each at the rate of a large matrix product, and 16384
-// exponentials, 1024 cycles of an SM.
+// Over BF16 weights are two words (the first truncated, the second what is left, rounded): 16
+// bits of them, as one word's 8 would be the largest error of the call.  So a tile costs a block
+// 24 products of 128 x 128 x 16, 80 cycles each at the rate of a large matrix product, and 16384
+// exponentials, 1024 cycles of an SM.  FP8 and FP4 rows become f16 operands in shared memory, by
+// four more warps; their weights are one f16 word, 16 products a tile.
 //
-// 16 requests of 8192 tokens, 61 drafted, 64 query heads on 8: 320 us, 475 with tokens on M
-// (tree_attn.cu), 140 at the rate of a large product were a weight one word, 220 as it is.  What
-// is left is a block's chain, weights after S after O, which two blocks hide only in part.
-// Tried: S of half tiles, so that the softmax begins earlier, 424 us (the tensor cores drain
-// between products of different shapes); O of half tiles and an issuer that takes whichever
-// block is ready, 386; all 128 logits of a row in registers with the others' given up, 348.
+// 16 requests of 8192 tokens, 61 drafted, 64 query heads on 8: 320 us over BF16 (475 with tokens
+// on M; 140 at the rate of a large product were a weight one word, 220 as it is), 265 over FP8
+// (398), 263 over FP4 (394).  What is left is a block's chain, weights after S after O, which
+// two groups hide only in part.  Tried: S of half tiles, so that the softmax begins earlier, 424
+// us (the tensor cores drain between products of different shapes); O of half tiles and an
+// issuer that takes whichever block is ready, 386; all 128 logits of a row in registers, 348.
 //
-// One CTA per SM, 10 warps: two softmax groups of four, a producer (a unit's geometry; K and V
-// tiles by turns into one ring of 32 KB stages), an issuer.
+// One CTA per SM: two softmax groups of four warps, a producer (a unit's geometry; K and V tiles
+// by turns into one ring), an issuer, and the four converters.
 #include <cudaTypedefs.h>
 
 #include <mutex>
