@@ -31,8 +31,8 @@
 // FP8 and FP4 weights are one f16 word, BF16 ones two BF16 words.
 //
 // Few rows over BF16 are bound by memory (8 requests, window of 32768: 86 us, 93% of a copy's
-// rate); 64 requests around 16k tokens, 8 drafted, over FP8 nearly so (565 to 650 us from run to
-// run, 66 to 77%): there a tile's way through five kinds of warps, and the instruction cache
+// rate); 64 requests around 16k tokens, 8 drafted, over FP8 nearly so (565 to 660 us from run to
+// run, 65 to 77%): there a tile's way through five kinds of warps, and the instruction cache
 // that their code shares, cost what is missing.
 #include <cudaTypedefs.h>
 

@@ -364,9 +364,10 @@ def test_python_refusals():
         fkv.alloc_tree_workspace(2, 2, 7, 2)
 
 
-WIDE = [  # 128 to 1300 rows of a KV head, in units of 128 and 256
+WIDE = [  # 72 to 1300 rows of a KV head, in units of 128 and 256
     (16, 1, 16, [90, 0, 1000], [9, 30, 17]), (32, 1, 32, [130, 255, 256], [5, 8, 64]), (48, 2, 64, [700, 3], [11, 6]),
-    (128, 1, 128, [400, 127], [2, 3]), (20, 4, 16, [4000, 60], [33, 61]), (8, 8, 64, [500, 30], [256, 200]), (127, 1, 32, [77], [10])]
+    (128, 1, 128, [400, 127], [2, 3]), (20, 4, 16, [4000, 60], [33, 61]), (8, 8, 64, [500, 30], [256, 200]), (127, 1, 32, [77], [10]),
+    (16, 1, 64, [900, 50, 3], [6, 7, 5]), (72, 1, 16, [300], [1]), (96, 1, 32, [2000, 127, 0], [1, 1, 1]), (7, 1, 64, [5000], [18])]
 
 
 @pytest.mark.parametrize("kind", KINDS)
@@ -433,9 +434,10 @@ def test_few_requests_in_many_parts(kind):
 
 
 @pytest.mark.parametrize("kind", ["fp8", "bf16"])
-def test_wide_units_of_rising_logits(kind):
+@pytest.mark.parametrize("n", [[12, 17], [5, 7]])
+def test_wide_units_of_rising_logits(kind, n):
     """Logits that grow along the tokens, by 150 nats in all and again: references move in either half of a tile."""
-    c = Case(kind, 16, 1, 64, [900, 333], [12, 17], seed=35)
+    c = Case(kind, 16, 1, 64, [900, 333], n, seed=35)
     one = np.uint16(0x3F80) if kind == "bf16" else np.uint8(0x38)
     c.kc[..., 0], c.sm = 0, 0.3
     if c.ks is not None:
