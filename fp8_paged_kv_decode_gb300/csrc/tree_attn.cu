@@ -1059,7 +1059,8 @@ int rows_of(int64_t n_tokens, int64_t batch, int64_t group) {
 
 // Which kernel.  Up to 32 rows over FP8 or FP4 the products are little work, and the hand-overs of a tile from warp to warp
 // cost more than they save: a window of 4096 over FP8 takes 98 us instead of 115, one of 1024 over 16-token FP4 pages 101
-// instead of 176, 64 requests around 16k tokens with up to 4 drafted (32 rows) 457 instead of 486 (batch of 16: 145, 140).
+// instead of 176, 64 requests around 16k tokens with up to 4 drafted (32 rows) 457 instead of 486 (batch of 16: 145, 140;
+// of 4: 67, 58, of which 13 are the joining of a hundred parts a unit).
 // BF16 needs no conversions and is read by the tensor cores as it lies.
 bool small_call(int kv, int rows) { return kv != FKV_KV_BF16 && rows <= 32; }
 
