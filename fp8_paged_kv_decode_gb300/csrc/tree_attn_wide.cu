@@ -641,9 +641,11 @@ tree_wide_kernel(const TreeParams p, int rows, const __grid_constant__ CUtensorM
             }
             __syncwarp();
             if (turns) {
-                // both groups have read each other's sums
+                // all eight warps have read the sums: the next unit's Q may lie over those that this group's other warps
+                // read, and its sums over the other group's
                 if (lane == 0) mbar_arrive(bar(ct.xdone[g]));
-                wait(ct.xdone[g ^ 1], n_turns & 1);
+                wait(ct.xdone[0], n_turns & 1);
+                wait(ct.xdone[1], n_turns & 1);
                 ++n_turns;
                 next_q();
             }

@@ -544,3 +544,17 @@ def test_head_scales_of_zero_and_below(kind, Hq, n):
         c.vs[1] = -c.vs[1]
         c.check(c.tree())
         c.check(c.tree(window=60, sinks=2), 60, 2)
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("n", [40, 47])
+def test_wide_units_of_one_and_two_blocks_in_turn(kind, n):
+    """Each KV head's drafted tokens are a unit of 256 rows and one of 64 (or 120), whose sums lie where the next Q goes."""
+    import torch
+    c = Case(kind, 64, 8, 16, [5, 150, 2, 90, 260, 31, 0, 120] * 8, [n] * 64, seed=n)
+    t = c.tensors()
+    first = c.tree(t).clone()
+    c.check(first)
+    for _ in range(10):
+        t["out"].fill_(float("nan"))
+        assert torch.equal(c.tree(t).view(torch.int16), first.view(torch.int16))
