@@ -298,7 +298,7 @@ tree_attn_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmK, co
         TreeRequest cur = tree_request(p, r), nxt = tree_request(p, r + 1);
         Ring d, k, v;
         const int npg = kTreeTok / p.page_size;
-        while (left > 0 && !*dead) {
+        while (left > 0 && !__any_sync(kAll, *dead != 0)) {
             const TreeSpan sp = tree_span<kTreeTok>(p, cur);
             const int mt = (cur.n + tpt - 1) / tpt, units = mt * p.hkv;
             const uint64_t policy = mt > 1 ? again : once;
@@ -306,7 +306,7 @@ tree_attn_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmK, co
                 const int te = left < sp.tiles - tb ? tb + static_cast<int>(left) : sp.tiles;
                 const int h = ui / mt, m = ui - h * mt;
                 wait(ct.dempty[d.i], d.ph ^ 1);
-                if (*dead) break;                                  // others may still read what is there
+                if (__any_sync(kAll, *dead != 0)) break;           // others may still read what is there
                 TreeUnit u;
                 u.tb = tb;
                 u.te = te;
@@ -404,8 +404,7 @@ tree_attn_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmK, co
             for (uint32_t units = 0;; ++units) {
                 wait(ct.dfull[d.i], d.ph);
                 const int tb = *const_cast<volatile int32_t *>(&ct.unit[d.i].tb), te = *const_cast<volatile int32_t *>(&ct.unit[d.i].te);
-                if (te < 0 || *dead) break;
-                __syncwarp();
+                if (__any_sync(kAll, te < 0 || *dead != 0)) break;
                 if (elect_one()) mbar_arrive(bar(ct.dempty[d.i]));
                 d.template next<C::kND>();
                 wait(ct.qfull, units & 1);
@@ -438,8 +437,7 @@ tree_attn_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmK, co
             for (uint32_t units = 0;; ++units) {
                 wait(ct.dfull[d.i], d.ph);
                 const int tb = *const_cast<volatile int32_t *>(&ct.unit[d.i].tb), te = *const_cast<volatile int32_t *>(&ct.unit[d.i].te);
-                if (te < 0 || *dead) break;
-                __syncwarp();
+                if (__any_sync(kAll, te < 0 || *dead != 0)) break;
                 if (elect_one()) mbar_arrive(bar(ct.dempty[d.i]));
                 d.template next<C::kND>();
                 if (units) wait(ct.oempty, (units - 1) & 1);
@@ -487,7 +485,7 @@ tree_attn_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmK, co
         while (true) {
             wait(ct.dfull[d.i], d.ph);
             const TreeUnit u = ct.unit[d.i];
-            if (u.te < 0 || *dead) break;
+            if (group_any(4, u.te < 0 || *dead != 0)) break;       // all four warps or none: they meet at barriers below
             // ---- the unit's Q ----
             wait(ct.qempty, (nu & 1) ^ 1);
             constexpr int kU = kR / 8 < 8 ? kR / 8 : 8;        // rows of a thread at a time

@@ -146,14 +146,14 @@ tree_wide_kernel(const TreeParams p, int rows, const __grid_constant__ CUtensorM
         Ring raw;
         const int npg = kTreeTok / p.page_size;
         const uint64_t policy = l2_policy_evict_normal();
-        for (; left > 0 && r < p.batch && !*dead; ++r, off = 0) {
+        for (; left > 0 && r < p.batch && !__any_sync(kAll, *dead != 0); ++r, off = 0) {
             const TreeRequest q = tree_request(p, r);
             if (!q.live) continue;
             const TreeSpan sp = tree_span<kTreeTok>(p, q);
             const int mt = (q.n + tpt - 1) / tpt, units = mt * p.hkv;
             for (int ui = static_cast<int>(off / sp.tiles), tb = static_cast<int>(off % sp.tiles); ui < units && left > 0; ++ui, tb = 0) {
                 wait(ct.dempty[d.i], d.ph ^ 1);
-                if (*dead) break;                                  // others may still read what is there
+                if (__any_sync(kAll, *dead != 0)) break;           // others may still read what is there
                 TreeUnit u;
                 const int m = ui % mt;
                 u.tb = tb;
