@@ -595,11 +595,12 @@ def kernels_per_call(entry_point: str) -> int:
 
 def selftest_wait(limit_ns: int, complete: bool = False, result=None, stream=None):
     """Run the failure path of the kernels' bounded waits on the GPU: one
-    block waits, with the library's two wait helpers, on an mbarrier that
+    block waits, with the library's three wait helpers, on an mbarrier that
     nothing completes (``complete=False``) and gives up after ``limit_ns``,
     setting DEVERR_TIMEOUT; with ``complete=True`` the waits return at once.
     ``result``: None or a CUDA uint32 tensor of 2 (1 = the wait saw the
-    barrier complete, 0 = it gave up, per warp)."""
+    barrier complete, 0 = it gave up; [0] of the spinning helper and that of
+    tree and window attention, 2 if they differ, [1] of the sleeping one)."""
     if result is not None:
         _dev(result)
         import torch

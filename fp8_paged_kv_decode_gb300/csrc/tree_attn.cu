@@ -256,7 +256,7 @@ tree_attn_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmK, co
     constexpr int kConvW = 8, kProdW = 12, kMmaW = kProdW + 1, kMmaW2 = kProdW + 2;
     volatile int32_t *dead = &ct.dead;
     auto bar = [&](uint64_t &b) { return smem_u32(&b); };
-    auto wait = [&](uint64_t &b, uint32_t parity) { tree_wait(smem_u32(&b), parity, dead, p.err); };
+    auto wait = [&](uint64_t &b, uint32_t parity) { return tree_wait(smem_u32(&b), parity, dead, p.err); };
 
     if (tid == 0) {
         constexpr int kKC = C::kConv ? 4 : 1;                      // who empties a stage: converter warps, or the issuer
@@ -359,10 +359,10 @@ tree_attn_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmK, co
                             if (kKv == FKV_KV_BF16) tma_load_4d(dst + 16384 + lane * p.page_size * 128, tm, bar(full), 64, 0, h, pg, policy);
                         }
                     };
-                    wait(ct.kempty[k.i], k.ph ^ 1);
+                    if (__any_sync(kAll, !wait(ct.kempty[k.i], k.ph ^ 1))) break;         // a stage that is still read
                     copy(ct.kfull[k.i], sK + k.i * C::kStageB, &tmK, p.k_cache);
                     k.template next<C::kNK>();
-                    wait(ct.vempty[v.i], v.ph ^ 1);
+                    if (__any_sync(kAll, !wait(ct.vempty[v.i], v.ph ^ 1))) break;
                     copy(ct.vfull[v.i], sV + v.i * C::kStageB, &tmV, p.v_cache);
                     v.template next<C::kNV>();
                 }

@@ -314,7 +314,7 @@ __device__ __forceinline__ TreeTotal tree_shares(const TreeParams &p, int tpt, T
 // ---------------------------------------------------------------------------
 constexpr int kTreeTok = 128;                  // tokens of a tile
 constexpr int kTreePoison = 10;                // tiles of a unit that hold tokens not seen by every row, at most (9)
-constexpr int kTreeTests = 1 << 24;
+constexpr uint32_t kTreeWaitTicks = 2000000000ull >> 10;      // of 1024 ns: a wait's limit
 constexpr uint64_t kTreeDrainNs = 2000000000ull;
 
 struct Ring {                                  // a buffer of a ring and the parity of its current round
@@ -329,22 +329,27 @@ struct Ring {                                  // a buffer of a ring and the par
     }
 };
 
-// Waits for a phase.  After kTreeTests tests without it (each sleeps in hardware for a while;
-// some seconds in all) the call has failed: that is recorded, and from then on no wait of the
-// block waits, so that it ends soon, with outputs that are not valid.
-__device__ __forceinline__ void tree_wait(uint32_t bar, uint32_t parity, volatile int32_t *dead, uint32_t *err) {
-    if (__builtin_expect(mbar_try_wait(bar, parity), 1)) return;
-    int left = kTreeTests;
+// Waits for a phase; false: it gave up.  After `limit` ticks without it the call has failed: that
+// is recorded, and from then on no wait of the block waits, so that it ends soon, with outputs
+// that are not valid.  The clock is read only every 64 tests (a test sleeps in hardware for a
+// while; most waits are over before).
+__device__ __forceinline__ bool tree_wait(uint32_t bar, uint32_t parity, volatile int32_t *dead, uint32_t *err,
+                                          uint32_t limit = kTreeWaitTicks) {
+    if (__builtin_expect(mbar_try_wait(bar, parity), 1)) return true;
+    uint32_t since = 0;
 #pragma unroll 1
-    while (!mbar_try_wait(bar, parity)) {
-        if (__builtin_expect((--left & 0xFFF) == 0, 0)) {
-            if (left <= 0) {
+    for (uint32_t i = 1; !mbar_try_wait(bar, parity); ++i) {
+        if (__builtin_expect((i & 63u) == 0, 0)) {
+            const uint32_t now = static_cast<uint32_t>(globaltimer_ns() >> 10);
+            if (i == 64) since = now;
+            if (now - since > limit) {
                 *dead = 1;
                 atomicOr(err, FKV_DEVERR_TIMEOUT);
             }
-            if (*dead) return;
+            if (*dead) return false;
         }
     }
+    return true;
 }
 
 // ---------------------------------------------------------------------------

@@ -48,6 +48,7 @@ struct SmallCtrl {
     uint64_t full[C::kWarps][C::kStages];
     uint32_t poison[C::kWarps][kSmallPoison];  // tokens whose V holds NaN, of each tile that not every row sees whole
     TreeShares<C::kThreads, C::kWarps> shares;
+    int32_t dead;                              // a wait gave up
 };
 
 // 16 dims of two K chunks of token g as the second operand of the eight steps of K.
@@ -81,6 +82,7 @@ tree_small_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmK, c
     __shared__ SmallCtrl<kKv, kMB> ct;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
     const uint32_t ring = smem_u32(smem) + warp * C::kWarpB, sQ = ring + C::kStages * C::kStageB, bars = smem_u32(ct.full[warp]);
+    if (threadIdx.x == 0) ct.dead = 0;
     if (lane == 0) {
         for (int i = 0; i < C::kStages; ++i) mbar_init(bars + 8 * i, 1);
         fence_mbar_init();
@@ -220,10 +222,7 @@ tree_small_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmK, c
 #pragma unroll 1
             for (int i = u.tb; i < u.te; ++i) {
                 const uint32_t tile = ring + stage * C::kStageB;
-                int tests = 1 << 24;
-                while (!mbar_try_wait(bars + 8 * stage, phase) && --tests) {
-                }
-                if (__any_sync(kAll, !tests)) {
+                if (__any_sync(kAll, !tree_wait(bars + 8 * stage, phase, &ct.dead, p.err))) {
                     gone = true;
                     break;
                 }
@@ -440,7 +439,6 @@ tree_small_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmK, c
     if (lane == 0) p.joins[share] = join;
     if (gone) {
         // copies in flight still land in this warp's memory
-        if (lane == 0) atomicOr(p.err, FKV_DEVERR_TIMEOUT);
         const uint64_t began = globaltimer_ns();
         while (globaltimer_ns() - began < 200000000ull) __nanosleep(1000);
     }

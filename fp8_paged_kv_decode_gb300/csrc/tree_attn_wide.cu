@@ -111,7 +111,7 @@ tree_wide_kernel(const TreeParams p, int rows, const __grid_constant__ CUtensorM
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     volatile int32_t *dead = &ct.dead;
     auto bar = [&](uint64_t &b) { return smem_u32(&b); };
-    auto wait = [&](uint64_t &b, uint32_t parity) { tree_wait(smem_u32(&b), parity, dead, p.err); };
+    auto wait = [&](uint64_t &b, uint32_t parity) { return tree_wait(smem_u32(&b), parity, dead, p.err); };
     if (tid == 0) {
         for (int i = 0; i < C::kStages; ++i) mbar_init(bar(ct.full[i]), C::kConv ? 4 : 1), mbar_init(bar(ct.empty[i]), 1);
         for (int i = 0; i < C::kRaw; ++i) mbar_init(bar(ct.rfull[i]), 1), mbar_init(bar(ct.rempty[i]), 4);
@@ -212,12 +212,12 @@ tree_wide_kernel(const TreeParams p, int rows, const __grid_constant__ CUtensorM
                         const CUtensorMap *tm = kv ? &tmV : &tmK;
                         const uint8_t *cache = kv ? p.v_cache : p.k_cache;
                         if constexpr (C::kConv) {
-                            wait(ct.rempty[raw.i], raw.ph ^ 1);
+                            if (__any_sync(kAll, !wait(ct.rempty[raw.i], raw.ph ^ 1))) break;   // a stage that is still read
                             copy(ct.rfull[raw.i], sRaw + raw.i * C::kRawB, tm, cache);
                             raw.template next<C::kRaw>();
                         } else {
                             Turn &at = kv ? v : k;
-                            wait(ct.empty[at.i], at.ph ^ 1);
+                            if (__any_sync(kAll, !wait(ct.empty[at.i], at.ph ^ 1))) break;
                             copy(ct.full[at.i], sRing + at.i * kStageB, tm, cache);
                             at.template next<C::kStages>();
                         }

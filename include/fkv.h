@@ -676,13 +676,15 @@ FKV_API int32_t fkv_kernels_per_call(const char *entry_point);
  * (diagnostic; the pages have no counterpart).  Every wait in the library's
  * kernels is on an mbarrier that a copy or another warp completes, and gives
  * up after a time limit, recording FKV_DEVERR_TIMEOUT instead of hanging.
- * This launches one block whose two warps run those two wait helpers (the
- * spinning and the sleeping one) on an mbarrier that nothing completes: each
- * gives up after limit_ns nanoseconds, sets FKV_DEVERR_TIMEOUT and the kernel
- * ends normally.  With complete != 0 the block completes the barrier first
- * and both waits return at once (no error bit).  result: NULL, or a device
- * uint32[2] receiving 1 (the wait saw the barrier complete) or 0 (it gave
- * up) per warp.  limit_ns above 10 s returns FKV_ERR_INVALID_ARG.
+ * This launches one block whose three warps run those wait helpers (the
+ * spinning one, the sleeping one, and that of tree and window attention) on an
+ * mbarrier that nothing completes: each gives up after limit_ns nanoseconds,
+ * sets FKV_DEVERR_TIMEOUT and the kernel ends normally.  With complete != 0 the
+ * block completes the barrier first and all waits return at once (no error
+ * bit).  result: NULL, or a device uint32[2] receiving 1 (the wait saw the
+ * barrier complete) or 0 (it gave up): [0] of the first and third helper (2:
+ * they do not agree), [1] of the sleeping one.  limit_ns above 10 s returns
+ * FKV_ERR_INVALID_ARG.
  * Asynchronous on `stream`; read the outcome with fkv_device_error.
  */
 FKV_API fkv_status fkv_selftest_wait(uint64_t limit_ns, int32_t complete, uint32_t *result, void *stream);

@@ -21,3 +21,18 @@ def test_threads_leave_together():
             vote = VOTE.search(code)
             assert vote and vote.start() < code.index("*dead"), (name, line)
     assert seen >= 8
+
+
+def test_every_wait_is_one_of_the_helpers_that_the_selftest_runs():
+    """A barrier is tested in helpers that give up by the clock, nowhere else, and fkv_selftest_wait runs each of them."""
+    helpers = set()
+    for name, text in SOURCES.items():
+        for body in re.sub(r"//.*", "", text).split("\n}\n"):          # a function each (or several declarations)
+            if not re.search(r"(?<!bool )\bmbar_try_wait(_sleep)?\(", body):
+                continue
+            head = re.findall(r"\n__device__ __forceinline__ bool (\w+)\(", body)
+            assert len(head) == 1 and "globaltimer_ns()" in body, (name, head)
+            helpers.add(head[0])
+    assert helpers == {"mbar_wait_bounded", "mbar_wait_bounded_sleep", "tree_wait"}
+    for h in helpers:
+        assert h + "(bar" in SOURCES["selftest.cu"], h
