@@ -116,6 +116,12 @@ __device__ __forceinline__ bool tile_whole(const TreeUnit &u, int i) { return i 
 // ---------------------------------------------------------------------------
 // which rows see a token
 // ---------------------------------------------------------------------------
+// Word w of a row's mask, without the bits of tokens that are not there (`n` are): they name
+// nothing, and count for no depth, so no row is deeper than unit_whole takes for the deepest.
+__device__ __forceinline__ uint64_t mask_word(const uint64_t *m, int w, int n) {
+    const int left = n - 64 * w;
+    return __ldg(m + w) & (left >= 64 ? ~0ull : left > 0 ? (1ull << left) - 1 : 0ull);
+}
 struct RowSight {
     uint64_t word;                             // the row's mask word of the token asked for
     int32_t lo;                                // its first committed token apart from the first ones
@@ -126,10 +132,10 @@ __device__ __forceinline__ RowSight row_sight(const TreeParams &p, const TreeUni
     int bits = 1;
     if (p.mask) {
         const uint64_t *m = p.mask + static_cast<int64_t>(tok) * p.words;
-        s.word = w < p.words ? __ldg(m + w) : 0ull;
+        s.word = w < p.words ? mask_word(m, w, u.len - u.ctx) : 0ull;
         if (p.window) {
             bits = 0;
-            for (int i = 0; i < p.words; ++i) bits += __popcll(__ldg(m + i));
+            for (int i = 0; i < p.words; ++i) bits += __popcll(mask_word(m, i, u.len - u.ctx));
         }
     }
     if (p.window) s.lo = static_cast<int32_t>(static_cast<int64_t>(u.ctx) + max(bits - 1, 0) - p.window + 1 > 0 ? static_cast<int64_t>(u.ctx) + max(bits - 1, 0) - p.window + 1 : 0);
@@ -158,7 +164,7 @@ __device__ __forceinline__ uint32_t seen_of(const TreeParams &p, const TreeUnit 
         bits = 0;
 #pragma unroll
         for (int i = 0; i < kTreeMaxWords; ++i) {
-            const uint64_t w = i < p.words ? __ldg(m + i) : 0ull;
+            const uint64_t w = i < p.words ? mask_word(m, i, u.len - u.ctx) : 0ull;
             bits += __popcll(w);
             if (at >= 64 * i && at < 64 * i + 64) lo = w;
             if (at + 63 >= 64 * i && at + 63 < 64 * i + 64) hi = w;

@@ -562,9 +562,9 @@ FKV_API fkv_status kv_append_rope(const void *q, int64_t q_token_stride, int32_t
  *   - committed token t if window is 0, or t < sinks, or t > p - window with p =
  *     c + max(0, bits set in its mask - 1), the position of its depth in the tree.
  * and out = softmax(sm_scale * q . k) v over what it sees, as in paged_decode_attn.
- * Bits of tokens that are not there are ignored.  A row that sees nothing is
- * zeros.  What a row does not see has no part in it, whatever it holds (NaN,
- * infinities; but infinite V that every row of a request sees may give NaN).  Query
+ * Bits of tokens that are not there (n and above) are ignored, in the count too.  A
+ * row that sees nothing is zeros.  What a row does not see has no part in it, whatever
+ * it holds (NaN, infinities; but infinite V that every row of a request sees may give NaN).  Query
  * elements down to 2^-32 of the largest among the rows of a KV head are exact over FP8
  * and FP4, BF16 ones always.  Any order of the drafted tokens is taken; positions (depths) of
  * siblings are the caller's, in kv_append_rope.

@@ -558,3 +558,24 @@ def test_wide_units_of_one_and_two_blocks_in_turn(kind, n):
     for _ in range(10):
         t["out"].fill_(float("nan"))
         assert torch.equal(c.tree(t).view(torch.int16), first.view(torch.int16))
+
+
+ROWS = [(4, 3), (4, 7), (8, 8), (16, 7), (16, 13)]                    # query heads a KV head, drafted tokens: 16, 32, 64, 128 and 256 rows a unit
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("G,n", ROWS)
+@pytest.mark.parametrize("words", [1, 4])
+def test_bits_of_tokens_that_are_not_there(kind, G, n, words):
+    """They change nothing, the depth by which a window is placed included."""
+    import torch
+    c = Case(kind, 2 * G, 2, 64, [1000, 3000, 700], [n, n - 1, n], seed=45, words=words)
+    own = c.sets
+    most = [k for k in (n, n - 1, n) for _ in range(k)]
+    every = [m | (((1 << 64 * words) - 1) >> k << k) for m, k in zip(own, most)]
+    for window, sinks in ((0, 0), (300, 0), (1000, 5), (129, 70), (650, 0)):
+        c.sets = every
+        out = c.tree(window=window, sinks=sinks)
+        c.sets = own
+        c.check(out, window, sinks)
+        assert torch.equal(out.view(torch.int16), c.tree(window=window, sinks=sinks).view(torch.int16))
