@@ -698,7 +698,7 @@ tree_attn_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmK, co
                     if (tok < kNC) {
                         const float z = fmaxf(fmaxf(red[0][tok], red[1][tok]), fmaxf(red[2][tok], red[3][tok])), was = -refs[tok];
                         move = z - was > kTreeMost;
-                        const float ref = move ? z - kTreeTop : was;
+                        const float ref = move ? tree_reference(z) : was;
                         refs[tok] = -ref;
                         ct.up[g][tok] = move ? ex2(was - ref) : 1.f;
                     }

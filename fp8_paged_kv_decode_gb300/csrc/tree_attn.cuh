@@ -14,6 +14,12 @@ namespace fkv {
 constexpr int kTreeMaxWords = 4;               // 64-bit words of a row's mask
 constexpr float kTreeTop = 10.f, kTreeMost = 15.9f;   // log2 of a moved reference's largest weight, and of any weight
 constexpr float kTreeNone = -3e38f;            // the reference of a row that has seen nothing
+// The reference that a largest logit of z asks for.  Past 2^27 fp32 neighbours are 16 and more apart, and z - 10 may round
+// to z - 16, whose weight of 2^16 f16 does not hold: there it is z itself.
+__device__ __forceinline__ float tree_reference(float z) {
+    const float r = __fsub_rn(z, kTreeTop);
+    return __fsub_rn(z, r) > kTreeMost ? z : r;
+}
 constexpr uint32_t kAll = 0xffffffffu;
 
 struct TreeParams {

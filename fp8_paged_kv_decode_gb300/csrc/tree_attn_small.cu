@@ -297,8 +297,8 @@ tree_small_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmK, c
                             x = fmaxf(x, __shfl_xor_sync(kAll, x, 1));
                             x = fmaxf(x, __shfl_xor_sync(kAll, x, 2));
                             if (x - ref[mb][hf] > kTreeMost) {
-                                const float f = ex2(ref[mb][hf] - (x - kTreeTop));
-                                ref[mb][hf] = x - kTreeTop;
+                                const float to = tree_reference(x), f = ex2(ref[mb][hf] - to);
+                                ref[mb][hf] = to;
                                 l[mb][hf] *= f;
 #pragma unroll
                                 for (int d = 0; d < 16; ++d) {

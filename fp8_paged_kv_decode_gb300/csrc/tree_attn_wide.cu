@@ -465,7 +465,7 @@ tree_wide_kernel(const TreeParams p, int rows, const __grid_constant__ CUtensorM
                     const bool move = top - ref > kTreeMost;
                     if (__builtin_expect(__any_sync(kAll, move), 0)) {
                         // the sums so far, and the weights of the tile's first half, are scaled to the new reference
-                        const float to = move ? top - kTreeTop : ref, f = move ? ex2(ref - to) : 1.f;
+                        const float to = move ? tree_reference(top) : ref, f = move ? ex2(ref - to) : 1.f;
                         if (i > tb + turns) {
                             wait(ct.odone[g], (n - 1) & 1);
                             umma_fence_after();

@@ -579,3 +579,42 @@ def test_bits_of_tokens_that_are_not_there(kind, G, n, words):
         c.sets = own
         c.check(out, window, sinks)
         assert torch.equal(out.view(torch.int16), c.tree(window=window, sinks=sinks).view(torch.int16))
+
+
+def one_dim_keys(c, value, rows):
+    """Keys of dim 0 alone: `value` (1, 0.5, -1 or -2; the K scales become 1) at these cache rows [page, offset]."""
+    code = {"fp8": {1: 0x38, 0.5: 0x30, -1: 0xB8, -2: 0xC0}, "bf16": {1: 0x3F80, 0.5: 0x3F00, -1: 0xBF80, -2: 0xC000}, "fp4": {1: 2, 0.5: 1, -1: 10, -2: 12}}
+    if c.ks is not None:
+        c.ks[:] = 1.0
+    for pg, off in rows:
+        c.kc[pg, :, off] = 0
+        c.kc[pg, :, off, 0] = code[c.kind][value]
+        if c.kind == "fp4":
+            c.kc[pg, :, off, 64] = 0x38
+
+
+def few_on_top(kind, G, n, sign):
+    """A few tokens share each row's largest logit, of either sign, and the others are far below it: the output is the mean of
+    those few.  Rows' logits are 1, 1.125 ... 1.5 times 1024 c.sm."""
+    c = Case(kind, 2 * G, 2, 64, [300, 500], [n, n], seed=46)
+    top, low = (1, 0.5) if sign > 0 else (-1, -2)
+    for r in range(2):
+        at = [(c.idx[c.ptr[r] + t // 64], t % 64) for t in range(int(c.lens[r]))]
+        one_dim_keys(c, low, at)
+        one_dim_keys(c, top, [at[t] for t in (3, 70, 71, 200, 290)])
+    q = np.zeros(c.q.shape, np.float32)
+    q[..., 0] = 1024 * (1 + np.arange(c.q.shape[0] * 2 * G).reshape(c.q.shape[:2]) % 5 / 8)
+    c.q = W.bf16_bits(q)
+    return c
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("G,n", ROWS)
+@pytest.mark.parametrize("sign", [1, -1])
+def test_logits_whose_references_round(kind, G, n, sign):
+    """Logits (in log2 units) up to 4e8, where fp32 neighbours are 8, 16 and 32 apart."""
+    c = few_on_top(kind, G, n, sign)
+    for z in (3e4, 3e6, 6e7, 1.4e8, 2e8, 2.6e8):
+        c.sm = z * np.log(2.0) / 1024
+        c.check(c.tree())
+        c.check(c.tree(window=260, sinks=4), 260, 4)
