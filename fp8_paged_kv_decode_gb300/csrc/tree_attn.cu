@@ -640,8 +640,8 @@ tree_attn_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmK, co
             wait(ct.cfull[d.i], d.ph);
             group_sync(barrier);
             const float cs = *const_cast<volatile float *>(&ct.colscale[d.i]);
-            const uint64_t cs2 = pack2(cs, cs);
             bool had = false;                                      // a tile of this unit
+            bool far = false;                                      // a reference so large that products are rounded first
             for (int i = u.tb + static_cast<int>((g ^ turn) & 1); i < u.te; i += 2) {
                 const bool whole = tile_whole(u, i);
                 uint64_t see = ~0ull;
@@ -655,15 +655,24 @@ tree_attn_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmK, co
                     constexpr bool kLess = decltype(less)::value;
 #pragma unroll
                     for (int c = 0; c < kNC; c += kLd) tmem_load(ts + c, *reinterpret_cast<float(*)[kLd]>(&x[c]));
+                    float cc = cs;
+                    if (__builtin_expect(kLess && far, 0)) {
+                        asm volatile("" ::: "memory");
+#pragma unroll
+                        for (int j = 0; j < kNC; ++j) x[j] = __fmul_rn(x[j], cs);
+                        cc = 1.f;
+                    }
+                    const uint64_t cc2 = pack2(cc, cc);
 #pragma unroll
                     for (int j = 0; j < kNC; j += 4) {
-                        uint64_t a = mul2(pack2(x[j], x[j + 1]), cs2), b = mul2(pack2(x[j + 2], x[j + 3]), cs2);
+                        uint64_t a, b;
                         if (kLess) {
-                            // rounded products, as the references': a fused one would leave their rounding, up to 2^9
-                            // at logits of 1e10, in the exponent
                             const float4 r4 = ld_shared_f4(sref + 4 * j);
-                            a = add2(a, pack2(r4.x, r4.y));
-                            b = add2(b, pack2(r4.z, r4.w));
+                            a = fma2(pack2(x[j], x[j + 1]), cc2, pack2(r4.x, r4.y));
+                            b = fma2(pack2(x[j + 2], x[j + 3]), cc2, pack2(r4.z, r4.w));
+                        } else {
+                            a = mul2(pack2(x[j], x[j + 1]), cc2);
+                            b = mul2(pack2(x[j + 2], x[j + 3]), cc2);
                         }
                         const float2 e = unpack2(a), f = unpack2(b);
                         x[j] = e.x, x[j + 1] = e.y, x[j + 2] = f.x, x[j + 3] = f.y;
@@ -675,7 +684,7 @@ tree_attn_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmK, co
                             if (!((see >> j) & 1)) x[j] = -INFINITY;
                     }
                 };
-                for (int tries = 0;; ++tries) {                    // (a second time only where logits are so large that a reference is rounded)
+                for (int tries = 0;; ++tries) {                    // (again after references have moved)
                     logits(std::true_type{});
                     float m4[4] = {x[0], x[1], x[2], x[3]};
 #pragma unroll
@@ -694,15 +703,17 @@ tree_attn_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmK, co
                         for (int j = 0; j < kHas; ++j) red[wq][(lane / kSame) * kHas + j] = x[j];
                     }
                     group_sync(barrier);
-                    bool move = false;
+                    bool move = false, off = false;
                     if (tok < kNC) {
                         const float z = fmaxf(fmaxf(red[0][tok], red[1][tok]), fmaxf(red[2][tok], red[3][tok])), was = -refs[tok];
                         move = z - was > kTreeMost;
                         const float ref = move ? tree_reference(z) : was;
                         refs[tok] = -ref;
                         ct.up[g][tok] = move ? ex2(was - ref) : 1.f;
+                        off = reference_far(ref);
                     }
                     const bool any = group_any(barrier, move);
+                    far = group_any(barrier, off);
                     const uint32_t sup = smem_u32(ct.up[g]);
                     if (any && had) {
 #pragma unroll

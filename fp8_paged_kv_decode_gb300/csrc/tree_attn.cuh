@@ -20,6 +20,10 @@ __device__ __forceinline__ float tree_reference(float z) {
     const float r = __fsub_rn(z, kTreeTop);
     return __fsub_rn(z, r) > kTreeMost ? z : r;
 }
+// Whether an exponent c s - ref needs c s rounded first, as the reference's logit was.  One fused operation leaves
+// that rounding in the exponent, up to half an fp32 step of the logit: 1/16 below 2^20, 2^9 at 1e10, where weights would
+// overflow or vanish.  (The compiler fuses the packed mul.rn and add.rn of PTX too; __fmul_rn and __fadd_rn stay apart.)
+__device__ __forceinline__ bool reference_far(float ref) { return fabsf(ref) >= 0x1p20f && ref > kTreeNone; }
 constexpr uint32_t kAll = 0xffffffffu;
 
 struct TreeParams {
@@ -189,6 +193,12 @@ __device__ __forceinline__ uint32_t seen_of(const TreeParams &p, const TreeUnit 
 // ---------------------------------------------------------------------------
 // values
 // ---------------------------------------------------------------------------
+// Two fp32 operations an instruction.
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+    return d;
+}
 __device__ __forceinline__ void st_shared_v4(uint32_t addr, uint4 v) {
     asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
 }

@@ -433,6 +433,7 @@ tree_wide_kernel(const TreeParams p, int rows, const __grid_constant__ CUtensorM
             const int row = turns ? gtid : 128 * g + gtid, rtok = row / p.group, rhead = row - rtok * p.group;
             const int tok = rtok < u.ntok ? u.tok0 + rtok : -1;    // the row's token (of the call)
             float ref = kTreeNone, l = 0.f;
+            bool far = false;                                      // of any of the warp's rows: products are rounded first
             int odd_tiles = 0;
             c = c_next;
 #pragma unroll 1
@@ -461,8 +462,8 @@ tree_wide_kernel(const TreeParams p, int rows, const __grid_constant__ CUtensorM
                     float top = -INFINITY;
 #pragma unroll
                     for (int j = 0; j < 64; j += 2) top = fmaxf(top, fmaxf(s[j], s[j + 1]));
-                    top *= c;
-                    const bool move = top - ref > kTreeMost;
+                    top = __fmul_rn(top, c);
+                    const bool move = __fsub_rn(top, ref) > kTreeMost;
                     if (__builtin_expect(__any_sync(kAll, move), 0)) {
                         // the sums so far, and the weights of the tile's first half, are scaled to the new reference
                         const float to = move ? tree_reference(top) : ref, f = move ? ex2(ref - to) : 1.f;
@@ -511,8 +512,16 @@ tree_wide_kernel(const TreeParams p, int rows, const __grid_constant__ CUtensorM
                         l *= f;
                         sum[0].x *= f, sum[0].y *= f, sum[1].x *= f, sum[1].y *= f;
                         ref = to;
+                        far = __any_sync(kAll, reference_far(ref));
                     }
-                    const float2 c2 = make_float2(c, c), r2 = make_float2(-ref, -ref);
+                    float cc = c;
+                    if (__builtin_expect(far, 0)) {
+                        asm volatile("" ::: "memory");
+#pragma unroll
+                        for (int j = 0; j < 64; ++j) s[j] = __fmul_rn(s[j], c);
+                        cc = 1.f;
+                    }
+                    const float2 c2 = make_float2(cc, cc), r2 = make_float2(-ref, -ref);
                     uint32_t hi[32], lo[C::kConv ? 1 : 32];
 #pragma unroll
                     for (int j = 0; j < 32; ++j) {

@@ -618,3 +618,16 @@ def test_logits_whose_references_round(kind, G, n, sign):
         c.sm = z * np.log(2.0) / 1024
         c.check(c.tree())
         c.check(c.tree(window=260, sinks=4), 260, 4)
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("G,n", ROWS)
+@pytest.mark.parametrize("sign", [1, -1])
+def test_huge_logits(kind, G, n, sign):
+    """Logits (in log2 units) of 1e9 and more, where a product that is not rounded as the reference was leaves tens to
+    thousands of log2 units in the exponent."""
+    c = few_on_top(kind, G, n, sign)
+    for z in (1e9, 1e10, 3e12, 1e30):
+        c.sm = z * np.log(2.0) / 1024
+        c.check(c.tree())
+        c.check(c.tree(window=260, sinks=4), 260, 4)
