@@ -408,10 +408,12 @@ tree_wide_kernel(const TreeParams p, int rows, const __grid_constant__ CUtensorM
                         int e = static_cast<int>(big >> 7);
                         if (e == 0 || e == 255) e = 141;           // zeros, infinities and NaN stay what they are
                         e = max(e, 15);
-                        // (the scale's sign goes to Q, and a scale of zero is next to nothing: -infinity times it is itself)
+                        // (the scale's sign goes to Q, and a factor of zero, or one that underflows, is next to nothing: |S| is
+                        // below 2^36, so its logits are zero all the same, and -infinity times it is itself)
                         const float up = copysignf(__uint_as_float(static_cast<uint32_t>(268 - e) << 23), ks);
                         const float down = __shfl_sync(kAll, __uint_as_float(static_cast<uint32_t>(e - 14) << 23), 16 * (lane & 1));
-                        if (lane >> 1 == r8 + i) c_next = p.scale_log2 * (ks == 0.f ? 1e-30f : fabsf(ks)) * down;
+                        const float cr = p.scale_log2 * fabsf(ks) * down;
+                        if (lane >> 1 == r8 + i) c_next = cr < 0x1p-126f ? 0x1p-126f : cr;     // (NaN stays)
 #pragma unroll
                         for (int j = 0; j < 4; ++j) w[j] = pack_f16x2(__uint_as_float(w[j] << 16) * up, __uint_as_float(w[j] & 0xFFFF0000u) * up);
                         x[i] = make_uint4(w[0], w[1], w[2], w[3]);

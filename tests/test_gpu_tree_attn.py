@@ -631,3 +631,22 @@ def test_huge_logits(kind, G, n, sign):
         c.sm = z * np.log(2.0) / 1024
         c.check(c.tree())
         c.check(c.tree(window=260, sinks=4), 260, 4)
+
+
+@pytest.mark.parametrize("kind", ["fp8", "fp4"])
+@pytest.mark.parametrize("G,n", ROWS)
+@pytest.mark.parametrize("size", [1e-12, 1e-30, 1e-37])
+def test_a_head_scale_of_zero_and_tiny_queries(kind, G, n, size):
+    c = Case(kind, 2 * G, 2, 16, [70, 300], [n, n - 1], seed=47, q_std=size)
+    c.ks[0] = 0.0
+    c.check(c.tree())
+    c.check(c.tree(window=60, sinks=2), 60, 2)
+
+
+@pytest.mark.parametrize("kind", ["fp8", "fp4"])
+@pytest.mark.parametrize("G,n", ROWS)
+def test_a_head_scale_that_is_no_number(kind, G, n):
+    c = Case(kind, 2 * G, 2, 16, [70, 300], [n, n - 1], seed=53)
+    c.ks[0] = np.nan
+    got = bf16_out(c.tree())
+    assert np.isnan(got[:, :G]).all() and np.isfinite(got[:, G:]).all()
