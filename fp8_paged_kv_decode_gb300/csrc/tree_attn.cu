@@ -503,8 +503,7 @@ tree_attn_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmK, co
             };
             float up = 1.f, cs = p.scale_log2;
             if (C::kConv) {
-                // f16 with a power of two that puts the unit's largest finite element into [2^14, 2^15): elements
-                // down to 2^-32 of it stay exact
+                // by the unit's largest finite element: those down to 2^-32 of it stay exact
                 uint32_t big = 0;
 #pragma unroll 1
                 for (int r8 = 0; r8 < kR / 8; r8 += kU) {
@@ -522,10 +521,9 @@ tree_attn_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmK, co
                 big = __reduce_max_sync(kAll, big);
                 if (lane == 0) atomicMax(&ct.qmax[d.i], big);
                 group_sync(4);
-                int e = static_cast<int>(*const_cast<volatile uint32_t *>(&ct.qmax[d.i]) >> 7);
-                e = max(e == 0 ? 141 : e, 15);
-                up = __uint_as_float(static_cast<uint32_t>(268 - e) << 23);
-                cs = cs * __ldg(p.k_scale + u.h) * __uint_as_float(static_cast<uint32_t>(e - 14) << 23);
+                const QueryPower qp = query_power(*const_cast<volatile uint32_t *>(&ct.qmax[d.i]));
+                up = qp.up;
+                cs = cs * __ldg(p.k_scale + u.h) * qp.down;
             }
 #pragma unroll 1
             for (int r8 = 0; r8 < kR / 8; r8 += kU) {

@@ -193,6 +193,18 @@ __device__ __forceinline__ uint32_t seen_of(const TreeParams &p, const TreeUnit 
 // ---------------------------------------------------------------------------
 // values
 // ---------------------------------------------------------------------------
+// Queries become f16 with a power of two that puts the largest of them into [2^15, 2^16): BF16's 8 bits end at 65280 there,
+// below f16's 65504, and 2^-32 of the largest keeps its last bit at 2^-24, f16's lowest.
+struct QueryPower {
+    float up, down;                            // 2^k and 2^-k
+};
+// For a largest element with these bits (BF16, no sign).  Zeros, infinities and NaN stay what they are.
+__device__ __forceinline__ QueryPower query_power(uint32_t big) {
+    int e = static_cast<int>(big >> 7);
+    if (e == 0 || e == 255) e = 142;
+    e = max(e, 16);
+    return {__uint_as_float(static_cast<uint32_t>(269 - e) << 23), __uint_as_float(static_cast<uint32_t>(e - 15) << 23)};
+}
 // Two fp32 operations an instruction.
 __device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
     uint64_t d;

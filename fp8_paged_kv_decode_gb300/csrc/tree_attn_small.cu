@@ -166,7 +166,7 @@ tree_small_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmK, c
             const int ahead = min(u.te - u.tb, C::kStages);
             for (int k = 0; k < ahead; ++k) issue(u.tb + k, (stage + k) % C::kStages);
 
-            // ---- Q: f16 with a power of two per row that puts its largest element into [2^14, 2^15) ----
+            // ---- Q: f16 with a power of two per row ----
             uint32_t qa[kMB == 1 ? 8 : 1][4];
             float cs[kMB][2];                                      // a logit in log2 units per unit of S
             int tk[kMB][2];                                        // the rows' tokens (of the call)
@@ -192,11 +192,9 @@ tree_small_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmK, c
                     for (int j = 0; j < 16; ++j) big = max(big, max(w[j] & 0x7FFFu, (w[j] >> 16) & 0x7FFFu));
                     big = max(big, __shfl_xor_sync(kAll, big, 1));
                     big = max(big, __shfl_xor_sync(kAll, big, 2));
-                    int e = static_cast<int>(big >> 7);
-                    if (e == 0 || e == 255) e = 141;               // zeros, infinities and NaN stay what they are
-                    e = max(e, 15);
-                    const float up = __uint_as_float(static_cast<uint32_t>(268 - e) << 23);
-                    cs[mb][hf] = p.scale_log2 * ks * __uint_as_float(static_cast<uint32_t>(e - 14) << 23);
+                    const QueryPower qp = query_power(big);
+                    const float up = qp.up;
+                    cs[mb][hf] = p.scale_log2 * ks * qp.down;
 #pragma unroll
                     for (int j = 0; j < 16; ++j) f[hf][j] = pack_f16x2(__uint_as_float(w[j] << 16) * up, __uint_as_float(w[j] & 0xFFFF0000u) * up);
                 }

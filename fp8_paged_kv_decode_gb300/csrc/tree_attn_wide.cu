@@ -380,8 +380,7 @@ tree_wide_kernel(const TreeParams p, int rows, const __grid_constant__ CUtensorM
         Turn v{1};
         uint32_t n = 0, n_other = 0, n_turns = 0;                  // tiles of this group and the other, units in turns so far
         auto load_q = [&](const TreeUnit &u) {
-            // the warp's own rows, two at a time; f16 with a power of two that puts a row's largest element into
-            // [2^14, 2^15) (BF16: as it is)
+            // the warp's own rows, two at a time; f16 with a power of two per row (BF16: as it is)
             const bool alone = u.ntok * p.group <= 128;            // one block, which group 0 loads
             const int c16 = lane & 15, row0 = (alone ? 0 : 128 * g) + 32 * (warp & 3) + (lane >> 4);
             const float ks = C::kConv ? __ldg(p.k_scale + u.h) : 1.f;
@@ -405,13 +404,11 @@ tree_wide_kernel(const TreeParams p, int rows, const __grid_constant__ CUtensorM
                         for (int j = 0; j < 4; ++j) big = max(big, max(w[j] & 0x7FFFu, (w[j] >> 16) & 0x7FFFu));
 #pragma unroll
                         for (int o = 1; o < 16; o <<= 1) big = max(big, __shfl_xor_sync(kAll, big, o));
-                        int e = static_cast<int>(big >> 7);
-                        if (e == 0 || e == 255) e = 141;           // zeros, infinities and NaN stay what they are
-                        e = max(e, 15);
+                        const QueryPower qp = query_power(big);
                         // (the scale's sign goes to Q, and a factor of zero, or one that underflows, is next to nothing: |S| is
                         // below 2^36, so its logits are zero all the same, and -infinity times it is itself)
-                        const float up = copysignf(__uint_as_float(static_cast<uint32_t>(268 - e) << 23), ks);
-                        const float down = __shfl_sync(kAll, __uint_as_float(static_cast<uint32_t>(e - 14) << 23), 16 * (lane & 1));
+                        const float up = copysignf(qp.up, ks);
+                        const float down = __shfl_sync(kAll, qp.down, 16 * (lane & 1));
                         const float cr = p.scale_log2 * fabsf(ks) * down;
                         if (lane >> 1 == r8 + i) c_next = cr < 0x1p-126f ? 0x1p-126f : cr;     // (NaN stays)
 #pragma unroll

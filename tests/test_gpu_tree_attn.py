@@ -650,3 +650,23 @@ def test_a_head_scale_that_is_no_number(kind, G, n):
     c.ks[0] = np.nan
     got = bf16_out(c.tree())
     assert np.isnan(got[:, :G]).all() and np.isfinite(got[:, G:]).all()
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("G,n", ROWS)
+def test_query_elements_far_below_the_largest(kind, G, n):
+    """2^-32 of the largest of a KV head's rows counts, to its last bit: a logit of 8 + 1/16 against 3000 of zero."""
+    c = Case(kind, 2 * G, 2, 64, [3000], [n], seed=48)
+    q = np.zeros(c.q.shape, np.float32)
+    q[::2, :, 0] = 1.0                                                # the other rows have only the small element
+    q[..., 1] = 2.0 ** -32 * (1 + 2.0 ** -7)
+    c.q, c.sm = W.bf16_bits(q), 2.0 ** 32
+    c.kc[...] = 0
+    if c.ks is not None:
+        c.ks[:] = 1.0
+    pg, off = c.idx[1234 // 64], 1234 % 64
+    if kind == "fp4":
+        c.kc[pg, :, off, 0], c.kc[pg, :, off, 64] = 0x60, 0x40        # 4 times 2
+    else:
+        c.kc[pg, :, off, 1] = 0x50 if kind == "fp8" else 0x4100
+    c.check(c.tree())
