@@ -132,13 +132,13 @@ __device__ __forceinline__ uint32_t ld_shared_u16(uint32_t addr) {
     return v;
 }
 
-// Bits of this group's columns whose rows see token t (rows past the unit's: unset).
+// Bits of this group's columns whose rows see token t of a tile up to `end` (rows past the unit's: unset).
 template <int kNC>
-__device__ __forceinline__ uint64_t seen_by(const TreeParams &p, const TreeUnit &u, int col0, uint32_t t) {
+__device__ __forceinline__ uint64_t seen_by(const TreeParams &p, const TreeUnit &u, int col0, uint32_t t, uint32_t end) {
     uint64_t v = 0;
     const int w = word_of(u, t), G = p.group;
     for (int i = col0 / G; i < u.ntok && i * G < col0 + kNC; ++i) {
-        if (sees(p, u, row_sight(p, u, u.tok0 + i, w), t)) {
+        if (sees(p, u, row_sight(p, u, u.tok0 + i, w), t, end)) {
             const int a = max(i * G, col0) - col0, b = min((i + 1) * G, col0 + kNC) - col0;
             v |= (b - a == 64 ? ~0ull : (1ull << (b - a)) - 1) << a;
         }
@@ -643,7 +643,7 @@ tree_attn_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmK, co
             for (int i = u.tb + static_cast<int>((g ^ turn) & 1); i < u.te; i += 2) {
                 const bool whole = tile_whole(u, i);
                 uint64_t see = ~0ull;
-                if (__builtin_expect(!whole, 0)) see = seen_by<kNC>(p, u, 0, tile_at<kTreeTok>(u, i) + tok);
+                if (__builtin_expect(!whole, 0)) see = seen_by<kNC>(p, u, 0, tile_at<kTreeTok>(u, i) + tok, tile_end(u, i));
                 wait(ct.sfull[g], ph);
                 umma_fence_after();
                 const uint32_t ts = tmem + tlane + C::kTmS + g * kR;
@@ -848,7 +848,7 @@ tree_attn_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmK, co
                         for (int b = 0; b < kTreeTok; ++b) {
                             if (!((*const_cast<volatile uint32_t *>(&ct.poison[d.i][min(k, kTreePoison - 1)][b >> 5]) >> (b & 31)) & 1)) continue;
                             const float add = odd_value<kKv>(p, u, t0 + b, dim);
-                            const uint64_t see = seen_by<8>(p, u, c0 + c, t0 + b);
+                            const uint64_t see = seen_by<8>(p, u, c0 + c, t0 + b, tile_end(u, i));
 #pragma unroll
                             for (int j = 0; j < 8; ++j)
                                 if ((see >> j) & 1) y[j] += add;

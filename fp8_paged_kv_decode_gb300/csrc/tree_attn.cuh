@@ -74,8 +74,9 @@ __device__ __forceinline__ TreeRequest tree_request(const TreeParams &p, int r) 
     return q;
 }
 
-// The tiles of a live request: those over the first tokens, if they lie apart, then those
-// from `start` on, the page of the first token that a row at depth 0 sees.
+// The tiles of a live request: those over the first tokens, if there are pages between (which
+// are not read: they may be given back, their entries stale), then those from `start` on, the
+// page of the first token that a row at depth 0 sees.
 struct TreeSpan {
     int32_t start, sink_tiles, head, tiles;
 };
@@ -88,7 +89,7 @@ __device__ __forceinline__ TreeSpan tree_span(const TreeParams &p, const TreeReq
         s.start = lo - lo % p.page_size;
         s.head = min(p.sinks, lo);
         s.sink_tiles = s.head / kTok + (s.head % kTok != 0);
-        if (s.start <= static_cast<int64_t>(s.sink_tiles) * kTok) s = TreeSpan{0, 0, 0, 0};
+        if (s.start < static_cast<int64_t>(s.head) + p.page_size) s = TreeSpan{0, 0, 0, 0};    // (start begins a page)
     }
     s.tiles = s.sink_tiles + (q.len - s.start - 1) / kTok + 1;
     return s;
@@ -151,16 +152,17 @@ __device__ __forceinline__ RowSight row_sight(const TreeParams &p, const TreeUni
     if (p.window) s.lo = static_cast<int32_t>(static_cast<int64_t>(u.ctx) + max(bits - 1, 0) - p.window + 1 > 0 ? static_cast<int64_t>(u.ctx) + max(bits - 1, 0) - p.window + 1 : 0);
     return s;
 }
-__device__ __forceinline__ bool sees(const TreeParams &p, const TreeUnit &u, const RowSight &s, uint32_t t) {
-    if (t >= static_cast<uint32_t>(u.len)) return false;
+// (end: of the tile's tokens; those over the first ones may reach into the others' places)
+__device__ __forceinline__ bool sees(const TreeParams &p, const TreeUnit &u, const RowSight &s, uint32_t t, uint32_t end) {
+    if (t >= end) return false;
     if (t >= static_cast<uint32_t>(u.ctx)) return (s.word >> ((t - u.ctx) & 63)) & 1;
     return !p.window || t < static_cast<uint32_t>(p.sinks) || t >= static_cast<uint32_t>(s.lo);
 }
 __device__ __forceinline__ int word_of(const TreeUnit &u, uint32_t t) {
     return t >= static_cast<uint32_t>(u.ctx) ? static_cast<int>((t - u.ctx) >> 6) : 0;
 }
-// Which of the 32 tokens from t0 on row `tok` (of the call; -1: none) sees.
-__device__ __forceinline__ uint32_t seen_of(const TreeParams &p, const TreeUnit &u, int tok, uint32_t t0) {
+// Which of the 32 tokens from t0 on row `tok` (of the call; -1: none) sees, of a tile's up to `end`.
+__device__ __forceinline__ uint32_t seen_of(const TreeParams &p, const TreeUnit &u, int tok, uint32_t t0, uint32_t end) {
     if (tok < 0) return 0u;
     auto below = [t0](int64_t x) {                                 // tokens before x
         const int64_t d = x - t0;
@@ -187,7 +189,7 @@ __device__ __forceinline__ uint32_t seen_of(const TreeParams &p, const TreeUnit 
     const uint32_t drafted = static_cast<uint32_t>((lo >> sh) | (sh ? hi << (64 - sh) : 0ull));
     uint32_t old = below(u.ctx);
     if (p.window) old &= below(p.sinks) | ~below(static_cast<int64_t>(u.ctx) + max(bits - 1, 0) - p.window + 1);
-    return (old | (drafted & ~below(u.ctx))) & below(u.len);
+    return (old | (drafted & ~below(u.ctx))) & below(end);
 }
 
 // ---------------------------------------------------------------------------

@@ -27,7 +27,7 @@
 
 namespace fkv {
 
-constexpr int kSmallPoison = 24;               // tiles of a unit that hold tokens not seen by every row, at most (23)
+constexpr int kSmallPoison = 26;               // tiles of a unit that hold tokens not seen by every row, at most
 
 template <int kKv, int kMB>                    // kMB: blocks of 16 rows
 struct SmallCfg {
@@ -258,7 +258,7 @@ tree_small_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmK, c
                     if (lane == 0) ct.poison[warp][min(odd_tiles, kSmallPoison - 1)] = m32;
                     odd |= m32 != 0;
                     ++odd_tiles;
-                    const uint32_t mine = seen_of(p, u, lane < C::kRows && lane / p.group < u.ntok ? u.tok0 + lane / p.group : -1, t0);
+                    const uint32_t mine = seen_of(p, u, lane < C::kRows && lane / p.group < u.ntok ? u.tok0 + lane / p.group : -1, t0, tile_end(u, i));
 #pragma unroll
                     for (int mb = 0; mb < kMB; ++mb)
 #pragma unroll
@@ -417,7 +417,7 @@ tree_small_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmK, c
 #pragma unroll 1
                     for (int j = 0; j < 32 * 2 * kMB; ++j) {
                         const int b = j & 31, hf = (j >> 5) & 1, mb = j >> 6, tok = mb ? (hf ? tk[kMB - 1][1] : tk[kMB - 1][0]) : hf ? tk[0][1] : tk[0][0];
-                        if (!((m32 >> b) & 1) || tok < 0 || !sees(p, u, row_sight(p, u, tok, word_of(u, t0 + b)), t0 + b)) continue;
+                        if (!((m32 >> b) & 1) || tok < 0 || !sees(p, u, row_sight(p, u, tok, word_of(u, t0 + b)), t0 + b, tile_end(u, i))) continue;
                         const int row = 16 * mb + g + 8 * hf;
 #pragma unroll 1
                         for (int d = 32 * t; d < 32 * t + 32; ++d) {

@@ -453,7 +453,8 @@ tree_wide_kernel(const TreeParams p, int rows, const __grid_constant__ CUtensorM
                     tmem_load(tS + at, s);
                     if (__builtin_expect(!whole, 0)) {
                         const uint32_t t0 = tile_at<kTreeTok>(u, i) + at;
-                        const uint64_t see = seen_of(p, u, tok, t0) | static_cast<uint64_t>(seen_of(p, u, tok, t0 + 32)) << 32;
+                        const uint32_t end = tile_end(u, i);
+                        const uint64_t see = seen_of(p, u, tok, t0, end) | static_cast<uint64_t>(seen_of(p, u, tok, t0 + 32, end)) << 32;
 #pragma unroll
                         for (int j = 0; j < 64; ++j)
                             if (!((see >> j) & 1)) s[j] = -INFINITY;   // (c is above zero)
@@ -634,7 +635,7 @@ tree_wide_kernel(const TreeParams p, int rows, const __grid_constant__ CUtensorM
 #pragma unroll 1
                         for (int b = 0; b < kTreeTok; ++b) {
                             if (!((*const_cast<volatile uint32_t *>(&ct.poison[d.i][min(k, kTreePoison - 1)][b >> 5]) >> (b & 31)) & 1)) continue;
-                            if (!sees(p, u, row_sight(p, u, tok, word_of(u, t0 + b)), t0 + b)) continue;
+                            if (!sees(p, u, row_sight(p, u, tok, word_of(u, t0 + b)), t0 + b, tile_end(u, i))) continue;
 #pragma unroll 1
                             for (int dim = d0; dim < d1; ++dim) {
                                 const float add = odd_value<kKv>(p, u, t0 + b, dim);

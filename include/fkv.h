@@ -607,9 +607,9 @@ FKV_API fkv_status paged_tree_attn(const void *q, int32_t n_tokens, int32_t num_
  * tokens: paged_decode_attn's arguments and results, over the tokens
  *     t < sinks  or  t >= seq_lens[r] - window
  * of request r, whose query is its last token.  window >= 1, sinks >= 0.  Pages
- * whose tokens are all outside are not read and may hold any id.  The workspace
- * is paged_tree_attn_workspace_size(batch, batch, ...) bytes; limits, failing
- * closed and determinism are paged_tree_attn's.
+ * whose tokens are all outside are not read and their entries may hold any id (of
+ * pages given back, say).  The workspace is paged_tree_attn_workspace_size(batch,
+ * batch, ...) bytes; limits, failing closed and determinism are paged_tree_attn's.
  */
 FKV_API fkv_status paged_window_attn(const void *q, int32_t batch, int32_t num_q_heads,
                                      const void *k_cache, const void *v_cache, int32_t kv_dtype,

@@ -670,3 +670,27 @@ def test_query_elements_far_below_the_largest(kind, G, n):
     else:
         c.kc[pg, :, off, 1] = 0x50 if kind == "fp8" else 0x4100
     c.check(c.tree())
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("S", [16, 32, 64])
+@pytest.mark.parametrize("window,sinks", [(60, 5), (60, 0), (33, 17), (100, 40), (100, 130)])
+@pytest.mark.parametrize("tree", [False, True])
+def test_pages_between_the_first_tokens_and_the_window(kind, S, window, sinks, tree):
+    """They are not read and may hold any id, however near the two are."""
+    import fp8_paged_kv_decode_gb300 as fkv
+    fkv.device_error()
+    lens = np.arange(30, 420, 11)
+    k = 3 if tree else 1
+    c = Case(kind, 8, 2, S, lens - k, np.full(len(lens), k), seed=49, sets=None if tree else [1] * len(lens))
+    gone = 0
+    for r, length in enumerate(lens):
+        first = max(0, length - k - window + 1)                       # of the committed tokens of a row at depth 0
+        for j in range(c.ptr[r], c.ptr[r + 1]):
+            a = (j - c.ptr[r]) * S
+            if a >= min(sinks, first) and a + S <= first:
+                c.idx[j] = (-1, c.P, 2 ** 31 - 1)[j % 3]
+                gone += 1
+    assert gone or sinks == 130
+    c.check((c.tree if tree else c.window)(window=window, sinks=sinks), window, sinks)
+    assert fkv.device_error() == 0
