@@ -341,12 +341,18 @@ kv_append_rope_kernel(const AppendRopeParams p) {
 #pragma unroll
         for (int i = 0; i < kArUnroll; ++i) {
             const int row = row0 + 2 * i + hw;
-            float x[8];
-            unpack_bf16x8(u[i], x);
+            const uint4 mine = u[i];
             if (row + kArBatch < last)
                 u[i] = reinterpret_cast<const uint4 *>(vrow + static_cast<int64_t>(row + kArBatch) * 128)[lane];
             const int h = min(row, p.heads - 1) - v0;
-            store_cached<kKv>(row < last ? cached(p.v_cache, h) : nullptr, lane, half_mask, x, head_scale<kKv>(p.v_scale, h));
+            uint8_t *const dst = row < last ? cached(p.v_cache, h) : nullptr;
+            if constexpr (kKv == FKV_KV_BF16) {                    // as they are: a conversion would change a NaN's bits
+                if (dst) __stcs(reinterpret_cast<uint4 *>(dst) + lane, mine);
+            } else {
+                float x[8];
+                unpack_bf16x8(mine, x);
+                store_cached<kKv>(dst, lane, half_mask, x, head_scale<kKv>(p.v_scale, h));
+            }
         }
     }
 }

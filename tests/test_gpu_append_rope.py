@@ -292,3 +292,16 @@ def test_python_refusals():
             fkv.kv_append_rope(**c.args(**bad))
     e = lambda *s: z(0, *s)                                                      # noqa: E731
     fkv.kv_append_rope(**c.args(q=e(4, D), k=e(2, D), v=e(2, D), q_out=e(4, D), positions=z(0, dt=torch.int32), slot_mapping=z(0, dt=torch.int64)))
+
+
+def test_bf16_values_are_copied_bit_by_bit():
+    """Every BF16 value, NaN with their payloads and signs among them, as kv_append_bf16 puts it."""
+    import torch
+    import fp8_paged_kv_decode_gb300 as fkv
+    c = Case("bf16", 128, 2, 4, 128, 1, False, False, 100, 16, seed=11, fused=False)
+    v = np.random.default_rng(12).permutation(1 << 16).astype(np.uint16).reshape(128, 4, D)
+    vt = dev(v, dtype=torch.bfloat16)
+    kc, vc = c.kc.clone(), c.vc.clone()
+    fkv.kv_append_bf16(c.kt, vt, dev(c.slots), kc, vc)
+    fkv.kv_append_rope(**c.args(v=vt))
+    assert np.array_equal(c.rows(c.vc, c.slots), v.view(np.uint8).reshape(128, 4, 256)) and np.array_equal(raw(c.vc), raw(vc))
