@@ -216,7 +216,8 @@ extern "C" fkv_status kv_tree_commit(void *k_cache, void *v_cache, int32_t kv_dt
         if (!k_cache || !v_cache || !page_indptr || !seq_lens || !token_indptr || !accepted_counts || !lens_out)
             return FKV_ERR_INVALID_ARG;
         if ((nnz > 0 && !page_indices) || (max_accepted > 0 && !accepted)) return FKV_ERR_INVALID_ARG;
-        if (lens_out == seq_lens) return FKV_ERR_INVALID_ARG;          // read while it is written
+        // read by a request's other warps while one of them writes its kept length
+        if (lens_out == seq_lens || lens_out == accepted_counts || lens_out == accepted) return FKV_ERR_INVALID_ARG;
         if (!aligned16(k_cache) || !aligned16(v_cache)) return FKV_ERR_INVALID_ARG;
     }
     uint32_t *err = device_error_word();

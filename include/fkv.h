@@ -629,7 +629,7 @@ FKV_API fkv_status paged_window_attn(const void *q, int32_t batch, int32_t num_q
  *   - for i = 0, 1, ...: the K and V rows of position c + accepted[r][i] go to
  *     position c + i (all KV heads);
  *   - lens_out[r] = c + accepted_counts[r], the length kept for the next step;
- *   - with free_pages: the request's pages past ceil(lens_out[r] / page_size) go
+ *   - with free_pages: the pages of its tokens past ceil(lens_out[r] / page_size) go
  *     back onto the free list, their live tags bumped by one if page_tags is given
  *     (holders of the old tag fail the check).  They are pushed so that the next
  *     kv_step_tables takes them in the order in which this step did: request 0's
@@ -642,8 +642,9 @@ FKV_API fkv_status paged_window_attn(const void *q, int32_t batch, int32_t num_q
  *
  *   k_cache, v_cache  pools of dtype kv_dtype; bytes of other rows are not touched
  *   accepted       int32 [batch][max_accepted]; accepted_counts int32 [batch]
- *   lens_out       int32 [batch], not seq_lens itself (kv_step_tables' cached_lens_out
- *                  fits: it is already the length kept for requests left as they are)
+ *   lens_out       int32 [batch], not seq_lens, accepted or accepted_counts themselves
+ *                  (kv_step_tables' cached_lens_out fits: it is already the length kept
+ *                  for requests left as they are)
  *   free_pages     int32 [num_free], free_count int32 [1] (the entries in use), free_left
  *                  int32 [1] (in use afterwards; may be free_count), page_tags uint32
  *                  [num_pages] or NULL; or all NULL and num_free 0: no page goes back.

@@ -131,3 +131,9 @@ def test_commit_refusals(lib):
 def test_launch_counts(lib):
     assert fkv.kernels_per_call("kv_append_rope") == 1 and fkv.kernels_per_call("kv_tree_commit") == 1
     assert fkv.kernels_per_call("paged_tree_attn") == fkv.kernels_per_call("paged_window_attn") > 0
+
+
+def test_commit_refuses_lengths_over_what_it_reads(lib):
+    """Other warps still read a request's count, list and length when one of them writes its kept length."""
+    for name in ("lens", "counts", "acc"):
+        assert commit(lib, batch=2, **{name: 7 * A, "out": 7 * A}) == 1, name
