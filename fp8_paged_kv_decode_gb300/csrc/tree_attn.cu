@@ -1201,7 +1201,7 @@ extern "C" size_t paged_tree_attn_workspace_size(int32_t n_tokens, int32_t batch
     if (head_dim != 128 || !known_kv(kv_dtype) || num_q_heads / num_kv_heads > 128) return 0;
     const int sms = device_sm_count();
     // of any call of up to n_tokens tokens, however many requests they are of: fewer rows can mean more shares
-    const int group = num_q_heads / num_kv_heads, most = rows_of(n_tokens, 1, group);
+    const int group = num_q_heads / num_kv_heads, most = rows_of(std::max(n_tokens, 1), 1, group);
     size_t need = 0;
     for (int rows = rows_of(1, 1, group); rows <= most && sms > 0; rows *= 2)
         need = std::max(need, tree_ws(sms, kv_dtype, rows).total);

@@ -694,3 +694,19 @@ def test_pages_between_the_first_tokens_and_the_window(kind, S, window, sinks, t
     assert gone or sinks == 130
     c.check((c.tree if tree else c.window)(window=window, sinks=sinks), window, sinks)
     assert fkv.device_error() == 0
+
+
+@pytest.mark.parametrize("Hq,H", [(8, 2), (64, 2), (128, 1)])
+def test_no_tokens(Hq, H):
+    """A workspace for no tokens, and the calls that it is for."""
+    import torch
+    import fp8_paged_kv_decode_gb300 as fkv
+    c = Case("fp8", Hq, H, 16, [40, 5], [1, 1], seed=50, sets=[1, 1])
+    t = c.tensors()
+    ws = fkv.alloc_tree_workspace(0, 0, Hq, H)
+    assert ws.numel() <= fkv.alloc_tree_workspace(1, 1, Hq, H).numel()
+    none = dict(t, q=t["q"][:0], out=t["out"][:0], workspace=ws)
+    fkv.paged_tree_attn(**none, token_indptr=torch.zeros(3, dtype=torch.int32, device="cuda"), tree_mask=torch.zeros(0, dtype=torch.int64, device="cuda"))
+    none.update(page_indptr=t["page_indptr"][:1], seq_lens=t["seq_lens"][:0])
+    fkv.paged_window_attn(**none, window=5)
+    assert fkv.device_error() == 0
