@@ -554,7 +554,7 @@ def paged_tree_attn(q, k_cache, v_cache, page_indptr, page_indices, seq_lens, to
     request r's, whose drafted tokens are the last of its ``seq_lens[r]`` cached ones.  A row sees the
     committed tokens before them (with ``window``: those less than that far behind its own depth, and
     the first ``sinks``) and drafted token j if bit j of its ``tree_mask`` (int64 or uint64 [N] or
-    [N][words], up to 4 words) is set.  The other arguments are ``paged_decode_attn``'s;
+    [N][words], up to 4 words) is set, whatever the window.  The other arguments are ``paged_decode_attn``'s;
     workspace from ``alloc_tree_workspace``."""
     (_bind or _load_bind()).paged_tree_attn(q, k_cache, v_cache, page_indptr, page_indices, seq_lens, token_indptr, tree_mask,
                                             sm_scale, out, workspace, k_scale, v_scale, abort_mask, window, sinks, stream)

@@ -562,6 +562,9 @@ FKV_API fkv_status kv_append_rope(const void *q, int64_t q_token_stride, int32_t
  *   - committed token t if window is 0, or t < sinks, or t > p - window with p =
  *     c + max(0, bits set in its mask - 1), the position of its depth in the tree.
  * and out = softmax(sm_scale * q . k) v over what it sees, as in paged_decode_attn.
+ * The window says nothing of drafted tokens: they are seen by their bits alone.  For a
+ * sliding window along a path deeper than it, leave out the bits of the ancestors that
+ * the window (and sinks) leave out; each row is then paged_window_attn's of its token.
  * Bits of tokens that are not there (n and above) are ignored, in the count too.  A
  * row that sees nothing is zeros.  What a row does not see has no part in it, whatever
  * it holds (NaN, infinities; but infinite V that every row of a request sees may give NaN).  Query

@@ -137,3 +137,22 @@ def test_commit_refuses_lengths_over_what_it_reads(lib):
     """Other warps still read a request's count, list and length when one of them writes its kept length."""
     for name in ("lens", "counts", "acc"):
         assert commit(lib, batch=2, **{name: 7 * A, "out": 7 * A}) == 1, name
+
+
+@pytest.mark.parametrize("ctx,window,sinks", [(6, 4, 1), (0, 3, 0), (1, 3, 3), (20, 1, 2), (3, 9, 0), (5, 30, 0)])
+def test_a_chain_deeper_than_the_window(ctx, window, sinks):
+    """Drafted tokens are seen by their bits alone: with those of the ancestors unset that a sliding window leaves out, each row is
+    the windowed decode step's of its token."""
+    rng = np.random.default_rng(1)
+    n = 9
+    kc, ks = T.pool(rng, "fp8", 4, 2, 16)
+    vc, vs = T.pool(rng, "fp8", 4, 2, 16)
+    q = W.bf16_bits(rng.standard_normal((n, 8, D)).astype(np.float32))
+    ptr, idx = np.array([0, 3], np.int32), np.array([2, 0, 3], np.int32)
+    sets = [sum(1 << j for j in range(i + 1) if i - j < window or ctx + j < sinks) for i in range(n)]
+    out, _, _ = T.tree_attention(q, kc, vc, "fp8", ks, vs, ptr, idx, [ctx + n], [0, n], sets, 0.1, window, sinks)
+    for i in range(n):
+        see = T.visible([1], 1, ctx + i, window, sinks)[0]
+        assert see.nonzero()[0].tolist() == [t for t in range(ctx + i + 1) if t < sinks or t > ctx + i - window]
+        want, _, _ = T.tree_attention(q[i:i + 1], kc, vc, "fp8", ks, vs, ptr, idx, [ctx + i + 1], [0, 1], [1], 0.1, window, sinks)
+        assert np.allclose(out[i], want[0])

@@ -710,3 +710,40 @@ def test_no_tokens(Hq, H):
     none.update(page_indptr=t["page_indptr"][:1], seq_lens=t["seq_lens"][:0])
     fkv.paged_window_attn(**none, window=5)
     assert fkv.device_error() == 0
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("window,sinks", [(5, 0), (5, 3), (40, 8)])
+def test_a_chain_deeper_than_the_window(kind, window, sinks):
+    """With the bits of the ancestors unset that the window leaves out, each row is paged_window_attn's of the same token."""
+    ctx, n = np.array([90, 3, 400]), np.array([12, 50, 9])
+    sets = [sum(1 << j for j in range(i + 1) if i - j < window or c + j < sinks) for c, k in zip(ctx, n) for i in range(k)]
+    c = Case(kind, 8, 2, 16, ctx, n, seed=52, sets=sets)
+    c.check(c.tree(window=window, sinks=sinks), window, sinks)
+    w = Case(kind, 8, 2, 16, ctx, n, seed=52, sets=sets)                # the same pools, one token of each request at a time
+    w.sets, w.N = [1] * 3, 3
+    rows = c.tptr[:-1]
+    for i in range(int(n.max())):
+        at = np.minimum(i, n - 1)
+        w.lens, w.q, w.tptr = (ctx + at + 1).astype(np.int32), c.q[rows + at], np.arange(4, dtype=np.int32)
+        w.check(w.window(window=window, sinks=sinks), window, sinks)
+        want, got = w.ref(window, sinks)[0], c.ref(window, sinks)[0][rows + at]
+        assert np.allclose(got, want)
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("Hq,H", [(8, 2), (16, 2), (16, 1)])
+def test_requests_beside_an_aborted_one(kind, Hq, H):
+    """Aborted requests take nothing from the others, whose bytes stay the same, and leave zeros."""
+    import torch
+    c = Case(kind, Hq, H, 64, [2000, 40, 900, 600], [8, 8, 8, 8], seed=51)
+    alone = c.tree().clone()
+    c.dead = np.array([0, 1, 0, 1])
+    for r in (1, 3):
+        c.idx[c.ptr[r]:c.ptr[r + 1]] = -1                              # not read either
+    out = c.tree()
+    c.check(out)
+    assert (out[8:16] == 0).all() and (out[24:] == 0).all()
+    c = Case(kind, Hq, H, 64, [2000, 40, 900, 600], [8, 8, 8, 8], seed=51)
+    c.dead = np.zeros(4)
+    assert torch.equal(c.tree().view(torch.int16), alone.view(torch.int16))
