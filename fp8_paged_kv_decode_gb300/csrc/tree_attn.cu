@@ -26,8 +26,9 @@
 //   softmax    two groups of four warps, one token a thread: weights against a running
 //              reference, stored as the second product's operand.  The groups take turns at
 //              tiles, with references and sums of their own that are joined at a unit's end
-// The reference of a column moves only when a weight would pass f16's range: a maximum is
-// put at 2^10, later ones may grow to 2^15.9, so sums are rescaled a few times per unit.
+// The reference of a column moves only when a weight would pass its range: a maximum is
+// put at 2^10, later ones may grow to 2^15.9 (BF16: 2^-6 and 1), so sums are rescaled a few
+// times per unit.
 // FP8 and FP4 weights are one f16 word, BF16 ones two BF16 words.
 //
 // Few rows over BF16 are bound by memory (8 requests, window of 32768: 86 us, 93% of a copy's
@@ -688,7 +689,7 @@ tree_attn_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmK, co
 #pragma unroll
                     for (int j = 4; j < kNC; ++j) m4[j & 3] = fmaxf(m4[j & 3], x[j]);
                     const float most = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
-                    if (__builtin_expect(!group_any(barrier, most > kTreeMost) || tries == 4, 1)) break;
+                    if (__builtin_expect(!group_any(barrier, most > kTreeMost<kKv>) || tries == 4, 1)) break;
                     // ---- move the references of the columns that need it ----
                     if (had) wait(ct.pempty[g], ph ^ 1);                      // the sums so far are complete
                     umma_fence_after();
@@ -704,8 +705,8 @@ tree_attn_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmK, co
                     bool move = false, off = false;
                     if (tok < kNC) {
                         const float z = fmaxf(fmaxf(red[0][tok], red[1][tok]), fmaxf(red[2][tok], red[3][tok])), was = -refs[tok];
-                        move = z - was > kTreeMost;
-                        const float ref = move ? tree_reference(z) : was;
+                        move = z - was > kTreeMost<kKv>;
+                        const float ref = move ? tree_reference<kKv>(z) : was;
                         refs[tok] = -ref;
                         ct.up[g][tok] = move ? ex2(was - ref) : 1.f;
                         off = reference_far(ref);

@@ -12,13 +12,19 @@
 namespace fkv {
 
 constexpr int kTreeMaxWords = 4;               // 64-bit words of a row's mask
-constexpr float kTreeTop = 10.f, kTreeMost = 15.9f;   // log2 of a moved reference's largest weight, and of any weight
 constexpr float kTreeNone = -3e38f;            // the reference of a row that has seen nothing
+// log2 of a moved reference's largest weight, and of any weight: f16 words take all of f16's range; of BF16 ones, which have
+// fp32's, none is above 1, so that no sum over V of any size overflows that the output does not.
+template <int kKv>
+constexpr float kTreeTop = kKv == FKV_KV_BF16 ? -6.f : 10.f;
+template <int kKv>
+constexpr float kTreeMost = kKv == FKV_KV_BF16 ? 0.f : 15.9f;
 // The reference that a largest logit of z asks for.  Past 2^27 fp32 neighbours are 16 and more apart, and z - 10 may round
 // to z - 16, whose weight of 2^16 f16 does not hold: there it is z itself.
+template <int kKv>
 __device__ __forceinline__ float tree_reference(float z) {
-    const float r = __fsub_rn(z, kTreeTop);
-    return __fsub_rn(z, r) > kTreeMost ? z : r;
+    const float r = __fsub_rn(z, kTreeTop<kKv>);
+    return __fsub_rn(z, r) > kTreeMost<kKv> ? z : r;
 }
 // Whether an exponent c s - ref needs c s rounded first, as the reference's logit was.  One fused operation leaves
 // that rounding in the exponent, up to half an fp32 step of the logit: 1/16 below 2^20, 2^9 at 1e10, where weights would

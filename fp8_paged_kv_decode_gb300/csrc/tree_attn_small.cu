@@ -284,7 +284,7 @@ tree_small_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmK, c
 #pragma unroll
                         for (int nb = 1; nb < 4; ++nb) x = fmaxf(x, fmaxf(s[mb][nb][2 * hf], s[mb][nb][2 * hf + 1]));
                         top[mb][hf] = x;
-                        move |= x - ref[mb][hf] > kTreeMost;
+                        move |= x - ref[mb][hf] > kTreeMost<kKv>;
                     }
                 if (__builtin_expect(__any_sync(kAll, move), 0)) {
 #pragma unroll
@@ -294,8 +294,8 @@ tree_small_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmK, c
                             float x = top[mb][hf];
                             x = fmaxf(x, __shfl_xor_sync(kAll, x, 1));
                             x = fmaxf(x, __shfl_xor_sync(kAll, x, 2));
-                            if (x - ref[mb][hf] > kTreeMost) {
-                                const float to = tree_reference(x), f = ex2(ref[mb][hf] - to);
+                            if (x - ref[mb][hf] > kTreeMost<kKv>) {
+                                const float to = tree_reference<kKv>(x), f = ex2(ref[mb][hf] - to);
                                 ref[mb][hf] = to;
                                 l[mb][hf] *= f;
 #pragma unroll

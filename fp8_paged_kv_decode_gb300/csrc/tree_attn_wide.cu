@@ -463,10 +463,10 @@ tree_wide_kernel(const TreeParams p, int rows, const __grid_constant__ CUtensorM
 #pragma unroll
                     for (int j = 0; j < 64; j += 2) top = fmaxf(top, fmaxf(s[j], s[j + 1]));
                     top = __fmul_rn(top, c);
-                    const bool move = __fsub_rn(top, ref) > kTreeMost;
+                    const bool move = __fsub_rn(top, ref) > kTreeMost<kKv>;
                     if (__builtin_expect(__any_sync(kAll, move), 0)) {
                         // the sums so far, and the weights of the tile's first half, are scaled to the new reference
-                        const float to = move ? tree_reference(top) : ref, f = move ? ex2(ref - to) : 1.f;
+                        const float to = move ? tree_reference<kKv>(top) : ref, f = move ? ex2(ref - to) : 1.f;
                         if (i > tb + turns) {
                             wait(ct.odone[g], (n - 1) & 1);
                             umma_fence_after();

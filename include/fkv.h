@@ -587,6 +587,10 @@ FKV_API fkv_status kv_append_rope(const void *q, int64_t q_token_stride, int32_t
  * that it reads outside [0, num_pages) (FKV_DEVERR_ATTN_PAGE) are zeros.  token_indptr
  * entries that are negative, decreasing or past n_tokens leave the request's rows
  * unwritten.
+ * Softmax weights and their sums are fp32; the product with V takes them as f16
+ * for FP8 and FP4 (each within 2^-11 of itself, down to 2^-24 of the row's largest)
+ * and as two bf16 words for BF16.  Logits may have any size that fp32 holds; tokens
+ * times the largest |V| has to stay below 2^128.
  * Deterministic: the same call gives the same bytes every time.  Two launches.
  * Supported: head_dim 128, page_size in {16, 32, 64, 128}, up to 128 query heads
  * per KV head.  batch == 0 or n_tokens == 0 is a no-op.

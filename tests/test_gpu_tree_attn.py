@@ -747,3 +747,13 @@ def test_requests_beside_an_aborted_one(kind, Hq, H):
     c = Case(kind, Hq, H, 64, [2000, 40, 900, 600], [8, 8, 8, 8], seed=51)
     c.dead = np.zeros(4)
     assert torch.equal(c.tree().view(torch.int16), alone.view(torch.int16))
+
+
+@pytest.mark.parametrize("G,n", ROWS)
+@pytest.mark.parametrize("power", [110, 119])
+def test_bf16_values_near_the_largest(G, n, power):
+    """Values of 2^110 and 2^119: their sum over 400 tokens is below 2^128, and so is every sum on the way."""
+    c = Case("bf16", 2 * G, 2, 64, [300, 390], [n, n - 1], seed=54, q_std=3.0)
+    c.vc = ((c.vc & 0x8000) | ((c.vc & 0x7F) + ((power + 127) << 7))).astype(np.uint16)      # [2^power, 2^(power + 1)), either sign
+    c.check(c.tree())
+    c.check(c.tree(window=100, sinks=2), 100, 2)
