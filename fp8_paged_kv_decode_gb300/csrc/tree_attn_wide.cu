@@ -26,6 +26,7 @@
 #include <cudaTypedefs.h>
 
 #include <mutex>
+#include <type_traits>
 
 #include "tree_attn.cuh"
 #include "umma.cuh"
@@ -447,94 +448,98 @@ tree_wide_kernel(const TreeParams p, int rows, const __grid_constant__ CUtensorM
                 // 64 logits at a time, their weights' two words in their place
                 const bool whole = tile_whole(u, i);
                 float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+                // (two forms of the loop: a branch in each half costs trees of 61 over FP8 272 us instead of 264)
+                auto weights = [&](auto rounded, int at) {         // from token `at` on; returns where references got far
+                    constexpr bool kRounded = decltype(rounded)::value;
 #pragma unroll 1
-                for (int at = 0; at < 128; at += 64) {
-                    float s[64];
-                    tmem_load(tS + at, s);
-                    if (__builtin_expect(!whole, 0)) {
-                        const uint32_t t0 = tile_at<kTreeTok>(u, i) + at;
-                        const uint32_t end = tile_end(u, i);
-                        const uint64_t see = seen_of(p, u, tok, t0, end) | static_cast<uint64_t>(seen_of(p, u, tok, t0 + 32, end)) << 32;
+                    for (; at < 128; at += 64) {
+                        float s[64];
+                        tmem_load(tS + at, s);
+                        if (__builtin_expect(!whole, 0)) {
+                            const uint32_t t0 = tile_at<kTreeTok>(u, i) + at;
+                            const uint32_t end = tile_end(u, i);
+                            const uint64_t see = seen_of(p, u, tok, t0, end) | static_cast<uint64_t>(seen_of(p, u, tok, t0 + 32, end)) << 32;
 #pragma unroll
-                        for (int j = 0; j < 64; ++j)
-                            if (!((see >> j) & 1)) s[j] = -INFINITY;   // (c is above zero)
-                    }
-                    float top = -INFINITY;
-#pragma unroll
-                    for (int j = 0; j < 64; j += 2) top = fmaxf(top, fmaxf(s[j], s[j + 1]));
-                    top = __fmul_rn(top, c);
-                    const bool move = __fsub_rn(top, ref) > kTreeMost<kKv>;
-                    if (__builtin_expect(__any_sync(kAll, move), 0)) {
-                        // the sums so far, and the weights of the tile's first half, are scaled to the new reference
-                        const float to = move ? tree_reference<kKv>(top) : ref, f = move ? ex2(ref - to) : 1.f;
-                        if (i > tb + turns) {
-                            wait(ct.odone[g], (n - 1) & 1);
-                            umma_fence_after();
-#pragma unroll 1
-                            for (int b = 0; b < 128; b += 32) {
-                                float o[32];
-                                uint32_t w[32];
-                                tmem_load(tO + b, o);
-#pragma unroll
-                                for (int j = 0; j < 32; ++j) w[j] = __float_as_uint(move ? o[j] * f : o[j]);
-                                tmem_store(tO + b, w);
-                            }
+                            for (int j = 0; j < 64; ++j)
+                                if (!((see >> j) & 1)) s[j] = -INFINITY;   // (c is above zero)
                         }
-                        if (at) {
-                            tmem_store_wait();
+                        float top = -INFINITY;
+#pragma unroll
+                        for (int j = 0; j < 64; j += 2) top = fmaxf(top, fmaxf(s[j], s[j + 1]));
+                        top = __fmul_rn(top, c);
+                        const bool move = __fsub_rn(top, ref) > kTreeMost<kKv>;
+                        if (__builtin_expect(__any_sync(kAll, move), 0)) {
+                            // the sums so far, and the weights of the tile's first half, are scaled to the new reference
+                            const float to = move ? tree_reference<kKv>(top) : ref, f = move ? ex2(ref - to) : 1.f;
+                            if (i > tb + turns) {
+                                wait(ct.odone[g], (n - 1) & 1);
+                                umma_fence_after();
 #pragma unroll 1
-                            for (int b = 0; b < 32; b += 8) {
-                                float hi[8];
-                                uint32_t wh[8];
-                                tmem_load(tS + b, hi);
-                                if constexpr (C::kConv) {
+                                for (int b = 0; b < 128; b += 32) {
+                                    float o[32];
+                                    uint32_t w[32];
+                                    tmem_load(tO + b, o);
 #pragma unroll
-                                    for (int j = 0; j < 8; ++j) {
-                                        const uint32_t x = __float_as_uint(hi[j]);
-                                        const float2 y = __half22float2(*reinterpret_cast<const __half2 *>(&x));
-                                        wh[j] = pack_f16x2(y.x * f, y.y * f);
-                                    }
-                                } else {
-                                    float lo[8];
-                                    uint32_t wl[8];
-                                    tmem_load(tS + 32 + b, lo);
-#pragma unroll
-                                    for (int j = 0; j < 8; ++j) {
-                                        const uint32_t x = __float_as_uint(hi[j]), y = __float_as_uint(lo[j]);
-                                        split((__uint_as_float(x << 16) + __uint_as_float(y << 16)) * f,
-                                              (__uint_as_float(x & 0xFFFF0000u) + __uint_as_float(y & 0xFFFF0000u)) * f, wh[j], wl[j]);
-                                    }
-                                    tmem_store(tS + 32 + b, wl);
+                                    for (int j = 0; j < 32; ++j) w[j] = __float_as_uint(move ? o[j] * f : o[j]);
+                                    tmem_store(tO + b, w);
                                 }
-                                tmem_store(tS + b, wh);
                             }
+                            if (at) {
+                                tmem_store_wait();
+#pragma unroll 1
+                                for (int b = 0; b < 32; b += 8) {
+                                    float hi[8];
+                                    uint32_t wh[8];
+                                    tmem_load(tS + b, hi);
+                                    if constexpr (C::kConv) {
+#pragma unroll
+                                        for (int j = 0; j < 8; ++j) {
+                                            const uint32_t x = __float_as_uint(hi[j]);
+                                            const float2 y = __half22float2(*reinterpret_cast<const __half2 *>(&x));
+                                            wh[j] = pack_f16x2(y.x * f, y.y * f);
+                                        }
+                                    } else {
+                                        float lo[8];
+                                        uint32_t wl[8];
+                                        tmem_load(tS + 32 + b, lo);
+#pragma unroll
+                                        for (int j = 0; j < 8; ++j) {
+                                            const uint32_t x = __float_as_uint(hi[j]), y = __float_as_uint(lo[j]);
+                                            split((__uint_as_float(x << 16) + __uint_as_float(y << 16)) * f,
+                                                  (__uint_as_float(x & 0xFFFF0000u) + __uint_as_float(y & 0xFFFF0000u)) * f, wh[j], wl[j]);
+                                        }
+                                        tmem_store(tS + 32 + b, wl);
+                                    }
+                                    tmem_store(tS + b, wh);
+                                }
+                            }
+                            l *= f;
+                            sum[0].x *= f, sum[0].y *= f, sum[1].x *= f, sum[1].y *= f;
+                            ref = to;
+                            far = __any_sync(kAll, reference_far(ref));
+                            if (!kRounded && far) return at;           // once more, with what is scaled already
                         }
-                        l *= f;
-                        sum[0].x *= f, sum[0].y *= f, sum[1].x *= f, sum[1].y *= f;
-                        ref = to;
-                        far = __any_sync(kAll, reference_far(ref));
-                    }
-                    float cc = c;
-                    if (__builtin_expect(far, 0)) {
-                        asm volatile("" ::: "memory");
+                        const float2 c2 = make_float2(c, c), r2 = make_float2(-ref, -ref);
+                        uint32_t hi[32];
+                        [[maybe_unused]] uint32_t lo[C::kConv ? 1 : 32];
 #pragma unroll
-                        for (int j = 0; j < 64; ++j) s[j] = __fmul_rn(s[j], c);
-                        cc = 1.f;
+                        for (int j = 0; j < 32; ++j) {
+                            float2 x;
+                            if constexpr (kRounded) x = make_float2(__fadd_rn(__fmul_rn(s[2 * j], c), -ref), __fadd_rn(__fmul_rn(s[2 * j + 1], c), -ref));
+                            else x = fma2(make_float2(s[2 * j], s[2 * j + 1]), c2, r2);
+                            x.x = ex2(x.x);
+                            x.y = ex2(x.y);
+                            sum[j & 1] = add2(sum[j & 1], x);
+                            if constexpr (C::kConv) hi[j] = pack_f16x2(x.x, x.y);
+                            else split(x.x, x.y, hi[j], lo[j]);
+                        }
+                        tmem_store(tS + at, hi);
+                        if constexpr (!C::kConv) tmem_store(tS + at + 32, lo);
                     }
-                    const float2 c2 = make_float2(cc, cc), r2 = make_float2(-ref, -ref);
-                    uint32_t hi[32], lo[C::kConv ? 1 : 32];
-#pragma unroll
-                    for (int j = 0; j < 32; ++j) {
-                        float2 x = fma2(make_float2(s[2 * j], s[2 * j + 1]), c2, r2);
-                        x.x = ex2(x.x);
-                        x.y = ex2(x.y);
-                        sum[j & 1] = add2(sum[j & 1], x);
-                        if constexpr (C::kConv) hi[j] = pack_f16x2(x.x, x.y);
-                        else split(x.x, x.y, hi[j], lo[j]);
-                    }
-                    tmem_store(tS + at, hi);
-                    if constexpr (!C::kConv) tmem_store(tS + at + 32, lo);
-                }
+                    return at;
+                };
+                const int got = far ? 0 : weights(std::false_type{}, 0);
+                if (__builtin_expect(got < 128, 0)) weights(std::true_type{}, got);
                 sum[0] = add2(sum[0], sum[1]);
                 l += sum[0].x + sum[0].y;
                 if (__builtin_expect(!C::kConv && !whole, 0)) {

@@ -757,3 +757,28 @@ def test_bf16_values_near_the_largest(G, n, power):
     c.vc = ((c.vc & 0x8000) | ((c.vc & 0x7F) + ((power + 127) << 7))).astype(np.uint16)      # [2^power, 2^(power + 1)), either sign
     c.check(c.tree())
     c.check(c.tree(window=100, sinks=2), 100, 2)
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("G,n", ROWS)
+@pytest.mark.parametrize("levels", [(-2, -1, 0), (0, 0.5, 1), (-2, 0, 0.5), (0.5, 1, -2)])
+def test_references_that_get_huge_and_small_again(kind, G, n, levels):
+    """Logits that rise along the tokens, from huge negative ones to zero or from there to huge ones: the output is the mean of the
+    last level's (or, falling, the second's)."""
+    c = Case(kind, 2 * G, 2, 64, [290, 600], [n, n], seed=55)
+    for r in range(2):
+        at = [(c.idx[c.ptr[r] + t // 64], t % 64) for t in range(int(c.lens[r]))]
+        one_dim_keys(c, -2, at)
+        for k, value in enumerate(levels):
+            rows = at[45 + 75 * k:45 + 75 * (k + 1)]
+            if value:
+                one_dim_keys(c, value, rows)
+            else:
+                for pg, off in rows:
+                    c.kc[pg, :, off] = 0
+    q = np.zeros(c.q.shape, np.float32)
+    q[..., 0] = 1024 * (1 + np.arange(c.q.shape[0] * 2 * G).reshape(c.q.shape[:2]) % 5 / 8)
+    c.q = W.bf16_bits(q)
+    for z in (4e5, 2e6, 1e9, 1e12):
+        c.sm = z * np.log(2.0) / 1024
+        c.check(c.tree())
