@@ -32,9 +32,10 @@
 // FP8 and FP4 weights are one f16 word, BF16 ones two BF16 words.
 //
 // Few rows over BF16 are bound by memory (8 requests, window of 32768: 86 us, 93% of a copy's
-// rate); 64 requests around 16k tokens, 8 drafted, over FP8 nearly so (565 to 660 us from run to
-// run, 65 to 77%): there a tile's way through five kinds of warps, and the instruction cache
-// that their code shares, cost what is missing.
+// rate).  64 requests around 16k tokens, 8 drafted, over FP8 take 422 to 482 us a million tokens
+// (302 at a copy's rate), by their lengths; FP4 870 to 960 us in all, BF16 905: a tile's way
+// through five kinds of warps, and the instruction cache that their code shares, cost what is
+// missing.
 #include <cudaTypedefs.h>
 
 #include <algorithm>
@@ -1055,9 +1056,10 @@ bool known_kv(int kv) { return kv == FKV_KV_FP8_E4M3 || kv == FKV_KV_BF16 || kv 
 
 // Rows of a unit: the smallest instance that holds the query heads of the requests' mean
 // number of tokens.
-// From 128 rows on they lie on M (tree_attn_wide.cu): with 128 that is 126 us instead of 145 over BF16, 117 instead of
-// 130 over FP8 and 103 instead of 130 over FP4 (16 requests of 8192 tokens, 16 drafted); with 64, half of M, 801 instead
-// of 603 (FP8, 64 requests around 16k, 8 drafted).
+// From 128 rows on they lie on M (tree_attn_wide.cu): with 128 that was 126 us instead of 145 over BF16, 117 instead of
+// 130 over FP8 and 103 instead of 130 over FP4 when both were measured (16 requests of 8192 tokens, 16 drafted; 113, 112 and
+// 104 now); with 64, half of M, 801 instead of 603 (FP8, 64 requests around 16k, 8 drafted).  The mean, not the largest, as
+// rows of a unit that are not used cost their products; what a ragged step pays is a second unit for requests above it.
 int rows_of(int64_t n_tokens, int64_t batch, int64_t group) {
     const int64_t want = group * ((n_tokens + batch - 1) / (batch > 0 ? batch : 1));
     for (int r = 16; r < 128; r *= 2)
@@ -1067,8 +1069,9 @@ int rows_of(int64_t n_tokens, int64_t batch, int64_t group) {
 
 // Which kernel.  Up to 32 rows over FP8 or FP4 the products are little work, and the hand-overs of a tile from warp to warp
 // cost more than they save: a window of 4096 over FP8 takes 98 us instead of 115, one of 1024 over 16-token FP4 pages 101
-// instead of 176, 64 requests around 16k tokens with up to 4 drafted (32 rows) 457 instead of 486 (batch of 16: 145, 140;
-// of 4: 67, 58, of which 13 are the joining of a hundred parts a unit).
+// instead of 176, 64 requests around 16k tokens with up to 4 drafted (32 rows) 457 instead of 486.  Few long requests would
+// be served faster by the other kernel, 140 us instead of 145 for 16 of them and 58 instead of 67 for 4 (13 of these are the
+// joining of a hundred parts a unit): the rule does not look at the batch.
 // BF16 needs no conversions and is read by the tensor cores as it lies.
 bool small_call(int kv, int rows) { return kv != FKV_KV_BF16 && rows <= 32; }
 

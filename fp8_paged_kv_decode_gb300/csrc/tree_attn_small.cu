@@ -9,9 +9,11 @@
 // the warps and all run the same small loop.
 //
 // FP8 streams at 90% of a copy's rate once it runs (a window of 4096 over 64 requests: 98 us,
-// of which 10 are the start, the last tiles and the joining).  FP4 is bound by the conversions,
-// 800 instructions a tile and warp of 16 rows (256 requests, window of 1024: 103 us, 41 at the
-// copy's rate); 12 warps of 168 registers or 16 of 128 gained nothing over 8 (102, 126 us).
+// of which 10 are the start, the last tiles and the joining).  FP4 fills no unit (256 requests,
+// window of 1024: 103 us, 41 at the copy's rate; issue slots 42%, DRAM 32%, tensor pipe 26%):
+// a tile is 800 instructions of a warp, conversions and products for 16 rows of which a group of
+// 4 uses 4, and eight warps do not cover their latencies; 12 warps of 168 registers or 16 of 128
+// gained nothing (102, 126 us).
 //
 // Operand layouts: lane (g, t) = (lane / 4, lane % 4).
 //   K of 8 tokens: token g, dims 16t .. and 64 + 16t .. (one 16-byte load each, or 8 bytes and
