@@ -584,7 +584,9 @@ FKV_API fkv_status kv_append_rope(const void *q, int64_t q_token_stride, int32_t
  *   the others     as in paged_decode_attn
  * Fail closed: the rows of a request that is aborted, has a malformed CSR row, has
  * n > seq_lens[r], n > 64 * mask_words, more tokens than its pages hold, or a page
- * that it reads outside [0, num_pages) (FKV_DEVERR_ATTN_PAGE) are zeros.  token_indptr
+ * that it reads outside [0, num_pages) (FKV_DEVERR_ATTN_PAGE) are zeros.  It reads the
+ * pages of all its tokens, with a window those of the first sinks tokens and from the
+ * window of a row at depth 0 on, whatever the masks name of them.  token_indptr
  * entries that are negative, decreasing or past n_tokens leave the request's rows
  * unwritten.
  * Softmax weights and their sums are fp32; the product with V takes them as f16
