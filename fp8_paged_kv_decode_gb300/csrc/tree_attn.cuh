@@ -373,17 +373,19 @@ struct Ring {                                  // a buffer of a ring and the par
 
 // Waits for a phase; false: it gave up.  After `limit` ticks without it the call has failed: that
 // is recorded, and from then on no wait of the block waits, so that it ends soon, with outputs
-// that are not valid.  The clock is read only every 64 tests (a test sleeps in hardware for a
-// while; most waits are over before).
+// that are not valid: a long share may have tens of thousands of waits left by then, so each
+// looks at `dead` every 8 tests (one that fails has slept in hardware for 2 us).  Out of line:
+// with both looks after every test 64 requests around 16k tokens, 8 drafted, took 628 us
+// instead of 580 (tree_attn.cu: its roles share the instruction cache).
 __device__ __forceinline__ bool tree_wait(uint32_t bar, uint32_t parity, volatile int32_t *dead, uint32_t *err,
                                           uint32_t limit = kTreeWaitTicks) {
     if (__builtin_expect(mbar_try_wait(bar, parity), 1)) return true;
     uint32_t since = 0;
 #pragma unroll 1
     for (uint32_t i = 1; !mbar_try_wait(bar, parity); ++i) {
-        if (__builtin_expect((i & 63u) == 0, 0)) {
+        if (__builtin_expect((i & 7u) == 0, 0)) {
             const uint32_t now = static_cast<uint32_t>(globaltimer_ns() >> 10);
-            if (i == 64) since = now;
+            if (i == 8) since = now;
             if (now - since > limit) {
                 *dead = 1;
                 atomicOr(err, FKV_DEVERR_TIMEOUT);

@@ -208,21 +208,25 @@ tree_wide_kernel(const TreeParams p, int rows, const __grid_constant__ CUtensorM
                         }
                         __syncwarp();
                     };
+                    bool gone = false;                             // a wait for a stage that is still read gave up
 #pragma unroll
-                    for (int kv = 0; kv < 2; ++kv) {
+                    for (int kv = 0; kv < 2 && !gone; ++kv) {
                         const CUtensorMap *tm = kv ? &tmV : &tmK;
                         const uint8_t *cache = kv ? p.v_cache : p.k_cache;
                         if constexpr (C::kConv) {
-                            if (__any_sync(kAll, !wait(ct.rempty[raw.i], raw.ph ^ 1))) break;   // a stage that is still read
+                            gone = __any_sync(kAll, !wait(ct.rempty[raw.i], raw.ph ^ 1));
+                            if (gone) break;
                             copy(ct.rfull[raw.i], sRaw + raw.i * C::kRawB, tm, cache);
                             raw.template next<C::kRaw>();
                         } else {
                             Turn &at = kv ? v : k;
-                            if (__any_sync(kAll, !wait(ct.empty[at.i], at.ph ^ 1))) break;
+                            gone = __any_sync(kAll, !wait(ct.empty[at.i], at.ph ^ 1));
+                            if (gone) break;
                             copy(ct.full[at.i], sRing + at.i * kStageB, tm, cache);
                             at.template next<C::kStages>();
                         }
                     }
+                    if (gone) break;
                 }
                 left -= u.te - u.tb;
                 d.template next<kDesc>();
