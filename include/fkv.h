@@ -693,8 +693,8 @@ FKV_API int32_t fkv_kernels_per_call(const char *entry_point);
  * block completes the barrier first and all waits return at once (no error
  * bit).  result: NULL, or a device uint32[2] receiving 1 (the wait saw the
  * barrier complete) or 0 (it gave up): [0] of the first and third helper (2:
- * they do not agree), [1] of the sleeping one.  limit_ns above 10 s returns
- * FKV_ERR_INVALID_ARG.
+ * they do not agree, or waits of the third kind still wait after one gave up),
+ * [1] of the sleeping one.  limit_ns above 10 s returns FKV_ERR_INVALID_ARG.
  * Asynchronous on `stream`; read the outcome with fkv_device_error.
  */
 FKV_API fkv_status fkv_selftest_wait(uint64_t limit_ns, int32_t complete, uint32_t *result, void *stream);

@@ -567,7 +567,8 @@ ROWS = [(4, 3), (4, 7), (8, 8), (16, 7), (16, 13)]                    # query he
 @pytest.mark.parametrize("G,n", ROWS)
 @pytest.mark.parametrize("words", [1, 4])
 def test_bits_of_tokens_that_are_not_there(kind, G, n, words):
-    """They change nothing, the depth by which a window is placed included."""
+    """They change nothing, the depth by which a window is placed included (the reference counts every bit that it is given:
+    it gets the masks without them)."""
     import torch
     c = Case(kind, 2 * G, 2, 64, [1000, 3000, 700], [n, n - 1, n], seed=45, words=words)
     own = c.sets
