@@ -14,7 +14,7 @@
 // exponentials, 1024 cycles of an SM.  FP8 and FP4 rows become f16 operands in shared memory, by
 // four more warps; their weights are one f16 word, 16 products a tile.
 //
-// 16 requests of 8192 tokens, 61 drafted, 64 query heads on 8: 326 us over BF16 (475 with tokens
+// 16 requests of 8192 tokens, 61 drafted, 64 query heads on 8: 320 us over BF16 (475 with tokens
 // on M; 140 at the rate of a large product were a weight one word, 220 as it is), 264 over FP8
 // (398), 266 over FP4 (394).  What is left is a block's chain, weights after S after O, which
 // two groups hide only in part.  Tried: S of half tiles, so that the softmax begins earlier, 424
